@@ -334,6 +334,99 @@ int orca_attention_decode_noalloc(int32_t dtype, const void *qkv, const void *kv
                                   const int64_t *kv_offset, void *out, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* K/V cache held in 4 bits                                                  */
+/* ------------------------------------------------------------------------ */
+/* A layer of a cache in 4 bits takes head_dim / 2 + 4 G bytes per slot, head
+ * and K or V (G = head_dim / 32 groups, at least one), against head_dim * 2 in
+ * bf16: 80 against 256 at head_dim 128.  Each group of min(32, head_dim)
+ * components has a scale s and a minimum m in bf16; a component x is held as
+ * the code c = the integer nearest to (x - m) / s (ties to even) within
+ * 0 .. 15, with s = bf16((max - min) / 15) (fp32 difference and quotient) and
+ * m = bf16(min), and stands for m + s c.  s = 0 holds c = 0.  A group in which
+ * a value, s or m is not finite reads back as NaN.
+ *
+ * Layout of a layer, with S = kv_slots rounded up to a multiple of 16:
+ *   K codes  [n_heads][S][head_dim / 2]      component 2b in the low, 2b + 1 in
+ *                                            the high four bits of byte b
+ *   V codes  [n_heads][S / 2][head_dim / 4]  32-bit words: four components of
+ *            the even slot in the low half, of the odd slot in the high half
+ *   K params [n_heads][S][G]                 s in the low, m in the high half
+ *   V params [n_heads][S / 2][G][2]          the same, the even slot first
+ * The caller owns the memory (16-byte aligned, orca_kv4_layer_bytes, any
+ * contents at first); slots that no range of a call covers are neither used
+ * nor changed.  Slots are reserved as for the engine's own pool.
+ *
+ * A plan describes a batch of ranges over a layer to the three operators
+ * below: request i has rows n_input[i] (>= 1) at positions ctx_len[i] + j
+ * (ctx_len >= 0) of its slots kv_offset[i] + position, all within kv_slots.
+ * The same plan serves every layer of that shape.  The HOST arrays (n_req
+ * entries) are read during the call.  orca_kv4_plan_build packs
+ * orca_kv4_plan_words() int32 words into host_buf; the caller copies them to
+ * device memory (16-byte aligned) once and passes both copies.  `eng` gives
+ * the number of SMs the work is split for (NULL: 152).  The device
+ * copy also holds counters that a launch leaves at zero: it is not shared by
+ * calls that may overlap on the GPU, and nor is a workspace.  Contents of a
+ * plan other than what orca_kv4_plan_build wrote are not checked.
+ * Supported: n_heads <= 1024, head_dim 16, 32, 64 or 128, kv_slots <=
+ * INT32_MAX - 15.  Errors: INVALID (also for a batch whose tables exceed
+ * 32-bit offsets), OOM. */
+int64_t orca_kv4_layer_bytes(int32_t n_heads, int32_t head_dim, int64_t kv_slots);
+int64_t orca_kv4_plan_words(const orca_engine *eng, int32_t dtype, int32_t n_heads, int32_t head_dim, int64_t kv_slots,
+                            int32_t n_req, const int32_t *n_input, const int32_t *ctx_len, const int64_t *kv_offset);
+int orca_kv4_plan_build(const orca_engine *eng, int32_t dtype, int32_t n_heads, int32_t head_dim, int64_t kv_slots,
+                        int32_t n_req, const int32_t *n_input, const int32_t *ctx_len, const int64_t *kv_offset,
+                        int32_t *host_buf, int64_t cap_words);
+/* Bytes of device memory that orca_op_kv4_attention needs beside the plan
+ * (0: none, workspace may be NULL); any contents, 16-byte aligned. */
+int64_t orca_kv4_workspace_bytes(const int32_t *host_plan);
+
+/* The three operators are asynchronous on the engine's stream, allocate
+ * nothing and may be captured into a CUDA graph; the engine's device must be
+ * the current one.  Pointers are device pointers (16-byte aligned) but for
+ * host_plan.  Types and sizes come from the plan.
+ *
+ * append: write the k and v columns ([hidden, 3*hidden)) of qkv
+ *   [sum(n_input), 3*hidden] into the rows' slots.  INVALID if two rows of the
+ *   batch share a slot.
+ * read: the values of every request's slots, positions 0 .. ctx_len + n_input
+ *   - 1, requests one after another: out [K|V][n_heads][sum(ctx_len +
+ *   n_input)][head_dim] in the plan's dtype (the layout of a K/V pool layer).
+ * attention: as orca_op_attention, the keys and values being what the slots
+ *   stand for; the rows' own K/V must have been appended.  Scores and sums are
+ *   held in fp32.  Errors: INVALID, CUDA. */
+int orca_op_kv4_append(orca_engine *eng, const void *qkv, void *kv4_layer, const int32_t *host_plan,
+                       const int32_t *dev_plan);
+int orca_op_kv4_read(orca_engine *eng, const void *kv4_layer, const int32_t *host_plan, const int32_t *dev_plan,
+                     void *out);
+int orca_op_kv4_attention(orca_engine *eng, const void *qkv, const void *kv4_layer, const int32_t *host_plan,
+                          int32_t *dev_plan, void *workspace, void *out);
+
+/* ------------------------------------------------------------------------ */
+/* sampling                                                                  */
+/* ------------------------------------------------------------------------ */
+/* One token per row of logits [n_rows][ld] (dtype elements, the first `vocab`
+ * of each row used; vocab <= 2^20, ld >= vocab), from one given uniform number
+ * per row.  Parameters are DEVICE arrays of n_rows entries; a null array means
+ * its default.  With m the row's largest logit and w_i = exp((l_i - m) / T):
+ *   temperature T (1)  0 takes the largest logit (lowest id on ties), ignoring the rest
+ *   top_k (0)          keep the k largest logits (lowest ids on ties); <= 0 or >= vocab keeps all
+ *   top_p (1)          of those, in descending order (ids ascending on ties), the
+ *                      shortest prefix, of at least one, whose mass is >= top_p times theirs
+ *   min_p (0)          of those, the tokens with w_i >= min_p
+ *   uniform u          the first kept id, in ascending order, whose cumulative
+ *                      weight exceeds u times the kept total
+ * The weights are rounded to 42 fraction bits and summed exactly.  Logits of
+ * -inf and NaN are never drawn (a row of nothing else gives -1); +inf leaves
+ * only the +inf logits, equally likely.  Ranges: 0 <= T <= 1e6, top_p and
+ * min_p in [0, 1], u in [0, 1); a row with a value outside (or NaN) gives -1
+ * and a device error (ORCA_ERR_DEVICE_FLAG at the next orca_engine_sync).
+ * Asynchronous on the engine's stream, allocates nothing, may be captured; the
+ * engine's device must be the current one.  Errors: INVALID, CUDA. */
+int orca_op_sample(orca_engine *eng, int32_t dtype, const void *logits, int32_t n_rows, int32_t vocab, int64_t ld,
+                   const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                   const float *uniform, int32_t *out_tokens);
+
+/* ------------------------------------------------------------------------ */
 /* iteration-level scheduler ([houmin] 3.1.1, [0h-n0] scheduler algorithm,    */
 /* [arcsin2] 4.2)                                                            */
 /* ------------------------------------------------------------------------ */

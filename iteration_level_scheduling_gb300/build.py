@@ -23,7 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
-SOURCES = ["engine.cu", "k_gemm_tc.cu", "k_gemm_simt.cu", "k_attn.cu", "k_misc.cu", "sched.cpp"]
+SOURCES = ["engine.cu", "k_gemm_tc.cu", "k_gemm_simt.cu", "k_attn.cu", "k_misc.cu", "k_kv4.cu", "k_sample.cu",
+           "sched.cpp"]
 
 
 def nvcc() -> str:

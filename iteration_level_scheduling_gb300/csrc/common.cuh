@@ -13,6 +13,7 @@ enum : unsigned {
     ERR_WAIT_TIMEOUT = 1u,  // a bounded mbarrier wait expired
     ERR_BAD_TOKEN = 2u,     // token id / feedback index out of range
     ERR_BAD_POS = 4u,       // position outside the position table
+    ERR_BAD_SAMPLE = 16u,   // sampling parameter out of range (8: shared-memory alignment, k_attn.cu)
 };
 
 // Bounded waits give up after this many nanoseconds of %globaltimer.

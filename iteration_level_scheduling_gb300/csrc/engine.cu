@@ -102,7 +102,7 @@ struct orca_engine {
     bool bf = false;
     size_t es = 4;
     cudaStream_t st = nullptr;
-    int num_sms = 148;
+    int num_sms = 148, device = 0;
     bool has_weights = false;
     const void *tok_emb = nullptr, *pos_emb = nullptr;
     const float *lnf_g = nullptr, *lnf_b = nullptr;
@@ -598,6 +598,7 @@ int orca_engine_create(const orca_model_config *cfg, const orca_weights *w, void
         delete E;
         return ORCA_ERR_CUDA;
     }
+    E->device = dev;
     if (w) {
         if (!w->tok_emb || !w->pos_emb || !w->lnf_g || !w->lnf_b || !w->layers) {
             delete E;
@@ -1020,6 +1021,104 @@ int orca_op_linear(orca_engine *E, int32_t dtype, const void *x, const void *w, 
         return ORCA_ERR_CUDA;
     }
     return ORCA_OK;
+}
+
+// ---------------------------------------------------------------------------
+// 4-bit K/V cache and sampling
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kPlanSms = 152;  // SMs a plan made without an engine splits its work for
+bool kv4_shape_ok(int32_t n_heads, int32_t d, int64_t kv_slots) {
+    return n_heads >= 1 && n_heads <= 1024 && (d == 16 || d == 32 || d == 64 || d == 128) && kv_slots >= 1 &&
+           kv_slots <= INT32_MAX - 15;
+}
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// The launches go to the current device: it has to be the engine's.
+bool on_device(const orca_engine *E) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == E->device;
+}
+int launched(orca_engine *E, cudaError_t e) {
+    E->launches++;
+    if (e == cudaSuccess) return ORCA_OK;
+    cudaGetLastError();
+    return ORCA_ERR_CUDA;
+}
+bool kv4_batch(int32_t dtype, int32_t n_heads, int32_t d, int64_t kv_slots, int32_t n_req, const int32_t *n_input,
+               const int32_t *ctx_len, const int64_t *kv_offset, Kv4Batch *b) {
+    if ((dtype != ORCA_DTYPE_FP32 && dtype != ORCA_DTYPE_BF16) || !kv4_shape_ok(n_heads, d, kv_slots) || n_req < 1 ||
+        !n_input || !ctx_len || !kv_offset)
+        return false;
+    *b = {dtype, n_heads, d, n_req, kv_slots, n_input, ctx_len, kv_offset};
+    return true;
+}
+}  // namespace
+
+int64_t orca_kv4_layer_bytes(int32_t n_heads, int32_t head_dim, int64_t kv_slots) {
+    if (!kv4_shape_ok(n_heads, head_dim, kv_slots)) return ORCA_ERR_INVALID;
+    return kv4_layer_bytes(n_heads, head_dim, kv_slots);
+}
+
+int64_t orca_kv4_plan_words(const orca_engine *E, int32_t dtype, int32_t n_heads, int32_t head_dim, int64_t kv_slots,
+                            int32_t n_req, const int32_t *n_input, const int32_t *ctx_len, const int64_t *kv_offset) {
+    Kv4Batch b;
+    if (!kv4_batch(dtype, n_heads, head_dim, kv_slots, n_req, n_input, ctx_len, kv_offset, &b))
+        return ORCA_ERR_INVALID;
+    const int64_t w = kv4_plan_words(b, E ? E->num_sms : kPlanSms);
+    return w < 0 ? ORCA_ERR_INVALID : w;
+}
+
+int orca_kv4_plan_build(const orca_engine *E, int32_t dtype, int32_t n_heads, int32_t head_dim, int64_t kv_slots,
+                        int32_t n_req, const int32_t *n_input, const int32_t *ctx_len, const int64_t *kv_offset,
+                        int32_t *host_buf, int64_t cap_words) {
+    Kv4Batch b;
+    if (!host_buf || !kv4_batch(dtype, n_heads, head_dim, kv_slots, n_req, n_input, ctx_len, kv_offset, &b))
+        return ORCA_ERR_INVALID;
+    try {
+        return kv4_plan_build(b, E ? E->num_sms : kPlanSms, host_buf, cap_words) ? ORCA_OK : ORCA_ERR_INVALID;
+    } catch (const std::bad_alloc &) {
+        return ORCA_ERR_OOM;
+    }
+}
+
+int64_t orca_kv4_workspace_bytes(const int32_t *host_plan) {
+    return kv4_plan_ok(host_plan) ? kv4_workspace_bytes(host_plan) : ORCA_ERR_INVALID;
+}
+
+int orca_op_kv4_append(orca_engine *E, const void *qkv, void *kv4_layer, const int32_t *host_plan,
+                       const int32_t *dev_plan) {
+    if (!E || !qkv || !kv4_layer || !dev_plan || !kv4_plan_ok(host_plan) || !kv4_plan_writes_once(host_plan) ||
+        !aligned16(qkv) || !aligned16(kv4_layer) || !aligned16(dev_plan) || !on_device(E))
+        return ORCA_ERR_INVALID;
+    return launched(E, kv4_append(qkv, kv4_layer, host_plan, dev_plan, E->st));
+}
+
+int orca_op_kv4_read(orca_engine *E, const void *kv4_layer, const int32_t *host_plan, const int32_t *dev_plan,
+                     void *out) {
+    if (!E || !out || !kv4_layer || !dev_plan || !kv4_plan_ok(host_plan) || !aligned16(out) || !aligned16(kv4_layer) ||
+        !aligned16(dev_plan) || !on_device(E))
+        return ORCA_ERR_INVALID;
+    return launched(E, kv4_read(kv4_layer, host_plan, dev_plan, out, E->st));
+}
+
+int orca_op_kv4_attention(orca_engine *E, const void *qkv, const void *kv4_layer, const int32_t *host_plan,
+                          int32_t *dev_plan, void *workspace, void *out) {
+    if (!E || !qkv || !kv4_layer || !dev_plan || !out || !kv4_plan_ok(host_plan) || !aligned16(qkv) ||
+        !aligned16(kv4_layer) || !aligned16(dev_plan) || !aligned16(out) || !aligned16(workspace) ||
+        (!workspace && kv4_workspace_bytes(host_plan) > 0) || !on_device(E))
+        return ORCA_ERR_INVALID;
+    return launched(E, kv4_attention(qkv, kv4_layer, host_plan, dev_plan, workspace, out, E->st));
+}
+
+int orca_op_sample(orca_engine *E, int32_t dtype, const void *logits, int32_t n_rows, int32_t vocab, int64_t ld,
+                   const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                   const float *uniform, int32_t *out_tokens) {
+    if (!E || !logits || !uniform || !out_tokens || n_rows < 0 || vocab < 1 || vocab > (1 << 20) || ld < vocab ||
+        (dtype != ORCA_DTYPE_FP32 && dtype != ORCA_DTYPE_BF16) || !on_device(E))
+        return ORCA_ERR_INVALID;
+    if (n_rows == 0) return ORCA_OK;
+    return launched(E, sample_rows(dtype == ORCA_DTYPE_BF16, logits, ld, n_rows, vocab, temperature, top_k, top_p,
+                                   min_p, uniform, out_tokens, E->d_err, E->st));
 }
 
 }  // extern "C"

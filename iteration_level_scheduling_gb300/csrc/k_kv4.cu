@@ -1,0 +1,564 @@
+// A K/V cache held in 4 bits: quantising rows as they are written, reading
+// slots back, and attention over the held codes.
+//
+// A component x of a group of min(32, head_dim) components of one head of one
+// slot is held as code c with the group's scale s and minimum m (both bf16):
+//   s = bf16((max - min) / 15), m = bf16(min),
+//   c = the integer nearest to (x - m) / s (ties to even) within 0 .. 15,
+// and stands for m + s c.  The differences and the quotient of the scale are
+// taken in fp32; the code is the one real arithmetic gives (below), so it does
+// not depend on how the division rounds.  s = 0 holds c = 0.  A group whose
+// scale or minimum is not finite (an infinity or NaN among its values, or a
+// range beyond fp32) holds s = m = NaN and reads back as NaN.
+//
+// Layout of a layer (S = kv_slots rounded up to 16, G groups per head):
+//   K codes  [head][S][D / 2]      component 2b in the low, 2b + 1 in the high bits of byte b
+//   V codes  [head][S / 2][D / 4]  32-bit words: four components of the even slot in the low
+//                                  half, the same four of the odd slot in the high half
+//   K params [head][S][G]          s in the low, m in the high 16 bits
+//   V params [head][S / 2][G][2]   the same, even slot first
+// K's codes are read along a key (the reduction of q k runs over components);
+// V's reduction runs over keys, so a word pairs the two keys that a tensor-core
+// operand register wants side by side.  A slot is written in 16-bit pieces at
+// least, so no two slots' writers ever share a word to be merged.
+#include <algorithm>
+#include <cfloat>
+#include <cstring>
+#include <vector>
+
+#include "common.cuh"
+#include "kernels.cuh"
+
+namespace orca {
+
+namespace {
+
+constexpr float kLow = -FLT_MAX;
+
+struct Kv4View {
+    uint8_t *kc, *vc;
+    uint32_t *kp, *vp;
+    int64_t S;  // slots, padded
+};
+
+Kv4View kv4_view(const void *layer, int n_heads, int d, int64_t kv_slots) {
+    Kv4View v;
+    const int G = kv4_groups(d);
+    v.S = (kv_slots + 15) / 16 * 16;
+    const int64_t codes = (int64_t)n_heads * v.S * d / 2, params = (int64_t)n_heads * v.S * G;
+    v.kc = (uint8_t *)layer;
+    v.vc = v.kc + codes;
+    v.kp = (uint32_t *)(v.vc + codes);
+    v.vp = v.kp + params;
+    return v;
+}
+
+// min / max that return NaN if either operand is NaN
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ uint32_t bf_bits(float x) { return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+
+// The code of x for scale s > 0 and minimum m.  The fp32 quotient may round
+// onto or across a border k + 1/2, so the candidate is put right with the
+// residual x - m - c s, which is exact: a + e = x - m (a rounded, e its
+// error), and r = a - c s is a difference of near multiples of one grid.
+__device__ __forceinline__ uint32_t kv4_code(float x, float m, float s) {
+    const float a = __fsub_rn(x, m);
+    const float bb = __fsub_rn(x, a);                                            // m as the subtraction saw it
+    const float e = __fadd_rn(__fsub_rn(x, __fadd_rn(a, bb)), __fsub_rn(bb, m));  // x - m = a + e
+    float c = rintf(__fdiv_rn(a, s));
+    c = fminf(fmaxf(c, 0.f), 15.f);
+    const float r = __fmaf_rn(-c, s, a), h = 0.5f * s;
+    const bool odd = ((int)c & 1) != 0;
+    if (r > h || (r == h && (e > 0.f || (e == 0.f && odd)))) c += 1.f;
+    else if (r < -h || (r == -h && (e < 0.f || (e == 0.f && odd)))) c -= 1.f;
+    return (uint32_t)fminf(fmaxf(c, 0.f), 15.f);
+}
+
+// ---------------------------------------------------------------------------
+// write: k and v of every row, one thread per 8 components
+// ---------------------------------------------------------------------------
+constexpr int kApThreads = 128;
+
+template <typename T>
+__global__ void __launch_bounds__(kApThreads) kv4_append_kernel(const T *qkv, const int32_t *row_slot, Kv4View v, int H,
+                                                                int d, int G, int gt) {
+    pdl_trigger();
+    pdl_wait();
+    const int r = blockIdx.x;
+    const int64_t slot = row_slot[r];
+    const int u = blockIdx.y * kApThreads + threadIdx.x;  // 8-component unit of k, then v
+    const bool on = u * 8 < 2 * H;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    if (on) {
+        const T *src = qkv + (size_t)r * 3 * H + H + (size_t)u * 8;
+#pragma unroll
+        for (int i = 0; i < 8; i += Elem<T>::kPer16) load16_stream(src + i, x + i);
+    }
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) lo = min_nan(lo, x[i]), hi = max_nan(hi, x[i]);
+    // the group's 2 or 4 threads (gt) are neighbours; units of k and v and of heads never share a group
+    for (int o = 1; o < gt; o <<= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    if (!on) return;
+    uint32_t sb = bf_bits(__fdiv_rn(__fsub_rn(hi, lo), 15.f)), mb = bf_bits(lo);
+    const bool fine = (sb & 0x7f80u) != 0x7f80u && (mb & 0x7f80u) != 0x7f80u;
+    if (!fine) sb = mb = 0x7fc0u;
+    const float s = bf_lo(sb), m = bf_lo(mb);
+    uint32_t w = 0;
+    if (fine && s > 0.f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w |= kv4_code(x[i], m, s) << (4 * i);
+    }
+    const int c = u * 8, which = c >= H, cc = c - which * H, h = cc / d, dd = cc - h * d;
+    const uint32_t par = sb | (mb << 16);
+    const bool lead = (u % gt) == 0;
+    const int g = dd / (8 * gt);
+    if (!which) {
+        *reinterpret_cast<uint32_t *>(v.kc + ((int64_t)h * v.S + slot) * (d / 2) + dd / 2) = w;
+        if (lead) v.kp[((int64_t)h * v.S + slot) * G + g] = par;
+    } else {
+        const int64_t pair = (int64_t)h * (v.S / 2) + (slot >> 1);
+        uint16_t *dst = reinterpret_cast<uint16_t *>(v.vc + (pair * (d / 4) + dd / 4) * 4) + (slot & 1);
+        dst[0] = (uint16_t)w;
+        dst[2] = (uint16_t)(w >> 16);
+        if (lead) v.vp[(pair * G + g) * 2 + (slot & 1)] = par;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// read back: tiles of up to 64 slots of one range, one head's K and V per CTA
+// ---------------------------------------------------------------------------
+constexpr int kRdThreads = 128;
+
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float *x) {
+#pragma unroll
+    for (int i = 0; i < 8; i += Elem<T>::kPer16) store16(p + i, x + i);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRdThreads) kv4_read_kernel(Kv4View v, const int32_t *tiles, T *out, int64_t out_slots,
+                                                              int n_heads, int d, int G) {
+    pdl_trigger();
+    pdl_wait();
+    const int4 tl = reinterpret_cast<const int4 *>(tiles)[blockIdx.x];  // first slot, slots, first output index
+    const int h = blockIdx.y, gs = d / G, upr = d / 8;                  // 8-component units per row
+    const int64_t s0 = tl.x, s1 = s0 + tl.y;
+    T *ko = out + ((int64_t)h * out_slots + tl.z) * d, *vo = ko + (int64_t)n_heads * out_slots * d;
+    for (int i = threadIdx.x; i < tl.y * upr; i += kRdThreads) {
+        const int j = i / upr, u = i - j * upr;
+        const int64_t row = (int64_t)h * v.S + s0 + j;
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(v.kc + row * (d / 2) + u * 4);
+        const uint32_t p = v.kp[row * G + u * 8 / gs];
+        const float s = bf_lo(p), m = bf_hi(p);
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = fmaf(s, (float)((w >> (4 * k)) & 15u), m);
+        store8(ko + (int64_t)j * d + u * 8, x);
+    }
+    const int64_t p0 = s0 >> 1, np = ((s1 + 1) >> 1) - p0;
+    for (int i = threadIdx.x; i < (int)np * upr; i += kRdThreads) {
+        const int j = i / upr, u = i - j * upr;
+        const int64_t pair = (int64_t)h * (v.S / 2) + p0 + j;
+        const uint2 w = *reinterpret_cast<const uint2 *>(v.vc + (pair * (d / 4) + u * 2) * 4);
+        const uint2 p = *reinterpret_cast<const uint2 *>(v.vp + (pair * G + u * 8 / gs) * 2);
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            const int64_t slot = 2 * (p0 + j) + o;
+            if (slot < s0 || slot >= s1) continue;
+            const uint32_t a = w.x >> (16 * o), b = w.y >> (16 * o), pp = o ? p.y : p.x;
+            const float s = bf_lo(pp), m = bf_hi(pp);
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[k] = fmaf(s, (float)((a >> (4 * k)) & 15u), m);
+                x[4 + k] = fmaf(s, (float)((b >> (4 * k)) & 15u), m);
+            }
+            store8(vo + (slot - s0) * d + u * 8, x);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// attention of single rows: item = (row, chunk of its keys) x head, four warps
+// ---------------------------------------------------------------------------
+constexpr int kKvThreads = 128, kKvWarps = 4;
+
+struct Kv4Attn {
+    const void *qkv;
+    void *out;
+    Kv4View v;
+    int H, n_heads;
+    float scale_log2;
+    const int32_t *items;  // 8 words: first slot, keys, row, chunks of the row, this chunk, the row's first partial, its counter
+    int *counters;         // [row counter][head], zero between launches
+    float *part;           // [partial][head][D + 2]
+};
+
+template <int D>
+struct Kv4Merge {
+    float m[kKvWarps], l[kKvWarps], o[kKvWarps][D];
+    int last;
+};
+
+// The four warps' states (each already in sm) -> the row's output, or this
+// chunk's partial; the last chunk to arrive joins all of them in chunk order,
+// so the result does not depend on which that is.
+template <typename T, int D>
+__device__ __forceinline__ void kv4_finish(const Kv4Attn &a, Kv4Merge<D> &sm, const int4 &r0, const int4 &r1, int h) {
+    __syncthreads();
+    const int tid = threadIdx.x;
+    float M = kLow, L = 0.f, O = 0.f, c[kKvWarps];
+#pragma unroll
+    for (int w = 0; w < kKvWarps; ++w) M = fmaxf(M, sm.m[w]);
+#pragma unroll
+    for (int w = 0; w < kKvWarps; ++w) c[w] = exp2f(sm.m[w] - M), L += sm.l[w] * c[w];
+    if (tid < D) {
+#pragma unroll
+        for (int w = 0; w < kKvWarps; ++w) O += sm.o[w][tid] * c[w];
+    }
+    T *dst = (T *)a.out + (size_t)r0.z * a.H + h * D;
+    const int nch = r0.w;
+    if (nch == 1) {
+        if (tid < D) dst[tid] = Elem<T>::from_f(O / L);
+        return;
+    }
+    float *mine = a.part + ((size_t)(r1.y + r1.x) * a.n_heads + h) * (D + 2);
+    if (tid < D) mine[tid] = O;
+    if (tid == 0) mine[D] = M, mine[D + 1] = L;
+    __syncthreads();
+    if (tid == 0) {
+        int *cnt = a.counters + (size_t)r1.z * a.n_heads + h;
+        __threadfence();
+        const int last = atom_add_acq_rel(cnt, 1) == nch - 1;
+        if (last) *cnt = 0;
+        sm.last = last;
+    }
+    __syncthreads();
+    if (!sm.last) return;
+    __threadfence();
+    float Mt = kLow, Lt = 0.f, Ot = 0.f;
+    for (int j = 0; j < nch; ++j) {
+        const float *pj = a.part + ((size_t)(r1.y + j) * a.n_heads + h) * (D + 2);
+        const float pm = __ldcg(pj + D), pl = __ldcg(pj + D + 1), po = tid < D ? __ldcg(pj + tid) : 0.f;
+        const float mn = fmaxf(Mt, pm), co = exp2f(Mt - mn), cn = exp2f(pm - mn);
+        Lt = Lt * co + pl * cn;
+        Ot = Ot * co + po * cn;
+        Mt = mn;
+    }
+    if (tid < D) dst[tid] = Elem<T>::from_f(Ot / Lt);
+}
+
+// Any type and head_dim, fp32 arithmetic.  A warp takes 32 slots at a time:
+// for the scores a lane owns a key and walks its components against q in
+// shared memory; for the values a lane owns four components and walks the
+// keys, two per word.
+template <typename T, int D>
+__global__ void __launch_bounds__(kKvThreads) kv4_decode_kernel(const Kv4Attn a) {
+    constexpr int G = D / 32 > 0 ? D / 32 : 1, GS = D / G;
+    constexpr int LP = D / 4, PP = 32 / LP;  // lanes per pair of keys, pairs per step
+    __shared__ Kv4Merge<D> sm;
+    __shared__ float q[D];
+    __shared__ float qs[G];
+    pdl_trigger();
+    pdl_wait();
+    const int4 r0 = reinterpret_cast<const int4 *>(a.items)[2 * blockIdx.x],
+               r1 = reinterpret_cast<const int4 *>(a.items)[2 * blockIdx.x + 1];
+    const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x < D)
+        q[threadIdx.x] = Elem<T>::to_f(((const T *)a.qkv)[(size_t)r0.z * 3 * a.H + h * D + threadIdx.x]) * a.scale_log2;
+    __syncthreads();
+    if (threadIdx.x < G) {
+        float s = 0.f;
+        for (int i = 0; i < GS; ++i) s += q[threadIdx.x * GS + i];
+        qs[threadIdx.x] = s;
+    }
+    __syncthreads();
+    const int64_t s0 = r0.x, s1 = s0 + r0.y;
+    const int sub = lane % LP, grp = lane / LP;
+    float m = kLow, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int64_t b = (s0 & ~int64_t(1)) + 32 * warp; b < s1; b += 32 * kKvWarps) {
+        const int64_t slot = b + lane;
+        const bool valid = slot >= s0 && slot < s1;
+        float sc = kLow;
+        if (valid) {
+            const int64_t row = (int64_t)h * a.v.S + slot;
+            sc = 0.f;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const uint32_t p = a.v.kp[row * G + g];
+                float acc = 0.f;
+#pragma unroll
+                for (int w = 0; w < GS / 8; ++w) {
+                    const uint32_t x =
+                        *reinterpret_cast<const uint32_t *>(a.v.kc + row * (D / 2) + g * (GS / 2) + w * 4);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) acc = fmaf(q[g * GS + w * 8 + k], (float)((x >> (4 * k)) & 15u), acc);
+                }
+                sc += bf_lo(p) * acc + bf_hi(p) * qs[g];
+            }
+        }
+        float mx = sc;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        mx = fmaxf(mx, m);
+        const float corr = exp2f(m - mx);
+        m = mx;
+        const float p = valid ? exp2f(sc - m) : 0.f;
+        l = l * corr + p;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] *= corr;
+#pragma unroll 4
+        for (int j = 0; j < 16; j += PP) {
+            const int pr = j + grp;  // this lane's pair
+            const float pe = __shfl_sync(0xffffffffu, p, 2 * pr), po = __shfl_sync(0xffffffffu, p, 2 * pr + 1);
+            const int64_t se = b + 2 * pr;
+            const bool ve = se >= s0 && se < s1, vo = se + 1 >= s0 && se + 1 < s1;
+            if (!ve && !vo) continue;
+            const int64_t pair = (int64_t)h * (a.v.S / 2) + (se >> 1);
+            const uint32_t x = *reinterpret_cast<const uint32_t *>(a.v.vc + (pair * (D / 4) + sub) * 4);
+            const uint2 pp = *reinterpret_cast<const uint2 *>(a.v.vp + (pair * G + sub * 4 / GS) * 2);
+            // (an unused slot's parameters may be anything)
+            const float ws = ve ? pe * bf_lo(pp.x) : 0.f, wm = ve ? pe * bf_hi(pp.x) : 0.f;
+            const float xs = vo ? po * bf_lo(pp.y) : 0.f, xm = vo ? po * bf_hi(pp.y) : 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                o[k] += fmaf(ws, (float)((x >> (4 * k)) & 15u), wm) + fmaf(xs, (float)((x >> (16 + 4 * k)) & 15u), xm);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+#pragma unroll
+    for (int off = LP; off < 32; off <<= 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] += __shfl_xor_sync(0xffffffffu, o[k], off);
+    if (grp == 0)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sm.o[warp][4 * sub + k] = o[k];
+    if (lane == 0) sm.m[warp] = m, sm.l[warp] = l;
+    kv4_finish<T, D>(a, sm, r0, r1, h);
+}
+
+template <typename T>
+cudaError_t launch_decode(const Kv4Attn &a, int d, int n_items, cudaStream_t st) {
+    const dim3 grid(n_items, a.n_heads), block(kKvThreads);
+    switch (d) {
+        case 16: return launch_pdl(kv4_decode_kernel<T, 16>, grid, block, 0, st, a);
+        case 32: return launch_pdl(kv4_decode_kernel<T, 32>, grid, block, 0, st, a);
+        case 64: return launch_pdl(kv4_decode_kernel<T, 64>, grid, block, 0, st, a);
+        case 128: return launch_pdl(kv4_decode_kernel<T, 128>, grid, block, 0, st, a);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// plans
+// ---------------------------------------------------------------------------
+constexpr int32_t kKv4Magic = 0x4B563450;
+constexpr int kKv4Hdr = 32;
+constexpr int kReadTile = 64;  // slots per read-back tile
+enum : int {
+    Q_MAGIC = 0,
+    Q_DTYPE,
+    Q_HEADS,
+    Q_DIM,
+    Q_SLOTS,
+    Q_ROWS,
+    Q_ITEMS,     // work items of single rows
+    Q_SPLITS,    // rows whose keys span several items
+    Q_PARTS,     // partials of those rows
+    Q_TILES,     // read-back tiles
+    Q_KEYS,      // keys of all requests
+    Q_TWICE,     // a slot is written by two rows of the batch
+    Q_TOTAL,
+    Q_O_ROWSLOT,  // word offsets of the tables
+    Q_O_ITEMS,
+    Q_O_COUNT,
+    Q_O_TILES,
+};
+
+int64_t up4(int64_t w) { return (w + 3) & ~int64_t(3); }
+
+struct Kv4Sizes {
+    int64_t rows = 0, items = 0, splits = 0, parts = 0, tiles = 0, keys = 0;
+    int chunk = 0;
+    int64_t off_rowslot, off_items, off_count, off_tiles, total;
+};
+
+// Keys per work item: the largest chunk (a power of two, 64 .. 2048 keys) that
+// still gives every SM several blocks of four warps; short chunks cost a join,
+// long ones leave SMs idle.
+int kv4_chunk(int n_req, const int32_t *n_input, const int32_t *ctx, int n_heads, int num_sms) {
+    int chunk = 2048;
+    while (chunk > 64) {
+        int64_t items = 0;
+        for (int i = 0; i < n_req && items * n_heads < 6LL * num_sms; ++i)
+            items += (int64_t)n_input[i] * ((ctx[i] + (int64_t)n_input[i] + chunk - 1) / chunk);
+        if (items * n_heads >= 6LL * num_sms) break;
+        chunk /= 2;
+    }
+    return chunk;
+}
+
+bool kv4_sizes(const Kv4Batch &b, int num_sms, Kv4Sizes *z) {
+    int64_t rows = 0;
+    for (int i = 0; i < b.n_req; ++i) {
+        const int64_t n = b.n_input[i], c = b.ctx_len[i], o = b.kv_offset[i];
+        if (n < 1 || c < 0 || o < 0 || o > b.kv_slots || o + c + n > b.kv_slots) return false;
+        rows += n;
+        if (rows > INT32_MAX / 8) return false;
+    }
+    z->chunk = kv4_chunk(b.n_req, b.n_input, b.ctx_len, b.n_heads, num_sms);
+    for (int i = 0; i < b.n_req; ++i) {
+        const int64_t n = b.n_input[i], c = b.ctx_len[i];
+        z->rows += n;
+        z->keys += c + n;
+        z->tiles += (c + n + kReadTile - 1) / kReadTile;
+        for (int64_t j = 0; j < n; ++j) {
+            const int64_t nch = (c + j + 1 + z->chunk - 1) / z->chunk;
+            z->items += nch;
+            if (nch > 1) z->splits++, z->parts += nch;
+        }
+    }
+    int64_t w = kKv4Hdr;
+    z->off_rowslot = w, w = up4(w + z->rows);
+    z->off_items = w, w = up4(w + 8 * z->items);
+    z->off_count = w, w = up4(w + z->splits * b.n_heads);
+    z->off_tiles = w, w = up4(w + 4 * z->tiles);
+    z->total = w;
+    // 32-bit table entries and grid sizes
+    return w <= INT32_MAX && z->keys <= INT32_MAX && z->rows <= INT32_MAX / 4;
+}
+
+}  // namespace
+
+int kv4_groups(int head_dim) { return head_dim >= 32 ? head_dim / 32 : 1; }
+
+int64_t kv4_layer_bytes(int n_heads, int head_dim, int64_t kv_slots) {
+    const int64_t S = (kv_slots + 15) / 16 * 16;
+    return n_heads * S * (head_dim + 8 * (int64_t)kv4_groups(head_dim));
+}
+
+int64_t kv4_plan_words(const Kv4Batch &b, int num_sms) {
+    Kv4Sizes z;
+    return kv4_sizes(b, num_sms, &z) ? z.total : -1;
+}
+
+bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
+    Kv4Sizes z;
+    if (!kv4_sizes(b, num_sms, &z) || cap < z.total) return false;
+    std::memset(buf, 0, sizeof(int32_t) * (size_t)z.total);  // (the device copy's counters start at zero)
+    int32_t *slot = buf + z.off_rowslot, *it = buf + z.off_items, *tl = buf + z.off_tiles;
+    int64_t row = 0, split = 0, part = 0, key = 0;
+    for (int i = 0; i < b.n_req; ++i) {
+        const int64_t n = b.n_input[i], c = b.ctx_len[i], o = b.kv_offset[i];
+        for (int64_t j = 0; j < n; ++j, ++row) {
+            slot[row] = (int32_t)(o + c + j);
+            const int64_t keys = c + j + 1, nch = (keys + z.chunk - 1) / z.chunk;
+            for (int64_t k = 0; k < nch; ++k, it += 8) {
+                it[0] = (int32_t)(o + k * z.chunk);
+                it[1] = (int32_t)std::min<int64_t>(z.chunk, keys - k * z.chunk);
+                it[2] = (int32_t)row;
+                it[3] = (int32_t)nch;
+                it[4] = (int32_t)k;
+                it[5] = (int32_t)part;
+                it[6] = (int32_t)split;
+            }
+            if (nch > 1) ++split, part += nch;
+        }
+        for (int64_t t = 0; t < c + n; t += kReadTile, tl += 4) {
+            tl[0] = (int32_t)(o + t);
+            tl[1] = (int32_t)std::min<int64_t>(kReadTile, c + n - t);
+            tl[2] = (int32_t)(key + t);
+        }
+        key += c + n;
+    }
+    // slots written by two rows
+    std::vector<std::pair<int64_t, int64_t>> w((size_t)b.n_req);
+    for (int i = 0; i < b.n_req; ++i)
+        w[i] = {b.kv_offset[i] + b.ctx_len[i], b.kv_offset[i] + b.ctx_len[i] + b.n_input[i]};
+    std::sort(w.begin(), w.end());
+    bool twice = false;
+    for (int i = 1; i < b.n_req; ++i) twice |= w[i].first < w[i - 1].second;
+    buf[Q_MAGIC] = kKv4Magic;
+    buf[Q_DTYPE] = b.dtype;
+    buf[Q_HEADS] = b.n_heads;
+    buf[Q_DIM] = b.head_dim;
+    buf[Q_SLOTS] = (int32_t)b.kv_slots;
+    buf[Q_ROWS] = (int32_t)z.rows;
+    buf[Q_ITEMS] = (int32_t)z.items;
+    buf[Q_SPLITS] = (int32_t)z.splits;
+    buf[Q_PARTS] = (int32_t)z.parts;
+    buf[Q_TILES] = (int32_t)z.tiles;
+    buf[Q_KEYS] = (int32_t)z.keys;
+    buf[Q_TWICE] = twice;
+    buf[Q_TOTAL] = (int32_t)z.total;
+    buf[Q_O_ROWSLOT] = (int32_t)z.off_rowslot;
+    buf[Q_O_ITEMS] = (int32_t)z.off_items;
+    buf[Q_O_COUNT] = (int32_t)z.off_count;
+    buf[Q_O_TILES] = (int32_t)z.off_tiles;
+    return true;
+}
+
+bool kv4_plan_ok(const int32_t *hp) { return hp && hp[Q_MAGIC] == kKv4Magic; }
+bool kv4_plan_writes_once(const int32_t *hp) { return !hp[Q_TWICE]; }
+
+int64_t kv4_workspace_bytes(const int32_t *hp) {
+    return (int64_t)hp[Q_PARTS] * hp[Q_HEADS] * (hp[Q_DIM] + 2) * 4;
+}
+
+cudaError_t kv4_append(const void *qkv, void *layer, const int32_t *hp, const int32_t *dp, cudaStream_t st) {
+    const int nh = hp[Q_HEADS], d = hp[Q_DIM], H = nh * d, G = kv4_groups(d), gt = d / G / 8;
+    const Kv4View v = kv4_view(layer, nh, d, hp[Q_SLOTS]);
+    const dim3 grid(hp[Q_ROWS], (2 * H / 8 + kApThreads - 1) / kApThreads);
+    if (hp[Q_DTYPE] == 1)
+        return launch_pdl(kv4_append_kernel<bf16>, grid, dim3(kApThreads), 0, st, (const bf16 *)qkv,
+                          dp + hp[Q_O_ROWSLOT], v, H, d, G, gt);
+    return launch_pdl(kv4_append_kernel<float>, grid, dim3(kApThreads), 0, st, (const float *)qkv, dp + hp[Q_O_ROWSLOT],
+                      v, H, d, G, gt);
+}
+
+cudaError_t kv4_read(const void *layer, const int32_t *hp, const int32_t *dp, void *out, cudaStream_t st) {
+    const int nh = hp[Q_HEADS], d = hp[Q_DIM], G = kv4_groups(d);
+    const Kv4View v = kv4_view(layer, nh, d, hp[Q_SLOTS]);
+    const dim3 grid(hp[Q_TILES], nh);
+    if (hp[Q_DTYPE] == 1)
+        return launch_pdl(kv4_read_kernel<bf16>, grid, dim3(kRdThreads), 0, st, v, dp + hp[Q_O_TILES], (bf16 *)out,
+                          (int64_t)hp[Q_KEYS], nh, d, G);
+    return launch_pdl(kv4_read_kernel<float>, grid, dim3(kRdThreads), 0, st, v, dp + hp[Q_O_TILES], (float *)out,
+                      (int64_t)hp[Q_KEYS], nh, d, G);
+}
+
+cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp, int32_t *dp, void *workspace,
+                          void *out, cudaStream_t st) {
+    const int nh = hp[Q_HEADS], d = hp[Q_DIM];
+    Kv4Attn a;
+    a.qkv = qkv;
+    a.out = out;
+    a.v = kv4_view(layer, nh, d, hp[Q_SLOTS]);
+    a.H = nh * d;
+    a.n_heads = nh;
+    a.scale_log2 = 1.4426950408889634f / sqrtf((float)d);
+    a.items = dp + hp[Q_O_ITEMS];
+    a.counters = dp + hp[Q_O_COUNT];
+    a.part = (float *)workspace;
+    return hp[Q_DTYPE] == 1 ? launch_decode<bf16>(a, d, hp[Q_ITEMS], st) : launch_decode<float>(a, d, hp[Q_ITEMS], st);
+}
+
+}  // namespace orca

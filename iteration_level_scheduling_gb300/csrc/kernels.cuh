@@ -156,6 +156,32 @@ void decode_items(const int32_t *order, const int32_t *dec_work, int n_work, con
 // next[b] = argmax_j logits[b, j] (lowest j on ties); also to out2 if non-null.
 cudaError_t argmax_rows(const float *logits, int n_rows, int V, int32_t *next, int32_t *out2, cudaStream_t st);
 
+// Sampled token of every row (k_sample.cu); parameter arrays on the device, null = off.
+cudaError_t sample_rows(int dtype_bf16, const void *logits, int64_t ld, int n_rows, int V, const float *temperature,
+                        const int32_t *top_k, const float *top_p, const float *min_p, const float *uniform,
+                        int32_t *out, unsigned *err, cudaStream_t st);
+
+// 4-bit K/V cache (k_kv4.cu).  A batch of ranges over one layer, and the plan
+// built from it (int32 words; the device copy also holds arrival counters,
+// zero between launches).
+struct Kv4Batch {
+    int dtype, n_heads, head_dim, n_req;
+    int64_t kv_slots;
+    const int32_t *n_input, *ctx_len;
+    const int64_t *kv_offset;
+};
+int kv4_groups(int head_dim);
+int64_t kv4_layer_bytes(int n_heads, int head_dim, int64_t kv_slots);
+int64_t kv4_plan_words(const Kv4Batch &b, int num_sms);  // -1: a range is empty or leaves the layer, or it is too large
+bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap);
+bool kv4_plan_ok(const int32_t *hp);
+bool kv4_plan_writes_once(const int32_t *hp);
+int64_t kv4_workspace_bytes(const int32_t *hp);
+cudaError_t kv4_append(const void *qkv, void *layer, const int32_t *hp, const int32_t *dp, cudaStream_t st);
+cudaError_t kv4_read(const void *layer, const int32_t *hp, const int32_t *dp, void *out, cudaStream_t st);
+cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp, int32_t *dp, void *workspace,
+                          void *out, cudaStream_t st);
+
 constexpr int kPrefillRowsPerTile = 128;  // query rows per prefill tile (the tcgen05 kernel's M)
 
 // A bounded wait that nothing satisfies, given up after limit_ns (failure-

@@ -32,7 +32,9 @@ EXPORTS = [
     "orca_engine_sync", "orca_get_last_hidden", "orca_get_last_logits", "orca_engine_stats_get",
     "orca_engine_timing", "orca_engine_timing_read", "orca_op_linear", "orca_op_attention", "orca_packed_weight_elems",
     "orca_pack_weight",
-    "orca_attention_decode_noalloc", "orca_debug_expire_wait", "orca_sched_create", "orca_sched_destroy",
+    "orca_attention_decode_noalloc", "orca_kv4_layer_bytes", "orca_kv4_plan_words", "orca_kv4_plan_build",
+    "orca_kv4_workspace_bytes", "orca_op_kv4_append", "orca_op_kv4_read", "orca_op_kv4_attention", "orca_op_sample",
+    "orca_debug_expire_wait", "orca_sched_create", "orca_sched_destroy",
     "orca_sched_submit", "orca_sched_set_token_feedback", "orca_sched_next", "orca_sched_complete", "orca_sched_cancel",
     "orca_sched_stats_get", "orca_sched_request_get",
     "orca_sched_request_tokens", "orca_sched_run",
@@ -125,6 +127,15 @@ _sig = {
     "orca_op_attention": (C.c_int, [P, C.c_int32, P, P, C.c_int64, C.c_int32, C.c_int32, C.c_int32, P, P, P, P]),
     "orca_attention_decode_noalloc": (C.c_int, [C.c_int32, P, P, C.c_int64, C.c_int32, C.c_int32, C.c_int32, P, P,
                                                 P, P]),
+    "orca_kv4_layer_bytes": (C.c_int64, [C.c_int32, C.c_int32, C.c_int64]),
+    "orca_kv4_plan_words": (C.c_int64, [P, C.c_int32, C.c_int32, C.c_int32, C.c_int64, C.c_int32, P, P, P]),
+    "orca_kv4_plan_build": (C.c_int, [P, C.c_int32, C.c_int32, C.c_int32, C.c_int64, C.c_int32, P, P, P, P,
+                                      C.c_int64]),
+    "orca_kv4_workspace_bytes": (C.c_int64, [P]),
+    "orca_op_kv4_append": (C.c_int, [P, P, P, P, P]),
+    "orca_op_kv4_read": (C.c_int, [P, P, P, P, P]),
+    "orca_op_kv4_attention": (C.c_int, [P, P, P, P, P, P, P]),
+    "orca_op_sample": (C.c_int, [P, C.c_int32, P, C.c_int32, C.c_int32, C.c_int64, P, P, P, P, P, P]),
     "orca_debug_expire_wait": (C.c_int, [P, C.c_int64]),
     "orca_sched_create": (C.c_int, [C.POINTER(SchedConfig), P, C.POINTER(P)]),
     "orca_sched_destroy": (C.c_int, [P]),
@@ -310,6 +321,53 @@ class Engine:
                                     _ptr(n), _ptr(c), _ptr(o), P(out)), "orca_op_attention")
         if sync:
             self.sync()
+
+    def kv4_plan(self, dtype: int, n_heads: int, head_dim: int, kv_slots: int, n_input, ctx_len,
+                 kv_offset) -> np.ndarray:
+        """Plan of a batch over a 4-bit K/V layer (see orca.h): int32 words, to be copied to the device once."""
+        n, c, o = _attn_host_arrays(n_input, ctx_len, kv_offset)
+        if not len(n) == len(c) == len(o):
+            raise ValueError("n_input, ctx_len and kv_offset differ in length")
+        a = (self._h, dtype, n_heads, head_dim, kv_slots, len(n), _ptr(n), _ptr(c), _ptr(o))
+        buf = np.zeros(check(lib.orca_kv4_plan_words(*a), "orca_kv4_plan_words"), np.int32)
+        check(lib.orca_kv4_plan_build(*a, _ptr(buf), buf.size), "orca_kv4_plan_build")
+        return buf
+
+    @staticmethod
+    def kv4_workspace_bytes(plan: np.ndarray) -> int:
+        return check(lib.orca_kv4_workspace_bytes(_ptr(plan)), "orca_kv4_workspace_bytes")
+
+    def op_kv4_append(self, qkv: int, layer: int, plan: np.ndarray, dev_plan: int, sync: bool = True):
+        check(lib.orca_op_kv4_append(self._h, P(qkv), P(layer), _ptr(plan), P(dev_plan)), "orca_op_kv4_append")
+        if sync:
+            self.sync()
+
+    def op_kv4_read(self, layer: int, plan: np.ndarray, dev_plan: int, out: int, sync: bool = True):
+        check(lib.orca_op_kv4_read(self._h, P(layer), _ptr(plan), P(dev_plan), P(out)), "orca_op_kv4_read")
+        if sync:
+            self.sync()
+
+    def op_kv4_attention(self, qkv: int, layer: int, plan: np.ndarray, dev_plan: int, workspace: int, out: int,
+                         sync: bool = True):
+        check(lib.orca_op_kv4_attention(self._h, P(qkv), P(layer), _ptr(plan), P(dev_plan), P(workspace or None),
+                                        P(out)), "orca_op_kv4_attention")
+        if sync:
+            self.sync()
+
+    def op_sample(self, dtype: int, logits: int, n_rows: int, vocab: int, out_tokens: int, uniform: int,
+                  temperature: int = 0, top_k: int = 0, top_p: int = 0, min_p: int = 0, ld: int = 0,
+                  sync: bool = True):
+        """Sampled tokens of n_rows logits rows (device pointers; parameter arrays may be left out, see orca.h)."""
+        check(lib.orca_op_sample(self._h, dtype, P(logits), n_rows, vocab, ld or vocab, P(temperature or None),
+                                 P(top_k or None), P(top_p or None), P(min_p or None), P(uniform), P(out_tokens)),
+              "orca_op_sample")
+        if sync:
+            self.sync()
+
+
+def kv4_layer_bytes(n_heads: int, head_dim: int, kv_slots: int) -> int:
+    """Bytes of one layer of a 4-bit K/V cache (see orca.h)."""
+    return check(lib.orca_kv4_layer_bytes(n_heads, head_dim, kv_slots), "orca_kv4_layer_bytes")
 
 
 def _attn_host_arrays(n_input, ctx_len, kv_offset):

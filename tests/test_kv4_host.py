@@ -1,0 +1,102 @@
+"""Host side of the 4-bit K/V cache and of sampling: sizes, plans and refusals.  No GPU."""
+
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from iteration_level_scheduling_gb300 import build
+from oracle import kv4
+
+
+@pytest.fixture(scope="module")
+def native():
+    build.build()
+    from iteration_level_scheduling_gb300 import native as n
+    return n
+
+
+def words(native, dtype=1, heads=4, d=64, slots=100, n=(1,), c=(10,), o=(3,), eng=None):
+    n, c, o = np.array(n, np.int32), np.array(c, np.int32), np.array(o, np.int64)
+    return native.lib.orca_kv4_plan_words(eng, dtype, heads, d, slots, len(n), n.ctypes.data, c.ctypes.data,
+                                          o.ctypes.data)
+
+
+def plan(native, dtype=1, heads=4, d=64, slots=100, n=(1,), c=(10,), o=(3,)):
+    w = words(native, dtype, heads, d, slots, n, c, o)
+    assert w > 0
+    buf = np.zeros(w, np.int32)
+    n, c, o = np.array(n, np.int32), np.array(c, np.int32), np.array(o, np.int64)
+    assert native.lib.orca_kv4_plan_build(None, dtype, heads, d, slots, len(n), n.ctypes.data, c.ctypes.data,
+                                          o.ctypes.data, buf.ctypes.data, w) == 0
+    return buf
+
+
+@pytest.mark.parametrize("heads,d,slots", [(1, 16, 1), (3, 32, 17), (40, 128, 4096), (7, 64, 15)])
+def test_layer_bytes(native, heads, d, slots):
+    S, G = (slots + 15) // 16 * 16, max(1, d // 32)
+    want = 2 * heads * S * (d // 2 + 4 * G)
+    assert native.kv4_layer_bytes(heads, d, slots) == want
+    kv4.Layer(heads, d, slots, np.zeros(want, np.uint8))
+
+
+@pytest.mark.parametrize("bad", [(0, 64, 10), (1025, 64, 10), (4, 48, 10), (4, 256, 10), (4, 64, 0),
+                                 (4, 64, 2 ** 31 - 1)])
+def test_layer_bytes_refusals(native, bad):
+    with pytest.raises(native.OrcaError) as e:
+        native.kv4_layer_bytes(*bad)
+    assert e.value.code == native.ERR_INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dtype=2), dict(heads=0), dict(d=20), dict(slots=0),
+    dict(n=(0,)), dict(c=(-1,)), dict(o=(-1,)), dict(slots=13), dict(o=(2 ** 40,)),
+    dict(n=(1, 2 ** 31 - 1), c=(0, 0), o=(0, 1), slots=2 ** 31 - 16),  # tables beyond 32-bit offsets
+])
+def test_plan_refusals(native, kw):
+    assert words(native, **kw) == native.ERR_INVALID
+
+
+def test_plan_null_arrays_and_short_buffer(native):
+    a = np.array([1], np.int32)
+    o = np.array([0], np.int64)
+    args = [None, 1, 4, 64, 100, 1, a.ctypes.data, a.ctypes.data, o.ctypes.data]
+    w = native.lib.orca_kv4_plan_words(*args)
+    buf = np.zeros(w, np.int32)
+    assert native.lib.orca_kv4_plan_build(*args, buf.ctypes.data, w - 1) == native.ERR_INVALID
+    assert not buf.any()
+    assert native.lib.orca_kv4_plan_build(*args, None, w) == native.ERR_INVALID
+    for i in (6, 7, 8):
+        bad = list(args)
+        bad[i] = None
+        assert native.lib.orca_kv4_plan_words(*bad) == native.ERR_INVALID
+    args[5] = 0
+    assert native.lib.orca_kv4_plan_words(*args) == native.ERR_INVALID
+
+
+def test_workspace_of_something_else(native):
+    junk = np.zeros(64, np.int32)
+    assert native.lib.orca_kv4_workspace_bytes(junk.ctypes.data) == native.ERR_INVALID
+    assert native.lib.orca_kv4_workspace_bytes(None) == native.ERR_INVALID
+
+
+def test_operators_need_an_engine(native):
+    p = plan(native)
+    assert native.lib.orca_op_kv4_append(None, 16, 16, p.ctypes.data, 16) == native.ERR_INVALID
+    assert native.lib.orca_op_kv4_read(None, 16, p.ctypes.data, 16, 16) == native.ERR_INVALID
+    assert native.lib.orca_op_kv4_attention(None, 16, 16, p.ctypes.data, 16, 16, 16) == native.ERR_INVALID
+    assert native.lib.orca_op_sample(None, 0, 16, 1, 10, 10, None, None, None, None, 16, 16) == native.ERR_INVALID
+
+
+def test_oracle_quantise_ties_and_edges():
+    """Worked by hand: scale 1, minimum 0; halves go to the even code; -0, constants, non-finite groups."""
+    x = np.zeros((1, 32), np.float32)
+    x[0, :6] = [0, 15, 0.5, 1.5, 2.5, 14.5]
+    c, s, m = kv4.quantise(x)
+    assert s[0, 0] == 1 and m[0, 0] == 0
+    assert c[0, :6].tolist() == [0, 15, 0, 2, 2, 14]
+    c, s, m = kv4.quantise(np.full((1, 32), -3.5, np.float32))
+    assert s[0, 0] == 0 and m[0, 0] == -3.5 and not c.any()
+    for bad in (np.inf, -np.inf, np.nan):
+        x[0, 7] = bad
+        assert np.isnan(kv4.stands_for(*kv4.quantise(x))).all()
