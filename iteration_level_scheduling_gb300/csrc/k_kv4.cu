@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cstring>
+#include <type_traits>
 #include <vector>
 
 #include "common.cuh"
@@ -355,9 +356,233 @@ __global__ void __launch_bounds__(kKvThreads) kv4_decode_kernel(const Kv4Attn a)
     kv4_finish<T, D>(a, sm, r0, r1, h);
 }
 
+// bf16, head_dim 32 and more: both products on mma.sync m16n8k16 with the
+// codes as the A operand, unpacked in registers straight from 16-byte loads.
+//   scores   rows = 16 keys.  A lane's loads of one key are components of one
+//            group; q enters column g of B only where the component's group is
+//            g, so the columns of S gather sum q c group by group and s, m
+//            apply afterwards.  A = 128 + c (the bits of c in the mantissa of
+//            bf16's 128); -128 sum q is the accumulator's start.
+//   values   rows = 16 components, k = 16 keys.  A = c - 8, exact; column g of
+//            B is p s_g rounded to bf16, column 4 + g what the rounding left,
+//            so the weights keep 16 bits; sum p (m + 8 s) is added in fp32.
+// Codes are centred for the values because those sums run over all keys:
+// taken around 0 .. 15 the accumulator would grow with every key and cancel
+// against the minima at the end.
+__device__ __forceinline__ void kv4_mma(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// {128 + nibble n, 128 + nibble n + 4} of w as two bf16
+template <int N>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+    return ((w >> (4 * N)) & 0x000f000fu) | 0x43004300u;
+}
+// the same less 136: {nibble n - 8, nibble n + 4 - 8}
+template <int N>
+__device__ __forceinline__ uint32_t code_pair_centred(uint32_t w) {
+    const uint32_t u = code_pair<N>(w);
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&u), __float2bfloat162_rn(136.f));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+// W consecutive words, streamed
+template <int W>
+__device__ __forceinline__ void load_words(const void *p, uint32_t *w) {
+    if constexpr (W == 4) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (W == 2) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = __ldcs(reinterpret_cast<const uint32_t *>(p));
+    }
+}
+
+// One block of 16 slots as a lane (g, t) = (lane / 4, lane % 4) of a warp holds it.
+template <int D>
+struct Kv4Block {
+    static constexpr int W = D / 32;  // words per lane and row, and groups
+    uint32_t k[2][W];                 // keys g, g + 8: components 8 W t ..
+    uint32_t v[2][W];                 // pairs t, t + 4: components 4 W g ..
+    uint32_t kp[2][2];                // keys g, g + 8: groups 2t, 2t + 1
+    uint32_t vp[2][2];                // pairs t, t + 4: group g % 4, even and odd slot
+    __device__ __forceinline__ void load(const Kv4View &v4, int h, int64_t b, int g, int t) {
+        const int64_t row = (int64_t)h * v4.S + b, pair = row >> 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            load_words<W>(v4.kc + (row + g + 8 * i) * (D / 2) + t * (4 * W), k[i]);
+            load_words<W>(v4.vc + (pair + t + 4 * i) * D + g * (4 * W), v[i]);
+            const uint32_t *p = v4.kp + (row + g + 8 * i) * W;
+            if constexpr (W == 4) load_words<2>(p + 2 * (t & 1), kp[i]);
+            else if constexpr (W == 2) load_words<2>(p, kp[i]);
+            else kp[i][0] = __ldcs(p), kp[i][1] = 0u;
+            load_words<2>(v4.vp + ((pair + t + 4 * i) * W + (g & (W - 1))) * 2, vp[i]);
+        }
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kKvThreads, 4) kv4_decode_mma_kernel(const Kv4Attn a) {
+    constexpr int W = D / 32;
+    constexpr unsigned kAll = 0xffffffffu;
+    __shared__ Kv4Merge<D> sm;
+    pdl_trigger();
+    pdl_wait();
+    const int4 r0 = reinterpret_cast<const int4 *>(a.items)[2 * blockIdx.x],
+               r1 = reinterpret_cast<const int4 *>(a.items)[2 * blockIdx.x + 1];
+    const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int64_t s0 = r0.x, s1 = s0 + r0.y;
+    int64_t b = (s0 & ~int64_t(15)) + 16 * warp;  // (S is a multiple of 16: a block never leaves the layer)
+    Kv4Block<D> nx;
+    if (b < s1) nx.load(a.v, h, b, g, t);
+
+    // q: word w of a lane covers components 8 (W t + w) ..; pairs (n, n + 4)
+    uint32_t qf[W][4];
+    float qsum[2];  // sum of q over groups 2t and 2t + 1
+    {
+        const bf16 *q = (const bf16 *)a.qkv + (size_t)r0.z * 3 * a.H + h * D + 8 * W * t;
+        const bool mine = g == (t * W) / 4;
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            float x[8];
+            load16(q + 8 * w, x);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) sum += x[n];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) qf[w][n] = mine ? pack2(x[n], x[n + 4]) : 0u;
+        }
+        float of[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) of[j] = __shfl_sync(kAll, sum, j);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            qsum[j] = 0.f;
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt)
+                if ((tt * W) / 4 == 2 * t + j) qsum[j] += of[tt];
+        }
+    }
+    float m = kLow, l = 0.f, zero = 0.f, o[2 * W][4];
+#pragma unroll
+    for (int i = 0; i < 2 * W; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    while (b < s1) {
+        const Kv4Block<D> x = nx;
+        const int64_t here = b;
+        b += 16 * kKvWarps;
+        if (b < s1) nx.load(a.v, h, b, g, t);
+        // scores of keys g and g + 8
+        float c[4] = {-128.f * qsum[0], -128.f * qsum[1], -128.f * qsum[0], -128.f * qsum[1]};
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            kv4_mma(c, code_pair<0>(x.k[0][w]), code_pair<0>(x.k[1][w]), code_pair<1>(x.k[0][w]),
+                    code_pair<1>(x.k[1][w]), qf[w][0], qf[w][1]);
+            kv4_mma(c, code_pair<2>(x.k[0][w]), code_pair<2>(x.k[1][w]), code_pair<3>(x.k[0][w]),
+                    code_pair<3>(x.k[1][w]), qf[w][2], qf[w][3]);
+        }
+        float sc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // (lanes whose columns hold no group have c = qsum = 0 but may have read another's parameters)
+            float s = 0.f;
+            if (2 * t < W)
+                s = bf_lo(x.kp[i][0]) * c[2 * i] + bf_hi(x.kp[i][0]) * qsum[0] + bf_lo(x.kp[i][1]) * c[2 * i + 1] +
+                    bf_hi(x.kp[i][1]) * qsum[1];
+            s += __shfl_xor_sync(kAll, s, 1);
+            s += __shfl_xor_sync(kAll, s, 2);
+            sc[i] = s * a.scale_log2;
+        }
+        const bool whole = here >= s0 && here + 16 <= s1;  // warp-uniform
+        bool v_lo = true, v_hi = true;
+        if (!whole) {
+            v_lo = here + g >= s0 && here + g < s1;
+            v_hi = here + g + 8 >= s0 && here + g + 8 < s1;
+            if (!v_lo) sc[0] = kLow;
+            if (!v_hi) sc[1] = kLow;
+        }
+        float mx = fmaxf(sc[0], sc[1]);
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
+        if (mx > m) {  // warp-uniform
+            const float corr = exp2f(m - mx);
+            m = mx;
+            l *= corr, zero *= corr;
+#pragma unroll
+            for (int i = 0; i < 2 * W; ++i) o[i][0] *= corr, o[i][1] *= corr, o[i][2] *= corr, o[i][3] *= corr;
+        }
+        const float p_lo = v_lo ? exp2f(sc[0] - m) : 0.f, p_hi = v_hi ? exp2f(sc[1] - m) : 0.f;
+        l += p_lo + p_hi;
+        // weights of keys 2t, 2t + 1, 2t + 8, 2t + 9 in group g % 4
+        uint32_t bw[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float pe = __shfl_sync(kAll, i ? p_hi : p_lo, 8 * t), po = __shfl_sync(kAll, i ? p_hi : p_lo, 8 * t + 4);
+            float se = bf_lo(x.vp[i][0]), me = bf_hi(x.vp[i][0]), so = bf_lo(x.vp[i][1]), mo = bf_hi(x.vp[i][1]);
+            if (!whole) {  // an unused slot's parameters may be anything
+                const int64_t slot = here + 8 * i + 2 * t;
+                if (slot < s0 || slot >= s1) se = me = 0.f;
+                if (slot + 1 < s0 || slot + 1 >= s1) so = mo = 0.f;
+            }
+            const float we = pe * se, wo = po * so;
+            zero += pe * fmaf(8.f, se, me) + po * fmaf(8.f, so, mo);
+            const uint32_t hi = pack2(we, wo);
+            const uint32_t left = pack2(we - bf_lo(hi), wo - bf_hi(hi));
+            bw[i] = (g & 3) >= W ? 0u : g < 4 ? hi : left;
+        }
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            kv4_mma(o[2 * w], code_pair_centred<0>(x.v[0][w]), code_pair_centred<1>(x.v[0][w]),
+                    code_pair_centred<0>(x.v[1][w]), code_pair_centred<1>(x.v[1][w]), bw[0], bw[1]);
+            kv4_mma(o[2 * w + 1], code_pair_centred<2>(x.v[0][w]), code_pair_centred<3>(x.v[0][w]),
+                    code_pair_centred<2>(x.v[1][w]), code_pair_centred<3>(x.v[1][w]), bw[0], bw[1]);
+        }
+    }
+    // l over the keys of a lane's column; the minima's part over the keys of its group
+    l += __shfl_xor_sync(kAll, l, 4);
+    l += __shfl_xor_sync(kAll, l, 8);
+    l += __shfl_xor_sync(kAll, l, 16);
+    zero += __shfl_xor_sync(kAll, zero, 1);
+    zero += __shfl_xor_sync(kAll, zero, 2);
+    // row g of o[2w + j] is component 4 (W g + w) + 2j of group W g / 8, row g + 8 the one after it; that
+    // group's column and its remainder's are 2t + (group & 1) at t = group / 2 and t = group / 2 + 2
+    const int gr = W * g / 8;
+    const float z = __shfl_sync(kAll, zero, 4 * gr);
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float *c = o[2 * w + j];
+            float e0 = (gr & 1) ? c[1] : c[0], e1 = (gr & 1) ? c[3] : c[2];
+            e0 += __shfl_xor_sync(kAll, e0, 2);
+            e1 += __shfl_xor_sync(kAll, e1, 2);
+            if (t == gr / 2) {
+                float *dst = &sm.o[warp][4 * (W * g + w) + 2 * j];
+                dst[0] = e0 + z, dst[1] = e1 + z;
+            }
+        }
+    if (lane == 0) sm.m[warp] = m, sm.l[warp] = l;
+    kv4_finish<bf16, D>(a, sm, r0, r1, h);
+}
+
 template <typename T>
 cudaError_t launch_decode(const Kv4Attn &a, int d, int n_items, cudaStream_t st) {
     const dim3 grid(n_items, a.n_heads), block(kKvThreads);
+    if constexpr (std::is_same<T, bf16>::value) {
+        if (d == 32) return launch_pdl(kv4_decode_mma_kernel<32>, grid, block, 0, st, a);
+        if (d == 64) return launch_pdl(kv4_decode_mma_kernel<64>, grid, block, 0, st, a);
+        if (d == 128) return launch_pdl(kv4_decode_mma_kernel<128>, grid, block, 0, st, a);
+    }
     switch (d) {
         case 16: return launch_pdl(kv4_decode_kernel<T, 16>, grid, block, 0, st, a);
         case 32: return launch_pdl(kv4_decode_kernel<T, 32>, grid, block, 0, st, a);
