@@ -1032,7 +1032,8 @@ bool kv4_shape_ok(int32_t n_heads, int32_t d, int64_t kv_slots) {
     return n_heads >= 1 && n_heads <= 1024 && (d == 16 || d == 32 || d == 64 || d == 128) && kv_slots >= 1 &&
            kv_slots <= INT32_MAX - 15;
 }
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned(const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+bool aligned16(const void *p) { return aligned(p, 16); }
 // The launches go to the current device: it has to be the engine's.
 bool on_device(const orca_engine *E) {
     int dev = -1;
@@ -1114,11 +1115,13 @@ int orca_op_sample(orca_engine *E, int32_t dtype, const void *logits, int32_t n_
                    const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
                    const float *uniform, int32_t *out_tokens) {
     if (!E || !logits || !uniform || !out_tokens || n_rows < 0 || vocab < 1 || vocab > (1 << 20) || ld < vocab ||
-        (dtype != ORCA_DTYPE_FP32 && dtype != ORCA_DTYPE_BF16) || !on_device(E))
+        (dtype != ORCA_DTYPE_FP32 && dtype != ORCA_DTYPE_BF16) ||
+        !aligned(logits, dtype == ORCA_DTYPE_BF16 ? 2 : 4) || !aligned(temperature, 4) || !aligned(top_k, 4) ||
+        !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(uniform, 4) || !aligned(out_tokens, 4) || !on_device(E))
         return ORCA_ERR_INVALID;
     if (n_rows == 0) return ORCA_OK;
     return launched(E, sample_rows(dtype == ORCA_DTYPE_BF16, logits, ld, n_rows, vocab, temperature, top_k, top_p,
-                                   min_p, uniform, out_tokens, E->d_err, E->st));
+                                   min_p, uniform, out_tokens, E->d_err, E->num_sms, E->st));
 }
 
 }  // extern "C"

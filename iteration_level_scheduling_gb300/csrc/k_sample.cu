@@ -12,7 +12,22 @@
 // not depend on how the work is spread, and 2^20 weights of at most 1 fit.
 // (In fp32 the running sums of 50257 probabilities are off by more than many
 // of the tokens weigh; the token drawn would then often be a neighbour.)
+//
+// A row is read from memory once and kept in shared memory; a cluster of CTAs
+// shares it when there are few rows or one SM cannot hold it, meeting in
+// distributed shared memory.  Which tokens a filter keeps is decided from a
+// histogram (counts or exact masses) of 2048 bins, linear in the logit over the
+// 43 octaves below m that carry weight: the bins down to the one in which the
+// count or the mass is reached hold every token that can be kept.  Up to 1024
+// of them are gathered, sorted and settled by one CTA; more are settled by
+// selecting the last kept logit and passing over the row in the order of the
+// ids.
+#include <cooperative_groups.h>
+
+#include <algorithm>
 #include <cfloat>
+#include <cstddef>
+#include <cstdlib>
 
 #include "common.cuh"
 #include "kernels.cuh"
@@ -21,36 +36,110 @@ namespace orca {
 
 namespace {
 
-constexpr int kSpThreads = 1024, kSpWarps = kSpThreads / 32;
-constexpr int kFrac = 42;  // fraction bits of a weight
+namespace cg = cooperative_groups;
+
+constexpr int kSpThreads = 512, kSpWarps = kSpThreads / 32;
+constexpr int kFrac = 42;     // fraction bits of a weight
+constexpr int kBins = 2048;   // histogram bins (four per thread)
+constexpr int kList = 1024;   // tokens settled by sorting (two per thread)
+constexpr int kMaxCluster = 8;
+
 using u64 = unsigned long long;
+static_assert(kBins == 4 * kSpThreads && kList == 2 * kSpThreads, "bins and list per thread");
 
 struct SampleArgs {
     const void *logits;
     int64_t ld;
-    int V;
+    int V, per;  // ids of one CTA (a multiple of 32 per warp)
     const float *temperature, *top_p, *min_p, *uniform;
     const int32_t *top_k;
     int32_t *out;
     unsigned *err;
 };
 
-// Keys ordered as the logits are (a row's NaN below everything; -0 = +0).
+// A logit as it is held: NaN as -inf (neither is ever drawn), -0 as +0.
+__device__ __forceinline__ float sp_logit(float l) { return l == l ? l + 0.f : -INFINITY; }
+// Keys ordered as the logits are.
 __device__ __forceinline__ uint32_t sp_key(float l) {
-    if (l != l) return 0u;
-    const uint32_t u = __float_as_uint(l + 0.f);
+    const uint32_t u = __float_as_uint(l);
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float sp_value(uint32_t key) {
-    return key == 0u ? -INFINITY : __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+    return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
 }
 
-// The weight of a key in fixed point; inv_t = 1 / T.
-__device__ __forceinline__ u64 sp_weight(uint32_t key, uint32_t top, double inv_t) {
-    if (key == top) return 1ull << kFrac;
-    const double x = ((double)sp_value(key) - (double)sp_value(top)) * inv_t;
-    if (!(x > -30.5)) return 0ull;  // below half of the last place
-    return (u64)llrint(exp(x) * (double)(1ull << kFrac));
+// ---------------------------------------------------------------------------
+// 2^-t in fixed point, table-driven (P. T. P. Tang, "Table-driven
+// implementation of the exponential function in IEEE floating-point
+// arithmetic", 1989): t = n - j / 32 - g with |g| <= 1/64, so
+// 2^-t = 2^-n 2^(j/32) 2^g, 2^g by its Taylor polynomial.  In pairs of floats,
+// since fp64 runs at 1/64 of the fp32 rate here: relative error below 2^-34
+// (measured over 2^22 arguments: 2^-34.3).
+// ---------------------------------------------------------------------------
+struct alignas(16) ExpEntry {
+    u64 fixed;  // 2^(j / 32) with 42 fraction bits
+    float hi, lo;  // the same as a pair of floats
+};
+constexpr int kExpEntries = 33;  // j = -16 .. 16
+constexpr double exp_series(double x) {
+    double term = 1, sum = 1;
+    for (int i = 1; i < 30; ++i) term *= x / i, sum += term;
+    return sum;
+}
+struct ExpTable {
+    ExpEntry e[kExpEntries];
+};
+constexpr double kLn2 = 0.69314718055994530942;
+constexpr ExpTable make_exp_table() {
+    ExpTable t{};
+    for (int j = 0; j < kExpEntries; ++j) {
+        const double v = exp_series((j - 16) * (kLn2 / 32));
+        t.e[j].fixed = (u64)(v * (double)(1ull << kFrac) + 0.5);
+        t.e[j].hi = (float)v;
+        t.e[j].lo = (float)(v - (double)t.e[j].hi);
+    }
+    return t;
+}
+__constant__ ExpTable kExp = make_exp_table();
+
+// log2(e) / T as a pair of floats
+struct Scale {
+    float hi, lo;
+};
+
+// the weight of logit l in a row whose largest is top (l <= top, both finite or l = -inf)
+__device__ __forceinline__ u64 sp_weight_of(float l, float top, const Scale &c, const ExpEntry *table) {
+    // d + e = top - l exactly
+    const float d = __fsub_rn(top, l);
+    const float bb = __fsub_rn(top, d);
+    const float e = __fadd_rn(__fsub_rn(top, __fadd_rn(d, bb)), __fsub_rn(bb, l));
+    // t + tl = (d + e) log2(e) / T
+    const float t = __fmul_rn(d, c.hi);
+    if (!(t < 43.5f)) return 0ull;  // 2^-t is below half of the last place
+    const float tl = __fmaf_rn(d, c.hi, -t) + __fmaf_rn(d, c.lo, __fmul_rn(e, c.hi));
+    const float n = rintf(t);
+    const float f = __fsub_rn(n, t);  // exact, |f| <= 1/2
+    const float jf = rintf(f * 32.f);
+    const float g = __fmaf_rn(jf, -0.03125f, f);  // exact, |g| <= 1/64
+    const ExpEntry x = table[(int)jf + 16];
+    // 2^(g - tl) - 1 = a + (b + a^2 / 2 + ..) with a + b = (g - tl) ln 2
+    constexpr float kL = (float)kLn2, kLl = (float)(kLn2 - (double)(float)kLn2);
+    const float a = __fmul_rn(g, kL);
+    const float b = __fmaf_rn(g, kL, -a) + __fmaf_rn(g, kLl, -tl * kL);
+    // a^2 / 2 + a^3 / 6 + .. + a^5 / 120, and the cross term a b
+    float q = __fmaf_rn(a, 1.f / 120.f, 1.f / 24.f);
+    q = __fmaf_rn(a, q, 1.f / 6.f);
+    q = __fmaf_rn(a, q, 0.5f);
+    const float a2 = __fmul_rn(a, a), a2l = __fmaf_rn(a, a, -a2);
+    const float r = __fmaf_rn(a2, q, b) + __fmaf_rn(a, b, 0.5f * a2l);
+    // 2^(j/32) (a + r): the leading part on a grid of 2^-19, the rest below it
+    const float p = __fmul_rn(x.hi, a);
+    const float rest = __fmaf_rn(x.hi, a, -p) + __fmaf_rn(x.hi, r, x.lo * a);
+    const float i1 = rintf(p * 524288.f);
+    const float i2 = rintf((__fmaf_rn(i1, -1.f / 524288.f, p) + rest) * 4398046511104.f);
+    const long long m = (long long)x.fixed + ((long long)(int)i1 << (kFrac - 19)) + (long long)(int)i2;
+    const int sh = (int)n;
+    return sh ? (u64)((m + (1ll << (sh - 1))) >> sh) : (u64)m;
 }
 
 template <typename V>
@@ -60,178 +149,551 @@ __device__ __forceinline__ V warp_add(V v) {
     return v;
 }
 
-// x * f for a fraction f given as f * 2^64
-__device__ __forceinline__ u64 frac64(float f) { return (u64)((double)f * 18446744073709551616.0); }
+// f < 1 as a multiple of 2^-64 (exact but for what lies below)
+__device__ __forceinline__ u64 frac64(float f) { return __float2ull_rz(f * 18446744073709551616.f); }
 
-struct SampleSmem {
-    u64 mass[256];
-    uint32_t count[256];
-    u64 wsum[kSpWarps];
-    uint32_t wcnt[kSpWarps], wkey[kSpWarps];
-    uint32_t bin;
-    uint32_t above_n;
-    u64 above_m;
-    int found;
+// What the CTAs of a row share; a CTA's copy is written by the others through
+// distributed shared memory, each word once between two cluster barriers.
+struct SampleShare {
+    float top[kMaxCluster];
+    u64 sum[kMaxCluster];
+    uint32_t count[kMaxCluster];  // of gathered logits, or of those equal to the cut
+    uint32_t first[kMaxCluster];  // first id of the largest logit; ties of the final pass
+    // what rank 0 decides, in its copy read by all
+    uint32_t bin, found, key;
+    u64 want, wanted, left, total;
+    uint32_t gathered;  // this CTA's
 };
 
-template <typename T>
+struct alignas(16) SampleSmem {
+    SampleShare sh;
+    ExpEntry exp[kExpEntries];
+    union {
+        struct {
+            alignas(16) uint32_t lo[kBins];  // counts in lo, or masses in (hi, lo)
+            alignas(16) uint32_t hi[kBins];
+        };
+        struct {
+            alignas(16) u64 list[kList];  // (key, ~id) of gathered tokens, then sorted
+            uint32_t order[kList];  // (id, place) of the kept ones
+        };
+    };
+    u64 mass[kList];
+    u64 wsum[kSpWarps];
+    uint32_t wcnt[kSpWarps];
+};
+// 16-byte accesses: the histograms and the row behind this object
+static_assert(offsetof(SampleSmem, lo) % 16 == 0 && offsetof(SampleSmem, hi) % 16 == 0 &&
+                  offsetof(SampleSmem, exp) % 16 == 0 && sizeof(SampleSmem) % 16 == 0,
+              "alignment");
+
+// Inclusive sums over the block of two values per thread (2t, 2t + 1).
+__device__ __forceinline__ void block_scan2(u64 &x0, u64 &x1, u64 *wsum) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    u64 c = x0 + x1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += y;
+    }
+    __syncthreads();
+    if (lane == 31) wsum[warp] = c;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) c += wsum[w];
+    x0 = c - x1, x1 = c;
+}
+
+// Sort v[0 .. n), distinct but for the padding up to a power of two (`pad`, last in the order), ascending or
+// descending; n <= kList, v has room for kList.  Few: every element counts those in front of it.  More: a
+// bitonic network, a pair per thread; pairs at most 32 apart stay within the 64 elements of one warp, whose steps
+// need no block barrier.
+template <bool Up, typename V>
+__device__ __forceinline__ void block_sort(V *v, int n, V pad) {
+    const int t = threadIdx.x;
+    if (n <= 128) {
+        V x = pad;
+        int place = 0;
+        if (t < n) {
+            x = v[t];
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) place += Up ? v[j] < x : v[j] > x;
+        }
+        __syncthreads();
+        if (t < n) v[place] = x;
+        __syncthreads();
+        return;
+    }
+    int full = 256;
+    while (full < n) full *= 2;
+    for (int j = n + t; j < full; j += kSpThreads) v[j] = pad;
+    __syncthreads();
+    for (int size = 2; size <= full; size <<= 1)
+        for (int stride = size >> 1; stride > 0; stride >>= 1) {
+            if (t < full / 2) {
+                const int i = 2 * (t & ~(stride - 1)) | (t & (stride - 1)), j = i + stride;
+                const bool up = ((i & size) == 0) == Up;
+                const V a = v[i], b = v[j];
+                if ((a > b) == up) v[i] = b, v[j] = a;
+            }
+            if (stride > 32 || (stride == 1 && size >= 64)) __syncthreads();
+            else __syncwarp();
+        }
+    __syncthreads();
+}
+
+// Held: the row is kept in shared memory; otherwise (rows of more ids than a cluster holds) every pass reads the
+// logits again.
+template <typename T, bool Held>
 __global__ void __launch_bounds__(kSpThreads) sample_kernel(const SampleArgs a) {
-    __shared__ SampleSmem sm;
+    extern __shared__ __align__(16) uint8_t sp_raw[];
+    SampleSmem &sm = *reinterpret_cast<SampleSmem *>(sp_raw);
+    float *val = reinterpret_cast<float *>(sp_raw + sizeof(SampleSmem));
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int r = blockIdx.x / C;
+    constexpr unsigned kAll = 0xffffffffu;
+    // the same object in another CTA of the row
+    auto peer = [&](int c) -> SampleSmem & { return *cluster.map_shared_rank(&sm, c); };
+    auto meet = [&]() {
+        if (C > 1) cluster.sync();
+        else __syncthreads();
+    };
+    if (tid < kExpEntries) sm.exp[tid] = kExp.e[tid];
+    if (C > 1) cluster.sync();  // every CTA of the row runs before another writes to its shared memory
     pdl_trigger();
     pdl_wait();
-    const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const T *row = (const T *)a.logits + (size_t)r * a.ld;
-    const int V = a.V;
+
     const float temp = a.temperature ? a.temperature[r] : 1.f, p = a.top_p ? a.top_p[r] : 1.f,
                 mp = a.min_p ? a.min_p[r] : 0.f, u = a.uniform[r];
     const int k = a.top_k ? a.top_k[r] : 0;
     if (!(temp >= 0.f && temp <= 1e6f && p >= 0.f && p <= 1.f && mp >= 0.f && mp <= 1.f && u >= 0.f && u < 1.f)) {
-        if (tid == 0) raise_err(a.err, ERR_BAD_SAMPLE), a.out[r] = -1;
-        return;
+        if (rank == 0 && tid == 0) raise_err(a.err, ERR_BAD_SAMPLE), a.out[r] = -1;
+        return;  // (the whole cluster)
     }
-    auto key_at = [&](int i) { return sp_key(Elem<T>::to_f(row[i])); };
-    // the largest key
-    uint32_t top = 0;
-    for (int i = tid; i < V; i += kSpThreads) top = max(top, key_at(i));
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) sm.wkey[warp] = top;
-    if (tid == 0) sm.found = -1;
-    __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, sm.wkey[lane]);
-    if (top <= sp_key(-INFINITY)) {  // nothing but -inf and NaN
-        if (tid == 0) a.out[r] = -1;
-        return;
-    }
-    const double inv_t = temp > 0.f ? 1.0 / (double)temp : 0.0;
-    uint32_t cut = 0;             // kept: keys above cut, and the first `ties` of those equal to it
-    uint32_t ties = 0xffffffffu;
-    if (temp == 0.f) {
-        cut = top, ties = 1;
-    } else {
-        // one round of a radix selection: the histogram of 8 key bits of the
-        // keys above `floor_key` with the prefix chosen so far, from the top
-        // bin down to where the count (or mass) reaches what is wanted
-        auto select = [&](bool by_mass, u64 want, uint32_t floor_key, uint32_t *got, u64 *left) {
-            uint32_t prefix = 0;
-            for (int shift = 24; shift >= 0; shift -= 8) {
-                if (tid < 256) sm.mass[tid] = 0, sm.count[tid] = 0;
-                __syncthreads();
-                for (int i = tid; i < V; i += kSpThreads) {
-                    const uint32_t key = key_at(i);
-                    if (key <= floor_key || (shift < 24 && (key >> (shift + 8)) != (prefix >> (shift + 8)))) continue;
-                    const uint32_t b = (key >> shift) & 255u;
-                    if (by_mass) {
-                        const u64 w = sp_weight(key, top, inv_t);
-                        if (w) atomicAdd(&sm.mass[b], w);
-                    } else {
-                        atomicAdd(&sm.count[b], 1u);
-                    }
-                }
-                __syncthreads();
-                if (tid == 0) {
-                    int b = 255;
-                    for (; b > 0; --b) {
-                        const u64 x = by_mass ? sm.mass[b] : (u64)sm.count[b];
-                        if (x >= want) break;
-                        want -= x;
-                    }
-                    sm.bin = b;
-                    sm.above_m = want;
-                }
-                __syncthreads();
-                prefix |= sm.bin << shift;
-                want = sm.above_m;
-                __syncthreads();
+    // this CTA's ids: first .. first + n - 1
+    const int first = min(a.V, rank * a.per), n = min(a.V - first, a.per);
+    const T *row = (const T *)a.logits + (size_t)r * a.ld + first;
+    auto at = [&](int i) -> float {
+        if constexpr (Held) return val[i];
+        else return sp_logit(Elem<T>::to_f(row[i]));
+    };
+    // f(i, logit) for every id of this CTA, in any order (held rows are padded to a multiple of four with -inf)
+    auto each = [&](auto f) {
+        if constexpr (Held) {
+            for (int i = 4 * tid; i < n; i += 4 * kSpThreads) {
+                const float4 x = *reinterpret_cast<const float4 *>(val + i);
+                f(i, x.x), f(i + 1, x.y), f(i + 2, x.z), f(i + 3, x.w);
             }
-            *got = prefix;
-            *left = want;  // of the keys equal to *got
-        };
-        if (k > 0 && k < V) {
-            u64 left;
-            select(false, (u64)k, 0u, &cut, &left);
-            ties = (uint32_t)left;
+        } else {
+            for (int i = tid; i < n; i += kSpThreads) f(i, at(i));
         }
-        if (p < 1.f) {
-            // masses of the keys above the cut, and of the kept ones equal to it
-            u64 s = 0;
-            uint32_t c = 0;
-            for (int i = tid; i < V; i += kSpThreads) {
-                const uint32_t key = key_at(i);
-                if (key > cut) s += sp_weight(key, top, inv_t);
-                c += key == cut;
+    };
+    float top = -INFINITY;
+    if constexpr (!Held) {
+        for (int i = tid; i < n; i += kSpThreads) top = fmaxf(top, at(i));
+    } else {
+        constexpr int VEC = Elem<T>::kPer16;
+        const int head = min(n, (int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(T)));
+        const int body = (n - head) / VEC;
+        auto put = [&](int i, float l) {
+            l = sp_logit(l);
+            val[i] = l;
+            top = fmaxf(top, l);
+        };
+        if (tid < head) put(tid, Elem<T>::to_f(row[tid]));
+#pragma unroll 4
+        for (int i = tid; i < body; i += kSpThreads) {
+            float x[VEC];
+            load16_stream(row + head + i * VEC, x);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) put(head + i * VEC + e, x[e]);
+        }
+        for (int i = head + body * VEC + tid; i < n; i += kSpThreads) put(i, Elem<T>::to_f(row[i]));
+        if (tid < 4 && n + tid < (n + 3) / 4 * 4) val[n + tid] = -INFINITY;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    if (lane == 0) sm.wcnt[warp] = __float_as_uint(top);
+    __syncthreads();
+    if (warp == 0) {
+        top = lane < kSpWarps ? __uint_as_float(sm.wcnt[lane]) : -INFINITY;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+        if (lane < C) peer(lane).sh.top[rank] = top;
+    }
+    meet();
+    top = -INFINITY;
+    for (int c = 0; c < C; ++c) top = fmaxf(top, sm.sh.top[c]);
+
+    if (top == -INFINITY) {  // nothing but -inf and NaN
+        if (rank == 0 && tid == 0) a.out[r] = -1;
+        return;
+    }
+    if (temp == 0.f) {  // the lowest id of the largest logit
+        uint32_t low = 0xffffffffu;
+        each([&](int i, float l) {
+            if (l == top) low = min(low, (uint32_t)(first + i));
+        });
+        low = __reduce_min_sync(kAll, low);
+        if (lane == 0) sm.wcnt[warp] = low;
+        __syncthreads();
+        if (warp == 0) {
+            low = __reduce_min_sync(kAll, lane < kSpWarps ? sm.wcnt[lane] : 0xffffffffu);
+            if (lane == 0) peer(0).sh.first[rank] = low;
+        }
+        meet();
+        if (rank == 0 && tid == 0) {
+            for (int c = 0; c < C; ++c) low = min(low, sm.sh.first[c]);
+            a.out[r] = (int32_t)low;
+        }
+        return;
+    }
+
+    Scale cs;
+    {
+        constexpr float kE = 1.4426950408889634074f, kEl = (float)(1.4426950408889634074 - (double)kE);
+        cs.hi = fminf(__fdiv_rn(kE, temp), 3e38f);
+        cs.lo = __fdiv_rn(__fmaf_rn(-cs.hi, temp, kE) + kEl, temp);
+        if (!(fabsf(cs.lo) < 1e30f)) cs.lo = 0.f;  // (a subnormal T: only the largest logits keep weight)
+    }
+    auto weight = [&](float l) -> u64 { return l == top ? 1ull << kFrac : sp_weight_of(l, top, cs, sm.exp); };
+    // The bin of a logit: octaves below the largest, kBins of them over 43.5 (monotone in the logit;
+    // the last bin also takes everything without weight)
+    auto bin_of = [&](float l) {
+        const float d = __fmul_rn(__fmul_rn(__fsub_rn(top, l), cs.hi), (float)(kBins / 43.5));
+        return l == top ? 0 : (int)fminf(d, (float)(kBins - 1));
+    };
+    SampleSmem &root = peer(0);
+
+    // the mass that a prefix has to reach: p times the whole, rounded up, at least one
+    const u64 pf = p < 1.f ? frac64(p) : 0ull;
+    auto share = [&](u64 whole) {
+        const u64 want = __umul64hi(pf, whole) + (pf * whole != 0);
+        return want < 1 ? 1ull : want;
+    };
+    const u64 least = __float2ull_ru(mp * (float)(1ull << kFrac));
+    bool by_count = k > 0 && k < a.V;
+    // kept: logits above cut, and the first `ties` of those equal to it
+    float cut = -INFINITY;
+    uint32_t ties = 0xffffffffu;
+
+    // Histogram over the bins of(l) >= 0 of the logits above the cut, counts or masses, added up in rank 0.  There
+    // pick(total) says what is wanted, and root.sh gets whether that much is there (found), the bin in which it is
+    // reached from the largest logits down, what is left of it for that bin (want) and all of it (wanted).  `down`:
+    // larger logits are in higher bins.
+    auto histogram = [&](bool by_mass, bool down, auto of, auto pick) {
+        for (int i = tid; i < kBins / 4; i += kSpThreads) {
+            reinterpret_cast<uint4 *>(sm.lo)[i] = make_uint4(0, 0, 0, 0);
+            if (by_mass) reinterpret_cast<uint4 *>(sm.hi)[i] = make_uint4(0, 0, 0, 0);
+        }
+        __syncthreads();
+        each([&](int, float l) {
+            if (!(l > cut)) return;
+            const int b = of(l);
+            if (b < 0) return;
+            if (by_mass) {
+                const u64 w = weight(l);
+                const uint32_t wl = (uint32_t)w, old = atomicAdd(&sm.lo[b], wl);
+                const uint32_t wh = (uint32_t)(w >> 32) + (old + wl < old);
+                if (wh) atomicAdd(&sm.hi[b], wh);
+            } else {
+                atomicAdd(&sm.lo[b], 1u);
             }
-            s = warp_add(s), c = warp_add(c);
-            if (lane == 0) sm.wsum[warp] = s, sm.wcnt[warp] = c;
+        });
+        meet();
+        if (rank == 0) {
+            // thread t: four bins, in the order of descending logits
+            const int q = down ? kBins / 4 - 1 - tid : tid;
+            u64 x[4] = {0, 0, 0, 0}, s = 0;
+            for (int c = 0; c < C; ++c) {
+                const SampleSmem &o = peer(c);
+                const uint4 lo = reinterpret_cast<const uint4 *>(o.lo)[q];
+                uint4 hi = make_uint4(0, 0, 0, 0);
+                if (by_mass) hi = reinterpret_cast<const uint4 *>(o.hi)[q];
+                x[0] += (u64)hi.x << 32 | lo.x, x[1] += (u64)hi.y << 32 | lo.y;
+                x[2] += (u64)hi.z << 32 | lo.z, x[3] += (u64)hi.w << 32 | lo.w;
+            }
+            s = x[0] + x[1] + x[2] + x[3];
+            u64 incl = s;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 y = __shfl_up_sync(kAll, incl, o);
+                if (lane >= o) incl += y;
+            }
+            if (lane == 31) sm.wsum[warp] = incl;
+            if (tid == 0) sm.sh.found = 0;
             __syncthreads();
-            s = warp_add(sm.wsum[lane]), c = warp_add(sm.wcnt[lane]);
-            const u64 wt = cut ? sp_weight(cut, top, inv_t) : 0ull;
-            const u64 all = s + wt * min(c, ties);
-            const u64 f = frac64(p);
-            u64 want = __umul64hi(f, all) + (f * all != 0);
-            if (want < 1) want = 1;
-            if (want <= s) {
-                u64 left;
-                uint32_t got;
-                select(true, want, cut, &got, &left);
-                const u64 w = sp_weight(got, top, inv_t);
-                cut = got;
-                ties = (uint32_t)((left + w - 1) / w);
-            } else if (wt) {
-                ties = min(ties, (uint32_t)min((want - s + wt - 1) / wt, (u64)0xffffffffu));
+            u64 base = incl - s, all = 0;
+#pragma unroll
+            for (int w = 0; w < kSpWarps; ++w) {
+                const u64 y = sm.wsum[w];
+                base += w < warp ? y : 0ull;
+                all += y;
             }
+            const u64 want = pick(all);
+            if (tid == 0) sm.sh.total = all, sm.sh.wanted = want;
+            if (base < want && want <= base + s) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const u64 y = down ? x[3 - e] : x[e];
+                    if (base < want && want <= base + y) {
+                        sm.sh.bin = (uint32_t)(4 * q + (down ? 3 - e : e));
+                        sm.sh.want = want - base;
+                        sm.sh.found = 1;
+                    }
+                    base += y;
+                }
+            }
+        }
+        meet();
+    };
+
+    // Every (key, ~id) of the logits above the cut that take(l) names, in rank 0's list; returns how many there
+    // are (more than kList: the list is not to be used).
+    auto collect = [&](auto take) {
+        if (tid == 0) sm.sh.gathered = 0;
+        __syncthreads();
+        each([&](int i, float l) {
+            if (!(l > cut) || !take(l)) return;
+            const uint32_t j = atomicAdd(&sm.sh.gathered, 1u);
+            if (j < kList) sm.list[j] = (u64)sp_key(l) << 32 | (uint32_t) ~(first + i);
+        });
+        __syncthreads();
+        if (tid < C) peer(tid).sh.count[rank] = sm.sh.gathered;
+        meet();
+        uint32_t m = 0;
+        for (int c = 0; c < C; ++c) m += sm.sh.count[c];
+        if (C > 1) {
+            if (rank == 0 && m <= kList) {
+                uint32_t at_c = sm.sh.count[0];
+                for (int c = 1; c < C; ++c) {
+                    const uint32_t nc = sm.sh.count[c];
+                    for (uint32_t j = tid; j < nc; j += kSpThreads) sm.list[at_c + j] = peer(c).list[j];
+                    at_c += nc;
+                }
+            }
+            meet();  // (the other CTAs' lists are free, and they may leave)
+        } else {
+            __syncthreads();
+        }
+        return (int)m;
+    };
+
+    // Rank 0: the token, from a list of m that holds all that may be kept: of the first `most` by logit descending
+    // and id ascending those whose mass in front is below `want` (share_of_most: p times the mass of the `most`).
+    auto finish = [&](int m, int most, u64 want, bool share_of_most) {
+        block_sort<false>(sm.list, m, 0ull);
+        u64 w[2], c[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int j = 2 * tid + e;
+            w[e] = c[e] = j < most ? weight(sp_value((uint32_t)(sm.list[j] >> 32))) : 0ull;
+            sm.mass[j] = w[e];
+        }
+        block_scan2(c[0], c[1], sm.wsum);
+        if (share_of_most) {
+            if (tid == kSpThreads - 1) sm.sh.total = c[1];
+            __syncthreads();
+            want = share(sm.sh.total);
+        }
+        bool keep[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) keep[e] = w[e] >= max(least, 1ull) && c[e] - w[e] < want;
+        const int kept = __syncthreads_count(keep[0]) + __syncthreads_count(keep[1]);  // a prefix
+        if (2 * tid == kept - 1) sm.sh.total = c[0];
+        if (2 * tid + 1 == kept - 1) sm.sh.total = c[1];
+        // the kept ones in the order of their ids
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int j = 2 * tid + e;
+            if (j < kept) sm.order[j] = ~(uint32_t)sm.list[j] << 10 | (uint32_t)j;
+        }
+        __syncthreads();
+        const u64 target = __umul64hi(frac64(u), sm.sh.total);
+        block_sort<true>(sm.order, kept, 0xffffffffu);
+        uint32_t o[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            o[e] = 2 * tid + e < kept ? sm.order[2 * tid + e] : 0u;
+            w[e] = c[e] = 2 * tid + e < kept ? sm.mass[o[e] & (kList - 1)] : 0ull;
+        }
+        block_scan2(c[0], c[1], sm.wsum);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (c[e] - w[e] <= target && target < c[e]) a.out[r] = (int32_t)(o[e] >> 10);
+    };
+
+    // The cut from bin bin0 of the logits' histogram, in which what is left to reach is `want`: while the bin holds
+    // more logits than a list takes, it is split by 11, 11 and 10 bits of their keys.
+    auto settle = [&](bool by_mass, int bin0, u64 want) {
+        uint32_t prefix = 0;
+        for (int level = 0;; ++level) {
+            auto of = [&](float l) {  // the bin of the keys at this level, or -1
+                const uint32_t key = sp_key(l);
+                int b = -1;
+                if (bin_of(l) == bin0) {
+                    if (level == 1) b = (int)(key >> 21);
+                    else if (level == 2) b = (key >> 21) == (prefix >> 21) ? (int)((key >> 10) & 2047u) : -1;
+                    else b = (key >> 10) == (prefix >> 10) ? (int)(key & 1023u) : -1;
+                }
+                return b;
+            };
+            if (level > 0) {
+                const u64 goal = want;
+                histogram(by_mass, true, of, [=](u64) { return goal; });
+                want = root.sh.want;
+                prefix |= root.sh.bin << (level == 1 ? 21 : level == 2 ? 10 : 0);
+                meet();  // (rank 0's state is free again)
+                if (level == 3) {
+                    cut = sp_value(prefix);
+                    break;
+                }
+            }
+            const int low = level == 0 ? 31 : level == 1 ? 21 : 10;  // bits of the keys not yet fixed
+            const uint32_t high = level == 0 ? 0u : prefix >> low;
+            auto in_bin = [&](float l) { return bin_of(l) == bin0 && (level == 0 || sp_key(l) >> low == high); };
+            const int m = collect(in_bin);
+            if (m > kList) continue;
+            if (rank == 0) {
+                block_sort<false>(sm.list, m, 0ull);
+                uint32_t key[2];
+                u64 x[2], c[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int j = 2 * tid + e;
+                    key[e] = j < m ? (uint32_t)(sm.list[j] >> 32) : 0u;
+                    x[e] = c[e] = j >= m ? 0ull : by_mass ? weight(sp_value(key[e])) : 1ull;
+                }
+                block_scan2(c[0], c[1], sm.wsum);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (c[e] - x[e] < want && want <= c[e]) sm.sh.key = key[e];
+                __syncthreads();
+                const uint32_t hit = sm.sh.key;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {  // the first of those equal to it says what is left for them
+                    const int j = 2 * tid + e;
+                    if (j < m && key[e] == hit && (j == 0 || (uint32_t)(sm.list[j - 1] >> 32) != hit))
+                        sm.sh.left = want - (c[e] - x[e]);
+                }
+            }
+            meet();
+            cut = sp_value(root.sh.key);
+            want = root.sh.left;
+            meet();  // (rank 0's state is free again)
+            break;
+        }
+        const u64 w = by_mass ? weight(cut) : 1ull;
+        ties = (uint32_t)((want + w - 1) / w);
+    };
+
+    if (by_count) {
+        histogram(false, false, bin_of, [&](u64) { return (u64)k; });
+        const int bin = (int)root.sh.bin;
+        const u64 want = root.sh.want;
+        // fewer than k logits, or the k-th without weight: the same as all kept
+        by_count = root.sh.found && bin != kBins - 1;
+        meet();  // (rank 0's state is free again)
+        if (by_count) {
+            const int m = collect([&](float l) { return bin_of(l) <= bin; });
+            if (m <= kList) {
+                if (rank == 0) finish(m, k, ~0ull, p < 1.f);
+                return;
+            }
+            settle(false, bin, want);
+        }
+    }
+    if (p < 1.f) {
+        const u64 wt = by_count ? weight(cut) : 0ull;
+        histogram(true, false, bin_of, [&](u64 above) { return share(above + wt * (by_count ? ties : 0u)); });
+        const bool found = root.sh.found;
+        const int bin = (int)root.sh.bin;
+        const u64 want = root.sh.want, wanted = root.sh.wanted, above = root.sh.total;
+        meet();  // (rank 0's state is free again)
+        if (found) {
+            const int m = collect([&](float l) { return bin_of(l) <= bin; });
+            if (m <= kList) {
+                if (rank == 0) finish(m, m, wanted, false);
+                return;
+            }
+            settle(true, bin, want);
+        } else if (wt) {  // it reaches into those equal to the k-th
+            ties = (uint32_t)min((u64)ties, (wanted - above + wt - 1) / wt);
         }
     }
     // the tokens in the order of their ids: a warp takes a contiguous stretch
-    const u64 least = temp > 0.f ? (u64)ceil((double)mp * (double)(1ull << kFrac)) : 0ull;
-    const int per = ((V + kSpThreads - 1) / kSpThreads) * 32, i0 = warp * per, i1 = min(V, i0 + per);
-    uint32_t before = 0;  // keys equal to the cut in front of this stretch
-    {
-        uint32_t c = 0;
-        for (int i = i0 + lane; i < i1; i += 32) c += key_at(i) == cut;
-        c = warp_add(c);
-        __syncthreads();
-        if (lane == 0) sm.wcnt[warp] = c;
-        __syncthreads();
-        const uint32_t x = lane < warp ? sm.wcnt[lane] : 0u;
-        before = warp_add(x);
-    }
-    // weight of token i (0 if it is not kept); advances the count of ties by the warp's
-    auto kept = [&](int i, uint32_t &seen) -> u64 {
-        const uint32_t key = i < i1 ? key_at(i) : 0u;
-        const bool tie = i < i1 && key == cut;
-        const uint32_t mask = __ballot_sync(0xffffffffu, tie);
-        const uint32_t rank = seen + __popc(mask & ((1u << lane) - 1u));
-        seen += __popc(mask);
-        if (i >= i1 || key < cut || (tie && rank >= ties)) return 0ull;
-        const u64 w = key == top ? 1ull << kFrac : temp > 0.f ? sp_weight(key, top, inv_t) : 0ull;
-        return w >= least ? w : 0ull;
-    };
+    const int per_warp = (n + 4 * kSpThreads - 1) / (4 * kSpThreads) * 128;
+    const int i0 = min(n, warp * per_warp), i1 = min(n, i0 + per_warp);
+    const bool tied = cut != -INFINITY;
+    u64 wt = tied ? weight(cut) : 0ull;
+    if (wt < least) wt = 0ull;
     u64 s = 0;
-    uint32_t seen = before;
-    for (int b = i0; b < i1; b += 32) s += kept(b + lane, seen);
-    s = warp_add(s);
-    if (lane == 0) sm.wsum[warp] = s;
+    uint32_t c = 0;
+    auto add = [&](float l) {
+        if (l > cut) {
+            const u64 w = weight(l);
+            s += w >= least ? w : 0ull;
+        }
+        c += l == cut;
+    };
+    if constexpr (Held) {
+        for (int i = i0 + 4 * lane; i < i1; i += 128) {
+            const float4 x = *reinterpret_cast<const float4 *>(val + i);
+            add(x.x), add(x.y), add(x.z), add(x.w);
+        }
+    } else {
+        for (int i = i0 + lane; i < i1; i += 32) add(at(i));
+    }
+    s = warp_add(s), c = warp_add(c);
     __syncthreads();
-    const u64 mine = sm.wsum[lane];
-    const u64 all = warp_add(mine), first = warp_add(lane < warp ? mine : 0ull);
+    if (lane == 0) sm.wsum[warp] = s, sm.wcnt[warp] = c;
+    __syncthreads();
+    if (warp == 0) {
+        const u64 sc = warp_add(lane < kSpWarps ? sm.wsum[lane] : 0ull);
+        const uint32_t cc = warp_add(lane < kSpWarps ? sm.wcnt[lane] : 0u);
+        if (lane < C) peer(lane).sh.sum[rank] = sc, peer(lane).sh.first[rank] = cc;
+    }
+    meet();
+    // mass of a stretch with s above the cut and c equal to it, `seen` of those equal lying in front
+    auto stretch = [&](u64 sx, uint32_t cx, uint32_t seen) {
+        return sx + wt * (seen < ties ? min(ties - seen, cx) : 0u);
+    };
+    u64 all = 0, start = 0;
+    uint32_t seen = 0, before = 0;
+    for (int x = 0; x < C; ++x) {
+        if (x == rank) start = all, before = seen;
+        all += stretch(sm.sh.sum[x], sm.sh.first[x], seen);
+        seen += sm.sh.first[x];
+    }
+    for (int w = 0; w < warp; ++w) {
+        start += stretch(sm.wsum[w], sm.wcnt[w], before);
+        before += sm.wcnt[w];
+    }
     const u64 target = __umul64hi(frac64(u), all);
-    if (target >= first && target < first + s) {
-        u64 sum = first;
-        seen = before;
+    if (target >= start && target < start + stretch(s, c, before)) {
+        u64 sum = start;
         for (int b = i0; b < i1; b += 32) {
-            const u64 w = kept(b + lane, seen);
-            u64 c = w;
+            const float l = b + lane < i1 ? at(b + lane) : -INFINITY;
+            u64 x = 0;
+            if (l > cut) {
+                x = weight(l);
+                if (x < least) x = 0;
+            }
+            const uint32_t mask = __ballot_sync(kAll, tied && l == cut);
+            if (tied && l == cut && before + __popc(mask & ((1u << lane) - 1u)) < ties) x = wt;
+            before += __popc(mask);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const u64 x = __shfl_up_sync(0xffffffffu, c, o);
-                if (lane >= o) c += x;
+                const u64 y = __shfl_up_sync(kAll, x, o);
+                if (lane >= o) x += y;
             }
-            const uint32_t hit = __ballot_sync(0xffffffffu, sum + c > target);
+            const uint32_t hit = __ballot_sync(kAll, sum + x > target);
             if (hit) {
-                if (lane == 0) a.out[r] = b + __ffs(hit) - 1;
+                if (lane == 0) a.out[r] = first + b + __ffs(hit) - 1;
                 break;
             }
-            sum += __shfl_sync(0xffffffffu, c, 31);
+            sum += __shfl_sync(kAll, x, 31);
         }
     }
 }
@@ -240,11 +702,36 @@ __global__ void __launch_bounds__(kSpThreads) sample_kernel(const SampleArgs a) 
 
 cudaError_t sample_rows(int dtype_bf16, const void *logits, int64_t ld, int n_rows, int V, const float *temperature,
                         const int32_t *top_k, const float *top_p, const float *min_p, const float *uniform,
-                        int32_t *out, unsigned *err, cudaStream_t st) {
+                        int32_t *out, unsigned *err, int num_sms, cudaStream_t st) {
     if (n_rows <= 0) return cudaSuccess;
-    SampleArgs a{logits, ld, V, temperature, top_p, min_p, uniform, top_k, out, err};
-    if (dtype_bf16) return launch_pdl(sample_kernel<bf16>, dim3(n_rows), dim3(kSpThreads), 0, st, a);
-    return launch_pdl(sample_kernel<float>, dim3(n_rows), dim3(kSpThreads), 0, st, a);
+    constexpr int kMaxPer = (227 * 1024 - (int)sizeof(SampleSmem)) / 4 / kSpThreads * kSpThreads;
+    static const int forced = [] { const char *e = getenv("SP_C"); return e ? atoi(e) : 0; }();
+    int C = 1;
+    while (C < kMaxCluster && ((V + C - 1) / C > kMaxPer || (int64_t)n_rows * C * 2 <= num_sms)) C *= 2;
+    if (forced) C = forced;
+    const int per = ((V + C - 1) / C + 3) / 4 * 4;
+    const bool held = per <= kMaxPer;
+    SampleArgs a{logits, ld, V, per, temperature, top_p, min_p, uniform, top_k, out, err};
+    const void *f = dtype_bf16 ? (held ? (const void *)sample_kernel<bf16, true> : (const void *)sample_kernel<bf16, false>)
+                               : (held ? (const void *)sample_kernel<float, true> : (const void *)sample_kernel<float, false>);
+    const size_t smem = sizeof(SampleSmem) + (held ? (size_t)per * 4 : 0);
+    cudaError_t e = max_smem_once(f, (int)(sizeof(SampleSmem) + kMaxPer * 4));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)n_rows * C);
+    cfg.blockDim = dim3(kSpThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    void *args[] = {&a};
+    return cudaLaunchKernelExC(&cfg, f, args);
 }
 
 }  // namespace orca

@@ -159,7 +159,7 @@ cudaError_t argmax_rows(const float *logits, int n_rows, int V, int32_t *next, i
 // Sampled token of every row (k_sample.cu); parameter arrays on the device, null = off.
 cudaError_t sample_rows(int dtype_bf16, const void *logits, int64_t ld, int n_rows, int V, const float *temperature,
                         const int32_t *top_k, const float *top_p, const float *min_p, const float *uniform,
-                        int32_t *out, unsigned *err, cudaStream_t st);
+                        int32_t *out, unsigned *err, int num_sms, cudaStream_t st);
 
 // 4-bit K/V cache (k_kv4.cu).  A batch of ranges over one layer, and the plan
 // built from it (int32 words; the device copy also holds arrival counters,

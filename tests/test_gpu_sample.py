@@ -182,7 +182,9 @@ def test_refusals(native, eng):
     for args in ((0, 0, 1, 10, 10, None, None, None, None, a, b), (0, a, 1, 10, 10, None, None, None, None, 0, b),
                  (0, a, 1, 10, 10, None, None, None, None, a, 0), (0, a, -1, 10, 10, None, None, None, None, a, b),
                  (0, a, 1, 0, 10, None, None, None, None, a, b), (0, a, 1, 10, 9, None, None, None, None, a, b),
-                 (2, a, 1, 10, 10, None, None, None, None, a, b),
+                 (2, a, 1, 10, 10, None, None, None, None, a, b), (0, a + 2, 1, 10, 10, None, None, None, None, a, b),
+                 (1, a + 1, 1, 10, 10, None, None, None, None, a, b), (0, a, 1, 10, 10, a + 1, None, None, None, a, b),
+                 (0, a, 1, 10, 10, None, None, None, None, a, b + 2),
                  (0, a, 1, (1 << 20) + 1, 1 << 21, None, None, None, None, a, b)):
         assert L.orca_op_sample(h, *args) == E
     assert L.orca_op_sample(h, 0, a, 0, 10, 10, None, None, None, None, a, b) == 0
