@@ -27,7 +27,6 @@
 #include <algorithm>
 #include <cfloat>
 #include <cstddef>
-#include <cstdlib>
 
 #include "common.cuh"
 #include "kernels.cuh"
@@ -43,6 +42,7 @@ constexpr int kFrac = 42;     // fraction bits of a weight
 constexpr int kBins = 2048;   // histogram bins (four per thread)
 constexpr int kList = 1024;   // tokens settled by sorting (two per thread)
 constexpr int kMaxCluster = 8;
+static_assert(kSpWarps / 2 + 1 >= kMaxCluster, "two warps fetch a CTA's list");
 
 using u64 = unsigned long long;
 static_assert(kBins == 4 * kSpThreads && kList == 2 * kSpThreads, "bins and list per thread");
@@ -71,16 +71,17 @@ __device__ __forceinline__ float sp_value(uint32_t key) {
 // ---------------------------------------------------------------------------
 // 2^-t in fixed point, table-driven (P. T. P. Tang, "Table-driven
 // implementation of the exponential function in IEEE floating-point
-// arithmetic", 1989): t = n - j / 32 - g with |g| <= 1/64, so
-// 2^-t = 2^-n 2^(j/32) 2^g, 2^g by its Taylor polynomial.  In pairs of floats,
-// since fp64 runs at 1/64 of the fp32 rate here: relative error below 2^-34
-// (measured over 2^22 arguments: 2^-34.3).
+// arithmetic", 1989): t = n - j / 8 - g with j = 0 .. 7 and |g| <= 1/16, so
+// 2^-t = 2^-n 2^(j/8) 2^g, 2^g by its Taylor polynomial.  In pairs of floats,
+// since fp64 runs at 1/64 of the fp32 rate here: relative error below 2^-37
+// (the worst of 2 million random arguments: 2^-38.1).  Eight entries of 16 bytes
+// span the 32 banks once: lanes that read different ones never conflict.
 // ---------------------------------------------------------------------------
 struct alignas(16) ExpEntry {
-    u64 fixed;  // 2^(j / 32) with 42 fraction bits
+    u64 fixed;  // 2^(j / 8) with 43 fraction bits
     float hi, lo;  // the same as a pair of floats
 };
-constexpr int kExpEntries = 33;  // j = -16 .. 16
+constexpr int kExpEntries = 8;
 constexpr double exp_series(double x) {
     double term = 1, sum = 1;
     for (int i = 1; i < 30; ++i) term *= x / i, sum += term;
@@ -93,8 +94,8 @@ constexpr double kLn2 = 0.69314718055994530942;
 constexpr ExpTable make_exp_table() {
     ExpTable t{};
     for (int j = 0; j < kExpEntries; ++j) {
-        const double v = exp_series((j - 16) * (kLn2 / 32));
-        t.e[j].fixed = (u64)(v * (double)(1ull << kFrac) + 0.5);
+        const double v = exp_series(j * (kLn2 / 8));
+        t.e[j].fixed = (u64)(v * (double)(2ull << kFrac) + 0.5);
         t.e[j].hi = (float)v;
         t.e[j].lo = (float)(v - (double)t.e[j].hi);
     }
@@ -114,32 +115,37 @@ __device__ __forceinline__ u64 sp_weight_of(float l, float top, const Scale &c, 
     const float bb = __fsub_rn(top, d);
     const float e = __fadd_rn(__fsub_rn(top, __fadd_rn(d, bb)), __fsub_rn(bb, l));
     // t + tl = (d + e) log2(e) / T
-    const float t = __fmul_rn(d, c.hi);
-    if (!(t < 43.5f)) return 0ull;  // 2^-t is below half of the last place
+    const float t0 = __fmul_rn(d, c.hi);
+    const bool some = t0 < 43.5f;  // otherwise 2^-t is below half of the last place
+    const float t = some ? t0 : 0.f;
     const float tl = __fmaf_rn(d, c.hi, -t) + __fmaf_rn(d, c.lo, __fmul_rn(e, c.hi));
-    const float n = rintf(t);
-    const float f = __fsub_rn(n, t);  // exact, |f| <= 1/2
-    const float jf = rintf(f * 32.f);
-    const float g = __fmaf_rn(jf, -0.03125f, f);  // exact, |g| <= 1/64
-    const ExpEntry x = table[(int)jf + 16];
-    // 2^(g - tl) - 1 = a + (b + a^2 / 2 + ..) with a + b = (g - tl) ln 2
+    // (integers are read off the low bits of a float near 1.5 2^23: conversions run at an eighth of the rate)
+    constexpr float kRound = 12582912.f;
+    const float vr = __fmaf_rn(t, 8.f, kRound);
+    const int v = __float_as_int(vr) - __float_as_int(kRound), sh = (v + 7) >> 3;
+    const float g = __fmaf_rn(vr - kRound, 0.125f, -t);  // v / 8 - t: exact
+    const ExpEntry x = table[-v & 7];
+    // 2^(g - tl) - 1 = a + b + a^2 / 2 + .. with a + b = (g - tl) ln 2
     constexpr float kL = (float)kLn2, kLl = (float)(kLn2 - (double)(float)kLn2);
     const float a = __fmul_rn(g, kL);
     const float b = __fmaf_rn(g, kL, -a) + __fmaf_rn(g, kLl, -tl * kL);
-    // a^2 / 2 + a^3 / 6 + .. + a^5 / 120, and the cross term a b
-    float q = __fmaf_rn(a, 1.f / 120.f, 1.f / 24.f);
-    q = __fmaf_rn(a, q, 1.f / 6.f);
-    q = __fmaf_rn(a, q, 0.5f);
-    const float a2 = __fmul_rn(a, a), a2l = __fmaf_rn(a, a, -a2);
-    const float r = __fmaf_rn(a2, q, b) + __fmaf_rn(a, b, 0.5f * a2l);
-    // 2^(j/32) (a + r): the leading part on a grid of 2^-19, the rest below it
-    const float p = __fmul_rn(x.hi, a);
-    const float rest = __fmaf_rn(x.hi, a, -p) + __fmaf_rn(x.hi, r, x.lo * a);
-    const float i1 = rintf(p * 524288.f);
-    const float i2 = rintf((__fmaf_rn(i1, -1.f / 524288.f, p) + rest) * 4398046511104.f);
-    const long long m = (long long)x.fixed + ((long long)(int)i1 << (kFrac - 19)) + (long long)(int)i2;
-    const int sh = (int)n;
-    return sh ? (u64)((m + (1ll << (sh - 1))) >> sh) : (u64)m;
+    // a^2 / 2 = h + hl; u = a^3 / 6 + .. + a^6 / 720; b times the whole 2^g
+    const float h = __fmul_rn(0.5f * a, a), hl = __fmaf_rn(0.5f * a, a, -h);
+    float q = __fmaf_rn(a, 1.f / 360.f, 1.f / 60.f);
+    q = __fmaf_rn(a, q, 1.f / 12.f);
+    q = __fmaf_rn(a, q, 1.f / 3.f);
+    // 2^(j/8) (a + h + rest) = y + yl
+    const float s1 = __fadd_rn(a, h), u = __fmul_rn(h * a, q), rest = u + (__fmaf_rn(b, s1 + u, b) + hl);
+    const float s2 = __fadd_rn(__fsub_rn(a, s1), h) + rest;
+    const float p = __fmul_rn(x.hi, s1), pl = __fmaf_rn(x.hi, s1, -p) + __fmaf_rn(x.hi, s2, x.lo * s1);
+    const float y = __fadd_rn(p, pl), yl = __fadd_rn(__fsub_rn(p, y), pl);
+    // y's leading part on a grid of 2^-21, the rest below it
+    const float r1 = __fmaf_rn(y, 2097152.f, kRound), i1 = r1 - kRound;
+    const float r2 = __fmaf_rn(__fmaf_rn(i1, -1.f / 2097152.f, y) + yl, 8796093022208.f, kRound);
+    const long long m = (long long)x.fixed + (long long)(__float_as_int(r1) - __float_as_int(kRound)) * (1 << (kFrac - 20)) +
+                        (__float_as_int(r2) - __float_as_int(kRound));
+    const u64 w = (((u64)m >> sh) + 1) >> 1;
+    return some ? w : 0ull;  // (no branch: several logits are worked on at a time)
 }
 
 template <typename V>
@@ -159,9 +165,12 @@ struct SampleShare {
     u64 sum[kMaxCluster];
     uint32_t count[kMaxCluster];  // of gathered logits, or of those equal to the cut
     uint32_t first[kMaxCluster];  // first id of the largest logit; ties of the final pass
-    // what rank 0 decides, in its copy read by all
-    uint32_t bin, found, key;
-    u64 want, wanted, left, total;
+    // what a histogram says (every CTA finds it by itself)
+    uint32_t bin, found;
+    u64 want, wanted, total;
+    // what rank 0 settles, in its copy read by all (before they enter the next barrier; it is written behind one)
+    uint32_t key;
+    u64 left;
     uint32_t gathered;  // this CTA's
 };
 
@@ -170,15 +179,15 @@ struct alignas(16) SampleSmem {
     ExpEntry exp[kExpEntries];
     union {
         struct {
-            alignas(16) uint32_t lo[kBins];  // counts in lo, or masses in (hi, lo)
+            alignas(16) uint32_t lo[kBins];  // counts in lo, or masses in (hi, lo); read by the row's other CTAs
             alignas(16) uint32_t hi[kBins];
         };
-        struct {
-            alignas(16) u64 list[kList];  // (key, ~id) of gathered tokens, then sorted
+        struct {                    // rank 0, once nobody reads its histogram
+            u64 mass[kList];        // weights of the sorted list
             uint32_t order[kList];  // (id, place) of the kept ones
         };
     };
-    u64 mass[kList];
+    alignas(16) u64 list[kList];  // (key, ~id) of gathered tokens, in rank 0 sorted; each warp's queue (each_above)
     u64 wsum[kSpWarps];
     uint32_t wcnt[kSpWarps];
 };
@@ -203,10 +212,9 @@ __device__ __forceinline__ void block_scan2(u64 &x0, u64 &x1, u64 *wsum) {
     x0 = c - x1, x1 = c;
 }
 
-// Sort v[0 .. n), distinct but for the padding up to a power of two (`pad`, last in the order), ascending or
-// descending; n <= kList, v has room for kList.  Few: every element counts those in front of it.  More: a
-// bitonic network, a pair per thread; pairs at most 32 apart stay within the 64 elements of one warp, whose steps
-// need no block barrier.
+// Sort v[0 .. n), distinct but for the padding (`pad`, last in the order), ascending or descending; n <= kList, v has
+// room for kList.  Few: every element counts those in front of it.  More: a bitonic network over two elements per
+// thread, 2t and 2t + 1: partners up to 32 apart are a shuffle away, others meet in v.
 template <bool Up, typename V>
 __device__ __forceinline__ void block_sort(V *v, int n, V pad) {
     const int t = threadIdx.x;
@@ -225,26 +233,45 @@ __device__ __forceinline__ void block_sort(V *v, int n, V pad) {
     }
     int full = 256;
     while (full < n) full *= 2;
-    for (int j = n + t; j < full; j += kSpThreads) v[j] = pad;
-    __syncthreads();
-    for (int size = 2; size <= full; size <<= 1)
-        for (int stride = size >> 1; stride > 0; stride >>= 1) {
-            if (t < full / 2) {
-                const int i = 2 * (t & ~(stride - 1)) | (t & (stride - 1)), j = i + stride;
-                const bool up = ((i & size) == 0) == Up;
-                const V a = v[i], b = v[j];
-                if ((a > b) == up) v[i] = b, v[j] = a;
+    V x[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) x[e] = 2 * t + e < n ? v[2 * t + e] : pad;
+    for (int size = 2; size <= full; size <<= 1) {
+        const bool up = ((2 * t & size) == 0) == Up;
+        int stride = size >> 1;
+        for (; stride > 32; stride >>= 1) {
+            __syncthreads();
+            v[2 * t] = x[0], v[2 * t + 1] = x[1];
+            __syncthreads();
+            const bool low = ((2 * t & stride) == 0) == up;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const V o = v[(2 * t + e) ^ stride];
+                x[e] = (o < x[e]) == low ? o : x[e];
             }
-            if (stride > 32 || (stride == 1 && size >= 64)) __syncthreads();
-            else __syncwarp();
         }
+        for (; stride > 1; stride >>= 1) {
+            const bool low = ((2 * t & stride) == 0) == up;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const V o = __shfl_xor_sync(0xffffffffu, x[e], stride >> 1);
+                x[e] = (o < x[e]) == low ? o : x[e];
+            }
+        }
+        if ((x[0] > x[1]) == up) {
+            const V y = x[0];
+            x[0] = x[1], x[1] = y;
+        }
+    }
+    __syncthreads();
+    v[2 * t] = x[0], v[2 * t + 1] = x[1];
     __syncthreads();
 }
 
 // Held: the row is kept in shared memory; otherwise (rows of more ids than a cluster holds) every pass reads the
 // logits again.
 template <typename T, bool Held>
-__global__ void __launch_bounds__(kSpThreads) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kSpThreads, 1) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t sp_raw[];
     SampleSmem &sm = *reinterpret_cast<SampleSmem *>(sp_raw);
     float *val = reinterpret_cast<float *>(sp_raw + sizeof(SampleSmem));
@@ -287,6 +314,20 @@ __global__ void __launch_bounds__(kSpThreads) sample_kernel(const SampleArgs a) 
             }
         } else {
             for (int i = tid; i < n; i += kSpThreads) f(i, at(i));
+        }
+    };
+    // the same by fours (f(first id, four logits); those past the end are -inf)
+    auto each4 = [&](auto f) {
+        for (int i = 4 * tid; i < n; i += 4 * kSpThreads) {
+            float l[4];
+            if constexpr (Held) {
+                const float4 x = *reinterpret_cast<const float4 *>(val + i);
+                l[0] = x.x, l[1] = x.y, l[2] = x.z, l[3] = x.w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) l[e] = i + e < n ? at(i + e) : -INFINITY;
+            }
+            f(i, l);
         }
     };
     float top = -INFINITY;
@@ -362,9 +403,53 @@ __global__ void __launch_bounds__(kSpThreads) sample_kernel(const SampleArgs a) 
     // the last bin also takes everything without weight)
     auto bin_of = [&](float l) {
         const float d = __fmul_rn(__fmul_rn(__fsub_rn(top, l), cs.hi), (float)(kBins / 43.5));
-        return l == top ? 0 : (int)fminf(d, (float)(kBins - 1));
+        const float near = fminf(d, (float)(kBins - 1)) + 8388608.f;  // (to the nearest: the low bits of 2^23 + bin)
+        return l == top ? 0 : __float_as_int(near) & (2 * kBins - 1);
     };
+    // a logit that none of bins 0 .. b is below (one bin of slack for the roundings)
+    auto low_of = [&](int b) { return top - (float)(b + 2) * (float)(43.5 / kBins) * 1.000001f / cs.hi; };
     SampleSmem &root = peer(0);
+    // f(l, on) for 32 logits above the cut at a time (all lanes; `on`: this lane has one), g(l) for every logit, over
+    // a warp's contiguous stretch of ids; the logits above are queued so that few of them cost little.
+    const int per_warp = (n + 4 * kSpThreads - 1) / (4 * kSpThreads) * 128;
+    const int i0 = min(n, warp * per_warp), i1 = min(n, i0 + per_warp);
+    auto each_above = [&](float above, auto f, auto g) {
+        constexpr int kQueue = 2 * kList / kSpWarps;  // floats per warp
+        static_assert(kQueue >= 31 + 64, "what two ballots add to a rest of 31");
+        float *queue = reinterpret_cast<float *>(sm.list) + warp * kQueue;
+        int held = 0;
+        for (int i = i0 + 4 * lane; i - 4 * lane < i1; i += 128) {
+            float l[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) l[e] = -INFINITY;
+            if (i < i1) {
+                if constexpr (Held) {
+                    const float4 x = *reinterpret_cast<const float4 *>(val + i);
+                    l[0] = x.x, l[1] = x.y, l[2] = x.z, l[3] = x.w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (i + e < i1) l[e] = at(i + e);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                g(l[e]);
+                const uint32_t mask = __ballot_sync(kAll, l[e] > above);
+                if (l[e] > above) queue[held + __popc(mask & ((1u << lane) - 1u))] = l[e];
+                held += __popc(mask);
+                if (e & 1) {
+                    __syncwarp();
+                    while (held >= 32) {
+                        held -= 32;
+                        f(queue[held + lane], true);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (held > 0) f(lane < held ? queue[lane] : above, lane < held);
+    };
 
     // the mass that a prefix has to reach: p times the whole, rounded up, at least one
     const u64 pf = p < 1.f ? frac64(p) : 0ull;
@@ -378,35 +463,52 @@ __global__ void __launch_bounds__(kSpThreads) sample_kernel(const SampleArgs a) 
     float cut = -INFINITY;
     uint32_t ties = 0xffffffffu;
 
-    // Histogram over the bins of(l) >= 0 of the logits above the cut, counts or masses, added up in rank 0.  There
-    // pick(total) says what is wanted, and root.sh gets whether that much is there (found), the bin in which it is
-    // reached from the largest logits down, what is left of it for that bin (want) and all of it (wanted).  `down`:
-    // larger logits are in higher bins.
+    // Histogram over the bins of(l) >= 0 of the logits above the cut, counts or masses, added up over the row's CTAs
+    // by each of them.  pick(total) says what is wanted, and sm.sh gets whether that much is there (found), the bin in
+    // which it is reached from the largest logits down, what is left of it for that bin (want) and all of it (wanted).
+    // `down`: larger logits are in higher bins.  A barrier has to follow before the next histogram.
     auto histogram = [&](bool by_mass, bool down, auto of, auto pick) {
         for (int i = tid; i < kBins / 4; i += kSpThreads) {
             reinterpret_cast<uint4 *>(sm.lo)[i] = make_uint4(0, 0, 0, 0);
             if (by_mass) reinterpret_cast<uint4 *>(sm.hi)[i] = make_uint4(0, 0, 0, 0);
         }
         __syncthreads();
-        each([&](int, float l) {
-            if (!(l > cut)) return;
-            const int b = of(l);
+        auto put = [&](float l, u64 w) {
+            const int b = l > cut ? of(l) : -1;
             if (b < 0) return;
-            if (by_mass) {
-                const u64 w = weight(l);
-                const uint32_t wl = (uint32_t)w, old = atomicAdd(&sm.lo[b], wl);
-                const uint32_t wh = (uint32_t)(w >> 32) + (old + wl < old);
-                if (wh) atomicAdd(&sm.hi[b], wh);
-            } else {
-                atomicAdd(&sm.lo[b], 1u);
-            }
-        });
+            const uint32_t wl = (uint32_t)w, old = atomicAdd(&sm.lo[b], wl);
+            const uint32_t wh = (uint32_t)(w >> 32) + (old + wl < old);
+            if (wh) atomicAdd(&sm.hi[b], wh);
+        };
+        if (by_mass && cut != -INFINITY)
+            each_above(
+                cut,
+                [&](float l, bool on) {
+                    const u64 w = weight(l);
+                    if (on) put(l, w);
+                },
+                [](float) {});
+        else if (by_mass)
+            each4([&](int, const float *l) {
+                u64 w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = weight(l[e]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) put(l[e], w[e]);
+            });
+        else
+            each([&](int, float l) {
+                const int b = l > cut ? of(l) : -1;
+                if (b >= 0) atomicAdd(&sm.lo[b], 1u);
+            });
         meet();
-        if (rank == 0) {
+        {
             // thread t: four bins, in the order of descending logits
             const int q = down ? kBins / 4 - 1 - tid : tid;
             u64 x[4] = {0, 0, 0, 0}, s = 0;
-            for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) {  // (all loads in flight)
+                if (c >= C) break;
                 const SampleSmem &o = peer(c);
                 const uint4 lo = reinterpret_cast<const uint4 *>(o.lo)[q];
                 uint4 hi = make_uint4(0, 0, 0, 0);
@@ -446,18 +548,24 @@ __global__ void __launch_bounds__(kSpThreads) sample_kernel(const SampleArgs a) 
                 }
             }
         }
-        meet();
+        __syncthreads();
     };
 
     // Every (key, ~id) of the logits above the cut that take(l) names, in rank 0's list; returns how many there
     // are (more than kList: the list is not to be used).
-    auto collect = [&](auto take) {
+    // `low`: no logit below it is taken.
+    auto collect = [&](float low, auto take) {
         if (tid == 0) sm.sh.gathered = 0;
         __syncthreads();
-        each([&](int i, float l) {
-            if (!(l > cut) || !take(l)) return;
-            const uint32_t j = atomicAdd(&sm.sh.gathered, 1u);
-            if (j < kList) sm.list[j] = (u64)sp_key(l) << 32 | (uint32_t) ~(first + i);
+        each4([&](int i, const float *l) {
+            if (!(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= low)) return;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (!(l[e] > cut) || !take(l[e])) continue;
+                if (*const_cast<volatile uint32_t *>(&sm.sh.gathered) > kList) continue;  // too many: only that counts
+                const uint32_t j = atomicAdd(&sm.sh.gathered, 1u);
+                if (j < kList) sm.list[j] = (u64)sp_key(l[e]) << 32 | (uint32_t) ~(first + i + e);
+            }
         });
         __syncthreads();
         if (tid < C) peer(tid).sh.count[rank] = sm.sh.gathered;
@@ -465,12 +573,13 @@ __global__ void __launch_bounds__(kSpThreads) sample_kernel(const SampleArgs a) 
         uint32_t m = 0;
         for (int c = 0; c < C; ++c) m += sm.sh.count[c];
         if (C > 1) {
-            if (rank == 0 && m <= kList) {
-                uint32_t at_c = sm.sh.count[0];
-                for (int c = 1; c < C; ++c) {
-                    const uint32_t nc = sm.sh.count[c];
-                    for (uint32_t j = tid; j < nc; j += kSpThreads) sm.list[at_c + j] = peer(c).list[j];
-                    at_c += nc;
+            if (rank == 0 && m <= kList) {  // two warps per CTA
+                const int from = warp / 2 + 1;
+                if (from < C) {
+                    uint32_t to = 0;
+                    for (int c = 0; c < from; ++c) to += sm.sh.count[c];
+                    const u64 *theirs = peer(from).list;
+                    for (uint32_t j = tid & 63; j < sm.sh.count[from]; j += 64) sm.list[to + j] = theirs[j];
                 }
             }
             meet();  // (the other CTAs' lists are free, and they may leave)
@@ -542,18 +651,18 @@ __global__ void __launch_bounds__(kSpThreads) sample_kernel(const SampleArgs a) 
             if (level > 0) {
                 const u64 goal = want;
                 histogram(by_mass, true, of, [=](u64) { return goal; });
-                want = root.sh.want;
-                prefix |= root.sh.bin << (level == 1 ? 21 : level == 2 ? 10 : 0);
-                meet();  // (rank 0's state is free again)
+                want = sm.sh.want;
+                prefix |= sm.sh.bin << (level == 1 ? 21 : level == 2 ? 10 : 0);
                 if (level == 3) {
                     cut = sp_value(prefix);
+                    meet();
                     break;
                 }
             }
             const int low = level == 0 ? 31 : level == 1 ? 21 : 10;  // bits of the keys not yet fixed
             const uint32_t high = level == 0 ? 0u : prefix >> low;
             auto in_bin = [&](float l) { return bin_of(l) == bin0 && (level == 0 || sp_key(l) >> low == high); };
-            const int m = collect(in_bin);
+            const int m = collect(low_of(bin0), in_bin);
             if (m > kList) continue;
             if (rank == 0) {
                 block_sort<false>(sm.list, m, 0ull);
@@ -581,7 +690,6 @@ __global__ void __launch_bounds__(kSpThreads) sample_kernel(const SampleArgs a) 
             meet();
             cut = sp_value(root.sh.key);
             want = root.sh.left;
-            meet();  // (rank 0's state is free again)
             break;
         }
         const u64 w = by_mass ? weight(cut) : 1ull;
@@ -590,13 +698,13 @@ __global__ void __launch_bounds__(kSpThreads) sample_kernel(const SampleArgs a) 
 
     if (by_count) {
         histogram(false, false, bin_of, [&](u64) { return (u64)k; });
-        const int bin = (int)root.sh.bin;
-        const u64 want = root.sh.want;
+        const int bin = (int)sm.sh.bin;
+        const u64 want = sm.sh.want;
         // fewer than k logits, or the k-th without weight: the same as all kept
-        by_count = root.sh.found && bin != kBins - 1;
-        meet();  // (rank 0's state is free again)
+        by_count = sm.sh.found && bin != kBins - 1;
+        if (!by_count) meet();
         if (by_count) {
-            const int m = collect([&](float l) { return bin_of(l) <= bin; });
+            const int m = collect(low_of(bin), [&](float l) { return bin_of(l) <= bin; });
             if (m <= kList) {
                 if (rank == 0) finish(m, k, ~0ull, p < 1.f);
                 return;
@@ -607,12 +715,11 @@ __global__ void __launch_bounds__(kSpThreads) sample_kernel(const SampleArgs a) 
     if (p < 1.f) {
         const u64 wt = by_count ? weight(cut) : 0ull;
         histogram(true, false, bin_of, [&](u64 above) { return share(above + wt * (by_count ? ties : 0u)); });
-        const bool found = root.sh.found;
-        const int bin = (int)root.sh.bin;
-        const u64 want = root.sh.want, wanted = root.sh.wanted, above = root.sh.total;
-        meet();  // (rank 0's state is free again)
+        const bool found = sm.sh.found;
+        const int bin = (int)sm.sh.bin;
+        const u64 want = sm.sh.want, wanted = sm.sh.wanted, above = sm.sh.total;
         if (found) {
-            const int m = collect([&](float l) { return bin_of(l) <= bin; });
+            const int m = collect(low_of(bin), [&](float l) { return bin_of(l) <= bin; });
             if (m <= kList) {
                 if (rank == 0) finish(m, m, wanted, false);
                 return;
@@ -622,28 +729,36 @@ __global__ void __launch_bounds__(kSpThreads) sample_kernel(const SampleArgs a) 
             ties = (uint32_t)min((u64)ties, (wanted - above + wt - 1) / wt);
         }
     }
-    // the tokens in the order of their ids: a warp takes a contiguous stretch
-    const int per_warp = (n + 4 * kSpThreads - 1) / (4 * kSpThreads) * 128;
-    const int i0 = min(n, warp * per_warp), i1 = min(n, i0 + per_warp);
+    // the tokens in the order of their ids, by the warps' stretches
     const bool tied = cut != -INFINITY;
     u64 wt = tied ? weight(cut) : 0ull;
     if (wt < least) wt = 0ull;
     u64 s = 0;
     uint32_t c = 0;
-    auto add = [&](float l) {
-        if (l > cut) {
-            const u64 w = weight(l);
-            s += w >= least ? w : 0ull;
-        }
-        c += l == cut;
-    };
-    if constexpr (Held) {
-        for (int i = i0 + 4 * lane; i < i1; i += 128) {
-            const float4 x = *reinterpret_cast<const float4 *>(val + i);
-            add(x.x), add(x.y), add(x.z), add(x.w);
-        }
+    if (tied) {
+        each_above(
+            cut,
+            [&](float l, bool on) {
+                const u64 w = weight(l);
+                s += on && w >= least ? w : 0ull;
+            },
+            [&](float l) { c += l == cut; });
     } else {
-        for (int i = i0 + lane; i < i1; i += 32) add(at(i));
+        for (int i = i0 + 4 * lane; i < i1; i += 128) {
+            float l[4];
+            if constexpr (Held) {
+                const float4 x = *reinterpret_cast<const float4 *>(val + i);
+                l[0] = x.x, l[1] = x.y, l[2] = x.z, l[3] = x.w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) l[e] = i + e < i1 ? at(i + e) : -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const u64 w = weight(l[e]);
+                s += w >= least ? w : 0ull;
+            }
+        }
     }
     s = warp_add(s), c = warp_add(c);
     __syncthreads();
@@ -705,10 +820,11 @@ cudaError_t sample_rows(int dtype_bf16, const void *logits, int64_t ld, int n_ro
                         int32_t *out, unsigned *err, int num_sms, cudaStream_t st) {
     if (n_rows <= 0) return cudaSuccess;
     constexpr int kMaxPer = (227 * 1024 - (int)sizeof(SampleSmem)) / 4 / kSpThreads * kSpThreads;
-    static const int forced = [] { const char *e = getenv("SP_C"); return e ? atoi(e) : 0; }();
+    // CTAs per row: enough to hold it; two for long rows (192 mixed rows of 50257: 106 us, with one 124, with four
+    // 122), more while SMs would stand idle (one row: one 19.1, two 14.7, four 12.2, eight 12.7 us).
     int C = 1;
-    while (C < kMaxCluster && ((V + C - 1) / C > kMaxPer || (int64_t)n_rows * C * 2 <= num_sms)) C *= 2;
-    if (forced) C = forced;
+    while (C < kMaxCluster && (V + C - 1) / C > kMaxPer) C *= 2;
+    while (C < 4 && V / C > 8192 && (C == 1 || (int64_t)n_rows * C * 2 <= num_sms)) C *= 2;
     const int per = ((V + C - 1) / C + 3) / 4 * 4;
     const bool held = per <= kMaxPer;
     SampleArgs a{logits, ld, V, per, temperature, top_p, min_p, uniform, top_k, out, err};
