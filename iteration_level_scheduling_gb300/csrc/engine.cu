@@ -1108,7 +1108,10 @@ int orca_op_kv4_attention(orca_engine *E, const void *qkv, const void *kv4_layer
         !aligned16(kv4_layer) || !aligned16(dev_plan) || !aligned16(out) || !aligned16(workspace) ||
         (!workspace && kv4_workspace_bytes(host_plan) > 0) || !on_device(E))
         return ORCA_ERR_INVALID;
-    return launched(E, kv4_attention(qkv, kv4_layer, host_plan, dev_plan, workspace, out, E->st));
+    int n = 0;
+    const cudaError_t e = kv4_attention(qkv, kv4_layer, host_plan, dev_plan, workspace, out, E->d_err, &n, E->st);
+    E->launches += n - 1;
+    return launched(E, e);
 }
 
 int orca_op_sample(orca_engine *E, int32_t dtype, const void *logits, int32_t n_rows, int32_t vocab, int64_t ld,

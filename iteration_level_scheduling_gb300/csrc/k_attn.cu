@@ -33,6 +33,8 @@
 #include <cstdlib>
 #include <type_traits>
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -92,6 +94,9 @@ struct AttnArgs {
     int *counters;
     unsigned *err;
     int early;  // the decode producer may load keys before the context end ahead of the grid wait
+    // fp16 prefill: the powers of two by which q (per row and head) and K and V (per request and head) were scaled,
+    // inverted: [row][head], [request][head][K|V]
+    const float *q_scale = nullptr, *kv_scale = nullptr;
 };
 
 // One warp attends its query (q, already scaled, VEC values of its lane's
@@ -788,7 +793,9 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-template <int D>
+// F16: q, K and V are fp16 scaled into its range (AttnArgs::q_scale, kv_scale), P is rounded to fp16: three more
+// bits than bf16 for operands that were not bf16 to begin with (K and V held in 4 bits).
+template <int D, bool F16>
 __global__ void __launch_bounds__(kPtThreads, 1)
     attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmkv,
                            const AttnArgs<bf16> a) {
@@ -841,7 +848,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     // (longest first).
     const int n_items = a.p.n_pre_tiles * a.n_heads;
     struct Item {
-        int h, off, q0, ctx, kv0, rows, n_keys, n_kt;
+        int h, req, off, q0, ctx, kv0, rows, n_keys, n_kt;
     };
     auto item_at = [&](int k) {
         Item it;
@@ -849,6 +856,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         it.h = idx / a.p.n_pre_tiles;
         const int t = idx - it.h * a.p.n_pre_tiles;
         const int i = a.p.pre_tiles[2 * t];
+        it.req = i;
         it.q0 = a.p.pre_tiles[2 * t + 1];
         it.off = a.p.req_off[i];
         it.ctx = a.p.req_ctx[i];
@@ -926,8 +934,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
         const bool leader = elect_one();
-        const uint32_t idesc_s = idesc_bf16_f32(kPtRows, kPtKeys);
-        const uint32_t idesc_pv = idesc_bf16_f32(kPtRows, D) | (1u << 16);  // B (V) MN-major
+        constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // A and B bf16; cleared: fp16
+        const uint32_t idesc_s = idesc_bf16_f32(kPtRows, kPtKeys) & ~(F16 ? kBf16 : 0u);
+        const uint32_t idesc_pv = (idesc_bf16_f32(kPtRows, D) & ~(F16 ? kBf16 : 0u)) | (1u << 16);  // B (V) MN-major
         const uint32_t q_s = smem_u32(sm + L::kQ);
         // S of key tile g (the item's j-th): Q K_g^T into S buffer g & 1; the item's
         // last S also releases Q
@@ -1035,12 +1044,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             return other;
         };
         constexpr int kOc = D / 2;  // O columns of this half
+        constexpr float kMask = F16 ? -INFINITY : kNegBig;  // (scaled scores of F16 may be of any size)
         // An item's output is read out of O after the next item's first P has
         // been written (O has two buffers), so the tensor pipe has that
         // item's P V and S to work on meanwhile.
         struct Done {  // a finished item whose output is still in O
             int k, g_last, row, h, rows;
-            float l;
+            float l, v_scale;
         };
         auto write_out = [&](const Done &e) {
             bool met;
@@ -1050,7 +1060,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 return false;
             tc_fence_after();
             const uint32_t ot = lane_t + kPtTmemO + (uint32_t)((e.k & 1) * kPtOCols + kOc * half);
-            const float inv = 1.f / lt;
+            const float inv = F16 ? e.v_scale / lt : 1.f / lt;
             bf16 *dst = a.out + (size_t)(e.row + r) * a.H + e.h * D + kOc * half;
 #pragma unroll
             for (int c = 0; c < kOc / 32; ++c) {
@@ -1087,6 +1097,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int row_keys = min(it.ctx + it.q0 + r + 1, it.n_keys);  // keys 0 .. row_keys - 1 are this row's
             const int first_keys = min(it.ctx + it.q0 + 1, it.n_keys);    // the fewest any row of the tile sees
             float m = kNegBig, l = 0.f;
+            float scale = a.scale_log2, v_scale = 1.f;
+            if constexpr (F16) {
+                const float *kv = a.kv_scale + 2 * ((size_t)it.req * a.n_heads + it.h);
+                scale *= kv[0] * a.q_scale[(size_t)(it.off + it.q0 + min(r, it.rows - 1)) * a.n_heads + it.h];
+                scale = fmaxf(scale, 1e-37f);  // (a masked -inf times it stays -inf)
+                v_scale = kv[1];
+            }
             for (int j = 0; j < it.n_kt; ++j, ++g) {
                 const int b = g & 1, kbase = j * kPtKeys;
                 if (!__all_sync(kFull, !*abort && mbar_wait_bounded(&bar.s_full[b], (uint32_t)(g >> 1) & 1u, a.err))) {
@@ -1105,13 +1122,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     const int valid = min(max(row_keys - kbase - 64 * half, 0), 64);
 #pragma unroll
                     for (int c = 0; c < 64; ++c)
-                        if (c >= valid) s[c] = __float_as_uint(kNegBig);
+                        if (c >= valid) s[c] = __float_as_uint(kMask);
                 }
-                float mx = kNegBig;
+                float mx = kMask;
 #pragma unroll
                 for (int c = 0; c < 64; ++c) mx = fmaxf(mx, __uint_as_float(s[c]));
                 bool met;
-                mx = fmaxf(mx, exchange(mx, met)) * a.scale_log2;  // (scale > 0)
+                mx = fmaxf(mx, exchange(mx, met)) * scale;  // (scale > 0)
                 if (!met) {
                     ok = false;
                     break;
@@ -1159,11 +1176,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     uint32_t w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float p0 = ex2_approx(fmaf(__uint_as_float(s[8 * c8 + 2 * e]), a.scale_log2, neg_m));
-                        const float p1 = ex2_approx(fmaf(__uint_as_float(s[8 * c8 + 2 * e + 1]), a.scale_log2, neg_m));
+                        const float p0 = ex2_approx(fmaf(__uint_as_float(s[8 * c8 + 2 * e]), scale, neg_m));
+                        const float p1 = ex2_approx(fmaf(__uint_as_float(s[8 * c8 + 2 * e + 1]), scale, neg_m));
                         ls += p0 + p1;
-                        const __nv_bfloat162 pv = __floats2bfloat162_rn(p0, p1);
-                        w[e] = *reinterpret_cast<const uint32_t *>(&pv);
+                        if constexpr (F16) {
+                            const __half2 pv = __floats2half2_rn(p0, p1);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&pv);
+                        } else {
+                            const __nv_bfloat162 pv = __floats2bfloat162_rn(p0, p1);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&pv);
+                        }
                     }
                     st_shared_v4(p_row + ((uint32_t)(c8 ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
                 }
@@ -1195,7 +1217,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
             }
             if (!ok) break;
-            late = Done{k, g - 1, it.off + it.q0, it.h, it.rows, l};
+            late = Done{k, g - 1, it.off + it.q0, it.h, it.rows, l, v_scale};
             has_late = true;
         }
         if (ok && has_late) ok = write_out(late);
@@ -1698,14 +1720,14 @@ cudaError_t launch_attn(const AttnArgs<T> &a, bool decode, bool prefill, cudaStr
                     !encode_tensor_map(&tmkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.kpool, kdims, kstrides, kbox,
                                        CU_TENSOR_MAP_SWIZZLE_128B))
                     return cudaErrorInvalidValue;
-                e = max_smem_once((const void *)attn_prefill_tc_kernel<D>, (int)PtLayout<D>::kBytes);
+                e = max_smem_once((const void *)attn_prefill_tc_kernel<D, false>, (int)PtLayout<D>::kBytes);
                 if (e != cudaSuccess) return e;
                 // persistent: one CTA per SM walks the (head, tile) items
                 int sms = 0, dev = 0;
                 cudaGetDevice(&dev);
                 cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
                 const int grid = std::max(1, std::min(a.p.n_pre_tiles * a.n_heads, sms));
-                e = launch_pdl(attn_prefill_tc_kernel<D>, dim3(grid), dim3(kPtThreads), PtLayout<D>::kBytes, st, tmq,
+                e = launch_pdl(attn_prefill_tc_kernel<D, false>, dim3(grid), dim3(kPtThreads), PtLayout<D>::kBytes, st, tmq,
                                tmkv, a);
             } else {
                 e = launch_pdl(attn_prefill_mma_kernel<D>, dim3(a.p.n_pre_tiles, a.n_heads, 2), dim3(128),
@@ -1763,6 +1785,45 @@ void decode_items(const int32_t *order, const int32_t *dec_work, int n_work, con
         r[0] = req_kvoff[i] + t0, r[1] = t1 - t0, r[2] = req_off[i], r[3] = i;
         r[4] = c, r[5] = dec_nch[i], r[6] = dec_wbegin[i], r[7] = t0;
     }
+}
+
+cudaError_t attention_prefill_f16(const void *q16, int n_rows, const void *pool16, int64_t slots, bf16 *out,
+                                  const AttnPlan &p, int H, int n_heads, const float *q_scale, const float *kv_scale,
+                                  unsigned *err, cudaStream_t st) {
+    const int D = H / n_heads;
+    if (p.n_pre_tiles <= 0) return cudaSuccess;
+    AttnArgs<bf16> a{};
+    a.out = out;
+    a.H = H;
+    a.n_heads = n_heads;
+    a.scale_log2 = 1.4426950408889634f / sqrtf((float)D);
+    a.p = p;
+    a.err = err;
+    a.q_scale = q_scale;
+    a.kv_scale = kv_scale;
+    CUtensorMap tmq, tmkv;
+    const uint64_t qdims[2] = {(uint64_t)H, (uint64_t)n_rows};
+    const uint64_t qstrides[1] = {(uint64_t)H * 2};
+    const uint32_t qbox[2] = {64, kPtRows};
+    const uint64_t kdims[3] = {(uint64_t)D, (uint64_t)slots, (uint64_t)2 * n_heads};
+    const uint64_t kstrides[2] = {(uint64_t)D * 2, (uint64_t)slots * D * 2};
+    const uint32_t kbox[3] = {64, kPtKeys, 1};
+    if (!encode_tensor_map(&tmq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q16, qdims, qstrides, qbox,
+                           CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tensor_map(&tmkv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, pool16, kdims, kstrides, kbox,
+                           CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    int sms = 0, dev = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int grid = std::max(1, std::min(p.n_pre_tiles * n_heads, sms));
+    auto run = [&](auto kernel, int smem) {
+        const cudaError_t e = max_smem_once((const void *)kernel, smem);
+        return e != cudaSuccess ? e : launch_pdl(kernel, dim3(grid), dim3(kPtThreads), smem, st, tmq, tmkv, a);
+    };
+    if (D == 64) return run(attn_prefill_tc_kernel<64, true>, (int)PtLayout<64>::kBytes);
+    if (D == 128) return run(attn_prefill_tc_kernel<128, true>, (int)PtLayout<128>::kBytes);
+    return cudaErrorInvalidValue;
 }
 
 template <typename T>

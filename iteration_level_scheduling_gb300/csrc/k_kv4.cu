@@ -27,6 +27,8 @@
 #include <type_traits>
 #include <vector>
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -153,21 +155,42 @@ __device__ __forceinline__ void store8(T *p, const float *x) {
     for (int i = 0; i < 8; i += Elem<T>::kPer16) store16(p + i, x + i);
 }
 
+__device__ __forceinline__ void store8(__half *p, const float *x) {
+    uint4 u;
+    __half2 *h = reinterpret_cast<__half2 *>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    *reinterpret_cast<uint4 *>(p) = u;
+}
+
+// scale: the inverses of the powers of two that the values are to be multiplied by ([request][head][K|V]), or null
 template <typename T>
 __global__ void __launch_bounds__(kRdThreads) kv4_read_kernel(Kv4View v, const int32_t *tiles, T *out, int64_t out_slots,
-                                                              int n_heads, int d, int G) {
+                                                              int n_heads, int d, int G, const float *scale) {
     pdl_trigger();
     pdl_wait();
-    const int4 tl = reinterpret_cast<const int4 *>(tiles)[blockIdx.x];  // first slot, slots, first output index
+    const int4 tl = reinterpret_cast<const int4 *>(tiles)[blockIdx.x];  // first slot, slots, first output index, request
     const int h = blockIdx.y, gs = d / G, upr = d / 8;                  // 8-component units per row
     const int64_t s0 = tl.x, s1 = s0 + tl.y;
+    float kf = 1.f, vf = 1.f;
+    if (scale) {
+        const float *f = scale + 2 * ((size_t)tl.w * n_heads + h);
+        kf = 1.f / f[0], vf = 1.f / f[1];
+    }
     T *ko = out + ((int64_t)h * out_slots + tl.z) * d, *vo = ko + (int64_t)n_heads * out_slots * d;
     for (int i = threadIdx.x; i < tl.y * upr; i += kRdThreads) {
         const int j = i / upr, u = i - j * upr;
         const int64_t row = (int64_t)h * v.S + s0 + j;
         const uint32_t w = *reinterpret_cast<const uint32_t *>(v.kc + row * (d / 2) + u * 4);
         const uint32_t p = v.kp[row * G + u * 8 / gs];
-        const float s = bf_lo(p), m = bf_hi(p);
+        float s = bf_lo(p) * kf, m = bf_hi(p) * kf;
+        if (scale) {
+            // a NaN among the values is moved to the key: a weight of 0 times it would reach rows that do not see
+            // the key, while a masked score is dropped whatever it is
+            const int64_t slot = s0 + j;
+            const uint32_t pv = v.vp[(((int64_t)h * (v.S / 2) + (slot >> 1)) * G + u * 8 / gs) * 2 + (slot & 1)];
+            if (bf_lo(pv) != bf_lo(pv)) m = bf_lo(pv);
+        }
         float x[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = fmaf(s, (float)((w >> (4 * k)) & 15u), m);
@@ -184,7 +207,8 @@ __global__ void __launch_bounds__(kRdThreads) kv4_read_kernel(Kv4View v, const i
             const int64_t slot = 2 * (p0 + j) + o;
             if (slot < s0 || slot >= s1) continue;
             const uint32_t a = w.x >> (16 * o), b = w.y >> (16 * o), pp = o ? p.y : p.x;
-            const float s = bf_lo(pp), m = bf_hi(pp);
+            float s = bf_lo(pp) * vf, m = bf_hi(pp) * vf;
+            if (scale && s != s) s = m = 0.f;
             float x[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -194,6 +218,95 @@ __global__ void __launch_bounds__(kRdThreads) kv4_read_kernel(Kv4View v, const i
             store8(vo + (slot - s0) * d + u * 8, x);
         }
     }
+}
+
+// ---------------------------------------------------------------------------
+// prompts on the tcgen05 prefill kernel: q, K and V as fp16 in a workspace
+// ---------------------------------------------------------------------------
+// fp16 rather than bf16: K and V come from codes and not from bf16 values, so
+// rounding them to 8 bits would add an error as large as the output's own.
+// fp16 keeps 11 bits; its narrow range is met by powers of two, one per row and
+// head for q and one per request and head for K and V, that bring the largest
+// magnitude to [2^14, 2^15) (values 2^-28 of it and below lose bits).
+
+// The power of two for a largest magnitude, as its inverse; 1 where that is zero or subnormal.
+__device__ __forceinline__ float kv4_inverse_scale(float amax) {
+    const int e = (int)(__float_as_uint(amax) >> 23);  // (amax >= 0)
+    if (e == 0) return 1.f;
+    return __uint_as_float((uint32_t)max(e - 14, 27) << 23);  // 2^(e - 127 - 14), not below 2^-100
+}
+
+struct Kv4Prep {
+    const bf16 *qkv;
+    __half *q16;
+    float *q_scale, *kv_scale;
+    Kv4View v;
+    int H, n_heads, d, G, n_rows, n_pre;
+    const int32_t *pre;  // 4 words per prompt: request, first slot, slots, 0
+};
+constexpr int kPrepThreads = 256;
+
+// Blocks 0 .. n_pre * n_heads - 1: the scales of K and V of one prompt and head, from the parameters (a component lies
+// between m and m + 15 s).  The others: a warp scales and rounds q of one row and head.
+__global__ void __launch_bounds__(kPrepThreads) kv4_prep_kernel(const Kv4Prep a) {
+    __shared__ float red[2][kPrepThreads / 32];
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = a.n_pre * a.n_heads;
+    if ((int)blockIdx.x < first) {
+        const int i = blockIdx.x / a.n_heads, h = blockIdx.x - i * a.n_heads;
+        const int4 pr = reinterpret_cast<const int4 *>(a.pre)[i];
+        const int64_t s0 = pr.y, s1 = s0 + pr.z;
+        float km = 0.f, vm = 0.f;
+        // (fmaxf drops NaN: a group that reads back as NaN does so whatever the scale)
+        auto size = [](uint32_t p) { return fmaxf(fabsf(bf_hi(p)), fabsf(fmaf(15.f, bf_lo(p), bf_hi(p)))); };
+        const uint32_t *kp = a.v.kp + ((int64_t)h * a.v.S + s0) * a.G;
+        const int64_t nk = (s1 - s0) * a.G;
+#pragma unroll 4
+        for (int64_t j = threadIdx.x; j < nk; j += kPrepThreads) km = fmaxf(km, size(kp[j]));
+        const int64_t p0 = s0 >> 1, np = ((s1 + 1) >> 1) - p0;
+        const uint2 *vp = reinterpret_cast<const uint2 *>(a.v.vp) + ((int64_t)h * (a.v.S / 2) + p0) * a.G;
+#pragma unroll 4
+        for (int64_t j = threadIdx.x; j < np * a.G; j += kPrepThreads) {
+            const uint2 p = vp[j];
+            const int64_t slot = 2 * (p0 + j / a.G);
+            if (slot >= s0) vm = fmaxf(vm, size(p.x));
+            if (slot + 1 < s1) vm = fmaxf(vm, size(p.y));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, o));
+            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        }
+        if (lane == 0) red[0][warp] = km, red[1][warp] = vm;
+        __syncthreads();
+        if (threadIdx.x < 2) {
+            float m = 0.f;
+            for (int w = 0; w < kPrepThreads / 32; ++w) m = fmaxf(m, red[threadIdx.x][w]);
+            a.kv_scale[2 * ((size_t)pr.x * a.n_heads + h) + threadIdx.x] = kv4_inverse_scale(m);
+        }
+        return;
+    }
+    const int64_t unit = ((int64_t)blockIdx.x - first) * (kPrepThreads / 32) + warp;  // (row, head)
+    if (unit >= (int64_t)a.n_rows * a.n_heads) return;
+    const int64_t r = unit / a.n_heads;
+    const int h = (int)(unit - r * a.n_heads);
+    const bool on = lane * 8 < a.d;  // 8 components per lane
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    if (on) load16_stream(a.qkv + r * 3 * a.H + h * a.d + lane * 8, x);
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(x[e]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float inv = kv4_inverse_scale(m), f = 1.f / inv;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= f;
+    if (on) store8(a.q16 + r * a.H + h * a.d + lane * 8, x);
+    if (lane == 0) a.q_scale[r * a.n_heads + h] = inv;
 }
 
 // ---------------------------------------------------------------------------
@@ -616,26 +729,46 @@ enum : int {
     Q_O_ITEMS,
     Q_O_COUNT,
     Q_O_TILES,
+    Q_PRE,       // prompts: requests whose rows run on the prefill kernel
+    Q_PRETILES,  // their (request, 128 rows) tiles
+    Q_PREREAD,   // read-back tiles of their slots
+    Q_PREKEYS,   // their slots
+    Q_REQS,
+    Q_O_PRE,
+    Q_O_PRETILES,
+    Q_O_PREREAD,
+    Q_O_REQOFF,
+    Q_O_REQCTX,
+    Q_O_REQWS,  // a prompt's first slot in the workspace's pool
 };
+// Requests of at least this many rows run on the prefill kernel (bf16, head_dim 64 or 128).
+constexpr int kPromptRows = 16;
 
 int64_t up4(int64_t w) { return (w + 3) & ~int64_t(3); }
 
 struct Kv4Sizes {
     int64_t rows = 0, items = 0, splits = 0, parts = 0, tiles = 0, keys = 0;
+    int64_t pre = 0, pre_tiles = 0, pre_read = 0, pre_keys = 0;
     int chunk = 0;
-    int64_t off_rowslot, off_items, off_count, off_tiles, total;
+    int64_t off_rowslot, off_items, off_count, off_tiles, off_pre, off_pretiles, off_preread, off_reqoff, off_reqctx,
+        off_reqws, total;
 };
 
 // Keys per work item: the largest chunk (a power of two, 64 .. 2048 keys) that
 // still gives every SM several blocks of four warps; short chunks cost a join,
 // long ones leave SMs idle.
-int kv4_chunk(int n_req, const int32_t *n_input, const int32_t *ctx, int n_heads, int num_sms) {
+bool is_prompt(const Kv4Batch &b, int i) {
+    return b.dtype == 1 && (b.head_dim == 64 || b.head_dim == 128) && b.n_input[i] >= kPromptRows;
+}
+
+int kv4_chunk(const Kv4Batch &b, int num_sms) {
     int chunk = 2048;
     while (chunk > 64) {
         int64_t items = 0;
-        for (int i = 0; i < n_req && items * n_heads < 6LL * num_sms; ++i)
-            items += (int64_t)n_input[i] * ((ctx[i] + (int64_t)n_input[i] + chunk - 1) / chunk);
-        if (items * n_heads >= 6LL * num_sms) break;
+        for (int i = 0; i < b.n_req && items * b.n_heads < 6LL * num_sms; ++i)
+            if (!is_prompt(b, i))
+                items += (int64_t)b.n_input[i] * ((b.ctx_len[i] + (int64_t)b.n_input[i] + chunk - 1) / chunk);
+        if (items * b.n_heads >= 6LL * num_sms) break;
         chunk /= 2;
     }
     return chunk;
@@ -649,12 +782,19 @@ bool kv4_sizes(const Kv4Batch &b, int num_sms, Kv4Sizes *z) {
         rows += n;
         if (rows > INT32_MAX / 8) return false;
     }
-    z->chunk = kv4_chunk(b.n_req, b.n_input, b.ctx_len, b.n_heads, num_sms);
+    z->chunk = kv4_chunk(b, num_sms);
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i];
         z->rows += n;
         z->keys += c + n;
         z->tiles += (c + n + kReadTile - 1) / kReadTile;
+        if (is_prompt(b, i)) {
+            z->pre++;
+            z->pre_tiles += (n + kPrefillRowsPerTile - 1) / kPrefillRowsPerTile;
+            z->pre_read += (c + n + kReadTile - 1) / kReadTile;
+            z->pre_keys += c + n;
+            continue;
+        }
         for (int64_t j = 0; j < n; ++j) {
             const int64_t nch = (c + j + 1 + z->chunk - 1) / z->chunk;
             z->items += nch;
@@ -666,9 +806,16 @@ bool kv4_sizes(const Kv4Batch &b, int num_sms, Kv4Sizes *z) {
     z->off_items = w, w = up4(w + 8 * z->items);
     z->off_count = w, w = up4(w + z->splits * b.n_heads);
     z->off_tiles = w, w = up4(w + 4 * z->tiles);
+    z->off_pre = w, w = up4(w + 4 * z->pre);
+    z->off_pretiles = w, w = up4(w + 2 * z->pre_tiles);
+    z->off_preread = w, w = up4(w + 4 * z->pre_read);
+    z->off_reqoff = w, w = up4(w + b.n_req + 1);
+    z->off_reqctx = w, w = up4(w + b.n_req);
+    z->off_reqws = w, w = up4(w + b.n_req);
     z->total = w;
     // 32-bit table entries and grid sizes
-    return w <= INT32_MAX && z->keys <= INT32_MAX && z->rows <= INT32_MAX / 4;
+    return w <= INT32_MAX && z->keys <= INT32_MAX && z->pre_tiles * b.n_heads <= INT32_MAX &&
+           (z->pre + z->rows) * b.n_heads <= INT32_MAX;
 }
 
 }  // namespace
@@ -690,11 +837,18 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     if (!kv4_sizes(b, num_sms, &z) || cap < z.total) return false;
     std::memset(buf, 0, sizeof(int32_t) * (size_t)z.total);  // (the device copy's counters start at zero)
     int32_t *slot = buf + z.off_rowslot, *it = buf + z.off_items, *tl = buf + z.off_tiles;
-    int64_t row = 0, split = 0, part = 0, key = 0;
+    int32_t *pre = buf + z.off_pre, *pt = buf + z.off_pretiles, *pd = buf + z.off_preread;
+    int32_t *req_off = buf + z.off_reqoff, *req_ctx = buf + z.off_reqctx, *req_ws = buf + z.off_reqws;
+    int64_t row = 0, split = 0, part = 0, key = 0, ws = 0;
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i], o = b.kv_offset[i];
+        const bool prompt = is_prompt(b, i);
+        req_off[i] = (int32_t)row;
+        req_ctx[i] = (int32_t)c;
+        req_ws[i] = (int32_t)ws;
         for (int64_t j = 0; j < n; ++j, ++row) {
             slot[row] = (int32_t)(o + c + j);
+            if (prompt) continue;
             const int64_t keys = c + j + 1, nch = (keys + z.chunk - 1) / z.chunk;
             for (int64_t k = 0; k < nch; ++k, it += 8) {
                 it[0] = (int32_t)(o + k * z.chunk);
@@ -711,9 +865,23 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
             tl[0] = (int32_t)(o + t);
             tl[1] = (int32_t)std::min<int64_t>(kReadTile, c + n - t);
             tl[2] = (int32_t)(key + t);
+            if (prompt) {
+                std::memcpy(pd, tl, 4 * sizeof(int32_t));
+                pd[2] = (int32_t)(ws + t);
+                pd[3] = i;
+                pd += 4;
+            }
         }
         key += c + n;
+        if (prompt) {
+            pre[0] = i, pre[1] = (int32_t)o, pre[2] = (int32_t)(c + n);
+            pre += 4;
+            for (int64_t q = 0; q < n; q += kPrefillRowsPerTile, pt += 2) pt[0] = i, pt[1] = (int32_t)q;
+            ws += c + n;
+        }
     }
+    req_off[b.n_req] = (int32_t)row;
+    prefill_order(buf + z.off_pretiles, (int)z.pre_tiles, req_off, req_ctx);
     // slots written by two rows
     std::vector<std::pair<int64_t, int64_t>> w((size_t)b.n_req);
     for (int i = 0; i < b.n_req; ++i)
@@ -738,15 +906,49 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     buf[Q_O_ITEMS] = (int32_t)z.off_items;
     buf[Q_O_COUNT] = (int32_t)z.off_count;
     buf[Q_O_TILES] = (int32_t)z.off_tiles;
+    buf[Q_PRE] = (int32_t)z.pre;
+    buf[Q_PRETILES] = (int32_t)z.pre_tiles;
+    buf[Q_PREREAD] = (int32_t)z.pre_read;
+    buf[Q_PREKEYS] = (int32_t)z.pre_keys;
+    buf[Q_REQS] = b.n_req;
+    buf[Q_O_PRE] = (int32_t)z.off_pre;
+    buf[Q_O_PRETILES] = (int32_t)z.off_pretiles;
+    buf[Q_O_PREREAD] = (int32_t)z.off_preread;
+    buf[Q_O_REQOFF] = (int32_t)z.off_reqoff;
+    buf[Q_O_REQCTX] = (int32_t)z.off_reqctx;
+    buf[Q_O_REQWS] = (int32_t)z.off_reqws;
     return true;
 }
 
 bool kv4_plan_ok(const int32_t *hp) { return hp && hp[Q_MAGIC] == kKv4Magic; }
 bool kv4_plan_writes_once(const int32_t *hp) { return !hp[Q_TWICE]; }
 
-int64_t kv4_workspace_bytes(const int32_t *hp) {
-    return (int64_t)hp[Q_PARTS] * hp[Q_HEADS] * (hp[Q_DIM] + 2) * 4;
+namespace {
+// byte offsets in the workspace
+struct Kv4Work {
+    int64_t q16, pool16, q_scale, kv_scale, total;
+};
+Kv4Work kv4_work(const int32_t *hp) {
+    const int64_t nh = hp[Q_HEADS], d = hp[Q_DIM];
+    Kv4Work w;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t o = at;
+        at += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    take((int64_t)hp[Q_PARTS] * nh * (d + 2) * 4);
+    const bool pre = hp[Q_PRE] > 0;
+    w.q16 = take(pre ? (int64_t)hp[Q_ROWS] * nh * d * 2 : 0);
+    w.pool16 = take(2 * nh * hp[Q_PREKEYS] * d * 2);
+    w.q_scale = take(pre ? (int64_t)hp[Q_ROWS] * nh * 4 : 0);
+    w.kv_scale = take(pre ? (int64_t)hp[Q_REQS] * nh * 2 * 4 : 0);
+    w.total = at;
+    return w;
 }
+}  // namespace
+
+int64_t kv4_workspace_bytes(const int32_t *hp) { return kv4_work(hp).total; }
 
 cudaError_t kv4_append(const void *qkv, void *layer, const int32_t *hp, const int32_t *dp, cudaStream_t st) {
     const int nh = hp[Q_HEADS], d = hp[Q_DIM], H = nh * d, G = kv4_groups(d), gt = d / G / 8;
@@ -765,13 +967,13 @@ cudaError_t kv4_read(const void *layer, const int32_t *hp, const int32_t *dp, vo
     const dim3 grid(hp[Q_TILES], nh);
     if (hp[Q_DTYPE] == 1)
         return launch_pdl(kv4_read_kernel<bf16>, grid, dim3(kRdThreads), 0, st, v, dp + hp[Q_O_TILES], (bf16 *)out,
-                          (int64_t)hp[Q_KEYS], nh, d, G);
+                          (int64_t)hp[Q_KEYS], nh, d, G, (const float *)nullptr);
     return launch_pdl(kv4_read_kernel<float>, grid, dim3(kRdThreads), 0, st, v, dp + hp[Q_O_TILES], (float *)out,
-                      (int64_t)hp[Q_KEYS], nh, d, G);
+                      (int64_t)hp[Q_KEYS], nh, d, G, (const float *)nullptr);
 }
 
 cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp, int32_t *dp, void *workspace,
-                          void *out, cudaStream_t st) {
+                          void *out, unsigned *err, int *launches, cudaStream_t st) {
     const int nh = hp[Q_HEADS], d = hp[Q_DIM];
     Kv4Attn a;
     a.qkv = qkv;
@@ -783,7 +985,43 @@ cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp,
     a.items = dp + hp[Q_O_ITEMS];
     a.counters = dp + hp[Q_O_COUNT];
     a.part = (float *)workspace;
-    return hp[Q_DTYPE] == 1 ? launch_decode<bf16>(a, d, hp[Q_ITEMS], st) : launch_decode<float>(a, d, hp[Q_ITEMS], st);
+    cudaError_t e = cudaSuccess;
+    *launches = 0;
+    if (hp[Q_ITEMS] > 0) {
+        e = hp[Q_DTYPE] == 1 ? launch_decode<bf16>(a, d, hp[Q_ITEMS], st) : launch_decode<float>(a, d, hp[Q_ITEMS], st);
+        ++*launches;
+    }
+    if (e != cudaSuccess || hp[Q_PRE] == 0) return e;
+    const Kv4Work w = kv4_work(hp);
+    uint8_t *ws = (uint8_t *)workspace;
+    Kv4Prep pr;
+    pr.qkv = (const bf16 *)qkv;
+    pr.q16 = (__half *)(ws + w.q16);
+    pr.q_scale = (float *)(ws + w.q_scale);
+    pr.kv_scale = (float *)(ws + w.kv_scale);
+    pr.v = a.v;
+    pr.H = a.H, pr.n_heads = nh, pr.d = d, pr.G = kv4_groups(d);
+    pr.n_rows = hp[Q_ROWS], pr.n_pre = hp[Q_PRE];
+    pr.pre = dp + hp[Q_O_PRE];
+    constexpr int kWarps = kPrepThreads / 32;
+    const int64_t blocks = (int64_t)pr.n_pre * nh + ((int64_t)pr.n_rows * nh + kWarps - 1) / kWarps;
+    e = launch_pdl(kv4_prep_kernel, dim3((unsigned)blocks), dim3(kPrepThreads), 0, st, pr);
+    if (e == cudaSuccess)
+        e = launch_pdl(kv4_read_kernel<__half>, dim3(hp[Q_PREREAD], nh), dim3(kRdThreads), 0, st, a.v,
+                       dp + hp[Q_O_PREREAD], (__half *)(ws + w.pool16), (int64_t)hp[Q_PREKEYS], nh, d, pr.G,
+                       (const float *)pr.kv_scale);
+    AttnPlan ap{};
+    ap.req_off = dp + hp[Q_O_REQOFF];
+    ap.req_ctx = dp + hp[Q_O_REQCTX];
+    ap.req_kvoff = dp + hp[Q_O_REQWS];
+    ap.pre_tiles = dp + hp[Q_O_PRETILES];
+    ap.n_pre_tiles = hp[Q_PRETILES];
+    ap.n_rows = hp[Q_ROWS];
+    if (e == cudaSuccess)
+        e = attention_prefill_f16(pr.q16, hp[Q_ROWS], ws + w.pool16, hp[Q_PREKEYS], (bf16 *)out, ap, a.H, nh, pr.q_scale,
+                                  pr.kv_scale, err, st);
+    *launches += 3;
+    return e;
 }
 
 }  // namespace orca

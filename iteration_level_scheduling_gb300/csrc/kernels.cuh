@@ -137,6 +137,12 @@ cudaError_t attention(const T *qkv, const T *pool_layer, int64_t kv_slots, T *ou
                       int n_heads, float *part, int *counters, unsigned *err, cudaStream_t st, bool decode,
                       bool prefill);
 
+// The tcgen05 prefill (head_dim 64 or 128) on fp16 operands: q16 [n_rows, H], pool16 [K|V][head][slots][head_dim],
+// scaled by powers of two whose inverses are q_scale [row][head] and kv_scale [request][head][K|V].
+cudaError_t attention_prefill_f16(const void *q16, int n_rows, const void *pool16, int64_t slots, bf16 *out,
+                                  const AttnPlan &p, int H, int n_heads, const float *q_scale, const float *kv_scale,
+                                  unsigned *err, cudaStream_t st);
+
 // Order of the decode work items (request, chunk) by number of keys, longest
 // first (stable), for the persistent decode kernel's load balance.
 // req_keys[i]: the keys request i's items cover (AttnPlan::req_keys).
@@ -180,7 +186,7 @@ int64_t kv4_workspace_bytes(const int32_t *hp);
 cudaError_t kv4_append(const void *qkv, void *layer, const int32_t *hp, const int32_t *dp, cudaStream_t st);
 cudaError_t kv4_read(const void *layer, const int32_t *hp, const int32_t *dp, void *out, cudaStream_t st);
 cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp, int32_t *dp, void *workspace,
-                          void *out, cudaStream_t st);
+                          void *out, unsigned *err, int *launches, cudaStream_t st);
 
 constexpr int kPrefillRowsPerTile = 128;  // query rows per prefill tile (the tcgen05 kernel's M)
 

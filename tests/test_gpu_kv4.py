@@ -9,8 +9,9 @@ more for the group sums: (D + 16) is used), a weight is off by a factor within
 the last rounding is eps / 2: so
   |out - ref| <= eps / 2 |ref| + (4 B + 2^-19 + T 2^-24) max |v|.
 The tensor-core path splits a weight times a scale into two bf16 (2^-16 left),
-and prompts run on K and V rounded to bf16 with weights rounded to bf16: 2^-8
-on each of the value and the weight and 2^-8 sum |q k| log2(e) / sqrt(D) on a
+and prompts run on K and V rounded to fp16 with weights rounded to fp16: 2^-11
+on each of the value and the weight (and 2^-25 of the largest for those that
+fall below fp16's normal range) and 2^-11 sum |q k| log2(e) / sqrt(D) on a
 score, whose natural exponential moves by ln 2 times that."""
 
 import math
@@ -109,7 +110,7 @@ class Case:
             size = np.einsum("nhd,hkd->nhk", np.abs(q), np.abs(k)).max() * math.log2(math.e) / math.sqrt(self.d)
             tol = 4 * (self.d + 16) * 2.0 ** -24 * size + 2.0 ** -15 + (c + n) * 2.0 ** -24
             if rounded_operands:
-                tol += 2 * 2.0 ** -8 + 2 * 2.0 ** -8 * size * math.log(2)
+                tol += 2 * 2.0 ** -11 + (c + n) * 2.0 ** -25 + 2 * 2.0 ** -11 * size * math.log(2)
             lim = eps * np.abs(ref) + tol * np.abs(v).max()
             d = np.abs(got[r:r + n] - ref)
             assert np.isfinite(got[r:r + n]).all() and (d <= lim).all(), (n, c, float((d / lim).max()))
@@ -225,12 +226,30 @@ def test_few_rows(native, eng, dtype, d):
     s.check(s.attention())
 
 
+@pytest.mark.parametrize("std", [1.0, 1e-5, 3e4])
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 32), ("bf16", 16), ("fp32", 64)])
-def test_prompts(native, eng, dtype, d):
-    s = Case(native, eng, 8, dtype, 3, d, [(130, 0), (64, 0), (127, 200), (257, 65), (1, 300), (4, 30), (33, 1)])
+def test_prompts(native, eng, dtype, d, std):
+    s = Case(native, eng, 8, dtype, 3, d, [(130, 0), (64, 0), (127, 200), (257, 65), (1, 300), (4, 30), (33, 1)],
+             std=std)
+    s.qkv[:, 0] = rounded(s.qkv[:, 0] * min(1.0, 1 / std), dtype).float().numpy()
+    s.upload()
     s.append()
     s.append_oracle()
     s.check(s.attention(), rounded_operands=dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype,d,n", [("bf16", 128, 200), ("bf16", 64, 200), ("bf16", 32, 70), ("fp32", 64, 70),
+                                       ("bf16", 128, 9)])
+def test_nan_reaches_the_rows_that_see_it_and_no_other(native, eng, dtype, d, n):
+    s = Case(native, eng, 20, dtype, 2, d, [(n, 20)])
+    a, b = n // 3, n // 2
+    s.qkv[a, 2, 0, 3] = np.nan   # a value of head 0 from row a on
+    s.qkv[b, 1, 1, 5] = np.inf   # a key of head 1 from row b on
+    s.upload()
+    s.append()
+    out = s.attention().float().reshape(n, 2, d)
+    assert out[:a, 0].isfinite().all() and out[:b, 1].isfinite().all()
+    assert out[a:, 0, :min(32, d)].isnan().all() and out[b:, 1].isnan().all()
 
 
 def test_rows_do_not_depend_on_their_company(native, eng):
