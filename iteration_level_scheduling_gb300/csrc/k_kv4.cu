@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cstring>
+#include <cstdlib>
 #include <type_traits>
 #include <vector>
 
@@ -88,59 +89,115 @@ __device__ __forceinline__ uint32_t kv4_code(float x, float m, float s) {
     return (uint32_t)fminf(fmaxf(c, 0.f), 15.f);
 }
 
+// Eight components' codes, component i in bits 4 i ..  The candidate from a
+// product with 1 / s is right if what it leaves is less than half a step (the
+// residual is exact, as above).  The others -- halves, which bf16 data meet
+// about once in 256 -- are done the long way, one after the other.
+__device__ __forceinline__ uint32_t kv4_codes(const float *x, float m, float s, float inv) {
+    constexpr float kRound = 12582912.f;  // 1.5 2^23: the integer in the low bits
+    const float h = 0.5f * s;
+    uint32_t w = 0, open = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float a = __fsub_rn(x[i], m);
+        const float cr = fminf(fmaxf(__fmul_rn(a, inv), 0.f), 15.f) + kRound;
+        const float r = __fmaf_rn(-(cr - kRound), s, a);
+        if (!(fabsf(r) < h)) open |= 1u << i;
+        w |= (__float_as_uint(cr) & 15u) << (4 * i);
+    }
+    if (!(s > 0.f)) return 0u;
+    while (open) {
+        const int i = __ffs(open) - 1;
+        open &= open - 1;
+        float xi = x[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) xi = i == e ? x[e] : xi;  // (x stays in registers)
+        w = (w & ~(15u << (4 * i))) | kv4_code(xi, m, s) << (4 * i);
+    }
+    return w;
+}
+
+// Scale and minimum (packed, bf16) and the codes of a group's share of 8 components, GT neighbouring threads each
+// holding 8; every thread of the warp takes part.
+template <int GT>
+__device__ __forceinline__ uint32_t kv4_quantise(const float *x, uint32_t *par) {
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) lo = min_nan(lo, x[i]), hi = max_nan(hi, x[i]);
+#pragma unroll
+    for (int o = 1; o < GT; o <<= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    uint32_t sb = bf_bits(__fdiv_rn(__fsub_rn(hi, lo), 15.f)), mb = bf_bits(lo);
+    if ((sb & 0x7f80u) == 0x7f80u || (mb & 0x7f80u) == 0x7f80u) sb = mb = 0x7fc0u;
+    *par = sb | (mb << 16);
+    const float s = bf_lo(sb);
+    float inv;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    return kv4_codes(x, bf_lo(mb), s, inv);
+}
+
 // ---------------------------------------------------------------------------
-// write: k and v of every row, one thread per 8 components
+// write: one thread per 8 components of k and of v, of one row or of two whose
+// slots share a pair (then V goes out in whole words)
 // ---------------------------------------------------------------------------
 constexpr int kApThreads = 128;
 
 template <typename T>
-__global__ void __launch_bounds__(kApThreads) kv4_append_kernel(const T *qkv, const int32_t *row_slot, Kv4View v, int H,
-                                                                int d, int G, int gt) {
+__device__ __forceinline__ void load8_stream(const T *p, float *x) {
+#pragma unroll
+    for (int i = 0; i < 8; i += Elem<T>::kPer16) load16_stream(p + i, x + i);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kApThreads) kv4_append_kernel(const T *qkv, const int32_t *units, Kv4View v, int H) {
+    constexpr int G = D >= 32 ? D / 32 : 1, GT = D / G / 8;
     pdl_trigger();
     pdl_wait();
-    const int r = blockIdx.x;
-    const int64_t slot = row_slot[r];
-    const int u = blockIdx.y * kApThreads + threadIdx.x;  // 8-component unit of k, then v
-    const bool on = u * 8 < 2 * H;
-    float x[8];
+    const int4 un = reinterpret_cast<const int4 *>(units)[blockIdx.x];  // first row, its slot, rows (1, or 2 in one pair)
+    const int64_t slot = un.y;
+    const bool two = un.z == 2;
+    const int c = (blockIdx.y * kApThreads + threadIdx.x) * 8;  // component of the row; whole warps pass the end together
+    const bool on = c < H;                                      // or by groups
+    float x[4][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    for (int i = 0; i < 4; ++i) {  // k, v of the first row; of the second
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+        if (on && (i < 2 || two)) load8_stream(qkv + ((size_t)un.x + (i >> 1)) * 3 * H + (1 + (i & 1)) * (size_t)H + c, x[i]);
+    }
+    const int h = c / D, dd = c % D;
+    const int64_t row = (int64_t)h * v.S + slot, pair = row >> 1;  // (S is even)
+    const bool lead = dd % (8 * GT) == 0;
+    const int g = dd / (8 * GT);
+    uint32_t par[2], w[2];
+    w[0] = kv4_quantise<GT>(x[0], &par[0]);
     if (on) {
-        const T *src = qkv + (size_t)r * 3 * H + H + (size_t)u * 8;
-#pragma unroll
-        for (int i = 0; i < 8; i += Elem<T>::kPer16) load16_stream(src + i, x + i);
+        *reinterpret_cast<uint32_t *>(v.kc + row * (D / 2) + dd / 2) = w[0];
+        if (lead) v.kp[row * G + g] = par[0];
     }
-    float lo = x[0], hi = x[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) lo = min_nan(lo, x[i]), hi = max_nan(hi, x[i]);
-    // the group's 2 or 4 threads (gt) are neighbours; units of k and v and of heads never share a group
-    for (int o = 1; o < gt; o <<= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    if (!on) return;
-    uint32_t sb = bf_bits(__fdiv_rn(__fsub_rn(hi, lo), 15.f)), mb = bf_bits(lo);
-    const bool fine = (sb & 0x7f80u) != 0x7f80u && (mb & 0x7f80u) != 0x7f80u;
-    if (!fine) sb = mb = 0x7fc0u;
-    const float s = bf_lo(sb), m = bf_lo(mb);
-    uint32_t w = 0;
-    if (fine && s > 0.f) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w |= kv4_code(x[i], m, s) << (4 * i);
-    }
-    const int c = u * 8, which = c >= H, cc = c - which * H, h = cc / d, dd = cc - h * d;
-    const uint32_t par = sb | (mb << 16);
-    const bool lead = (u % gt) == 0;
-    const int g = dd / (8 * gt);
-    if (!which) {
-        *reinterpret_cast<uint32_t *>(v.kc + ((int64_t)h * v.S + slot) * (d / 2) + dd / 2) = w;
-        if (lead) v.kp[((int64_t)h * v.S + slot) * G + g] = par;
+    if (two) {
+        w[0] = kv4_quantise<GT>(x[2], &par[0]);
+        if (on) {
+            *reinterpret_cast<uint32_t *>(v.kc + (row + 1) * (D / 2) + dd / 2) = w[0];
+            if (lead) v.kp[(row + 1) * G + g] = par[0];
+        }
+        w[0] = kv4_quantise<GT>(x[1], &par[0]);
+        w[1] = kv4_quantise<GT>(x[3], &par[1]);
+        if (on) {
+            *reinterpret_cast<uint2 *>(v.vc + pair * D + dd) =
+                make_uint2((w[0] & 0xffffu) | (w[1] << 16), (w[0] >> 16) | (w[1] & 0xffff0000u));
+            if (lead) *reinterpret_cast<uint2 *>(v.vp + (pair * G + g) * 2) = make_uint2(par[0], par[1]);
+        }
     } else {
-        const int64_t pair = (int64_t)h * (v.S / 2) + (slot >> 1);
-        uint16_t *dst = reinterpret_cast<uint16_t *>(v.vc + (pair * (d / 4) + dd / 4) * 4) + (slot & 1);
-        dst[0] = (uint16_t)w;
-        dst[2] = (uint16_t)(w >> 16);
-        if (lead) v.vp[(pair * G + g) * 2 + (slot & 1)] = par;
+        w[0] = kv4_quantise<GT>(x[1], &par[0]);
+        if (on) {
+            uint16_t *dst = reinterpret_cast<uint16_t *>(v.vc + pair * D + dd) + (slot & 1);
+            dst[0] = (uint16_t)w[0];
+            dst[2] = (uint16_t)(w[0] >> 16);
+            if (lead) v.vp[(pair * G + g) * 2 + (slot & 1)] = par[0];
+        }
     }
 }
 
@@ -148,13 +205,20 @@ __global__ void __launch_bounds__(kApThreads) kv4_append_kernel(const T *qkv, co
 // read back: tiles of up to 64 slots of one range, one head's K and V per CTA
 // ---------------------------------------------------------------------------
 constexpr int kRdThreads = 128;
+constexpr int kReadTile = 64;  // slots per tile
+
+// nibbles N and N + 4 of w as floats, through bf16's 128 + c (conversions run at an eighth of the rate)
+template <int N>
+__device__ __forceinline__ void code_floats(uint32_t w, float &a, float &b) {
+    const uint32_t u = ((w >> (4 * N)) & 0x000f000fu) | 0x43004300u;
+    a = bf_lo(u) - 128.f, b = bf_hi(u) - 128.f;
+}
 
 template <typename T>
 __device__ __forceinline__ void store8(T *p, const float *x) {
 #pragma unroll
     for (int i = 0; i < 8; i += Elem<T>::kPer16) store16(p + i, x + i);
 }
-
 __device__ __forceinline__ void store8(__half *p, const float *x) {
     uint4 u;
     __half2 *h = reinterpret_cast<__half2 *>(&u);
@@ -163,61 +227,95 @@ __device__ __forceinline__ void store8(__half *p, const float *x) {
     *reinterpret_cast<uint4 *>(p) = u;
 }
 
-// scale: the inverses of the powers of two that the values are to be multiplied by ([request][head][K|V]), or null
-template <typename T>
+// Scaled (prompts, below): scale holds the inverses of the powers of two that the values are to be multiplied by,
+// [request][head][K|V].  Every load of a thread is issued before the first is used.
+template <typename T, int D, bool Scaled>
 __global__ void __launch_bounds__(kRdThreads) kv4_read_kernel(Kv4View v, const int32_t *tiles, T *out, int64_t out_slots,
-                                                              int n_heads, int d, int G, const float *scale) {
+                                                              int n_heads, const float *scale) {
+    constexpr int G = D >= 32 ? D / 32 : 1, GS = D / G, U = D / 8;  // 8-component units per row
+    constexpr int KN = kReadTile * U / kRdThreads, VN = (KN + 1) / 2;  // units of K per thread, pairs of V
     pdl_trigger();
     pdl_wait();
     const int4 tl = reinterpret_cast<const int4 *>(tiles)[blockIdx.x];  // first slot, slots, first output index, request
-    const int h = blockIdx.y, gs = d / G, upr = d / 8;                  // 8-component units per row
+    const int h = blockIdx.y;
     const int64_t s0 = tl.x, s1 = s0 + tl.y;
     float kf = 1.f, vf = 1.f;
-    if (scale) {
+    if constexpr (Scaled) {
         const float *f = scale + 2 * ((size_t)tl.w * n_heads + h);
         kf = 1.f / f[0], vf = 1.f / f[1];
     }
-    T *ko = out + ((int64_t)h * out_slots + tl.z) * d, *vo = ko + (int64_t)n_heads * out_slots * d;
-    for (int i = threadIdx.x; i < tl.y * upr; i += kRdThreads) {
-        const int j = i / upr, u = i - j * upr;
-        const int64_t row = (int64_t)h * v.S + s0 + j;
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(v.kc + row * (d / 2) + u * 4);
-        const uint32_t p = v.kp[row * G + u * 8 / gs];
-        float s = bf_lo(p) * kf, m = bf_hi(p) * kf;
-        if (scale) {
+    T *ko = out + ((int64_t)h * out_slots + tl.z) * D, *vo = ko + (int64_t)n_heads * out_slots * D;
+    const int u = threadIdx.x % U, gr = u * 8 / GS;
+    uint32_t kw[KN], kp[KN], pv[KN];
+#pragma unroll
+    for (int n = 0; n < KN; ++n) {
+        const int j = (threadIdx.x + n * kRdThreads) / U;
+        if (j < tl.y) {
+            const int64_t row = (int64_t)h * v.S + s0 + j;
+            kw[n] = __ldcs(reinterpret_cast<const uint32_t *>(v.kc + row * (D / 2)) + u);
+            kp[n] = v.kp[row * G + gr];
+            if constexpr (Scaled) pv[n] = v.vp[((row >> 1) * G + gr) * 2 + ((s0 + j) & 1)];
+        }
+    }
+    const int64_t p0 = s0 >> 1;
+    const int np = (int)(((s1 + 1) >> 1) - p0);  // up to 33 pairs: the 33rd is left to a second round
+    uint2 vw[VN], vp[VN];
+    auto load_v = [&](int n, int j) {
+        if (j < np) {
+            const int64_t pair = (int64_t)h * (v.S / 2) + p0 + j;
+            vw[n] = __ldcs(reinterpret_cast<const uint2 *>(v.vc + pair * D) + u);
+            vp[n] = *reinterpret_cast<const uint2 *>(v.vp + (pair * G + gr) * 2);
+        }
+    };
+#pragma unroll
+    for (int n = 0; n < VN; ++n) load_v(n, (threadIdx.x + n * kRdThreads) / U);
+#pragma unroll
+    for (int n = 0; n < KN; ++n) {
+        const int j = (threadIdx.x + n * kRdThreads) / U;
+        if (j >= tl.y) continue;
+        float s = bf_lo(kp[n]) * kf, m = bf_hi(kp[n]) * kf;
+        if constexpr (Scaled) {
             // a NaN among the values is moved to the key: a weight of 0 times it would reach rows that do not see
             // the key, while a masked score is dropped whatever it is
-            const int64_t slot = s0 + j;
-            const uint32_t pv = v.vp[(((int64_t)h * (v.S / 2) + (slot >> 1)) * G + u * 8 / gs) * 2 + (slot & 1)];
-            if (bf_lo(pv) != bf_lo(pv)) m = bf_lo(pv);
+            const float sv = bf_lo(pv[n]);
+            if (sv != sv) m = sv;
         }
         float x[8];
+        code_floats<0>(kw[n], x[0], x[4]);
+        code_floats<1>(kw[n], x[1], x[5]);
+        code_floats<2>(kw[n], x[2], x[6]);
+        code_floats<3>(kw[n], x[3], x[7]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = fmaf(s, (float)((w >> (4 * k)) & 15u), m);
-        store8(ko + (int64_t)j * d + u * 8, x);
+        for (int k = 0; k < 8; ++k) x[k] = fmaf(s, x[k], m);
+        store8(ko + (int64_t)j * D + u * 8, x);
     }
-    const int64_t p0 = s0 >> 1, np = ((s1 + 1) >> 1) - p0;
-    for (int i = threadIdx.x; i < (int)np * upr; i += kRdThreads) {
-        const int j = i / upr, u = i - j * upr;
-        const int64_t pair = (int64_t)h * (v.S / 2) + p0 + j;
-        const uint2 w = *reinterpret_cast<const uint2 *>(v.vc + (pair * (d / 4) + u * 2) * 4);
-        const uint2 p = *reinterpret_cast<const uint2 *>(v.vp + (pair * G + u * 8 / gs) * 2);
+    auto store_v = [&](int n, int j) {
+        if (j >= np) return;
+        float xe[8], xo[8];  // even and odd slot
+        code_floats<0>(vw[n].x, xe[0], xo[0]);
+        code_floats<1>(vw[n].x, xe[1], xo[1]);
+        code_floats<2>(vw[n].x, xe[2], xo[2]);
+        code_floats<3>(vw[n].x, xe[3], xo[3]);
+        code_floats<0>(vw[n].y, xe[4], xo[4]);
+        code_floats<1>(vw[n].y, xe[5], xo[5]);
+        code_floats<2>(vw[n].y, xe[6], xo[6]);
+        code_floats<3>(vw[n].y, xe[7], xo[7]);
+        const int64_t slot = 2 * (p0 + j);
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
-            const int64_t slot = 2 * (p0 + j) + o;
-            if (slot < s0 || slot >= s1) continue;
-            const uint32_t a = w.x >> (16 * o), b = w.y >> (16 * o), pp = o ? p.y : p.x;
+            if (slot + o < s0 || slot + o >= s1) continue;
+            const uint32_t pp = o ? vp[n].y : vp[n].x;
             float s = bf_lo(pp) * vf, m = bf_hi(pp) * vf;
-            if (scale && s != s) s = m = 0.f;
+            if (Scaled && s != s) s = m = 0.f;
             float x[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                x[k] = fmaf(s, (float)((a >> (4 * k)) & 15u), m);
-                x[4 + k] = fmaf(s, (float)((b >> (4 * k)) & 15u), m);
-            }
-            store8(vo + (slot - s0) * d + u * 8, x);
+            for (int k = 0; k < 8; ++k) x[k] = fmaf(s, o ? xo[k] : xe[k], m);
+            store8(vo + (slot + o - s0) * D + u * 8, x);
         }
-    }
+    };
+#pragma unroll
+    for (int n = 0; n < VN; ++n) store_v(n, (threadIdx.x + n * kRdThreads) / U);
+    for (int j = (threadIdx.x + VN * kRdThreads) / U; j < np; j += kRdThreads / U) load_v(0, j), store_v(0, j);
 }
 
 // ---------------------------------------------------------------------------
@@ -241,13 +339,13 @@ struct Kv4Prep {
     __half *q16;
     float *q_scale, *kv_scale;
     Kv4View v;
-    int H, n_heads, d, G, n_rows, n_pre;
+    int H, n_heads, d, G, n_rows, n_pre;  // G is 2 or 4
     const int32_t *pre;  // 4 words per prompt: request, first slot, slots, 0
 };
-constexpr int kPrepThreads = 256;
+constexpr int kPrepThreads = 256, kPrepQ = 4;
 
 // Blocks 0 .. n_pre * n_heads - 1: the scales of K and V of one prompt and head, from the parameters (a component lies
-// between m and m + 15 s).  The others: a warp scales and rounds q of one row and head.
+// between m and m + 15 s).  The others scale and round q.
 __global__ void __launch_bounds__(kPrepThreads) kv4_prep_kernel(const Kv4Prep a) {
     __shared__ float red[2][kPrepThreads / 32];
     pdl_trigger();
@@ -261,19 +359,37 @@ __global__ void __launch_bounds__(kPrepThreads) kv4_prep_kernel(const Kv4Prep a)
         float km = 0.f, vm = 0.f;
         // (fmaxf drops NaN: a group that reads back as NaN does so whatever the scale)
         auto size = [](uint32_t p) { return fmaxf(fabsf(bf_hi(p)), fabsf(fmaf(15.f, bf_lo(p), bf_hi(p)))); };
-        const uint32_t *kp = a.v.kp + ((int64_t)h * a.v.S + s0) * a.G;
-        const int64_t nk = (s1 - s0) * a.G;
-#pragma unroll 4
-        for (int64_t j = threadIdx.x; j < nk; j += kPrepThreads) km = fmaxf(km, size(kp[j]));
-        const int64_t p0 = s0 >> 1, np = ((s1 + 1) >> 1) - p0;
-        const uint2 *vp = reinterpret_cast<const uint2 *>(a.v.vp) + ((int64_t)h * (a.v.S / 2) + p0) * a.G;
-#pragma unroll 4
-        for (int64_t j = threadIdx.x; j < np * a.G; j += kPrepThreads) {
-            const uint2 p = vp[j];
-            const int64_t slot = 2 * (p0 + j / a.G);
-            if (slot >= s0) vm = fmaxf(vm, size(p.x));
-            if (slot + 1 < s1) vm = fmaxf(vm, size(p.y));
-        }
+        const uint32_t *kp = a.v.kp + (int64_t)h * a.v.S * a.G, *vp = a.v.vp + (int64_t)h * a.v.S * a.G;
+        // words of K: s0 G .. s1 G; of V, whose pairs hold group by group the even and the odd slot, those of the
+        // pairs, less the even slot of the first or the odd one of the last.  16 bytes at a time: the 16 slots' words
+        // of a head are whole vectors, what lies outside is dropped.
+        const int64_t k0 = s0 * a.G, k1 = s1 * a.G, v0 = (s0 >> 1) * 2 * a.G, v1 = ((s1 + 1) >> 1) * 2 * a.G;
+        auto take = [&](const uint32_t *base, int64_t lo, int64_t hi, auto in) {
+            float mx = 0.f;
+            for (int64_t j = (lo & ~int64_t(3)) + 4 * threadIdx.x; j < hi; j += 4 * 8 * kPrepThreads) {
+                uint4 p[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    p[e] = j + 4 * e * kPrepThreads < hi
+                               ? *reinterpret_cast<const uint4 *>(base + j + 4 * e * kPrepThreads)
+                               : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t w[4] = {p[e].x, p[e].y, p[e].z, p[e].w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int64_t at = j + 4 * e * kPrepThreads + q;
+                        if (at >= lo && at < hi && in(at)) mx = fmaxf(mx, size(w[q]));
+                    }
+                }
+            }
+            return mx;
+        };
+        km = take(kp, k0, k1, [](int64_t) { return true; });
+        vm = take(vp, v0, v1, [&](int64_t at) {
+            const int64_t slot = (at >> (a.G == 4 ? 3 : 2)) * 2 + (at & 1);
+            return slot >= s0 && slot < s1;
+        });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, o));
@@ -288,25 +404,36 @@ __global__ void __launch_bounds__(kPrepThreads) kv4_prep_kernel(const Kv4Prep a)
         }
         return;
     }
-    const int64_t unit = ((int64_t)blockIdx.x - first) * (kPrepThreads / 32) + warp;  // (row, head)
-    if (unit >= (int64_t)a.n_rows * a.n_heads) return;
-    const int64_t r = unit / a.n_heads;
-    const int h = (int)(unit - r * a.n_heads);
-    const bool on = lane * 8 < a.d;  // 8 components per lane
-    float x[8];
+    // q: a thread's units of 8 components, kPrepQ of them in flight; d / 8 neighbouring threads hold a head
+    const int upr = a.H / 8, per_head = a.d / 8;
+    const int64_t units = (int64_t)a.n_rows * upr;
+    const int64_t u0 = ((int64_t)blockIdx.x - first) * (kPrepThreads * kPrepQ) + threadIdx.x;
+    float x[kPrepQ][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    if (on) load16_stream(a.qkv + r * 3 * a.H + h * a.d + lane * 8, x);
-    float m = 0.f;
+    for (int n = 0; n < kPrepQ; ++n) {
+        const int64_t u = u0 + n * kPrepThreads;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(x[e]));
+        for (int e = 0; e < 8; ++e) x[n][e] = 0.f;
+        if (u < units) {
+            const int64_t r = u / upr;
+            load16_stream(a.qkv + r * 3 * a.H + (u - r * upr) * 8, x[n]);
+        }
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float inv = kv4_inverse_scale(m), f = 1.f / inv;
+    for (int n = 0; n < kPrepQ; ++n) {
+        const int64_t u = u0 + n * kPrepThreads;
+        float m = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= f;
-    if (on) store8(a.q16 + r * a.H + h * a.d + lane * 8, x);
-    if (lane == 0) a.q_scale[r * a.n_heads + h] = inv;
+        for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(x[n][e]));
+        for (int o = per_head / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float inv = kv4_inverse_scale(m), f = 1.f / inv;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[n][e] *= f;
+        if (u < units) {
+            store8(a.q16 + u * 8, x[n]);
+            if (u % per_head == 0) a.q_scale[u / per_head] = inv;  // [row][head]
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -323,7 +450,34 @@ struct Kv4Attn {
     const int32_t *items;  // 8 words: first slot, keys, row, chunks of the row, this chunk, the row's first partial, its counter
     int *counters;         // [row counter][head], zero between launches
     float *part;           // [partial][head][D + 2]
+    const int32_t *row_items;  // the same for groups of rows (kv4_rows_mma_kernel), 12 words an item
+    const int32_t *row_joins;
+    float *row_part;  // [partial][head][16][D + 2]
 };
+
+// Join the partials of `nch` chunks, `stride` floats apart, in chunk order: component `at`, the maximum at D and the
+// sum at D + 1.  Eight chunks' loads are in flight at a time.
+template <int D>
+__device__ __forceinline__ float kv4_join(const float *part, size_t stride, int nch, int at) {
+    float Mt = kLow, Lt = 0.f, Ot = 0.f;
+    for (int c = 0; c < nch; c += 8) {
+        float pm[8], pl[8], po[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float *p = part + (size_t)min(c + j, nch - 1) * stride;
+            pm[j] = __ldcg(p + D), pl[j] = __ldcg(p + D + 1), po[j] = __ldcg(p + at);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < nch) {
+                const float mn = fmaxf(Mt, pm[j]), co = exp2f(Mt - mn), cn = exp2f(pm[j] - mn);
+                Lt = Lt * co + pl[j] * cn;
+                Ot = Ot * co + po[j] * cn;
+                Mt = mn;
+            }
+    }
+    return Ot / Lt;
+}
 
 template <int D>
 struct Kv4Merge {
@@ -367,16 +521,9 @@ __device__ __forceinline__ void kv4_finish(const Kv4Attn &a, Kv4Merge<D> &sm, co
     __syncthreads();
     if (!sm.last) return;
     __threadfence();
-    float Mt = kLow, Lt = 0.f, Ot = 0.f;
-    for (int j = 0; j < nch; ++j) {
-        const float *pj = a.part + ((size_t)(r1.y + j) * a.n_heads + h) * (D + 2);
-        const float pm = __ldcg(pj + D), pl = __ldcg(pj + D + 1), po = tid < D ? __ldcg(pj + tid) : 0.f;
-        const float mn = fmaxf(Mt, pm), co = exp2f(Mt - mn), cn = exp2f(pm - mn);
-        Lt = Lt * co + pl * cn;
-        Ot = Ot * co + po * cn;
-        Mt = mn;
-    }
-    if (tid < D) dst[tid] = Elem<T>::from_f(Ot / Lt);
+    if (tid < D)
+        dst[tid] = Elem<T>::from_f(kv4_join<D>(a.part + ((size_t)r1.y * a.n_heads + h) * (D + 2),
+                                               (size_t)a.n_heads * (D + 2), nch, tid));
 }
 
 // Any type and head_dim, fp32 arithmetic.  A warp takes 32 slots at a time:
@@ -688,6 +835,246 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv4_decode_mma_kernel(const Kv4
     kv4_finish<bf16, D>(a, sm, r0, r1, h);
 }
 
+// Up to 16 rows of one request at a time (bf16, head_dim 32 and more): the rows are the A operand's 16 rows, so
+// 16 keys are unpacked once for all of them.  Item = (16 rows, chunk of keys) x head, four warps taking 16 keys
+// each in turn.
+//   S    A = q, B = 128 + c of 8 keys; two MMAs per group of components, whose sums the key's s and m then apply to.
+//   O    A = p s of the group, as two bf16 (16 bits kept), B = c - 8 of 8 components of that group; the part of the
+//        minima, sum p (m + 8 s), in fp32.
+// P leaves the first product in the very registers that the second one takes it from.
+constexpr int kRowsPerItem = 16;
+
+template <int D>
+struct Kv4RowsMerge {
+    float m[kKvWarps][kRowsPerItem], l[kKvWarps][kRowsPerItem];
+    float o[kKvWarps][kRowsPerItem][D];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kKvThreads) kv4_rows_mma_kernel(const Kv4Attn a) {
+    constexpr int W = D / 32;  // groups
+    constexpr unsigned kAll = 0xffffffffu;
+    __shared__ Kv4RowsMerge<D> sm;
+    pdl_trigger();
+    pdl_wait();
+    // first slot, keys, first row, rows | the rows' chunks, this chunk, first partial, - | keys row 0 sees
+    const int4 *rec = reinterpret_cast<const int4 *>(a.row_items) + 3 * blockIdx.x;
+    const int4 r0 = rec[0], r1 = rec[1], r2 = rec[2];
+    const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int64_t s0 = r0.x, s1 = s0 + r0.y;
+    const int rows = r0.w;
+
+    uint32_t qf[W][2][4];
+    float qsum[W][2];  // rows g and g + 8
+#pragma unroll
+    for (int y = 0; y < W; ++y) {
+        float x[2][8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+            if (g + 8 * i < rows)
+                load16((const bf16 *)a.qkv + (size_t)(r0.z + g + 8 * i) * 3 * a.H + h * D + 32 * y + 8 * t, x[i]);
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += x[i][e];
+            s += __shfl_xor_sync(kAll, s, 1);
+            s += __shfl_xor_sync(kAll, s, 2);
+            qsum[y][i] = s;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            qf[y][k][0] = pack2(x[0][2 * k], x[0][2 * k + 4]), qf[y][k][1] = pack2(x[1][2 * k], x[1][2 * k + 4]);
+            qf[y][k][2] = pack2(x[0][2 * k + 1], x[0][2 * k + 5]), qf[y][k][3] = pack2(x[1][2 * k + 1], x[1][2 * k + 5]);
+        }
+    }
+    float m[2] = {kLow, kLow}, l[2] = {0.f, 0.f}, zero[W][2], o[W][4][4];
+#pragma unroll
+    for (int y = 0; y < W; ++y) {
+        zero[y][0] = zero[y][1] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[y][j][0] = o[y][j][1] = o[y][j][2] = o[y][j][3] = 0.f;
+    }
+    for (int64_t b = (s0 & ~int64_t(15)) + 16 * warp; b < s1; b += 16 * kKvWarps) {
+        const int64_t row = (int64_t)h * a.v.S + b, pair = row >> 1;
+        if (b + 16 * kKvWarps < s1) {  // the warp's next 16 slots into L1, a line per lane (16 slots are whole lines)
+            constexpr int kCode = 16 * D / 2 / 128, kPar = 16 * W * 4 / 128 > 0 ? 16 * W * 4 / 128 : 1;
+            const int64_t next = row + 16 * kKvWarps;
+            const uint8_t *p = lane < kCode               ? a.v.kc + next * (D / 2) + lane * 128
+                               : lane < 2 * kCode         ? a.v.vc + next * (D / 2) + (lane - kCode) * 128
+                               : lane < 2 * kCode + kPar  ? (const uint8_t *)(a.v.kp + next * W) + (lane - 2 * kCode) * 128
+                                                          : (const uint8_t *)(a.v.vp + next * W) + (lane - 2 * kCode - kPar) * 128;
+            if (lane < 2 * (kCode + kPar)) prefetch_l1(p);
+        }
+        uint32_t kw[2][W], vw[2][W], kp[4][W], vp[2][2 * W];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t *kc = reinterpret_cast<const uint32_t *>(a.v.kc + (row + g + 8 * i) * (D / 2)) + t;
+            const uint32_t *vc = reinterpret_cast<const uint32_t *>(a.v.vc + (pair + t + 4 * i) * D) + g;
+#pragma unroll
+            for (int y = 0; y < W; ++y) kw[i][y] = kc[4 * y], vw[i][y] = vc[8 * y];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) load_words<W>(a.v.kp + (row + 8 * i + 2 * t + e) * W, kp[2 * i + e]);
+            if constexpr (W == 4) {
+                load_words<4>(a.v.vp + (pair + t + 4 * i) * 8, vp[i]);
+                load_words<4>(a.v.vp + (pair + t + 4 * i) * 8 + 4, vp[i] + 4);
+            } else {
+                load_words<2 * W>(a.v.vp + (pair + t + 4 * i) * (2 * W), vp[i]);
+            }
+        }
+        // scores: c[i][..] = keys 8 i + 2 t, + 1 of rows g (0, 1) and g + 8 (2, 3)
+        float sc[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+#pragma unroll
+            for (int y = 0; y < W; ++y) {
+                float c[4] = {-128.f * qsum[y][0], -128.f * qsum[y][0], -128.f * qsum[y][1], -128.f * qsum[y][1]};
+                const uint32_t w = kw[i][y];
+                kv4_mma(c, qf[y][0][0], qf[y][0][1], qf[y][0][2], qf[y][0][3], code_pair<0>(w), code_pair<1>(w));
+                kv4_mma(c, qf[y][1][0], qf[y][1][1], qf[y][1][2], qf[y][1][3], code_pair<2>(w), code_pair<3>(w));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float s = bf_lo(kp[2 * i + e][y]), z = bf_hi(kp[2 * i + e][y]);
+                    sc[i][e] = fmaf(s, c[e], fmaf(z, qsum[y][0], sc[i][e]));
+                    sc[i][2 + e] = fmaf(s, c[2 + e], fmaf(z, qsum[y][1], sc[i][2 + e]));
+                }
+            }
+        }
+        // causal: row j of the item sees the chunk's first r2.x + j keys (the chunk itself ends at s1)
+        const bool whole = b >= s0 && b + 16 <= s1 && b + 16 - s0 <= r2.x;
+        const int first = (int)(b - s0) + 2 * t;  // this lane's first key, in the chunk
+        float mx[2] = {kLow, kLow};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sc[i][e] *= a.scale_log2;
+                if (!whole) {
+                    const int key = first + 8 * i + (e & 1), j = g + 8 * (e >> 1);
+                    if (key < 0 || key >= r0.y || key >= r2.x + j) sc[i][e] = -INFINITY;
+                }
+                mx[e >> 1] = fmaxf(mx[e >> 1], sc[i][e]);
+            }
+        bool grown = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(kAll, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(kAll, mx[i], 2));
+            grown |= mx[i] > m[i];
+        }
+        if (__any_sync(kAll, grown)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float n = fmaxf(m[i], mx[i]), corr = exp2f(m[i] - n);
+                m[i] = n;
+                l[i] *= corr;
+#pragma unroll
+                for (int y = 0; y < W; ++y) {
+                    zero[y][i] *= corr;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[y][j][2 * i] *= corr, o[y][j][2 * i + 1] *= corr;
+                }
+            }
+        }
+        float p[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                p[i][e] = exp2f(sc[i][e] - m[e >> 1]);  // (-inf: 0)
+                l[e >> 1] += p[i][e];
+            }
+#pragma unroll
+        for (int y = 0; y < W; ++y) {
+            // A: rows g, g + 8 at keys 2t, 2t + 1 (a0, a1) and 2t + 8, 2t + 9 (a2, a3)
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float se = bf_lo(vp[i][2 * y]), me = bf_hi(vp[i][2 * y]), so = bf_lo(vp[i][2 * y + 1]),
+                            mo = bf_hi(vp[i][2 * y + 1]);
+                const float ze = fmaf(8.f, se, me), zo = fmaf(8.f, so, mo);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {  // row g + 8 x
+                    const float pe = p[i][2 * x], po = p[i][2 * x + 1];
+                    float we = pe * se, wo = po * so, ye = pe * ze, yo = po * zo;
+                    if (!whole) {  // (what a row does not see may hold anything: 0 times a NaN)
+                        if (pe == 0.f) we = ye = 0.f;
+                        if (po == 0.f) wo = yo = 0.f;
+                    }
+                    zero[y][x] += ye + yo;
+                    hi[2 * i + x] = pack2(we, wo);
+                    lo[2 * i + x] = pack2(we - bf_lo(hi[2 * i + x]), wo - bf_hi(hi[2 * i + x]));
+                }
+            }
+            const uint32_t c0[4] = {code_pair_centred<0>(vw[0][y]), code_pair_centred<1>(vw[0][y]),
+                                    code_pair_centred<2>(vw[0][y]), code_pair_centred<3>(vw[0][y])};
+            const uint32_t c1[4] = {code_pair_centred<0>(vw[1][y]), code_pair_centred<1>(vw[1][y]),
+                                    code_pair_centred<2>(vw[1][y]), code_pair_centred<3>(vw[1][y])};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                kv4_mma(o[y][j], hi[0], hi[1], hi[2], hi[3], c0[j], c1[j]);
+                kv4_mma(o[y][j], lo[0], lo[1], lo[2], lo[3], c0[j], c1[j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(kAll, l[i], 1);
+        l[i] += __shfl_xor_sync(kAll, l[i], 2);
+        if (t == 0) sm.m[warp][g + 8 * i] = m[i], sm.l[warp][g + 8 * i] = l[i];
+#pragma unroll
+        for (int y = 0; y < W; ++y) {
+            float z = zero[y][i];
+            z += __shfl_xor_sync(kAll, z, 1);
+            z += __shfl_xor_sync(kAll, z, 2);
+            // columns 2t and 2t + 1 of o[y][j]: components 32 y + 8 t + j and + 4
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sm.o[warp][g + 8 * i][32 * y + 8 * t + j] = o[y][j][2 * i] + z;
+                sm.o[warp][g + 8 * i][32 * y + 8 * t + 4 + j] = o[y][j][2 * i + 1] + z;
+            }
+        }
+    }
+    __syncthreads();
+    // join the warps; of several chunks, the partials are joined by the next kernel
+    const int nch = r1.x;
+    for (int x = threadIdx.x; x < rows * D; x += kKvThreads) {
+        const int j = x / D, d = x - j * D;
+        float M = kLow, L = 0.f, O = 0.f;
+#pragma unroll
+        for (int w = 0; w < kKvWarps; ++w) M = fmaxf(M, sm.m[w][j]);
+#pragma unroll
+        for (int w = 0; w < kKvWarps; ++w) {
+            const float c = exp2f(sm.m[w][j] - M);
+            L += sm.l[w][j] * c, O += sm.o[w][j][d] * c;
+        }
+        if (nch == 1) {
+            ((bf16 *)a.out)[(size_t)(r0.z + j) * a.H + h * D + d] = __float2bfloat16_rn(O / L);
+        } else {
+            float *mine = a.row_part + (((size_t)(r1.z + r1.y) * a.n_heads + h) * kRowsPerItem + j) * (D + 2);
+            mine[d] = O;
+            if (d == 0) mine[D] = M, mine[D + 1] = L;
+        }
+    }
+}
+
+// The chunks' partials of one group of rows and head, a warp per row.  (A launch of its own: the last block of a group
+// joining them alone took longer than the attention, 16 rows of 130 floats for every chunk.)
+template <int D>
+__global__ void __launch_bounds__(32 * kRowsPerItem) kv4_rows_join_kernel(const Kv4Attn a) {
+    pdl_trigger();
+    pdl_wait();
+    const int4 r = reinterpret_cast<const int4 *>(a.row_joins)[blockIdx.x];  // first row, rows, chunks, first partial
+    const int h = blockIdx.y, j = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (j >= r.y) return;
+    const float *part = a.row_part + (((size_t)r.w * a.n_heads + h) * kRowsPerItem + j) * (D + 2);
+    bf16 *dst = (bf16 *)a.out + (size_t)(r.x + j) * a.H + h * D;
+#pragma unroll
+    for (int d = lane; d < D; d += 32)
+        dst[d] = __float2bfloat16_rn(kv4_join<D>(part, (size_t)a.n_heads * kRowsPerItem * (D + 2), r.z, d));
+}
+
 template <typename T>
 cudaError_t launch_decode(const Kv4Attn &a, int d, int n_items, cudaStream_t st) {
     const dim3 grid(n_items, a.n_heads), block(kKvThreads);
@@ -709,8 +1096,7 @@ cudaError_t launch_decode(const Kv4Attn &a, int d, int n_items, cudaStream_t st)
 // plans
 // ---------------------------------------------------------------------------
 constexpr int32_t kKv4Magic = 0x4B563450;
-constexpr int kKv4Hdr = 32;
-constexpr int kReadTile = 64;  // slots per read-back tile
+constexpr int kKv4Hdr = 64;
 enum : int {
     Q_MAGIC = 0,
     Q_DTYPE,
@@ -725,7 +1111,8 @@ enum : int {
     Q_KEYS,      // keys of all requests
     Q_TWICE,     // a slot is written by two rows of the batch
     Q_TOTAL,
-    Q_O_ROWSLOT,  // word offsets of the tables
+    Q_UNITS,     // rows to write, by ones and by twos that share a pair of slots
+    Q_O_UNITS,   // word offsets of the tables
     Q_O_ITEMS,
     Q_O_COUNT,
     Q_O_TILES,
@@ -739,36 +1126,48 @@ enum : int {
     Q_O_PREREAD,
     Q_O_REQOFF,
     Q_O_REQCTX,
+    Q_RITEMS,   // work items of groups of rows, their partials and the groups that have some
+    Q_RPARTS,
+    Q_RJOINS,
+    Q_O_RITEMS,
+    Q_O_RJOINS,
     Q_O_REQWS,  // a prompt's first slot in the workspace's pool
 };
 // Requests of at least this many rows run on the prefill kernel (bf16, head_dim 64 or 128).
-constexpr int kPromptRows = 16;
+static const int kPromptRows = [] { const char *e = getenv("KV4_R"); return e ? atoi(e) : 17; }();
 
 int64_t up4(int64_t w) { return (w + 3) & ~int64_t(3); }
 
 struct Kv4Sizes {
-    int64_t rows = 0, items = 0, splits = 0, parts = 0, tiles = 0, keys = 0;
+    int64_t rows = 0, units = 0, items = 0, splits = 0, parts = 0, tiles = 0, keys = 0;
+    int64_t ritems = 0, rsplits = 0, rparts = 0;
     int64_t pre = 0, pre_tiles = 0, pre_read = 0, pre_keys = 0;
-    int chunk = 0;
-    int64_t off_rowslot, off_items, off_count, off_tiles, off_pre, off_pretiles, off_preread, off_reqoff, off_reqctx,
+    int chunk = 0, rchunk = 0;
+    int64_t off_ritems, off_rjoins, off_units, off_items, off_count, off_tiles, off_pre, off_pretiles, off_preread, off_reqoff, off_reqctx,
         off_reqws, total;
 };
+
+// How a request's rows are attended: on the prefill kernel, in groups of rows, or row by row.
+enum Kv4Form { kPromptForm, kGroupForm, kRowForm };
+Kv4Form form_of(const Kv4Batch &b, int i) {
+    if (b.dtype != 1 || b.n_input[i] == 1 || b.head_dim == 16) return kRowForm;
+    return b.n_input[i] >= kPromptRows && b.head_dim >= 64 ? kPromptForm : kGroupForm;
+}
+int rows_per_item(Kv4Form f) { return f == kGroupForm ? kRowsPerItem : 1; }
 
 // Keys per work item: the largest chunk (a power of two, 64 .. 2048 keys) that
 // still gives every SM several blocks of four warps; short chunks cost a join,
 // long ones leave SMs idle.
-bool is_prompt(const Kv4Batch &b, int i) {
-    return b.dtype == 1 && (b.head_dim == 64 || b.head_dim == 128) && b.n_input[i] >= kPromptRows;
-}
-
-int kv4_chunk(const Kv4Batch &b, int num_sms) {
+int kv4_chunk(const Kv4Batch &b, Kv4Form f, int num_sms) {
+    static const int mult = [] { const char *e = getenv("KV4_M"); return e ? atoi(e) : 6; }();
+    const int64_t most = (int64_t)mult * num_sms, per = rows_per_item(f);
     int chunk = 2048;
     while (chunk > 64) {
         int64_t items = 0;
-        for (int i = 0; i < b.n_req && items * b.n_heads < 6LL * num_sms; ++i)
-            if (!is_prompt(b, i))
-                items += (int64_t)b.n_input[i] * ((b.ctx_len[i] + (int64_t)b.n_input[i] + chunk - 1) / chunk);
-        if (items * b.n_heads >= 6LL * num_sms) break;
+        for (int i = 0; i < b.n_req && items * b.n_heads < most; ++i)
+            if (form_of(b, i) == f)
+                items += (b.n_input[i] + per - 1) / per * ((b.ctx_len[i] + (int64_t)b.n_input[i] + chunk - 1) / chunk);
+        if (items * b.n_heads >= most) break;
         chunk /= 2;
     }
     return chunk;
@@ -782,17 +1181,28 @@ bool kv4_sizes(const Kv4Batch &b, int num_sms, Kv4Sizes *z) {
         rows += n;
         if (rows > INT32_MAX / 8) return false;
     }
-    z->chunk = kv4_chunk(b, num_sms);
+    z->chunk = kv4_chunk(b, kRowForm, num_sms);
+    z->rchunk = kv4_chunk(b, kGroupForm, num_sms);
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i];
         z->rows += n;
         z->keys += c + n;
+        z->units += n / 2 + (n % 2 || (b.kv_offset[i] + c) % 2 ? 1 : 0);
         z->tiles += (c + n + kReadTile - 1) / kReadTile;
-        if (is_prompt(b, i)) {
+        const Kv4Form form = form_of(b, i);
+        if (form == kPromptForm) {
             z->pre++;
             z->pre_tiles += (n + kPrefillRowsPerTile - 1) / kPrefillRowsPerTile;
             z->pre_read += (c + n + kReadTile - 1) / kReadTile;
             z->pre_keys += c + n;
+            continue;
+        }
+        if (form == kGroupForm) {
+            for (int64_t r = 0; r < n; r += kRowsPerItem) {
+                const int64_t nch = (c + std::min<int64_t>(n, r + kRowsPerItem) + z->rchunk - 1) / z->rchunk;
+                z->ritems += nch;
+                if (nch > 1) z->rsplits++, z->rparts += nch;
+            }
             continue;
         }
         for (int64_t j = 0; j < n; ++j) {
@@ -802,10 +1212,12 @@ bool kv4_sizes(const Kv4Batch &b, int num_sms, Kv4Sizes *z) {
         }
     }
     int64_t w = kKv4Hdr;
-    z->off_rowslot = w, w = up4(w + z->rows);
+    z->off_units = w, w = up4(w + 4 * z->units);
     z->off_items = w, w = up4(w + 8 * z->items);
     z->off_count = w, w = up4(w + z->splits * b.n_heads);
     z->off_tiles = w, w = up4(w + 4 * z->tiles);
+    z->off_ritems = w, w = up4(w + 12 * z->ritems);
+    z->off_rjoins = w, w = up4(w + 4 * z->rsplits);
     z->off_pre = w, w = up4(w + 4 * z->pre);
     z->off_pretiles = w, w = up4(w + 2 * z->pre_tiles);
     z->off_preread = w, w = up4(w + 4 * z->pre_read);
@@ -836,19 +1248,26 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     Kv4Sizes z;
     if (!kv4_sizes(b, num_sms, &z) || cap < z.total) return false;
     std::memset(buf, 0, sizeof(int32_t) * (size_t)z.total);  // (the device copy's counters start at zero)
-    int32_t *slot = buf + z.off_rowslot, *it = buf + z.off_items, *tl = buf + z.off_tiles;
+    int32_t *un = buf + z.off_units, *it = buf + z.off_items, *tl = buf + z.off_tiles;
     int32_t *pre = buf + z.off_pre, *pt = buf + z.off_pretiles, *pd = buf + z.off_preread;
     int32_t *req_off = buf + z.off_reqoff, *req_ctx = buf + z.off_reqctx, *req_ws = buf + z.off_reqws;
-    int64_t row = 0, split = 0, part = 0, key = 0, ws = 0;
+    int32_t *ri = buf + z.off_ritems, *rj = buf + z.off_rjoins;
+    int64_t row = 0, split = 0, part = 0, key = 0, ws = 0, rpart = 0;
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i], o = b.kv_offset[i];
-        const bool prompt = is_prompt(b, i);
+        const Kv4Form form = form_of(b, i);
+        const bool prompt = form == kPromptForm;
         req_off[i] = (int32_t)row;
         req_ctx[i] = (int32_t)c;
         req_ws[i] = (int32_t)ws;
+        for (int64_t j = 0; j < n; un += 4) {
+            un[0] = (int32_t)(row + j);
+            un[1] = (int32_t)(o + c + j);
+            un[2] = (o + c + j) % 2 == 0 && j + 1 < n ? 2 : 1;
+            j += un[2];
+        }
         for (int64_t j = 0; j < n; ++j, ++row) {
-            slot[row] = (int32_t)(o + c + j);
-            if (prompt) continue;
+            if (form != kRowForm) continue;
             const int64_t keys = c + j + 1, nch = (keys + z.chunk - 1) / z.chunk;
             for (int64_t k = 0; k < nch; ++k, it += 8) {
                 it[0] = (int32_t)(o + k * z.chunk);
@@ -860,6 +1279,24 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
                 it[6] = (int32_t)split;
             }
             if (nch > 1) ++split, part += nch;
+        }
+        for (int64_t r = 0; form == kGroupForm && r < n; r += kRowsPerItem) {
+            const int64_t rows = std::min<int64_t>(kRowsPerItem, n - r), keys = c + r + rows;
+            const int64_t nch = (keys + z.rchunk - 1) / z.rchunk;
+            for (int64_t k = 0; k < nch; ++k, ri += 12) {
+                ri[0] = (int32_t)(o + k * z.rchunk);
+                ri[1] = (int32_t)std::min<int64_t>(z.rchunk, keys - k * z.rchunk);
+                ri[2] = (int32_t)(req_off[i] + r);
+                ri[3] = (int32_t)rows;
+                ri[4] = (int32_t)nch;
+                ri[5] = (int32_t)k;
+                ri[6] = (int32_t)rpart;
+                ri[8] = (int32_t)(c + r + 1 - k * z.rchunk);
+            }
+            if (nch > 1) {
+                rj[0] = (int32_t)(req_off[i] + r), rj[1] = (int32_t)rows, rj[2] = (int32_t)nch, rj[3] = (int32_t)rpart;
+                rj += 4, rpart += nch;
+            }
         }
         for (int64_t t = 0; t < c + n; t += kReadTile, tl += 4) {
             tl[0] = (int32_t)(o + t);
@@ -895,6 +1332,7 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     buf[Q_DIM] = b.head_dim;
     buf[Q_SLOTS] = (int32_t)b.kv_slots;
     buf[Q_ROWS] = (int32_t)z.rows;
+    buf[Q_UNITS] = (int32_t)z.units;
     buf[Q_ITEMS] = (int32_t)z.items;
     buf[Q_SPLITS] = (int32_t)z.splits;
     buf[Q_PARTS] = (int32_t)z.parts;
@@ -902,10 +1340,15 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     buf[Q_KEYS] = (int32_t)z.keys;
     buf[Q_TWICE] = twice;
     buf[Q_TOTAL] = (int32_t)z.total;
-    buf[Q_O_ROWSLOT] = (int32_t)z.off_rowslot;
+    buf[Q_O_UNITS] = (int32_t)z.off_units;
     buf[Q_O_ITEMS] = (int32_t)z.off_items;
     buf[Q_O_COUNT] = (int32_t)z.off_count;
     buf[Q_O_TILES] = (int32_t)z.off_tiles;
+    buf[Q_RITEMS] = (int32_t)z.ritems;
+    buf[Q_RPARTS] = (int32_t)z.rparts;
+    buf[Q_RJOINS] = (int32_t)z.rsplits;
+    buf[Q_O_RITEMS] = (int32_t)z.off_ritems;
+    buf[Q_O_RJOINS] = (int32_t)z.off_rjoins;
     buf[Q_PRE] = (int32_t)z.pre;
     buf[Q_PRETILES] = (int32_t)z.pre_tiles;
     buf[Q_PREREAD] = (int32_t)z.pre_read;
@@ -926,7 +1369,7 @@ bool kv4_plan_writes_once(const int32_t *hp) { return !hp[Q_TWICE]; }
 namespace {
 // byte offsets in the workspace
 struct Kv4Work {
-    int64_t q16, pool16, q_scale, kv_scale, total;
+    int64_t row_part, q16, pool16, q_scale, kv_scale, total;
 };
 Kv4Work kv4_work(const int32_t *hp) {
     const int64_t nh = hp[Q_HEADS], d = hp[Q_DIM];
@@ -938,6 +1381,7 @@ Kv4Work kv4_work(const int32_t *hp) {
         return o;
     };
     take((int64_t)hp[Q_PARTS] * nh * (d + 2) * 4);
+    w.row_part = take((int64_t)hp[Q_RPARTS] * nh * kRowsPerItem * (d + 2) * 4);
     const bool pre = hp[Q_PRE] > 0;
     w.q16 = take(pre ? (int64_t)hp[Q_ROWS] * nh * d * 2 : 0);
     w.pool16 = take(2 * nh * hp[Q_PREKEYS] * d * 2);
@@ -950,26 +1394,46 @@ Kv4Work kv4_work(const int32_t *hp) {
 
 int64_t kv4_workspace_bytes(const int32_t *hp) { return kv4_work(hp).total; }
 
+namespace {
+// f(head_dim as a constant)
+template <typename F>
+cudaError_t for_dim(int d, F f) {
+    switch (d) {
+        case 16: return f(std::integral_constant<int, 16>());
+        case 32: return f(std::integral_constant<int, 32>());
+        case 64: return f(std::integral_constant<int, 64>());
+        case 128: return f(std::integral_constant<int, 128>());
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+template <typename T>
+cudaError_t append(const void *qkv, const Kv4View &v, const int32_t *hp, const int32_t *dp, cudaStream_t st) {
+    const int H = hp[Q_HEADS] * hp[Q_DIM];
+    const dim3 grid(hp[Q_UNITS], (H / 8 + kApThreads - 1) / kApThreads);
+    return for_dim(hp[Q_DIM], [&](auto d) {
+        return launch_pdl(kv4_append_kernel<T, d()>, grid, dim3(kApThreads), 0, st, (const T *)qkv, dp + hp[Q_O_UNITS], v,
+                          H);
+    });
+}
+
+template <typename T>
+cudaError_t read(const Kv4View &v, const int32_t *hp, const int32_t *dp, void *out, cudaStream_t st) {
+    return for_dim(hp[Q_DIM], [&](auto d) {
+        return launch_pdl(kv4_read_kernel<T, d(), false>, dim3(hp[Q_TILES], hp[Q_HEADS]), dim3(kRdThreads), 0, st, v,
+                          dp + hp[Q_O_TILES], (T *)out, (int64_t)hp[Q_KEYS], hp[Q_HEADS], (const float *)nullptr);
+    });
+}
+}  // namespace
+
 cudaError_t kv4_append(const void *qkv, void *layer, const int32_t *hp, const int32_t *dp, cudaStream_t st) {
-    const int nh = hp[Q_HEADS], d = hp[Q_DIM], H = nh * d, G = kv4_groups(d), gt = d / G / 8;
-    const Kv4View v = kv4_view(layer, nh, d, hp[Q_SLOTS]);
-    const dim3 grid(hp[Q_ROWS], (2 * H / 8 + kApThreads - 1) / kApThreads);
-    if (hp[Q_DTYPE] == 1)
-        return launch_pdl(kv4_append_kernel<bf16>, grid, dim3(kApThreads), 0, st, (const bf16 *)qkv,
-                          dp + hp[Q_O_ROWSLOT], v, H, d, G, gt);
-    return launch_pdl(kv4_append_kernel<float>, grid, dim3(kApThreads), 0, st, (const float *)qkv, dp + hp[Q_O_ROWSLOT],
-                      v, H, d, G, gt);
+    const Kv4View v = kv4_view(layer, hp[Q_HEADS], hp[Q_DIM], hp[Q_SLOTS]);
+    return hp[Q_DTYPE] == 1 ? append<bf16>(qkv, v, hp, dp, st) : append<float>(qkv, v, hp, dp, st);
 }
 
 cudaError_t kv4_read(const void *layer, const int32_t *hp, const int32_t *dp, void *out, cudaStream_t st) {
-    const int nh = hp[Q_HEADS], d = hp[Q_DIM], G = kv4_groups(d);
-    const Kv4View v = kv4_view(layer, nh, d, hp[Q_SLOTS]);
-    const dim3 grid(hp[Q_TILES], nh);
-    if (hp[Q_DTYPE] == 1)
-        return launch_pdl(kv4_read_kernel<bf16>, grid, dim3(kRdThreads), 0, st, v, dp + hp[Q_O_TILES], (bf16 *)out,
-                          (int64_t)hp[Q_KEYS], nh, d, G, (const float *)nullptr);
-    return launch_pdl(kv4_read_kernel<float>, grid, dim3(kRdThreads), 0, st, v, dp + hp[Q_O_TILES], (float *)out,
-                      (int64_t)hp[Q_KEYS], nh, d, G, (const float *)nullptr);
+    const Kv4View v = kv4_view(layer, hp[Q_HEADS], hp[Q_DIM], hp[Q_SLOTS]);
+    return hp[Q_DTYPE] == 1 ? read<bf16>(v, hp, dp, out, st) : read<float>(v, hp, dp, out, st);
 }
 
 cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp, int32_t *dp, void *workspace,
@@ -984,16 +1448,34 @@ cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp,
     a.scale_log2 = 1.4426950408889634f / sqrtf((float)d);
     a.items = dp + hp[Q_O_ITEMS];
     a.counters = dp + hp[Q_O_COUNT];
+    const Kv4Work w = kv4_work(hp);
+    uint8_t *ws = (uint8_t *)workspace;
     a.part = (float *)workspace;
+    a.row_items = dp + hp[Q_O_RITEMS];
+    a.row_joins = dp + hp[Q_O_RJOINS];
+    a.row_part = (float *)(ws + w.row_part);
     cudaError_t e = cudaSuccess;
     *launches = 0;
     if (hp[Q_ITEMS] > 0) {
         e = hp[Q_DTYPE] == 1 ? launch_decode<bf16>(a, d, hp[Q_ITEMS], st) : launch_decode<float>(a, d, hp[Q_ITEMS], st);
         ++*launches;
     }
+    if (e == cudaSuccess && hp[Q_RITEMS] > 0) {
+        const dim3 grid(hp[Q_RITEMS], nh), block(kKvThreads);
+        const dim3 joins(hp[Q_RJOINS], nh), join_block(32 * kRowsPerItem);
+        e = for_dim(d, [&](auto dim) {
+            if constexpr (dim() >= 32) {
+                const cudaError_t r = launch_pdl(kv4_rows_mma_kernel<dim()>, grid, block, 0, st, a);
+                if (r != cudaSuccess || hp[Q_RJOINS] == 0) return r;
+                ++*launches;
+                return launch_pdl(kv4_rows_join_kernel<dim()>, joins, join_block, 0, st, a);
+            } else {
+                return cudaErrorInvalidValue;
+            }
+        });
+        ++*launches;
+    }
     if (e != cudaSuccess || hp[Q_PRE] == 0) return e;
-    const Kv4Work w = kv4_work(hp);
-    uint8_t *ws = (uint8_t *)workspace;
     Kv4Prep pr;
     pr.qkv = (const bf16 *)qkv;
     pr.q16 = (__half *)(ws + w.q16);
@@ -1003,13 +1485,15 @@ cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp,
     pr.H = a.H, pr.n_heads = nh, pr.d = d, pr.G = kv4_groups(d);
     pr.n_rows = hp[Q_ROWS], pr.n_pre = hp[Q_PRE];
     pr.pre = dp + hp[Q_O_PRE];
-    constexpr int kWarps = kPrepThreads / 32;
-    const int64_t blocks = (int64_t)pr.n_pre * nh + ((int64_t)pr.n_rows * nh + kWarps - 1) / kWarps;
+    constexpr int kPer = kPrepThreads * kPrepQ;
+    const int64_t blocks = (int64_t)pr.n_pre * nh + ((int64_t)pr.n_rows * (a.H / 8) + kPer - 1) / kPer;
     e = launch_pdl(kv4_prep_kernel, dim3((unsigned)blocks), dim3(kPrepThreads), 0, st, pr);
     if (e == cudaSuccess)
-        e = launch_pdl(kv4_read_kernel<__half>, dim3(hp[Q_PREREAD], nh), dim3(kRdThreads), 0, st, a.v,
-                       dp + hp[Q_O_PREREAD], (__half *)(ws + w.pool16), (int64_t)hp[Q_PREKEYS], nh, d, pr.G,
-                       (const float *)pr.kv_scale);
+        e = for_dim(d, [&](auto dim) {
+            return launch_pdl(kv4_read_kernel<__half, dim(), true>, dim3(hp[Q_PREREAD], nh), dim3(kRdThreads), 0, st, a.v,
+                              dp + hp[Q_O_PREREAD], (__half *)(ws + w.pool16), (int64_t)hp[Q_PREKEYS], nh,
+                              (const float *)pr.kv_scale);
+        });
     AttnPlan ap{};
     ap.req_off = dp + hp[Q_O_REQOFF];
     ap.req_ctx = dp + hp[Q_O_REQCTX];
