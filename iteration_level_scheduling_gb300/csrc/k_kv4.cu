@@ -485,6 +485,13 @@ struct Kv4Merge {
     int last;
 };
 
+// 2^x by the SFU's approximation (x <= 0 here; results below 2^-126 are zero)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // The four warps' states (each already in sm) -> the row's output, or this
 // chunk's partial; the last chunk to arrive joins all of them in chunk order,
 // so the result does not depend on which that is.
@@ -621,8 +628,7 @@ __global__ void __launch_bounds__(kKvThreads) kv4_decode_kernel(const Kv4Attn a)
 //   scores   rows = 16 keys.  A lane's loads of one key are components of one
 //            group; q enters column g of B only where the component's group is
 //            g, so the columns of S gather sum q c group by group and s, m
-//            apply afterwards.  A = 128 + c (the bits of c in the mantissa of
-//            bf16's 128); -128 sum q is the accumulator's start.
+//            apply afterwards.  A = the codes as fp16 subnormals, q in fp16.
 //   values   rows = 16 components, k = 16 keys.  A = c - 8, exact; column g of
 //            B is p s_g rounded to bf16, column 4 + g what the rounding left,
 //            so the weights keep 16 bits; sum p (m + 8 s) is added in fp32.
@@ -675,20 +681,52 @@ struct Kv4Block {
     uint32_t v[2][W];                 // pairs t, t + 4: components 4 W g ..
     uint32_t kp[2][2];                // keys g, g + 8: groups 2t, 2t + 1
     uint32_t vp[2][2];                // pairs t, t + 4: group g % 4, even and odd slot
-    __device__ __forceinline__ void load(const Kv4View &v4, int h, int64_t b, int g, int t) {
-        const int64_t row = (int64_t)h * v4.S + b, pair = row >> 1;
+};
+// Where a lane reads; a block ahead is a constant step.
+template <int D>
+struct Kv4Lane {
+    static constexpr int W = D / 32;
+    const uint8_t *kc, *vc;
+    const uint32_t *kp, *vp;
+    __device__ __forceinline__ Kv4Lane(const Kv4View &v, int h, int64_t b, int g, int t) {
+        const int64_t row = (int64_t)h * v.S + b, pair = row >> 1;
+        kc = v.kc + (row + g) * (D / 2) + t * (4 * W);
+        vc = v.vc + (pair + t) * D + g * (4 * W);
+        kp = v.kp + (row + g) * W + (W == 4 ? 2 * (t & 1) : 0);
+        vp = v.vp + ((pair + t) * W + (g & (W - 1))) * 2;
+    }
+    __device__ __forceinline__ void load(Kv4Block<D> &x) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            load_words<W>(v4.kc + (row + g + 8 * i) * (D / 2) + t * (4 * W), k[i]);
-            load_words<W>(v4.vc + (pair + t + 4 * i) * D + g * (4 * W), v[i]);
-            const uint32_t *p = v4.kp + (row + g + 8 * i) * W;
-            if constexpr (W == 4) load_words<2>(p + 2 * (t & 1), kp[i]);
-            else if constexpr (W == 2) load_words<2>(p, kp[i]);
-            else kp[i][0] = __ldcs(p), kp[i][1] = 0u;
-            load_words<2>(v4.vp + ((pair + t + 4 * i) * W + (g & (W - 1))) * 2, vp[i]);
+            load_words<W>(kc + i * 4 * D, x.k[i]);
+            load_words<W>(vc + i * 4 * D, x.v[i]);
+            if constexpr (W > 1) load_words<2>(kp + i * 8 * W, x.kp[i]);
+            else x.kp[i][0] = __ldcs(kp + i * 8), x.kp[i][1] = 0u;
+            load_words<2>(vp + i * 8 * W, x.vp[i]);
         }
+        kc += 8 * D * kKvWarps, vc += 8 * D * kKvWarps;
+        kp += 16 * W * kKvWarps, vp += 16 * W * kKvWarps;
     }
 };
+
+// Nibbles N and N + 4 of a word as fp16: N even, the value c 2^-24 (a subnormal: the bits themselves); N odd, c 2^-20.
+// Two of the four pairs need no shift, and nothing is added that the product would have to lose again.
+template <int N>
+__device__ __forceinline__ uint32_t code_pair_f16(uint32_t w) {
+    return (N < 2 ? w : w >> 8) & (N % 2 ? 0x00f000f0u : 0x000f000fu);
+}
+__device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ void kv4_mma_f16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
 template <int D>
 __global__ void __launch_bounds__(kKvThreads, 4) kv4_decode_mma_kernel(const Kv4Attn a) {
@@ -700,27 +738,39 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv4_decode_mma_kernel(const Kv4
     const int4 r0 = reinterpret_cast<const int4 *>(a.items)[2 * blockIdx.x],
                r1 = reinterpret_cast<const int4 *>(a.items)[2 * blockIdx.x + 1];
     const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int64_t s0 = r0.x, s1 = s0 + r0.y;
-    int64_t b = (s0 & ~int64_t(15)) + 16 * warp;  // (S is a multiple of 16: a block never leaves the layer)
-    Kv4Block<D> nx;
-    if (b < s1) nx.load(a.v, h, b, g, t);
+    // slots relative to the chunk's first block of 16 (S is a multiple of 16: a block never leaves the layer)
+    const int64_t base = r0.x & ~15;
+    const int s0 = r0.x & 15, s1 = s0 + r0.y;
+    int b = 16 * warp;
+    Kv4Lane<D> at(a.v, h, base + b, g, t);
+    Kv4Block<D> xa, xb;
+    if (b < s1) at.load(xa);
 
-    // q: word w of a lane covers components 8 (W t + w) ..; pairs (n, n + 4)
+    // q in fp16, its largest magnitude brought to 2^14 by a power of two (bf16 has fewer bits: nothing is lost down to
+    // 2^-28 of that).  Word w of a lane covers components 8 (W t + w) ..; pairs (n, n + 4), those of odd n over 16.
     uint32_t qf[W][4];
-    float qsum[2];  // sum of q over groups 2t and 2t + 1
+    float qsum[2], q_inv;  // sums of q over groups 2t and 2t + 1
     {
         const bf16 *q = (const bf16 *)a.qkv + (size_t)r0.z * 3 * a.H + h * D + 8 * W * t;
         const bool mine = g == (t * W) / 4;
-        float sum = 0.f;
+        float x[W][8], sum = 0.f, big = 0.f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            float x[8];
-            load16(q + 8 * w, x);
+            load16(q + 8 * w, x[w]);
 #pragma unroll
-            for (int n = 0; n < 8; ++n) sum += x[n];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) qf[w][n] = mine ? pack2(x[n], x[n + 4]) : 0u;
+            for (int n = 0; n < 8; ++n) sum += x[w][n], big = max_nan(big, fabsf(x[w][n]));
         }
+        big = max_nan(big, __shfl_xor_sync(kAll, big, 1));
+        big = max_nan(big, __shfl_xor_sync(kAll, big, 2));
+        q_inv = kv4_inverse_scale(big);
+        const float f = 1.f / q_inv;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const float fn = n % 2 ? f * 0.0625f : f;
+                qf[w][n] = mine ? pack2_f16(x[w][n] * fn, x[w][n + 4] * fn) : 0u;
+            }
         float of[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) of[j] = __shfl_sync(kAll, sum, j);
@@ -730,38 +780,38 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv4_decode_mma_kernel(const Kv4
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt)
                 if ((tt * W) / 4 == 2 * t + j) qsum[j] += of[tt];
+            qsum[j] *= a.scale_log2;
         }
+        q_inv *= a.scale_log2;
     }
     float m = kLow, l = 0.f, zero = 0.f, o[2 * W][4];
 #pragma unroll
     for (int i = 0; i < 2 * W; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-    while (b < s1) {
-        const Kv4Block<D> x = nx;
-        const int64_t here = b;
-        b += 16 * kKvWarps;
-        if (b < s1) nx.load(a.v, h, b, g, t);
+    auto step = [&](const Kv4Block<D> &x, int here) {
         // scores of keys g and g + 8
-        float c[4] = {-128.f * qsum[0], -128.f * qsum[1], -128.f * qsum[0], -128.f * qsum[1]};
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            kv4_mma(c, code_pair<0>(x.k[0][w]), code_pair<0>(x.k[1][w]), code_pair<1>(x.k[0][w]),
-                    code_pair<1>(x.k[1][w]), qf[w][0], qf[w][1]);
-            kv4_mma(c, code_pair<2>(x.k[0][w]), code_pair<2>(x.k[1][w]), code_pair<3>(x.k[0][w]),
-                    code_pair<3>(x.k[1][w]), qf[w][2], qf[w][3]);
+            kv4_mma_f16(c, code_pair_f16<0>(x.k[0][w]), code_pair_f16<0>(x.k[1][w]), code_pair_f16<1>(x.k[0][w]),
+                        code_pair_f16<1>(x.k[1][w]), qf[w][0], qf[w][1]);
+            kv4_mma_f16(c, code_pair_f16<2>(x.k[0][w]), code_pair_f16<2>(x.k[1][w]), code_pair_f16<3>(x.k[0][w]),
+                        code_pair_f16<3>(x.k[1][w]), qf[w][2], qf[w][3]);
         }
         float sc[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            // (lanes whose columns hold no group have c = qsum = 0 but may have read another's parameters)
             float s = 0.f;
-            if (2 * t < W)
-                s = bf_lo(x.kp[i][0]) * c[2 * i] + bf_hi(x.kp[i][0]) * qsum[0] + bf_lo(x.kp[i][1]) * c[2 * i + 1] +
-                    bf_hi(x.kp[i][1]) * qsum[1];
-            s += __shfl_xor_sync(kAll, s, 1);
-            s += __shfl_xor_sync(kAll, s, 2);
-            sc[i] = s * a.scale_log2;
+            if (2 * t < W) {  // (the other lanes' columns hold no group)
+                const float u = fmaf(bf_lo(x.kp[i][0]), c[2 * i], bf_lo(x.kp[i][1]) * c[2 * i + 1]) * 16777216.f;
+                s = fmaf(u, q_inv, fmaf(bf_hi(x.kp[i][0]), qsum[0], bf_hi(x.kp[i][1]) * qsum[1]));
+            }
+            if (W == 4) s += __shfl_xor_sync(kAll, s, 1);
+            sc[i] = s;
         }
+        // from lanes t = 0 to the key's other lanes: for W = 4 lanes 0 and 1 have the sum
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sc[i] = __shfl_sync(kAll, sc[i], lane & ~3);
         const bool whole = here >= s0 && here + 16 <= s1;  // warp-uniform
         bool v_lo = true, v_hi = true;
         if (!whole) {
@@ -771,17 +821,17 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv4_decode_mma_kernel(const Kv4
             if (!v_hi) sc[1] = kLow;
         }
         float mx = fmaxf(sc[0], sc[1]);
-        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
-        if (mx > m) {  // warp-uniform
-            const float corr = exp2f(m - mx);
+        if (__any_sync(kAll, mx > m)) {
+            mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
+            const float corr = ex2(m - mx);
             m = mx;
             l *= corr, zero *= corr;
 #pragma unroll
             for (int i = 0; i < 2 * W; ++i) o[i][0] *= corr, o[i][1] *= corr, o[i][2] *= corr, o[i][3] *= corr;
         }
-        const float p_lo = v_lo ? exp2f(sc[0] - m) : 0.f, p_hi = v_hi ? exp2f(sc[1] - m) : 0.f;
+        const float p_lo = v_lo ? ex2(sc[0] - m) : 0.f, p_hi = v_hi ? ex2(sc[1] - m) : 0.f;
         l += p_lo + p_hi;
         // weights of keys 2t, 2t + 1, 2t + 8, 2t + 9 in group g % 4
         uint32_t bw[2];
@@ -790,12 +840,12 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv4_decode_mma_kernel(const Kv4
             const float pe = __shfl_sync(kAll, i ? p_hi : p_lo, 8 * t), po = __shfl_sync(kAll, i ? p_hi : p_lo, 8 * t + 4);
             float se = bf_lo(x.vp[i][0]), me = bf_hi(x.vp[i][0]), so = bf_lo(x.vp[i][1]), mo = bf_hi(x.vp[i][1]);
             if (!whole) {  // an unused slot's parameters may be anything
-                const int64_t slot = here + 8 * i + 2 * t;
+                const int slot = here + 8 * i + 2 * t;
                 if (slot < s0 || slot >= s1) se = me = 0.f;
                 if (slot + 1 < s0 || slot + 1 >= s1) so = mo = 0.f;
             }
             const float we = pe * se, wo = po * so;
-            zero += pe * fmaf(8.f, se, me) + po * fmaf(8.f, so, mo);
+            zero = fmaf(8.f, we + wo, fmaf(pe, me, fmaf(po, mo, zero)));
             const uint32_t hi = pack2(we, wo);
             const uint32_t left = pack2(we - bf_lo(hi), wo - bf_hi(hi));
             bw[i] = (g & 3) >= W ? 0u : g < 4 ? hi : left;
@@ -807,6 +857,16 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv4_decode_mma_kernel(const Kv4
             kv4_mma(o[2 * w + 1], code_pair_centred<2>(x.v[0][w]), code_pair_centred<3>(x.v[0][w]),
                     code_pair_centred<2>(x.v[1][w]), code_pair_centred<3>(x.v[1][w]), bw[0], bw[1]);
         }
+    };
+    constexpr int kStep = 16 * kKvWarps;
+    while (b < s1) {
+        if (b + kStep < s1) at.load(xb);
+        step(xa, b);
+        b += kStep;
+        if (b >= s1) break;
+        if (b + kStep < s1) at.load(xa);
+        step(xb, b);
+        b += kStep;
     }
     // l over the keys of a lane's column; the minima's part over the keys of its group
     l += __shfl_xor_sync(kAll, l, 4);
@@ -848,11 +908,14 @@ template <int D>
 struct Kv4RowsMerge {
     float m[kKvWarps][kRowsPerItem], l[kKvWarps][kRowsPerItem];
     float o[kKvWarps][kRowsPerItem][D];
+    uint4 q[D / 32][2][32];  // q as the A operand: group, half of it, lane
 };
 
-template <int D>
-__global__ void __launch_bounds__(kKvThreads) kv4_rows_mma_kernel(const Kv4Attn a) {
+// Half: every item of the launch has at most 8 rows, and the A operand's rows 8 .. 15 are zero.
+template <int D, bool Half>
+__global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4Attn a) {
     constexpr int W = D / 32;  // groups
+    constexpr int R = Half ? 1 : 2;  // row g, and g + 8
     constexpr unsigned kAll = 0xffffffffu;
     __shared__ Kv4RowsMerge<D> sm;
     pdl_trigger();
@@ -864,7 +927,6 @@ __global__ void __launch_bounds__(kKvThreads) kv4_rows_mma_kernel(const Kv4Attn 
     const int64_t s0 = r0.x, s1 = s0 + r0.y;
     const int rows = r0.w;
 
-    uint32_t qf[W][2][4];
     float qsum[W][2];  // rows g and g + 8
 #pragma unroll
     for (int y = 0; y < W; ++y) {
@@ -873,7 +935,7 @@ __global__ void __launch_bounds__(kKvThreads) kv4_rows_mma_kernel(const Kv4Attn 
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-            if (g + 8 * i < rows)
+            if (i < R && g + 8 * i < rows)
                 load16((const bf16 *)a.qkv + (size_t)(r0.z + g + 8 * i) * 3 * a.H + h * D + 32 * y + 8 * t, x[i]);
             float s = 0.f;
 #pragma unroll
@@ -883,11 +945,13 @@ __global__ void __launch_bounds__(kKvThreads) kv4_rows_mma_kernel(const Kv4Attn 
             qsum[y][i] = s;
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            qf[y][k][0] = pack2(x[0][2 * k], x[0][2 * k + 4]), qf[y][k][1] = pack2(x[1][2 * k], x[1][2 * k + 4]);
-            qf[y][k][2] = pack2(x[0][2 * k + 1], x[0][2 * k + 5]), qf[y][k][3] = pack2(x[1][2 * k + 1], x[1][2 * k + 5]);
-        }
+        for (int k = 0; k < 2; ++k)
+            if (warp == (2 * y + k) % kKvWarps)
+                sm.q[y][k][lane] = make_uint4(pack2(x[0][2 * k], x[0][2 * k + 4]), pack2(x[1][2 * k], x[1][2 * k + 4]),
+                                              pack2(x[0][2 * k + 1], x[0][2 * k + 5]),
+                                              pack2(x[1][2 * k + 1], x[1][2 * k + 5]));
     }
+    __syncthreads();
     float m[2] = {kLow, kLow}, l[2] = {0.f, 0.f}, zero[W][2], o[W][4][4];
 #pragma unroll
     for (int y = 0; y < W; ++y) {
@@ -931,13 +995,14 @@ __global__ void __launch_bounds__(kKvThreads) kv4_rows_mma_kernel(const Kv4Attn 
             for (int y = 0; y < W; ++y) {
                 float c[4] = {-128.f * qsum[y][0], -128.f * qsum[y][0], -128.f * qsum[y][1], -128.f * qsum[y][1]};
                 const uint32_t w = kw[i][y];
-                kv4_mma(c, qf[y][0][0], qf[y][0][1], qf[y][0][2], qf[y][0][3], code_pair<0>(w), code_pair<1>(w));
-                kv4_mma(c, qf[y][1][0], qf[y][1][1], qf[y][1][2], qf[y][1][3], code_pair<2>(w), code_pair<3>(w));
+                const uint4 qa = sm.q[y][0][lane], qb = sm.q[y][1][lane];
+                kv4_mma(c, qa.x, qa.y, qa.z, qa.w, code_pair<0>(w), code_pair<1>(w));
+                kv4_mma(c, qb.x, qb.y, qb.z, qb.w, code_pair<2>(w), code_pair<3>(w));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float s = bf_lo(kp[2 * i + e][y]), z = bf_hi(kp[2 * i + e][y]);
                     sc[i][e] = fmaf(s, c[e], fmaf(z, qsum[y][0], sc[i][e]));
-                    sc[i][2 + e] = fmaf(s, c[2 + e], fmaf(z, qsum[y][1], sc[i][2 + e]));
+                    if (!Half) sc[i][2 + e] = fmaf(s, c[2 + e], fmaf(z, qsum[y][1], sc[i][2 + e]));
                 }
             }
         }
@@ -948,7 +1013,7 @@ __global__ void __launch_bounds__(kKvThreads) kv4_rows_mma_kernel(const Kv4Attn 
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2 * R; ++e) {
                 sc[i][e] *= a.scale_log2;
                 if (!whole) {
                     const int key = first + 8 * i + (e & 1), j = g + 8 * (e >> 1);
@@ -958,15 +1023,15 @@ __global__ void __launch_bounds__(kKvThreads) kv4_rows_mma_kernel(const Kv4Attn 
             }
         bool grown = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < R; ++i) {
             mx[i] = fmaxf(mx[i], __shfl_xor_sync(kAll, mx[i], 1));
             mx[i] = fmaxf(mx[i], __shfl_xor_sync(kAll, mx[i], 2));
             grown |= mx[i] > m[i];
         }
         if (__any_sync(kAll, grown)) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float n = fmaxf(m[i], mx[i]), corr = exp2f(m[i] - n);
+            for (int i = 0; i < R; ++i) {
+                const float n = fmaxf(m[i], mx[i]), corr = ex2(m[i] - n);
                 m[i] = n;
                 l[i] *= corr;
 #pragma unroll
@@ -981,21 +1046,21 @@ __global__ void __launch_bounds__(kKvThreads) kv4_rows_mma_kernel(const Kv4Attn 
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                p[i][e] = exp2f(sc[i][e] - m[e >> 1]);  // (-inf: 0)
+            for (int e = 0; e < 2 * R; ++e) {
+                p[i][e] = ex2(sc[i][e] - m[e >> 1]);  // (-inf: 0)
                 l[e >> 1] += p[i][e];
             }
 #pragma unroll
         for (int y = 0; y < W; ++y) {
             // A: rows g, g + 8 at keys 2t, 2t + 1 (a0, a1) and 2t + 8, 2t + 9 (a2, a3)
-            uint32_t hi[4], lo[4];
+            uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float se = bf_lo(vp[i][2 * y]), me = bf_hi(vp[i][2 * y]), so = bf_lo(vp[i][2 * y + 1]),
                             mo = bf_hi(vp[i][2 * y + 1]);
                 const float ze = fmaf(8.f, se, me), zo = fmaf(8.f, so, mo);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {  // row g + 8 x
+                for (int x = 0; x < R; ++x) {  // row g + 8 x
                     const float pe = p[i][2 * x], po = p[i][2 * x + 1];
                     float we = pe * se, wo = po * so, ye = pe * ze, yo = po * zo;
                     if (!whole) {  // (what a row does not see may hold anything: 0 times a NaN)
@@ -1019,7 +1084,7 @@ __global__ void __launch_bounds__(kKvThreads) kv4_rows_mma_kernel(const Kv4Attn 
         }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < R; ++i) {
         l[i] += __shfl_xor_sync(kAll, l[i], 1);
         l[i] += __shfl_xor_sync(kAll, l[i], 2);
         if (t == 0) sm.m[warp][g + 8 * i] = m[i], sm.l[warp][g + 8 * i] = l[i];
@@ -1129,12 +1194,15 @@ enum : int {
     Q_RITEMS,   // work items of groups of rows, their partials and the groups that have some
     Q_RPARTS,
     Q_RJOINS,
+    Q_RHALF,  // no group has more than 8 rows
     Q_O_RITEMS,
     Q_O_RJOINS,
     Q_O_REQWS,  // a prompt's first slot in the workspace's pool
 };
-// Requests of at least this many rows run on the prefill kernel (bf16, head_dim 64 or 128).
-static const int kPromptRows = [] { const char *e = getenv("KV4_R"); return e ? atoi(e) : 17; }();
+// Requests of at least this many rows run on the prefill kernel (bf16, head_dim 64 or 128).  8 requests over 2000 keys,
+// 40 heads of 128: 16 rows 89 us in groups and 174 on it, 32 rows 144 and 176, 48 rows 199 and 177; one request over
+// 300 keys: 32 rows 15 and 21 us, 64 rows 21 and 21.
+constexpr int kPromptRows = 33;
 
 int64_t up4(int64_t w) { return (w + 3) & ~int64_t(3); }
 
@@ -1159,8 +1227,8 @@ int rows_per_item(Kv4Form f) { return f == kGroupForm ? kRowsPerItem : 1; }
 // still gives every SM several blocks of four warps; short chunks cost a join,
 // long ones leave SMs idle.
 int kv4_chunk(const Kv4Batch &b, Kv4Form f, int num_sms) {
-    static const int mult = [] { const char *e = getenv("KV4_M"); return e ? atoi(e) : 6; }();
-    const int64_t most = (int64_t)mult * num_sms, per = rows_per_item(f);
+    static const int mult = [] { const char *e = getenv("KV4_M"); return e ? atoi(e) : 2; }();
+    const int64_t most = (int64_t)(f == kGroupForm ? mult : 6) * num_sms, per = rows_per_item(f);
     int chunk = 2048;
     while (chunk > 64) {
         int64_t items = 0;
@@ -1253,6 +1321,7 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     int32_t *req_off = buf + z.off_reqoff, *req_ctx = buf + z.off_reqctx, *req_ws = buf + z.off_reqws;
     int32_t *ri = buf + z.off_ritems, *rj = buf + z.off_rjoins;
     int64_t row = 0, split = 0, part = 0, key = 0, ws = 0, rpart = 0;
+    bool half = true;
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i], o = b.kv_offset[i];
         const Kv4Form form = form_of(b, i);
@@ -1288,6 +1357,7 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
                 ri[1] = (int32_t)std::min<int64_t>(z.rchunk, keys - k * z.rchunk);
                 ri[2] = (int32_t)(req_off[i] + r);
                 ri[3] = (int32_t)rows;
+                half &= rows <= 8;
                 ri[4] = (int32_t)nch;
                 ri[5] = (int32_t)k;
                 ri[6] = (int32_t)rpart;
@@ -1347,6 +1417,7 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     buf[Q_RITEMS] = (int32_t)z.ritems;
     buf[Q_RPARTS] = (int32_t)z.rparts;
     buf[Q_RJOINS] = (int32_t)z.rsplits;
+    buf[Q_RHALF] = half;
     buf[Q_O_RITEMS] = (int32_t)z.off_ritems;
     buf[Q_O_RJOINS] = (int32_t)z.off_rjoins;
     buf[Q_PRE] = (int32_t)z.pre;
@@ -1465,7 +1536,8 @@ cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp,
         const dim3 joins(hp[Q_RJOINS], nh), join_block(32 * kRowsPerItem);
         e = for_dim(d, [&](auto dim) {
             if constexpr (dim() >= 32) {
-                const cudaError_t r = launch_pdl(kv4_rows_mma_kernel<dim()>, grid, block, 0, st, a);
+                const cudaError_t r = hp[Q_RHALF] ? launch_pdl(kv4_rows_mma_kernel<dim(), true>, grid, block, 0, st, a)
+                                                  : launch_pdl(kv4_rows_mma_kernel<dim(), false>, grid, block, 0, st, a);
                 if (r != cudaSuccess || hp[Q_RJOINS] == 0) return r;
                 ++*launches;
                 return launch_pdl(kv4_rows_join_kernel<dim()>, joins, join_block, 0, st, a);
