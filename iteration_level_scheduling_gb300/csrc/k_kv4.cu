@@ -24,7 +24,6 @@
 #include <algorithm>
 #include <cfloat>
 #include <cstring>
-#include <cstdlib>
 #include <type_traits>
 #include <vector>
 
@@ -682,32 +681,63 @@ struct Kv4Block {
     uint32_t kp[2][2];                // keys g, g + 8: groups 2t, 2t + 1
     uint32_t vp[2][2];                // pairs t, t + 4: group g % 4, even and odd slot
 };
-// Where a lane reads; a block ahead is a constant step.
+// A warp's ring of blocks in shared memory, filled by 16-byte asynchronous copies kRing - 1 blocks ahead: the loads in
+// flight cost no registers (with one block ahead in registers, 41 KB per SM, the 64-request case ran at 62 % of the copy
+// rate).  Each block is four pieces that lie together in the layer: 16 rows of K codes, 8 pairs of V codes, their
+// parameters.
+constexpr int kRing = 4;  // (5 blocks: 216 us, 6: 235, 3: 222 at five CTAs per SM)
 template <int D>
-struct Kv4Lane {
+struct Kv4Ring {
     static constexpr int W = D / 32;
-    const uint8_t *kc, *vc;
-    const uint32_t *kp, *vp;
-    __device__ __forceinline__ Kv4Lane(const Kv4View &v, int h, int64_t b, int g, int t) {
-        const int64_t row = (int64_t)h * v.S + b, pair = row >> 1;
-        kc = v.kc + (row + g) * (D / 2) + t * (4 * W);
-        vc = v.vc + (pair + t) * D + g * (4 * W);
-        kp = v.kp + (row + g) * W + (W == 4 ? 2 * (t & 1) : 0);
-        vp = v.vp + ((pair + t) * W + (g & (W - 1))) * 2;
+    uint8_t kc[kRing][16][D / 2];
+    uint8_t vc[kRing][8][D];
+    uint32_t kp[kRing][16][W];
+    uint32_t vp[kRing][8][W][2];
+};
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// Where a lane's copies come from; the warp's next block is a constant step.
+template <int D>
+struct Kv4Source {
+    static constexpr int W = D / 32, kCode = D / 2, kPar = D / 8;  // 16-byte pieces of codes (K or V), of parameters
+    const uint8_t *kc, *vc, *par;
+    __device__ __forceinline__ Kv4Source(const Kv4View &v, int h, int64_t b, int lane) {
+        const int64_t row = (int64_t)h * v.S + b;
+        kc = v.kc + row * (D / 2) + lane * 16;
+        vc = v.vc + row * (D / 2) + lane * 16;
+        par = lane < kPar ? (const uint8_t *)(v.kp + row * W) + lane * 16
+                          : (const uint8_t *)(v.vp + row * W) + (lane - kPar) * 16;
     }
-    __device__ __forceinline__ void load(Kv4Block<D> &x) {
+    __device__ __forceinline__ void copy(Kv4Ring<D> &r, int stage, int lane) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            load_words<W>(kc + i * 4 * D, x.k[i]);
-            load_words<W>(vc + i * 4 * D, x.v[i]);
-            if constexpr (W > 1) load_words<2>(kp + i * 8 * W, x.kp[i]);
-            else x.kp[i][0] = __ldcs(kp + i * 8), x.kp[i][1] = 0u;
-            load_words<2>(vp + i * 8 * W, x.vp[i]);
-        }
-        kc += 8 * D * kKvWarps, vc += 8 * D * kKvWarps;
-        kp += 16 * W * kKvWarps, vp += 16 * W * kKvWarps;
+        for (int c = 0; c < kCode; c += 32)
+            if (kCode >= 32 || lane < kCode) {
+                copy16(&r.kc[stage][0][0] + (c + lane) * 16, kc + c * 16);
+                copy16(&r.vc[stage][0][0] + (c + lane) * 16, vc + c * 16);
+            }
+        if (lane < kPar) copy16((uint8_t *)&r.kp[stage][0][0] + lane * 16, par);
+        else if (lane < 2 * kPar) copy16((uint8_t *)&r.vp[stage][0][0][0] + (lane - kPar) * 16, par);
+        kc += 8 * D * kKvWarps, vc += 8 * D * kKvWarps, par += 64 * W * kKvWarps;
     }
 };
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int W>
+__device__ __forceinline__ void lds_words(const void *p, uint32_t *w) {
+    if constexpr (W == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (W == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
 
 // Nibbles N and N + 4 of a word as fp16: N even, the value c 2^-24 (a subnormal: the bits themselves); N odd, c 2^-20.
 // Two of the four pairs need no shift, and nothing is added that the product would have to lose again.
@@ -728,11 +758,16 @@ __device__ __forceinline__ void kv4_mma_f16(float *c, uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+constexpr int kDecodeCtas = 4;  // per SM (the 64-request case: four 213 us, five 223, six 233)
 template <int D>
-__global__ void __launch_bounds__(kKvThreads, 4) kv4_decode_mma_kernel(const Kv4Attn a) {
+__global__ void __launch_bounds__(kKvThreads, kDecodeCtas) kv4_decode_mma_kernel(const Kv4Attn a) {
     constexpr int W = D / 32;
     constexpr unsigned kAll = 0xffffffffu;
-    __shared__ Kv4Merge<D> sm;
+    __shared__ __align__(16) union {
+        Kv4Ring<D> ring[kKvWarps];
+        Kv4Merge<D> merge;  // once the rings are done with
+    } shared;
+    Kv4Merge<D> &sm = shared.merge;
     pdl_trigger();
     pdl_wait();
     const int4 r0 = reinterpret_cast<const int4 *>(a.items)[2 * blockIdx.x],
@@ -741,10 +776,15 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv4_decode_mma_kernel(const Kv4
     // slots relative to the chunk's first block of 16 (S is a multiple of 16: a block never leaves the layer)
     const int64_t base = r0.x & ~15;
     const int s0 = r0.x & 15, s1 = s0 + r0.y;
-    int b = 16 * warp;
-    Kv4Lane<D> at(a.v, h, base + b, g, t);
-    Kv4Block<D> xa, xb;
-    if (b < s1) at.load(xa);
+    int b = 16 * warp, ahead = b;
+    constexpr int kStep = 16 * kKvWarps;
+    Kv4Ring<D> &ring = shared.ring[warp];
+    Kv4Source<D> src(a.v, h, base + b, lane);
+#pragma unroll
+    for (int n = 0; n < kRing - 1; ++n, ahead += kStep) {
+        if (ahead < s1) src.copy(ring, n, lane);
+        copies_commit();
+    }
 
     // q in fp16, its largest magnitude brought to 2^14 by a power of two (bf16 has fewer bits: nothing is lost down to
     // 2^-28 of that).  Word w of a lane covers components 8 (W t + w) ..; pairs (n, n + 4), those of odd n over 16.
@@ -858,16 +898,24 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv4_decode_mma_kernel(const Kv4
                     code_pair_centred<2>(x.v[1][w]), code_pair_centred<3>(x.v[1][w]), bw[0], bw[1]);
         }
     };
-    constexpr int kStep = 16 * kKvWarps;
-    while (b < s1) {
-        if (b + kStep < s1) at.load(xb);
-        step(xa, b);
-        b += kStep;
-        if (b >= s1) break;
-        if (b + kStep < s1) at.load(xa);
-        step(xb, b);
-        b += kStep;
+    for (int stage = 0; b < s1; b += kStep, ahead += kStep) {
+        copies_wait<kRing - 2>();
+        __syncwarp();  // the block is there for every lane, and every lane is done with the one before
+        if (ahead < s1) src.copy(ring, stage == 0 ? kRing - 1 : stage - 1, lane);
+        copies_commit();
+        Kv4Block<D> x;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            lds_words<W>(&ring.kc[stage][g + 8 * i][t * 4 * W], x.k[i]);
+            lds_words<W>(&ring.vc[stage][t + 4 * i][g * 4 * W], x.v[i]);
+            if constexpr (W > 1) lds_words<2>(&ring.kp[stage][g + 8 * i][W == 4 ? 2 * (t & 1) : 0], x.kp[i]);
+            else x.kp[i][0] = ring.kp[stage][g + 8 * i][0], x.kp[i][1] = 0u;
+            lds_words<2>(&ring.vp[stage][t + 4 * i][g & (W - 1)][0], x.vp[i]);
+        }
+        step(x, b);
+        stage = stage == kRing - 1 ? 0 : stage + 1;
     }
+    __syncthreads();  // the merge takes the rings' place
     // l over the keys of a lane's column; the minima's part over the keys of its group
     l += __shfl_xor_sync(kAll, l, 4);
     l += __shfl_xor_sync(kAll, l, 8);
@@ -1223,14 +1271,15 @@ Kv4Form form_of(const Kv4Batch &b, int i) {
 }
 int rows_per_item(Kv4Form f) { return f == kGroupForm ? kRowsPerItem : 1; }
 
-// Keys per work item: the largest chunk (a power of two, 64 .. 2048 keys) that
-// still gives every SM several blocks of four warps; short chunks cost a join,
-// long ones leave SMs idle.
+// Keys per work item: the largest chunk (a power of two, 128 .. 2048 keys) that
+// still gives every SM three blocks of four warps.  Short chunks cost a join:
+// 16 requests of 300 keys, 40 heads of 128, took 18.2 us at six blocks per SM
+// and 11.5 at three, one of 100 keys 5.1 us in chunks of 64 and 3.2 in one;
+// one of 4000 keys 17.1 us at six, 13.8 at three, 19.7 at one.
 int kv4_chunk(const Kv4Batch &b, Kv4Form f, int num_sms) {
-    static const int mult = [] { const char *e = getenv("KV4_M"); return e ? atoi(e) : 2; }();
-    const int64_t most = (int64_t)(f == kGroupForm ? mult : 6) * num_sms, per = rows_per_item(f);
+    const int64_t most = 3LL * num_sms, per = rows_per_item(f);
     int chunk = 2048;
-    while (chunk > 64) {
+    while (chunk > 128) {
         int64_t items = 0;
         for (int i = 0; i < b.n_req && items * b.n_heads < most; ++i)
             if (form_of(b, i) == f)
