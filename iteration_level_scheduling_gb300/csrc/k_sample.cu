@@ -108,44 +108,84 @@ struct Scale {
     float hi, lo;
 };
 
-// the weight of logit l in a row whose largest is top (l <= top, both finite or l = -inf)
-__device__ __forceinline__ u64 sp_weight_of(float l, float top, const Scale &c, const ExpEntry *table) {
+// Two floats in one instruction (rounded each as the scalar operation is).
+struct F2 {
+    u64 v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void split(F2 x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 sub(F2 a, F2 b) { return fma(b, f2(-1.f), a); }  // (exact product: rounded once)
+
+// The weights of two logits in a row whose largest is top (l <= top).
+__device__ __forceinline__ void sp_weights(float l0, float l1, float top, const Scale &c, const ExpEntry *table, u64 *w) {
+    const F2 l = f2(l0, l1), tp = f2(top);
     // d + e = top - l exactly
-    const float d = __fsub_rn(top, l);
-    const float bb = __fsub_rn(top, d);
-    const float e = __fadd_rn(__fsub_rn(top, __fadd_rn(d, bb)), __fsub_rn(bb, l));
+    const F2 d = sub(tp, l), bb = sub(tp, d);
+    const F2 e = add(sub(tp, add(d, bb)), sub(bb, l));
     // t + tl = (d + e) log2(e) / T
-    const float t0 = __fmul_rn(d, c.hi);
-    const bool some = t0 < 43.5f;  // otherwise 2^-t is below half of the last place
-    const float t = some ? t0 : 0.f;
-    const float tl = __fmaf_rn(d, c.hi, -t) + __fmaf_rn(d, c.lo, __fmul_rn(e, c.hi));
+    const F2 t2 = mul(d, f2(c.hi));
+    float t0, t1;
+    split(t2, t0, t1);
+    const bool some0 = t0 < 43.5f, some1 = t1 < 43.5f;  // otherwise 2^-t is below half of the last place
+    const F2 t = f2(some0 ? t0 : 0.f, some1 ? t1 : 0.f), nt = mul(t, f2(-1.f));
+    const F2 tl = add(fma(d, f2(c.hi), nt), fma(d, f2(c.lo), mul(e, f2(c.hi))));
     // (integers are read off the low bits of a float near 1.5 2^23: conversions run at an eighth of the rate)
     constexpr float kRound = 12582912.f;
-    const float vr = __fmaf_rn(t, 8.f, kRound);
-    const int v = __float_as_int(vr) - __float_as_int(kRound), sh = (v + 7) >> 3;
-    const float g = __fmaf_rn(vr - kRound, 0.125f, -t);  // v / 8 - t: exact
-    const ExpEntry x = table[-v & 7];
+    const F2 vr = fma(t, f2(8.f), f2(kRound));
+    float v0f, v1f;
+    split(vr, v0f, v1f);
+    const int v0 = __float_as_int(v0f) - __float_as_int(kRound), v1 = __float_as_int(v1f) - __float_as_int(kRound);
+    const F2 g = fma(add(vr, f2(-kRound)), f2(0.125f), nt);  // v / 8 - t: exact
+    const ExpEntry x0 = table[-v0 & 7], x1 = table[-v1 & 7];
+    const F2 xh = f2(x0.hi, x1.hi), xl = f2(x0.lo, x1.lo);
     // 2^(g - tl) - 1 = a + b + a^2 / 2 + .. with a + b = (g - tl) ln 2
     constexpr float kL = (float)kLn2, kLl = (float)(kLn2 - (double)(float)kLn2);
-    const float a = __fmul_rn(g, kL);
-    const float b = __fmaf_rn(g, kL, -a) + __fmaf_rn(g, kLl, -tl * kL);
+    const F2 a = mul(g, f2(kL)), na = mul(a, f2(-1.f));
+    const F2 b = add(fma(g, f2(kL), na), fma(g, f2(kLl), mul(tl, f2(-kL))));
     // a^2 / 2 = h + hl; u = a^3 / 6 + .. + a^6 / 720; b times the whole 2^g
-    const float h = __fmul_rn(0.5f * a, a), hl = __fmaf_rn(0.5f * a, a, -h);
-    float q = __fmaf_rn(a, 1.f / 360.f, 1.f / 60.f);
-    q = __fmaf_rn(a, q, 1.f / 12.f);
-    q = __fmaf_rn(a, q, 1.f / 3.f);
+    const F2 ha = mul(a, f2(0.5f)), h = mul(ha, a), hl = fma(ha, a, mul(h, f2(-1.f)));
+    F2 q = fma(a, f2(1.f / 360.f), f2(1.f / 60.f));
+    q = fma(a, q, f2(1.f / 12.f));
+    q = fma(a, q, f2(1.f / 3.f));
     // 2^(j/8) (a + h + rest) = y + yl
-    const float s1 = __fadd_rn(a, h), u = __fmul_rn(h * a, q), rest = u + (__fmaf_rn(b, s1 + u, b) + hl);
-    const float s2 = __fadd_rn(__fsub_rn(a, s1), h) + rest;
-    const float p = __fmul_rn(x.hi, s1), pl = __fmaf_rn(x.hi, s1, -p) + __fmaf_rn(x.hi, s2, x.lo * s1);
-    const float y = __fadd_rn(p, pl), yl = __fadd_rn(__fsub_rn(p, y), pl);
+    const F2 s1 = add(a, h), u = mul(mul(h, a), q), rest = add(u, add(fma(b, add(s1, u), b), hl));
+    const F2 s2 = add(add(sub(a, s1), h), rest);
+    const F2 p = mul(xh, s1), pl = add(fma(xh, s1, mul(p, f2(-1.f))), fma(xh, s2, mul(xl, s1)));
+    const F2 y = add(p, pl), yl = add(sub(p, y), pl);
     // y's leading part on a grid of 2^-21, the rest below it
-    const float r1 = __fmaf_rn(y, 2097152.f, kRound), i1 = r1 - kRound;
-    const float r2 = __fmaf_rn(__fmaf_rn(i1, -1.f / 2097152.f, y) + yl, 8796093022208.f, kRound);
-    const long long m = (long long)x.fixed + (long long)(__float_as_int(r1) - __float_as_int(kRound)) * (1 << (kFrac - 20)) +
-                        (__float_as_int(r2) - __float_as_int(kRound));
-    const u64 w = (((u64)m >> sh) + 1) >> 1;
-    return some ? w : 0ull;  // (no branch: several logits are worked on at a time)
+    const F2 r1 = fma(y, f2(2097152.f), f2(kRound)), i1 = add(r1, f2(-kRound));
+    const F2 r2 = fma(add(fma(i1, f2(-1.f / 2097152.f), y), yl), f2(8796093022208.f), f2(kRound));
+    float r10, r11, r20, r21;
+    split(r1, r10, r11);
+    split(r2, r20, r21);
+    auto fixed = [&](u64 base, float hi, float lo, int v, bool some) {
+        const long long m = (long long)base + (long long)(__float_as_int(hi) - __float_as_int(kRound)) * (1 << (kFrac - 20)) +
+                            (__float_as_int(lo) - __float_as_int(kRound));
+        const u64 r = (((u64)m >> ((v + 7) >> 3)) + 1) >> 1;
+        return some ? r : 0ull;  // (no branch: several logits are worked on at a time)
+    };
+    w[0] = fixed(x0.fixed, r10, r20, v0, some0);
+    w[1] = fixed(x1.fixed, r11, r21, v1, some1);
 }
 
 template <typename V>
@@ -398,7 +438,16 @@ __global__ void __launch_bounds__(kSpThreads, 1) sample_kernel(const SampleArgs 
         cs.lo = __fdiv_rn(__fmaf_rn(-cs.hi, temp, kE) + kEl, temp);
         if (!(fabsf(cs.lo) < 1e30f)) cs.lo = 0.f;  // (a subnormal T: only the largest logits keep weight)
     }
-    auto weight = [&](float l) -> u64 { return l == top ? 1ull << kFrac : sp_weight_of(l, top, cs, sm.exp); };
+    auto weights = [&](float l0, float l1, u64 *w) {
+        sp_weights(l0, l1, top, cs, sm.exp, w);
+        if (l0 == top) w[0] = 1ull << kFrac;  // (top may be +inf)
+        if (l1 == top) w[1] = 1ull << kFrac;
+    };
+    auto weight = [&](float l) {
+        u64 w[2];
+        weights(l, l, w);
+        return w[0];
+    };
     // The bin of a logit: octaves below the largest, kBins of them over 43.5 (monotone in the logit;
     // the last bin also takes everything without weight)
     auto bin_of = [&](float l) {
@@ -409,13 +458,13 @@ __global__ void __launch_bounds__(kSpThreads, 1) sample_kernel(const SampleArgs 
     // a logit that none of bins 0 .. b is below (one bin of slack for the roundings)
     auto low_of = [&](int b) { return top - (float)(b + 2) * (float)(43.5 / kBins) * 1.000001f / cs.hi; };
     SampleSmem &root = peer(0);
-    // f(l, on) for 32 logits above the cut at a time (all lanes; `on`: this lane has one), g(l) for every logit, over
-    // a warp's contiguous stretch of ids; the logits above are queued so that few of them cost little.
+    // f(l0, l1, on0, on1) for 64 logits above the cut at a time (all lanes; on: this lane has that one), g(l) for every
+    // logit, over a warp's contiguous stretch of ids; the logits above are queued so that few of them cost little.
     const int per_warp = (n + 4 * kSpThreads - 1) / (4 * kSpThreads) * 128;
     const int i0 = min(n, warp * per_warp), i1 = min(n, i0 + per_warp);
     auto each_above = [&](float above, auto f, auto g) {
         constexpr int kQueue = 2 * kList / kSpWarps;  // floats per warp
-        static_assert(kQueue >= 31 + 64, "what two ballots add to a rest of 31");
+        static_assert(kQueue >= 63 + 64, "what two ballots add to a rest of 63");
         float *queue = reinterpret_cast<float *>(sm.list) + warp * kQueue;
         int held = 0;
         for (int i = i0 + 4 * lane; i - 4 * lane < i1; i += 128) {
@@ -438,17 +487,17 @@ __global__ void __launch_bounds__(kSpThreads, 1) sample_kernel(const SampleArgs 
                 const uint32_t mask = __ballot_sync(kAll, l[e] > above);
                 if (l[e] > above) queue[held + __popc(mask & ((1u << lane) - 1u))] = l[e];
                 held += __popc(mask);
-                if (e & 1) {
+                if ((e & 1) && held >= 64) {
                     __syncwarp();
-                    while (held >= 32) {
-                        held -= 32;
-                        f(queue[held + lane], true);
-                    }
+                    held -= 64;
+                    f(queue[held + lane], queue[held + 32 + lane], true, true);
                     __syncwarp();
                 }
             }
         }
-        if (held > 0) f(lane < held ? queue[lane] : above, lane < held);
+        __syncwarp();
+        const bool on0 = lane < held, on1 = lane + 32 < held;
+        if (held > 0) f(on0 ? queue[lane] : above, on1 ? queue[lane + 32] : above, on0, on1);
     };
 
     // the mass that a prefix has to reach: p times the whole, rounded up, at least one
@@ -483,16 +532,17 @@ __global__ void __launch_bounds__(kSpThreads, 1) sample_kernel(const SampleArgs 
         if (by_mass && cut != -INFINITY)
             each_above(
                 cut,
-                [&](float l, bool on) {
-                    const u64 w = weight(l);
-                    if (on) put(l, w);
+                [&](float l0, float l1, bool on0, bool on1) {
+                    u64 w[2];
+                    weights(l0, l1, w);
+                    if (on0) put(l0, w[0]);
+                    if (on1) put(l1, w[1]);
                 },
                 [](float) {});
         else if (by_mass)
             each4([&](int, const float *l) {
                 u64 w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = weight(l[e]);
+                weights(l[0], l[1], w), weights(l[2], l[3], w + 2);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) put(l[e], w[e]);
             });
@@ -559,10 +609,10 @@ __global__ void __launch_bounds__(kSpThreads, 1) sample_kernel(const SampleArgs 
         __syncthreads();
         each4([&](int i, const float *l) {
             if (!(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= low)) return;
+            if (*const_cast<volatile uint32_t *>(&sm.sh.gathered) > kList) return;  // too many: only that counts
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if (!(l[e] > cut) || !take(l[e])) continue;
-                if (*const_cast<volatile uint32_t *>(&sm.sh.gathered) > kList) continue;  // too many: only that counts
                 const uint32_t j = atomicAdd(&sm.sh.gathered, 1u);
                 if (j < kList) sm.list[j] = (u64)sp_key(l[e]) << 32 | (uint32_t) ~(first + i + e);
             }
@@ -704,10 +754,12 @@ __global__ void __launch_bounds__(kSpThreads, 1) sample_kernel(const SampleArgs 
         by_count = sm.sh.found && bin != kBins - 1;
         if (!by_count) meet();
         if (by_count) {
-            const int m = collect(low_of(bin), [&](float l) { return bin_of(l) <= bin; });
-            if (m <= kList) {
-                if (rank == 0) finish(m, k, ~0ull, p < 1.f);
-                return;
+            if (k <= kList) {
+                const int m = collect(low_of(bin), [&](float l) { return bin_of(l) <= bin; });
+                if (m <= kList) {
+                    if (rank == 0) finish(m, k, ~0ull, p < 1.f);
+                    return;
+                }
             }
             settle(false, bin, want);
         }
@@ -738,9 +790,10 @@ __global__ void __launch_bounds__(kSpThreads, 1) sample_kernel(const SampleArgs 
     if (tied) {
         each_above(
             cut,
-            [&](float l, bool on) {
-                const u64 w = weight(l);
-                s += on && w >= least ? w : 0ull;
+            [&](float l0, float l1, bool on0, bool on1) {
+                u64 w[2];
+                weights(l0, l1, w);
+                s += (on0 && w[0] >= least ? w[0] : 0ull) + (on1 && w[1] >= least ? w[1] : 0ull);
             },
             [&](float l) { c += l == cut; });
     } else {
@@ -753,11 +806,10 @@ __global__ void __launch_bounds__(kSpThreads, 1) sample_kernel(const SampleArgs 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) l[e] = i + e < i1 ? at(i + e) : -INFINITY;
             }
+            u64 w[4];
+            weights(l[0], l[1], w), weights(l[2], l[3], w + 2);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const u64 w = weight(l[e]);
-                s += w >= least ? w : 0ull;
-            }
+            for (int e = 0; e < 4; ++e) s += w[e] >= least ? w[e] : 0ull;
         }
     }
     s = warp_add(s), c = warp_add(c);
