@@ -311,7 +311,7 @@ __device__ __forceinline__ void block_sort(V *v, int n, V pad) {
 // Held: the row is kept in shared memory; otherwise (rows of more ids than a cluster holds) every pass reads the
 // logits again.
 template <typename T, bool Held>
-__global__ void __launch_bounds__(kSpThreads, 1) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t sp_raw[];
     SampleSmem &sm = *reinterpret_cast<SampleSmem *>(sp_raw);
     float *val = reinterpret_cast<float *>(sp_raw + sizeof(SampleSmem));
@@ -872,11 +872,12 @@ cudaError_t sample_rows(int dtype_bf16, const void *logits, int64_t ld, int n_ro
                         int32_t *out, unsigned *err, int num_sms, cudaStream_t st) {
     if (n_rows <= 0) return cudaSuccess;
     constexpr int kMaxPer = (227 * 1024 - (int)sizeof(SampleSmem)) / 4 / kSpThreads * kSpThreads;
-    // CTAs per row: enough to hold it; two for long rows (192 mixed rows of 50257: 106 us, with one 124, with four
-    // 122), more while SMs would stand idle (one row: one 19.1, two 14.7, four 12.2, eight 12.7 us).
+    // CTAs per row: enough that two of them share an SM (192 mixed rows of 50257: four per row 83 us, two, which leave
+    // an SM to one CTA, 101), more while SMs would stand idle (one row: one 19.1, two 14.7, four 12.2, eight 12.7 us).
+    constexpr int kPairPer = (113 * 1024 - (int)sizeof(SampleSmem)) / 4;
     int C = 1;
-    while (C < kMaxCluster && (V + C - 1) / C > kMaxPer) C *= 2;
-    while (C < 4 && V / C > 8192 && (C == 1 || (int64_t)n_rows * C * 2 <= num_sms)) C *= 2;
+    while (C < kMaxCluster && (V + C - 1) / C > kPairPer) C *= 2;
+    while (C < 4 && V / C > 8192 && (int64_t)n_rows * C * 2 <= num_sms) C *= 2;
     const int per = ((V + C - 1) / C + 3) / 4 * 4;
     const bool held = per <= kMaxPer;
     SampleArgs a{logits, ld, V, per, temperature, top_p, min_p, uniform, top_k, out, err};
