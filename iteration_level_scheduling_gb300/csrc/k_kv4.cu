@@ -532,54 +532,133 @@ __device__ __forceinline__ void kv4_finish(const Kv4Attn &a, Kv4Merge<D> &sm, co
                                                (size_t)a.n_heads * (D + 2), nch, tid));
 }
 
-// Any type and head_dim, fp32 arithmetic.  A warp takes 32 slots at a time:
-// for the scores a lane owns a key and walks its components against q in
-// shared memory; for the values a lane owns four components and walks the
-// keys, two per word.
+// W consecutive words
+template <int W>
+__device__ __forceinline__ void get_words(const void *p, uint32_t *w) {
+    if constexpr (W == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (W == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
+
+// W consecutive words, streamed
+template <int W>
+__device__ __forceinline__ void load_words(const void *p, uint32_t *w) {
+    if constexpr (W == 4) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (W == 2) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = __ldcs(reinterpret_cast<const uint32_t *>(p));
+    }
+}
+
+// Any type and head_dim, fp32 arithmetic (fp32 models; head_dim 16).  A warp
+// takes 32 slots at a time: for the scores a lane owns a key and walks its
+// components against q in shared memory; for the values a lane owns four
+// components and walks the keys, two per word.  A code is used as the fp32
+// subnormal that its bits are in place (nibble n of a word: c 2^(4n - 149), for
+// n <= 4), times a factor that carries the power of two: an AND instead of a
+// shift, an AND and a conversion at an eighth of the rate.  Bound by latency and
+// issue: 64 requests of 4000 keys, 12 heads of 64, fp32: 135 us (277 with the
+// conversions; 162 at four CTAs per SM, 207 without the prefetch).
+__device__ __forceinline__ float nibble_bits(uint32_t w, int n) { return __uint_as_float(w & (15u << (4 * n))); }
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kKvThreads) kv4_decode_kernel(const Kv4Attn a) {
-    constexpr int G = D / 32 > 0 ? D / 32 : 1, GS = D / G;
+__global__ void __launch_bounds__(kKvThreads, 6) kv4_decode_kernel(const Kv4Attn a) {
+    constexpr int G = D / 32 > 0 ? D / 32 : 1, GS = D / G, GW = GS / 8;  // words of a group and key
     constexpr int LP = D / 4, PP = 32 / LP;  // lanes per pair of keys, pairs per step
     __shared__ Kv4Merge<D> sm;
-    __shared__ float q[D];
-    __shared__ float qs[G];
+    __shared__ __align__(16) float q[D];
+    __shared__ float qs[G], big[kKvWarps];
     pdl_trigger();
     pdl_wait();
     const int4 r0 = reinterpret_cast<const int4 *>(a.items)[2 * blockIdx.x],
                r1 = reinterpret_cast<const int4 *>(a.items)[2 * blockIdx.x + 1];
     const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x < D)
-        q[threadIdx.x] = Elem<T>::to_f(((const T *)a.qkv)[(size_t)r0.z * 3 * a.H + h * D + threadIdx.x]) * a.scale_log2;
-    __syncthreads();
-    if (threadIdx.x < G) {
-        float s = 0.f;
-        for (int i = 0; i < GS; ++i) s += q[threadIdx.x * GS + i];
-        qs[threadIdx.x] = s;
+    // q brought to 2^14 by a power of two and on to 2^100, by nibble (5 .. 7 are used two places to the right)
+    float k_unit;
+    {
+        const float x = threadIdx.x < D
+                            ? Elem<T>::to_f(((const T *)a.qkv)[(size_t)r0.z * 3 * a.H + h * D + threadIdx.x]) : 0.f;
+        float m = fabsf(x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) big[warp] = m;
+        if (threadIdx.x < D) q[threadIdx.x] = x;
+        __syncthreads();
+        m = 0.f;
+#pragma unroll
+        for (int w = 0; w < kKvWarps; ++w) m = max_nan(m, big[w]);
+        if (threadIdx.x < G) {
+            float s = 0.f;
+            for (int i = 0; i < GS; ++i) s += q[threadIdx.x * GS + i];
+            qs[threadIdx.x] = s * a.scale_log2;
+        }
+        const float inv = kv4_inverse_scale(m);
+        const int n = threadIdx.x & 7, place = n < 5 ? n : n - 3;
+        __syncthreads();
+        if (threadIdx.x < D) q[threadIdx.x] = x * (1.f / inv) * __uint_as_float((127u + 86u - 4u * place) << 23);
+        k_unit = inv * a.scale_log2;  // of the scores' sums, with 2^(149 - 86) in two steps below
+        __syncthreads();
     }
-    __syncthreads();
     const int64_t s0 = r0.x, s1 = s0 + r0.y;
     const int sub = lane % LP, grp = lane / LP;
-    float m = kLow, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    float m = kLow, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f}, zero = 0.f;
     for (int64_t b = (s0 & ~int64_t(1)) + 32 * warp; b < s1; b += 32 * kKvWarps) {
         const int64_t slot = b + lane;
         const bool valid = slot >= s0 && slot < s1;
+        if (b + 32 * kKvWarps + 32 <= s1) {  // the warp's next 32 slots into L1, line by line
+            constexpr int kCode = 32 * D / 2 / 128, kPar = 32 * G * 4 / 128;
+            const int64_t next = (int64_t)h * a.v.S + b + 32 * kKvWarps;
+#pragma unroll
+            for (int c = 0; c < 2 * (kCode + kPar); c += 32) {
+                const int n = c + lane;
+                const uint8_t *at = n < kCode              ? a.v.kc + next * (D / 2) + n * 128
+                                    : n < 2 * kCode        ? a.v.vc + next * (D / 2) + (n - kCode) * 128
+                                    : n < 2 * kCode + kPar ? (const uint8_t *)(a.v.kp + next * G) + (n - 2 * kCode) * 128
+                                                           : (const uint8_t *)(a.v.vp + next * G) + (n - 2 * kCode - kPar) * 128;
+                if (n < 2 * (kCode + kPar)) prefetch_l1(at);
+            }
+        }
         float sc = kLow;
         if (valid) {
             const int64_t row = (int64_t)h * a.v.S + slot;
+            uint32_t w[G * GW];
+            const uint32_t *kc = reinterpret_cast<const uint32_t *>(a.v.kc + row * (D / 2));
+            if constexpr (D >= 32) {
+#pragma unroll
+                for (int g = 0; g < G; ++g) get_words<4>(kc + 4 * g, w + 4 * g);
+            } else {
+                get_words<2>(kc, w);
+            }
             sc = 0.f;
+            float acc = 0.f;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 const uint32_t p = a.v.kp[row * G + g];
-                float acc = 0.f;
+                float e[2] = {0.f, 0.f};
 #pragma unroll
-                for (int w = 0; w < GS / 8; ++w) {
-                    const uint32_t x =
-                        *reinterpret_cast<const uint32_t *>(a.v.kc + row * (D / 2) + g * (GS / 2) + w * 4);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) acc = fmaf(q[g * GS + w * 8 + k], (float)((x >> (4 * k)) & 15u), acc);
+                for (int x = 0; x < GW; ++x) {
+                    const float4 qa = *reinterpret_cast<const float4 *>(&q[(g * GW + x) * 8]),
+                                 qb = *reinterpret_cast<const float4 *>(&q[(g * GW + x) * 8 + 4]);
+                    const uint32_t lo = w[g * GW + x], hi = lo >> 12;
+                    e[0] = fmaf(qa.x, nibble_bits(lo, 0), e[0]), e[1] = fmaf(qa.y, nibble_bits(lo, 1), e[1]);
+                    e[0] = fmaf(qa.z, nibble_bits(lo, 2), e[0]), e[1] = fmaf(qa.w, nibble_bits(lo, 3), e[1]);
+                    e[0] = fmaf(qb.x, nibble_bits(lo, 4), e[0]), e[1] = fmaf(qb.y, nibble_bits(hi, 2), e[1]);
+                    e[0] = fmaf(qb.z, nibble_bits(hi, 3), e[0]), e[1] = fmaf(qb.w, nibble_bits(hi, 4), e[1]);
                 }
-                sc += bf_lo(p) * acc + bf_hi(p) * qs[g];
+                acc = fmaf(bf_lo(p), (e[0] + e[1]) * __uint_as_float((127u + 63u) << 23), acc);
+                sc = fmaf(bf_hi(p), qs[g], sc);
             }
+            sc = fmaf(acc, k_unit, sc);
         }
         float mx = sc;
 #pragma unroll
@@ -589,6 +668,7 @@ __global__ void __launch_bounds__(kKvThreads) kv4_decode_kernel(const Kv4Attn a)
         m = mx;
         const float p = valid ? exp2f(sc - m) : 0.f;
         l = l * corr + p;
+        zero *= corr;
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] *= corr;
 #pragma unroll 4
@@ -597,27 +677,39 @@ __global__ void __launch_bounds__(kKvThreads) kv4_decode_kernel(const Kv4Attn a)
             const float pe = __shfl_sync(0xffffffffu, p, 2 * pr), po = __shfl_sync(0xffffffffu, p, 2 * pr + 1);
             const int64_t se = b + 2 * pr;
             const bool ve = se >= s0 && se < s1, vo = se + 1 >= s0 && se + 1 < s1;
-            if (!ve && !vo) continue;
-            const int64_t pair = (int64_t)h * (a.v.S / 2) + (se >> 1);
-            const uint32_t x = *reinterpret_cast<const uint32_t *>(a.v.vc + (pair * (D / 4) + sub) * 4);
-            const uint2 pp = *reinterpret_cast<const uint2 *>(a.v.vp + (pair * G + sub * 4 / GS) * 2);
-            // (an unused slot's parameters may be anything)
-            const float ws = ve ? pe * bf_lo(pp.x) : 0.f, wm = ve ? pe * bf_hi(pp.x) : 0.f;
-            const float xs = vo ? po * bf_lo(pp.y) : 0.f, xm = vo ? po * bf_hi(pp.y) : 0.f;
+            uint32_t x = 0;
+            uint2 pp = make_uint2(0, 0);
+            if (ve || vo) {
+                const int64_t pair = (int64_t)h * (a.v.S / 2) + (se >> 1);
+                x = reinterpret_cast<const uint32_t *>(a.v.vc + pair * D)[sub];
+                pp = *reinterpret_cast<const uint2 *>(a.v.vp + (pair * G + sub * 4 / GS) * 2);
+            }
+            // around code 8, as the sums run over all keys; an unused slot's parameters may be anything
+            constexpr float kUp = 1.2089258196146292e24f;  // 2^80
+            const float we = ve ? pe * bf_lo(pp.x) : 0.f, wo = vo ? po * bf_lo(pp.y) : 0.f;
+            zero += (ve ? pe * fmaf(8.f, bf_lo(pp.x), bf_hi(pp.x)) : 0.f) +
+                    (vo ? po * fmaf(8.f, bf_lo(pp.y), bf_hi(pp.y)) : 0.f);
+            const float ue = we * kUp, uo = wo * kUp;
+            const uint32_t y = x >> 16;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                o[k] += fmaf(ws, (float)((x >> (4 * k)) & 15u), wm) + fmaf(xs, (float)((x >> (16 + 4 * k)) & 15u), xm);
+            for (int k = 0; k < 4; ++k) {
+                const float eight = __uint_as_float(8u << (4 * k));
+                o[k] = fmaf(ue, nibble_bits(x, k) - eight, fmaf(uo, nibble_bits(y, k) - eight, o[k]));
+            }
         }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
 #pragma unroll
-    for (int off = LP; off < 32; off <<= 1)
+    for (int off = LP; off < 32; off <<= 1) {
+        zero += __shfl_xor_sync(0xffffffffu, zero, off);
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] += __shfl_xor_sync(0xffffffffu, o[k], off);
+    }
     if (grp == 0)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sm.o[warp][4 * sub + k] = o[k];
+        for (int k = 0; k < 4; ++k)  // 2^(149 - 80 - 4k)
+            sm.o[warp][4 * sub + k] = fmaf(o[k], __uint_as_float((127u + 69u - 4u * k) << 23), zero);
     if (lane == 0) sm.m[warp] = m, sm.l[warp] = l;
     kv4_finish<T, D>(a, sm, r0, r1, h);
 }
@@ -658,20 +750,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&r);
 }
-// W consecutive words, streamed
-template <int W>
-__device__ __forceinline__ void load_words(const void *p, uint32_t *w) {
-    if constexpr (W == 4) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else if constexpr (W == 2) {
-        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
-        w[0] = v.x, w[1] = v.y;
-    } else {
-        w[0] = __ldcs(reinterpret_cast<const uint32_t *>(p));
-    }
-}
-
 // One block of 16 slots as a lane (g, t) = (lane / 4, lane % 4) of a warp holds it.
 template <int D>
 struct Kv4Block {
@@ -726,19 +804,6 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-template <int W>
-__device__ __forceinline__ void lds_words(const void *p, uint32_t *w) {
-    if constexpr (W == 4) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else if constexpr (W == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        w[0] = v.x, w[1] = v.y;
-    } else {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
-    }
-}
-
 // Nibbles N and N + 4 of a word as fp16: N even, the value c 2^-24 (a subnormal: the bits themselves); N odd, c 2^-20.
 // Two of the four pairs need no shift, and nothing is added that the product would have to lose again.
 template <int N>
@@ -906,11 +971,11 @@ __global__ void __launch_bounds__(kKvThreads, kDecodeCtas) kv4_decode_mma_kernel
         Kv4Block<D> x;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            lds_words<W>(&ring.kc[stage][g + 8 * i][t * 4 * W], x.k[i]);
-            lds_words<W>(&ring.vc[stage][t + 4 * i][g * 4 * W], x.v[i]);
-            if constexpr (W > 1) lds_words<2>(&ring.kp[stage][g + 8 * i][W == 4 ? 2 * (t & 1) : 0], x.kp[i]);
+            get_words<W>(&ring.kc[stage][g + 8 * i][t * 4 * W], x.k[i]);
+            get_words<W>(&ring.vc[stage][t + 4 * i][g * 4 * W], x.v[i]);
+            if constexpr (W > 1) get_words<2>(&ring.kp[stage][g + 8 * i][W == 4 ? 2 * (t & 1) : 0], x.kp[i]);
             else x.kp[i][0] = ring.kp[stage][g + 8 * i][0], x.kp[i][1] = 0u;
-            lds_words<2>(&ring.vp[stage][t + 4 * i][g & (W - 1)][0], x.vp[i]);
+            get_words<2>(&ring.vp[stage][t + 4 * i][g & (W - 1)][0], x.vp[i]);
         }
         step(x, b);
         stage = stage == kRing - 1 ? 0 : stage + 1;
