@@ -446,7 +446,7 @@ struct Kv4Attn {
     Kv4View v;
     int H, n_heads;
     float scale_log2;
-    const int32_t *items;  // 8 words: first slot, keys, row, chunks of the row, this chunk, the row's first partial, its counter
+    const int32_t *items;  // block = item * n_heads + head; 8 words: first slot, keys, row, chunks of the row, this chunk, the row's first partial, its counter
     int *counters;         // [row counter][head], zero between launches
     float *part;           // [partial][head][D + 2]
     const int32_t *row_items;  // the same for groups of rows (kv4_rows_mma_kernel), 12 words an item
@@ -580,9 +580,10 @@ __global__ void __launch_bounds__(kKvThreads, 6) kv4_decode_kernel(const Kv4Attn
     __shared__ float qs[G], big[kKvWarps];
     pdl_trigger();
     pdl_wait();
-    const int4 r0 = reinterpret_cast<const int4 *>(a.items)[2 * blockIdx.x],
-               r1 = reinterpret_cast<const int4 *>(a.items)[2 * blockIdx.x + 1];
-    const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int item = blockIdx.x / a.n_heads, h = blockIdx.x - item * a.n_heads;
+    const int4 r0 = reinterpret_cast<const int4 *>(a.items)[2 * item],
+               r1 = reinterpret_cast<const int4 *>(a.items)[2 * item + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // q brought to 2^14 by a power of two and on to 2^100, by nibble (5 .. 7 are used two places to the right)
     float k_unit;
     {
@@ -835,9 +836,10 @@ __global__ void __launch_bounds__(kKvThreads, kDecodeCtas) kv4_decode_mma_kernel
     Kv4Merge<D> &sm = shared.merge;
     pdl_trigger();
     pdl_wait();
-    const int4 r0 = reinterpret_cast<const int4 *>(a.items)[2 * blockIdx.x],
-               r1 = reinterpret_cast<const int4 *>(a.items)[2 * blockIdx.x + 1];
-    const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int item = blockIdx.x / a.n_heads, h = blockIdx.x - item * a.n_heads;
+    const int4 r0 = reinterpret_cast<const int4 *>(a.items)[2 * item],
+               r1 = reinterpret_cast<const int4 *>(a.items)[2 * item + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // slots relative to the chunk's first block of 16 (S is a multiple of 16: a block never leaves the layer)
     const int64_t base = r0.x & ~15;
     const int s0 = r0.x & 15, s1 = s0 + r0.y;
@@ -1034,9 +1036,10 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
     pdl_trigger();
     pdl_wait();
     // first slot, keys, first row, rows | the rows' chunks, this chunk, first partial, - | keys row 0 sees
-    const int4 *rec = reinterpret_cast<const int4 *>(a.row_items) + 3 * blockIdx.x;
+    const int item = blockIdx.x / a.n_heads, h = blockIdx.x - item * a.n_heads;
+    const int4 *rec = reinterpret_cast<const int4 *>(a.row_items) + 3 * item;
     const int4 r0 = rec[0], r1 = rec[1], r2 = rec[2];
-    const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int64_t s0 = r0.x, s1 = s0 + r0.y;
     const int rows = r0.w;
 
@@ -1255,7 +1258,7 @@ __global__ void __launch_bounds__(32 * kRowsPerItem) kv4_rows_join_kernel(const 
 
 template <typename T>
 cudaError_t launch_decode(const Kv4Attn &a, int d, int n_items, cudaStream_t st) {
-    const dim3 grid(n_items, a.n_heads), block(kKvThreads);
+    const dim3 grid((unsigned)n_items * a.n_heads), block(kKvThreads);
     if constexpr (std::is_same<T, bf16>::value) {
         if (d == 32) return launch_pdl(kv4_decode_mma_kernel<32>, grid, block, 0, st, a);
         if (d == 64) return launch_pdl(kv4_decode_mma_kernel<64>, grid, block, 0, st, a);
@@ -1408,7 +1411,7 @@ bool kv4_sizes(const Kv4Batch &b, int num_sms, Kv4Sizes *z) {
     z->off_reqws = w, w = up4(w + b.n_req);
     z->total = w;
     // 32-bit table entries and grid sizes
-    return w <= INT32_MAX && z->keys <= INT32_MAX && z->pre_tiles * b.n_heads <= INT32_MAX &&
+    return w <= INT32_MAX && z->keys <= INT32_MAX && (z->items + z->ritems) * b.n_heads <= INT32_MAX && z->pre_tiles * b.n_heads <= INT32_MAX &&
            (z->pre + z->rows) * b.n_heads <= INT32_MAX;
 }
 
@@ -1425,6 +1428,18 @@ int64_t kv4_plan_words(const Kv4Batch &b, int num_sms) {
     Kv4Sizes z;
     return kv4_sizes(b, num_sms, &z) ? z.total : -1;
 }
+
+namespace {
+// Order records of N words by their second, largest first (stable).
+template <int N>
+void longest_first(int32_t *rec, int64_t n) {
+    struct R {
+        int32_t w[N];
+    };
+    R *r = reinterpret_cast<R *>(rec);
+    std::stable_sort(r, r + n, [](const R &x, const R &y) { return x.w[1] > y.w[1]; });
+}
+}  // namespace
 
 bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     Kv4Sizes z;
@@ -1502,6 +1517,9 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
         }
     }
     req_off[b.n_req] = (int32_t)row;
+    // blocks are dealt in order, all heads of an item after one another: the longest first, so that none starts late
+    longest_first<8>(buf + z.off_items, z.items);
+    longest_first<12>(buf + z.off_ritems, z.ritems);
     prefill_order(buf + z.off_pretiles, (int)z.pre_tiles, req_off, req_ctx);
     // slots written by two rows
     std::vector<std::pair<int64_t, int64_t>> w((size_t)b.n_req);
@@ -1646,7 +1664,7 @@ cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp,
         ++*launches;
     }
     if (e == cudaSuccess && hp[Q_RITEMS] > 0) {
-        const dim3 grid(hp[Q_RITEMS], nh), block(kKvThreads);
+        const dim3 grid((unsigned)hp[Q_RITEMS] * nh), block(kKvThreads);
         const dim3 joins(hp[Q_RJOINS], nh), join_block(32 * kRowsPerItem);
         e = for_dim(d, [&](auto dim) {
             if constexpr (dim() >= 32) {
