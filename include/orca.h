@@ -405,7 +405,7 @@ int orca_op_kv4_attention(orca_engine *eng, const void *qkv, const void *kv4_lay
 /* sampling                                                                  */
 /* ------------------------------------------------------------------------ */
 /* One token per row of logits [n_rows][ld] (dtype elements, the first `vocab`
- * of each row used; vocab <= 2^20, ld >= vocab), from one given uniform number
+ * of each row used; vocab <= 2^20, ld >= vocab, n_rows <= 2^24), from one given uniform number
  * per row.  Parameters are DEVICE arrays of n_rows entries; a null array means
  * its default.  With m the row's largest logit and w_i = exp((l_i - m) / T):
  *   temperature T (1)  0 takes the largest logit (lowest id on ties), ignoring the rest
@@ -425,6 +425,15 @@ int orca_op_kv4_attention(orca_engine *eng, const void *qkv, const void *kv4_lay
 int orca_op_sample(orca_engine *eng, int32_t dtype, const void *logits, int32_t n_rows, int32_t vocab, int64_t ld,
                    const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
                    const float *uniform, int32_t *out_tokens);
+/* The same for the requests of the engine's last iteration (their order, its
+ * kept logits): the sampled tokens replace the greedy ones, so that a negative
+ * entry of the next iteration's tokens (see orca_batch) refers to them, and are
+ * copied to dev_out_next (device, may be NULL).  A caller that samples passes
+ * them, not the iteration's own, to orca_sched_complete.  A row without a token
+ * (-1) must not be referred to.  Asynchronous; may follow orca_run_planned.
+ * Errors: INVALID (also before any iteration, or vocab > 2^20), CUDA. */
+int orca_sample_last(orca_engine *eng, const float *temperature, const int32_t *top_k, const float *top_p,
+                     const float *min_p, const float *uniform, int32_t *dev_out_next);
 
 /* ------------------------------------------------------------------------ */
 /* iteration-level scheduler ([houmin] 3.1.1, [0h-n0] scheduler algorithm,    */

@@ -1117,7 +1117,7 @@ int orca_op_kv4_attention(orca_engine *E, const void *qkv, const void *kv4_layer
 int orca_op_sample(orca_engine *E, int32_t dtype, const void *logits, int32_t n_rows, int32_t vocab, int64_t ld,
                    const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
                    const float *uniform, int32_t *out_tokens) {
-    if (!E || !logits || !uniform || !out_tokens || n_rows < 0 || vocab < 1 || vocab > (1 << 20) || ld < vocab ||
+    if (!E || !logits || !uniform || !out_tokens || n_rows < 0 || n_rows > (1 << 24) || vocab < 1 || vocab > (1 << 20) || ld < vocab ||
         (dtype != ORCA_DTYPE_FP32 && dtype != ORCA_DTYPE_BF16) ||
         !aligned(logits, dtype == ORCA_DTYPE_BF16 ? 2 : 4) || !aligned(temperature, 4) || !aligned(top_k, 4) ||
         !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(uniform, 4) || !aligned(out_tokens, 4) || !on_device(E))
@@ -1125,6 +1125,18 @@ int orca_op_sample(orca_engine *E, int32_t dtype, const void *logits, int32_t n_
     if (n_rows == 0) return ORCA_OK;
     return launched(E, sample_rows(dtype == ORCA_DTYPE_BF16, logits, ld, n_rows, vocab, temperature, top_k, top_p,
                                    min_p, uniform, out_tokens, E->d_err, E->num_sms, E->st));
+}
+
+int orca_sample_last(orca_engine *E, const float *temperature, const int32_t *top_k, const float *top_p,
+                     const float *min_p, const float *uniform, int32_t *dev_out_next) {
+    if (!E || !uniform || E->last_n < 1 || E->V > (1 << 20) || !aligned(temperature, 4) || !aligned(top_k, 4) ||
+        !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(uniform, 4) || !aligned(dev_out_next, 4) || !on_device(E))
+        return ORCA_ERR_INVALID;
+    cudaError_t e = sample_rows(0, E->logits, E->V, E->last_n, E->V, temperature, top_k, top_p, min_p, uniform, E->next,
+                                E->d_err, E->num_sms, E->st);
+    if (e == cudaSuccess && dev_out_next)
+        e = cudaMemcpyAsync(dev_out_next, E->next, (size_t)E->last_n * 4, cudaMemcpyDeviceToDevice, E->st);
+    return launched(E, e);
 }
 
 }  // extern "C"

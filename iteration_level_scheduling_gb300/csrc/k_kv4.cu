@@ -565,7 +565,8 @@ __device__ __forceinline__ void load_words(const void *p, uint32_t *w) {
 // components against q in shared memory; for the values a lane owns four
 // components and walks the keys, two per word.  A code is used as the fp32
 // subnormal that its bits are in place (nibble n of a word: c 2^(4n - 149), for
-// n <= 4), times a factor that carries the power of two: an AND instead of a
+// n <= 4), times a factor that carries the power of two -- q's, scaled -- or, for
+// the values, added to 2^23 and taken around code 8: an AND or two instead of a
 // shift, an AND and a conversion at an eighth of the rate.  Bound by latency and
 // issue: 64 requests of 4000 keys, 12 heads of 64, fp32: 135 us (277 with the
 // conversions; 162 at four CTAs per SM, 207 without the prefetch).
@@ -686,16 +687,17 @@ __global__ void __launch_bounds__(kKvThreads, 6) kv4_decode_kernel(const Kv4Attn
                 pp = *reinterpret_cast<const uint2 *>(a.v.vp + (pair * G + sub * 4 / GS) * 2);
             }
             // around code 8, as the sums run over all keys; an unused slot's parameters may be anything
-            constexpr float kUp = 1.2089258196146292e24f;  // 2^80
             const float we = ve ? pe * bf_lo(pp.x) : 0.f, wo = vo ? po * bf_lo(pp.y) : 0.f;
             zero += (ve ? pe * fmaf(8.f, bf_lo(pp.x), bf_hi(pp.x)) : 0.f) +
                     (vo ? po * fmaf(8.f, bf_lo(pp.y), bf_hi(pp.y)) : 0.f);
-            const float ue = we * kUp, uo = wo * kUp;
             const uint32_t y = x >> 16;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float eight = __uint_as_float(8u << (4 * k));
-                o[k] = fmaf(ue, nibble_bits(x, k) - eight, fmaf(uo, nibble_bits(y, k) - eight, o[k]));
+                // (2^23 + c 2^(4k)) - (2^23 + 8 2^(4k)): exact
+                const float eight = 8388608.f + (float)(8u << (4 * k));
+                const float ce = __uint_as_float((x & (15u << (4 * k))) | 0x4b000000u) - eight;
+                const float co = __uint_as_float((y & (15u << (4 * k))) | 0x4b000000u) - eight;
+                o[k] = fmaf(we, ce, fmaf(wo, co, o[k]));
             }
         }
     }
@@ -709,8 +711,8 @@ __global__ void __launch_bounds__(kKvThreads, 6) kv4_decode_kernel(const Kv4Attn
     }
     if (grp == 0)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // 2^(149 - 80 - 4k)
-            sm.o[warp][4 * sub + k] = fmaf(o[k], __uint_as_float((127u + 69u - 4u * k) << 23), zero);
+        for (int k = 0; k < 4; ++k)  // 2^(-4k)
+            sm.o[warp][4 * sub + k] = fmaf(o[k], __uint_as_float((127u - 4u * k) << 23), zero);
     if (lane == 0) sm.m[warp] = m, sm.l[warp] = l;
     kv4_finish<T, D>(a, sm, r0, r1, h);
 }
@@ -1340,12 +1342,14 @@ Kv4Form form_of(const Kv4Batch &b, int i) {
 int rows_per_item(Kv4Form f) { return f == kGroupForm ? kRowsPerItem : 1; }
 
 // Keys per work item: the largest chunk (a power of two, 128 .. 2048 keys) that
-// still gives every SM three blocks of four warps.  Short chunks cost a join:
+// still gives every SM three blocks of four warps (two of groups).  Short chunks cost a join:
 // 16 requests of 300 keys, 40 heads of 128, took 18.2 us at six blocks per SM
 // and 11.5 at three, one of 100 keys 5.1 us in chunks of 64 and 3.2 in one;
-// one of 4000 keys 17.1 us at six, 13.8 at three, 19.7 at one.
+// one of 4000 keys 17.1 us at six, 13.8 at three, 19.7 at one.  Groups of rows,
+// whose blocks are heavier: two (8 requests of 2 rows over 300 keys 13.4 us, at
+// three 18.6).
 int kv4_chunk(const Kv4Batch &b, Kv4Form f, int num_sms) {
-    const int64_t most = 3LL * num_sms, per = rows_per_item(f);
+    const int64_t most = (f == kGroupForm ? 2LL : 3LL) * num_sms, per = rows_per_item(f);
     int chunk = 2048;
     while (chunk > 128) {
         int64_t items = 0;

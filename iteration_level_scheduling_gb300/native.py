@@ -34,6 +34,7 @@ EXPORTS = [
     "orca_pack_weight",
     "orca_attention_decode_noalloc", "orca_kv4_layer_bytes", "orca_kv4_plan_words", "orca_kv4_plan_build",
     "orca_kv4_workspace_bytes", "orca_op_kv4_append", "orca_op_kv4_read", "orca_op_kv4_attention", "orca_op_sample",
+    "orca_sample_last",
     "orca_debug_expire_wait", "orca_sched_create", "orca_sched_destroy",
     "orca_sched_submit", "orca_sched_set_token_feedback", "orca_sched_next", "orca_sched_complete", "orca_sched_cancel",
     "orca_sched_stats_get", "orca_sched_request_get",
@@ -136,6 +137,7 @@ _sig = {
     "orca_op_kv4_read": (C.c_int, [P, P, P, P, P]),
     "orca_op_kv4_attention": (C.c_int, [P, P, P, P, P, P, P]),
     "orca_op_sample": (C.c_int, [P, C.c_int32, P, C.c_int32, C.c_int32, C.c_int64, P, P, P, P, P, P]),
+    "orca_sample_last": (C.c_int, [P, P, P, P, P, P, P]),
     "orca_debug_expire_wait": (C.c_int, [P, C.c_int64]),
     "orca_sched_create": (C.c_int, [C.POINTER(SchedConfig), P, C.POINTER(P)]),
     "orca_sched_destroy": (C.c_int, [P]),
@@ -361,6 +363,14 @@ class Engine:
         check(lib.orca_op_sample(self._h, dtype, P(logits), n_rows, vocab, ld or vocab, P(temperature or None),
                                  P(top_k or None), P(top_p or None), P(min_p or None), P(uniform), P(out_tokens)),
               "orca_op_sample")
+        if sync:
+            self.sync()
+
+    def sample_last(self, uniform: int, temperature: int = 0, top_k: int = 0, top_p: int = 0, min_p: int = 0,
+                    out_tokens: int = 0, sync: bool = True):
+        """Sample the last iteration's requests; their tokens replace the greedy ones (device pointers, see orca.h)."""
+        check(lib.orca_sample_last(self._h, P(temperature or None), P(top_k or None), P(top_p or None),
+                                   P(min_p or None), P(uniform), P(out_tokens or None)), "orca_sample_last")
         if sync:
             self.sync()
 

@@ -86,6 +86,7 @@ def test_operators_need_an_engine(native):
     assert native.lib.orca_op_kv4_read(None, 16, p.ctypes.data, 16, 16) == native.ERR_INVALID
     assert native.lib.orca_op_kv4_attention(None, 16, 16, p.ctypes.data, 16, 16, 16) == native.ERR_INVALID
     assert native.lib.orca_op_sample(None, 0, 16, 1, 10, 10, None, None, None, None, 16, 16) == native.ERR_INVALID
+    assert native.lib.orca_sample_last(None, None, None, None, None, 16, None) == native.ERR_INVALID
 
 
 def test_oracle_quantise_ties_and_edges():
