@@ -219,6 +219,18 @@ def test_decode_small_and_large_values(native, eng, dtype, d, std):
 
 
 @pytest.mark.parametrize("dtype,d", TYPES)
+@pytest.mark.parametrize("std", [1e-20, 1e15])
+def test_magnitudes_far_from_one(native, eng, dtype, d, std):
+    """Keys and values of any size (queries of the inverse size): increments, a few rows and a prompt."""
+    s = Case(native, eng, 21, dtype, 2, d, [(1, 40), (1, 333), (5, 60), (40, 30)], std=std)
+    s.qkv[:, 0] = rounded(s.qkv[:, 0] / np.float32(std), dtype).float().numpy()
+    s.upload()
+    s.append()
+    s.append_oracle()
+    s.check(s.attention(), rounded_operands=dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
 def test_few_rows(native, eng, dtype, d):
     s = Case(native, eng, 7, dtype, 3, d, [(2, 0), (3, 1), (7, 130), (15, 64), (1, 77), (5, 700)])
     s.append()
