@@ -568,12 +568,12 @@ __device__ __forceinline__ void load_words(const void *p, uint32_t *w) {
 // n <= 4), times a factor that carries the power of two -- q's, scaled -- or, for
 // the values, added to 2^23 and taken around code 8: an AND or two instead of a
 // shift, an AND and a conversion at an eighth of the rate.  Bound by latency and
-// issue: 64 requests of 4000 keys, 12 heads of 64, fp32: 135 us (277 with the
-// conversions; 162 at four CTAs per SM, 207 without the prefetch).
+// issue: 64 requests of 4000 keys, 12 heads of 64, fp32: 123 us (277 with the
+// conversions, 139 without the values' early loads); 17 of <= 900 keys 10.8.
 __device__ __forceinline__ float nibble_bits(uint32_t w, int n) { return __uint_as_float(w & (15u << (4 * n))); }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kKvThreads, 6) kv4_decode_kernel(const Kv4Attn a) {
+__global__ void __launch_bounds__(kKvThreads, 4) kv4_decode_kernel(const Kv4Attn a) {
     constexpr int G = D / 32 > 0 ? D / 32 : 1, GS = D / G, GW = GS / 8;  // words of a group and key
     constexpr int LP = D / 4, PP = 32 / LP;  // lanes per pair of keys, pairs per step
     __shared__ Kv4Merge<D> sm;
@@ -630,6 +630,21 @@ __global__ void __launch_bounds__(kKvThreads, 6) kv4_decode_kernel(const Kv4Attn
                 if (n < 2 * (kCode + kPar)) prefetch_l1(at);
             }
         }
+        // the values' words of the first steps, in flight with the keys
+        constexpr int kSteps = 16 / PP, kEarly = kSteps < 8 ? kSteps : 8;
+        uint32_t vx[kEarly];
+        uint2 vpp[kEarly];
+        auto load_v = [&](int j, uint32_t &x, uint2 &pp) {
+            const int64_t se = b + 2 * (j * PP + grp);
+            x = 0u, pp = make_uint2(0u, 0u);
+            if (se + 1 >= s0 && se < s1) {
+                const int64_t pair = (int64_t)h * (a.v.S / 2) + (se >> 1);
+                x = reinterpret_cast<const uint32_t *>(a.v.vc + pair * D)[sub];
+                pp = *reinterpret_cast<const uint2 *>(a.v.vp + (pair * G + sub * 4 / GS) * 2);
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < kEarly; ++j) load_v(j, vx[j], vpp[j]);
         float sc = kLow;
         if (valid) {
             const int64_t row = (int64_t)h * a.v.S + slot;
@@ -673,19 +688,16 @@ __global__ void __launch_bounds__(kKvThreads, 6) kv4_decode_kernel(const Kv4Attn
         zero *= corr;
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] *= corr;
-#pragma unroll 4
-        for (int j = 0; j < 16; j += PP) {
-            const int pr = j + grp;  // this lane's pair
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            const int pr = j * PP + grp;  // this lane's pair
             const float pe = __shfl_sync(0xffffffffu, p, 2 * pr), po = __shfl_sync(0xffffffffu, p, 2 * pr + 1);
             const int64_t se = b + 2 * pr;
             const bool ve = se >= s0 && se < s1, vo = se + 1 >= s0 && se + 1 < s1;
-            uint32_t x = 0;
-            uint2 pp = make_uint2(0, 0);
-            if (ve || vo) {
-                const int64_t pair = (int64_t)h * (a.v.S / 2) + (se >> 1);
-                x = reinterpret_cast<const uint32_t *>(a.v.vc + pair * D)[sub];
-                pp = *reinterpret_cast<const uint2 *>(a.v.vp + (pair * G + sub * 4 / GS) * 2);
-            }
+            uint32_t x;
+            uint2 pp;
+            if (j < kEarly) x = vx[j < kEarly ? j : 0], pp = vpp[j < kEarly ? j : 0];
+            else load_v(j, x, pp);
             // around code 8, as the sums run over all keys; an unused slot's parameters may be anything
             const float we = ve ? pe * bf_lo(pp.x) : 0.f, wo = vo ? po * bf_lo(pp.y) : 0.f;
             zero += (ve ? pe * fmaf(8.f, bf_lo(pp.x), bf_hi(pp.x)) : 0.f) +
