@@ -90,28 +90,43 @@ __device__ __forceinline__ uint32_t kv4_code(float x, float m, float s) {
 
 // Eight components' codes, component i in bits 4 i ..  The candidate from a
 // product with 1 / s is right if what it leaves is less than half a step (the
-// residual is exact, as above).  The others -- halves, which bf16 data meet
-// about once in 256 -- are done the long way, one after the other.
+// residual is exact, as above).  Halves, which bf16 data meet about once in 256,
+// are settled one after the other, by the error of x - m or to the even code;
+// what is further off (a minimum that rounded up by more than half a step) is
+// done the long way.  Digits are put together in fp32, four at a time.
 __device__ __forceinline__ uint32_t kv4_codes(const float *x, float m, float s, float inv) {
     constexpr float kRound = 12582912.f;  // 1.5 2^23: the integer in the low bits
-    const float h = 0.5f * s;
-    uint32_t w = 0, open = 0;
+    const float h = 0.5f * s, inv15 = inv * (1.f / 15.f);
+    uint32_t open = 0;
+    float d[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 7; i >= 0; --i) {
         const float a = __fsub_rn(x[i], m);
-        const float cr = fminf(fmaxf(__fmul_rn(a, inv), 0.f), 15.f) + kRound;
-        const float r = __fmaf_rn(-(cr - kRound), s, a);
+        const float c = __fmaf_rn(__saturatef(a * inv15), 15.f, kRound) - kRound;  // clamped to 0 .. 15
+        const float r = __fmaf_rn(-c, s, a);
         if (!(fabsf(r) < h)) open |= 1u << i;
-        w |= (__float_as_uint(cr) & 15u) << (4 * i);
+        d[i >> 2] = __fmaf_rn(d[i >> 2], 16.f, c);
     }
     if (!(s > 0.f)) return 0u;
+    uint32_t w = (__float_as_uint(d[0] + 8388608.f) & 0xffffu) | (__float_as_uint(d[1] + 8388608.f) << 16);
     while (open) {
         const int i = __ffs(open) - 1;
         open &= open - 1;
         float xi = x[0];
 #pragma unroll
         for (int e = 1; e < 8; ++e) xi = i == e ? x[e] : xi;  // (x stays in registers)
-        w = (w & ~(15u << (4 * i))) | kv4_code(xi, m, s) << (4 * i);
+        const uint32_t c = (w >> (4 * i)) & 15u;
+        const float a = __fsub_rn(xi, m), r = __fmaf_rn(-(float)c, s, a);
+        uint32_t to;
+        if (fabsf(r) == h) {
+            const float bb = __fsub_rn(xi, a);
+            const float e = __fadd_rn(__fsub_rn(xi, __fadd_rn(a, bb)), __fsub_rn(bb, m));  // x - m = a + e
+            const bool away = e == 0.f ? (c & 1u) != 0 : (e > 0.f) == (r > 0.f);
+            to = !away ? c : r > 0.f ? min(c + 1, 15u) : max(c, 1u) - 1;
+        } else {
+            to = kv4_code(xi, m, s);
+        }
+        w = (w & ~(15u << (4 * i))) | to << (4 * i);
     }
     return w;
 }
