@@ -1366,27 +1366,52 @@ Kv4Form form_of(const Kv4Batch &b, int i) {
     if (b.dtype != 1 || b.n_input[i] == 1 || b.head_dim == 16) return kRowForm;
     return b.n_input[i] >= kPromptRows && b.head_dim >= 64 ? kPromptForm : kGroupForm;
 }
-int rows_per_item(Kv4Form f) { return f == kGroupForm ? kRowsPerItem : 1; }
 
-// Keys per work item: the largest chunk (a power of two, 128 .. 2048 keys) that
-// still gives every SM three blocks of four warps (two of groups).  Short chunks cost a join:
-// 16 requests of 300 keys, 40 heads of 128, took 18.2 us at six blocks per SM
-// and 11.5 at three, one of 100 keys 5.1 us in chunks of 64 and 3.2 in one;
-// one of 4000 keys 17.1 us at six, 13.8 at three, 19.7 at one.  Groups of rows,
-// whose blocks are heavier: two (8 requests of 2 rows over 300 keys 13.4 us, at
-// three 18.6).
-int kv4_chunk(const Kv4Batch &b, Kv4Form f, int num_sms) {
-    const int64_t most = (f == kGroupForm ? 2LL : 3LL) * num_sms, per = rows_per_item(f);
+// Keys per work item of rows one by one: the largest chunk (a power of two,
+// 128 .. 2048 keys) that still gives every SM three blocks of four warps.  Short
+// chunks cost a join: 16 requests of 300 keys, 40 heads of 128, took 18.2 us at
+// six blocks per SM and 11.5 at three, one of 100 keys 5.1 us in chunks of 64 and
+// 3.2 in one; one of 4000 keys 17.1 us at six, 13.8 at three, 19.7 at one.
+int kv4_row_chunk(const Kv4Batch &b, int num_sms) {
+    const int64_t most = 3LL * num_sms;
     int chunk = 2048;
     while (chunk > 128) {
         int64_t items = 0;
         for (int i = 0; i < b.n_req && items * b.n_heads < most; ++i)
-            if (form_of(b, i) == f)
-                items += (b.n_input[i] + per - 1) / per * ((b.ctx_len[i] + (int64_t)b.n_input[i] + chunk - 1) / chunk);
+            if (form_of(b, i) == kRowForm)
+                items += (int64_t)b.n_input[i] * ((b.ctx_len[i] + (int64_t)b.n_input[i] + chunk - 1) / chunk);
         if (items * b.n_heads >= most) break;
         chunk /= 2;
     }
     return chunk;
+}
+
+// The same for groups of rows, whose blocks are fewer and longer: the chunk with
+// the least time by a simple model, in units of a key's time in a block -- the
+// blocks' keys, 60 more for each block, over the blocks that run at once, half of
+// the longest block (the last ones to start are the shortest), and 120 for the
+// launch that joins chunks.  (9 requests of <= 7 rows over <= 1500 keys, 32 heads:
+// 43.0 us in chunks of 512, 38.3 of 256, 51.2 of 1024; 8 requests of 2 rows over
+// 300 keys, 40 heads: 13.4 us whole, 18.6 in chunks of 256.)
+int kv4_group_chunk(const Kv4Batch &b, int num_sms) {
+    const int64_t at_once = 3LL * num_sms;
+    int best = 2048;
+    double best_time = 0;
+    for (int chunk = 2048; chunk >= 128; chunk /= 2) {
+        int64_t keys = 0, items = 0, longest = 0;
+        bool split = false;
+        for (int i = 0; i < b.n_req; ++i) {
+            if (form_of(b, i) != kGroupForm) continue;
+            const int64_t groups = (b.n_input[i] + kRowsPerItem - 1) / kRowsPerItem, k = b.ctx_len[i] + b.n_input[i];
+            keys += groups * k;
+            items += groups * ((k + chunk - 1) / chunk);
+            longest = std::max(longest, std::min<int64_t>(k, chunk));
+            split |= k > chunk;
+        }
+        const double time = (double)(keys + 60 * items) * b.n_heads / at_once + 0.5 * (longest + 60) + (split ? 120 : 0);
+        if (chunk == 2048 || time < best_time) best = chunk, best_time = time;
+    }
+    return best;
 }
 
 bool kv4_sizes(const Kv4Batch &b, int num_sms, Kv4Sizes *z) {
@@ -1397,8 +1422,8 @@ bool kv4_sizes(const Kv4Batch &b, int num_sms, Kv4Sizes *z) {
         rows += n;
         if (rows > INT32_MAX / 8) return false;
     }
-    z->chunk = kv4_chunk(b, kRowForm, num_sms);
-    z->rchunk = kv4_chunk(b, kGroupForm, num_sms);
+    z->chunk = kv4_row_chunk(b, num_sms);
+    z->rchunk = kv4_group_chunk(b, num_sms);
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i];
         z->rows += n;
