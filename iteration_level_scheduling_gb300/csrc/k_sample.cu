@@ -206,7 +206,7 @@ struct SampleShare {
     uint32_t count[kMaxCluster];  // of gathered logits, or of those equal to the cut
     uint32_t first[kMaxCluster];  // first id of the largest logit; ties of the final pass
     // what a histogram says (every CTA finds it by itself)
-    uint32_t bin, found;
+    uint32_t bin, found, fewest;
     u64 want, wanted, total;
     // what rank 0 settles, in its copy read by all (before they enter the next barrier; it is written behind one)
     uint32_t key;
@@ -457,6 +457,8 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
     };
     // a logit that none of bins 0 .. b is below (one bin of slack for the roundings)
     auto low_of = [&](int b) { return top - (float)(b + 2) * (float)(43.5 / kBins) * 1.000001f / cs.hi; };
+    // and one that none of bins b .. is above
+    auto high_of = [&](int b) { return b < 3 ? INFINITY : top - (float)(b - 2) * (float)(43.5 / kBins) * 0.999999f / cs.hi; };
     SampleSmem &root = peer(0);
     // f(l0, l1, on0, on1) for 64 logits above the cut at a time (all lanes; on: this lane has that one), g(l) for every
     // logit, over a warp's contiguous stretch of ids; the logits above are queued so that few of them cost little.
@@ -584,7 +586,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
                 all += y;
             }
             const u64 want = pick(all);
-            if (tid == 0) sm.sh.total = all, sm.sh.wanted = want;
+            if (tid == 0) sm.sh.total = all, sm.sh.wanted = want, sm.sh.fewest = 0;
             if (base < want && want <= base + s) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -597,14 +599,28 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
                     base += y;
                 }
             }
+            if (by_mass && !down) {
+                // how many logits the bins down to that one hold at least: a bin's mass over the largest weight in it
+                // (its upper edge, half a bin above; a little more for the roundings)
+                __syncthreads();
+                float few = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int b = 4 * tid + e;
+                    if (sm.sh.found && b <= (int)sm.sh.bin)
+                        few += (float)x[e] * exp2f(((float)b - 0.51f) * (float)(43.5 / kBins) - (float)kFrac);
+                }
+                few = warp_add(few * 0.999f);
+                if (lane == 0) atomicAdd(&sm.sh.fewest, (uint32_t)fminf(few, 1e9f));
+            }
         }
         __syncthreads();
     };
 
     // Every (key, ~id) of the logits above the cut that take(l) names, in rank 0's list; returns how many there
     // are (more than kList: the list is not to be used).
-    // `low`: no logit below it is taken.
-    auto collect = [&](float low, auto take) {
+    // No logit below `low` or above `high` is taken.
+    auto collect = [&](float low, float high, auto take) {
         if (tid == 0) sm.sh.gathered = 0;
         __syncthreads();
         each4([&](int i, const float *l) {
@@ -612,7 +628,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
             if (*const_cast<volatile uint32_t *>(&sm.sh.gathered) > kList) return;  // too many: only that counts
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                if (!(l[e] > cut) || !take(l[e])) continue;
+                if (!(l[e] > cut && l[e] >= low && l[e] <= high) || !take(l[e])) continue;
                 const uint32_t j = atomicAdd(&sm.sh.gathered, 1u);
                 if (j < kList) sm.list[j] = (u64)sp_key(l[e]) << 32 | (uint32_t) ~(first + i + e);
             }
@@ -712,7 +728,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
             const int low = level == 0 ? 31 : level == 1 ? 21 : 10;  // bits of the keys not yet fixed
             const uint32_t high = level == 0 ? 0u : prefix >> low;
             auto in_bin = [&](float l) { return bin_of(l) == bin0 && (level == 0 || sp_key(l) >> low == high); };
-            const int m = collect(low_of(bin0), in_bin);
+            const int m = collect(low_of(bin0), high_of(bin0), in_bin);
             if (m > kList) continue;
             if (rank == 0) {
                 block_sort<false>(sm.list, m, 0ull);
@@ -755,7 +771,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
         if (!by_count) meet();
         if (by_count) {
             if (k <= kList) {
-                const int m = collect(low_of(bin), [&](float l) { return bin_of(l) <= bin; });
+                const int m = collect(low_of(bin), high_of(0), [&](float l) { return bin_of(l) <= bin; });
                 if (m <= kList) {
                     if (rank == 0) finish(m, k, ~0ull, p < 1.f);
                     return;
@@ -770,11 +786,14 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
         const bool found = sm.sh.found;
         const int bin = (int)sm.sh.bin;
         const u64 want = sm.sh.want, wanted = sm.sh.wanted, above = sm.sh.total;
+        const bool many = sm.sh.fewest > kList;
         if (found) {
-            const int m = collect(low_of(bin), [&](float l) { return bin_of(l) <= bin; });
-            if (m <= kList) {
-                if (rank == 0) finish(m, m, wanted, false);
-                return;
+            if (!many) {
+                const int m = collect(low_of(bin), high_of(0), [&](float l) { return bin_of(l) <= bin; });
+                if (m <= kList) {
+                    if (rank == 0) finish(m, m, wanted, false);
+                    return;
+                }
             }
             settle(true, bin, want);
         } else if (wt) {  // it reaches into those equal to the k-th
