@@ -50,7 +50,9 @@ static_assert(kBins == 4 * kSpThreads && kList == 2 * kSpThreads, "bins and list
 struct SampleArgs {
     const void *logits;
     int64_t ld;
-    int V, per;  // ids of one CTA (a multiple of 32 per warp)
+    int V, per;     // ids of one CTA (a multiple of four)
+    int n_rows;
+    bool by_work;  // rows are taken by the work that their parameters mean, the most first
     const float *temperature, *top_p, *min_p, *uniform;
     const int32_t *top_k;
     int32_t *out;
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int r = blockIdx.x / C;
+    int r = blockIdx.x / C;
     constexpr unsigned kAll = 0xffffffffu;
     // the same object in another CTA of the row
     auto peer = [&](int c) -> SampleSmem & { return *cluster.map_shared_rank(&sm, c); };
@@ -331,6 +333,40 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
     pdl_trigger();
     pdl_wait();
 
+    if (a.by_work) {
+        // 0: a top-p over all ids, or a long top-k; 1: no filter; 2: a short top-k; 3: greedy.  A row's position is by
+        // (class, index); every CTA finds the one of its cluster's.
+        auto work = [&](int i) {
+            if (i >= a.n_rows) return 4;
+            const int ki = a.top_k ? a.top_k[i] : 0;
+            const float pi = a.top_p ? a.top_p[i] : 1.f, ti = a.temperature ? a.temperature[i] : 1.f;
+            const bool listed = ki > 0 && ki <= kList;
+            return ti == 0.f ? 3 : listed ? 2 : pi < 1.f || (ki > kList && ki < a.V) ? 0 : 1;
+        };
+        int place = r, cls = -1, before;
+        do {  // the class
+            ++cls, before = place;
+            for (int i = 0; i < a.n_rows; i += kSpThreads) place -= __syncthreads_count(work(i + tid) == cls);
+        } while (place >= 0 && cls < 3);
+        place = before;
+        for (int i = 0; i < a.n_rows; i += kSpThreads) {
+            const bool in = work(i + tid) == cls;
+            const uint32_t mask = __ballot_sync(kAll, in);
+            if (lane == 0) sm.wcnt[warp] = __popc(mask);
+            const int count = __syncthreads_count(in);
+            if (place < count) {
+                int rank_in = __popc(mask & ((1u << lane) - 1u));
+                for (int w = 0; w < warp; ++w) rank_in += sm.wcnt[w];
+                if (in && rank_in == place) sm.sh.bin = (uint32_t)(i + tid);
+                break;
+            }
+            place -= count;
+            __syncthreads();
+        }
+        __syncthreads();
+        r = (int)sm.sh.bin;
+        __syncthreads();
+    }
     const float temp = a.temperature ? a.temperature[r] : 1.f, p = a.top_p ? a.top_p[r] : 1.f,
                 mp = a.min_p ? a.min_p[r] : 0.f, u = a.uniform[r];
     const int k = a.top_k ? a.top_k[r] : 0;
@@ -899,7 +935,10 @@ cudaError_t sample_rows(int dtype_bf16, const void *logits, int64_t ld, int n_ro
     while (C < 4 && V / C > 8192 && (int64_t)n_rows * C * 2 <= num_sms) C *= 2;
     const int per = ((V + C - 1) / C + 3) / 4 * 4;
     const bool held = per <= kMaxPer;
-    SampleArgs a{logits, ld, V, per, temperature, top_p, min_p, uniform, top_k, out, err};
+    // more rows than run at once: the ones with the most work first, so that none of them starts last (with thousands
+    // the last ones matter little, and every CTA looks through all of them)
+    const bool by_work = (int64_t)n_rows * C > 2 * num_sms && n_rows <= 1024 && (temperature || top_k || top_p);
+    SampleArgs a{logits, ld, V, per, n_rows, by_work, temperature, top_p, min_p, uniform, top_k, out, err};
     const void *f = dtype_bf16 ? (held ? (const void *)sample_kernel<bf16, true> : (const void *)sample_kernel<bf16, false>)
                                : (held ? (const void *)sample_kernel<float, true> : (const void *)sample_kernel<float, false>);
     const size_t smem = sizeof(SampleSmem) + (held ? (size_t)per * 4 : 0);

@@ -57,7 +57,7 @@ def logits(seed, rows, V, dtype, std=3.0):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("V", [1, 2, 31, 32, 33, 512, 1000, 1023, 1025, 4097, 50257, 131071])
+@pytest.mark.parametrize("V", [1, 2, 31, 32, 33, 512, 1000, 1023, 1025, 4097, 50257, 131071, 300001])
 def test_every_filter(native, eng, V, dtype):
     rows = 24
     x, g = logits(V, rows, V, dtype)
@@ -156,6 +156,18 @@ def test_many_rows(native, eng):
     u = g.random(700, dtype=np.float32).tolist()
     k, p = [40] * 700, [float(np.float32(0.92))] * 700
     assert draw(native, eng, x, u, k=k, p=p) == want(x, u, k=k, p=p)
+
+
+@pytest.mark.parametrize("rows,V", [(320, 20011), (1024, 700), (1025, 700), (513, 33000)])
+def test_rows_of_every_kind_in_one_batch(native, eng, rows, V):
+    """More rows than run at once, which are taken by their work: greedy, unfiltered, short and long top-k and nuclei."""
+    x, g = logits(rows, rows, V, torch.float32, std=2.0)
+    u = g.random(rows, dtype=np.float32).tolist()
+    t = [float(a) for a in np.float32(g.choice([0.0, 0.7, 1.0, 1.5], rows))]
+    k = [int(a) for a in g.choice([0, 0, 5, 40, 1024, 1025, 5000], rows)]
+    p = [float(a) for a in np.float32(g.choice([0.3, 0.9, 0.99, 1.0], rows))]
+    assert draw(native, eng, x, u, t, k, p) == want(x, u, t, k, p)
+    assert draw(native, eng, x, u, k=k) == want(x, u, k=k)
 
 
 @pytest.mark.parametrize("name,value", [("t", -1.0), ("t", float("nan")), ("t", INF), ("t", 1.1e6), ("p", -0.1),
