@@ -155,6 +155,11 @@ __device__ __forceinline__ uint32_t kv4_quantise(const float *x, uint32_t *par) 
 // ---------------------------------------------------------------------------
 // write: one thread per 8 components of k and of v, of one row or of two whose
 // slots share a pair (then V goes out in whole words)
+//
+// Bound by issue (80 % of active cycles; 25 warp instructions per 32 components,
+// 5 of them for halves): 10.5 k rows of 40 heads of 128, bf16, 89 us under the
+// profiler for 215 MB read and 67 MB written (42 us at the copy rate); with an
+// IEEE quotient per component 189.
 // ---------------------------------------------------------------------------
 constexpr int kApThreads = 128;
 
@@ -217,6 +222,9 @@ __global__ void __launch_bounds__(kApThreads) kv4_append_kernel(const T *qkv, co
 
 // ---------------------------------------------------------------------------
 // read back: tiles of up to 64 slots of one range, one head's K and V per CTA
+//
+// Bound by memory: the same 10.5 k slots, 67 MB read and 215 MB written, in 44 us
+// (96 % of the copy rate; part of the writes is still in L2).
 // ---------------------------------------------------------------------------
 constexpr int kRdThreads = 128;
 constexpr int kReadTile = 64;  // slots per tile
@@ -340,6 +348,9 @@ __global__ void __launch_bounds__(kRdThreads) kv4_read_kernel(Kv4View v, const i
 // fp16 keeps 11 bits; its narrow range is met by powers of two, one per row and
 // head for q and one per request and head for K and V, that bring the largest
 // magnitude to [2^14, 2^15) (values 2^-28 of it and below lose bits).
+// Four prompts of 900 rows over 1000 keys, 40 heads of 128: scales and q 25 us, K
+// and V 42 us, the attention 168 us under the profiler (tensor pipe 36 % of active
+// cycles, as on a bf16 cache); against rows one by one 4968 us.
 
 // The power of two for a largest magnitude, as its inverse; 1 where that is zero or subnormal.
 __device__ __forceinline__ float kv4_inverse_scale(float amax) {
@@ -750,9 +761,13 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv4_decode_kernel(const Kv4Attn
 //            group; q enters column g of B only where the component's group is
 //            g, so the columns of S gather sum q c group by group and s, m
 //            apply afterwards.  A = the codes as fp16 subnormals, q in fp16.
+//            (128 + c in bf16 with the accumulator started at -128 sum q took
+//            two more shifts per word and four more products per block.)
 //   values   rows = 16 components, k = 16 keys.  A = c - 8, exact; column g of
 //            B is p s_g rounded to bf16, column 4 + g what the rounding left,
 //            so the weights keep 16 bits; sum p (m + 8 s) is added in fp32.
+// Bound by issue and the integer pipe (each 66 % of their peak): 64 requests of <= 4000 keys, 40 heads of 128, 1.04 GB, in
+// 197 us, 78 % of the copy rate; 378 warp instructions per 16 keys and head, a third of them to unpack.
 // Codes are centred for the values because those sums run over all keys:
 // taken around 0 .. 15 the accumulator would grow with every key and cancel
 // against the minima at the end.
@@ -1046,6 +1061,8 @@ __global__ void __launch_bounds__(kKvThreads, kDecodeCtas) kv4_decode_mma_kernel
 //   O    A = p s of the group, as two bf16 (16 bits kept), B = c - 8 of 8 components of that group; the part of the
 //        minima, sum p (m + 8 s), in fp32.
 // P leaves the first product in the very registers that the second one takes it from.
+// Bound by issue and latency: 9 requests of <= 7 rows over <= 1500 keys, 32 heads of 128, 41 us (row by row 65), 51 MB:
+// 7.6 us at the copy rate; the schedulers issue in 51 % of active cycles, three CTAs of 168 registers per SM.
 constexpr int kRowsPerItem = 16;
 
 template <int D>

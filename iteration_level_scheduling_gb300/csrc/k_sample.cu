@@ -22,6 +22,15 @@
 // of them are gathered, sorted and settled by one CTA; more are settled by
 // selecting the last kept logit and passing over the row in the order of the
 // ids.
+//
+// Bound by barriers and latency, then by issue: 192 rows of 50257 with mixed
+// parameters take 73 us (38.6 MB: 5.8 us of reading), the schedulers issuing in
+// 42 % of their active cycles, barriers the first stall; a weight is about 95
+// warp instructions per 32 logits with its comparison and sum, two thirds of
+// them integer.  One row at T 0.8, top-k 50, top-p 0.95 takes 12.3 us, 23 000
+// cycles of four CTAs: 5 600 to load, 7 300 for the histogram, 4 500 to gather,
+// 5 000 to sort and draw.  With weights by fp64 exp, masses by a radix selection
+// over the row in global memory, these were 2453 and 142 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
