@@ -1210,6 +1210,7 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
 #pragma unroll
             for (int e = 0; e < 2 * R; ++e) {
                 p[i][e] = ex2(sc[i][e] - m[e >> 1]);  // (-inf: 0)
+                if (!whole && sc[i][e] == -INFINITY) p[i][e] = -0.f;  // marks what the row does not see
                 l[e >> 1] += p[i][e];
             }
 #pragma unroll
@@ -1225,9 +1226,9 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
                 for (int x = 0; x < R; ++x) {  // row g + 8 x
                     const float pe = p[i][2 * x], po = p[i][2 * x + 1];
                     float we = pe * se, wo = po * so, ye = pe * ze, yo = po * zo;
-                    if (!whole) {  // (what a row does not see may hold anything: 0 times a NaN)
-                        if (pe == 0.f) we = ye = 0.f;
-                        if (po == 0.f) wo = yo = 0.f;
+                    if (!whole) {  // what a row does not see may hold anything, 0 times which may be NaN
+                        if (__float_as_uint(pe) == 0x80000000u) we = ye = 0.f;
+                        if (__float_as_uint(po) == 0x80000000u) wo = yo = 0.f;
                     }
                     zero[y][x] += ye + yo;
                     hi[2 * i + x] = pack2(we, wo);

@@ -145,3 +145,48 @@ def test_sampling_in_the_engines_iterations(native, dtype):
     finally:
         a.close()
         b.close()
+
+
+def test_sampling_between_planned_iterations(native):
+    """Planned iterations and sampling queued one behind the other, tokens passed on by reference, nothing read back in
+    between: the tokens of a run that waits for every step and passes them by value."""
+    from gpu_util import make_engine
+    cfg = synth.ModelConfig(n_layers=2, hidden=128, n_heads=2, ffn=256, vocab=700, max_pos=64, dtype="bf16")
+    w = synth.make_weights(cfg, 6, random_affine=True, std=0.2)
+    prompts, steps = [[3, 1, 4, 1, 5], [9, 2], [6, 5, 3, 5, 8, 9, 7]], 6
+    lens = [len(x) for x in prompts]
+    u = torch.from_numpy(np.random.default_rng(2).random((steps, 3), dtype=np.float32)).cuda()
+    t, p = torch.tensor([2.0, 1.0, 0.0], device="cuda"), torch.tensor([0.9, 1.0, 1.0], device="cuda")
+
+    def batch(it, offs, tokens):
+        if it == 0:
+            return native.BatchDesc([0, 1, 2], [0] * 3, lens, [0] * 3, offs, sum(prompts, []))
+        return native.BatchDesc([0, 1, 2], [1] * 3, [1] * 3, [n + it - 1 for n in lens], offs, tokens)
+
+    a, b = make_engine(cfg, w, 64, 4, 256), make_engine(cfg, w, 64, 4, 256)
+    try:
+        offs = [a.kv_alloc(i, 64) for i in range(3)]
+        assert offs == [b.kv_alloc(i, 64) for i in range(3)]
+        want, tok = [], None
+        for it in range(steps):
+            a.run_iteration(batch(it, offs, tok))
+            out = torch.zeros(3, dtype=torch.int32, device="cuda")
+            a.sample_last(u[it].data_ptr(), temperature=t.data_ptr(), top_p=p.data_ptr(), out_tokens=out.data_ptr())
+            tok = out.tolist()
+            want.append(tok)
+        plans, got = [], torch.zeros((steps, 3), dtype=torch.int32, device="cuda")
+        for it in range(steps):
+            d = batch(it, offs, [-1, -2, -3])
+            plans.append(np.zeros(b.plan_words(d), np.int32))
+            b.plan_build(d, plans[it])
+        dev = [torch.from_numpy(x).cuda() for x in plans]
+        torch.cuda.synchronize()
+        for it in range(steps):
+            b.run_planned(plans[it], dev[it].data_ptr())
+            b.sample_last(u[it].data_ptr(), temperature=t.data_ptr(), top_p=p.data_ptr(),
+                          out_tokens=got[it].data_ptr(), sync=False)
+        b.sync()
+        assert got.tolist() == want
+    finally:
+        a.close()
+        b.close()

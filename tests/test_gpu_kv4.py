@@ -368,3 +368,64 @@ def test_shared_prefix(native, eng):
     s.qkv = np.concatenate([s.qkv, s.qkv])
     s.n, s.c, s.off = [1, 1], [100, 57], s.off * 2
     s.check(out)
+
+
+@pytest.mark.parametrize("n", [1, 9, 20, 40])
+def test_nan_value_of_a_key_that_weighs_nothing(native, eng, n):
+    """A key that a row sees, but whose weight underflows: 0 times its NaN value is NaN, as in the formula."""
+    s = Case(native, eng, 22, "bf16", 2, 128, [(n, 20)])
+    s.qkv[:, 0, 0], s.qkv[:, 1, 0] = 8.0, 8.0
+    s.qkv[0, 1, 0] = -8.0          # head 0, row 0: a score of 8192 / sqrt(128) below the other rows'
+    s.qkv[0, 2, 0, 3] = np.nan
+    s.upload()
+    s.append()
+    out = s.attention().float().reshape(n, 2, 128)
+    assert out[:, 0, :32].isnan().all() and out[:, 1].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 32), ("fp32", 64)])
+def test_nothing_else_is_written(native, eng, dtype, d):
+    """Rows behind the last one, what lies behind a read, slots outside the ranges and what follows a workspace."""
+    s = Case(native, eng, 23, dtype, 3, d, [(1, 700), (5, 600), (150, 33), (1, 0)])
+    H, rows, keys = s.heads * d, len(s.qkv), sum(s.n) + sum(s.c)
+    need = eng.kv4_workspace_bytes(s.plan)
+    s.work = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.full((rows + 200, H), float("nan"), dtype=TD[dtype], device="cuda")
+    back = torch.full((2 * s.heads * keys + 200, d), float("nan"), dtype=TD[dtype], device="cuda")
+    tail = torch.full((s.dev.numel() + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    tail[:s.dev.numel()] = s.dev
+    s.dev = tail
+    s.append()
+    eng.op_kv4_attention(s.dqkv.data_ptr(), s.dev.data_ptr(), s.plan, s.dplan.data_ptr(), s.work.data_ptr(),
+                         out.data_ptr())
+    eng.op_kv4_read(s.dev.data_ptr(), s.plan, s.dplan.data_ptr(), back.data_ptr())
+    s.append_oracle()
+    assert np.array_equal(s.dev[:-4096].cpu().numpy(), s.host)
+    assert (s.dev[-4096:] == 0xFF).all() and (s.work[need:] == 0xA5).all()
+    assert out[rows:].isnan().all() and back[-200:].isnan().all() and back[:-200].isfinite().all()
+    s.check(out[:rows], rounded_operands=dtype == "bf16")
+    # and the plan is as it was: the next call finds its counters at zero
+    assert np.array_equal(s.dplan.cpu().numpy(), s.plan)
+
+
+def test_two_streams_at_once(native):
+    """Two engines on streams of their own, each with its layer, plan and workspace, queued without a wait."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    engines = [native.Engine(1, 64, 1, 64, 64, 64, native.DTYPE_BF16, 64, 64, 64, None, st.cuda_stream)
+               for st in streams]
+    cases, outs = [], []
+    for i, (e, st) in enumerate(zip(engines, streams)):
+        with torch.cuda.stream(st):
+            cases.append(Case(native, e, 24 + i, "bf16", 8, 128, [(1, 3000), (7, 1500), (40, 200), (1, 17)]))
+            outs.append(torch.zeros((len(cases[i].qkv), 8 * 128), dtype=torch.bfloat16, device="cuda"))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, e, o in zip(cases, engines, outs):
+            s.append(sync=False)
+            e.op_kv4_attention(s.dqkv.data_ptr(), s.dev.data_ptr(), s.plan, s.dplan.data_ptr(), s.work.data_ptr(),
+                               o.data_ptr(), sync=False)
+    for s, e, o in zip(cases, engines, outs):
+        e.sync()
+        s.append_oracle()
+        s.check(o, rounded_operands=True)
+        e.close()
