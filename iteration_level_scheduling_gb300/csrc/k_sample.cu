@@ -24,13 +24,14 @@
 // ids.
 //
 // Bound by barriers and latency, then by issue: 192 rows of 50257 with mixed
-// parameters take 73 us (38.6 MB: 5.8 us of reading), the schedulers issuing in
+// parameters take 67 us (38.6 MB: 5.8 us of reading), the schedulers issuing in
 // 42 % of their active cycles, barriers the first stall; a weight is about 95
 // warp instructions per 32 logits with its comparison and sum, two thirds of
-// them integer.  One row at T 0.8, top-k 50, top-p 0.95 takes 12.3 us, 23 000
-// cycles of four CTAs: 5 600 to load, 7 300 for the histogram, 4 500 to gather,
-// 5 000 to sort and draw.  With weights by fp64 exp, masses by a radix selection
-// over the row in global memory, these were 2453 and 142 us.
+// them integer.  One row at T 0.8, top-k 50, top-p 0.95 takes 11.0 us on four
+// CTAs: a quarter to load, a quarter to gather, the rest in barriers and in sums
+// over the block (12.1 us, and the batch 73, with every logit in the histogram).
+// With weights by fp64 exp, masses by a radix selection over the row in global
+// memory, these were 2453 and 142 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -338,7 +339,8 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
         else __syncthreads();
     };
     if (tid < kExpEntries) sm.exp[tid] = kExp.e[tid];
-    if (C > 1) cluster.sync();  // every CTA of the row runs before another writes to its shared memory
+    cg::cluster_group::arrival_token here;  // every CTA of the row runs before another writes to its shared memory
+    if (C > 1) here = cluster.barrier_arrive();
     pdl_trigger();
     pdl_wait();
 
@@ -379,10 +381,6 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
     const float temp = a.temperature ? a.temperature[r] : 1.f, p = a.top_p ? a.top_p[r] : 1.f,
                 mp = a.min_p ? a.min_p[r] : 0.f, u = a.uniform[r];
     const int k = a.top_k ? a.top_k[r] : 0;
-    if (!(temp >= 0.f && temp <= 1e6f && p >= 0.f && p <= 1.f && mp >= 0.f && mp <= 1.f && u >= 0.f && u < 1.f)) {
-        if (rank == 0 && tid == 0) raise_err(a.err, ERR_BAD_SAMPLE), a.out[r] = -1;
-        return;  // (the whole cluster)
-    }
     // this CTA's ids: first .. first + n - 1
     const int first = min(a.V, rank * a.per), n = min(a.V - first, a.per);
     const T *row = (const T *)a.logits + (size_t)r * a.ld + first;
@@ -438,6 +436,12 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
         for (int i = head + body * VEC + tid; i < n; i += kSpThreads) put(i, Elem<T>::to_f(row[i]));
         if (tid < 4 && n + tid < (n + 3) / 4 * 4) val[n + tid] = -INFINITY;
     }
+    if (C > 1) cluster.barrier_wait(std::move(here));
+    if (!(temp >= 0.f && temp <= 1e6f && p >= 0.f && p <= 1.f && mp >= 0.f && mp <= 1.f && u >= 0.f && u < 1.f)) {
+        if (rank == 0 && tid == 0) raise_err(a.err, ERR_BAD_SAMPLE), a.out[r] = -1;
+        return;  // (the whole cluster)
+    }
+    const float own = top;  // the largest of this thread's
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
     if (lane == 0) sm.wcnt[warp] = __float_as_uint(top);
@@ -562,8 +566,9 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
     // Histogram over the bins of(l) >= 0 of the logits above the cut, counts or masses, added up over the row's CTAs
     // by each of them.  pick(total) says what is wanted, and sm.sh gets whether that much is there (found), the bin in
     // which it is reached from the largest logits down, what is left of it for that bin (want) and all of it (wanted).
-    // `down`: larger logits are in higher bins.  A barrier has to follow before the next histogram.
-    auto histogram = [&](bool by_mass, bool down, auto of, auto pick) {
+    // `down`: larger logits are in higher bins.  `largest`: of each thread's largest logit alone.  A barrier has to
+    // follow before the next histogram.
+    auto histogram = [&](bool by_mass, bool down, bool largest, auto of, auto pick) {
         for (int i = tid; i < kBins / 4; i += kSpThreads) {
             reinterpret_cast<uint4 *>(sm.lo)[i] = make_uint4(0, 0, 0, 0);
             if (by_mass) reinterpret_cast<uint4 *>(sm.hi)[i] = make_uint4(0, 0, 0, 0);
@@ -593,11 +598,14 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) put(l[e], w[e]);
             });
-        else
-            each([&](int, float l) {
+        else {
+            auto count = [&](int, float l) {
                 const int b = l > cut ? of(l) : -1;
                 if (b >= 0) atomicAdd(&sm.lo[b], 1u);
-            });
+            };
+            if (largest) count(0, own);
+            else each(count);
+        }
         meet();
         {
             // thread t: four bins, in the order of descending logits
@@ -761,7 +769,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
             };
             if (level > 0) {
                 const u64 goal = want;
-                histogram(by_mass, true, of, [=](u64) { return goal; });
+                histogram(by_mass, true, false, of, [=](u64) { return goal; });
                 want = sm.sh.want;
                 prefix |= sm.sh.bin << (level == 1 ? 21 : level == 2 ? 10 : 0);
                 if (level == 3) {
@@ -808,7 +816,23 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
     };
 
     if (by_count) {
-        histogram(false, false, bin_of, [&](u64) { return (u64)k; });
+        // No logit of the k largest is below the k-th largest of the threads' largest: with k well below the number of
+        // threads few more than k lie above it (n ln(n / (n - k)) of logits in any order, n threads), and counting
+        // one logit a thread is enough.
+        if (k <= kList / 2 && k <= kSpThreads / 2 * C) {
+            histogram(false, false, true, bin_of, [&](u64) { return (u64)k; });
+            const int bin = (int)sm.sh.bin;
+            if (sm.sh.found && bin != kBins - 1) {
+                const int m = collect(low_of(bin), high_of(0), [&](float l) { return bin_of(l) <= bin; });
+                if (m <= kList) {
+                    if (rank == 0) finish(m, k, ~0ull, p < 1.f);
+                    return;
+                }
+            } else {
+                meet();
+            }
+        }
+        histogram(false, false, false, bin_of, [&](u64) { return (u64)k; });
         const int bin = (int)sm.sh.bin;
         const u64 want = sm.sh.want;
         // fewer than k logits, or the k-th without weight: the same as all kept
@@ -827,7 +851,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
     }
     if (p < 1.f) {
         const u64 wt = by_count ? weight(cut) : 0ull;
-        histogram(true, false, bin_of, [&](u64 above) { return share(above + wt * (by_count ? ties : 0u)); });
+        histogram(true, false, false, bin_of, [&](u64 above) { return share(above + wt * (by_count ? ties : 0u)); });
         const bool found = sm.sh.found;
         const int bin = (int)sm.sh.bin;
         const u64 want = sm.sh.want, wanted = sm.sh.wanted, above = sm.sh.total;

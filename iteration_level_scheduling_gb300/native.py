@@ -163,8 +163,15 @@ def check(rc: int, what: str) -> int:
     return rc
 
 
+_addressof, _char_at = C.addressof, C.c_char.from_buffer
+
+
 def _ptr(a: np.ndarray) -> int:
-    return a.ctypes.data
+    """Address of an array's first element (a.ctypes builds objects that take twice the time)."""
+    try:
+        return _addressof(_char_at(a))
+    except (TypeError, ValueError, BufferError):  # read-only, empty or strided
+        return a.ctypes.data
 
 
 def _i32(a) -> np.ndarray:
@@ -340,19 +347,19 @@ class Engine:
         return check(lib.orca_kv4_workspace_bytes(_ptr(plan)), "orca_kv4_workspace_bytes")
 
     def op_kv4_append(self, qkv: int, layer: int, plan: np.ndarray, dev_plan: int, sync: bool = True):
-        check(lib.orca_op_kv4_append(self._h, P(qkv), P(layer), _ptr(plan), P(dev_plan)), "orca_op_kv4_append")
+        check(lib.orca_op_kv4_append(self._h, qkv, layer, _ptr(plan), dev_plan), "orca_op_kv4_append")
         if sync:
             self.sync()
 
     def op_kv4_read(self, layer: int, plan: np.ndarray, dev_plan: int, out: int, sync: bool = True):
-        check(lib.orca_op_kv4_read(self._h, P(layer), _ptr(plan), P(dev_plan), P(out)), "orca_op_kv4_read")
+        check(lib.orca_op_kv4_read(self._h, layer, _ptr(plan), dev_plan, out), "orca_op_kv4_read")
         if sync:
             self.sync()
 
     def op_kv4_attention(self, qkv: int, layer: int, plan: np.ndarray, dev_plan: int, workspace: int, out: int,
                          sync: bool = True):
-        check(lib.orca_op_kv4_attention(self._h, P(qkv), P(layer), _ptr(plan), P(dev_plan), P(workspace or None),
-                                        P(out)), "orca_op_kv4_attention")
+        check(lib.orca_op_kv4_attention(self._h, qkv, layer, _ptr(plan), dev_plan, workspace, out),
+              "orca_op_kv4_attention")
         if sync:
             self.sync()
 
@@ -360,17 +367,15 @@ class Engine:
                   temperature: int = 0, top_k: int = 0, top_p: int = 0, min_p: int = 0, ld: int = 0,
                   sync: bool = True):
         """Sampled tokens of n_rows logits rows (device pointers; parameter arrays may be left out, see orca.h)."""
-        check(lib.orca_op_sample(self._h, dtype, P(logits), n_rows, vocab, ld or vocab, P(temperature or None),
-                                 P(top_k or None), P(top_p or None), P(min_p or None), P(uniform), P(out_tokens)),
-              "orca_op_sample")
+        check(lib.orca_op_sample(self._h, dtype, logits, n_rows, vocab, ld or vocab, temperature, top_k, top_p, min_p,
+                                 uniform, out_tokens), "orca_op_sample")
         if sync:
             self.sync()
 
     def sample_last(self, uniform: int, temperature: int = 0, top_k: int = 0, top_p: int = 0, min_p: int = 0,
                     out_tokens: int = 0, sync: bool = True):
         """Sample the last iteration's requests; their tokens replace the greedy ones (device pointers, see orca.h)."""
-        check(lib.orca_sample_last(self._h, P(temperature or None), P(top_k or None), P(top_p or None),
-                                   P(min_p or None), P(uniform), P(out_tokens or None)), "orca_sample_last")
+        check(lib.orca_sample_last(self._h, temperature, top_k, top_p, min_p, uniform, out_tokens), "orca_sample_last")
         if sync:
             self.sync()
 
