@@ -228,6 +228,8 @@ __global__ void __launch_bounds__(kApThreads) kv4_append_kernel(const T *qkv, co
 // ---------------------------------------------------------------------------
 constexpr int kRdThreads = 128;
 constexpr int kReadTile = 64;  // slots per tile
+// heads that a CTA of kv4_read_few_kernel takes
+__host__ __device__ constexpr int kv4_few_heads(int d, int per) { return 2 * kRdThreads / (d / 8) / per; }
 
 // nibbles N and N + 4 of w as floats, through bf16's 128 + c (conversions run at an eighth of the rate)
 template <int N>
@@ -338,6 +340,56 @@ __global__ void __launch_bounds__(kRdThreads) kv4_read_kernel(Kv4View v, const i
 #pragma unroll
     for (int n = 0; n < VN; ++n) store_v(n, (threadIdx.x + n * kRdThreads) / U);
     for (int j = (threadIdx.x + VN * kRdThreads) / U; j < np; j += kRdThreads / U) load_v(0, j), store_v(0, j);
+}
+
+// The same for a plan whose ranges are all short (increments): a CTA takes `per` slots of several heads, two units of
+// K and V per thread.  64 ranges, 40 heads of 128, against a CTA per range and head: one slot 1.7 us and 4.8, four
+// slots 2.8 and 5.2, eight 4.5 and 5.8; 12 heads of 32 in fp32: 1.25 and 1.7, 1.5 and 1.7, 2.1 and 1.7.
+constexpr int kFewSlots = 4;
+template <typename T, int D>
+__global__ void __launch_bounds__(kRdThreads) kv4_read_few_kernel(Kv4View v, const int32_t *tiles, T *out,
+                                                                  int64_t out_slots, int n_heads, int per) {
+    constexpr int G = D >= 32 ? D / 32 : 1, GS = D / G, U = D / 8, N = 2;
+    pdl_trigger();
+    pdl_wait();
+    const int4 tl = reinterpret_cast<const int4 *>(tiles)[blockIdx.x];
+    const int u = threadIdx.x % U, gr = u * 8 / GS, heads = kv4_few_heads(D, per);  // heads per CTA
+    uint32_t kw[N], kp[N], pv[N];
+    uint2 vw[N];
+    int h[N], s[N];
+    bool on[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int j = (threadIdx.x + n * kRdThreads) / U, hh = j / per;
+        h[n] = blockIdx.y * heads + hh, s[n] = j - hh * per;
+        on[n] = hh < heads && h[n] < n_heads && s[n] < tl.y;
+        if (on[n]) {
+            const int64_t row = h[n] * v.S + tl.x + s[n], pair = row >> 1;
+            kw[n] = __ldcs(reinterpret_cast<const uint32_t *>(v.kc + row * (D / 2)) + u);
+            kp[n] = v.kp[row * G + gr];
+            vw[n] = reinterpret_cast<const uint2 *>(v.vc + pair * D)[u];
+            pv[n] = v.vp[(pair * G + gr) * 2 + (row & 1)];
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        if (!on[n]) continue;
+        const bool odd = (tl.x + s[n]) & 1;
+        const uint32_t w = odd ? (vw[n].x >> 16) | (vw[n].y & 0xffff0000u) : (vw[n].x & 0xffffu) | (vw[n].y << 16);
+        T *dst = out + ((int64_t)h[n] * out_slots + tl.z + s[n]) * D + u * 8;
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            const uint32_t c = o ? w : kw[n], p = o ? pv[n] : kp[n];
+            float x[8];
+            code_floats<0>(c, x[0], x[4]);
+            code_floats<1>(c, x[1], x[5]);
+            code_floats<2>(c, x[2], x[6]);
+            code_floats<3>(c, x[3], x[7]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = fmaf(bf_lo(p), x[k], bf_hi(p));
+            store8(dst + (o ? (int64_t)n_heads * out_slots * D : 0), x);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -1361,6 +1413,7 @@ enum : int {
     Q_O_RITEMS,
     Q_O_RJOINS,
     Q_O_REQWS,  // a prompt's first slot in the workspace's pool
+    Q_TILEMOST,  // slots of the longest read-back tile
 };
 // Requests of at least this many rows run on the prefill kernel (bf16, head_dim 64 or 128).  8 requests over 2000 keys,
 // 40 heads of 128: 16 rows 89 us in groups and 174 on it, 32 rows 144 and 176, 48 rows 199 and 177; one request over
@@ -1525,6 +1578,7 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     int32_t *ri = buf + z.off_ritems, *rj = buf + z.off_rjoins;
     int64_t row = 0, split = 0, part = 0, key = 0, ws = 0, rpart = 0;
     bool half = true;
+    int32_t most = 0;
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i], o = b.kv_offset[i];
         const Kv4Form form = form_of(b, i);
@@ -1574,6 +1628,7 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
         for (int64_t t = 0; t < c + n; t += kReadTile, tl += 4) {
             tl[0] = (int32_t)(o + t);
             tl[1] = (int32_t)std::min<int64_t>(kReadTile, c + n - t);
+            most = std::max(most, tl[1]);
             tl[2] = (int32_t)(key + t);
             if (prompt) {
                 std::memcpy(pd, tl, 4 * sizeof(int32_t));
@@ -1637,6 +1692,7 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     buf[Q_O_REQOFF] = (int32_t)z.off_reqoff;
     buf[Q_O_REQCTX] = (int32_t)z.off_reqctx;
     buf[Q_O_REQWS] = (int32_t)z.off_reqws;
+    buf[Q_TILEMOST] = most;
     return true;
 }
 
@@ -1696,7 +1752,14 @@ cudaError_t append(const void *qkv, const Kv4View &v, const int32_t *hp, const i
 
 template <typename T>
 cudaError_t read(const Kv4View &v, const int32_t *hp, const int32_t *dp, void *out, cudaStream_t st) {
+    const int per = hp[Q_TILEMOST];
     return for_dim(hp[Q_DIM], [&](auto d) {
+        if (per <= kFewSlots) {
+            const int heads = kv4_few_heads(d(), per);
+            return launch_pdl(kv4_read_few_kernel<T, d()>, dim3(hp[Q_TILES], (hp[Q_HEADS] + heads - 1) / heads),
+                              dim3(kRdThreads), 0, st, v, dp + hp[Q_O_TILES], (T *)out, (int64_t)hp[Q_KEYS], hp[Q_HEADS],
+                              per);
+        }
         return launch_pdl(kv4_read_kernel<T, d(), false>, dim3(hp[Q_TILES], hp[Q_HEADS]), dim3(kRdThreads), 0, st, v,
                           dp + hp[Q_O_TILES], (T *)out, (int64_t)hp[Q_KEYS], hp[Q_HEADS], (const float *)nullptr);
     });

@@ -429,3 +429,21 @@ def test_two_streams_at_once(native):
         s.append_oracle()
         s.check(o, rounded_operands=True)
         e.close()
+
+
+@pytest.mark.parametrize("heads", [1, 37])
+@pytest.mark.parametrize("dtype,d", TYPES)
+@pytest.mark.parametrize("reqs", [[(1, 0)] * 5, [(1, 0), (1, 2), (2, 0), (2, 2), (1, 1), (4, 0)], [(5, 0), (1, 0)]])
+def test_read_of_short_ranges(native, eng, dtype, d, heads, reqs):
+    s = Case(native, eng, 26, dtype, heads, d, reqs)
+    s.append()
+    s.append_oracle()
+    total = sum(s.n) + sum(s.c)
+    out = torch.full((2 * heads * total + 8, d), float("nan"), dtype=TD[dtype], device="cuda")
+    eng.op_kv4_read(s.dev.data_ptr(), s.plan, s.dplan.data_ptr(), out.data_ptr())
+    assert out[-8:].isnan().all()
+    out, at = out[:-8].view(2, heads, total, d), 0
+    for n, c, o in zip(s.n, s.c, s.off):
+        for got, want in zip(out[:, :, at:at + n + c], s.layer.read(o, n + c)):
+            assert torch.equal(got.cpu(), torch.from_numpy(want.astype(np.float32)).to(TD[dtype]))
+        at += n + c
