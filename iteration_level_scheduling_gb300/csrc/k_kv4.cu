@@ -157,9 +157,9 @@ __device__ __forceinline__ uint32_t kv4_quantise(const float *x, uint32_t *par) 
 // slots share a pair (then V goes out in whole words)
 //
 // Bound by issue (80 % of active cycles; 25 warp instructions per 32 components,
-// 5 of them for halves): 10.5 k rows of 40 heads of 128, bf16, 89 us under the
-// profiler for 215 MB read and 67 MB written (42 us at the copy rate); with an
-// IEEE quotient per component 189.
+// 5 of them for halves): 10.5 k rows of 40 heads of 128, bf16, 81 us for 215 MB
+// read and 67 MB written (42 us at the copy rate); with an IEEE quotient per
+// component 189.
 // ---------------------------------------------------------------------------
 constexpr int kApThreads = 128;
 
@@ -169,16 +169,26 @@ __device__ __forceinline__ void load8_stream(const T *p, float *x) {
     for (int i = 0; i < 8; i += Elem<T>::kPer16) load16_stream(p + i, x + i);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kApThreads) kv4_append_kernel(const T *qkv, const int32_t *units, Kv4View v, int H) {
+// Flat: the threads of a block run on from unit to unit (a row whose H / 8 is no multiple of the block's threads would
+// leave the rest of them idle; 5 x <= 333 rows of 12 heads of 32, fp32: 4.2 -> 3.0 us).  A group's threads stay in one
+// unit.
+template <typename T, int D, bool Flat>
+__global__ void __launch_bounds__(kApThreads) kv4_append_kernel(const T *qkv, const int32_t *units, int n_units, Kv4View v,
+                                                                int H) {
     constexpr int G = D >= 32 ? D / 32 : 1, GT = D / G / 8;
     pdl_trigger();
     pdl_wait();
-    const int4 un = reinterpret_cast<const int4 *>(units)[blockIdx.x];  // first row, its slot, rows (1, or 2 in one pair)
-    const int64_t slot = un.y;
+    int unit, c;  // c: component of the row
+    if constexpr (Flat) {
+        const int64_t i = (int64_t)blockIdx.x * kApThreads + threadIdx.x;
+        unit = (int)(i / (H / 8)), c = (int)(i - (int64_t)unit * (H / 8)) * 8;
+    } else {
+        unit = blockIdx.x, c = (blockIdx.y * kApThreads + threadIdx.x) * 8;
+    }
+    const bool on = unit < n_units;
+    const int4 un = on ? reinterpret_cast<const int4 *>(units)[unit] : make_int4(0, 0, 0, 0);  // first row, its slot,
+    const int64_t slot = un.y;                                                                 // rows (1, or 2 in one pair)
     const bool two = un.z == 2;
-    const int c = (blockIdx.y * kApThreads + threadIdx.x) * 8;  // component of the row; whole warps pass the end together
-    const bool on = c < H;                                      // or by groups
     float x[4][8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // k, v of the first row; of the second
@@ -196,27 +206,27 @@ __global__ void __launch_bounds__(kApThreads) kv4_append_kernel(const T *qkv, co
         *reinterpret_cast<uint32_t *>(v.kc + row * (D / 2) + dd / 2) = w[0];
         if (lead) v.kp[row * G + g] = par[0];
     }
-    if (two) {
+    if (!Flat ? two : __any_sync(0xffffffffu, two)) {
         w[0] = kv4_quantise<GT>(x[2], &par[0]);
-        if (on) {
+        if (two) {
             *reinterpret_cast<uint32_t *>(v.kc + (row + 1) * (D / 2) + dd / 2) = w[0];
             if (lead) v.kp[(row + 1) * G + g] = par[0];
         }
         w[0] = kv4_quantise<GT>(x[1], &par[0]);
         w[1] = kv4_quantise<GT>(x[3], &par[1]);
-        if (on) {
+        if (two) {
             *reinterpret_cast<uint2 *>(v.vc + pair * D + dd) =
                 make_uint2((w[0] & 0xffffu) | (w[1] << 16), (w[0] >> 16) | (w[1] & 0xffff0000u));
             if (lead) *reinterpret_cast<uint2 *>(v.vp + (pair * G + g) * 2) = make_uint2(par[0], par[1]);
         }
     } else {
         w[0] = kv4_quantise<GT>(x[1], &par[0]);
-        if (on) {
-            uint16_t *dst = reinterpret_cast<uint16_t *>(v.vc + pair * D + dd) + (slot & 1);
-            dst[0] = (uint16_t)w[0];
-            dst[2] = (uint16_t)(w[0] >> 16);
-            if (lead) v.vp[(pair * G + g) * 2 + (slot & 1)] = par[0];
-        }
+    }
+    if (on && !two) {
+        uint16_t *dst = reinterpret_cast<uint16_t *>(v.vc + pair * D + dd) + (slot & 1);
+        dst[0] = (uint16_t)w[0];
+        dst[2] = (uint16_t)(w[0] >> 16);
+        if (lead) v.vp[(pair * G + g) * 2 + (slot & 1)] = par[0];
     }
 }
 
@@ -1743,10 +1753,13 @@ cudaError_t for_dim(int d, F f) {
 template <typename T>
 cudaError_t append(const void *qkv, const Kv4View &v, const int32_t *hp, const int32_t *dp, cudaStream_t st) {
     const int H = hp[Q_HEADS] * hp[Q_DIM];
-    const dim3 grid(hp[Q_UNITS], (H / 8 + kApThreads - 1) / kApThreads);
+    const int per = H / 8, n = hp[Q_UNITS];  // threads of a unit
     return for_dim(hp[Q_DIM], [&](auto d) {
-        return launch_pdl(kv4_append_kernel<T, d()>, grid, dim3(kApThreads), 0, st, (const T *)qkv, dp + hp[Q_O_UNITS], v,
-                          H);
+        if (per % kApThreads == 0)
+            return launch_pdl(kv4_append_kernel<T, d(), false>, dim3(n, per / kApThreads), dim3(kApThreads), 0, st,
+                              (const T *)qkv, dp + hp[Q_O_UNITS], n, v, H);
+        return launch_pdl(kv4_append_kernel<T, d(), true>, dim3((unsigned)(((int64_t)n * per + kApThreads - 1) / kApThreads)),
+                          dim3(kApThreads), 0, st, (const T *)qkv, dp + hp[Q_O_UNITS], n, v, H);
     });
 }
 
