@@ -388,6 +388,18 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
         if constexpr (Held) return val[i];
         else return sp_logit(Elem<T>::to_f(row[i]));
     };
+    // logits i .. i + 3 below `end` (a multiple of four, or n; held rows are padded to a multiple of four with -inf)
+    auto load4 = [&](int i, int end, float *l) {
+        if (i >= end) return;
+        if constexpr (Held) {
+            const float4 x = *reinterpret_cast<const float4 *>(val + i);
+            l[0] = x.x, l[1] = x.y, l[2] = x.z, l[3] = x.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < end) l[e] = at(i + e);
+        }
+    };
     // f(i, logit) for every id of this CTA, in any order (held rows are padded to a multiple of four with -inf)
     auto each = [&](auto f) {
         if constexpr (Held) {
@@ -403,13 +415,9 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
     auto each4 = [&](auto f) {
         for (int i = 4 * tid; i < n; i += 4 * kSpThreads) {
             float l[4];
-            if constexpr (Held) {
-                const float4 x = *reinterpret_cast<const float4 *>(val + i);
-                l[0] = x.x, l[1] = x.y, l[2] = x.z, l[3] = x.w;
-            } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) l[e] = i + e < n ? at(i + e) : -INFINITY;
-            }
+            for (int e = 0; e < 4; ++e) l[e] = -INFINITY;
+            load4(i, n, l);
             f(i, l);
         }
     };
@@ -522,16 +530,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
             float l[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) l[e] = -INFINITY;
-            if (i < i1) {
-                if constexpr (Held) {
-                    const float4 x = *reinterpret_cast<const float4 *>(val + i);
-                    l[0] = x.x, l[1] = x.y, l[2] = x.z, l[3] = x.w;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (i + e < i1) l[e] = at(i + e);
-                }
-            }
+            load4(i, i1, l);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 g(l[e]);
@@ -712,13 +711,13 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
     // and id ascending those whose mass in front is below `want` (share_of_most: p times the mass of the `most`).
     auto finish = [&](int m, int most, u64 want, bool share_of_most) {
         block_sort<false>(sm.list, m, 0ull);
-        u64 w[2], c[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int j = 2 * tid + e;
-            w[e] = c[e] = j < most ? weight(sp_value((uint32_t)(sm.list[j] >> 32))) : 0ull;
-            sm.mass[j] = w[e];
+        u64 w[2] = {0, 0}, c[2];
+        if (2 * tid < most) {
+            weights(sp_value((uint32_t)(sm.list[2 * tid] >> 32)), sp_value((uint32_t)(sm.list[2 * tid + 1] >> 32)), w);
+            if (2 * tid + 1 >= most) w[1] = 0;
         }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) c[e] = sm.mass[2 * tid + e] = w[e];
         block_scan2(c[0], c[1], sm.wsum);
         if (share_of_most) {
             if (tid == kSpThreads - 1) sm.sh.total = c[1];
@@ -731,6 +730,43 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
         const int kept = __syncthreads_count(keep[0]) + __syncthreads_count(keep[1]);  // a prefix
         if (2 * tid == kept - 1) sm.sh.total = c[0];
         if (2 * tid + 1 == kept - 1) sm.sh.total = c[1];
+        if (kept > 128) {
+            // the id by its upper, then its lower bits: masses per digit, and the one in which u times the total lies
+            // (sorted by id instead, 5 500 to 8 200 cycles: one row of 4486 at top-p 0.9 17.3 us, now 16.1)
+            const int shift = max(0, 22 - __clz(a.V - 1));  // (at most 2^10 digits each)
+            uint32_t digit = 0;
+            u64 target = 0;
+            for (int level = 0; level < 2; ++level) {
+                __syncthreads();
+                if (level == 0) target = __umul64hi(frac64(u), sm.sh.total);
+                *reinterpret_cast<uint2 *>(sm.lo + 2 * tid) = *reinterpret_cast<uint2 *>(sm.hi + 2 * tid) = make_uint2(0, 0);
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (!keep[e]) continue;
+                    const uint32_t id = ~(uint32_t)sm.list[2 * tid + e];
+                    if (level == 1 && id >> shift != digit) continue;
+                    const uint32_t b = level == 0 ? id >> shift : id & ((1u << shift) - 1u);
+                    const uint32_t wl = (uint32_t)w[e], old = atomicAdd(&sm.lo[b], wl);
+                    const uint32_t wh = (uint32_t)(w[e] >> 32) + (old + wl < old);
+                    if (wh) atomicAdd(&sm.hi[b], wh);
+                }
+                __syncthreads();
+                u64 x[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) x[e] = c[e] = (u64)sm.hi[2 * tid + e] << 32 | sm.lo[2 * tid + e];
+                block_scan2(c[0], c[1], sm.wsum);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (c[e] - x[e] <= target && target < c[e]) {
+                        sm.sh.bin = 2 * tid + e, sm.sh.want = target - (c[e] - x[e]);
+                        if (level == 1) a.out[r] = (int32_t)(digit << shift | (uint32_t)(2 * tid + e));
+                    }
+                __syncthreads();
+                digit = sm.sh.bin, target = sm.sh.want;
+            }
+            return;
+        }
         // the kept ones in the order of their ids
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -887,13 +923,9 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
     } else {
         for (int i = i0 + 4 * lane; i < i1; i += 128) {
             float l[4];
-            if constexpr (Held) {
-                const float4 x = *reinterpret_cast<const float4 *>(val + i);
-                l[0] = x.x, l[1] = x.y, l[2] = x.z, l[3] = x.w;
-            } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) l[e] = i + e < i1 ? at(i + e) : -INFINITY;
-            }
+            for (int e = 0; e < 4; ++e) l[e] = -INFINITY;
+            load4(i, i1, l);
             u64 w[4];
             weights(l[0], l[1], w), weights(l[2], l[3], w + 2);
 #pragma unroll
@@ -914,42 +946,79 @@ __global__ void __launch_bounds__(kSpThreads, 2) sample_kernel(const SampleArgs 
     auto stretch = [&](u64 sx, uint32_t cx, uint32_t seen) {
         return sx + wt * (seen < ties ? min(ties - seen, cx) : 0u);
     };
-    u64 all = 0, start = 0;
+    u64 all = 0, start = 0, mine = 0;
     uint32_t seen = 0, before = 0;
     for (int x = 0; x < C; ++x) {
-        if (x == rank) start = all, before = seen;
-        all += stretch(sm.sh.sum[x], sm.sh.first[x], seen);
+        const u64 part = stretch(sm.sh.sum[x], sm.sh.first[x], seen);
+        if (x == rank) start = all, before = seen, mine = part;
+        all += part;
         seen += sm.sh.first[x];
     }
+    const u64 target = __umul64hi(frac64(u), all);
+    if (target < start || target >= start + mine) return;  // (the whole CTA)
     for (int w = 0; w < warp; ++w) {
         start += stretch(sm.wsum[w], sm.wcnt[w], before);
         before += sm.wcnt[w];
     }
-    const u64 target = __umul64hi(frac64(u), all);
-    if (target >= start && target < start + stretch(s, c, before)) {
-        u64 sum = start;
-        for (int b = i0; b < i1; b += 32) {
-            const float l = b + lane < i1 ? at(b + lane) : -INFINITY;
-            u64 x = 0;
-            if (l > cut) {
-                x = weight(l);
-                if (x < least) x = 0;
-            }
-            const uint32_t mask = __ballot_sync(kAll, tied && l == cut);
-            if (tied && l == cut && before + __popc(mask & ((1u << lane) - 1u)) < ties) x = wt;
-            before += __popc(mask);
+    if (lane == 0 && target >= start && target < start + stretch(s, c, before))
+        sm.sh.bin = (uint32_t)warp, sm.sh.want = start, sm.sh.found = before;
+    __syncthreads();
+    // all warps look through the stretch in which it lies, four ids a thread (the warp alone, 32 ids at a time: one row
+    // of 102018 in bf16 without a filter 18.6 us, now 13.7)
+    const int j0 = min(n, (int)sm.sh.bin * per_warp), j1 = min(n, j0 + per_warp);
+    u64 sum = sm.sh.want;
+    seen = sm.sh.found;
+    auto scan = [&](u64 v, u64 &total) {  // inclusive, over the block
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const u64 y = __shfl_up_sync(kAll, x, o);
-                if (lane >= o) x += y;
-            }
-            const uint32_t hit = __ballot_sync(kAll, sum + x > target);
-            if (hit) {
-                if (lane == 0) a.out[r] = first + b + __ffs(hit) - 1;
-                break;
-            }
-            sum += __shfl_sync(kAll, x, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 y = __shfl_up_sync(kAll, v, o);
+            if (lane >= o) v += y;
         }
+        __syncthreads();
+        if (lane == 31) sm.wsum[warp] = v;
+        __syncthreads();
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < kSpWarps; ++w) {
+            const u64 y = sm.wsum[w];
+            v += w < warp ? y : 0ull;
+            total += y;
+        }
+        return v;
+    };
+    for (int b = j0; b < j1; b += 4 * kSpThreads) {
+        const int i = b + 4 * tid;
+        float l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l[e] = -INFINITY;
+        load4(i, j1, l);
+        u64 w[4] = {0, 0, 0, 0}, x = 0, total;
+        if (i < j1) weights(l[0], l[1], w), weights(l[2], l[3], w + 2);
+        if (tied) {
+            uint32_t equal = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) equal += l[e] == cut;
+            uint32_t place = seen + (uint32_t)scan(equal, total) - equal;
+            seen += (uint32_t)total;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (l[e] < cut) w[e] = 0;
+                if (l[e] == cut) w[e] = place++ < ties ? wt : 0ull;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (w[e] < least) w[e] = 0;
+            x += w[e];
+        }
+        u64 to = sum + scan(x, total) - x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (to <= target && target < to + w[e]) a.out[r] = first + i + e;
+            to += w[e];
+        }
+        sum += total;
+        if (target < sum) break;
     }
 }
 
