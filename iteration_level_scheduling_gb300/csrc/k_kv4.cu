@@ -1127,20 +1127,30 @@ __global__ void __launch_bounds__(kKvThreads, kDecodeCtas) kv4_decode_mma_kernel
 // 7.6 us at the copy rate; the schedulers issue in 51 % of active cycles, three CTAs of 168 registers per SM.
 constexpr int kRowsPerItem = 16;
 
-template <int D>
+template <typename T, int D>
 struct Kv4RowsMerge {
+    static constexpr int Q = std::is_same<T, float>::value ? 3 : 1;  // bf16 parts of q
     float m[kKvWarps][kRowsPerItem], l[kKvWarps][kRowsPerItem];
     float o[kKvWarps][kRowsPerItem][D];
-    uint4 q[D / 32][2][32];  // q as the A operand: group, half of it, lane
+    uint4 q[Q][D >= 32 ? D / 32 : 1][2][32];  // q as the A operand: part, group, half of it, lane
 };
 
+// The bf16 nearest to two floats; what it leaves of them stays.
+__device__ __forceinline__ uint32_t bf_part(float &a, float &b) {
+    const uint32_t u = pack2(a, b);
+    a -= bf_lo(u), b -= bf_hi(u);
+    return u;
+}
+
 // Half: every item of the launch has at most 8 rows, and the A operand's rows 8 .. 15 are zero.
-template <int D, bool Half>
+template <typename T, int D, bool Half>
 __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4Attn a) {
-    constexpr int W = D / 32;  // groups
+    constexpr bool F32 = std::is_same<T, float>::value;
+    constexpr int W = D >= 32 ? D / 32 : 1;  // groups
     constexpr int R = Half ? 1 : 2;  // row g, and g + 8
     constexpr unsigned kAll = 0xffffffffu;
-    __shared__ Kv4RowsMerge<D> sm;
+    using Merge = Kv4RowsMerge<T, D>;
+    __shared__ Merge sm;
     pdl_trigger();
     pdl_wait();
     // first slot, keys, first row, rows | the rows' chunks, this chunk, first partial, - | keys row 0 sees
@@ -1159,8 +1169,11 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-            if (i < R && g + 8 * i < rows)
-                load16((const bf16 *)a.qkv + (size_t)(r0.z + g + 8 * i) * 3 * a.H + h * D + 32 * y + 8 * t, x[i]);
+            if (i < R && g + 8 * i < rows && 32 * y + 8 * t < D) {
+                const T *q = (const T *)a.qkv + (size_t)(r0.z + g + 8 * i) * 3 * a.H + h * D + 32 * y + 8 * t;
+#pragma unroll
+                for (int e = 0; e < 8; e += Elem<T>::kPer16) load16(q + e, x[i] + e);
+            }
             float s = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) s += x[i][e];
@@ -1170,10 +1183,13 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            if (warp == (2 * y + k) % kKvWarps)
-                sm.q[y][k][lane] = make_uint4(pack2(x[0][2 * k], x[0][2 * k + 4]), pack2(x[1][2 * k], x[1][2 * k + 4]),
-                                              pack2(x[0][2 * k + 1], x[0][2 * k + 5]),
-                                              pack2(x[1][2 * k + 1], x[1][2 * k + 5]));
+            if (warp == (2 * y + k) % kKvWarps) {
+#pragma unroll
+                for (int n = 0; n < Merge::Q; ++n)
+                    sm.q[n][y][k][lane] = make_uint4(bf_part(x[0][2 * k], x[0][2 * k + 4]), bf_part(x[1][2 * k], x[1][2 * k + 4]),
+                                                     bf_part(x[0][2 * k + 1], x[0][2 * k + 5]),
+                                                     bf_part(x[1][2 * k + 1], x[1][2 * k + 5]));
+            }
     }
     __syncthreads();
     float m[2] = {kLow, kLow}, l[2] = {0.f, 0.f}, zero[W][2], o[W][4][4];
@@ -1200,7 +1216,10 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
             const uint32_t *kc = reinterpret_cast<const uint32_t *>(a.v.kc + (row + g + 8 * i) * (D / 2)) + t;
             const uint32_t *vc = reinterpret_cast<const uint32_t *>(a.v.vc + (pair + t + 4 * i) * D) + g;
 #pragma unroll
-            for (int y = 0; y < W; ++y) kw[i][y] = kc[4 * y], vw[i][y] = vc[8 * y];
+            for (int y = 0; y < W; ++y) {
+                kw[i][y] = D >= 32 || t < D / 8 ? kc[4 * y] : 0u;  // (q is zero there)
+                vw[i][y] = D >= 32 || g < D / 4 ? vc[8 * y] : 0u;  // (columns that are not used)
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) load_words<W>(a.v.kp + (row + 8 * i + 2 * t + e) * W, kp[2 * i + e]);
             if constexpr (W == 4) {
@@ -1217,14 +1236,26 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
             sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
 #pragma unroll
             for (int y = 0; y < W; ++y) {
-                float c[4] = {-128.f * qsum[y][0], -128.f * qsum[y][0], -128.f * qsum[y][1], -128.f * qsum[y][1]};
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
                 const uint32_t w = kw[i][y];
-                const uint4 qa = sm.q[y][0][lane], qb = sm.q[y][1][lane];
-                kv4_mma(c, qa.x, qa.y, qa.z, qa.w, code_pair<0>(w), code_pair<1>(w));
-                kv4_mma(c, qb.x, qb.y, qb.z, qb.w, code_pair<2>(w), code_pair<3>(w));
+                if constexpr (F32) {
+                    const uint32_t b[4] = {code_pair_centred<0>(w), code_pair_centred<1>(w), code_pair_centred<2>(w),
+                                           code_pair_centred<3>(w)};
+#pragma unroll
+                    for (int n = Merge::Q - 1; n >= 0; --n) {
+                        const uint4 qa = sm.q[n][y][0][lane], qb = sm.q[n][y][1][lane];
+                        kv4_mma(c, qa.x, qa.y, qa.z, qa.w, b[0], b[1]);
+                        kv4_mma(c, qb.x, qb.y, qb.z, qb.w, b[2], b[3]);
+                    }
+                } else {
+                    c[0] = c[1] = -128.f * qsum[y][0], c[2] = c[3] = -128.f * qsum[y][1];
+                    const uint4 qa = sm.q[0][y][0][lane], qb = sm.q[0][y][1][lane];
+                    kv4_mma(c, qa.x, qa.y, qa.z, qa.w, code_pair<0>(w), code_pair<1>(w));
+                    kv4_mma(c, qb.x, qb.y, qb.z, qb.w, code_pair<2>(w), code_pair<3>(w));
+                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float s = bf_lo(kp[2 * i + e][y]), z = bf_hi(kp[2 * i + e][y]);
+                    const float s = bf_lo(kp[2 * i + e][y]), z0 = bf_hi(kp[2 * i + e][y]), z = F32 ? fmaf(8.f, s, z0) : z0;
                     sc[i][e] = fmaf(s, c[e], fmaf(z, qsum[y][0], sc[i][e]));
                     if (!Half) sc[i][2 + e] = fmaf(s, c[2 + e], fmaf(z, qsum[y][1], sc[i][2 + e]));
                 }
@@ -1278,7 +1309,7 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
 #pragma unroll
         for (int y = 0; y < W; ++y) {
             // A: rows g, g + 8 at keys 2t, 2t + 1 (a0, a1) and 2t + 8, 2t + 9 (a2, a3)
-            uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+            uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u}, rest[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float se = bf_lo(vp[i][2 * y]), me = bf_hi(vp[i][2 * y]), so = bf_lo(vp[i][2 * y + 1]),
@@ -1293,8 +1324,9 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
                         if (__float_as_uint(po) == 0x80000000u) wo = yo = 0.f;
                     }
                     zero[y][x] += ye + yo;
-                    hi[2 * i + x] = pack2(we, wo);
-                    lo[2 * i + x] = pack2(we - bf_lo(hi[2 * i + x]), wo - bf_hi(hi[2 * i + x]));
+                    hi[2 * i + x] = bf_part(we, wo);
+                    lo[2 * i + x] = bf_part(we, wo);
+                    if (F32) rest[2 * i + x] = pack2(we, wo);
                 }
             }
             const uint32_t c0[4] = {code_pair_centred<0>(vw[0][y]), code_pair_centred<1>(vw[0][y]),
@@ -1303,8 +1335,17 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
                                     code_pair_centred<2>(vw[1][y]), code_pair_centred<3>(vw[1][y])};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                kv4_mma(o[y][j], hi[0], hi[1], hi[2], hi[3], c0[j], c1[j]);
-                kv4_mma(o[y][j], lo[0], lo[1], lo[2], lo[3], c0[j], c1[j]);
+                if constexpr (F32) {  // (these 16 keys' sum by itself: the tensor core cuts off where fp32 rounds)
+                    float n[4] = {0.f, 0.f, 0.f, 0.f};
+                    kv4_mma(n, rest[0], rest[1], rest[2], rest[3], c0[j], c1[j]);
+                    kv4_mma(n, lo[0], lo[1], lo[2], lo[3], c0[j], c1[j]);
+                    kv4_mma(n, hi[0], hi[1], hi[2], hi[3], c0[j], c1[j]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[y][j][e] += n[e];
+                } else {
+                    kv4_mma(o[y][j], hi[0], hi[1], hi[2], hi[3], c0[j], c1[j]);
+                    kv4_mma(o[y][j], lo[0], lo[1], lo[2], lo[3], c0[j], c1[j]);
+                }
             }
         }
     }
@@ -1319,6 +1360,7 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
             z += __shfl_xor_sync(kAll, z, 1);
             z += __shfl_xor_sync(kAll, z, 2);
             // columns 2t and 2t + 1 of o[y][j]: components 32 y + 8 t + j and + 4
+            if (8 * t >= D) continue;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 sm.o[warp][g + 8 * i][32 * y + 8 * t + j] = o[y][j][2 * i] + z;
@@ -1340,7 +1382,7 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
             L += sm.l[w][j] * c, O += sm.o[w][j][d] * c;
         }
         if (nch == 1) {
-            ((bf16 *)a.out)[(size_t)(r0.z + j) * a.H + h * D + d] = __float2bfloat16_rn(O / L);
+            ((T *)a.out)[(size_t)(r0.z + j) * a.H + h * D + d] = Elem<T>::from_f(O / L);
         } else {
             float *mine = a.row_part + (((size_t)(r1.z + r1.y) * a.n_heads + h) * kRowsPerItem + j) * (D + 2);
             mine[d] = O;
@@ -1351,7 +1393,7 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
 
 // The chunks' partials of one group of rows and head, a warp per row.  (A launch of its own: the last block of a group
 // joining them alone took longer than the attention, 16 rows of 130 floats for every chunk.)
-template <int D>
+template <typename T, int D>
 __global__ void __launch_bounds__(32 * kRowsPerItem) kv4_rows_join_kernel(const Kv4Attn a) {
     pdl_trigger();
     pdl_wait();
@@ -1359,10 +1401,10 @@ __global__ void __launch_bounds__(32 * kRowsPerItem) kv4_rows_join_kernel(const 
     const int h = blockIdx.y, j = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (j >= r.y) return;
     const float *part = a.row_part + (((size_t)r.w * a.n_heads + h) * kRowsPerItem + j) * (D + 2);
-    bf16 *dst = (bf16 *)a.out + (size_t)(r.x + j) * a.H + h * D;
+    T *dst = (T *)a.out + (size_t)(r.x + j) * a.H + h * D;
 #pragma unroll
     for (int d = lane; d < D; d += 32)
-        dst[d] = __float2bfloat16_rn(kv4_join<D>(part, (size_t)a.n_heads * kRowsPerItem * (D + 2), r.z, d));
+        dst[d] = Elem<T>::from_f(kv4_join<D>(part, (size_t)a.n_heads * kRowsPerItem * (D + 2), r.z, d));
 }
 
 template <typename T>
@@ -1444,8 +1486,8 @@ struct Kv4Sizes {
 // How a request's rows are attended: on the prefill kernel, in groups of rows, or row by row.
 enum Kv4Form { kPromptForm, kGroupForm, kRowForm };
 Kv4Form form_of(const Kv4Batch &b, int i) {
-    if (b.dtype != 1 || b.n_input[i] == 1 || b.head_dim == 16) return kRowForm;
-    return b.n_input[i] >= kPromptRows && b.head_dim >= 64 ? kPromptForm : kGroupForm;
+    if (b.n_input[i] == 1) return kRowForm;
+    return b.n_input[i] >= kPromptRows && b.head_dim >= 64 && b.dtype == 1 ? kPromptForm : kGroupForm;
 }
 
 // Keys per work item of rows one by one: the largest chunk (a power of two,
@@ -1789,6 +1831,21 @@ cudaError_t kv4_read(const void *layer, const int32_t *hp, const int32_t *dp, vo
     return hp[Q_DTYPE] == 1 ? read<bf16>(v, hp, dp, out, st) : read<float>(v, hp, dp, out, st);
 }
 
+namespace {
+template <typename T>
+cudaError_t launch_rows(const Kv4Attn &a, int d, int items, bool half, int joins, int *launches, cudaStream_t st) {
+    const dim3 grid((unsigned)items * a.n_heads), block(kKvThreads);
+    return for_dim(d, [&](auto dim) {
+        const cudaError_t e = half ? launch_pdl(kv4_rows_mma_kernel<T, dim(), true>, grid, block, 0, st, a)
+                                   : launch_pdl(kv4_rows_mma_kernel<T, dim(), false>, grid, block, 0, st, a);
+        ++*launches;
+        if (e != cudaSuccess || joins == 0) return e;
+        ++*launches;
+        return launch_pdl(kv4_rows_join_kernel<T, dim()>, dim3(joins, a.n_heads), dim3(32 * kRowsPerItem), 0, st, a);
+    });
+}
+}  // namespace
+
 cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp, int32_t *dp, void *workspace,
                           void *out, unsigned *err, int *launches, cudaStream_t st) {
     const int nh = hp[Q_HEADS], d = hp[Q_DIM];
@@ -1814,20 +1871,10 @@ cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp,
         ++*launches;
     }
     if (e == cudaSuccess && hp[Q_RITEMS] > 0) {
-        const dim3 grid((unsigned)hp[Q_RITEMS] * nh), block(kKvThreads);
-        const dim3 joins(hp[Q_RJOINS], nh), join_block(32 * kRowsPerItem);
-        e = for_dim(d, [&](auto dim) {
-            if constexpr (dim() >= 32) {
-                const cudaError_t r = hp[Q_RHALF] ? launch_pdl(kv4_rows_mma_kernel<dim(), true>, grid, block, 0, st, a)
-                                                  : launch_pdl(kv4_rows_mma_kernel<dim(), false>, grid, block, 0, st, a);
-                if (r != cudaSuccess || hp[Q_RJOINS] == 0) return r;
-                ++*launches;
-                return launch_pdl(kv4_rows_join_kernel<dim()>, joins, join_block, 0, st, a);
-            } else {
-                return cudaErrorInvalidValue;
-            }
-        });
-        ++*launches;
+        auto run = [&](auto type) {
+            return launch_rows<decltype(type)>(a, d, hp[Q_RITEMS], hp[Q_RHALF] != 0, hp[Q_RJOINS], launches, st);
+        };
+        e = hp[Q_DTYPE] == 1 ? run(bf16()) : run(0.f);
     }
     if (e != cudaSuccess || hp[Q_PRE] == 0) return e;
     Kv4Prep pr;
