@@ -648,7 +648,7 @@ __device__ __forceinline__ void load_words(const void *p, uint32_t *w) {
     }
 }
 
-// Any type and head_dim, fp32 arithmetic (fp32 models; head_dim 16).  A warp
+// Single rows of any type and head_dim, fp32 arithmetic (fp32 models; head_dim 16).  A warp
 // takes 32 slots at a time: for the scores a lane owns a key and walks its
 // components against q in shared memory; for the values a lane owns four
 // components and walks the keys, two per word.  A code is used as the fp32
@@ -1116,12 +1116,15 @@ __global__ void __launch_bounds__(kKvThreads, kDecodeCtas) kv4_decode_mma_kernel
     kv4_finish<bf16, D>(a, sm, r0, r1, h);
 }
 
-// Up to 16 rows of one request at a time (bf16, head_dim 32 and more): the rows are the A operand's 16 rows, so
-// 16 keys are unpacked once for all of them.  Item = (16 rows, chunk of keys) x head, four warps taking 16 keys
-// each in turn.
+// Up to 16 rows of one request at a time: the rows are the A operand's 16 rows, so 16 keys are unpacked once for all
+// of them.  Item = (16 rows, chunk of keys) x head, four warps taking 16 keys each in turn.  A head of 16 components
+// is half a group, the rest of it zero.
 //   S    A = q, B = 128 + c of 8 keys; two MMAs per group of components, whose sums the key's s and m then apply to.
 //   O    A = p s of the group, as two bf16 (16 bits kept), B = c - 8 of 8 components of that group; the part of the
 //        minima, sum p (m + 8 s), in fp32.
+// fp32: q and the weights in three bf16 parts (24 bits), K's codes centred too, each 16 keys' sum added in fp32: errors
+// as in fp32 throughout.  4 requests of <= 200 rows over <= 500 keys, 30 heads of 128: 84 us, against 578 row by row
+// on kv4_decode_kernel; 30 heads of 16, 4 x <= 1000 rows over <= 800 keys, bf16: 198 and 1109.
 // P leaves the first product in the very registers that the second one takes it from.
 // Bound by issue and latency: 9 requests of <= 7 rows over <= 1500 keys, 32 heads of 128, 41 us (row by row 65), 51 MB:
 // 7.6 us at the copy rate; the schedulers issue in 51 % of active cycles, three CTAs of 168 registers per SM.
@@ -1479,15 +1482,31 @@ struct Kv4Sizes {
     int64_t ritems = 0, rsplits = 0, rparts = 0;
     int64_t pre = 0, pre_tiles = 0, pre_read = 0, pre_keys = 0;
     int chunk = 0, rchunk = 0;
+    bool grouped = false;
     int64_t off_ritems, off_rjoins, off_units, off_items, off_count, off_tiles, off_pre, off_pretiles, off_preread, off_reqoff, off_reqctx,
         off_reqws, total;
 };
 
 // How a request's rows are attended: on the prefill kernel, in groups of rows, or row by row.
 enum Kv4Form { kPromptForm, kGroupForm, kRowForm };
-Kv4Form form_of(const Kv4Batch &b, int i) {
-    if (b.n_input[i] == 1) return kRowForm;
+Kv4Form form_of(const Kv4Batch &b, int i, bool grouped) {
+    if (b.n_input[i] == 1) return grouped ? kGroupForm : kRowForm;
     return b.n_input[i] >= kPromptRows && b.head_dim >= 64 && b.dtype == 1 ? kPromptForm : kGroupForm;
+}
+
+// Single rows among groups of rows: in a launch of their own, or, while that would take longer to start and to end than
+// its keys are worth, as groups of one row.  One request of 5 rows and single rows of so many keys x heads in all, bf16,
+// as groups and apart: head_dim 64, 23k 8.1 and 14.5 us, 187k 15.9 and 18.1, 316k 23.9 and 21.2, 1220k 62 and 39;
+// head_dim 128, 187k 24.4 and 24.8, 316k 37 and 31; fp32, 64: 187k 18.4 and 22.8, 316k 28 and 27.
+constexpr int64_t kGroupedKeys = 200000;
+bool singles_grouped(const Kv4Batch &b) {
+    int64_t keys = 0;
+    bool groups = false;
+    for (int i = 0; i < b.n_req; ++i) {
+        if (b.n_input[i] == 1) keys += b.ctx_len[i] + (int64_t)1;
+        else groups |= form_of(b, i, false) == kGroupForm;
+    }
+    return groups && keys * b.n_heads <= kGroupedKeys;
 }
 
 // Keys per work item of rows one by one: the largest chunk (a power of two,
@@ -1495,13 +1514,13 @@ Kv4Form form_of(const Kv4Batch &b, int i) {
 // chunks cost a join: 16 requests of 300 keys, 40 heads of 128, took 18.2 us at
 // six blocks per SM and 11.5 at three, one of 100 keys 5.1 us in chunks of 64 and
 // 3.2 in one; one of 4000 keys 17.1 us at six, 13.8 at three, 19.7 at one.
-int kv4_row_chunk(const Kv4Batch &b, int num_sms) {
+int kv4_row_chunk(const Kv4Batch &b, bool grouped, int num_sms) {
     const int64_t most = 3LL * num_sms;
     int chunk = 2048;
     while (chunk > 128) {
         int64_t items = 0;
         for (int i = 0; i < b.n_req && items * b.n_heads < most; ++i)
-            if (form_of(b, i) == kRowForm)
+            if (form_of(b, i, grouped) == kRowForm)
                 items += (int64_t)b.n_input[i] * ((b.ctx_len[i] + (int64_t)b.n_input[i] + chunk - 1) / chunk);
         if (items * b.n_heads >= most) break;
         chunk /= 2;
@@ -1516,7 +1535,7 @@ int kv4_row_chunk(const Kv4Batch &b, int num_sms) {
 // launch that joins chunks.  (9 requests of <= 7 rows over <= 1500 keys, 32 heads:
 // 43.0 us in chunks of 512, 38.3 of 256, 51.2 of 1024; 8 requests of 2 rows over
 // 300 keys, 40 heads: 13.4 us whole, 18.6 in chunks of 256.)
-int kv4_group_chunk(const Kv4Batch &b, int num_sms) {
+int kv4_group_chunk(const Kv4Batch &b, bool grouped, int num_sms) {
     const int64_t at_once = 3LL * num_sms;
     int best = 2048;
     double best_time = 0;
@@ -1524,7 +1543,7 @@ int kv4_group_chunk(const Kv4Batch &b, int num_sms) {
         int64_t keys = 0, items = 0, longest = 0;
         bool split = false;
         for (int i = 0; i < b.n_req; ++i) {
-            if (form_of(b, i) != kGroupForm) continue;
+            if (form_of(b, i, grouped) != kGroupForm) continue;
             const int64_t groups = (b.n_input[i] + kRowsPerItem - 1) / kRowsPerItem, k = b.ctx_len[i] + b.n_input[i];
             keys += groups * k;
             items += groups * ((k + chunk - 1) / chunk);
@@ -1545,15 +1564,16 @@ bool kv4_sizes(const Kv4Batch &b, int num_sms, Kv4Sizes *z) {
         rows += n;
         if (rows > INT32_MAX / 8) return false;
     }
-    z->chunk = kv4_row_chunk(b, num_sms);
-    z->rchunk = kv4_group_chunk(b, num_sms);
+    const bool grouped = z->grouped = singles_grouped(b);
+    z->chunk = kv4_row_chunk(b, grouped, num_sms);
+    z->rchunk = kv4_group_chunk(b, grouped, num_sms);
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i];
         z->rows += n;
         z->keys += c + n;
         z->units += n / 2 + (n % 2 || (b.kv_offset[i] + c) % 2 ? 1 : 0);
         z->tiles += (c + n + kReadTile - 1) / kReadTile;
-        const Kv4Form form = form_of(b, i);
+        const Kv4Form form = form_of(b, i, grouped);
         if (form == kPromptForm) {
             z->pre++;
             z->pre_tiles += (n + kPrefillRowsPerTile - 1) / kPrefillRowsPerTile;
@@ -1633,7 +1653,7 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     int32_t most = 0;
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i], o = b.kv_offset[i];
-        const Kv4Form form = form_of(b, i);
+        const Kv4Form form = form_of(b, i, z.grouped);
         const bool prompt = form == kPromptForm;
         req_off[i] = (int32_t)row;
         req_ctx[i] = (int32_t)c;
