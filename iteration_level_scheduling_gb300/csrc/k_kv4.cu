@@ -1470,28 +1470,43 @@ enum : int {
     Q_O_REQWS,  // a prompt's first slot in the workspace's pool
     Q_TILEMOST,  // slots of the longest read-back tile
 };
-// Requests of at least this many rows run on the prefill kernel (bf16, head_dim 64 or 128).  8 requests over 2000 keys,
-// 40 heads of 128: 16 rows 89 us in groups and 174 on it, 32 rows 144 and 176, 48 rows 199 and 177; one request over
-// 300 keys: 32 rows 15 and 21 us, 64 rows 21 and 21.
-constexpr int kPromptRows = 33;
-
 int64_t up4(int64_t w) { return (w + 3) & ~int64_t(3); }
-
-struct Kv4Sizes {
-    int64_t rows = 0, units = 0, items = 0, splits = 0, parts = 0, tiles = 0, keys = 0;
-    int64_t ritems = 0, rsplits = 0, rparts = 0;
-    int64_t pre = 0, pre_tiles = 0, pre_read = 0, pre_keys = 0;
-    int chunk = 0, rchunk = 0;
-    bool grouped = false;
-    int64_t off_ritems, off_rjoins, off_units, off_items, off_count, off_tiles, off_pre, off_pretiles, off_preread, off_reqoff, off_reqctx,
-        off_reqws, total;
-};
 
 // How a request's rows are attended: on the prefill kernel, in groups of rows, or row by row.
 enum Kv4Form { kPromptForm, kGroupForm, kRowForm };
-Kv4Form form_of(const Kv4Batch &b, int i, bool grouped) {
-    if (b.n_input[i] == 1) return grouped ? kGroupForm : kRowForm;
-    return b.n_input[i] >= kPromptRows && b.head_dim >= 64 && b.dtype == 1 ? kPromptForm : kGroupForm;
+enum Kv4Several { kAllGroups, kAllPrompts, kByRequest };  // requests of several rows
+struct Kv4Policy {
+    Kv4Several several = kAllGroups;
+    bool singles_grouped = false;
+};
+bool prompts_possible(const Kv4Batch &b) { return b.dtype == 1 && b.head_dim >= 64; }
+
+// Time of the two forms (us), by a model of their launches: a start (prompts: of three more), a time per key of the
+// longest request (its chunks, or the walk of one tile of 128 rows over it), and a time per key, head and group of 16
+// rows, or tile of 128, that reads it.  Measured at 152 SMs, 4 requests of <= 20 / 40 / 60 / 100 / 200 rows over <= 1500
+// keys, 30 heads: of 64, in groups 22 / 31 / 44 / 59 / 108 us and as prompts 33 / 35 / 35 / 35 / 49; of 128, 37 / 52 / 75 /
+// 100 / 185 and 49 / 54 / 55 / 56 / 75; one request of 200 rows alone, 5 heads of 128, 10 and 16.
+struct Kv4Cost {
+    struct {
+        double start, longest, each;
+    } group, tile;
+};
+Kv4Cost cost_of(const Kv4Batch &b) {
+    return b.head_dim == 64 ? Kv4Cost{{4.5, 0.0045, 65e-6}, {11, 0.0085, 90e-6}}
+                            : Kv4Cost{{5, 0.0085, 110e-6}, {13, 0.011, 210e-6}};
+}
+double group_time(const Kv4Batch &b, int i) {
+    const double n = b.n_input[i], g = (b.n_input[i] + kRowsPerItem - 1) / kRowsPerItem;
+    return cost_of(b).group.each * b.n_heads * (g * b.ctx_len[i] + kRowsPerItem / 2 * g * (g - 1) + n);
+}
+double tile_time(const Kv4Batch &b, int i) {
+    const double n = b.n_input[i], t = (b.n_input[i] + kPrefillRowsPerTile - 1) / kPrefillRowsPerTile;
+    return cost_of(b).tile.each * b.n_heads * (t * b.ctx_len[i] + kPrefillRowsPerTile / 2 * t * (t - 1) + n);
+}
+Kv4Form form_of(const Kv4Batch &b, int i, const Kv4Policy &p) {
+    if (b.n_input[i] == 1) return p.singles_grouped ? kGroupForm : kRowForm;
+    return p.several == kAllPrompts || (p.several == kByRequest && tile_time(b, i) < group_time(b, i)) ? kPromptForm
+                                                                                                     : kGroupForm;
 }
 
 // Single rows among groups of rows: in a launch of their own, or, while that would take longer to start and to end than
@@ -1499,28 +1514,57 @@ Kv4Form form_of(const Kv4Batch &b, int i, bool grouped) {
 // as groups and apart: head_dim 64, 23k 8.1 and 14.5 us, 187k 15.9 and 18.1, 316k 23.9 and 21.2, 1220k 62 and 39;
 // head_dim 128, 187k 24.4 and 24.8, 316k 37 and 31; fp32, 64: 187k 18.4 and 22.8, 316k 28 and 27.
 constexpr int64_t kGroupedKeys = 200000;
-bool singles_grouped(const Kv4Batch &b) {
+Kv4Policy policy_of(const Kv4Batch &b) {
+    Kv4Policy p;
+    if (prompts_possible(b)) {
+        const Kv4Cost c = cost_of(b);
+        double groups = 0, tiles = 0, longest = 0;  // of all
+        double some_groups = 0, some_tiles = 0, longest_group = 0, longest_tile = 0;  // each request as it is cheaper
+        for (int i = 0; i < b.n_req; ++i) {
+            if (b.n_input[i] == 1) continue;
+            const double g = group_time(b, i), t = tile_time(b, i), keys = (double)b.ctx_len[i] + b.n_input[i];
+            groups += g, tiles += t, longest = std::max(longest, keys);
+            if (t < g) some_tiles += t, longest_tile = std::max(longest_tile, keys);
+            else some_groups += g, longest_group = std::max(longest_group, keys);
+        }
+        const double as_groups = c.group.start + c.group.longest * longest + groups,
+                     as_prompts = c.tile.start + c.tile.longest * longest + tiles,
+                     split = c.group.start + c.group.longest * longest_group + some_groups + c.tile.start +
+                             c.tile.longest * longest_tile + some_tiles;
+        if (std::min(as_prompts, split) < as_groups) p.several = as_prompts <= split ? kAllPrompts : kByRequest;
+    }
     int64_t keys = 0;
-    bool groups = false;
+    bool any = false;
     for (int i = 0; i < b.n_req; ++i) {
         if (b.n_input[i] == 1) keys += b.ctx_len[i] + (int64_t)1;
-        else groups |= form_of(b, i, false) == kGroupForm;
+        else any |= form_of(b, i, p) == kGroupForm;
     }
-    return groups && keys * b.n_heads <= kGroupedKeys;
+    p.singles_grouped = any && keys * b.n_heads <= kGroupedKeys;
+    return p;
 }
+
+struct Kv4Sizes {
+    int64_t rows = 0, units = 0, items = 0, splits = 0, parts = 0, tiles = 0, keys = 0;
+    int64_t ritems = 0, rsplits = 0, rparts = 0;
+    int64_t pre = 0, pre_tiles = 0, pre_read = 0, pre_keys = 0;
+    int chunk = 0, rchunk = 0;
+    Kv4Policy policy;
+    int64_t off_ritems, off_rjoins, off_units, off_items, off_count, off_tiles, off_pre, off_pretiles, off_preread, off_reqoff, off_reqctx,
+        off_reqws, total;
+};
 
 // Keys per work item of rows one by one: the largest chunk (a power of two,
 // 128 .. 2048 keys) that still gives every SM three blocks of four warps.  Short
 // chunks cost a join: 16 requests of 300 keys, 40 heads of 128, took 18.2 us at
 // six blocks per SM and 11.5 at three, one of 100 keys 5.1 us in chunks of 64 and
 // 3.2 in one; one of 4000 keys 17.1 us at six, 13.8 at three, 19.7 at one.
-int kv4_row_chunk(const Kv4Batch &b, bool grouped, int num_sms) {
+int kv4_row_chunk(const Kv4Batch &b, const Kv4Policy &policy, int num_sms) {
     const int64_t most = 3LL * num_sms;
     int chunk = 2048;
     while (chunk > 128) {
         int64_t items = 0;
         for (int i = 0; i < b.n_req && items * b.n_heads < most; ++i)
-            if (form_of(b, i, grouped) == kRowForm)
+            if (form_of(b, i, policy) == kRowForm)
                 items += (int64_t)b.n_input[i] * ((b.ctx_len[i] + (int64_t)b.n_input[i] + chunk - 1) / chunk);
         if (items * b.n_heads >= most) break;
         chunk /= 2;
@@ -1535,7 +1579,7 @@ int kv4_row_chunk(const Kv4Batch &b, bool grouped, int num_sms) {
 // launch that joins chunks.  (9 requests of <= 7 rows over <= 1500 keys, 32 heads:
 // 43.0 us in chunks of 512, 38.3 of 256, 51.2 of 1024; 8 requests of 2 rows over
 // 300 keys, 40 heads: 13.4 us whole, 18.6 in chunks of 256.)
-int kv4_group_chunk(const Kv4Batch &b, bool grouped, int num_sms) {
+int kv4_group_chunk(const Kv4Batch &b, const Kv4Policy &policy, int num_sms) {
     const int64_t at_once = 3LL * num_sms;
     int best = 2048;
     double best_time = 0;
@@ -1543,7 +1587,7 @@ int kv4_group_chunk(const Kv4Batch &b, bool grouped, int num_sms) {
         int64_t keys = 0, items = 0, longest = 0;
         bool split = false;
         for (int i = 0; i < b.n_req; ++i) {
-            if (form_of(b, i, grouped) != kGroupForm) continue;
+            if (form_of(b, i, policy) != kGroupForm) continue;
             const int64_t groups = (b.n_input[i] + kRowsPerItem - 1) / kRowsPerItem, k = b.ctx_len[i] + b.n_input[i];
             keys += groups * k;
             items += groups * ((k + chunk - 1) / chunk);
@@ -1564,16 +1608,16 @@ bool kv4_sizes(const Kv4Batch &b, int num_sms, Kv4Sizes *z) {
         rows += n;
         if (rows > INT32_MAX / 8) return false;
     }
-    const bool grouped = z->grouped = singles_grouped(b);
-    z->chunk = kv4_row_chunk(b, grouped, num_sms);
-    z->rchunk = kv4_group_chunk(b, grouped, num_sms);
+    const Kv4Policy policy = z->policy = policy_of(b);
+    z->chunk = kv4_row_chunk(b, policy, num_sms);
+    z->rchunk = kv4_group_chunk(b, policy, num_sms);
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i];
         z->rows += n;
         z->keys += c + n;
         z->units += n / 2 + (n % 2 || (b.kv_offset[i] + c) % 2 ? 1 : 0);
         z->tiles += (c + n + kReadTile - 1) / kReadTile;
-        const Kv4Form form = form_of(b, i, grouped);
+        const Kv4Form form = form_of(b, i, policy);
         if (form == kPromptForm) {
             z->pre++;
             z->pre_tiles += (n + kPrefillRowsPerTile - 1) / kPrefillRowsPerTile;
@@ -1653,7 +1697,7 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     int32_t most = 0;
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i], o = b.kv_offset[i];
-        const Kv4Form form = form_of(b, i, z.grouped);
+        const Kv4Form form = form_of(b, i, z.policy);
         const bool prompt = form == kPromptForm;
         req_off[i] = (int32_t)row;
         req_ctx[i] = (int32_t)c;

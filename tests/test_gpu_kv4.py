@@ -447,3 +447,57 @@ def test_read_of_short_ranges(native, eng, dtype, d, heads, reqs):
         for got, want in zip(out[:, :, at:at + n + c], s.layer.read(o, n + c)):
             assert torch.equal(got.cpu(), torch.from_numpy(want.astype(np.float32)).to(TD[dtype]))
         at += n + c
+
+
+def prompt_case(native, eng, seed, d, **kw):
+    """A batch whose rows are many enough for the prefill kernel (its fp16 operands are in the workspace)."""
+    s = Case(native, eng, seed, "bf16", 40, d, [(600, 40), (140, 500), (1, 60), (5, 900)], **kw)
+    assert eng.kv4_workspace_bytes(s.plan) > 2 * len(s.qkv) * s.heads * d
+    return s
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("std", [1.0, 1e-20, 1e15])
+def test_prompts_of_many_heads(native, eng, d, std):
+    s = prompt_case(native, eng, 27, d, std=std)
+    s.qkv[:, 0] = rounded(s.qkv[:, 0] / np.float32(std), "bf16").float().numpy()
+    s.upload()
+    s.append()
+    s.append_oracle()
+    s.check(s.attention(), rounded_operands=True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_in_prompts_of_many_heads(native, eng, d):
+    s = prompt_case(native, eng, 28, d)
+    s.qkv[250, 2, 7, 3] = np.nan   # of the first request: a value of head 7 from row 250 on
+    s.qkv[300, 1, 9, 5] = np.inf   # a key of head 9 from row 300 on
+    s.upload()
+    s.append()
+    out = s.attention().float().reshape(len(s.qkv), 40, d)
+    bad = out.isnan()
+    assert bad[250:600, 7, :32].all() and bad[300:600, 9].all()
+    bad[250:600, 7], bad[300:600, 9] = False, False
+    assert not bad.any() and out[:250].isfinite().all()
+
+
+def test_prompts_behind_the_last_row(native, eng):
+    s = prompt_case(native, eng, 29, 128)
+    need, rows = eng.kv4_workspace_bytes(s.plan), len(s.qkv)
+    s.work = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    s.append()
+    out = torch.full((rows + 200, s.heads * s.d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    eng.op_kv4_attention(s.dqkv.data_ptr(), s.dev.data_ptr(), s.plan, s.dplan.data_ptr(), s.work.data_ptr(),
+                         out.data_ptr())
+    assert out[rows:].isnan().all() and out[:rows].isfinite().all() and (s.work[need:] == 0xA5).all()
+    assert np.array_equal(s.dplan.cpu().numpy(), s.plan)
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+def test_single_rows_beside_groups(native, eng, dtype, d):
+    """Single rows in the launch of the groups (few keys), and in their own (many)."""
+    for heads, reqs in ((3, [(1, 0), (2, 100), (1, 700), (7, 33), (1, 5)]), (40, [(1, 3000), (3, 20), (1, 2500)])):
+        s = Case(native, eng, 30, dtype, heads, d, reqs)
+        s.append()
+        s.append_oracle()
+        s.check(s.attention())
