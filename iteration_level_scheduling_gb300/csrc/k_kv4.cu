@@ -1558,6 +1558,10 @@ struct Kv4Sizes {
 // chunks cost a join: 16 requests of 300 keys, 40 heads of 128, took 18.2 us at
 // six blocks per SM and 11.5 at three, one of 100 keys 5.1 us in chunks of 64 and
 // 3.2 in one; one of 4000 keys 17.1 us at six, 13.8 at three, 19.7 at one.
+// A row of few keys stays whole whatever the chunk: 300 keys, 40 heads, in chunks of 128 / whole: of 64 6.7 and 4.1 us, of
+// 128 7.7 and 5.1, fp32 64 7.6 and 5.3; 400 keys 6.8 and 4.9, 7.7 and 6.2, 7.6 and 6.4; 600 keys 7.5 and 8.4.
+constexpr int kWholeRow = 400;
+int64_t row_items(int64_t keys, int chunk) { return keys <= kWholeRow ? 1 : (keys + chunk - 1) / chunk; }
 int kv4_row_chunk(const Kv4Batch &b, const Kv4Policy &policy, int num_sms) {
     const int64_t most = 3LL * num_sms;
     int chunk = 2048;
@@ -1565,7 +1569,7 @@ int kv4_row_chunk(const Kv4Batch &b, const Kv4Policy &policy, int num_sms) {
         int64_t items = 0;
         for (int i = 0; i < b.n_req && items * b.n_heads < most; ++i)
             if (form_of(b, i, policy) == kRowForm)
-                items += (int64_t)b.n_input[i] * ((b.ctx_len[i] + (int64_t)b.n_input[i] + chunk - 1) / chunk);
+                items += row_items(b.ctx_len[i] + (int64_t)1, chunk);
         if (items * b.n_heads >= most) break;
         chunk /= 2;
     }
@@ -1633,11 +1637,9 @@ bool kv4_sizes(const Kv4Batch &b, int num_sms, Kv4Sizes *z) {
             }
             continue;
         }
-        for (int64_t j = 0; j < n; ++j) {
-            const int64_t nch = (c + j + 1 + z->chunk - 1) / z->chunk;
-            z->items += nch;
-            if (nch > 1) z->splits++, z->parts += nch;
-        }
+        const int64_t nch = row_items(c + 1, z->chunk);
+        z->items += nch;
+        if (nch > 1) z->splits++, z->parts += nch;
     }
     int64_t w = kKv4Hdr;
     z->off_units = w, w = up4(w + 4 * z->units);
@@ -1708,12 +1710,11 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
             un[2] = (o + c + j) % 2 == 0 && j + 1 < n ? 2 : 1;
             j += un[2];
         }
-        for (int64_t j = 0; j < n; ++j, ++row) {
-            if (form != kRowForm) continue;
-            const int64_t keys = c + j + 1, nch = (keys + z.chunk - 1) / z.chunk;
+        if (form == kRowForm) {
+            const int64_t keys = c + 1, nch = row_items(keys, z.chunk), per = nch == 1 ? keys : z.chunk;
             for (int64_t k = 0; k < nch; ++k, it += 8) {
-                it[0] = (int32_t)(o + k * z.chunk);
-                it[1] = (int32_t)std::min<int64_t>(z.chunk, keys - k * z.chunk);
+                it[0] = (int32_t)(o + k * per);
+                it[1] = (int32_t)std::min<int64_t>(per, keys - k * per);
                 it[2] = (int32_t)row;
                 it[3] = (int32_t)nch;
                 it[4] = (int32_t)k;
@@ -1722,6 +1723,7 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
             }
             if (nch > 1) ++split, part += nch;
         }
+        row += n;
         for (int64_t r = 0; form == kGroupForm && r < n; r += kRowsPerItem) {
             const int64_t rows = std::min<int64_t>(kRowsPerItem, n - r), keys = c + r + rows;
             const int64_t nch = (keys + z.rchunk - 1) / z.rchunk;

@@ -334,7 +334,7 @@ def test_offsets_past_32_bits(native, eng):
 
 
 def test_refusals(native, eng):
-    s = Case(native, eng, 12, "bf16", 2, 64, [(1, 70), (1, 200)])
+    s = Case(native, eng, 12, "bf16", 2, 64, [(1, 70), (1, 900)])  # (900 keys are split: a workspace is needed)
     E, L = native.ERR_INVALID, native.lib
     h, pl = eng.handle, s.plan.ctypes.data
     q, la, dp, w, o = s.dqkv.data_ptr(), s.dev.data_ptr(), s.dplan.data_ptr(), s.work.data_ptr(), s.dqkv.data_ptr()
