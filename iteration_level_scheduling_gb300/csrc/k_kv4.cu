@@ -156,7 +156,7 @@ __device__ __forceinline__ uint32_t kv4_quantise(const float *x, uint32_t *par) 
 // write: one thread per 8 components of k and of v, of one row or of two whose
 // slots share a pair (then V goes out in whole words)
 //
-// Bound by issue (80 % of active cycles; 25 warp instructions per 32 components,
+// Bound by issue (84 % of active cycles; 25 warp instructions per 32 components,
 // 5 of them for halves): 10.5 k rows of 40 heads of 128, bf16, 81 us for 215 MB
 // read and 67 MB written (42 us at the copy rate); with an IEEE quotient per
 // component 189.
@@ -1127,7 +1127,7 @@ __global__ void __launch_bounds__(kKvThreads, kDecodeCtas) kv4_decode_mma_kernel
 // on kv4_decode_kernel; 30 heads of 16, 4 x <= 1000 rows over <= 800 keys, bf16: 198 and 1109.
 // P leaves the first product in the very registers that the second one takes it from.
 // Bound by issue and latency: 9 requests of <= 7 rows over <= 1500 keys, 32 heads of 128, 41 us (row by row 65), 51 MB:
-// 7.6 us at the copy rate; the schedulers issue in 51 % of active cycles, three CTAs of 168 registers per SM.
+// 7.6 us at the copy rate; the schedulers issue in 52 % of active cycles, three CTAs of 168 registers per SM.
 constexpr int kRowsPerItem = 16;
 
 template <typename T, int D>
