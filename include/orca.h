@@ -393,7 +393,10 @@ int64_t orca_kv4_workspace_bytes(const int32_t *host_plan);
  *   n_input)][head_dim] in the plan's dtype (the layout of a K/V pool layer).
  * attention: as orca_op_attention, the keys and values being what the slots
  *   stand for; the rows' own K/V must have been appended.  Scores and sums are
- *   held in fp32.  Errors: INVALID, CUDA. */
+ *   held in fp32.  A group that reads back as NaN makes the rows that see its
+ *   key NaN, and no others: of a key, in the whole head; of a value, in the
+ *   group's components at least (in the whole head where many rows at once run
+ *   on fp16 operands).  Errors: INVALID, CUDA. */
 int orca_op_kv4_append(orca_engine *eng, const void *qkv, void *kv4_layer, const int32_t *host_plan,
                        const int32_t *dev_plan);
 int orca_op_kv4_read(orca_engine *eng, const void *kv4_layer, const int32_t *host_plan, const int32_t *dev_plan,

@@ -1374,21 +1374,24 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
     __syncthreads();
     // join the warps; of several chunks, the partials are joined by the next kernel
     const int nch = r1.x;
-    for (int x = threadIdx.x; x < rows * D; x += kKvThreads) {
+    for (int x = 2 * threadIdx.x; x < rows * D; x += 2 * kKvThreads) {  // two components
         const int j = x / D, d = x - j * D;
-        float M = kLow, L = 0.f, O = 0.f;
+        float M = kLow, L = 0.f, O[2] = {0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kKvWarps; ++w) M = fmaxf(M, sm.m[w][j]);
 #pragma unroll
         for (int w = 0; w < kKvWarps; ++w) {
-            const float c = exp2f(sm.m[w][j] - M);
-            L += sm.l[w][j] * c, O += sm.o[w][j][d] * c;
+            const float c = ex2(sm.m[w][j] - M);
+            const float2 o2 = *reinterpret_cast<const float2 *>(&sm.o[w][j][d]);
+            L += sm.l[w][j] * c, O[0] += o2.x * c, O[1] += o2.y * c;
         }
         if (nch == 1) {
-            ((T *)a.out)[(size_t)(r0.z + j) * a.H + h * D + d] = Elem<T>::from_f(O / L);
+            T *dst = (T *)a.out + (size_t)(r0.z + j) * a.H + h * D + d;
+            if constexpr (F32) *reinterpret_cast<float2 *>(dst) = make_float2(O[0] / L, O[1] / L);
+            else *reinterpret_cast<uint32_t *>(dst) = pack2(O[0] / L, O[1] / L);
         } else {
             float *mine = a.row_part + (((size_t)(r1.z + r1.y) * a.n_heads + h) * kRowsPerItem + j) * (D + 2);
-            mine[d] = O;
+            *reinterpret_cast<float2 *>(mine + d) = make_float2(O[0], O[1]);
             if (d == 0) mine[D] = M, mine[D + 1] = L;
         }
     }

@@ -101,3 +101,12 @@ def test_oracle_quantise_ties_and_edges():
     for bad in (np.inf, -np.inf, np.nan):
         x[0, 7] = bad
         assert np.isnan(kv4.stands_for(*kv4.quantise(x))).all()
+
+
+def test_addresses_of_arrays(native):
+    """Arrays of every kind that a caller may pass: writable, read-only (a plan kept unchanged), empty, a view."""
+    plan = np.arange(12, dtype=np.int32)
+    fixed = plan.copy()
+    fixed.setflags(write=False)
+    for a in (plan, fixed, plan[:0], plan[3:], plan[::2], plan.reshape(3, 4).T):
+        assert native._ptr(a) == a.__array_interface__["data"][0] or a.size == 0
