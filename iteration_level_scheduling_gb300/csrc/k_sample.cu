@@ -24,7 +24,7 @@
 // ids.
 //
 // Bound by barriers and latency, then by issue: 192 rows of 50257 with mixed
-// parameters take 67 us (38.6 MB: 5.8 us of reading), the schedulers issuing in
+// parameters take 61 us (38.6 MB: 5.8 us of reading), the schedulers issuing in
 // 42 % of their active cycles, barriers the first stall; a weight is about 95
 // warp instructions per 32 logits with its comparison and sum, two thirds of
 // them integer.  One row at T 0.8, top-k 50, top-p 0.95 takes 11.0 us on four
@@ -1029,12 +1029,14 @@ cudaError_t sample_rows(int dtype_bf16, const void *logits, int64_t ld, int n_ro
                         int32_t *out, unsigned *err, int num_sms, cudaStream_t st) {
     if (n_rows <= 0) return cudaSuccess;
     constexpr int kMaxPer = (227 * 1024 - (int)sizeof(SampleSmem)) / 4 / kSpThreads * kSpThreads;
-    // CTAs per row: enough that two of them share an SM (192 mixed rows of 50257: four per row 83 us, two, which leave
-    // an SM to one CTA, 101), more while SMs would stand idle (one row: one 19.1, two 14.7, four 12.2, eight 12.7 us).
+    // CTAs per row: as few as let two of them share an SM (192 mixed rows of 50257: three per row 61 us, four 67.5, two,
+    // which leave an SM to one CTA, 101); more, by the ids, while all run at once (one row: one 19.1, two 14.7, four 12.2,
+    // eight 12.7 us; one of 70000 at top-p 0.9: four 30.8, six 27.4).  Larger clusters do not fill every SM: 40 rows of
+    // 102018 at top-p 0.9, five per row 57 us, seven 71, eight 77.
     constexpr int kPairPer = (113 * 1024 - (int)sizeof(SampleSmem)) / 4;
-    int C = 1;
-    while (C < kMaxCluster && (V + C - 1) / C > kPairPer) C *= 2;
-    while (C < 4 && V / C > 8192 && (int64_t)n_rows * C * 2 <= num_sms) C *= 2;
+    int C = std::min(kMaxCluster, (V + kPairPer - 1) / kPairPer);
+    const int goal = V <= 8192 ? 1 : V <= 16384 ? 2 : std::min(kMaxCluster, std::max(4, (V + 12999) / 13000));
+    while (C < goal && (int64_t)n_rows * (C + 1) <= (C < 4 ? 2 * num_sms : num_sms + num_sms / 2)) ++C;
     const int per = ((V + C - 1) / C + 3) / 4 * 4;
     const bool held = per <= kMaxPer;
     // more rows than run at once: the ones with the most work first, so that none of them starts last (with thousands
