@@ -1343,8 +1343,10 @@ __global__ void __launch_bounds__(kMdThreads) attn_decode_mma_kernel(const __gri
         // ------------------------------ producer ------------------------------
         // This iteration's K/V rows (key ctx of every request, ctx its context
         // before the iteration) are appended by the previous kernel; the keys
-        // before them were written by earlier iterations.  So the ring's first
-        // stages, while they hold only such keys, are loaded before waiting for
+        // before them were written in front of the iteration, whose first
+        // kernel triggers only behind its wait: all of that has ended.  (The
+        // operator calls copy their tables in front of this kernel, which it
+        // starts behind.)  So the ring's first stages, while they hold only such keys, are loaded before waiting for
         // the previous kernel: the stream starts during its tail.
         //
         // The CTA's items: the first is dealt (entry blockIdx.x, so it can

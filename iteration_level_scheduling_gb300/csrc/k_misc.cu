@@ -25,8 +25,11 @@ __global__ void __launch_bounds__(kRowThreads) embed_kernel(const int32_t *token
                                                             const T *pos_emb, float *x, int H, int V, int max_pos,
                                                             unsigned *err) {
     constexpr int VEC = Elem<T>::kPer16;
-    pdl_trigger();
+    // The iteration's first kernel lets the next start only once everything in front of the iteration has ended: the
+    // decode attention loads cached keys ahead of its own wait, and a chain of kernels that all trigger first would let
+    // it start beside, say, a read-back that is still writing the pool.
     pdl_wait();
+    pdl_trigger();
     const int r = blockIdx.x;
     int t = tokens[r];
     if (t < 0) {
