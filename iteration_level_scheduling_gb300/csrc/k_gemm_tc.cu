@@ -876,8 +876,8 @@ __global__ void __launch_bounds__(kSkThreads, 1)
 // element offset (ft * (k / 64) + kb) * 8192, each tile laid out exactly as
 // the 128-byte-swizzled K-major shared-memory image (row r at r * 128 bytes,
 // 16-byte chunk c at position c ^ (r % 8)); rows past n_out are zero.
+// No trigger: a GEMM behind it loads weights ahead of its own wait, so it may start only when this has ended.
 __global__ void __launch_bounds__(256) pack_weight_kernel(const bf16 *w, int n_out, int k, bf16 *out) {
-    pdl_trigger();
     pdl_wait();
     const int num_kb = k / BK;
     const int ft = blockIdx.x / num_kb, kb = blockIdx.x % num_kb;

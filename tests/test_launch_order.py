@@ -59,3 +59,10 @@ def test_decode_starts_behind_what_wrote_its_pool_before_the_iteration():
                   ("k_sample.cu", "sample_kernel")):
         chain = [kind(*k) for k in [first, ("k_misc.cu", "embed_kernel")] + layer]
         assert ended_at_start(chain + [False])[-1] >= 1, first
+
+
+def test_the_gemm_starts_behind_what_packed_its_weights():
+    """A linear layer straight behind the packing of its weights, which it loads ahead of its wait."""
+    for gemm in ("gemm_tc_kernel", "gemm_sk_kernel"):
+        assert body("k_gemm_tc.cu", gemm).find("pdl_trigger()") >= 0
+        assert ended_at_start([kind("k_gemm_tc.cu", "pack_weight_kernel"), False])[-1] == 1
