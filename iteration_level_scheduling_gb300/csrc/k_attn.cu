@@ -816,7 +816,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr unsigned kFull = 0xffffffffu;
 
-    pdl_trigger();
+    // (F16: behind the wait, so that the kernel behind this one can read ahead of its own wait what was written before)
+    if constexpr (!F16) pdl_trigger();
     if (threadIdx.x == 0) {
         mbar_init(&bar.q_full, 1);
         mbar_init(&bar.q_empty, 1);
@@ -846,6 +847,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
     pdl_wait();  // q and this iteration's K/V rows come from the kernels before
+    if constexpr (F16) pdl_trigger();
 
     // This CTA's items: b, b + G, ... of (head, tile) with the tiles of a head
     // innermost (the query tiles of one request, which read the same keys,

@@ -409,7 +409,11 @@ __global__ void __launch_bounds__(kRdThreads) kv4_read_few_kernel(Kv4View v, con
 // rounding them to 8 bits would add an error as large as the output's own.
 // fp16 keeps 11 bits; its narrow range is met by powers of two, one per row and
 // head for q and one per request and head for K and V, that bring the largest
-// magnitude to [2^14, 2^15) (values 2^-28 of it and below lose bits).
+// magnitude to [2^14, 2^15).  Groups below 2^-28 of the largest would lose bits
+// and those below 2^-40 everything, also for rows that do not see the largest:
+// a request and head with such a group is marked, and its rows are attended in
+// groups on the codes themselves behind the prefill kernel (kv4_rows_wide_kernel;
+// without marks the launch costs 1 us: the prompt chunks below 189.2 and 190.2).
 // Four prompts of 900 rows over 1000 keys, 40 heads of 128: scales and q 25 us, K
 // and V 42 us, the attention 168 us under the profiler (tensor pipe 36 % of active
 // cycles, as on a bf16 cache); against rows one by one 4968 us.
@@ -425,6 +429,7 @@ struct Kv4Prep {
     const bf16 *qkv;
     __half *q16;
     float *q_scale, *kv_scale;
+    int32_t *wide;  // [prompt][head]: fp16 does not hold the range of its K or V
     Kv4View v;
     int H, n_heads, d, G, n_rows, n_pre;  // G is 2 or 4
     const int32_t *pre;  // 4 words per prompt: request, first slot, slots, 0
@@ -434,7 +439,7 @@ constexpr int kPrepThreads = 256, kPrepQ = 4;
 // Blocks 0 .. n_pre * n_heads - 1: the scales of K and V of one prompt and head, from the parameters (a component lies
 // between m and m + 15 s).  The others scale and round q.
 __global__ void __launch_bounds__(kPrepThreads) kv4_prep_kernel(const Kv4Prep a) {
-    __shared__ float red[2][kPrepThreads / 32];
+    __shared__ float red[4][kPrepThreads / 32];
     pdl_trigger();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -443,8 +448,7 @@ __global__ void __launch_bounds__(kPrepThreads) kv4_prep_kernel(const Kv4Prep a)
         const int i = blockIdx.x / a.n_heads, h = blockIdx.x - i * a.n_heads;
         const int4 pr = reinterpret_cast<const int4 *>(a.pre)[i];
         const int64_t s0 = pr.y, s1 = s0 + pr.z;
-        float km = 0.f, vm = 0.f;
-        // (fmaxf drops NaN: a group that reads back as NaN does so whatever the scale)
+        // (fmaxf and fminf drop NaN: a group that reads back as NaN does so whatever the scale)
         auto size = [](uint32_t p) { return fmaxf(fabsf(bf_hi(p)), fabsf(fmaf(15.f, bf_lo(p), bf_hi(p)))); };
         const uint32_t *kp = a.v.kp + (int64_t)h * a.v.S * a.G, *vp = a.v.vp + (int64_t)h * a.v.S * a.G;
         // words of K: s0 G .. s1 G; of V, whose pairs hold group by group the even and the odd slot, those of the
@@ -452,7 +456,7 @@ __global__ void __launch_bounds__(kPrepThreads) kv4_prep_kernel(const Kv4Prep a)
         // of a head are whole vectors, what lies outside is dropped.
         const int64_t k0 = s0 * a.G, k1 = s1 * a.G, v0 = (s0 >> 1) * 2 * a.G, v1 = ((s1 + 1) >> 1) * 2 * a.G;
         auto take = [&](const uint32_t *base, int64_t lo, int64_t hi, auto in) {
-            float mx = 0.f;
+            float2 r = make_float2(0.f, INFINITY);  // the largest group, and the smallest that is not all zeros
             for (int64_t j = (lo & ~int64_t(3)) + 4 * threadIdx.x; j < hi; j += 4 * 8 * kPrepThreads) {
                 uint4 p[8];
 #pragma unroll
@@ -466,28 +470,42 @@ __global__ void __launch_bounds__(kPrepThreads) kv4_prep_kernel(const Kv4Prep a)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int64_t at = j + 4 * e * kPrepThreads + q;
-                        if (at >= lo && at < hi && in(at)) mx = fmaxf(mx, size(w[q]));
+                        if (at >= lo && at < hi && in(at)) {
+                            const float x = size(w[q]);
+                            r.x = fmaxf(r.x, x);
+                            if (x > 0.f) r.y = fminf(r.y, x);
+                        }
                     }
                 }
             }
-            return mx;
+            return r;
         };
-        km = take(kp, k0, k1, [](int64_t) { return true; });
-        vm = take(vp, v0, v1, [&](int64_t at) {
+        float2 km = take(kp, k0, k1, [](int64_t) { return true; });
+        float2 vm = take(vp, v0, v1, [&](int64_t at) {
             const int64_t slot = (at >> (a.G == 4 ? 3 : 2)) * 2 + (at & 1);
             return slot >= s0 && slot < s1;
         });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, o));
-            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+            km.x = fmaxf(km.x, __shfl_xor_sync(0xffffffffu, km.x, o));
+            vm.x = fmaxf(vm.x, __shfl_xor_sync(0xffffffffu, vm.x, o));
+            km.y = fminf(km.y, __shfl_xor_sync(0xffffffffu, km.y, o));
+            vm.y = fminf(vm.y, __shfl_xor_sync(0xffffffffu, vm.y, o));
         }
-        if (lane == 0) red[0][warp] = km, red[1][warp] = vm;
+        if (lane == 0) red[0][warp] = km.x, red[1][warp] = vm.x, red[2][warp] = km.y, red[3][warp] = vm.y;
         __syncthreads();
-        if (threadIdx.x < 2) {
-            float m = 0.f;
-            for (int w = 0; w < kPrepThreads / 32; ++w) m = fmaxf(m, red[threadIdx.x][w]);
-            a.kv_scale[2 * ((size_t)pr.x * a.n_heads + h) + threadIdx.x] = kv4_inverse_scale(m);
+        if (threadIdx.x < 32) {
+            bool wide = false;
+            if (threadIdx.x < 2) {
+                float big = 0.f, small = INFINITY;
+                for (int w = 0; w < kPrepThreads / 32; ++w)
+                    big = fmaxf(big, red[threadIdx.x][w]), small = fminf(small, red[2 + threadIdx.x][w]);
+                const float inv = kv4_inverse_scale(big);
+                a.kv_scale[2 * ((size_t)pr.x * a.n_heads + h) + threadIdx.x] = inv;
+                wide = small < inv * 6.103515625e-05f;  // 2^-14, fp16's smallest normal number
+            }
+            wide = __any_sync(0xffffffffu, wide);
+            if (threadIdx.x == 0) a.wide[blockIdx.x] = wide;
         }
         return;
     }
@@ -540,6 +558,8 @@ struct Kv4Attn {
     const int32_t *row_items;  // the same for groups of rows (kv4_rows_mma_kernel), 12 words an item
     const int32_t *row_joins;
     float *row_part;  // [partial][head][16][D + 2]
+    const int32_t *wide, *wide_items;  // prompts' heads beyond fp16's range, and the prompts' rows in groups
+    int n_wide, n_wide_items;          // prompts x heads, items
 };
 
 // Join the partials of `nch` chunks, `stride` floats apart, in chunk order: component `at`, the maximum at D and the
@@ -1147,19 +1167,16 @@ __device__ __forceinline__ uint32_t bf_part(float &a, float &b) {
 
 // Half: every item of the launch has at most 8 rows, and the A operand's rows 8 .. 15 are zero.
 template <typename T, int D, bool Half>
-__global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4Attn a) {
+__device__ __forceinline__ void kv4_rows_item(const Kv4Attn &a, Kv4RowsMerge<T, D> &sm, const int4 r0, const int4 *rec,
+                                              int h) {
     constexpr bool F32 = std::is_same<T, float>::value;
     constexpr int W = D >= 32 ? D / 32 : 1;  // groups
     constexpr int R = Half ? 1 : 2;  // row g, and g + 8
     constexpr unsigned kAll = 0xffffffffu;
     using Merge = Kv4RowsMerge<T, D>;
-    __shared__ Merge sm;
-    pdl_trigger();
-    pdl_wait();
-    // first slot, keys, first row, rows | the rows' chunks, this chunk, first partial, - | keys row 0 sees
-    const int item = blockIdx.x / a.n_heads, h = blockIdx.x - item * a.n_heads;
-    const int4 *rec = reinterpret_cast<const int4 *>(a.row_items) + 3 * item;
-    const int4 r0 = rec[0], r1 = rec[1], r2 = rec[2];
+    // r0: first slot, keys, first row, rows; then the rows' chunks, this chunk, first partial, prompt (wide items) (read
+    // late: registers); r2.x: keys that row 0 sees
+    const int4 r2 = rec[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int64_t s0 = r0.x, s1 = s0 + r0.y;
     const int rows = r0.w;
@@ -1373,6 +1390,7 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
     }
     __syncthreads();
     // join the warps; of several chunks, the partials are joined by the next kernel
+    const int4 r1 = rec[1];
     const int nch = r1.x;
     for (int x = 2 * threadIdx.x; x < rows * D; x += 2 * kKvThreads) {  // two components
         const int j = x / D, d = x - j * D;
@@ -1394,6 +1412,35 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4At
             *reinterpret_cast<float2 *>(mine + d) = make_float2(O[0], O[1]);
             if (d == 0) mine[D] = M, mine[D + 1] = L;
         }
+    }
+}
+
+template <typename T, int D, bool Half>
+__global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_mma_kernel(const Kv4Attn a) {
+    __shared__ Kv4RowsMerge<T, D> sm;
+    pdl_trigger();
+    pdl_wait();
+    const int item = blockIdx.x / a.n_heads, h = blockIdx.x - item * a.n_heads;
+    const int4 *rec = reinterpret_cast<const int4 *>(a.row_items) + 3 * item;
+    kv4_rows_item<T, D, Half>(a, sm, rec[0], rec, h);
+}
+
+// The rows of the prompts' marked heads again, over what the prefill kernel made of them.  As many blocks as run at
+// once: a call without marks costs one look at them.
+template <int D>
+__global__ void __launch_bounds__(kKvThreads, 3) kv4_rows_wide_kernel(const Kv4Attn a) {
+    __shared__ Kv4RowsMerge<bf16, D> sm;
+    pdl_trigger();
+    int any = 0;  // (the marks are there: the prefill kernel triggers behind its wait)
+    for (int i = threadIdx.x; i < a.n_wide; i += kKvThreads) any |= __ldcg(a.wide + i);
+    pdl_wait();
+    if (!__syncthreads_or(any)) return;
+    for (int64_t j = blockIdx.x; j < (int64_t)a.n_wide_items * a.n_heads; j += gridDim.x) {
+        const int item = (int)(j / a.n_heads), h = (int)(j - (int64_t)item * a.n_heads);
+        const int4 *rec = reinterpret_cast<const int4 *>(a.wide_items) + 3 * (int64_t)item;
+        if (!a.wide[rec[1].w * a.n_heads + h]) continue;
+        kv4_rows_item<bf16, D, false>(a, sm, rec[0], rec, h);
+        __syncthreads();
     }
 }
 
@@ -1472,6 +1519,8 @@ enum : int {
     Q_O_RJOINS,
     Q_O_REQWS,  // a prompt's first slot in the workspace's pool
     Q_TILEMOST,  // slots of the longest read-back tile
+    Q_WIDE,      // the prompts' rows in groups, for heads that fp16 does not hold
+    Q_O_WIDE,
 };
 int64_t up4(int64_t w) { return (w + 3) & ~int64_t(3); }
 
@@ -1549,11 +1598,11 @@ Kv4Policy policy_of(const Kv4Batch &b) {
 struct Kv4Sizes {
     int64_t rows = 0, units = 0, items = 0, splits = 0, parts = 0, tiles = 0, keys = 0;
     int64_t ritems = 0, rsplits = 0, rparts = 0;
-    int64_t pre = 0, pre_tiles = 0, pre_read = 0, pre_keys = 0;
+    int64_t pre = 0, pre_tiles = 0, pre_read = 0, pre_keys = 0, wide = 0;
     int chunk = 0, rchunk = 0;
     Kv4Policy policy;
     int64_t off_ritems, off_rjoins, off_units, off_items, off_count, off_tiles, off_pre, off_pretiles, off_preread, off_reqoff, off_reqctx,
-        off_reqws, total;
+        off_reqws, off_wide, total;
 };
 
 // Keys per work item of rows one by one: the largest chunk (a power of two,
@@ -1630,6 +1679,7 @@ bool kv4_sizes(const Kv4Batch &b, int num_sms, Kv4Sizes *z) {
             z->pre_tiles += (n + kPrefillRowsPerTile - 1) / kPrefillRowsPerTile;
             z->pre_read += (c + n + kReadTile - 1) / kReadTile;
             z->pre_keys += c + n;
+            z->wide += (n + kRowsPerItem - 1) / kRowsPerItem;
             continue;
         }
         if (form == kGroupForm) {
@@ -1657,6 +1707,7 @@ bool kv4_sizes(const Kv4Batch &b, int num_sms, Kv4Sizes *z) {
     z->off_reqoff = w, w = up4(w + b.n_req + 1);
     z->off_reqctx = w, w = up4(w + b.n_req);
     z->off_reqws = w, w = up4(w + b.n_req);
+    z->off_wide = w, w = up4(w + 12 * z->wide);
     z->total = w;
     // 32-bit table entries and grid sizes
     return w <= INT32_MAX && z->keys <= INT32_MAX && (z->items + z->ritems) * b.n_heads <= INT32_MAX && z->pre_tiles * b.n_heads <= INT32_MAX &&
@@ -1696,7 +1747,7 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     int32_t *un = buf + z.off_units, *it = buf + z.off_items, *tl = buf + z.off_tiles;
     int32_t *pre = buf + z.off_pre, *pt = buf + z.off_pretiles, *pd = buf + z.off_preread;
     int32_t *req_off = buf + z.off_reqoff, *req_ctx = buf + z.off_reqctx, *req_ws = buf + z.off_reqws;
-    int32_t *ri = buf + z.off_ritems, *rj = buf + z.off_rjoins;
+    int32_t *ri = buf + z.off_ritems, *rj = buf + z.off_rjoins, *wd = buf + z.off_wide;
     int64_t row = 0, split = 0, part = 0, key = 0, ws = 0, rpart = 0;
     bool half = true;
     int32_t most = 0;
@@ -1760,6 +1811,12 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
         }
         key += c + n;
         if (prompt) {
+            const int32_t index = (int32_t)((pre - (buf + z.off_pre)) / 4);
+            for (int64_t r = 0; r < n; r += kRowsPerItem, wd += 12) {
+                const int64_t rows = std::min<int64_t>(kRowsPerItem, n - r);
+                wd[0] = (int32_t)o, wd[1] = (int32_t)(c + r + rows), wd[2] = (int32_t)(req_off[i] + r), wd[3] = (int32_t)rows;
+                wd[4] = 1, wd[7] = index, wd[8] = (int32_t)(c + r + 1);
+            }
             pre[0] = i, pre[1] = (int32_t)o, pre[2] = (int32_t)(c + n);
             pre += 4;
             for (int64_t q = 0; q < n; q += kPrefillRowsPerTile, pt += 2) pt[0] = i, pt[1] = (int32_t)q;
@@ -1770,6 +1827,7 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     // blocks are dealt in order, all heads of an item after one another: the longest first, so that none starts late
     longest_first<8>(buf + z.off_items, z.items);
     longest_first<12>(buf + z.off_ritems, z.ritems);
+    longest_first<12>(buf + z.off_wide, z.wide);
     prefill_order(buf + z.off_pretiles, (int)z.pre_tiles, req_off, req_ctx);
     // slots written by two rows
     std::vector<std::pair<int64_t, int64_t>> w((size_t)b.n_req);
@@ -1814,6 +1872,8 @@ bool kv4_plan_build(const Kv4Batch &b, int num_sms, int32_t *buf, int64_t cap) {
     buf[Q_O_REQCTX] = (int32_t)z.off_reqctx;
     buf[Q_O_REQWS] = (int32_t)z.off_reqws;
     buf[Q_TILEMOST] = most;
+    buf[Q_WIDE] = (int32_t)z.wide;
+    buf[Q_O_WIDE] = (int32_t)z.off_wide;
     return true;
 }
 
@@ -1823,7 +1883,7 @@ bool kv4_plan_writes_once(const int32_t *hp) { return !hp[Q_TWICE]; }
 namespace {
 // byte offsets in the workspace
 struct Kv4Work {
-    int64_t row_part, q16, pool16, q_scale, kv_scale, total;
+    int64_t row_part, q16, pool16, q_scale, kv_scale, wide, total;
 };
 Kv4Work kv4_work(const int32_t *hp) {
     const int64_t nh = hp[Q_HEADS], d = hp[Q_DIM];
@@ -1841,6 +1901,7 @@ Kv4Work kv4_work(const int32_t *hp) {
     w.pool16 = take(2 * nh * hp[Q_PREKEYS] * d * 2);
     w.q_scale = take(pre ? (int64_t)hp[Q_ROWS] * nh * 4 : 0);
     w.kv_scale = take(pre ? (int64_t)hp[Q_REQS] * nh * 2 * 4 : 0);
+    w.wide = take(hp[Q_PRE] * nh * 4);
     w.total = at;
     return w;
 }
@@ -1951,6 +2012,7 @@ cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp,
     pr.q16 = (__half *)(ws + w.q16);
     pr.q_scale = (float *)(ws + w.q_scale);
     pr.kv_scale = (float *)(ws + w.kv_scale);
+    pr.wide = (int32_t *)(ws + w.wide);
     pr.v = a.v;
     pr.H = a.H, pr.n_heads = nh, pr.d = d, pr.G = kv4_groups(d);
     pr.n_rows = hp[Q_ROWS], pr.n_pre = hp[Q_PRE];
@@ -1975,7 +2037,16 @@ cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp,
         e = attention_prefill_f16(pr.q16, hp[Q_ROWS], ws + w.pool16, hp[Q_PREKEYS], (bf16 *)out, ap, a.H, nh, pr.q_scale,
                                   pr.kv_scale, err, st);
     *launches += 3;
-    return e;
+    if (e != cudaSuccess) return e;
+    a.wide = pr.wide, a.n_wide = hp[Q_PRE] * nh;
+    a.wide_items = dp + hp[Q_O_WIDE], a.n_wide_items = hp[Q_WIDE];
+    int sms = 0, dev = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const dim3 grid((unsigned)std::min<int64_t>((int64_t)a.n_wide_items * nh, 3LL * sms));
+    ++*launches;
+    return d == 64 ? launch_pdl(kv4_rows_wide_kernel<64>, grid, dim3(kKvThreads), 0, st, a)
+                   : launch_pdl(kv4_rows_wide_kernel<128>, grid, dim3(kKvThreads), 0, st, a);
 }
 
 }  // namespace orca

@@ -7,8 +7,8 @@ wait, the kernels that have ended for certain are all of those in front of kerne
 wait, and otherwise only those that had ended for certain when i - 1 itself started.  A chain of kernels that trigger
 first lets the last of them start while the first still runs.
 
-Two kernels load data ahead of their wait: tensor-core decode attention (keys in front of the iteration's own) and the
-tcgen05 GEMM (weights)."""
+Three kernels load data ahead of their wait: tensor-core decode attention (keys in front of the iteration's own), the
+tcgen05 GEMM (weights) and the row groups behind 4-bit prompts (the marks of heads that fp16 does not hold)."""
 
 import os
 import re
@@ -66,3 +66,13 @@ def test_the_gemm_starts_behind_what_packed_its_weights():
     for gemm in ("gemm_tc_kernel", "gemm_sk_kernel"):
         assert body("k_gemm_tc.cu", gemm).find("pdl_trigger()") >= 0
         assert ended_at_start([kind("k_gemm_tc.cu", "pack_weight_kernel"), False])[-1] == 1
+
+
+def test_row_groups_behind_prompts_start_behind_what_marked_their_heads():
+    """prep, read, prefill on fp16 operands, row groups: the marks are prep's."""
+    b = body("k_attn.cu", "attn_prefill_tc_kernel").replace("if constexpr (!F16) pdl_trigger();", "")
+    late = 0 <= b.find("pdl_wait()") < b.find("pdl_trigger()")
+    chain = [kind("k_kv4.cu", "kv4_prep_kernel"), kind("k_kv4.cu", "kv4_read_kernel"), late]
+    wide = body("k_kv4.cu", "kv4_rows_wide_kernel")
+    assert wide.find("a.wide + i") < wide.find("pdl_wait()")
+    assert ended_at_start(chain + [False])[-1] >= 1
