@@ -1599,7 +1599,8 @@ struct Kv4Sizes {
     int64_t rows = 0, units = 0, items = 0, splits = 0, parts = 0, tiles = 0, keys = 0;
     int64_t ritems = 0, rsplits = 0, rparts = 0;
     int64_t pre = 0, pre_tiles = 0, pre_read = 0, pre_keys = 0, wide = 0;
-    int chunk = 0, rchunk = 0;
+    int chunk = 0;
+    int64_t rchunk = 0;
     Kv4Policy policy;
     int64_t off_ritems, off_rjoins, off_units, off_items, off_count, off_tiles, off_pre, off_pretiles, off_preread, off_reqoff, off_reqctx,
         off_reqws, off_wide, total;
@@ -1634,24 +1635,34 @@ int kv4_row_chunk(const Kv4Batch &b, const Kv4Policy &policy, int num_sms) {
 // the longest block (the last ones to start are the shortest), and 120 for the
 // launch that joins chunks.  (9 requests of <= 7 rows over <= 1500 keys, 32 heads:
 // 43.0 us in chunks of 512, 38.3 of 256, 51.2 of 1024; 8 requests of 2 rows over
-// 300 keys, 40 heads: 13.4 us whole, 18.6 in chunks of 256.)
-int kv4_group_chunk(const Kv4Batch &b, const Kv4Policy &policy, int num_sms) {
+// 300 keys, 40 heads: 13.4 us whole, 18.6 in chunks of 256.)  Partial outputs are
+// written and read again, and what they take beyond 64 MiB is charged at the copy
+// rate (a key's time in a block is about 0.05 us): a long prompt's many groups
+// nearly fill the GPU whole (fp32, 32 heads of 128, 8192 rows behind 24576 keys:
+// 52.5 ms and 1885 MiB in chunks of 2048, 49.3 ms and 260 MiB in 16384; 2048
+// rows behind 30000: 14.2 ms and 509 MiB, 13.6 and 130).
+int64_t kv4_group_chunk(const Kv4Batch &b, const Kv4Policy &policy, int num_sms) {
     const int64_t at_once = 3LL * num_sms;
-    int best = 2048;
+    int64_t largest = 2048, best = 0;
+    for (int i = 0; i < b.n_req; ++i)
+        while (form_of(b, i, policy) == kGroupForm && largest < b.ctx_len[i] + (int64_t)b.n_input[i]) largest *= 2;
     double best_time = 0;
-    for (int chunk = 2048; chunk >= 128; chunk /= 2) {
-        int64_t keys = 0, items = 0, longest = 0;
+    for (int64_t chunk = largest; chunk >= 128; chunk /= 2) {
+        int64_t keys = 0, items = 0, longest = 0, parts = 0;
         bool split = false;
         for (int i = 0; i < b.n_req; ++i) {
             if (form_of(b, i, policy) != kGroupForm) continue;
-            const int64_t groups = (b.n_input[i] + kRowsPerItem - 1) / kRowsPerItem, k = b.ctx_len[i] + b.n_input[i];
+            const int64_t groups = (b.n_input[i] + kRowsPerItem - 1) / kRowsPerItem, k = b.ctx_len[i] + (int64_t)b.n_input[i];
             keys += groups * k;
             items += groups * ((k + chunk - 1) / chunk);
-            longest = std::max(longest, std::min<int64_t>(k, chunk));
+            longest = std::max(longest, std::min(k, chunk));
             split |= k > chunk;
+            if (k > chunk) parts += groups * ((k + chunk - 1) / chunk);
         }
-        const double time = (double)(keys + 60 * items) * b.n_heads / at_once + 0.5 * (longest + 60) + (split ? 120 : 0);
-        if (chunk == 2048 || time < best_time) best = chunk, best_time = time;
+        const double bytes = 4.0 * parts * b.n_heads * kRowsPerItem * (b.head_dim + 2);
+        const double time = (double)(keys + 60 * items) * b.n_heads / at_once + 0.5 * (longest + 60) + (split ? 120 : 0) +
+                            2 * std::max(0.0, bytes - (64 << 20)) / (6.7e6 * 0.05);
+        if (chunk == largest || time < best_time) best = chunk, best_time = time;
     }
     return best;
 }

@@ -110,3 +110,17 @@ def test_addresses_of_arrays(native):
     fixed.setflags(write=False)
     for a in (plan, fixed, plan[:0], plan[3:], plan[::2], plan.reshape(3, 4).T):
         assert native._ptr(a) == a.__array_interface__["data"][0] or a.size == 0
+
+
+@pytest.mark.parametrize("dtype,d,reqs", [
+    (0, 128, [(8192, 24576)]), (0, 128, [(2048, 30000)]), (0, 64, [(4096, 0), (512, 60000), (1, 900)]),
+    (1, 32, [(8192, 24576)]), (1, 16, [(3000, 100000)] * 2), (0, 128, [(20, 500000)]), (0, 16, [(16, 2000000)]),
+])
+def test_workspace_of_long_prompts_in_groups(native, dtype, d, reqs):
+    """Prompts that run in groups of rows: the partial outputs of their chunks stay below half of the K/V in
+    fp32 (32 heads, every key of the batch), or below 64 MiB."""
+    n, c = zip(*reqs)
+    o = np.cumsum([0] + [a + b for a, b in reqs])
+    p = plan(native, dtype, 32, d, int(o[-1]), n, c, o[:-1])
+    keys = int(o[-1])
+    assert native.lib.orca_kv4_workspace_bytes(p.ctypes.data) <= max(64 << 20, 2 * 32 * keys * d * 4 // 2)
