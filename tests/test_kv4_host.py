@@ -124,3 +124,32 @@ def test_workspace_of_long_prompts_in_groups(native, dtype, d, reqs):
     p = plan(native, dtype, 32, d, int(o[-1]), n, c, o[:-1])
     keys = int(o[-1])
     assert native.lib.orca_kv4_workspace_bytes(p.ctypes.data) <= max(64 << 20, 2 * 32 * keys * d * 4 // 2)
+
+
+def test_quantisation_error():
+    """Between the ends of what is held a component is off by half a step at most.  At the ends by what s and m lost to
+    bf16 (2^-8 each): 2^-8 of the range and 2^-8 of the minimum, which is more than half a step once the minimum is
+    some seven times the range or more."""
+    g = np.random.default_rng(1)
+    for offset in (0.0, 1.0, 10.0, 100.0):
+        x = (g.standard_normal((2000, 32)) + offset).astype(np.float32)
+        c, s, m = kv4.quantise(x)
+        off = np.abs(kv4.stands_for(c, s, m) - x).max(1)
+        lo, hi = x.min(1).astype(np.float64), x.max(1).astype(np.float64)
+        half, ends = s[:, 0] / 2.0, 2.0 ** -8 * (hi - lo + np.abs(lo))
+        assert (off <= np.maximum(half, ends) * (1 + 2.0 ** -20)).all()
+        assert (off <= half * (1 + 2.0 ** -6)).all() or offset > 1
+
+
+def test_attention_before_and_after_quantisation():
+    """Attention over what the cache stands for against attention over the rows as they were.  Of independent errors a
+    key's s / sqrt(12) moves a score by as much (|q| = sqrt(d)) and its weight by that share, a value's moves the output
+    like the values themselves: together sqrt(2) s / sqrt(12) of the output's root mean square (values of variance one),
+    taken half as large again."""
+    g = np.random.default_rng(2)
+    for d in (64, 128):
+        q, k, v = g.standard_normal((20, 4, d)), g.standard_normal((4, 500, d)), g.standard_normal((4, 500, d))
+        kc, vc = kv4.quantise(k), kv4.quantise(v)
+        out, ref = kv4.attention(q, kv4.stands_for(*kc), kv4.stands_for(*vc), 480), kv4.attention(q, k, v, 480)
+        step = np.sqrt((kc[1].astype(np.float64) ** 2).mean())
+        assert np.sqrt(((out - ref) ** 2).mean()) <= 1.5 * np.sqrt(2 / 12) * step * np.sqrt((ref ** 2).mean())
