@@ -1460,21 +1460,27 @@ __global__ void __launch_bounds__(32 * kRowsPerItem) kv4_rows_join_kernel(const 
         dst[d] = Elem<T>::from_f(kv4_join<D>(part, (size_t)a.n_heads * kRowsPerItem * (D + 2), r.z, d));
 }
 
+// f(head_dim as a constant)
+template <typename F>
+cudaError_t for_dim(int d, F f) {
+    switch (d) {
+        case 16: return f(std::integral_constant<int, 16>());
+        case 32: return f(std::integral_constant<int, 32>());
+        case 64: return f(std::integral_constant<int, 64>());
+        case 128: return f(std::integral_constant<int, 128>());
+        default: return cudaErrorInvalidValue;
+    }
+}
+
 template <typename T>
 cudaError_t launch_decode(const Kv4Attn &a, int d, int n_items, cudaStream_t st) {
     const dim3 grid((unsigned)n_items * a.n_heads), block(kKvThreads);
-    if constexpr (std::is_same<T, bf16>::value) {
-        if (d == 32) return launch_pdl(kv4_decode_mma_kernel<32>, grid, block, 0, st, a);
-        if (d == 64) return launch_pdl(kv4_decode_mma_kernel<64>, grid, block, 0, st, a);
-        if (d == 128) return launch_pdl(kv4_decode_mma_kernel<128>, grid, block, 0, st, a);
-    }
-    switch (d) {
-        case 16: return launch_pdl(kv4_decode_kernel<T, 16>, grid, block, 0, st, a);
-        case 32: return launch_pdl(kv4_decode_kernel<T, 32>, grid, block, 0, st, a);
-        case 64: return launch_pdl(kv4_decode_kernel<T, 64>, grid, block, 0, st, a);
-        case 128: return launch_pdl(kv4_decode_kernel<T, 128>, grid, block, 0, st, a);
-        default: return cudaErrorInvalidValue;
-    }
+    return for_dim(d, [&](auto dim) {
+        if constexpr (std::is_same<T, bf16>::value && dim() >= 32)
+            return launch_pdl(kv4_decode_mma_kernel<dim()>, grid, block, 0, st, a);
+        else
+            return launch_pdl(kv4_decode_kernel<T, dim()>, grid, block, 0, st, a);
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -1921,18 +1927,6 @@ Kv4Work kv4_work(const int32_t *hp) {
 int64_t kv4_workspace_bytes(const int32_t *hp) { return kv4_work(hp).total; }
 
 namespace {
-// f(head_dim as a constant)
-template <typename F>
-cudaError_t for_dim(int d, F f) {
-    switch (d) {
-        case 16: return f(std::integral_constant<int, 16>());
-        case 32: return f(std::integral_constant<int, 32>());
-        case 64: return f(std::integral_constant<int, 64>());
-        case 128: return f(std::integral_constant<int, 128>());
-        default: return cudaErrorInvalidValue;
-    }
-}
-
 template <typename T>
 cudaError_t append(const void *qkv, const Kv4View &v, const int32_t *hp, const int32_t *dp, cudaStream_t st) {
     const int H = hp[Q_HEADS] * hp[Q_DIM];
@@ -2032,11 +2026,9 @@ cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp,
     const int64_t blocks = (int64_t)pr.n_pre * nh + ((int64_t)pr.n_rows * (a.H / 8) + kPer - 1) / kPer;
     e = launch_pdl(kv4_prep_kernel, dim3((unsigned)blocks), dim3(kPrepThreads), 0, st, pr);
     if (e == cudaSuccess)
-        e = for_dim(d, [&](auto dim) {
-            return launch_pdl(kv4_read_kernel<__half, dim(), true>, dim3(hp[Q_PREREAD], nh), dim3(kRdThreads), 0, st, a.v,
-                              dp + hp[Q_O_PREREAD], (__half *)(ws + w.pool16), (int64_t)hp[Q_PREKEYS], nh,
-                              (const float *)pr.kv_scale);
-        });
+        e = launch_pdl(d == 64 ? kv4_read_kernel<__half, 64, true> : kv4_read_kernel<__half, 128, true>,
+                       dim3(hp[Q_PREREAD], nh), dim3(kRdThreads), 0, st, a.v, dp + hp[Q_O_PREREAD],
+                       (__half *)(ws + w.pool16), (int64_t)hp[Q_PREKEYS], nh, (const float *)pr.kv_scale);
     AttnPlan ap{};
     ap.req_off = dp + hp[Q_O_REQOFF];
     ap.req_ctx = dp + hp[Q_O_REQCTX];
@@ -2056,8 +2048,7 @@ cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp,
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const dim3 grid((unsigned)std::min<int64_t>((int64_t)a.n_wide_items * nh, 3LL * sms));
     ++*launches;
-    return d == 64 ? launch_pdl(kv4_rows_wide_kernel<64>, grid, dim3(kKvThreads), 0, st, a)
-                   : launch_pdl(kv4_rows_wide_kernel<128>, grid, dim3(kKvThreads), 0, st, a);
+    return launch_pdl(d == 64 ? kv4_rows_wide_kernel<64> : kv4_rows_wide_kernel<128>, grid, dim3(kKvThreads), 0, st, a);
 }
 
 }  // namespace orca
