@@ -54,11 +54,11 @@ def check(s, out, rms=True):
         r += n
 
 
-def run(s):
+def run(s, **kw):
     s.append()
     s.append_oracle()
     out = s.attention()
-    check(s, out)
+    check(s, out, **kw)
     return out
 
 
@@ -84,6 +84,18 @@ def test_prompts_in_groups(native, eng, dtype, d):  # noqa: F811
 
 
 SEVERAL = [(500, 0), (2, 1200), (1, 5200), (2, 1200), (1, 40)]  # at 40 heads of 128 in all forms
+
+
+def test_a_wide_head_beside_other_forms(native, eng):  # noqa: F811
+    """A prompt that is neither the first request nor alone, with one head whose values fp16 does not hold (attended on
+    the codes), beside groups and single rows."""
+    s = forms(Case(native, eng, 57, "bf16", 40, 128, SEVERAL[1:3] + SEVERAL[:1] + SEVERAL[3:]), prompts=1, groups=True,
+              split_groups=True, split_singles=True)
+    first = sum(s.n[:2])
+    s.qkv[first + 480, 2, 11] *= np.float32(2.0 ** 50)
+    s.qkv = rounded(s.qkv, "bf16").float().numpy()
+    s.upload()
+    run(s, rms=False)
 
 
 def test_all_forms_captured(native):  # noqa: F811
