@@ -343,7 +343,10 @@ int orca_attention_decode_noalloc(int32_t dtype, const void *qkv, const void *kv
  * the code c = the integer nearest to (x - m) / s (ties to even) within
  * 0 .. 15, with s = bf16((max - min) / 15) (fp32 difference and quotient) and
  * m = bf16(min), and stands for m + s c.  s = 0 holds c = 0.  A group in which
- * a value, s or m is not finite reads back as NaN.
+ * a value, s or m is not finite reads back as NaN.  What a component stands for
+ * is off by s / 2 at most, or, at the ends of the range, by what s and m lost to
+ * bf16: 2^-8 (max - min + |min|), the larger of the two where |min| is some
+ * seven times the range or more.
  *
  * Layout of a layer, with S = kv_slots rounded up to a multiple of 16:
  *   K codes  [n_heads][S][head_dim / 2]      component 2b in the low, 2b + 1 in
@@ -393,7 +396,14 @@ int64_t orca_kv4_workspace_bytes(const int32_t *host_plan);
  *   n_input)][head_dim] in the plan's dtype (the layout of a K/V pool layer).
  * attention: as orca_op_attention, the keys and values being what the slots
  *   stand for; the rows' own K/V must have been appended.  Scores and sums are
- *   held in fp32.  A group that reads back as NaN makes the rows that see its
+ *   held in fp32.  The plan chooses by the whole batch how a request's rows are
+ *   attended and where its keys are split, so the last bits of a row may depend
+ *   on the batch (never from call to call of a plan).  Few rows, fp32, and
+ *   head_dim 16 and 32: on the codes, weights times scales in 16 bits or more
+ *   (fp32: 24).  Many rows in bf16 at head_dim 64 and 128: keys, values and
+ *   weights rounded to fp16 (2^-11 each; a weight below 2^-25 of the largest by
+ *   2^-36 of it), except for heads in which groups differ by more than 2^28 in
+ *   size, which run on the codes.  A group that reads back as NaN makes the rows that see its
  *   key NaN, and no others: of a key, in the whole head; of a value, in the
  *   group's components at least (in the whole head where many rows at once run
  *   on fp16 operands).  Errors: INVALID, CUDA. */
@@ -418,7 +428,9 @@ int orca_op_kv4_attention(orca_engine *eng, const void *qkv, const void *kv4_lay
  *   min_p (0)          of those, the tokens with w_i >= min_p
  *   uniform u          the first kept id, in ascending order, whose cumulative
  *                      weight exceeds u times the kept total
- * The weights are rounded to 42 fraction bits and summed exactly.  Logits of
+ * The weights (to 2^-37 relative) are rounded to 42 fraction bits and summed
+ * exactly: a token below 2^-43 of the largest is never drawn, and of weights
+ * closer than that to min_p or to one another either side may be taken.  Logits of
  * -inf and NaN are never drawn (a row of nothing else gives -1); +inf leaves
  * only the +inf logits, equally likely.  Ranges: 0 <= T <= 1e6, top_p and
  * min_p in [0, 1], u in [0, 1); a row with a value outside (or NaN) gives -1

@@ -677,7 +677,7 @@ __device__ __forceinline__ void load_words(const void *p, uint32_t *w) {
 // the values, added to 2^23 and taken around code 8: an AND or two instead of a
 // shift, an AND and a conversion at an eighth of the rate.  Bound by latency and
 // issue: 64 requests of 4000 keys, 12 heads of 64, fp32: 123 us (277 with the
-// conversions, 139 without the values' early loads); 17 of <= 900 keys 10.8.
+// conversions, 139 without the values' early loads); 17 of <= 900 keys 11.6.
 __device__ __forceinline__ float nibble_bits(uint32_t w, int n) { return __uint_as_float(w & (15u << (4 * n))); }
 
 template <typename T, int D>
@@ -1146,7 +1146,7 @@ __global__ void __launch_bounds__(kKvThreads, kDecodeCtas) kv4_decode_mma_kernel
 // as in fp32 throughout.  4 requests of <= 200 rows over <= 500 keys, 30 heads of 128: 84 us, against 578 row by row
 // on kv4_decode_kernel; 30 heads of 16, 4 x <= 1000 rows over <= 800 keys, bf16: 198 and 1109.
 // P leaves the first product in the very registers that the second one takes it from.
-// Bound by issue and latency: 9 requests of <= 7 rows over <= 1500 keys, 32 heads of 128, 41 us (row by row 65), 51 MB:
+// Bound by issue and latency: 9 requests of <= 7 rows over <= 1500 keys, 32 heads of 128, 39 us (row by row 65), 51 MB:
 // 7.6 us at the copy rate; the schedulers issue in 52 % of active cycles, three CTAs of 168 registers per SM.
 constexpr int kRowsPerItem = 16;
 
@@ -1617,8 +1617,11 @@ struct Kv4Sizes {
 // chunks cost a join: 16 requests of 300 keys, 40 heads of 128, took 18.2 us at
 // six blocks per SM and 11.5 at three, one of 100 keys 5.1 us in chunks of 64 and
 // 3.2 in one; one of 4000 keys 17.1 us at six, 13.8 at three, 19.7 at one.
-// A row of few keys stays whole whatever the chunk: 300 keys, 40 heads, in chunks of 128 / whole: of 64 6.7 and 4.1 us, of
-// 128 7.7 and 5.1, fp32 64 7.6 and 5.3; 400 keys 6.8 and 4.9, 7.7 and 6.2, 7.6 and 6.4; 600 keys 7.5 and 8.4.
+// A row of few keys stays whole whatever the chunk.  One row, in chunks / whole, us at 350, 400, 450, 500, 550 and 600 keys
+// (replayed from a graph): 20 heads of 64 5.0/4.3 5.0/4.7 5.0/5.1 5.0/5.3 5.3/5.6 5.4/6.0; 40 heads of 64 6.0/4.3 6.3/4.8
+// 6.2/5.3 6.2/5.3 6.4/5.7 6.6/6.0; 40 heads of 128 6.9/5.5 7.1/5.9 7.1/6.5 7.2/6.5 6.9/7.2 6.4/7.7; two rows 7.9/6.6
+// 7.9/7.6 7.9/8.3 7.8/8.5; 5 heads of 128 5.2/5.1 5.2/5.6; fp32, 12 heads of 64 4.9/5.1 4.9/6.1, 40 heads 6.3/5.2 6.4/6.1
+// 6.5/6.3 6.5/6.3 5.7/7.6.  They cross between 350 and 620 keys by heads and type, in the middle at the value below.
 constexpr int kWholeRow = 400;
 int64_t row_items(int64_t keys, int chunk) { return keys <= kWholeRow ? 1 : (keys + chunk - 1) / chunk; }
 int kv4_row_chunk(const Kv4Batch &b, const Kv4Policy &policy, int num_sms) {
