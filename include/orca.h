@@ -403,7 +403,9 @@ int64_t orca_kv4_workspace_bytes(const int32_t *host_plan);
  *   (fp32: 24).  Many rows in bf16 at head_dim 64 and 128: keys, values and
  *   weights rounded to fp16 (2^-11 each; a weight below 2^-25 of the largest by
  *   2^-36 of it), except for heads in which groups differ by more than 2^28 in
- *   size, which run on the codes.  A group that reads back as NaN makes the rows that see its
+ *   size, which run on the codes.  Those rows, and single rows in bf16, take q as
+ *   fp16 scaled by its head's largest: exact down to 2^-28 of that.  Sizes beyond
+ *   2^100 may overflow.  A group that reads back as NaN makes the rows that see its
  *   key NaN, and no others: of a key, in the whole head; of a value, in the
  *   group's components at least (in the whole head where many rows at once run
  *   on fp16 operands).  Errors: INVALID, CUDA. */
