@@ -24,7 +24,7 @@
 // ids.
 //
 // Bound by barriers and latency, then by issue: 192 rows of 50257 with mixed
-// parameters take 61 to 63 us (38.6 MB: 5.8 us of reading), the schedulers issuing in
+// parameters take 61 to 64 us (38.6 MB: 5.8 us of reading), the schedulers issuing in
 // 44 % of their active cycles, barriers the first stall; a weight is about 95
 // warp instructions per 32 logits with its comparison and sum, two thirds of
 // them integer.  One row at T 0.8, top-k 50, top-p 0.95 takes 11.0 us on four
