@@ -417,6 +417,73 @@ int orca_op_kv4_attention(orca_engine *eng, const void *qkv, const void *kv4_lay
                           int32_t *dev_plan, void *workspace, void *out);
 
 /* ------------------------------------------------------------------------ */
+/* paged K/V cache                                                           */
+/* ------------------------------------------------------------------------ */
+/* A layer is [K|V][n_kv_heads][n_pages * page_size][head_dim] in the batch's
+ * dtype, the layout of a layer of the engine's own pool, its slots cut into
+ * n_pages pages of page_size slots (a multiple of 16).  Position t of request i
+ * is held in slot page_table[i * table_ld + t / page_size] * page_size +
+ * t % page_size: a request's pages may lie anywhere and requests may share
+ * pages.  Slots that no position of a call falls into are neither used nor
+ * changed.  The caller owns the memory (16-byte aligned).
+ *
+ * Query head h reads the keys and values of head h / (n_heads / n_kv_heads).
+ *
+ * A batch: request i has rows n_input[i] at positions ctx_len[i] + j; one with
+ * n_input[i] = 0 takes no part (neither its context nor its pages are read).
+ * The arrays are HOST memory, read during the call.  A plan made from it
+ * (orca_paged_plan_words int32 words, packed by orca_paged_plan_build; copied to
+ * device memory once, 16-byte aligned, both copies passed) serves every layer
+ * of that shape.  `eng` gives the number of SMs the work is split for (NULL:
+ * 152).  A plan is only read on the device: calls that overlap may share it, but
+ * not a workspace.  Contents of a plan other than what orca_paged_plan_build
+ * wrote are not checked.
+ * Supported: n_heads <= 1024, a multiple of n_kv_heads; head_dim 16, 32, 64 or
+ * 128; n_pages * page_size <= INT32_MAX - 15; contexts and rows of a request
+ * within n_pages * page_size; pages 0 .. n_pages - 1.  Errors: INVALID (also
+ * for a batch whose tables exceed 32-bit offsets), OOM. */
+typedef struct orca_paged_batch {
+    int32_t dtype, n_heads, n_kv_heads, head_dim, page_size, n_req;
+    int64_t n_pages;
+    int64_t table_ld; /* entries from one request's pages to the next one's */
+    const int32_t *n_input, *ctx_len, *page_table;
+} orca_paged_batch;
+int64_t orca_paged_plan_words(const orca_engine *eng, const orca_paged_batch *batch);
+int orca_paged_plan_build(const orca_engine *eng, const orca_paged_batch *batch, int32_t *host_buf, int64_t cap_words);
+/* Bytes of device memory that orca_op_paged_attention needs beside the plan
+ * (0: none, workspace may be NULL); any contents, 16-byte aligned. */
+int64_t orca_paged_workspace_bytes(const int32_t *host_plan);
+
+/* The two operators are asynchronous on the engine's stream, allocate nothing
+ * and may be captured into a CUDA graph (of that plan); the engine's device must be the
+ * current one.  Pointers are device pointers (16-byte aligned) but for
+ * host_plan; strides are in elements, a multiple of 16 bytes, 0 for rows
+ * without gaps.  Rows behind the
+ * batch's last and elements between a row's end and the next row are left alone.
+ *
+ * append: rows of qkv (ld_qkv apart) are n_heads queries, n_kv_heads keys and
+ *   n_kv_heads values side by side.  Queries and keys are rotated by their
+ *   position p: of the first rot_dim components (even, 0: none) of a head, the
+ *   pair (a, b) number i < rot_dim / 2 becomes (a c - b s, b c + a s) with
+ *   c = rope[p][i], s = rope[p][rot_dim / 2 + i], in fp32, rounded once.  A pair
+ *   is (i, i + rot_dim / 2), or (2 i, 2 i + 1) if neighbours is 1.  rope is fp32
+ *   [rope_len][rot_dim], rope_len at least every ctx_len + n_input of the batch.
+ *   Keys and values go to their positions' slots, queries to rows of q_out (ld_q
+ *   apart; NULL: left alone; qkv itself with ld_q = ld_qkv: in place).  INVALID
+ *   if two rows share a slot, or qkv, q_out and the layer overlap in another way.
+ * attention: row j of request i (a row of q: n_heads * head_dim elements) sees
+ *   the positions 0 .. ctx_len + j of its request: softmax(scale q k) v per
+ *   head, to the same row of out.  scale 0 means 1 / sqrt(head_dim); it must be
+ *   finite and not negative.  The rows' own K/V must have been appended.  INVALID if
+ *   out overlaps q or the layer. */
+int orca_op_paged_append(orca_engine *eng, const void *qkv, int64_t ld_qkv, void *kv_layer, const int32_t *host_plan,
+                         const int32_t *dev_plan, const float *rope, int32_t rope_len, int32_t rot_dim,
+                         int32_t neighbours, void *q_out, int64_t ld_q);
+int orca_op_paged_attention(orca_engine *eng, const void *q, int64_t ld_q, const void *kv_layer,
+                            const int32_t *host_plan, const int32_t *dev_plan, float scale, void *workspace, void *out,
+                            int64_t ld_out);
+
+/* ------------------------------------------------------------------------ */
 /* sampling                                                                  */
 /* ------------------------------------------------------------------------ */
 /* One token per row of logits [n_rows][ld] (dtype elements, the first `vocab`

@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <new>
 #include <type_traits>
@@ -1110,6 +1111,104 @@ int orca_op_kv4_attention(orca_engine *E, const void *qkv, const void *kv4_layer
         return ORCA_ERR_INVALID;
     int n = 0;
     const cudaError_t e = kv4_attention(qkv, kv4_layer, host_plan, dev_plan, workspace, out, E->d_err, &n, E->st);
+    E->launches += n - 1;
+    return launched(E, e);
+}
+
+// ---------------------------------------------------------------------------
+// paged K/V cache
+// ---------------------------------------------------------------------------
+namespace {
+bool paged_batch(const orca_paged_batch *o, PagedBatch *b) {
+    if (!o || (o->dtype != ORCA_DTYPE_FP32 && o->dtype != ORCA_DTYPE_BF16) || o->n_kv_heads < 1 ||
+        o->n_heads < o->n_kv_heads || o->n_heads > 1024 || o->n_heads % o->n_kv_heads ||
+        (o->head_dim != 16 && o->head_dim != 32 && o->head_dim != 64 && o->head_dim != 128) || o->page_size < 16 ||
+        o->page_size % 16 || o->n_pages < 1 || o->n_pages > (INT32_MAX - 15) / o->page_size || o->n_req < 1 ||
+        !o->n_input || !o->ctx_len || !o->page_table || o->table_ld < 1 || o->table_ld > INT32_MAX)
+        return false;
+    *b = {o->dtype,   o->n_heads,  o->n_kv_heads, o->head_dim, o->page_size, o->n_req,
+          o->n_pages, o->table_ld, o->n_input,    o->ctx_len,  o->page_table};
+    return true;
+}
+// rows of `width` elements, `ld` apart: at least as far as they are wide, every row 16-byte aligned
+bool rows_ok(const void *p, int64_t ld, int64_t width, int es) {
+    return aligned16(p) && ld >= width && ld <= INT32_MAX && ld * es % 16 == 0;
+}
+// Whether [a, a + an) and [b, b + bn) share a byte.
+bool overlap(const void *a, int64_t an, const void *b, int64_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+}  // namespace
+
+int64_t orca_paged_plan_words(const orca_engine *E, const orca_paged_batch *batch) {
+    PagedBatch b;
+    if (!paged_batch(batch, &b)) return ORCA_ERR_INVALID;
+    const int64_t w = paged_plan_words(b, E ? E->num_sms : kPlanSms);
+    return w < 0 ? ORCA_ERR_INVALID : w;
+}
+
+int orca_paged_plan_build(const orca_engine *E, const orca_paged_batch *batch, int32_t *host_buf, int64_t cap_words) {
+    PagedBatch b;
+    if (!host_buf || !paged_batch(batch, &b)) return ORCA_ERR_INVALID;
+    try {
+        return paged_plan_build(b, E ? E->num_sms : kPlanSms, host_buf, cap_words) ? ORCA_OK : ORCA_ERR_INVALID;
+    } catch (const std::bad_alloc &) {
+        return ORCA_ERR_OOM;
+    }
+}
+
+int64_t orca_paged_workspace_bytes(const int32_t *host_plan) {
+    return paged_plan_ok(host_plan) ? paged_workspace_bytes(host_plan) : ORCA_ERR_INVALID;
+}
+
+int orca_op_paged_append(orca_engine *E, const void *qkv, int64_t ld_qkv, void *kv_layer, const int32_t *host_plan,
+                         const int32_t *dev_plan, const float *rope, int32_t rope_len, int32_t rot_dim,
+                         int32_t neighbours, void *q_out, int64_t ld_q) {
+    if (!E || !qkv || !kv_layer || !dev_plan || !paged_plan_ok(host_plan)) return ORCA_ERR_INVALID;
+    const PagedInfo p = paged_plan_info(host_plan);
+    const int64_t es = p.dtype == ORCA_DTYPE_BF16 ? 2 : 4, qw = (int64_t)p.heads * p.head_dim;
+    const int64_t w = qw + 2 * (int64_t)p.kv_heads * p.head_dim;
+    if (!ld_qkv) ld_qkv = w;
+    if (!ld_q) ld_q = qw;
+    if (p.twice || !aligned16(kv_layer) || !aligned16(dev_plan) || !rows_ok(qkv, ld_qkv, w, (int)es) || rot_dim < 0 ||
+        rot_dim > p.head_dim || rot_dim % 2 || (neighbours != 0 && neighbours != 1) || !on_device(E))
+        return ORCA_ERR_INVALID;
+    if (rot_dim > 0 && (!rope || !aligned16(rope) || rope_len < p.max_pos)) return ORCA_ERR_INVALID;
+    const int64_t qkv_bytes = p.rows ? ((p.rows - 1) * ld_qkv + w) * es : 0;
+    const int64_t layer_bytes = 2 * (int64_t)p.kv_heads * p.slots * p.head_dim * es;
+    if (overlap(qkv, qkv_bytes, kv_layer, layer_bytes)) return ORCA_ERR_INVALID;
+    if (q_out) {
+        const int64_t q_bytes = p.rows ? ((p.rows - 1) * ld_q + qw) * es : 0;
+        if (!rows_ok(q_out, ld_q, qw, (int)es) || overlap(q_out, q_bytes, kv_layer, layer_bytes) ||
+            (q_out == qkv ? ld_q != ld_qkv : overlap(q_out, q_bytes, qkv, qkv_bytes)))
+            return ORCA_ERR_INVALID;
+    }
+    if (p.rows == 0) return ORCA_OK;
+    return launched(E, paged_append({qkv, kv_layer, q_out, rope, ld_qkv, ld_q, rot_dim, neighbours != 0}, host_plan,
+                                    dev_plan, E->st));
+}
+
+int orca_op_paged_attention(orca_engine *E, const void *q, int64_t ld_q, const void *kv_layer,
+                            const int32_t *host_plan, const int32_t *dev_plan, float scale, void *workspace, void *out,
+                            int64_t ld_out) {
+    if (!E || !q || !kv_layer || !dev_plan || !out || !paged_plan_ok(host_plan)) return ORCA_ERR_INVALID;
+    const PagedInfo p = paged_plan_info(host_plan);
+    const int64_t es = p.dtype == ORCA_DTYPE_BF16 ? 2 : 4, w = (int64_t)p.heads * p.head_dim;
+    if (!ld_q) ld_q = w;
+    if (!ld_out) ld_out = w;
+    if (!aligned16(kv_layer) || !aligned16(dev_plan) || !rows_ok(q, ld_q, w, (int)es) ||
+        !rows_ok(out, ld_out, w, (int)es) || !aligned16(workspace) ||
+        (!workspace && paged_workspace_bytes(host_plan) > 0) || !(scale >= 0.f) || scale > 3e38f || !on_device(E))
+        return ORCA_ERR_INVALID;
+    if (p.rows == 0) return ORCA_OK;
+    const int64_t q_bytes = ((p.rows - 1) * ld_q + w) * es, out_bytes = ((p.rows - 1) * ld_out + w) * es;
+    const int64_t layer_bytes = 2 * (int64_t)p.kv_heads * p.slots * p.head_dim * es;
+    if (overlap(out, out_bytes, q, q_bytes) || overlap(out, out_bytes, kv_layer, layer_bytes)) return ORCA_ERR_INVALID;
+    int n = 0;
+    const float s = scale > 0.f ? scale : 1.f / std::sqrt((float)p.head_dim);
+    const cudaError_t e =
+        paged_attention({q, kv_layer, workspace, out, ld_q, ld_out, s}, host_plan, dev_plan, E->d_err, &n, E->st);
     E->launches += n - 1;
     return launched(E, e);
 }

@@ -188,6 +188,40 @@ cudaError_t kv4_read(const void *layer, const int32_t *hp, const int32_t *dp, vo
 cudaError_t kv4_attention(const void *qkv, const void *layer, const int32_t *hp, int32_t *dp, void *workspace,
                           void *out, unsigned *err, int *launches, cudaStream_t st);
 
+// Paged K/V cache (k_paged.cu).  A batch over the pages of one layer and the
+// plan built from it (int32 words).
+struct PagedBatch {
+    int dtype, n_heads, n_kv_heads, head_dim, page_size, n_req;
+    int64_t n_pages, table_ld;
+    const int32_t *n_input, *ctx_len, *page_table;
+};
+struct PagedInfo {
+    int dtype, heads, kv_heads, head_dim, slots, rows, max_pos;
+    bool twice;  // two rows of the batch share a slot
+};
+struct PagedAppend {
+    const void *qkv;
+    void *layer, *q_out;
+    const float *rope;
+    int64_t ld_qkv, ld_q;
+    int rot;
+    bool neighbours;
+};
+struct PagedAttn {
+    const void *q, *layer;
+    void *workspace, *out;
+    int64_t ld_q, ld_out;
+    float scale;
+};
+int64_t paged_plan_words(const PagedBatch &b, int num_sms);  // -1: a range or page is out of bounds, or it is too large
+bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t cap);
+bool paged_plan_ok(const int32_t *hp);
+PagedInfo paged_plan_info(const int32_t *hp);
+int64_t paged_workspace_bytes(const int32_t *hp);
+cudaError_t paged_append(const PagedAppend &p, const int32_t *hp, const int32_t *dp, cudaStream_t st);
+cudaError_t paged_attention(const PagedAttn &p, const int32_t *hp, const int32_t *dp, unsigned *err, int *launches,
+                            cudaStream_t st);
+
 constexpr int kPrefillRowsPerTile = 128;  // query rows per prefill tile (the tcgen05 kernel's M)
 
 // A bounded wait that nothing satisfies, given up after limit_ns (failure-

@@ -34,7 +34,8 @@ EXPORTS = [
     "orca_pack_weight",
     "orca_attention_decode_noalloc", "orca_kv4_layer_bytes", "orca_kv4_plan_words", "orca_kv4_plan_build",
     "orca_kv4_workspace_bytes", "orca_op_kv4_append", "orca_op_kv4_read", "orca_op_kv4_attention", "orca_op_sample",
-    "orca_sample_last",
+    "orca_sample_last", "orca_paged_plan_words", "orca_paged_plan_build", "orca_paged_workspace_bytes",
+    "orca_op_paged_append", "orca_op_paged_attention",
     "orca_debug_expire_wait", "orca_sched_create", "orca_sched_destroy",
     "orca_sched_submit", "orca_sched_set_token_feedback", "orca_sched_next", "orca_sched_complete", "orca_sched_cancel",
     "orca_sched_stats_get", "orca_sched_request_get",
@@ -68,6 +69,12 @@ class Batch(C.Structure):
     _fields_ = [("n_req", C.c_int32), ("request_id", C.POINTER(C.c_int64)), ("phase", C.POINTER(C.c_int32)),
                 ("n_input", C.POINTER(C.c_int32)), ("ctx_len", C.POINTER(C.c_int32)),
                 ("kv_offset", C.POINTER(C.c_int64)), ("tokens", C.POINTER(C.c_int32))]
+
+
+class PagedBatch(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("n_heads", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("page_size", C.c_int32), ("n_req", C.c_int32), ("n_pages", C.c_int64), ("table_ld", C.c_int64),
+                ("n_input", C.c_void_p), ("ctx_len", C.c_void_p), ("page_table", C.c_void_p)]
 
 
 class KVLayout(C.Structure):
@@ -136,6 +143,11 @@ _sig = {
     "orca_op_kv4_append": (C.c_int, [P, P, P, P, P]),
     "orca_op_kv4_read": (C.c_int, [P, P, P, P, P]),
     "orca_op_kv4_attention": (C.c_int, [P, P, P, P, P, P, P]),
+    "orca_paged_plan_words": (C.c_int64, [P, C.POINTER(PagedBatch)]),
+    "orca_paged_plan_build": (C.c_int, [P, C.POINTER(PagedBatch), P, C.c_int64]),
+    "orca_paged_workspace_bytes": (C.c_int64, [P]),
+    "orca_op_paged_append": (C.c_int, [P, P, C.c_int64, P, P, P, P, C.c_int32, C.c_int32, C.c_int32, P, C.c_int64]),
+    "orca_op_paged_attention": (C.c_int, [P, P, C.c_int64, P, P, P, C.c_float, P, P, C.c_int64]),
     "orca_op_sample": (C.c_int, [P, C.c_int32, P, C.c_int32, C.c_int32, C.c_int64, P, P, P, P, P, P]),
     "orca_sample_last": (C.c_int, [P, P, P, P, P, P, P]),
     "orca_debug_expire_wait": (C.c_int, [P, C.c_int64]),
@@ -360,6 +372,40 @@ class Engine:
                          sync: bool = True):
         check(lib.orca_op_kv4_attention(self._h, qkv, layer, _ptr(plan), dev_plan, workspace, out),
               "orca_op_kv4_attention")
+        if sync:
+            self.sync()
+
+    def paged_plan(self, dtype: int, n_heads: int, n_kv_heads: int, head_dim: int, page_size: int, n_pages: int, n_input,
+                   ctx_len, page_table) -> np.ndarray:
+        """Plan of a batch over a paged K/V layer (see orca.h): int32 words, to be copied to the device once.
+        page_table: [requests, pages of the longest at least]."""
+        n, c, t = _i32(n_input), _i32(ctx_len), _i32(page_table)
+        if t.ndim != 2 or not len(n) == len(c) == len(t):
+            raise ValueError("n_input, ctx_len and the rows of page_table differ in number")
+        b = PagedBatch(dtype, n_heads, n_kv_heads, head_dim, page_size, len(n), n_pages, t.shape[1], _ptr(n), _ptr(c),
+                       _ptr(t))
+        buf = np.zeros(check(lib.orca_paged_plan_words(self._h, C.byref(b)), "orca_paged_plan_words"), np.int32)
+        check(lib.orca_paged_plan_build(self._h, C.byref(b), _ptr(buf), buf.size), "orca_paged_plan_build")
+        return buf
+
+    @staticmethod
+    def paged_workspace_bytes(plan: np.ndarray) -> int:
+        return check(lib.orca_paged_workspace_bytes(_ptr(plan)), "orca_paged_workspace_bytes")
+
+    def op_paged_append(self, qkv: int, layer: int, plan: np.ndarray, dev_plan: int, q_out: int = 0, rope: int = 0,
+                        rope_len: int = 0, rot_dim: int = 0, neighbours: bool = False, ld_qkv: int = 0, ld_q: int = 0,
+                        sync: bool = True):
+        """Rotate and append a batch's rows (device pointers; strides in elements, 0: rows without gaps; see orca.h)."""
+        check(lib.orca_op_paged_append(self._h, qkv, ld_qkv, layer, _ptr(plan), dev_plan, rope, rope_len, rot_dim,
+                                       neighbours, q_out, ld_q), "orca_op_paged_append")
+        if sync:
+            self.sync()
+
+    def op_paged_attention(self, q: int, layer: int, plan: np.ndarray, dev_plan: int, workspace: int, out: int,
+                           scale: float = 0.0, ld_q: int = 0, ld_out: int = 0, sync: bool = True):
+        """Attention of a batch's rows over their pages (device pointers; strides in elements, 0: rows without gaps)."""
+        check(lib.orca_op_paged_attention(self._h, q, ld_q, layer, _ptr(plan), dev_plan, scale, workspace, out, ld_out),
+              "orca_op_paged_attention")
         if sync:
             self.sync()
 

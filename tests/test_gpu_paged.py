@@ -1,0 +1,516 @@
+"""The paged K/V cache on the GPU: append with rotated positions and attention over
+the pages, against the float64 oracle (oracle/paged.py).
+
+Tolerances.  u is half a step of the type (bf16 2^-8, fp32 2^-24).
+Append: a rotated component is a c - b s in fp32, two products and a sum (2^-24
+of |a c| + |b s| each at most), then rounded once to the type: u |ref| + 2^-22
+(|a c| + |b s|).  What is not rotated is exact.
+Attention: a score is a sum of D products with a running rounding of 2^-23 at
+most each (tensor cores cut sums off instead of rounding), (D + 16) 2^-23 sum |q_i
+k_i| scale, and moves a weight by that factor; numerator and denominator both
+move: 2 of it times max |v|, and 2^-20 for the exponential (its argument is held
+to 2^-24 of its size, which the score's term covers too).  bf16: weights enter the second product rounded
+to bf16, independently of each other, |d_t| <= 2^-8, so that the output moves by
+sum w_t d_t (v_t - out): more than 7 * 2^-8 sqrt(sum w_t^2 (v_t - out)^2) has a
+probability of 2 exp(-24.5) = 5e-11 (Hoeffding).  Sums over T keys: T 2^-23
+relative at most.  fp32: the products of parts of 11 bits leave 2^-21 of each
+product.  Then u |ref|."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged
+
+pytestmark = pytest.mark.gpu
+
+TD = {"bf16": torch.bfloat16, "fp32": torch.float32}
+U = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -24}
+TYPES = [("bf16", 128), ("bf16", 64), ("bf16", 32), ("bf16", 16), ("fp32", 128), ("fp32", 64), ("fp32", 32),
+         ("fp32", 16)]
+
+
+@pytest.fixture(scope="module")
+def native():
+    from iteration_level_scheduling_gb300 import build
+    build.build()
+    from iteration_level_scheduling_gb300 import native as n
+    return n
+
+
+@pytest.fixture(scope="module")
+def eng(native):
+    e = native.Engine(1, 64, 1, 64, 64, 64, native.DTYPE_BF16, 64, 64, 64, None,
+                      torch.cuda.current_stream().cuda_stream)
+    yield e
+    e.close()
+
+
+def rounded(x, dtype):
+    """float32 values of the type."""
+    return torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(TD[dtype]).float().numpy()
+
+
+def limits(dtype, q, k, v, c, scale=None, equal=False):
+    """The oracle's output for q [n, heads, d] over k, v [kv_heads, keys, d], and what it may be off by."""
+    heads, d = q.shape[1:]
+    group, scale = heads // k.shape[0], scale or 1 / np.sqrt(d)
+    ref, spread = paged.attention(q, k, v, c, scale)
+    fin = np.abs(np.where(np.isfinite(k), k, 0))  # (a key of -inf has no weight)
+    size = 0 if equal else max((np.abs(q[:, h]) @ fin[h // group].T).max() for h in range(heads)) * scale
+    tol = 2 * (d + 16) * 2.0 ** -23 * size + 3 * 2.0 ** -20 + k.shape[1] * 2.0 ** -23
+    if dtype == "fp32":
+        tol += 2 * 2.0 ** -21 * size + 2.0 ** -21
+    lim = U[dtype] * np.abs(ref) + tol * np.abs(v).max()
+    return ref, lim + 7 * 2.0 ** -8 * spread if dtype == "bf16" else lim
+
+
+class Case:
+    """Requests (rows, ctx) over pages in random order; every slot that no request covers is NaN."""
+
+    def __init__(self, native, eng, seed, dtype, heads, kv_heads, d, page, reqs, std=1.0, pad=0, table=None, n_pages=0):
+        g = self.g = np.random.default_rng(seed)
+        self.native, self.eng, self.dtype, self.page, self.reqs = native, eng, dtype, page, reqs
+        self.heads, self.kv_heads, self.d, self.pad = heads, kv_heads, d, pad
+        self.n, self.c = [n for n, _ in reqs], [c for _, c in reqs]
+        need = [(n + c + page - 1) // page for n, c in reqs]
+        self.n_pages = n_pages or sum(need) + 2
+        if table is None:
+            order, table, at = g.permutation(self.n_pages), np.full((len(reqs), max(need + [1])), -1), 0
+            for i, m in enumerate(need):
+                table[i, :m] = order[at:at + m]
+                at += m
+        self.table = np.ascontiguousarray(table, np.int32)
+        self.rows, self.H = sum(self.n), heads * d
+        self.slots = self.n_pages * page
+        self.host = np.full((2, kv_heads, self.slots, d), np.nan, np.float32)
+        for (n, c), t in zip(reqs, self.table):
+            s = paged.slots(t, page, 0, n + c) if n else np.zeros(0, np.int64)
+            self.host[:, :, s] = rounded(g.standard_normal((2, kv_heads, len(s), d)) * std, dtype)
+        self.q = rounded(g.standard_normal((self.rows, heads, d)), dtype)
+        code = native.DTYPE_BF16 if dtype == "bf16" else native.DTYPE_FP32
+        self.plan = eng.paged_plan(code, heads, kv_heads, d, page, self.n_pages, self.n, self.c, self.table)
+        self.dplan = torch.from_numpy(self.plan).cuda()
+        self.work = torch.full((max(16, eng.paged_workspace_bytes(self.plan)),), 0xFF, dtype=torch.uint8, device="cuda")
+        self.upload()
+
+    def padded(self, x, pad):
+        """Device rows of x [rows, ...] with `pad` NaN behind each, and two rows of NaN behind the last."""
+        x = x.reshape(len(x), int(np.prod(x.shape[1:])))
+        t = torch.full((len(x) + 2, x.shape[1] + pad), float("nan"), dtype=TD[self.dtype], device="cuda")
+        t[:len(x), :x.shape[1]] = torch.from_numpy(np.ascontiguousarray(x)).cuda().to(TD[self.dtype])
+        return t
+
+    def upload(self):
+        self.layer = torch.from_numpy(self.host).cuda().to(TD[self.dtype])
+        self.dq = self.padded(self.q, self.pad)
+
+    def attention(self, work=None, dplan=None, **kw):
+        out = torch.full((self.rows + 2, self.H + self.pad), 768.0, dtype=TD[self.dtype], device="cuda")
+        self.eng.op_paged_attention(self.dq.data_ptr(), self.layer.data_ptr(), self.plan,
+                                    (self.dplan if dplan is None else dplan).data_ptr(),
+                                    (self.work if work is None else work).data_ptr(), out.data_ptr(),
+                                    ld_q=self.H + self.pad, ld_out=self.H + self.pad, **kw)
+        return out
+
+    def limits(self, scale=None, equal=False):
+        """Oracle's output and tolerance of every row (equal: all scores of a row are the same bits)."""
+        ref, lim, r = np.zeros((self.rows, self.heads, self.d)), np.zeros((self.rows, self.heads, self.d)), 0
+        for (n, c), t in zip(self.reqs, self.table):
+            if n:
+                k, v = self.host[:, :, paged.slots(t, self.page, 0, n + c)]
+                ref[r:r + n], lim[r:r + n] = limits(self.dtype, self.q[r:r + n], k, v, c, scale, equal)
+            r += n
+        return ref, lim
+
+    def check(self, out, **kw):
+        ref, lim = self.limits(**kw)
+        o = out.float().cpu().numpy()
+        assert (o[self.rows:] == 768).all() and (o[:, self.H:] == 768).all()  # what is behind the rows stays
+        got = o[:self.rows, :self.H].reshape(ref.shape).astype(np.float64)
+        off = np.abs(got - ref)
+        assert np.isfinite(got).all() and (off <= lim).all(), float((off / lim).max())
+
+
+# --------------------------------------------------------------------------- #
+# append
+# --------------------------------------------------------------------------- #
+def append_case(native, eng, seed, dtype, heads, kv_heads, d, page, reqs, rot, neighbours, pad=0, std=1.0):
+    s = Case(native, eng, seed, dtype, heads, kv_heads, d, page, reqs)
+    W = heads + 2 * kv_heads
+    s.qkv = rounded(s.g.standard_normal((s.rows, W, d)) * std, dtype)
+    s.dqkv = s.padded(s.qkv, pad)
+    s.rot, s.nb, s.apad = rot, neighbours, pad
+    s.rope = paged.rope_table(max(n + c for n, c in reqs) + 1, rot)
+    s.drope = torch.from_numpy(s.rope).cuda()
+    s.q_out = torch.full((s.rows + 2, s.H + pad), 512.0, dtype=TD[dtype], device="cuda")
+    return s
+
+
+def do_append(s, q_out=True, **kw):
+    s.eng.op_paged_append(s.dqkv.data_ptr(), s.layer.data_ptr(), s.plan, s.dplan.data_ptr(),
+                          q_out=s.q_out.data_ptr() if q_out else 0, rope=s.drope.data_ptr() if s.rot else 0,
+                          rope_len=len(s.rope) if s.rot else 0, rot_dim=s.rot, neighbours=s.nb,
+                          ld_qkv=s.dqkv.shape[1], ld_q=s.q_out.shape[1], **kw)
+
+
+def check_append(s, q=True):
+    pos = np.concatenate([np.arange(c, c + n) for n, c in s.reqs])
+    qk = s.heads + s.kv_heads
+    ref = s.qkv.astype(np.float64)
+    lim = np.zeros(ref.shape)
+    if s.rot:
+        ref[:, :qk] = paged.rotate(s.qkv[:, :qk], s.rope[pos], s.rot, s.nb)
+        big = np.abs(s.qkv[:, :qk, :s.rot]).max(-1, keepdims=True) * 2  # |a c| + |b s| of any pair of the head
+        lim[:, :qk, :s.rot] = U[s.dtype] * np.abs(ref[:, :qk, :s.rot]) + 2.0 ** -22 * big
+    if q:
+        got = s.q_out.float().cpu().numpy()
+        assert (got[s.rows:] == 512).all() and (got[:, s.H:] == 512).all()
+        got = got[:s.rows, :s.H].reshape(s.rows, s.heads, s.d)
+        assert (np.abs(got - ref[:, :s.heads]) <= lim[:, :s.heads]).all()
+    want, tol = s.host.astype(np.float64), np.zeros(s.host.shape)
+    r = 0
+    for (n, c), t in zip(s.reqs, s.table):
+        for j in range(n):
+            at = paged.slots(t, s.page, c + j, 1)[0]
+            for x in (0, 1):
+                h = s.heads + x * s.kv_heads
+                want[x, :, at], tol[x, :, at] = ref[r, h:h + s.kv_heads], lim[r, h:h + s.kv_heads]
+            r += 1
+    got = s.layer.float().cpu().numpy()
+    assert (np.isnan(got) == np.isnan(want)).all()  # no other slot is touched
+    assert (np.nan_to_num(np.abs(got - want)) <= tol).all()
+
+
+REQS = [(1, 0), (7, 3), (1, 12), (66, 0), (2, 31), (3, 47), (1, 16), (0, 5), (1, 15)]
+
+
+@pytest.mark.parametrize("neighbours", [False, True])
+@pytest.mark.parametrize("dtype,d", TYPES)
+def test_append(native, eng, dtype, d, neighbours):
+    for rot in sorted({0, d, d // 2, 2, 6, d - 2}):
+        s = append_case(native, eng, rot, dtype, 6, 3, d, 32, REQS, rot, neighbours, pad=8)
+        do_append(s)
+        check_append(s)
+
+
+@pytest.mark.parametrize("heads,kv_heads,page", [(1, 1, 16), (5, 1, 48), (40, 8, 16), (7, 7, 256), (71, 1, 128)])
+def test_append_shapes(native, eng, heads, kv_heads, page):
+    for dtype in ("bf16", "fp32"):
+        s = append_case(native, eng, 3, dtype, heads, kv_heads, 64, page, [(33, 100), (1, 0), (130, 7)], 64, False)
+        do_append(s)
+        check_append(s)
+
+
+@pytest.mark.parametrize("rot,neighbours", [(64, False), (20, False), (22, True), (0, False)])
+def test_append_in_place_and_without_queries(native, eng, rot, neighbours):
+    s = append_case(native, eng, 4, "bf16", 6, 2, 64, 16, REQS, rot, neighbours)
+    do_append(s, q_out=False)
+    check_append(s, q=False)
+    assert (s.q_out == 512).all()
+    before = s.dqkv.clone()
+    s.eng.op_paged_append(s.dqkv.data_ptr(), s.layer.data_ptr(), s.plan, s.dplan.data_ptr(), q_out=s.dqkv.data_ptr(),
+                          rope=s.drope.data_ptr() if rot else 0, rope_len=len(s.rope) if rot else 0, rot_dim=rot,
+                          neighbours=neighbours, ld_q=s.dqkv.shape[1])
+    assert torch.equal(s.dqkv[:s.rows, s.H:], before[:s.rows, s.H:])
+    s.q_out[:s.rows, :s.H] = s.dqkv[:s.rows, :s.H]
+    check_append(s)
+
+
+def test_append_of_infinities_and_nan(native, eng):
+    """They stay in their pair."""
+    s = append_case(native, eng, 5, "bf16", 2, 1, 64, 16, [(3, 2)], 64, False)
+    s.qkv[0, 0, 5], s.qkv[1, 2, 7], s.qkv[2, 3, 9] = np.inf, np.nan, -np.inf
+    s.dqkv = s.padded(s.qkv, 0)
+    do_append(s)
+    q = s.q_out[:3, :128].float().cpu().numpy().reshape(3, 2, 64)
+    assert not np.isfinite(q[0, 0, [5, 37]]).any() and np.isfinite(np.delete(q[0, 0], [5, 37])).all()
+    at = paged.slots(s.table[0], 16, 3, 2)
+    k = s.layer[0, 0, at[0]].float().cpu().numpy()
+    assert np.isnan(k[[7, 39]]).all() and np.isfinite(np.delete(k, [7, 39])).all()
+    v = s.layer[1, 0, at[1]].float().cpu().numpy()
+    assert v[9] == -np.inf and np.isfinite(np.delete(v, 9)).all()
+
+
+# --------------------------------------------------------------------------- #
+# attention
+# --------------------------------------------------------------------------- #
+EDGES = [(1, c) for c in (0, 1, 14, 15, 16, 17, 31, 32, 47, 63, 64, 65, 127, 128, 255, 256, 300, 511, 512, 700)]
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(3, 3), (8, 2), (5, 1)])
+@pytest.mark.parametrize("dtype,d", TYPES)
+def test_single_rows(native, eng, dtype, d, heads, kv_heads):
+    s = Case(native, eng, 1, dtype, heads, kv_heads, d, 16, EDGES, pad=8)
+    s.check(s.attention())
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(2, 2), (8, 2), (16, 1), (24, 1), (40, 1), (7, 1), (71, 1)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 32), ("fp32", 64), ("fp32", 128)])
+def test_shared_heads(native, eng, dtype, d, heads, kv_heads):
+    s = Case(native, eng, 2, dtype, heads, kv_heads, d, 48, [(1, 200), (2, 30), (5, 77), (0, 3), (1, 0), (33, 64)])
+    s.check(s.attention())
+
+
+@pytest.mark.parametrize("page", [16, 32, 48, 64, 128, 144, 256, 1024])
+def test_page_sizes(native, eng, page):
+    for dtype, d in (("bf16", 128), ("bf16", 64), ("fp32", 32)):
+        s = Case(native, eng, page, dtype, 4, 2, d, page, [(1, 900), (1, page - 1), (1, page), (4, page - 2), (150, 333)])
+        s.check(s.attention())
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+def test_several_rows(native, eng, dtype, d):
+    s = Case(native, eng, 3, dtype, 6, 2, d, 16, [(2, 0), (17, 0), (9, 100), (64, 0), (130, 1), (33, 500), (128, 128)])
+    s.check(s.attention())
+
+
+@pytest.mark.parametrize("dtype,d,heads,kv_heads", [("bf16", 128, 4, 4), ("bf16", 128, 8, 1), ("bf16", 64, 5, 1),
+                                                     ("bf16", 64, 6, 2), ("bf16", 128, 40, 1), ("fp32", 128, 4, 1),
+                                                     ("bf16", 16, 3, 1)])
+def test_prompts(native, eng, dtype, d, heads, kv_heads):
+    s = Case(native, eng, 4, dtype, heads, kv_heads, d, 32, [(300, 0), (257, 600), (128, 0), (1, 2000), (700, 13)], pad=8)
+    s.check(s.attention())
+
+
+@pytest.mark.parametrize("dtype,d,kv_heads,reqs", [
+    ("bf16", 128, 1, [(1, 40000)]), ("bf16", 64, 2, [(1, 30001), (1, 5)]), ("fp32", 64, 1, [(1, 20000)]),
+    ("bf16", 128, 1, [(7, 20000), (1, 9000)]), ("bf16", 128, 1, [(70, 9000)]), ("fp32", 128, 1, [(20, 5000)])])
+def test_long_contexts(native, eng, dtype, d, kv_heads, reqs):
+    s = Case(native, eng, 5, dtype, 4 * kv_heads, kv_heads, d, 64, reqs)
+    s.check(s.attention())
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.03, 1e-30])
+def test_scales(native, eng, scale):
+    for dtype in ("bf16", "fp32"):
+        s = Case(native, eng, 6, dtype, 4, 2, 64, 16, [(1, 333), (3, 40), (140, 20)])
+        s.check(s.attention(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 16), ("fp32", 64)])
+def test_large_scores(native, eng, dtype, d):
+    """Rows that grow along the context: the maximum moves all the time, most weights vanish."""
+    s = Case(native, eng, 7, dtype, 4, 2, d, 16, [(1, 700), (9, 200), (200, 100)])
+    for (n, c), t in zip(s.reqs, s.table):
+        at = paged.slots(t, 16, 0, n + c)
+        s.host[0][:, at] = rounded(s.host[0][:, at] * np.linspace(0, 30, n + c)[None, :, None], dtype)
+    s.upload()
+    s.check(s.attention())
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+def test_scores_far_from_zero(native, eng, dtype, d):
+    """All scores of a row near the type's lowest or highest values that still have a softmax."""
+    for sign in (1.0, -1.0):
+        s = Case(native, eng, 8, dtype, 2, 1, d, 16, [(1, 100), (5, 40), (140, 20)])
+        s.q[:], big = 0, rounded(np.full(1, 1e18), dtype)[0]
+        s.q[..., 0] = sign * big
+        for (n, c), t in zip(s.reqs, s.table):
+            s.host[0][:, paged.slots(t, 16, 0, n + c)] = 0
+            s.host[0][:, paged.slots(t, 16, 0, n + c), 0] = big
+        s.upload()
+        s.check(s.attention(), equal=True)  # (the mean of the values)
+
+
+NONFINITE = [("bf16", 128), ("bf16", 64), ("bf16", 32), ("fp32", 64)]
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dtype,d", NONFINITE)
+def test_values_that_are_not_finite(native, eng, dtype, d, bad):
+    """They reach the rows that see their key, and no others, whichever key it is."""
+    for reqs, key in (([(1, 100)], 100), ([(9, 50)], 54), ([(150, 60)], 60 + 33), ([(150, 0)], 149), ([(40, 300)], 310)):
+        s = Case(native, eng, 9, dtype, 4, 2, d, 16, reqs)
+        n, c = reqs[0]
+        at = paged.slots(s.table[0], 16, key, 1)[0]
+        s.host[1, 1, at, 3] = bad
+        s.upload()
+        out = s.attention().float().cpu().numpy()[:s.rows, :s.H].reshape(n, 4, d)
+        sees = np.arange(n) + c >= key
+        hit = np.zeros((n, 4), bool)
+        hit[sees, 2:] = True
+        assert (~np.isfinite(out[..., 3]) == hit).all()
+        assert np.isfinite(out[~hit]).all()
+        s.host[1, 1, at, 3] = 0
+        ref, lim = s.limits()
+        assert (np.abs(out - ref) <= lim)[~hit].all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype,d", NONFINITE)
+def test_keys_that_are_not_finite(native, eng, dtype, d, bad):
+    for reqs, key in (([(1, 100)], 37), ([(9, 50)], 54), ([(150, 60)], 60 + 33), ([(150, 0)], 149)):
+        s = Case(native, eng, 10, dtype, 4, 2, d, 16, reqs)
+        n, c = reqs[0]
+        s.host[0, 0, paged.slots(s.table[0], 16, key, 1)[0], 5] = bad
+        s.q[..., 5] = np.abs(s.q[..., 5]) + 1  # (a score of +inf, whose softmax is NaN, not one of -inf)
+        s.upload()
+        out = s.attention().float().cpu().numpy()[:s.rows, :s.H].reshape(n, 4, d)
+        hit = np.zeros((n, 4), bool)
+        hit[np.arange(n) + c >= key, :2] = True
+        assert np.isnan(out[hit]).all() and np.isfinite(out[~hit]).all()
+
+
+@pytest.mark.parametrize("dtype,d", NONFINITE)
+def test_keys_that_hide_themselves(native, eng, dtype, d):
+    """Scores of -inf take their key out; a row of nothing else has no softmax."""
+    for reqs in ([(1, 100)], [(9, 50)], [(150, 60)]):
+        s = Case(native, eng, 11, dtype, 2, 1, d, 16, reqs)
+        n, c = reqs[0]
+        s.q[..., 0] = 1.0
+        at = paged.slots(s.table[0], 16, 0, n + c)
+        hidden = np.arange(n + c) % 3 != 1
+        s.host[0][:, at[hidden], 0] = -np.inf
+        s.upload()
+        s.check(s.attention())
+        s.host[0][:, at, 0] = -np.inf
+        s.upload()
+        assert torch.isnan(s.attention()[:s.rows, :s.H]).all()
+
+
+def test_empty_batches(native, eng):
+    s = Case(native, eng, 12, "bf16", 4, 2, 64, 16, [(0, 5), (0, 0)])
+    out = s.attention()
+    assert (out == 768).all()
+    s = append_case(native, eng, 12, "bf16", 4, 2, 64, 16, [(0, 5), (0, 0)], 64, False)
+    do_append(s)
+    assert (s.q_out == 512).all() and torch.isnan(s.layer).all()
+
+
+def test_shared_pages(native, eng):
+    """Requests with a common beginning read its pages together; the second writes into pages of its own."""
+    table = [[4, 1, 0], [4, 1, 5], [4, 1, 3]]
+    s = Case(native, eng, 13, "bf16", 8, 2, 128, 32, [(1, 70), (5, 64), (1, 90)], table=table, n_pages=7)
+    s.check(s.attention())
+    for at, ok in ((70, True), (69, True), (68, False), (64, False), (63, True)):  # beside rows 64 .. 68 of one page
+        a = append_case(native, eng, 13, "bf16", 8, 2, 128, 32, [(1, at), (5, 64)], 128, False)
+        a.table = np.array([[4, 1, 0], [4, 1, 0]], np.int32)
+        a.plan = eng.paged_plan(1, 8, 2, 128, 32, a.n_pages, a.n, a.c, a.table)
+        a.dplan = torch.from_numpy(a.plan).cuda()
+        if ok:
+            do_append(a)
+            continue
+        with pytest.raises(native.OrcaError) as e:
+            do_append(a)
+        assert e.value.code == native.ERR_INVALID
+    # the same request's two rows in one slot, by a page that its table names twice
+    b = native.Engine.paged_plan(eng, 1, 8, 2, 128, 16, 4, [32], [0], np.array([[1, 1]], np.int32))
+    x = torch.zeros(32 * 12 * 128, dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros(2 * 2 * 64 * 128, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(native.OrcaError):
+        eng.op_paged_append(x.data_ptr(), y.data_ptr(), b, torch.from_numpy(b).cuda().data_ptr())
+
+
+def test_refusals(native, eng):
+    s = append_case(native, eng, 14, "bf16", 4, 2, 64, 16, [(2, 20)], 64, False)
+    ok = dict(qkv=s.dqkv.data_ptr(), layer=s.layer.data_ptr(), plan=s.plan, dev_plan=s.dplan.data_ptr(),
+              q_out=s.q_out.data_ptr(), rope=s.drope.data_ptr(), rope_len=len(s.rope), rot_dim=64, neighbours=False)
+    eng.op_paged_append(**ok)
+    for bad in (dict(qkv=0), dict(qkv=ok["qkv"] + 2), dict(layer=0), dict(layer=ok["layer"] + 8), dict(dev_plan=0),
+                dict(dev_plan=ok["dev_plan"] + 4), dict(q_out=ok["q_out"] + 8), dict(rope=0), dict(rope=ok["rope"] + 4),
+                dict(rope_len=21), dict(rot_dim=66), dict(rot_dim=3), dict(rot_dim=-2), dict(neighbours=2),
+                dict(ld_qkv=504), dict(ld_qkv=516), dict(ld_q=248), dict(ld_q=260), dict(ld_qkv=2 ** 31),
+                dict(q_out=ok["qkv"]), dict(q_out=ok["qkv"] + 16), dict(q_out=ok["layer"] + 1024),
+                dict(qkv=ok["layer"] + 1024), dict(plan=np.zeros(64, np.int32) + s.plan[1])):
+        with pytest.raises(native.OrcaError) as e:
+            eng.op_paged_append(**{**ok, **bad})
+        assert e.value.code == native.ERR_INVALID, bad
+    out = torch.zeros((2, 256), dtype=torch.bfloat16, device="cuda")
+    ok = dict(q=s.q_out.data_ptr(), layer=s.layer.data_ptr(), plan=s.plan, dev_plan=s.dplan.data_ptr(),
+              workspace=s.work.data_ptr(), out=out.data_ptr())
+    eng.op_paged_attention(**ok)
+    for bad in (dict(q=0), dict(q=ok["q"] + 2), dict(layer=0), dict(layer=ok["layer"] + 8), dict(dev_plan=0),
+                dict(dev_plan=ok["dev_plan"] + 4), dict(workspace=ok["workspace"] + 8), dict(out=0),
+                dict(out=ok["out"] + 8), dict(ld_q=248), dict(ld_q=260), dict(ld_out=248), dict(ld_out=260),
+                dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(out=ok["q"]),
+                dict(out=ok["layer"]), dict(plan=np.zeros(64, np.int32) + s.plan[1])):
+        with pytest.raises(native.OrcaError) as e:
+            eng.op_paged_attention(**{**ok, **bad})
+        assert e.value.code == native.ERR_INVALID, bad
+    s = Case(native, eng, 14, "bf16", 4, 1, 128, 16, [(1, 30000)])
+    if eng.paged_workspace_bytes(s.plan):  # split keys: a workspace is needed
+        with pytest.raises(native.OrcaError):
+            eng.op_paged_attention(s.dq.data_ptr(), s.layer.data_ptr(), s.plan, s.dplan.data_ptr(), 0, s.dq.data_ptr())
+
+
+MIX = [(1, 700), (1, 20000), (6, 300), (150, 200), (40, 3000), (1, 0)]
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 64)])
+def test_calls_repeat_bit_for_bit(native, eng, dtype, d):
+    """Twice in a row, captured and replayed, on a stream of another engine, with work of another call in the
+    workspace: the same bits."""
+    s = Case(native, eng, 15, dtype, 8, 2, d, 64, MIX)
+    first = s.attention()
+    s.check(first)
+    assert torch.equal(first, s.attention())
+    s.work.fill_(0x7F)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        e2 = native.Engine(1, 64, 1, 64, 64, 64, native.DTYPE_BF16, 64, 64, 64, None, side.cuda_stream)
+    side.wait_stream(torch.cuda.current_stream())
+    s.eng = e2
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = s.attention(sync=False)
+        for _ in range(3):
+            out.zero_()
+            graph.replay()
+            side.synchronize()
+            assert torch.equal(first[:s.rows, :s.H], out[:s.rows, :s.H])
+    s.eng = eng
+    del graph
+    e2.close()
+
+
+def test_two_streams_share_a_plan(native, eng):
+    s = Case(native, eng, 16, "bf16", 8, 2, 128, 64, MIX)
+    first = s.attention()
+    side = torch.cuda.Stream()
+    e2 = native.Engine(1, 64, 1, 64, 64, 64, native.DTYPE_BF16, 64, 64, 64, None, side.cuda_stream)
+    work2, outs = torch.empty_like(s.work), []
+    torch.cuda.synchronize()
+    for i in range(6):
+        s.eng = e2 if i % 2 else eng
+        with torch.cuda.stream(side if i % 2 else torch.cuda.current_stream()):
+            outs.append(s.attention(work=work2 if i % 2 else None, sync=False))
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, o) for o in outs)
+    s.eng = eng
+    e2.close()
+
+
+def test_a_prompt_and_its_tokens(native, eng):
+    """As a serving program uses them: a prompt in two chunks, then tokens one by one, against one prompt in 64 bits."""
+    heads, kv, d, page, N = 8, 2, 64, 16, 90
+    g = np.random.default_rng(17)
+    rope = paged.rope_table(N, d)
+    drope = torch.from_numpy(rope).cuda()
+    for dtype in ("bf16", "fp32"):
+        qkv = rounded(g.standard_normal((N, heads + 2 * kv, d)), dtype)
+        dqkv = torch.from_numpy(qkv.reshape(N, -1)).cuda().to(TD[dtype])
+        layer = torch.full((2, kv, 10 * page, d), float("nan"), dtype=TD[dtype], device="cuda")
+        table = g.permutation(10)[None, :6].astype(np.int32)
+        out = torch.empty((N, heads * d), dtype=TD[dtype], device="cuda")
+        q = torch.empty_like(out)
+        for at, n in [(0, 40), (40, 37)] + [(t, 1) for t in range(77, N)]:
+            plan = eng.paged_plan(1 if dtype == "bf16" else 0, heads, kv, d, page, 10, [n], [at], table)
+            dev = torch.from_numpy(plan).cuda()
+            work = torch.empty(max(16, eng.paged_workspace_bytes(plan)), dtype=torch.uint8, device="cuda")
+            eng.op_paged_append(dqkv[at:].data_ptr(), layer.data_ptr(), plan, dev.data_ptr(), q_out=q[at:].data_ptr(),
+                                rope=drope.data_ptr(), rope_len=N, rot_dim=d, sync=False)
+            eng.op_paged_attention(q[at:].data_ptr(), layer.data_ptr(), plan, dev.data_ptr(), work.data_ptr(),
+                                   out[at:].data_ptr())
+        # rotated rows against the oracle's, then attention over the very rows that were written
+        at = paged.slots(table[0], page, 0, N)
+        rot = torch.cat([q.view(N, heads, d), layer[0][:, at].transpose(0, 1)], 1).float().cpu().numpy()
+        want = paged.rotate(qkv[:, :heads + kv], rope, d, False)
+        big = 2 * np.abs(qkv[:, :heads + kv]).max(-1, keepdims=True)
+        assert (np.abs(rot - want) <= U[dtype] * np.abs(want) + 2.0 ** -22 * big).all()
+        assert torch.equal(layer[1][:, at], dqkv.view(N, -1, d)[:, heads + kv:].transpose(0, 1))
+        ref, lim = limits(dtype, rot[:, :heads], rot[:, heads:].transpose(1, 0, 2),
+                          qkv[:, heads + kv:].transpose(1, 0, 2), 0)
+        got = out.float().cpu().numpy().reshape(N, heads, d)
+        assert (np.abs(got - ref) <= lim).all()

@@ -1,0 +1,105 @@
+"""Host side of the paged K/V cache: plans, sizes and refusals.  No GPU."""
+
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from iteration_level_scheduling_gb300 import build
+from oracle import paged
+
+
+@pytest.fixture(scope="module")
+def native():
+    build.build()
+    from iteration_level_scheduling_gb300 import native as n
+    return n
+
+
+def batch(native, dtype=1, heads=8, kv_heads=2, d=64, page=16, n_pages=10, n=(3,), c=(40,), table=((7, 2, 5),), **over):
+    n, c, t = np.array(n, np.int32), np.array(c, np.int32), np.array(table, np.int32)
+    b = native.PagedBatch(dtype, heads, kv_heads, d, page, len(n), n_pages, t.shape[1], n.ctypes.data, c.ctypes.data,
+                          t.ctypes.data)
+    b._keep = (n, c, t)
+    for k, v in over.items():
+        setattr(b, k, v)
+    return b
+
+
+def words(native, **kw):
+    return native.lib.orca_paged_plan_words(None, C.byref(batch(native, **kw)))
+
+
+def plan(native, **kw):
+    b = batch(native, **kw)
+    w = native.lib.orca_paged_plan_words(None, C.byref(b))
+    assert w > 0
+    buf = np.zeros(w, np.int32)
+    assert native.lib.orca_paged_plan_build(None, C.byref(b), buf.ctypes.data, w) == 0
+    return buf
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dtype=2), dict(dtype=-1), dict(heads=0), dict(heads=7), dict(heads=1026), dict(kv_heads=0), dict(kv_heads=16),
+    dict(kv_heads=3), dict(d=48), dict(d=256), dict(page=0), dict(page=8), dict(page=24), dict(page=-16),
+    dict(n_pages=0), dict(n_pages=2 ** 27), dict(n_pages=2 ** 40), dict(n=(-1,)), dict(c=(-1,)),
+    dict(n=(9,)), dict(c=(46,)),                # a fourth page is needed, the table has three
+    dict(table=((7, 2, 10),)), dict(table=((7, -1, 5),)),
+    dict(n=(2 ** 31 - 1,), c=(2 ** 31 - 1,)), dict(n_req=0), dict(n_req=-1), dict(table_ld=0), dict(table_ld=2),
+    dict(n_input=None), dict(ctx_len=None), dict(page_table=None),
+    dict(n=(150,), c=(20,), table=(tuple(range(10)) + (0,),)),  # more positions than the layer has slots
+])
+def test_plan_refusals(native, kw):
+    assert words(native, **kw) == native.ERR_INVALID
+    buf = np.zeros(4096, np.int32)
+    assert native.lib.orca_paged_plan_build(None, C.byref(batch(native, **kw)), buf.ctypes.data, 4096) == \
+        native.ERR_INVALID
+    assert not buf.any()
+
+
+def test_plan_accepts_what_is_not_used(native):
+    """Pages behind the last position and all of a request without rows are not looked at."""
+    assert words(native, table=((7, 2, 5, -9),)) > 0
+    assert words(native, n=(3, 0), c=(40, -5), table=((7, 2, 5), (-1, -1, -1))) > 0
+    assert words(native, n=(0,), c=(0,), table=((-1,),)) > 0
+    assert words(native, page=1 << 20, n_pages=2000) > 0
+    assert words(native, n=(1, 1), c=(40, 40), table=((7, 2, 5), (7, 2, 6))) > 0  # shared pages
+
+
+def test_null_and_short_buffers(native):
+    b = batch(native)
+    w = native.lib.orca_paged_plan_words(None, C.byref(b))
+    buf = np.zeros(w, np.int32)
+    assert native.lib.orca_paged_plan_words(None, None) == native.ERR_INVALID
+    assert native.lib.orca_paged_plan_build(None, C.byref(b), None, w) == native.ERR_INVALID
+    assert native.lib.orca_paged_plan_build(None, C.byref(b), buf.ctypes.data, w - 1) == native.ERR_INVALID
+    assert not buf.any()
+    assert native.lib.orca_paged_workspace_bytes(None) == native.ERR_INVALID
+    assert native.lib.orca_paged_workspace_bytes(np.zeros(64, np.int32).ctypes.data) == native.ERR_INVALID
+
+
+def test_operators_need_an_engine(native):
+    p = plan(native)
+    assert native.lib.orca_op_paged_append(None, 16, 768, 16, p.ctypes.data, 16, None, 0, 0, 0, 16, 512) == \
+        native.ERR_INVALID
+    assert native.lib.orca_op_paged_attention(None, 16, 512, 16, p.ctypes.data, 16, 0.0, 16, 16, 512) == \
+        native.ERR_INVALID
+
+
+def test_oracle_by_hand():
+    x = np.arange(8, dtype=np.float64).reshape(1, 1, 8)
+    turn = np.array([[0.0, 1.0, 1.0, 0.0]])  # pair 0 by a quarter, pair 1 not at all
+    assert paged.rotate(x, turn, 4, False)[0, 0].tolist() == [-2, 1, 0, 3, 4, 5, 6, 7]
+    assert paged.rotate(x, turn, 4, True)[0, 0].tolist() == [-1, 0, 2, 3, 4, 5, 6, 7]
+    assert paged.slots([7, 2], 16, 14, 4).tolist() == [126, 127, 32, 33]
+    # two keys of equal score, the second row alone sees both
+    q, k = np.ones((2, 2, 1)), np.ones((1, 2, 1))
+    out, spread = paged.attention(q, k, np.array([[[1.0], [3.0]]]), 0, 1.0)
+    assert out[:, :, 0].tolist() == [[1, 1], [2, 2]] and spread[1, 0, 0] == pytest.approx(np.sqrt(0.5))
+    # a rotation keeps products of rows at equal distance
+    g = np.random.default_rng(0)
+    a, b = g.standard_normal((1, 1, 32)), g.standard_normal((1, 1, 32))
+    t = paged.rope_table(50, 24)
+    for nb in (False, True):
+        p = [(paged.rotate(a, t[i:i + 1], 24, nb) * paged.rotate(b, t[i + 7:i + 8], 24, nb)).sum() for i in (0, 13, 40)]
+        assert np.ptp(p) < 1e-5
