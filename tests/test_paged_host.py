@@ -103,3 +103,71 @@ def test_oracle_by_hand():
     for nb in (False, True):
         p = [(paged.rotate(a, t[i:i + 1], 24, nb) * paged.rotate(b, t[i + 7:i + 8], 24, nb)).sum() for i in (0, 13, 40)]
         assert np.ptp(p) < 1e-5
+
+
+# words of a plan's header (k_paged.cu)
+O_ROWS, O_REQS, O_TILES, ITEMS, PARTS, JOINS, O_ITEMS, O_JOINS = 10, 11, 12, 14, 17, 18, 19, 20
+
+
+def cover(native, p, n, c, table, page, group, kv_heads):
+    """What a plan's items read and write: every row's column sees its keys once, and nothing leaves its buffer."""
+    keys_of = {}
+    words, rows = len(p), sum(n)
+    first = np.concatenate([[0], np.cumsum(n)])
+    req_of = np.repeat(np.arange(len(n)), n)
+    at = p[O_ITEMS]
+    part_end = int(p[PARTS])
+    written = {}
+    for cl in range(3):
+        for r in p[at:at + 8 * p[ITEMS + cl]].reshape(-1, 8):
+            tile, keys, row0, col0, cols, last0, part = (int(x) for x in r[:7])
+            i = int(req_of[row0]) if n[req_of[row0]] else -1
+            assert row0 == first[i] and 1 <= cols <= 8 << cl and keys >= 1 and col0 + cols <= n[i] * group
+            k0 = 16 * (tile - int(p[p[O_REQS] + i]))
+            assert k0 % 16 == 0 and 0 <= k0 and k0 + keys <= c[i] + n[i] and last0 == c[i] - k0
+            slots = p[tile:tile + (keys + 15) // 16]
+            assert tile + len(slots) <= words
+            assert (slots == paged.slots(table[i], page, k0, keys)[::16] // 16).all()
+            if part >= 0:
+                assert part + (8 << cl) <= part_end
+            for x in range(cols):
+                j = (col0 + x) // group
+                seen = max(0, min(keys, last0 + j + 1))
+                keys_of.setdefault((row0 + j, (col0 + x) % group), []).append((k0, k0 + seen))
+                written.setdefault((i, col0 + x), []).append((part + x) if part >= 0 else None)
+        at += 8 * p[ITEMS + cl]
+    for r in range(rows):
+        for g in range(group):
+            spans = sorted(s for s in keys_of[(r, g)] if s[0] < s[1])
+            assert spans[0][0] == 0 and spans[-1][1] == c[req_of[r]] + r - first[req_of[r]] + 1
+            assert all(a[1] == b[0] for a, b in zip(spans, spans[1:]))
+    assert len(keys_of) == rows * group
+    joined = set()
+    for r in p[p[O_JOINS]:p[O_JOINS] + 8 * p[JOINS]].reshape(-1, 8):
+        row0, col, parts, part, step, x = (int(v) for v in r[:6])
+        i = int(req_of[row0])
+        assert sorted(written[(i, col)]) == [part + y * step + x for y in range(parts)]
+        joined.add((i, col))
+    for key, w in written.items():
+        assert (key in joined) == (w[0] is not None) and (w[0] is not None or len(w) == 1)
+    flat = [w for ws in written.values() for w in ws if w is not None]
+    assert len(flat) == len(set(flat))
+    assert native.lib.orca_paged_workspace_bytes(p.ctypes.data) == part_end * kv_heads * (int(p[4]) + 2) * 4
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_plans_cover_every_key_once(native, seed):
+    g = np.random.default_rng(seed)
+    reqs = int(g.integers(1, 12))
+    n = [int(g.choice([0, 1, 1, 1, 2, 7, 33, 200])) for _ in range(reqs)]
+    c = [int(g.choice([0, 1, 15, 16, 300, 700, 5000])) for _ in range(reqs)]
+    n[0] = max(1, n[0])
+    page, group, kv = int(g.choice([16, 48, 128])), int(g.choice([1, 3, 8, 17, 40])), int(g.choice([1, 4]))
+    need = [-(-(a + b) // page) for a, b in zip(n, c)]
+    order, table, at = g.permutation(sum(need)), np.zeros((reqs, max(need)), np.int32), 0
+    for i, m in enumerate(need):
+        table[i, :m] = order[at:at + m]
+        at += m
+    p = plan(native, dtype=1, heads=group * kv, kv_heads=kv, d=int(g.choice([16, 64, 128])), page=page,
+             n_pages=sum(need), n=n, c=c, table=table)
+    cover(native, p, n, c, table, page, group, kv)
