@@ -52,14 +52,14 @@ struct PagedSizes {
     int64_t off_rows, off_reqs, off_tiles, off_items, off_joins, total;
 };
 
-// Columns of a request: the smallest class that holds them all, else tiles of the widest.
-int class_of(int64_t cols) { return cols <= 8 ? 0 : cols <= 16 ? 1 : 2; }
+// Columns of a request: the smallest class that holds them all, else tiles of the widest (fp32: 16, by registers).
+int class_of(int64_t cols, int dtype) { return cols <= 8 ? 0 : cols <= 16 || !dtype ? 1 : 2; }
 
 // The column tiles of request i: fn(class, first column, columns, keys that the last of them sees).
 template <typename F>
 void column_tiles(const PagedBatch &b, int i, F fn) {
     const int64_t group = b.n_heads / b.n_kv_heads, cols = b.n_input[i] * group;
-    const int cl = class_of(cols);
+    const int cl = class_of(cols, b.dtype);
     for (int64_t c = 0; c < cols; c += 8 << cl) {
         const int64_t n = std::min<int64_t>(8 << cl, cols - c);
         fn(cl, c, n, b.ctx_len[i] + (c + n - 1) / group + 1);
@@ -471,6 +471,22 @@ __device__ __forceinline__ uint32_t cw_pack(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
+// fp32 operands as two tf32 parts of 11 bits each, x = hi + lo up to 2^-22 |x|:
+// products hi hi + hi lo + lo hi.  An infinity has no lower part and takes no part
+// in the mixed products (0 * inf, inf - inf): they use `fin`.
+__device__ __forceinline__ void cw_split(uint32_t x, uint32_t &hi, uint32_t &lo, uint32_t &fin) {
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "r"(x));
+    const float rest = hi == x ? 0.f : __uint_as_float(x) - __uint_as_float(hi);
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
+    fin = (hi & 0x7fffffffu) == 0x7f800000u ? 0u : hi;
+}
+__device__ __forceinline__ void cw_mma_tf32(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t cw_lds(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -483,8 +499,9 @@ template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kCwThreads, 2)
     paged_cols_kernel(const __grid_constant__ CUtensorMap tm, const PagedArgs a) {
     using S = CwShape<T, D, NT>;
-    constexpr int KS = D / 16, MT = D / 16;
-    constexpr bool kKeepQ = NT <= 2;  // the queries' fragments stay in registers (else they come from L1 every tile)
+    constexpr bool F32 = sizeof(T) == 4;
+    constexpr int KS = D / (F32 ? 8 : 16), MT = D / 16;
+    constexpr bool kKeepQ = NT <= 2 && !F32;  // the queries' fragments stay in registers (else they come from L1 every tile)
     constexpr unsigned kFull = 0xffffffffu;
     extern __shared__ __align__(1024) uint8_t cw_smem[];
     pdl_trigger();
@@ -591,16 +608,45 @@ __global__ void __launch_bounds__(kCwThreads, 2)
             float c[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+            if constexpr (F32) {
+                // chains of at most four products, added up in fp32: the tensor core cuts its sums off
+                constexpr int NC = KS < 4 ? KS : 4;
+                float hh[NC][NT][4];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                uint32_t f[4];
-                cw_ldsm(at(kb, lane & 15, 2 * ks + (lane >> 4)), f);
+                for (int x = 0; x < NC * NT * 4; ++x) (&hh[0][0][0])[x] = 0.f;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if constexpr (kKeepQ)
-                        cw_mma_bf16(c[nt], f, qb[nt][ks][0], qb[nt][ks][1]);
-                    else
-                        cw_mma_bf16(c[nt], f, qp[nt][8 * ks], qp[nt][8 * ks + 4]);
+                for (int ks = 0; ks < KS; ++ks) {
+                    uint32_t f[4], fh[4], fl[4], ff[4], qh[2], ql[2], qf[2];
+                    cw_ldsm(at(kb, lane & 15, 2 * ks + (lane >> 4)), f);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) cw_split(f[x], fh[x], fl[x], ff[x]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        cw_split(qp[nt][8 * ks], qh[0], ql[0], qf[0]);
+                        cw_split(qp[nt][8 * ks + 4], qh[1], ql[1], qf[1]);
+                        cw_mma_tf32(hh[ks % NC][nt], fh, qh[0], qh[1]);
+                        cw_mma_tf32(c[nt], ff, ql[0], ql[1]);
+                        cw_mma_tf32(c[nt], fl, qf[0], qf[1]);
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int n = 0; n < NC; ++n) c[nt][x] += hh[n][nt][x];
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    uint32_t f[4];
+                    cw_ldsm(at(kb, lane & 15, 2 * ks + (lane >> 4)), f);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if constexpr (kKeepQ)
+                            cw_mma_bf16(c[nt], f, qb[nt][ks][0], qb[nt][ks][1]);
+                        else
+                            cw_mma_bf16(c[nt], f, qp[nt][8 * ks], qp[nt][8 * ks + 4]);
+                    }
                 }
             }
             // scores of keys 16 t + g8 and + 8, columns 2 t4 and + 1 of every 8; those not seen are -inf
@@ -637,16 +683,20 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                         for (int mt = 0; mt < MT; ++mt) o[nt][mt][i] *= corr, o[nt][mt][2 + i] *= corr;
                     }
             }
-            // weights, rounded to bf16 for the second product; l sums what is used
+            // weights; bf16: rounded for the second product, and l sums what is used
             uint32_t pw[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float b0 = cw_base(m[nt][0]), b1 = cw_base(m[nt][1]);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    pw[nt][x] = cw_pack(cw_exp2(c[nt][2 * x] - b0), cw_exp2(c[nt][2 * x + 1] - b1));
-                    l[nt][0] += __uint_as_float(pw[nt][x] << 16);
-                    l[nt][1] += __uint_as_float(pw[nt][x] & 0xffff0000u);
+                    c[nt][2 * x] = cw_exp2(c[nt][2 * x] - b0), c[nt][2 * x + 1] = cw_exp2(c[nt][2 * x + 1] - b1);
+                    if constexpr (!F32) {
+                        pw[nt][x] = cw_pack(c[nt][2 * x], c[nt][2 * x + 1]);
+                        c[nt][2 * x] = __uint_as_float(pw[nt][x] << 16);
+                        c[nt][2 * x + 1] = __uint_as_float(pw[nt][x] & 0xffff0000u);
+                    }
+                    l[nt][0] += c[nt][2 * x], l[nt][1] += c[nt][2 * x + 1];
                 }
             }
             bool by_key = false;  // a value that is not finite behind a key that some column does not see
@@ -664,12 +714,71 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                     for (int x = lane; x < 16 * (D * S::kEs / 4); x += 32) {
                         const int r = x / (D * S::kEs / 4), w = x % (D * S::kEs / 4);
                         const uint32_t v = cw_lds(at(vb, r, w / 4) + 4 * (w % 4));
-                        by_key |= (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
+                        by_key |= (!F32 && (v & 0x7f80u) == 0x7f80u) || (v & 0x7f800000u) == 0x7f800000u;
                     }
                     by_key = __any_sync(kFull, by_key);
                 }
             }
-            if (!by_key) {
+            if (by_key) {  // key by key, so that 0 * inf reaches no column that does not see it
+                for (int r = 0; r < 16; ++r)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int src = (r & 7) * 4 + t4;
+                        const float p[2] = {__shfl_sync(kFull, r < 8 ? c[nt][0] : c[nt][2], src),
+                                            __shfl_sync(kFull, r < 8 ? c[nt][1] : c[nt][3], src)};
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const int d = (16 * mt + g8 + 8 * x) * S::kEs;  // (byte)
+                                const uint32_t v = cw_lds(at(vb, r, d / 16) + d % 16 / 4 * 4);
+                                const float vf = __uint_as_float(F32 ? v : d % 4 ? v & 0xffff0000u : v << 16);
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    if (16 * t + r < sees[nt][i]) o[nt][mt][2 * x + i] = fmaf(p[i], vf, o[nt][mt][2 * x + i]);
+                            }
+                    }
+            } else if constexpr (F32) {
+                // the keys of a product in the order 0 2 4 6 1 3 5 7, which spreads V's rows over the banks
+                uint32_t ph[NT][2][2], pl[NT][2][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int src = (2 * t4 + i) * 4 + (g8 >> 1);
+                            const float p0 = __shfl_sync(kFull, c[nt][2 * x], src);
+                            const float p1 = __shfl_sync(kFull, c[nt][2 * x + 1], src);
+                            uint32_t unused;  // (weights are finite, or their column is NaN)
+                            cw_split(__float_as_uint(g8 & 1 ? p1 : p0), ph[nt][x][i], pl[nt][x][i], unused);
+                        }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    float y[NT][4];  // this tile's sum on its own: o is added to in fp32
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) y[nt][0] = y[nt][1] = y[nt][2] = y[nt][3] = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t fh[4], fl[4], ff[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const int d = 16 * mt + g8 + 8 * (z & 1);
+                            cw_split(cw_lds(at(vb, 8 * x + 2 * t4 + (z >> 1), d / 4) + d % 4 * 4), fh[z], fl[z], ff[z]);
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            cw_mma_tf32(y[nt], fl, ph[nt][x][0], ph[nt][x][1]);
+                            cw_mma_tf32(y[nt], ff, pl[nt][x][0], pl[nt][x][1]);
+                            cw_mma_tf32(y[nt], fh, ph[nt][x][0], ph[nt][x][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[nt][mt][x] += y[nt][x];
+                }
+            } else {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) pw[nt][0] = cw_transpose(pw[nt][0]), pw[nt][1] = cw_transpose(pw[nt][1]);
 #pragma unroll
@@ -679,24 +788,6 @@ __global__ void __launch_bounds__(kCwThreads, 2)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) cw_mma_bf16(o[nt][mt], f, pw[nt][0], pw[nt][1]);
                 }
-            } else {  // key by key, so that 0 * inf reaches no column that does not see it
-                for (int r = 0; r < 16; ++r)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t w = __shfl_sync(kFull, r < 8 ? pw[nt][0] : pw[nt][1], (r & 7) * 4 + t4);
-                        const float p[2] = {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)};
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const int d = 16 * mt + g8 + 8 * x;
-                                const uint32_t v = cw_lds(at(vb, r, d / 8) + 4 * (d % 8 / 2));
-                                const float vf = __uint_as_float(d & 1 ? v & 0xffff0000u : v << 16);
-#pragma unroll
-                                for (int i = 0; i < 2; ++i)
-                                    if (16 * t + r < sees[nt][i]) o[nt][mt][2 * x + i] = fmaf(p[i], vf, o[nt][mt][2 * x + i]);
-                            }
-                    }
             }
             __syncwarp();  // every lane has read the stage
             ++used;
@@ -805,82 +896,6 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
     store4(dst, o.x * f, o.y * f, o.z * f, o.w * f);
 }
 
-struct RowArgs {
-    const void *q, *layer;
-    void *out;
-    int64_t ld_q, ld_out, slots;
-    const int32_t *plan;
-    const int4 *rows;
-    const int32_t *reqs;
-    int n_rows, heads, kv_heads;
-    float scale_log2;
-};
-
-// One warp per row and head: LPT lanes hold a key's components, 32 / LPT keys at
-// a time, the running maximum m and sum l of the softmax in each lane group.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) paged_attn_kernel(const RowArgs a) {
-    constexpr int VEC = Elem<T>::kPer16;
-    constexpr int LPT = D / VEC, TPW = 32 / LPT;
-    pdl_trigger();
-    pdl_wait();
-    const int at = blockIdx.x * 4 + threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int row = at / a.heads, h = at % a.heads;
-    if (row >= a.n_rows) return;
-    const int4 rec = a.rows[row];
-    const int32_t *tiles = a.plan + a.reqs[rec.z];
-    const int keys = rec.y + 1, g = lane / LPT, sub = lane % LPT;
-    const int64_t kvh = h / (a.heads / a.kv_heads);
-    const T *kb = reinterpret_cast<const T *>(a.layer) + kvh * a.slots * D + sub * VEC;
-    const T *vb = kb + a.kv_heads * a.slots * D;
-    float q[VEC], o[VEC], m = -INFINITY, l = 0.f;
-    load16(reinterpret_cast<const T *>(a.q) + row * a.ld_q + h * D + sub * VEC, q);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) o[e] = 0.f;
-    for (int t0 = 0; t0 < keys; t0 += TPW) {  // (uniform across the warp)
-        const int t = t0 + g;
-        const bool valid = t < keys;
-        float k[VEC], v[VEC], s = 0.f;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) k[e] = v[e] = 0.f;
-        if (valid) {
-            const int64_t slot = (int64_t)tiles[t / 16] * 16 + t % 16;
-            load16(kb + slot * D, k);
-            load16(vb + slot * D, v);
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s = fmaf(q[e], k[e], s);
-#pragma unroll
-        for (int x = LPT / 2; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s = valid ? s * a.scale_log2 : -INFINITY;
-        const float mx = fmaxf(m, s), base = mx == -INFINITY ? 0.f : mx;
-        const float corr = exp2f(m - base), p = exp2f(s - base);
-        l = l * corr + p;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] = fmaf(p, v[e], o[e] * corr);
-        m = mx;
-    }
-#pragma unroll
-    for (int x = LPT; x < 32; x <<= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, x), l2 = __shfl_xor_sync(0xffffffffu, l, x);
-        const float mx = fmaxf(m, m2), base = mx == -INFINITY ? 0.f : mx;
-        const float c1 = exp2f(m - base), c2 = exp2f(m2 - base);
-        l = l * c1 + l2 * c2;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] = o[e] * c1 + __shfl_xor_sync(0xffffffffu, o[e], x) * c2;
-        m = mx;
-    }
-    if (g == 0) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] /= l;
-        store16(reinterpret_cast<T *>(a.out) + row * a.ld_out + h * D + sub * VEC, o);
-    }
-}
-
-}  // namespace
-
-namespace {
-
 template <typename T, int D, int NT>
 cudaError_t launch_cols(const PagedArgs &a, const void *layer, int64_t slots, int sms, cudaStream_t st) {
     using S = CwShape<T, D, NT>;
@@ -906,39 +921,31 @@ template <typename T, int D>
 cudaError_t launch_attention(const PagedAttn &p, const int32_t *hp, const int32_t *dp, unsigned *err, int *launches,
                              cudaStream_t st) {
     const float scale_log2 = p.scale * 1.4426950408889634f;
-    if constexpr (sizeof(T) == 4) {
-        RowArgs a;
-        a.q = p.q, a.layer = p.layer, a.out = p.out, a.ld_q = p.ld_q, a.ld_out = p.ld_out;
-        a.plan = dp, a.rows = reinterpret_cast<const int4 *>(dp + hp[G_O_ROWS]), a.reqs = dp + hp[G_O_REQS];
-        a.slots = hp[G_SLOTS], a.n_rows = hp[G_ROWS], a.heads = hp[G_HEADS], a.kv_heads = hp[G_KV_HEADS];
-        a.scale_log2 = scale_log2;
-        *launches = 1;
-        return launch_pdl(paged_attn_kernel<T, D>, dim3((unsigned)(((int64_t)a.n_rows * a.heads + 3) / 4)), dim3(128), 0,
-                          st, a);
-    } else {
-        PagedArgs a;
-        a.q = p.q, a.out = p.out, a.ld_q = p.ld_q, a.ld_out = p.ld_out, a.plan = dp, a.err = err;
-        a.kv_heads = hp[G_KV_HEADS], a.group = hp[G_HEADS] / hp[G_KV_HEADS], a.scale_log2 = scale_log2;
-        a.part = reinterpret_cast<float *>(p.workspace);
-        a.part_ml = a.part + (int64_t)hp[G_PARTS] * a.kv_heads * D;
-        *launches = 0;
-        cudaError_t e = cudaSuccess;
-        const int32_t *at = dp + hp[G_O_ITEMS];
-        for (int c = 0; c < kClasses && e == cudaSuccess; ++c) {
-            a.items = reinterpret_cast<const int4 *>(at), a.n_items = hp[G_ITEMS + c];
-            at += 8 * a.n_items;
-            if (!a.n_items) continue;
-            ++*launches;
-            e = c == 0   ? launch_cols<T, D, 1>(a, p.layer, hp[G_SLOTS], hp[G_SMS], st)
-                : c == 1 ? launch_cols<T, D, 2>(a, p.layer, hp[G_SLOTS], hp[G_SMS], st)
-                         : launch_cols<T, D, 4>(a, p.layer, hp[G_SLOTS], hp[G_SMS], st);
-        }
-        if (e != cudaSuccess || !hp[G_JOINS]) return e;
+    PagedArgs a;
+    a.q = p.q, a.out = p.out, a.ld_q = p.ld_q, a.ld_out = p.ld_out, a.plan = dp, a.err = err;
+    a.kv_heads = hp[G_KV_HEADS], a.group = hp[G_HEADS] / hp[G_KV_HEADS], a.scale_log2 = p.scale * 1.4426950408889634f;
+    a.part = reinterpret_cast<float *>(p.workspace);
+    a.part_ml = a.part + (int64_t)hp[G_PARTS] * a.kv_heads * D;
+    *launches = 0;
+    cudaError_t e = cudaSuccess;
+    const int32_t *at = dp + hp[G_O_ITEMS];
+    for (int c = 0; c < kClasses && e == cudaSuccess; ++c) {
+        a.items = reinterpret_cast<const int4 *>(at), a.n_items = hp[G_ITEMS + c];
+        at += 8 * (int64_t)a.n_items;
+        if (!a.n_items) continue;
         ++*launches;
-        const JoinArgs j = {a.part, a.part_ml, reinterpret_cast<const int4 *>(dp + hp[G_O_JOINS]), p.out, p.ld_out,
-                            a.kv_heads, a.group};
-        return launch_pdl(paged_join_kernel<T, D>, dim3((unsigned)hp[G_JOINS] * a.kv_heads), dim3(128), 0, st, j);
+        if (c == 0)
+            e = launch_cols<T, D, 1>(a, p.layer, hp[G_SLOTS], hp[G_SMS], st);
+        else if (c == 1)
+            e = launch_cols<T, D, 2>(a, p.layer, hp[G_SLOTS], hp[G_SMS], st);
+        else if constexpr (sizeof(T) == 2)  // (an fp32 plan has no tiles of 32)
+            e = launch_cols<T, D, 4>(a, p.layer, hp[G_SLOTS], hp[G_SMS], st);
     }
+    if (e != cudaSuccess || !hp[G_JOINS]) return e;
+    ++*launches;
+    const JoinArgs j = {a.part, a.part_ml, reinterpret_cast<const int4 *>(dp + hp[G_O_JOINS]), p.out, p.ld_out,
+                        a.kv_heads, a.group};
+    return launch_pdl(paged_join_kernel<T, D>, dim3((unsigned)hp[G_JOINS] * a.kv_heads), dim3(128), 0, st, j);
 }
 
 }  // namespace

@@ -168,6 +168,6 @@ def test_plans_cover_every_key_once(native, seed):
     for i, m in enumerate(need):
         table[i, :m] = order[at:at + m]
         at += m
-    p = plan(native, dtype=1, heads=group * kv, kv_heads=kv, d=int(g.choice([16, 64, 128])), page=page,
+    p = plan(native, dtype=seed % 2, heads=group * kv, kv_heads=kv, d=int(g.choice([16, 64, 128])), page=page,
              n_pages=sum(need), n=n, c=c, table=table)
     cover(native, p, n, c, table, page, group, kv)
