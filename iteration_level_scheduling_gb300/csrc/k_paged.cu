@@ -9,6 +9,7 @@
 // tile of 16 keys never crosses a page.
 #include <algorithm>
 #include <cstring>
+#include <numeric>
 #include <vector>
 
 #include "common.cuh"
@@ -38,9 +39,17 @@ enum {  // header words of a plan
     G_SMS,
     G_ITEMS,                       // work items by class (8, 16, 32 columns)
     G_PARTS = G_ITEMS + kClasses,  // partial columns of split items (per key/value head)
-    G_JOINS,                       // columns whose keys are split
+    G_JOINS,                       // column tiles whose keys are split
+    G_JOINCOLS,                    // most columns of one
     G_O_ITEMS,                     // 8 words each, class by class, most keys first
     G_O_JOINS,                     // 8 words each
+    G_PITEMS,                      // the same for prompts: pairs of row tiles
+    G_PPARTS,
+    G_PJOINS,
+    G_O_PITEMS,
+    G_O_PJOINS,
+    G_PACK,  // heads of a prompt's row tile
+    G_BOX,   // slots that one load of a prompt's keys may take
 };
 constexpr int kCwCtasPerSm = 2;
 constexpr int kSplitAt = 256;  // fewest keys of a part
@@ -48,9 +57,19 @@ constexpr int kSplitAt = 256;  // fewest keys of a part
 int64_t up4(int64_t x) { return (x + 3) & ~int64_t(3); }
 
 struct PagedSizes {
-    int64_t rows, tiles, maxpos, chunk, items[kClasses], parts, joins;
-    int64_t off_rows, off_reqs, off_tiles, off_items, off_joins, total;
+    int64_t rows, tiles, maxpos, chunk, items[kClasses], parts, joins, join_cols;
+    int64_t pchunk, pitems, pparts, pjoins;
+    int64_t off_rows, off_reqs, off_tiles, off_items, off_joins, off_pitems, off_pjoins, total;
 };
+
+// Prompts: rows x heads of one key/value head as the 128 rows of a tensor-core tile; two tiles share their keys.
+constexpr int kPromptCols = 32;  // columns of a request from which on it is one
+constexpr int kPpRows = 128, kPpKeys = 128;
+bool is_prompt(const PagedBatch &b, int i) {
+    return b.dtype && b.head_dim >= 64 && (int64_t)b.n_input[i] * (b.n_heads / b.n_kv_heads) > kPromptCols;
+}
+// Heads in a tile: all that share a key/value head, or one where they are too many to fill 128 rows well.
+int pack_of(int group) { return group <= 64 ? group : 1; }
 
 // Columns of a request: the smallest class that holds them all, else tiles of the widest (fp32: 16, by registers).
 int class_of(int64_t cols, int dtype) { return cols <= 8 ? 0 : cols <= 16 || !dtype ? 1 : 2; }
@@ -65,12 +84,22 @@ void column_tiles(const PagedBatch &b, int i, F fn) {
         fn(cl, c, n, b.ctx_len[i] + (c + n - 1) / group + 1);
     }
 }
+// The pairs of row tiles of a prompt: fn(first row, rows, keys that the last of them sees).
+template <typename F>
+void row_pairs(const PagedBatch &b, int i, F fn) {
+    const int64_t per = 2 * (kPpRows / pack_of(b.n_heads / b.n_kv_heads));
+    for (int64_t r = 0; r < b.n_input[i]; r += per) {
+        const int64_t n = std::min<int64_t>(per, b.n_input[i] - r);
+        fn(r, n, b.ctx_len[i] + r + n);
+    }
+}
 // Parts that a tile's keys are cut into.
 int64_t parts_of(int64_t keys, int64_t chunk) { return keys * 2 <= chunk * 3 ? 1 : (keys + chunk - 1) / chunk; }
 
 bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
     *z = {};
-    int64_t work = 0;
+    int64_t work = 0, pwork = 0;
+    const int64_t vheads = b.n_heads / pack_of(b.n_heads / b.n_kv_heads);
     const int64_t slots = b.n_pages * b.page_size;
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i];
@@ -81,19 +110,32 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
         for (int64_t p = 0; p * b.page_size < c + n; ++p)
             if (t[p] < 0 || t[p] >= b.n_pages) return false;
         z->rows += n;
-        column_tiles(b, i, [&](int, int64_t, int64_t, int64_t keys) { work += keys * b.n_kv_heads; });
+        if (is_prompt(b, i))
+            row_pairs(b, i, [&](int64_t, int64_t, int64_t keys) { pwork += (keys + kPpKeys - 1) / kPpKeys * vheads; });
+        else
+            column_tiles(b, i, [&](int, int64_t, int64_t, int64_t keys) { work += keys * b.n_kv_heads; });
         z->tiles += (c + n + 15) / 16;
         z->maxpos = std::max(z->maxpos, c + n);
     }
     // a third of a block's share, so that uneven items even out over the blocks
     const int64_t share = work / ((int64_t)kCwCtasPerSm * num_sms * 3);
     z->chunk = std::max<int64_t>(kSplitAt, (share + 63) / 64 * 64);
+    // half of a block's share of key tiles, eight at least
+    z->pchunk = std::max<int64_t>(8, pwork / num_sms / 2) * kPpKeys;
     for (int i = 0; i < b.n_req; ++i) {
         if (b.n_input[i] == 0) continue;
+        if (is_prompt(b, i)) {
+            row_pairs(b, i, [&](int64_t, int64_t, int64_t keys) {
+                const int64_t parts = parts_of(keys, z->pchunk);
+                z->pitems += parts;
+                if (parts > 1) z->pparts += parts * 2 * kPpRows, z->pjoins++;
+            });
+            continue;
+        }
         column_tiles(b, i, [&](int cl, int64_t, int64_t n, int64_t keys) {
             const int64_t parts = parts_of(keys, z->chunk);
             z->items[cl] += parts;
-            if (parts > 1) z->parts += parts * (8 << cl), z->joins += n;
+            if (parts > 1) z->parts += parts * (8 << cl), z->joins++, z->join_cols = std::max(z->join_cols, n);
         });
     }
     int64_t w = kPagedHdr;
@@ -103,10 +145,13 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
     const int64_t items = z->items[0] + z->items[1] + z->items[2];
     z->off_items = w, w = up4(w + 8 * items);
     z->off_joins = w, w = up4(w + 8 * z->joins);
+    z->off_pitems = w, w = up4(w + 8 * z->pitems);
+    z->off_pjoins = w, w = up4(w + 8 * z->pjoins);
     z->total = w;
     // 32-bit table entries and grid sizes
     return w <= INT32_MAX && z->rows * b.n_heads <= INT32_MAX && items * b.n_kv_heads <= INT32_MAX / 2 &&
-           z->parts <= INT32_MAX && z->joins * b.n_kv_heads <= INT32_MAX;
+           z->parts <= INT32_MAX && z->joins * b.n_kv_heads <= INT32_MAX && z->pitems * vheads <= INT32_MAX / 2 &&
+           z->pparts <= INT32_MAX && z->pjoins * vheads <= INT32_MAX;
 }
 
 // Whether two rows of the batch are written to one slot.
@@ -149,7 +194,9 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
     int32_t *item[kClasses], *join = buf + z.off_joins;
     item[0] = buf + z.off_items;
     for (int c = 1; c < kClasses; ++c) item[c] = item[c - 1] + 8 * z.items[c - 1];
-    int64_t part = 0, first_row = 0;
+    int32_t *pitem = buf + z.off_pitems, *pjoin = buf + z.off_pjoins;
+    const int32_t pack = pack_of(b.n_heads / b.n_kv_heads), tile_rows = kPpRows / pack;
+    int64_t part = 0, ppart = 0, first_row = 0;
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i];
         if (n == 0) continue;
@@ -164,7 +211,7 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
             row[1] = (int32_t)pos;
             row[2] = i;
         }
-        column_tiles(b, i, [&](int cl, int64_t col, int64_t cols, int64_t keys) {
+        const auto tile_items = [&](int cl, int64_t col, int64_t cols, int64_t keys) {
             const int64_t parts = parts_of(keys, z.chunk), per = parts == 1 ? keys : z.chunk;
             for (int64_t p = 0; p < parts; ++p, item[cl] += 8) {
                 int32_t *r = item[cl];
@@ -176,16 +223,30 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
                 r[5] = (int32_t)(c - p * per);
                 r[6] = parts == 1 ? -1 : (int32_t)(part + p * (8 << cl));
             }
-            for (int64_t x = 0; parts > 1 && x < cols; ++x, join += 8) {
-                join[0] = (int32_t)first_row;
-                join[1] = (int32_t)(col + x);
-                join[2] = (int32_t)parts;
-                join[3] = (int32_t)part;
-                join[4] = 8 << cl;
-                join[5] = (int32_t)x;
+            if (parts == 1) return;
+            join[0] = (int32_t)first_row, join[1] = (int32_t)col, join[2] = (int32_t)cols, join[3] = (int32_t)parts;
+            join[4] = (int32_t)part, join[5] = 8 << cl, join[6] = kPpRows;
+            join += 8, part += parts * (8 << cl);
+        };
+        const auto pair = [&](int64_t r0, int64_t rows, int64_t keys) {
+            const int64_t parts = parts_of(keys, z.pchunk), per = parts == 1 ? keys : z.pchunk;
+            for (int64_t p = 0; p < parts; ++p, pitem += 8) {
+                pitem[0] = req[i] + (int32_t)(p * per / 16);
+                pitem[1] = (int32_t)std::min<int64_t>(per, keys - p * per);
+                pitem[2] = (int32_t)(first_row + r0);
+                pitem[3] = (int32_t)rows;
+                pitem[4] = (int32_t)(c + r0 + 1 - p * per);
+                pitem[5] = parts == 1 ? -1 : (int32_t)(ppart + p * 2 * kPpRows);
             }
-            if (parts > 1) part += parts * (8 << cl);
-        });
+            if (parts == 1) return;
+            pjoin[0] = (int32_t)(first_row + r0), pjoin[1] = 0, pjoin[2] = (int32_t)rows * pack, pjoin[3] = (int32_t)parts;
+            pjoin[4] = (int32_t)ppart, pjoin[5] = 2 * kPpRows, pjoin[6] = tile_rows * pack;
+            pjoin += 8, ppart += parts * 2 * kPpRows;
+        };
+        if (is_prompt(b, i))
+            row_pairs(b, i, pair);
+        else
+            column_tiles(b, i, tile_items);
         first_row += n;
     }
     struct Rec {
@@ -194,6 +255,8 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
     Rec *rec = reinterpret_cast<Rec *>(buf + z.off_items);
     for (int c = 0; c < kClasses; rec += z.items[c], ++c)
         std::stable_sort(rec, rec + z.items[c], [](const Rec &x, const Rec &y) { return x.w[1] > y.w[1]; });
+    rec = reinterpret_cast<Rec *>(buf + z.off_pitems);
+    std::stable_sort(rec, rec + z.pitems, [](const Rec &x, const Rec &y) { return x.w[1] > y.w[1]; });
     buf[G_MAGIC] = kPagedMagic;
     buf[G_DTYPE] = b.dtype;
     buf[G_HEADS] = b.n_heads;
@@ -213,6 +276,14 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
     buf[G_JOINS] = (int32_t)z.joins;
     buf[G_O_ITEMS] = (int32_t)z.off_items;
     buf[G_O_JOINS] = (int32_t)z.off_joins;
+    buf[G_JOINCOLS] = (int32_t)z.join_cols;
+    buf[G_PITEMS] = (int32_t)z.pitems;
+    buf[G_PPARTS] = (int32_t)z.pparts;
+    buf[G_PJOINS] = (int32_t)z.pjoins;
+    buf[G_O_PITEMS] = (int32_t)z.off_pitems;
+    buf[G_O_PJOINS] = (int32_t)z.off_pjoins;
+    buf[G_PACK] = pack;
+    buf[G_BOX] = std::gcd(b.page_size, kPpKeys);
     return true;
 }
 
@@ -222,7 +293,8 @@ PagedInfo paged_plan_info(const int32_t *hp) {
 }
 
 int64_t paged_workspace_bytes(const int32_t *hp) {
-    return (int64_t)hp[G_PARTS] * hp[G_KV_HEADS] * (hp[G_DIM] + 2) * 4;
+    return ((int64_t)hp[G_PARTS] * hp[G_KV_HEADS] + (int64_t)hp[G_PPARTS] * (hp[G_HEADS] / hp[G_PACK])) *
+           (hp[G_DIM] + 2) * 4;
 }
 
 // ---------------------------------------------------------------------------
@@ -852,14 +924,16 @@ __global__ void __launch_bounds__(kCwThreads, 2)
     for (; used < issued; ++used) mbar_wait_bounded(&full[used % S::kStages], (used / S::kStages) & 1u, a.err);
 }
 
-// Split keys: the parts of a column, in their order.  One block per (column,
-// key/value head); 4 components per thread, the parts dealt to the thread groups.
+// Split keys: the parts of a column, in their order.  One block per (column tile,
+// head) and column; 4 components per thread, the parts dealt to the thread groups.
+// `heads` and `group`: key/value heads and the query heads of each; for prompts
+// the tiles' heads and the heads packed into each.
 struct JoinArgs {
     const float *part, *part_ml;
-    const int4 *joins;  // {first row, column of the request, parts, first part}, {columns from part to part, column there, 0, 0}
+    const int4 *joins;  // {first row, first column, columns, parts}, {first part, from part to part, columns of 128, 0}
     void *out;
     int64_t ld_out;
-    int kv_heads, group;
+    int heads, group;
 };
 template <typename T, int D>
 __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
@@ -868,8 +942,11 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
     __shared__ float2 sml[N];
     pdl_trigger();
     pdl_wait();
-    const int j = blockIdx.x / a.kv_heads, h = blockIdx.x % a.kv_heads;
+    const int j = blockIdx.x / a.heads, h = blockIdx.x % a.heads, x = blockIdx.y;
     const int4 r0 = a.joins[2 * j], r1 = a.joins[2 * j + 1];
+    // (a tile of 128 may hold fewer columns than that)
+    const int col = x / kPpRows * r1.z + x % kPpRows;
+    if (x >= r1.y || x % kPpRows >= r1.z || col >= r0.z) return;
     const int grp = threadIdx.x / L4, d = threadIdx.x % L4;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -879,8 +956,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
         o.x = o.x * f + o2.x * f2, o.y = o.y * f + o2.y * f2, o.z = o.z * f + o2.z * f2, o.w = o.w * f + o2.w * f2;
     };
 #pragma unroll 4
-    for (int p = grp; p < r0.z; p += N) {
-        const int64_t at = (int64_t)(r0.w + p * r1.x) * a.kv_heads + h * r1.x + r1.y;
+    for (int p = grp; p < r0.w; p += N) {
+        const int64_t at = ((int64_t)r1.x + (int64_t)p * r1.y) * a.heads + (int64_t)h * r1.y + x;
         const float2 v = *reinterpret_cast<const float2 *>(a.part_ml + 2 * at);
         add(v.x, v.y, *reinterpret_cast<const float4 *>(a.part + at * D + 4 * d));
     }
@@ -889,12 +966,605 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
     __syncthreads();
     if (grp) return;
 #pragma unroll
-    for (int x = 1; x < N; ++x) add(sml[x].x, sml[x].y, so[x][d]);
-    T *dst = reinterpret_cast<T *>(a.out) + (int64_t)(r0.x + r0.y / a.group) * a.ld_out +
-             (h * a.group + r0.y % a.group) * D + 4 * d;
+    for (int z = 1; z < N; ++z) add(sml[z].x, sml[z].y, so[z][d]);
+    const int c = r0.y + col;
+    T *dst = reinterpret_cast<T *>(a.out) + (int64_t)(r0.x + c / a.group) * a.ld_out +
+             (h * a.group + c % a.group) * D + 4 * d;
     const float f = 1.f / l;
     store4(dst, o.x * f, o.y * f, o.z * f, o.w * f);
 }
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Prompts on the fifth-generation tensor cores (bf16, head_dim 64 or 128)
+// ---------------------------------------------------------------------------
+// The rows of a tile are (row, head) pairs of one key/value head, heads
+// innermost, 128 / pack rows of a request: every key tile is loaded once for all
+// heads that share it, and short chunks of prompts still fill tiles.  An item is
+// two such tiles, t = 0 and 1, over one range of keys; each has a warpgroup of its own (a
+// thread per tile row), and while one's softmax runs the other's products do.
+//   S_t = Q_t K^T   128 x 128, both operands from shared memory
+//   O_t += P_t V    P (bf16) from tensor memory, V as it lies in its pages
+// Tensor memory: S_0, S_1, O_0, O_1, 128 columns each; P_t takes the place of
+// S_t, so that S_t of the next key tile is issued once that P V has completed.
+// In step order the MMA warp issues P V of both tiles, then S of both: with X
+// from S to P, a step takes X + 1.5 of its products' time.  Shared memory:
+// Q of both tiles and a ring of key tiles; the loads are boxes of a page (or of
+// the part of it that divides 128 slots), a lane of the TMA warp each.
+// O is rescaled only where a row's maximum grew by more than 2^8, as every P is
+// formed against the maximum that O and l carry.
+// Keys past the item's last are masked by index and their V rows zeroed.  A
+// masked weight of 0 times a value that is not finite is NaN: rows whose output
+// is not finite are computed once more, key by key, over what they see.
+namespace {
+
+constexpr int kPpThreads = 384;  // two softmax warpgroups, one with the TMA and the MMA warp (and two that idle)
+constexpr uint32_t kPpAtom = 16384;  // 128 rows of 128 bytes
+constexpr float kPpRescale = 8.f;
+
+template <int D>
+struct PpLayout {
+    static constexpr int kAtoms = D / 64;
+    static constexpr int kStages = D == 64 ? 4 : 2;
+    static constexpr uint32_t kQ = 0;  // [tile][atom]
+    static constexpr uint32_t kK = 2 * kAtoms * kPpAtom;
+    static constexpr uint32_t kV = kK + kStages * kAtoms * kPpAtom;
+    static constexpr uint32_t kBars = kV + kStages * kAtoms * kPpAtom;
+    static constexpr uint32_t kBytes = kBars + 512;
+};
+struct PpBars {
+    uint64_t q_full, q_empty, k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], pv_done[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int abort;
+};
+struct PpArgs {
+    const bf16 *q, *layer;
+    bf16 *out;
+    float *part, *part_ml;
+    const int32_t *plan;
+    const int4 *items;  // {tiles at, keys, first row, rows}, {keys that the first row sees, part or -1, 0, 0}
+    int64_t ld_q, ld_out, slots;
+    int n_items, vheads, pack, per_kv, kv_heads, box;  // (per_kv: tile heads of a key/value head)
+    float scale_log2;
+    unsigned *err;
+};
+
+__device__ __forceinline__ void pp_tma_q(uint32_t dst, const void *tmap, uint64_t *bar, int c0, int head, int row) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(dst),
+        "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(head), "r"(row)
+        : "memory");
+}
+__device__ __forceinline__ void pp_tma_kv(uint32_t dst, const void *tmap, uint64_t *bar, int c0, int slot, int h, int kv,
+                                          uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+        "{%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+        "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(slot), "r"(h), "r"(kv), "l"(policy)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]: a row of A per lane, two elements per column.
+__device__ __forceinline__ void pp_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ uint64_t pp_desc_mn(uint32_t saddr) {  // MN-major, 64-element blocks kPpAtom apart
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((kPpAtom >> 4) & 0x3FFFu) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ void pp_ld32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// Waits for this thread's loads; the registers are operands, so that no use of them is placed before the wait.
+__device__ __forceinline__ void pp_wait_ld32(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void pp_st32(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        :
+        : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+          "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+          "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void pp_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};"
+        :
+        : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void pp_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Two fp32 operations at once.
+__device__ __forceinline__ uint64_t pp_pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void pp_unpair(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t pp_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t pp_add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// One row over keys 0 .. n - 1 of its item by the whole warp: afterwards every
+// lane holds m, l and 8 components of o, lane % (D / 8) * 8 on.
+template <int D>
+__device__ void pp_row(const PpArgs &a, const bf16 *q, const int32_t *tiles, int n, int kvh, float &m, float &l, float *o) {
+    constexpr int LPT = D / 8, TPW = 32 / LPT;
+    const int lane = threadIdx.x & 31, g = lane / LPT, sub = lane % LPT;
+    const bf16 *kb = a.layer + (int64_t)kvh * a.slots * D + sub * 8, *vb = kb + (int64_t)a.kv_heads * a.slots * D;
+    float qf[8];
+    load16(q + sub * 8, qf);
+    m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = 0.f;
+    for (int t0 = 0; t0 < n; t0 += TPW) {
+        const int t = t0 + g;
+        float k[8], v[8], s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) k[e] = v[e] = 0.f;
+        if (t < n) {
+            const int64_t slot = (int64_t)tiles[t / 16] * 16 + t % 16;
+            load16(kb + slot * D, k);
+            load16(vb + slot * D, v);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(qf[e], k[e], s);
+#pragma unroll
+        for (int x = LPT / 2; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        s = t < n ? s * a.scale_log2 : -INFINITY;
+        const float mx = fmaxf(m, s), base = cw_base(mx), corr = cw_exp2(m - base), p = cw_exp2(s - base);
+        l = l * corr + p, m = mx;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = fmaf(p, v[e], o[e] * corr);
+    }
+#pragma unroll
+    for (int x = LPT; x < 32; x <<= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, x), l2 = __shfl_xor_sync(0xffffffffu, l, x);
+        const float mx = fmaxf(m, m2), base = cw_base(mx), f = cw_exp2(m - base), f2 = cw_exp2(m2 - base);
+        l = l * f + l2 * f2, m = mx;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = o[e] * f + __shfl_xor_sync(0xffffffffu, o[e], x) * f2;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPpThreads, 1)
+    paged_prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmkv,
+                        const PpArgs a) {
+    using L = PpLayout<D>;
+    constexpr unsigned kFull = 0xffffffffu;
+    extern __shared__ __align__(1024) uint8_t pp_smem[];
+    pdl_trigger();
+    if (smem_u32(pp_smem) & 1023u) {  // uniform: every thread leaves before any barrier
+        if (threadIdx.x == 0) raise_err(a.err, 8u);
+        return;
+    }
+    uint8_t *const sm = pp_smem;
+    PpBars &bar = *reinterpret_cast<PpBars *>(sm + L::kBars);
+    volatile int *const abort = &bar.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar.q_full, 1);
+        mbar_init(&bar.q_empty, 1);
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(&bar.k_full[s], 1);
+            mbar_init(&bar.k_empty[s], 1);
+            mbar_init(&bar.v_full[s], 1);
+            mbar_init(&bar.v_empty[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bar.s_full[t], 1);
+            mbar_init(&bar.p_full[t], 4);  // an arrival per warp
+            mbar_init(&bar.pv_done[t], 1);
+        }
+        mbar_init(&bar.drain, 1);
+        *abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tmq);
+        prefetch_tmap(&tmkv);
+    }
+    if (warp == 9) {
+        tmem_alloc(&bar.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem;
+    pdl_wait();
+
+    const int total = a.n_items * a.vheads, G = gridDim.x, tile_rows = kPpRows / a.pack;
+    struct Item {
+        int vh, at, keys, row, rows, sees, part;
+        int n_rows[2], nk[2], n_kt;  // rows and key tiles of either row tile, key tiles of the item
+    };
+    // The block's k-th item (longest first, dealt forwards and backwards in turn); false behind the last.
+    const auto item_at = [&](int k, Item &it) {
+        const int e = k * G + ((k & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        if (e >= total) return false;
+        const int4 r0 = a.items[2 * (e / a.vheads)], r1 = a.items[2 * (e / a.vheads) + 1];
+        it.vh = e % a.vheads;
+        it.at = r0.x, it.keys = r0.y, it.row = r0.z, it.rows = r0.w, it.sees = r1.x, it.part = r1.y;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            it.n_rows[t] = min(max(it.rows - t * tile_rows, 0), tile_rows);
+            const int last = min(it.sees + t * tile_rows + it.n_rows[t] - 1, it.keys);  // keys that its last row sees
+            it.nk[t] = it.n_rows[t] > 0 && last > 0 ? (last + kPpKeys - 1) / kPpKeys : 0;
+        }
+        it.n_kt = max(it.nk[0], it.nk[1]);
+        return true;
+    };
+    const auto wait = [&](uint64_t *b, uint32_t phase) {  // (whole warps)
+        return __all_sync(kFull, !*abort && mbar_wait_bounded(b, phase & 1u, a.err)) != 0;
+    };
+    // Key tiles are numbered g = 0, 1, .. across this block's items (stage g % kStages, its use g / kStages).
+
+    // 384 threads of 168 registers: 4 x 32 of 88 leave 208 for the softmax warps, which hold a row of S
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 8) {
+            // ------------------------------ TMA ------------------------------
+            const uint64_t pol = l2_policy_evict_normal();  // every row tile of the request reads them
+            uint32_t g = 0, q_used = 0, k_used = 0, v_used = 0;
+            bool ok = true;
+            Item it;
+            for (int k = 0; ok && item_at(k, it); ++k) {
+                if (k >= 1 && !(ok = wait(&bar.q_empty, (uint32_t)(k - 1)))) break;
+                if (lane == 0) {
+                    const int tiles = it.n_rows[1] > 0 ? 2 : 1;
+                    mbar_arrive_expect_tx(&bar.q_full, (uint32_t)(tiles * L::kAtoms * tile_rows * a.pack * 128));
+                    for (int t = 0; t < tiles; ++t)
+                        for (int c = 0; c < L::kAtoms; ++c)
+                            pp_tma_q(smem_u32(sm + L::kQ + (t * L::kAtoms + c) * kPpAtom), &tmq, &bar.q_full, 64 * c,
+                                     it.vh * a.pack, it.row + t * tile_rows);
+                }
+                __syncwarp();
+                ++q_used;
+                const int kvh = it.vh / a.per_kv, n_tiles = (it.keys + 15) / 16, per = a.box / 16;
+                const int b = lane / L::kAtoms, c = lane % L::kAtoms;  // this lane's box of a key tile, and its 64 components
+                const auto index = [&](int j) {  // slot / 16 of the box's first key in key tile j
+                    const int x = j * (kPpKeys / 16) + b * per;
+                    return b * a.box < kPpKeys && x < n_tiles ? a.plan[it.at + x] : -1;
+                };
+                int next = index(0);
+                for (int j = 0; j < it.n_kt; ++j, ++g) {
+                    const uint32_t s = g % L::kStages, use = g / L::kStages;
+                    const int slot = next * 16;
+                    if (j + 1 < it.n_kt) next = index(j + 1);
+                    const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, slot >= 0)) * a.box * 128);
+                    if (g >= L::kStages && !(ok = wait(&bar.k_empty[s], use - 1))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&bar.k_full[s], bytes);
+                    __syncwarp();
+                    const uint32_t at = (s * L::kAtoms + c) * kPpAtom + (uint32_t)(b * a.box * 128);
+                    if (slot >= 0) pp_tma_kv(smem_u32(sm + L::kK + at), &tmkv, &bar.k_full[s], 64 * c, slot, kvh, 0, pol);
+                    ++k_used;
+                    if (g >= L::kStages && !(ok = wait(&bar.v_empty[s], use - 1))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&bar.v_full[s], bytes);
+                    __syncwarp();
+                    if (slot >= 0) pp_tma_kv(smem_u32(sm + L::kV + at), &tmkv, &bar.v_full[s], 64 * c, slot, kvh, 1, pol);
+                    ++v_used;
+                }
+            }
+            if (!ok) {  // the copies in flight land before the block ends
+                *abort = 1;
+                if (q_used > 0) mbar_wait_bounded(&bar.q_full, (q_used - 1) & 1u, a.err);
+                for (uint32_t x = k_used > L::kStages ? k_used - L::kStages : 0; x < k_used; ++x)
+                    mbar_wait_bounded(&bar.k_full[x % L::kStages], (x / L::kStages) & 1u, a.err);
+                for (uint32_t x = v_used > L::kStages ? v_used - L::kStages : 0; x < v_used; ++x)
+                    mbar_wait_bounded(&bar.v_full[x % L::kStages], (x / L::kStages) & 1u, a.err);
+            }
+        } else if (warp == 9) {
+            // ------------------------------ MMA ------------------------------
+            const uint32_t idesc_s = idesc_bf16_f32(kPpRows, kPpKeys);
+            const uint32_t idesc_pv = idesc_bf16_f32(kPpRows, D) | (1u << 16);  // B (V) MN-major
+            uint32_t n_s[2] = {0, 0}, n_pv[2] = {0, 0};  // products issued
+            bool pending[2] = {false, false}, first[2] = {false, false}, ok = true;
+            uint32_t g = 0;
+            // O_t (+)= P_t V of key tile v; `last`: nothing else reads that stage.  (An item's first P_t is written
+            // after the last item's O_t has been read out.)
+            const auto issue_pv = [&](int t, uint32_t v, bool last) {
+                const uint32_t s = v % L::kStages;
+                if (!wait(&bar.p_full[t], n_pv[t]) || !wait(&bar.v_full[s], v / L::kStages)) return false;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t vs = smem_u32(sm + L::kV + s * L::kAtoms * kPpAtom);
+#pragma unroll
+                    for (int ks = 0; ks < kPpKeys / 16; ++ks)  // 16 keys: two groups of 8 rows of V, 8 columns of P
+                        pp_mma_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * ks, pp_desc_mn(vs + (uint32_t)ks * 2048u),
+                                  idesc_pv, (uint32_t)(!first[t] || ks != 0));
+                    tc_commit(&bar.pv_done[t]);
+                    if (last) tc_commit(&bar.v_empty[s]);
+                }
+                __syncwarp();
+                ++n_pv[t];
+                pending[t] = false;
+                return true;
+            };
+            const auto issue_s = [&](int t, bool k_last, bool q_last) {
+                const uint32_t s = g % L::kStages;
+                if (n_s[t] > 0 && !wait(&bar.pv_done[t], n_s[t] - 1)) return false;  // P_t lies in S_t
+                if (!wait(&bar.k_full[s], g / L::kStages)) return false;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t qs = smem_u32(sm + L::kQ + t * L::kAtoms * kPpAtom);
+                    const uint32_t ks = smem_u32(sm + L::kK + s * L::kAtoms * kPpAtom);
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {  // 16 components: 32 bytes of a 64-component block
+                        const uint32_t o = (uint32_t)(x >> 2) * kPpAtom + (uint32_t)(x & 3) * 32u;
+                        tc_mma_f16(tmem + 128u * t, smem_desc_k128(qs + o), smem_desc_k128(ks + o), idesc_s,
+                                   (uint32_t)(x != 0));
+                    }
+                    tc_commit(&bar.s_full[t]);
+                    if (k_last) tc_commit(&bar.k_empty[s]);
+                    if (q_last) tc_commit(&bar.q_empty);
+                }
+                __syncwarp();
+                ++n_s[t];
+                return true;
+            };
+            Item it;
+            for (int k = 0; ok && item_at(k, it); ++k) {
+                for (int j = 0; ok && j < it.n_kt; ++j, ++g) {
+                    // (both of the last step's P V were issued only if both tiles had that step)
+                    if (pending[0]) ok = issue_pv(0, g - 1, !pending[1]);
+                    if (ok && pending[1]) ok = issue_pv(1, g - 1, true);
+                    if (ok && j == 0) ok = wait(&bar.q_full, (uint32_t)k);
+                    const bool act[2] = {j < it.nk[0], j < it.nk[1]};
+                    const bool q_last = j + 1 == it.n_kt;
+                    if (ok && act[0]) ok = issue_s(0, !act[1], q_last && !act[1]);
+                    if (ok && act[1]) ok = issue_s(1, true, q_last);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) pending[t] = act[t], first[t] = j == 0;
+                }
+            }
+            if (ok && pending[0]) ok = issue_pv(0, g - 1, !pending[1]);
+            if (ok && pending[1]) ok = issue_pv(1, g - 1, true);
+            if (!ok) *abort = 1;
+            // every product issued has completed before stages and tensor memory are given up
+            if (lane == 0) tc_commit(&bar.drain);
+            __syncwarp();
+            mbar_wait_bounded(&bar.drain, 0u, a.err);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // ------------------------------ softmax ------------------------------
+        const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t s_t = tmem + 128u * t + ((uint32_t)(quarter * 32) << 16), o_t = s_t + 256u;
+        uint32_t g0 = 0, n = 0;  // the item's first key tile, this tile's key tiles so far
+        bool ok = true;
+        Item it;
+        for (int k = 0; ok && item_at(k, it); g0 += it.n_kt, ++k) {
+            if (it.n_rows[t] == 0) continue;
+            const int jr = r / a.pack, sees = it.sees + t * tile_rows + jr;  // keys 0 .. sees - 1 of the item are this row's
+            const int first_sees = it.sees + t * tile_rows;
+            float m = -INFINITY, l = 0.f;  // (m in the units of S)
+            for (int j = 0; j < it.nk[t]; ++j, ++n) {
+                const int kbase = j * kPpKeys;
+                if (!(ok = wait(&bar.s_full[t], n))) break;
+                tc_fence_after();
+                uint32_t s[128];
+#pragma unroll
+                for (int x = 0; x < 128; x += 32) pp_ld32(s_t + x, s + x);
+#pragma unroll
+                for (int x = 0; x < 128; x += 32) pp_wait_ld32(s + x);
+                if (kbase + kPpKeys > first_sees || kbase + kPpKeys > it.keys) {
+                    const int valid = min(sees, it.keys) - kbase;
+#pragma unroll
+                    for (int x = 0; x < 128; ++x)
+                        if (x >= valid) s[x] = 0xff800000u;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int x = 0; x < 128; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                float alpha = 1.f;
+                if (j == 0) {
+                    m = top;
+                } else if ((top - m) * a.scale_log2 > kPpRescale) {  // (from no key seen, -inf, as well)
+                    alpha = cw_exp2((m - top) * a.scale_log2);
+                    m = top;
+                    l *= alpha;
+                }
+                if (__any_sync(kFull, alpha != 1.f)) {  // (the item's P V so far are done: S_t was issued behind them)
+#pragma unroll
+                    for (int x = 0; x < D; x += 32) {
+                        uint32_t o[32];
+                        pp_ld32(o_t + x, o);
+                        pp_wait_ld32(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        pp_st32(o_t + x, o);
+                    }
+                }
+                float neg = -cw_base(m) * a.scale_log2;
+                if (__any_sync(kFull, fabsf(neg) > 16384.f)) {  // s scale - neg in one step would keep what neg lost
+#pragma unroll
+                    for (int x = 0; x < 128; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) - cw_base(m));
+                    neg = 0.f;
+                }
+                const uint64_t scale2 = pp_pair(a.scale_log2, a.scale_log2), neg2 = pp_pair(neg, neg);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int x = 0; x < 128; x += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float p0, p1;
+                        pp_unpair(pp_fma2(pp_pair(__uint_as_float(s[x + 2 * e]), __uint_as_float(s[x + 2 * e + 1])), scale2,
+                                          neg2),
+                                  p0, p1);
+                        p0 = cw_exp2(p0), p1 = cw_exp2(p1);
+                        sum[e & 1] = pp_add2(sum[e & 1], pp_pair(p0, p1));
+                        w[e] = cw_pack(p0, p1);
+                    }
+                    pp_st16(s_t + x / 2, w);
+                }
+                float l0, l1;
+                pp_unpair(pp_add2(sum[0], sum[1]), l0, l1);
+                l += l0 + l1;
+                const int here = it.keys - kbase;  // V rows past the item's last key: zero, once they have landed
+                if (here < kPpKeys) {
+                    const uint32_t v = g0 + j, st = v % L::kStages;
+                    if (!(ok = wait(&bar.v_full[st], v / L::kStages))) break;
+                    if (r >= here)
+#pragma unroll
+                        for (int x = 0; x < 8 * L::kAtoms; ++x)
+                            *reinterpret_cast<uint4 *>(sm + L::kV + (st * L::kAtoms + x / 8) * kPpAtom + r * 128 +
+                                                       x % 8 * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+                pp_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full[t]);
+            }
+            if (!ok) break;
+            // ---- the item's output ----
+            const bool mine = r < it.n_rows[t] * a.pack;
+            const int row = it.row + t * tile_rows + jr, head = it.vh * a.pack + r % a.pack;
+            bf16 *const dst = a.out + (int64_t)row * a.ld_out + (int64_t)head * D;
+            const int64_t at = (int64_t)it.part * a.vheads + (int64_t)it.vh * (2 * kPpRows) + t * kPpRows + r;
+            bool bad = false;
+            if (it.nk[t] > 0) {
+                if (!(ok = wait(&bar.pv_done[t], n - 1))) break;
+                tc_fence_after();
+                const float inv = 1.f / l;
+#pragma unroll
+                for (int x = 0; x < D; x += 32) {
+                    uint32_t o[32];
+                    pp_ld32(o_t + x, o);
+                    pp_wait_ld32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) bad |= (o[e] & 0x7f800000u) == 0x7f800000u;
+                    if (!mine) continue;
+                    if (it.part < 0) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            float f[8];
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) f[z] = __uint_as_float(o[e + z]) * inv;
+                            store16(dst + x + e, f);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4 *>(a.part + at * D + x + e) =
+                                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+                tc_fence_before();
+            } else if (mine) {  // a part of the keys of which this tile sees none
+                for (int x = 0; x < D; x += 4) *reinterpret_cast<uint4 *>(a.part + at * D + x) = make_uint4(0, 0, 0, 0);
+            }
+            if (mine && it.part >= 0) *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m * a.scale_log2, l);
+            unsigned todo = __ballot_sync(kFull, mine && (bad || l != l));
+            for (; todo; todo &= todo - 1) {  // rows with something that is not finite, over what they see
+                const int x = __ffs(todo) - 1, rr = quarter * 32 + x;
+                const int row2 = it.row + t * tile_rows + rr / a.pack, head2 = it.vh * a.pack + rr % a.pack;
+                const int seen = min(it.sees + t * tile_rows + rr / a.pack, it.keys);
+                float m2, l2, o2[8];
+                pp_row<D>(a, a.q + (int64_t)row2 * a.ld_q + (int64_t)head2 * D, a.plan + it.at, seen, it.vh / a.per_kv, m2, l2,
+                          o2);
+                const int64_t at2 = at - r + rr;
+                if (lane < D / 8) {
+                    if (it.part < 0) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o2[e] /= l2;
+                        store16(a.out + (int64_t)row2 * a.ld_out + (int64_t)head2 * D + lane * 8, o2);
+                    } else {
+                        store16(a.part + at2 * D + lane * 8, o2);
+                        store16(a.part + at2 * D + lane * 8 + 4, o2 + 4);
+                        if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + 2 * at2) = make_float2(m2, l2);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) *abort = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch_prompts(const PagedAttn &p, const int32_t *hp, const int32_t *dp, float *part, float scale_log2,
+                           unsigned *err, int *launches, cudaStream_t st) {
+    using L = PpLayout<D>;
+    cudaError_t e = max_smem_once((const void *)paged_prompt_kernel<D>, (int)L::kBytes);
+    if (e != cudaSuccess) return e;
+    PpArgs a;
+    a.q = reinterpret_cast<const bf16 *>(p.q), a.layer = reinterpret_cast<const bf16 *>(p.layer);
+    a.out = reinterpret_cast<bf16 *>(p.out), a.ld_q = p.ld_q, a.ld_out = p.ld_out, a.slots = hp[G_SLOTS];
+    a.plan = dp, a.items = reinterpret_cast<const int4 *>(dp + hp[G_O_PITEMS]), a.n_items = hp[G_PITEMS];
+    a.pack = hp[G_PACK], a.vheads = hp[G_HEADS] / a.pack, a.kv_heads = hp[G_KV_HEADS];
+    a.per_kv = a.vheads / a.kv_heads, a.box = hp[G_BOX], a.scale_log2 = scale_log2, a.err = err;
+    a.part = part, a.part_ml = part + (int64_t)hp[G_PPARTS] * a.vheads * D;
+    CUtensorMap tmq, tmkv;  // q as [row][head][component], the layer as [K|V][head][slot][component]
+    const uint64_t qdims[3] = {(uint64_t)D, (uint64_t)hp[G_HEADS], (uint64_t)hp[G_ROWS]};
+    const uint64_t qstrides[2] = {(uint64_t)D * 2, (uint64_t)p.ld_q * 2};
+    const uint32_t qbox[3] = {64, (uint32_t)a.pack, (uint32_t)(kPpRows / a.pack)};
+    const uint64_t row = D * 2, dims[4] = {(uint64_t)D, (uint64_t)a.slots, (uint64_t)a.kv_heads, 2};
+    const uint64_t strides[3] = {row, row * (uint64_t)a.slots, row * (uint64_t)a.slots * (uint64_t)a.kv_heads};
+    const uint32_t box[4] = {64, (uint32_t)a.box, 1, 1};
+    if (!encode_tensor_map(&tmq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.q, qdims, qstrides, qbox,
+                           CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tensor_map(&tmkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p.layer, dims, strides, box,
+                           CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    const int grid = (int)std::min<int64_t>((int64_t)a.n_items * a.vheads, hp[G_SMS]);
+    ++*launches;
+    e = launch_pdl(paged_prompt_kernel<D>, dim3((unsigned)grid), dim3(kPpThreads), L::kBytes, st, tmq, tmkv, a);
+    if (e != cudaSuccess || !hp[G_PJOINS]) return e;
+    ++*launches;
+    const JoinArgs j = {a.part, a.part_ml, reinterpret_cast<const int4 *>(dp + hp[G_O_PJOINS]), p.out, p.ld_out, a.vheads,
+                        a.pack};
+    return launch_pdl(paged_join_kernel<bf16, D>, dim3((unsigned)hp[G_PJOINS] * a.vheads, 2 * kPpRows), dim3(128), 0, st,
+                      j);
+}
+
+}  // namespace
+
+namespace {
 
 template <typename T, int D, int NT>
 cudaError_t launch_cols(const PagedArgs &a, const void *layer, int64_t slots, int sms, cudaStream_t st) {
@@ -926,8 +1596,14 @@ cudaError_t launch_attention(const PagedAttn &p, const int32_t *hp, const int32_
     a.kv_heads = hp[G_KV_HEADS], a.group = hp[G_HEADS] / hp[G_KV_HEADS], a.scale_log2 = p.scale * 1.4426950408889634f;
     a.part = reinterpret_cast<float *>(p.workspace);
     a.part_ml = a.part + (int64_t)hp[G_PARTS] * a.kv_heads * D;
+    float *const ppart = a.part_ml + (int64_t)hp[G_PARTS] * a.kv_heads * 2;
     *launches = 0;
     cudaError_t e = cudaSuccess;
+    if constexpr (sizeof(T) == 2 && D >= 64)
+        if (hp[G_PITEMS]) {
+            e = launch_prompts<D>(p, hp, dp, ppart, a.scale_log2, err, launches, st);
+            if (e != cudaSuccess) return e;
+        }
     const int32_t *at = dp + hp[G_O_ITEMS];
     for (int c = 0; c < kClasses && e == cudaSuccess; ++c) {
         a.items = reinterpret_cast<const int4 *>(at), a.n_items = hp[G_ITEMS + c];
@@ -945,7 +1621,8 @@ cudaError_t launch_attention(const PagedAttn &p, const int32_t *hp, const int32_
     ++*launches;
     const JoinArgs j = {a.part, a.part_ml, reinterpret_cast<const int4 *>(dp + hp[G_O_JOINS]), p.out, p.ld_out,
                         a.kv_heads, a.group};
-    return launch_pdl(paged_join_kernel<T, D>, dim3((unsigned)hp[G_JOINS] * a.kv_heads), dim3(128), 0, st, j);
+    return launch_pdl(paged_join_kernel<T, D>, dim3((unsigned)hp[G_JOINS] * a.kv_heads, (unsigned)hp[G_JOINCOLS]),
+                      dim3(128), 0, st, j);
 }
 
 }  // namespace

@@ -106,63 +106,88 @@ def test_oracle_by_hand():
 
 
 # words of a plan's header (k_paged.cu)
-O_ROWS, O_REQS, O_TILES, ITEMS, PARTS, JOINS, O_ITEMS, O_JOINS = 10, 11, 12, 14, 17, 18, 19, 20
+O_ROWS, O_REQS, O_TILES, ITEMS, PARTS, JOINS, JOINCOLS, O_ITEMS, O_JOINS = 10, 11, 12, 14, 17, 18, 19, 20, 21
+PITEMS, PPARTS, PJOINS, O_PITEMS, O_PJOINS, PACK, BOX = 22, 23, 24, 25, 26, 27, 28
 
 
 def cover(native, p, n, c, table, page, group, kv_heads):
-    """What a plan's items read and write: every row's column sees its keys once, and nothing leaves its buffer."""
-    keys_of = {}
+    """What a plan's items read and write: every row and head sees its keys once, and nothing leaves its buffer."""
     words, rows = len(p), sum(n)
     first = np.concatenate([[0], np.cumsum(n)])
     req_of = np.repeat(np.arange(len(n)), n)
+    keys_of, written = {}, {}  # by (row, head of the tile or of the group): spans of keys, partial columns
+
+    def keys_ok(i, tile, keys):
+        k0 = 16 * (tile - int(p[p[O_REQS] + i]))
+        assert keys >= 1 and 0 <= k0 and k0 + keys <= c[i] + n[i]
+        slots = p[tile:tile + (keys + 15) // 16]
+        assert tile + len(slots) <= words
+        assert (slots == paged.slots(table[i], page, k0, keys)[::16] // 16).all()
+        return k0
+
     at = p[O_ITEMS]
-    part_end = int(p[PARTS])
-    written = {}
     for cl in range(3):
         for r in p[at:at + 8 * p[ITEMS + cl]].reshape(-1, 8):
             tile, keys, row0, col0, cols, last0, part = (int(x) for x in r[:7])
-            i = int(req_of[row0]) if n[req_of[row0]] else -1
-            assert row0 == first[i] and 1 <= cols <= 8 << cl and keys >= 1 and col0 + cols <= n[i] * group
-            k0 = 16 * (tile - int(p[p[O_REQS] + i]))
-            assert k0 % 16 == 0 and 0 <= k0 and k0 + keys <= c[i] + n[i] and last0 == c[i] - k0
-            slots = p[tile:tile + (keys + 15) // 16]
-            assert tile + len(slots) <= words
-            assert (slots == paged.slots(table[i], page, k0, keys)[::16] // 16).all()
-            if part >= 0:
-                assert part + (8 << cl) <= part_end
+            i = int(req_of[row0])
+            assert row0 == first[i] and 1 <= cols <= 8 << cl and col0 + cols <= n[i] * group
+            k0 = keys_ok(i, tile, keys)
+            assert last0 == c[i] - k0 and (part < 0 or part + (8 << cl) <= p[PARTS])
             for x in range(cols):
                 j = (col0 + x) // group
-                seen = max(0, min(keys, last0 + j + 1))
-                keys_of.setdefault((row0 + j, (col0 + x) % group), []).append((k0, k0 + seen))
-                written.setdefault((i, col0 + x), []).append((part + x) if part >= 0 else None)
+                key = (row0 + j, (col0 + x) % group)
+                keys_of.setdefault(key, []).append((k0, k0 + max(0, min(keys, last0 + j + 1))))
+                written.setdefault(key, []).append(("c", part + x) if part >= 0 else None)
         at += 8 * p[ITEMS + cl]
-    for r in range(rows):
-        for g in range(group):
-            spans = sorted(s for s in keys_of[(r, g)] if s[0] < s[1])
-            assert spans[0][0] == 0 and spans[-1][1] == c[req_of[r]] + r - first[req_of[r]] + 1
-            assert all(a[1] == b[0] for a, b in zip(spans, spans[1:]))
+    pack, box = int(p[PACK]), int(p[BOX])
+    assert group % pack == 0 and box % 16 == 0 and 128 % box == 0 and page % box == 0
+    for r in p[p[O_PITEMS]:p[O_PITEMS] + 8 * p[PITEMS]].reshape(-1, 8):
+        tile, keys, row0, nr, sees, part = (int(x) for x in r[:6])
+        i, per = int(req_of[row0]), 128 // pack
+        assert 1 <= nr <= 2 * per and row0 + nr <= first[i + 1]
+        k0 = keys_ok(i, tile, keys)
+        assert k0 % 128 == 0 and sees == c[i] + row0 - first[i] + 1 - k0 and sees + nr - 1 >= 1
+        assert keys <= sees + nr - 1 and (part < 0 or part + 256 <= p[PPARTS])
+        for j in range(nr):
+            for g in range(group):  # (packed one by one: every head has the item's columns of its own)
+                x = j // per * 128 + j % per * pack + (g if pack == group else 0)
+                keys_of.setdefault((row0 + j, g), []).append((k0, k0 + max(0, min(keys, sees + j))))
+                written.setdefault((row0 + j, g), []).append(("p", part + x) if part >= 0 else None)
     assert len(keys_of) == rows * group
-    joined = set()
-    for r in p[p[O_JOINS]:p[O_JOINS] + 8 * p[JOINS]].reshape(-1, 8):
-        row0, col, parts, part, step, x = (int(v) for v in r[:6])
-        i = int(req_of[row0])
-        assert sorted(written[(i, col)]) == [part + y * step + x for y in range(parts)]
-        joined.add((i, col))
+    for (r, g), spans in keys_of.items():
+        spans = sorted(s for s in spans if s[0] < s[1])
+        assert spans[0][0] == 0 and spans[-1][1] == c[req_of[r]] + r - first[req_of[r]] + 1
+        assert all(a[1] == b[0] for a, b in zip(spans, spans[1:]))
+    joined = {}
+    for kind, off, count, unit in (("c", O_JOINS, JOINS, group), ("p", O_PJOINS, PJOINS, pack)):
+        for r in p[p[off]:p[off] + 8 * p[count]].reshape(-1, 8):
+            row0, col0, cols, parts, part, step, tc = (int(v) for v in r[:7])
+            assert kind == "p" or cols <= p[JOINCOLS]
+            for x in range(256 if kind == "p" else int(p[JOINCOLS])):
+                col = x // 128 * tc + x % 128
+                if x >= step or x % 128 >= tc or col >= cols:
+                    continue
+                for g in range(group // unit):
+                    key = (row0 + (col0 + col) // unit, g * unit + (col0 + col) % unit if unit == group else g)
+                    assert key not in joined
+                    joined[key] = [(kind, part + y * step + x) for y in range(parts)]
     for key, w in written.items():
-        assert (key in joined) == (w[0] is not None) and (w[0] is not None or len(w) == 1)
-    flat = [w for ws in written.values() for w in ws if w is not None]
-    assert len(flat) == len(set(flat))
-    assert native.lib.orca_paged_workspace_bytes(p.ctypes.data) == part_end * kv_heads * (int(p[4]) + 2) * 4
+        assert joined.get(key) == w if w[0] is not None else (len(w) == 1 and key not in joined)
+    if pack == group:
+        flat = [w for ws in written.values() for w in ws if w is not None]
+        assert len(flat) == len(set(flat))
+    assert native.lib.orca_paged_workspace_bytes(p.ctypes.data) == \
+        (int(p[PARTS]) * kv_heads + int(p[PPARTS]) * (group * kv_heads // pack)) * (int(p[4]) + 2) * 4
 
 
-@pytest.mark.parametrize("seed", range(40))
+@pytest.mark.parametrize("seed", range(60))
 def test_plans_cover_every_key_once(native, seed):
     g = np.random.default_rng(seed)
     reqs = int(g.integers(1, 12))
     n = [int(g.choice([0, 1, 1, 1, 2, 7, 33, 200])) for _ in range(reqs)]
     c = [int(g.choice([0, 1, 15, 16, 300, 700, 5000])) for _ in range(reqs)]
     n[0] = max(1, n[0])
-    page, group, kv = int(g.choice([16, 48, 128])), int(g.choice([1, 3, 8, 17, 40])), int(g.choice([1, 4]))
+    page, group, kv = int(g.choice([16, 48, 128])), int(g.choice([1, 3, 8, 17, 40, 70])), int(g.choice([1, 4]))
     need = [-(-(a + b) // page) for a, b in zip(n, c)]
     order, table, at = g.permutation(sum(need)), np.zeros((reqs, max(need)), np.int32), 0
     for i, m in enumerate(need):
