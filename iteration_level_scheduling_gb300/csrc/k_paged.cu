@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <cstring>
 #include <numeric>
+#include <type_traits>
 #include <vector>
 
 #include "common.cuh"
@@ -987,9 +988,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 //   S_t = Q_t K^T   128 x 128, both operands from shared memory
 //   O_t += P_t V    P (bf16) from tensor memory, V as it lies in its pages
 // Tensor memory: S_0, S_1, O_0, O_1, 128 columns each; P_t takes the place of
-// S_t, so that S_t of the next key tile is issued once that P V has completed.
-// In step order the MMA warp issues P V of both tiles, then S of both: with X
-// from S to P, a step takes X + 1.5 of its products' time.  Shared memory:
+// S_t, so that S_t of the next key tile is issued once that P V has completed:
+// with X from S to P, a tile's step takes X and its two products, and the other
+// tile's products fit into X.  Shared memory:
 // Q of both tiles and a ring of key tiles; the loads are boxes of a page (or of
 // the part of it that divides 128 slots), a lane of the TMA warp each.
 // O is rescaled only where a row's maximum grew by more than 2^8, as every P is
@@ -1121,6 +1122,38 @@ __device__ __forceinline__ uint64_t pp_add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// A bounded wait; when it gives up, or another warp has, the abort flag is set and every later wait ends at once.
+__device__ __forceinline__ bool pp_wait(uint64_t *bar, uint32_t parity, unsigned *err, volatile int *abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if ((it & 63u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) {
+            raise_err(err, ERR_WAIT_TIMEOUT);
+            *abort = 1;
+            return false;
+        }
+    }
+}
+// Whether a phase has completed, without waiting for it.
+__device__ __forceinline__ bool pp_test(uint64_t *bar, uint32_t phase) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(phase & 1u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ float pp_max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // One row over keys 0 .. n - 1 of its item by the whole warp: afterwards every
 // lane holds m, l and 8 components of o, lane % (D / 8) * 8 on.
 template <int D>
@@ -1230,14 +1263,13 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         it.n_kt = max(it.nk[0], it.nk[1]);
         return true;
     };
-    const auto wait = [&](uint64_t *b, uint32_t phase) {  // (whole warps)
-        return __all_sync(kFull, !*abort && mbar_wait_bounded(b, phase & 1u, a.err)) != 0;
-    };
+    const auto wait = [&](uint64_t *b, uint32_t phase) { return pp_wait(b, phase & 1u, a.err, abort); };
+    const auto wait_all = [&](uint64_t *b, uint32_t phase) { return __all_sync(kFull, wait(b, phase)) != 0; };
     // Key tiles are numbered g = 0, 1, .. across this block's items (stage g % kStages, its use g / kStages).
 
-    // 384 threads of 168 registers: 4 x 32 of 88 leave 208 for the softmax warps, which hold a row of S
+    // 384 threads of 168 registers: 4 x 32 of 72 leave 216 for the softmax warps, which hold a row of S
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 8) {
             // ------------------------------ TMA ------------------------------
             const uint64_t pol = l2_policy_evict_normal();  // every row tile of the request reads them
@@ -1245,7 +1277,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             bool ok = true;
             Item it;
             for (int k = 0; ok && item_at(k, it); ++k) {
-                if (k >= 1 && !(ok = wait(&bar.q_empty, (uint32_t)(k - 1)))) break;
+                if (k >= 1 && !(ok = wait_all(&bar.q_empty, (uint32_t)(k - 1)))) break;
                 if (lane == 0) {
                     const int tiles = it.n_rows[1] > 0 ? 2 : 1;
                     mbar_arrive_expect_tx(&bar.q_full, (uint32_t)(tiles * L::kAtoms * tile_rows * a.pack * 128));
@@ -1268,13 +1300,13 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                     const int slot = next * 16;
                     if (j + 1 < it.n_kt) next = index(j + 1);
                     const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, slot >= 0)) * a.box * 128);
-                    if (g >= L::kStages && !(ok = wait(&bar.k_empty[s], use - 1))) break;
+                    if (g >= L::kStages && !(ok = wait_all(&bar.k_empty[s], use - 1))) break;
                     if (lane == 0) mbar_arrive_expect_tx(&bar.k_full[s], bytes);
                     __syncwarp();
                     const uint32_t at = (s * L::kAtoms + c) * kPpAtom + (uint32_t)(b * a.box * 128);
                     if (slot >= 0) pp_tma_kv(smem_u32(sm + L::kK + at), &tmkv, &bar.k_full[s], 64 * c, slot, kvh, 0, pol);
                     ++k_used;
-                    if (g >= L::kStages && !(ok = wait(&bar.v_empty[s], use - 1))) break;
+                    if (g >= L::kStages && !(ok = wait_all(&bar.v_empty[s], use - 1))) break;
                     if (lane == 0) mbar_arrive_expect_tx(&bar.v_full[s], bytes);
                     __syncwarp();
                     if (slot >= 0) pp_tma_kv(smem_u32(sm + L::kV + at), &tmkv, &bar.v_full[s], 64 * c, slot, kvh, 1, pol);
@@ -1291,92 +1323,129 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             }
         } else if (warp == 9) {
             // ------------------------------ MMA ------------------------------
-            const uint32_t idesc_s = idesc_bf16_f32(kPpRows, kPpKeys);
-            const uint32_t idesc_pv = idesc_bf16_f32(kPpRows, D) | (1u << 16);  // B (V) MN-major
-            uint32_t n_s[2] = {0, 0}, n_pv[2] = {0, 0};  // products issued
-            bool pending[2] = {false, false}, first[2] = {false, false}, ok = true;
-            uint32_t g = 0;
-            // O_t (+)= P_t V of key tile v; `last`: nothing else reads that stage.  (An item's first P_t is written
-            // after the last item's O_t has been read out.)
-            const auto issue_pv = [&](int t, uint32_t v, bool last) {
-                const uint32_t s = v % L::kStages;
-                if (!wait(&bar.p_full[t], n_pv[t]) || !wait(&bar.v_full[s], v / L::kStages)) return false;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t vs = smem_u32(sm + L::kV + s * L::kAtoms * kPpAtom);
-#pragma unroll
-                    for (int ks = 0; ks < kPpKeys / 16; ++ks)  // 16 keys: two groups of 8 rows of V, 8 columns of P
-                        pp_mma_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * ks, pp_desc_mn(vs + (uint32_t)ks * 2048u),
-                                  idesc_pv, (uint32_t)(!first[t] || ks != 0));
-                    tc_commit(&bar.pv_done[t]);
-                    if (last) tc_commit(&bar.v_empty[s]);
-                }
-                __syncwarp();
-                ++n_pv[t];
-                pending[t] = false;
-                return true;
-            };
-            const auto issue_s = [&](int t, bool k_last, bool q_last) {
-                const uint32_t s = g % L::kStages;
-                if (n_s[t] > 0 && !wait(&bar.pv_done[t], n_s[t] - 1)) return false;  // P_t lies in S_t
-                if (!wait(&bar.k_full[s], g / L::kStages)) return false;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t qs = smem_u32(sm + L::kQ + t * L::kAtoms * kPpAtom);
-                    const uint32_t ks = smem_u32(sm + L::kK + s * L::kAtoms * kPpAtom);
+            // One thread.  Each row tile has a cursor of its own over its key tiles, S and P V in turn; whichever
+            // tile's next product has all that it needs is issued.
+            if (elect_one()) {
+                const uint32_t idesc_s = idesc_bf16_f32(kPpRows, kPpKeys);
+                const uint32_t idesc_pv = idesc_bf16_f32(kPpRows, D) | (1u << 16);  // B (V) MN-major
+                struct Cursor {
+                    Item it;
+                    int k, j;
+                    uint32_t g, n;   // key tile, products of either kind so far
+                    bool pv, live;   // P V is next; there is a next one
+                } cur[2];
+                uint32_t half_k = 0, half_v = 0, half_q = 0;  // stages that one of two tiles is done with
+                const auto seek = [&](Cursor &c, int t) {  // from c.k on, the first item in which tile t sees keys
+                    c.j = 0;
+                    for (;; c.g += c.it.n_kt, ++c.k) {
+                        c.live = item_at(c.k, c.it);
+                        if (!c.live || c.it.nk[t] > 0) return;
+                    }
+                };
+                // Gives a stage back with the last of the products that read it.
+                const auto release = [&](uint32_t &half, uint32_t s, bool both, uint64_t *empty) {
+                    if (both && !(half >> s & 1u)) {
+                        half |= 1u << s;
+                        return;
+                    }
+                    half &= ~(1u << s);
+                    tc_commit(empty);
+                };
+                // Whether all that S_t of the cursor's key tile reads is there.  A phase is asked for only once the one
+                // before it is known to be over: a tile that skips steps in which it sees no keys stays less than a ring
+                // ahead of the other, and an item's keys are loaded behind the last item's Q.
+                const auto s_ready = [&](const Cursor &c, const Cursor &o) {
+                    return c.live && !(o.live && c.g >= o.g + L::kStages) &&
+                           pp_test(&bar.k_full[c.g % L::kStages], c.g / L::kStages) &&
+                           (c.j > 0 || pp_test(&bar.q_full, (uint32_t)c.k));
+                };
+                const auto issue_s = [&](Cursor &c, int t) {
+                    const uint32_t s = c.g % L::kStages;
+                    tc_fence_after();
+                    const uint64_t qd = smem_desc_k128(smem_u32(sm + L::kQ) + t * (L::kAtoms * kPpAtom));
+                    const uint64_t kd = smem_desc_k128(smem_u32(sm + L::kK) + s * (L::kAtoms * kPpAtom));
 #pragma unroll
                     for (int x = 0; x < D / 16; ++x) {  // 16 components: 32 bytes of a 64-component block
-                        const uint32_t o = (uint32_t)(x >> 2) * kPpAtom + (uint32_t)(x & 3) * 32u;
-                        tc_mma_f16(tmem + 128u * t, smem_desc_k128(qs + o), smem_desc_k128(ks + o), idesc_s,
-                                   (uint32_t)(x != 0));
+                        const uint64_t o = ((x >> 2) * kPpAtom + (x & 3) * 32) >> 4;
+                        tc_mma_f16(tmem + 128u * t, qd + o, kd + o, idesc_s, (uint32_t)(x != 0));
                     }
                     tc_commit(&bar.s_full[t]);
-                    if (k_last) tc_commit(&bar.k_empty[s]);
-                    if (q_last) tc_commit(&bar.q_empty);
-                }
-                __syncwarp();
-                ++n_s[t];
-                return true;
-            };
-            Item it;
-            for (int k = 0; ok && item_at(k, it); ++k) {
-                for (int j = 0; ok && j < it.n_kt; ++j, ++g) {
-                    // (both of the last step's P V were issued only if both tiles had that step)
-                    if (pending[0]) ok = issue_pv(0, g - 1, !pending[1]);
-                    if (ok && pending[1]) ok = issue_pv(1, g - 1, true);
-                    if (ok && j == 0) ok = wait(&bar.q_full, (uint32_t)k);
-                    const bool act[2] = {j < it.nk[0], j < it.nk[1]};
-                    const bool q_last = j + 1 == it.n_kt;
-                    if (ok && act[0]) ok = issue_s(0, !act[1], q_last && !act[1]);
-                    if (ok && act[1]) ok = issue_s(1, true, q_last);
+                    release(half_k, s, c.j < c.it.nk[1 - t], &bar.k_empty[s]);
+                    if (c.j + 1 == c.it.nk[t]) release(half_q, 0, c.it.nk[1 - t] > 0, &bar.q_empty);
+                    c.pv = true;
+                };
+                // Issues tile t's next product if it can.  S follows its tile's P V at once, behind it (S_t takes the
+                // place of P_t): with the other tile's P V in between, both softmaxes would run at the same time.
+                const auto step = [&](auto tt) {
+                    constexpr int t = decltype(tt)::value;
+                    Cursor &c = cur[t];
+                    if (!c.live) return false;
+                    if (!c.pv) {
+                        if ((c.n > 0 && !pp_test(&bar.pv_done[t], c.n - 1)) || !s_ready(c, cur[1 - t])) return false;
+                        issue_s(c, t);
+                        return true;
+                    }
+                    const uint32_t s = c.g % L::kStages;
+                    // (an item's first P_t is written after the last item's O_t has been read out)
+                    if (!pp_test(&bar.p_full[t], c.n) || !pp_test(&bar.v_full[s], c.g / L::kStages)) return false;
+                    tc_fence_after();
+                    const uint64_t vd = pp_desc_mn(smem_u32(sm + L::kV) + s * (L::kAtoms * kPpAtom));
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) pending[t] = act[t], first[t] = j == 0;
+                    for (int x = 0; x < kPpKeys / 16; ++x)  // 16 keys: two groups of 8 rows of V, 8 columns of P
+                        pp_mma_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * x, vd + (uint64_t)(x * (2048 >> 4)),
+                                  idesc_pv, (uint32_t)(c.j > 0 || x > 0));
+                    tc_commit(&bar.pv_done[t]);
+                    release(half_v, s, c.j < c.it.nk[1 - t], &bar.v_empty[s]);
+                    c.pv = false;
+                    ++c.n, ++c.g;
+                    if (++c.j == c.it.nk[t]) {
+                        c.g += c.it.n_kt - c.it.nk[t], ++c.k;
+                        seek(c, t);
+                    }
+                    if (s_ready(c, cur[1 - t]) && pp_wait(&bar.pv_done[t], (c.n - 1) & 1u, a.err, abort)) issue_s(c, t);
+                    return true;
+                };
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    cur[t].k = 0, cur[t].g = cur[t].n = 0, cur[t].pv = false;
+                    seek(cur[t], t);
                 }
+                unsigned long long since = 0;
+                for (uint32_t idle = 0; cur[0].live || cur[1].live;) {
+                    const bool x = step(std::integral_constant<int, 0>()), y = step(std::integral_constant<int, 1>());
+                    if (x || y) {
+                        idle = 0;
+                    } else if ((++idle & 255u) == 0) {
+                        if (idle == 256) since = global_timer_ns();
+                        if (*abort || global_timer_ns() - since > kWaitLimitNs) {
+                            raise_err(a.err, ERR_WAIT_TIMEOUT);
+                            *abort = 1;
+                            break;
+                        }
+                    }
+                }
+                // every product issued has completed before stages and tensor memory are given up
+                tc_commit(&bar.drain);
+                mbar_wait_bounded(&bar.drain, 0u, a.err);
             }
-            if (ok && pending[0]) ok = issue_pv(0, g - 1, !pending[1]);
-            if (ok && pending[1]) ok = issue_pv(1, g - 1, true);
-            if (!ok) *abort = 1;
-            // every product issued has completed before stages and tensor memory are given up
-            if (lane == 0) tc_commit(&bar.drain);
             __syncwarp();
-            mbar_wait_bounded(&bar.drain, 0u, a.err);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ------------------------------ softmax ------------------------------
         const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t s_t = tmem + 128u * t + ((uint32_t)(quarter * 32) << 16), o_t = s_t + 256u;
+        // (A wait that gave up sets the abort flag, and the rest runs through on what is there.)
         uint32_t g0 = 0, n = 0;  // the item's first key tile, this tile's key tiles so far
-        bool ok = true;
         Item it;
-        for (int k = 0; ok && item_at(k, it); g0 += it.n_kt, ++k) {
+        for (int k = 0; item_at(k, it); g0 += it.n_kt, ++k) {
             if (it.n_rows[t] == 0) continue;
             const int jr = r / a.pack, sees = it.sees + t * tile_rows + jr;  // keys 0 .. sees - 1 of the item are this row's
             const int first_sees = it.sees + t * tile_rows;
             float m = -INFINITY, l = 0.f;  // (m in the units of S)
             for (int j = 0; j < it.nk[t]; ++j, ++n) {
                 const int kbase = j * kPpKeys;
-                if (!(ok = wait(&bar.s_full[t], n))) break;
+                wait(&bar.s_full[t], n);
                 tc_fence_after();
                 uint32_t s[128];
 #pragma unroll
@@ -1389,59 +1458,75 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                     for (int x = 0; x < 128; ++x)
                         if (x >= valid) s[x] = 0xff800000u;
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                // Weights are formed against the last tile's m while the maximum is taken, and once more in the rare
+                // tile that lifts it by more than 2^8 (the first, and scores where s scale - m in one step would keep
+                // what m lost to rounding: maximum first).
+                bool known = j == 0 || __any_sync(kFull, fabsf(m * a.scale_log2) > 16384.f);
+                float top = -INFINITY, ls;
+                if (known) {
 #pragma unroll
-                for (int x = 0; x < 128; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                float alpha = 1.f;
-                if (j == 0) {
-                    m = top;
-                } else if ((top - m) * a.scale_log2 > kPpRescale) {  // (from no key seen, -inf, as well)
-                    alpha = cw_exp2((m - top) * a.scale_log2);
-                    m = top;
-                    l *= alpha;
+                    for (int x = 0; x < 128; x += 2) top = pp_max3(top, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
                 }
-                if (__any_sync(kFull, alpha != 1.f)) {  // (the item's P V so far are done: S_t was issued behind them)
+                for (;;) {
+                    float neg = -cw_base(m) * a.scale_log2;
+                    if (known) {
+                        float alpha = 1.f;
+                        if (j == 0) {
+                            m = top;
+                        } else if ((top - m) * a.scale_log2 > kPpRescale) {  // (from no key seen, -inf, as well)
+                            alpha = cw_exp2((m - top) * a.scale_log2);
+                            m = top;
+                            l *= alpha;
+                        }
+                        if (__any_sync(kFull, alpha != 1.f)) {  // (the P V so far are done: S_t was issued behind them)
 #pragma unroll
-                    for (int x = 0; x < D; x += 32) {
-                        uint32_t o[32];
-                        pp_ld32(o_t + x, o);
-                        pp_wait_ld32(o);
+                            for (int x = 0; x < D; x += 32) {
+                                uint32_t o[32];
+                                pp_ld32(o_t + x, o);
+                                pp_wait_ld32(o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        pp_st32(o_t + x, o);
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                pp_st32(o_t + x, o);
+                            }
+                        }
+                        neg = -cw_base(m) * a.scale_log2;
+                        if (__any_sync(kFull, fabsf(neg) > 16384.f)) {
+#pragma unroll
+                            for (int x = 0; x < 128; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) - cw_base(m));
+                            neg = 0.f;
+                        }
                     }
-                }
-                float neg = -cw_base(m) * a.scale_log2;
-                if (__any_sync(kFull, fabsf(neg) > 16384.f)) {  // s scale - neg in one step would keep what neg lost
+                    const uint64_t scale2 = pp_pair(a.scale_log2, a.scale_log2), neg2 = pp_pair(neg, neg);
+                    uint64_t sum[2] = {0, 0};
+                    float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int x = 0; x < 128; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) - cw_base(m));
-                    neg = 0.f;
-                }
-                const uint64_t scale2 = pp_pair(a.scale_log2, a.scale_log2), neg2 = pp_pair(neg, neg);
-                uint64_t sum[2] = {0, 0};
+                    for (int x = 0; x < 128; x += 32) {
+                        uint32_t w[16];
 #pragma unroll
-                for (int x = 0; x < 128; x += 32) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float p0, p1;
-                        pp_unpair(pp_fma2(pp_pair(__uint_as_float(s[x + 2 * e]), __uint_as_float(s[x + 2 * e + 1])), scale2,
-                                          neg2),
-                                  p0, p1);
-                        p0 = cw_exp2(p0), p1 = cw_exp2(p1);
-                        sum[e & 1] = pp_add2(sum[e & 1], pp_pair(p0, p1));
-                        w[e] = cw_pack(p0, p1);
+                        for (int e = 0; e < 16; ++e) {
+                            const float s0 = __uint_as_float(s[x + 2 * e]), s1 = __uint_as_float(s[x + 2 * e + 1]);
+                            float p0, p1;
+                            mx[e & 1] = pp_max3(mx[e & 1], s0, s1);
+                            pp_unpair(pp_fma2(pp_pair(s0, s1), scale2, neg2), p0, p1);
+                            p0 = cw_exp2(p0), p1 = cw_exp2(p1);
+                            sum[e & 1] = pp_add2(sum[e & 1], pp_pair(p0, p1));
+                            w[e] = cw_pack(p0, p1);
+                        }
+                        pp_st16(s_t + x / 2, w);
                     }
-                    pp_st16(s_t + x / 2, w);
+                    float l0, l1;
+                    pp_unpair(pp_add2(sum[0], sum[1]), l0, l1);
+                    ls = l0 + l1;
+                    if (known) break;
+                    top = fmaxf(mx[0], mx[1]);
+                    known = __any_sync(kFull, (top - m) * a.scale_log2 > kPpRescale);
+                    if (!known) break;
                 }
-                float l0, l1;
-                pp_unpair(pp_add2(sum[0], sum[1]), l0, l1);
-                l += l0 + l1;
+                l += ls;
                 const int here = it.keys - kbase;  // V rows past the item's last key: zero, once they have landed
                 if (here < kPpKeys) {
                     const uint32_t v = g0 + j, st = v % L::kStages;
-                    if (!(ok = wait(&bar.v_full[st], v / L::kStages))) break;
+                    wait(&bar.v_full[st], v / L::kStages);
                     if (r >= here)
 #pragma unroll
                         for (int x = 0; x < 8 * L::kAtoms; ++x)
@@ -1454,7 +1539,6 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[t]);
             }
-            if (!ok) break;
             // ---- the item's output ----
             const bool mine = r < it.n_rows[t] * a.pack;
             const int row = it.row + t * tile_rows + jr, head = it.vh * a.pack + r % a.pack;
@@ -1462,7 +1546,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             const int64_t at = (int64_t)it.part * a.vheads + (int64_t)it.vh * (2 * kPpRows) + t * kPpRows + r;
             bool bad = false;
             if (it.nk[t] > 0) {
-                if (!(ok = wait(&bar.pv_done[t], n - 1))) break;
+                wait(&bar.pv_done[t], n - 1);
                 tc_fence_after();
                 const float inv = 1.f / l;
 #pragma unroll
@@ -1516,7 +1600,6 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 __syncwarp();
             }
         }
-        if (!ok) *abort = 1;
     }
     tc_fence_before();
     __syncthreads();
