@@ -10,7 +10,6 @@
 #include <algorithm>
 #include <cstring>
 #include <numeric>
-#include <type_traits>
 #include <vector>
 
 #include "common.cuh"
@@ -1000,7 +999,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 // is not finite are computed once more, key by key, over what they see.
 namespace {
 
-constexpr int kPpThreads = 384;  // two softmax warpgroups, one with the TMA and the MMA warp (and two that idle)
+constexpr int kPpThreads = 640;  // four softmax warpgroups, one with the TMA and the MMA warp (and two that idle)
+constexpr int kPpTma = 16, kPpMma = 17;  // warps
 constexpr uint32_t kPpAtom = 16384;  // 128 rows of 128 bytes
 constexpr float kPpRescale = 8.f;
 
@@ -1012,7 +1012,8 @@ struct PpLayout {
     static constexpr uint32_t kK = 2 * kAtoms * kPpAtom;
     static constexpr uint32_t kV = kK + kStages * kAtoms * kPpAtom;
     static constexpr uint32_t kBars = kV + kStages * kAtoms * kPpAtom;
-    static constexpr uint32_t kBytes = kBars + 512;
+    static constexpr uint32_t kRed = kBars + 512;         // [tile][turn][half][row] floats
+    static constexpr uint32_t kBytes = kRed + 2 * 2 * 2 * kPpRows * 4;
 };
 struct PpBars {
     uint64_t q_full, q_empty, k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], pv_done[2];
@@ -1081,17 +1082,6 @@ __device__ __forceinline__ void pp_wait_ld32(uint32_t *r) {
                  :
                  : "memory");
 }
-__device__ __forceinline__ void pp_st32(uint32_t taddr, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-        :
-        : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-          "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-          "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
 __device__ __forceinline__ void pp_st16(uint32_t taddr, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -1125,28 +1115,20 @@ __device__ __forceinline__ uint64_t pp_add2(uint64_t a, uint64_t b) {
 // A bounded wait; when it gives up, or another warp has, the abort flag is set and every later wait ends at once.
 __device__ __forceinline__ bool pp_wait(uint64_t *bar, uint32_t parity, unsigned *err, volatile int *abort) {
     if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_timer_ns();
+    unsigned long long t0 = 0;
     for (uint32_t it = 1;; ++it) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
-        if ((it & 63u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) {
-            raise_err(err, ERR_WAIT_TIMEOUT);
-            *abort = 1;
-            return false;
+        if ((it & 63u) == 0) {
+            const unsigned long long now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) {
+                raise_err(err, ERR_WAIT_TIMEOUT);
+                *abort = 1;
+                return false;
+            }
         }
     }
-}
-// Whether a phase has completed, without waiting for it.
-__device__ __forceinline__ bool pp_test(uint64_t *bar, uint32_t phase) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(phase & 1u)
-        : "memory");
-    return ok != 0;
 }
 __device__ __forceinline__ float pp_max3(float a, float b, float c) {
     float d;
@@ -1157,7 +1139,7 @@ __device__ __forceinline__ float pp_max3(float a, float b, float c) {
 // One row over keys 0 .. n - 1 of its item by the whole warp: afterwards every
 // lane holds m, l and 8 components of o, lane % (D / 8) * 8 on.
 template <int D>
-__device__ void pp_row(const PpArgs &a, const bf16 *q, const int32_t *tiles, int n, int kvh, float &m, float &l, float *o) {
+__device__ __noinline__ void pp_row(const PpArgs &a, const bf16 *q, const int32_t *tiles, int n, int kvh, float &m, float &l, float *o) {
     constexpr int LPT = D / 8, TPW = 32 / LPT;
     const int lane = threadIdx.x & 31, g = lane / LPT, sub = lane % LPT;
     const bf16 *kb = a.layer + (int64_t)kvh * a.slots * D + sub * 8, *vb = kb + (int64_t)a.kv_heads * a.slots * D;
@@ -1223,7 +1205,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bar.s_full[t], 1);
-            mbar_init(&bar.p_full[t], 4);  // an arrival per warp
+            mbar_init(&bar.p_full[t], 8);  // an arrival per warp
             mbar_init(&bar.pv_done[t], 1);
         }
         mbar_init(&bar.drain, 1);
@@ -1232,7 +1214,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         prefetch_tmap(&tmq);
         prefetch_tmap(&tmkv);
     }
-    if (warp == 9) {
+    if (warp == kPpMma) {
         tmem_alloc(&bar.tmem, 512);
         tmem_relinquish();
     }
@@ -1267,10 +1249,10 @@ __global__ void __launch_bounds__(kPpThreads, 1)
     const auto wait_all = [&](uint64_t *b, uint32_t phase) { return __all_sync(kFull, wait(b, phase)) != 0; };
     // Key tiles are numbered g = 0, 1, .. across this block's items (stage g % kStages, its use g / kStages).
 
-    // 384 threads of 168 registers: 4 x 32 of 72 leave 216 for the softmax warps, which hold a row of S
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 8) {
+    // 640 threads of 96 registers: 4 x 32 of 64 leave 104 for the softmax warps, which hold half a row of S
+    if (warp >= kPpTma) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == kPpTma) {
             // ------------------------------ TMA ------------------------------
             const uint64_t pol = l2_policy_evict_normal();  // every row tile of the request reads them
             uint32_t g = 0, q_used = 0, k_used = 0, v_used = 0;
@@ -1321,109 +1303,69 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 for (uint32_t x = v_used > L::kStages ? v_used - L::kStages : 0; x < v_used; ++x)
                     mbar_wait_bounded(&bar.v_full[x % L::kStages], (x / L::kStages) & 1u, a.err);
             }
-        } else if (warp == 9) {
+        } else if (warp == kPpMma) {
             // ------------------------------ MMA ------------------------------
-            // One thread.  Each row tile has a cursor of its own over its key tiles, S and P V in turn; whichever
-            // tile's next product has all that it needs is issued.
+            // One thread, in small loops: with the products unrolled and the row tiles polled, its own instructions
+            // (fetched anew every time between those of the other warps) took 2100 cycles of a tile's step.  The tiles
+            // in turn, S behind its own P V, so that one softmax runs beside the other's products.
             if (elect_one()) {
                 const uint32_t idesc_s = idesc_bf16_f32(kPpRows, kPpKeys);
                 const uint32_t idesc_pv = idesc_bf16_f32(kPpRows, D) | (1u << 16);  // B (V) MN-major
-                struct Cursor {
-                    Item it;
-                    int k, j;
-                    uint32_t g, n;   // key tile, products of either kind so far
-                    bool pv, live;   // P V is next; there is a next one
-                } cur[2];
-                uint32_t half_k = 0, half_v = 0, half_q = 0;  // stages that one of two tiles is done with
-                const auto seek = [&](Cursor &c, int t) {  // from c.k on, the first item in which tile t sees keys
-                    c.j = 0;
-                    for (;; c.g += c.it.n_kt, ++c.k) {
-                        c.live = item_at(c.k, c.it);
-                        if (!c.live || c.it.nk[t] > 0) return;
+                uint32_t g = 0, par_s = 0, par_pv = 0, pending = 0;  // (bits by row tile: parities, P V to come)
+                bool ok = true, first = false;                       // first: the pending P V begin their item
+                // The last step's P V of tile t, then, if `s_too`, S of key tile g.
+                const auto issue = [&](uint32_t t, bool s_too, bool k_last, bool q_last) {
+                    if (pending >> t & 1u) {
+                        const uint32_t v = g - 1, st = v % L::kStages;
+                        if (!wait(&bar.p_full[t], par_pv >> t) || !wait(&bar.v_full[st], v / L::kStages)) return false;
+                        tc_fence_after();
+                        uint64_t vd = pp_desc_mn(smem_u32(sm + L::kV) + st * (L::kAtoms * kPpAtom));
+                        uint32_t pt = tmem + 128u * t;
+#pragma unroll 1
+                        for (uint32_t x = 0; x < kPpKeys / 16; ++x) {  // 16 keys: two groups of 8 rows of V, 8 columns of P
+                            pp_mma_ts(tmem + 256u + 128u * t, pt, vd, idesc_pv, (uint32_t)!first | x);
+                            vd += 2048 >> 4, pt += x == 3 ? 64u - 24u : 8u;
+                        }
+                        tc_commit(&bar.pv_done[t]);
+                        if (t == 1 || !(pending & 2u)) tc_commit(&bar.v_empty[st]);
+                        par_pv ^= 1u << t;
                     }
-                };
-                // Gives a stage back with the last of the products that read it.
-                const auto release = [&](uint32_t &half, uint32_t s, bool both, uint64_t *empty) {
-                    if (both && !(half >> s & 1u)) {
-                        half |= 1u << s;
-                        return;
-                    }
-                    half &= ~(1u << s);
-                    tc_commit(empty);
-                };
-                // Whether all that S_t of the cursor's key tile reads is there.  A phase is asked for only once the one
-                // before it is known to be over: a tile that skips steps in which it sees no keys stays less than a ring
-                // ahead of the other, and an item's keys are loaded behind the last item's Q.
-                const auto s_ready = [&](const Cursor &c, const Cursor &o) {
-                    return c.live && !(o.live && c.g >= o.g + L::kStages) &&
-                           pp_test(&bar.k_full[c.g % L::kStages], c.g / L::kStages) &&
-                           (c.j > 0 || pp_test(&bar.q_full, (uint32_t)c.k));
-                };
-                const auto issue_s = [&](Cursor &c, int t) {
-                    const uint32_t s = c.g % L::kStages;
+                    if (!s_too) return true;
+                    const uint32_t st = g % L::kStages;
+                    if (!wait(&bar.k_full[st], g / L::kStages)) return false;
+                    // S_t takes the place of P_t: behind the P V that read it (parity of the one before: none yet, passes)
+                    if (!wait(&bar.pv_done[t], (par_s >> t & 1u) ^ 1u)) return false;
                     tc_fence_after();
-                    const uint64_t qd = smem_desc_k128(smem_u32(sm + L::kQ) + t * (L::kAtoms * kPpAtom));
-                    const uint64_t kd = smem_desc_k128(smem_u32(sm + L::kK) + s * (L::kAtoms * kPpAtom));
-#pragma unroll
-                    for (int x = 0; x < D / 16; ++x) {  // 16 components: 32 bytes of a 64-component block
-                        const uint64_t o = ((x >> 2) * kPpAtom + (x & 3) * 32) >> 4;
-                        tc_mma_f16(tmem + 128u * t, qd + o, kd + o, idesc_s, (uint32_t)(x != 0));
+                    uint64_t qd = smem_desc_k128(smem_u32(sm + L::kQ) + t * (L::kAtoms * kPpAtom));
+                    uint64_t kd = smem_desc_k128(smem_u32(sm + L::kK) + st * (L::kAtoms * kPpAtom));
+#pragma unroll 1
+                    for (uint32_t x = 0; x < D / 16; ++x) {  // 16 components: 32 bytes of a 64-component block
+                        tc_mma_f16(tmem + 128u * t, qd, kd, idesc_s, x);
+                        const uint32_t o = (x & 3u) == 3u ? (kPpAtom - 96u) >> 4 : 32u >> 4;
+                        qd += o, kd += o;
                     }
                     tc_commit(&bar.s_full[t]);
-                    release(half_k, s, c.j < c.it.nk[1 - t], &bar.k_empty[s]);
-                    if (c.j + 1 == c.it.nk[t]) release(half_q, 0, c.it.nk[1 - t] > 0, &bar.q_empty);
-                    c.pv = true;
-                };
-                // Issues tile t's next product if it can.  S follows its tile's P V at once, behind it (S_t takes the
-                // place of P_t): with the other tile's P V in between, both softmaxes would run at the same time.
-                const auto step = [&](auto tt) {
-                    constexpr int t = decltype(tt)::value;
-                    Cursor &c = cur[t];
-                    if (!c.live) return false;
-                    if (!c.pv) {
-                        if ((c.n > 0 && !pp_test(&bar.pv_done[t], c.n - 1)) || !s_ready(c, cur[1 - t])) return false;
-                        issue_s(c, t);
-                        return true;
-                    }
-                    const uint32_t s = c.g % L::kStages;
-                    // (an item's first P_t is written after the last item's O_t has been read out)
-                    if (!pp_test(&bar.p_full[t], c.n) || !pp_test(&bar.v_full[s], c.g / L::kStages)) return false;
-                    tc_fence_after();
-                    const uint64_t vd = pp_desc_mn(smem_u32(sm + L::kV) + s * (L::kAtoms * kPpAtom));
-#pragma unroll
-                    for (int x = 0; x < kPpKeys / 16; ++x)  // 16 keys: two groups of 8 rows of V, 8 columns of P
-                        pp_mma_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * x, vd + (uint64_t)(x * (2048 >> 4)),
-                                  idesc_pv, (uint32_t)(c.j > 0 || x > 0));
-                    tc_commit(&bar.pv_done[t]);
-                    release(half_v, s, c.j < c.it.nk[1 - t], &bar.v_empty[s]);
-                    c.pv = false;
-                    ++c.n, ++c.g;
-                    if (++c.j == c.it.nk[t]) {
-                        c.g += c.it.n_kt - c.it.nk[t], ++c.k;
-                        seek(c, t);
-                    }
-                    if (s_ready(c, cur[1 - t]) && pp_wait(&bar.pv_done[t], (c.n - 1) & 1u, a.err, abort)) issue_s(c, t);
+                    if (k_last) tc_commit(&bar.k_empty[st]);
+                    if (q_last) tc_commit(&bar.q_empty);
+                    par_s ^= 1u << t;
                     return true;
                 };
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    cur[t].k = 0, cur[t].g = cur[t].n = 0, cur[t].pv = false;
-                    seek(cur[t], t);
-                }
-                unsigned long long since = 0;
-                for (uint32_t idle = 0; cur[0].live || cur[1].live;) {
-                    const bool x = step(std::integral_constant<int, 0>()), y = step(std::integral_constant<int, 1>());
-                    if (x || y) {
-                        idle = 0;
-                    } else if ((++idle & 255u) == 0) {
-                        if (idle == 256) since = global_timer_ns();
-                        if (*abort || global_timer_ns() - since > kWaitLimitNs) {
-                            raise_err(a.err, ERR_WAIT_TIMEOUT);
-                            *abort = 1;
-                            break;
+                Item it;
+                for (int k = 0; ok && item_at(k, it); ++k) {
+                    ok = wait(&bar.q_full, (uint32_t)k);
+                    for (int j = 0; ok && j < it.n_kt; ++j, ++g) {
+                        const uint32_t act = (j < it.nk[0] ? 1u : 0u) | (j < it.nk[1] ? 2u : 0u);
+#pragma unroll 1
+                        for (uint32_t t = 0; ok && t < 2; ++t) {
+                            const bool last = t == 1 || !(act & 2u);
+                            ok = issue(t, act >> t & 1u, last, last && j + 1 == it.n_kt);
                         }
+                        pending = act, first = j == 0;
                     }
                 }
+#pragma unroll 1
+                for (uint32_t t = 0; ok && t < 2; ++t) ok = issue(t, false, false, false);
+                if (!ok) *abort = 1;
                 // every product issued has completed before stages and tensor memory are given up
                 tc_commit(&bar.drain);
                 mbar_wait_bounded(&bar.drain, 0u, a.err);
@@ -1431,41 +1373,61 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         // ------------------------------ softmax ------------------------------
-        const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-        const uint32_t s_t = tmem + 128u * t + ((uint32_t)(quarter * 32) << 16), o_t = s_t + 256u;
+        // Two threads per row, 64 keys of a tile (and half of O's components) each: with one thread per row
+        // the chain from S to P took 1980 cycles of a step's 4020, most of it latency of few warps.  P of either
+        // half lies over that half's own columns of S.
         // (A wait that gave up sets the abort flag, and the rest runs through on what is there.)
-        uint32_t g0 = 0, n = 0;  // the item's first key tile, this tile's key tiles so far
+        const int t = warp >> 3, half = warp >> 2 & 1, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lane_t = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t s_t = lane_t + 128u * t + 64u * half, o_t = lane_t + 256u + 128u * t + (uint32_t)(D / 2 * half);
+        constexpr int DH = D / 2;
+        float *const red = reinterpret_cast<float *>(sm + L::kRed) + t * (4 * kPpRows) + r;
+        uint32_t turn = 0;
+        // The other half's value.  Slots of one parity are written again two turns later, when the other half has
+        // read them (it does so before it comes to the turn between).
+        const auto exchange = [&](float v) {
+            red[((turn & 1u) * 2 + half) * kPpRows] = v;
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + t * 4 + quarter) : "memory");
+            v = red[((turn & 1u) * 2 + (half ^ 1)) * kPpRows];
+            ++turn;
+            return v;
+        };
+        uint32_t g0 = 0, n = 0;  // the item's first key tile, this row tile's key tiles so far
         Item it;
         for (int k = 0; item_at(k, it); g0 += it.n_kt, ++k) {
-            if (it.n_rows[t] == 0) continue;
+            const int n_rows = t ? it.n_rows[1] : it.n_rows[0], nk = t ? it.nk[1] : it.nk[0];
+            if (n_rows == 0) continue;
             const int jr = r / a.pack, sees = it.sees + t * tile_rows + jr;  // keys 0 .. sees - 1 of the item are this row's
             const int first_sees = it.sees + t * tile_rows;
-            float m = -INFINITY, l = 0.f;  // (m in the units of S)
-            for (int j = 0; j < it.nk[t]; ++j, ++n) {
+            float m = -INFINITY, l = 0.f;  // (m in the units of S; l of this half)
+            for (int j = 0; j < nk; ++j, ++n) {
                 const int kbase = j * kPpKeys;
                 wait(&bar.s_full[t], n);
                 tc_fence_after();
-                uint32_t s[128];
-#pragma unroll
-                for (int x = 0; x < 128; x += 32) pp_ld32(s_t + x, s + x);
-#pragma unroll
-                for (int x = 0; x < 128; x += 32) pp_wait_ld32(s + x);
+                uint32_t s[64];
+                pp_ld32(s_t, s);
+                pp_ld32(s_t + 32, s + 32);
+                pp_wait_ld32(s);
+                pp_wait_ld32(s + 32);
                 if (kbase + kPpKeys > first_sees || kbase + kPpKeys > it.keys) {
-                    const int valid = min(sees, it.keys) - kbase;
+                    const int valid = min(sees, it.keys) - kbase - 64 * half;
+                    if (!__all_sync(kFull, valid >= 64)) {
 #pragma unroll
-                    for (int x = 0; x < 128; ++x)
-                        if (x >= valid) s[x] = 0xff800000u;
+                        for (int x = 0; x < 64; ++x)
+                            if (x >= valid) s[x] = 0xff800000u;
+                    }
                 }
                 // Weights are formed against the last tile's m while the maximum is taken, and once more in the rare
                 // tile that lifts it by more than 2^8 (the first, and scores where s scale - m in one step would keep
-                // what m lost to rounding: maximum first).
+                // what m lost to rounding: maximum first).  Both halves come to the same decisions.
                 bool known = j == 0 || __any_sync(kFull, fabsf(m * a.scale_log2) > 16384.f);
                 float top = -INFINITY, ls;
                 if (known) {
 #pragma unroll
-                    for (int x = 0; x < 128; x += 2) top = pp_max3(top, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+                    for (int x = 0; x < 64; x += 2) top = pp_max3(top, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+                    top = fmaxf(top, exchange(top));
                 }
                 for (;;) {
                     float neg = -cw_base(m) * a.scale_log2;
@@ -1479,20 +1441,20 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                             l *= alpha;
                         }
                         if (__any_sync(kFull, alpha != 1.f)) {  // (the P V so far are done: S_t was issued behind them)
+#pragma unroll 1
+                            for (int x = 0; x < DH; x += 16) {
+                                float o[16];
+                                tmem_ld16(o_t + x, o);
+                                uint32_t w[16];
 #pragma unroll
-                            for (int x = 0; x < D; x += 32) {
-                                uint32_t o[32];
-                                pp_ld32(o_t + x, o);
-                                pp_wait_ld32(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                pp_st32(o_t + x, o);
+                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+                                pp_st16(o_t + x, w);
                             }
                         }
                         neg = -cw_base(m) * a.scale_log2;
                         if (__any_sync(kFull, fabsf(neg) > 16384.f)) {
 #pragma unroll
-                            for (int x = 0; x < 128; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) - cw_base(m));
+                            for (int x = 0; x < 64; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) - cw_base(m));
                             neg = 0.f;
                         }
                     }
@@ -1500,7 +1462,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                     uint64_t sum[2] = {0, 0};
                     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int x = 0; x < 128; x += 32) {
+                    for (int x = 0; x < 64; x += 32) {
                         uint32_t w[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
@@ -1519,6 +1481,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                     ls = l0 + l1;
                     if (known) break;
                     top = fmaxf(mx[0], mx[1]);
+                    top = fmaxf(top, exchange(top));
                     known = __any_sync(kFull, (top - m) * a.scale_log2 > kPpRescale);
                     if (!known) break;
                 }
@@ -1527,11 +1490,11 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 if (here < kPpKeys) {
                     const uint32_t v = g0 + j, st = v % L::kStages;
                     wait(&bar.v_full[st], v / L::kStages);
-                    if (r >= here)
+                    if (r >= here && half < L::kAtoms)
 #pragma unroll
-                        for (int x = 0; x < 8 * L::kAtoms; ++x)
-                            *reinterpret_cast<uint4 *>(sm + L::kV + (st * L::kAtoms + x / 8) * kPpAtom + r * 128 +
-                                                       x % 8 * 16) = make_uint4(0, 0, 0, 0);
+                        for (int x = 0; x < 8; ++x)
+                            *reinterpret_cast<uint4 *>(sm + L::kV + (st * L::kAtoms + half) * kPpAtom + r * 128 + x * 16) =
+                                make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
                 pp_wait_st();
@@ -1540,17 +1503,19 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 if (lane == 0) mbar_arrive(&bar.p_full[t]);
             }
             // ---- the item's output ----
-            const bool mine = r < it.n_rows[t] * a.pack;
+            const bool mine = r < n_rows * a.pack;
             const int row = it.row + t * tile_rows + jr, head = it.vh * a.pack + r % a.pack;
-            bf16 *const dst = a.out + (int64_t)row * a.ld_out + (int64_t)head * D;
+            bf16 *const dst = a.out + (int64_t)row * a.ld_out + (int64_t)head * D + DH * half;
             const int64_t at = (int64_t)it.part * a.vheads + (int64_t)it.vh * (2 * kPpRows) + t * kPpRows + r;
+            float *const part = a.part + at * D + DH * half;
             bool bad = false;
-            if (it.nk[t] > 0) {
+            l += exchange(l);
+            if (nk > 0) {
                 wait(&bar.pv_done[t], n - 1);
                 tc_fence_after();
                 const float inv = 1.f / l;
 #pragma unroll
-                for (int x = 0; x < D; x += 32) {
+                for (int x = 0; x < DH; x += 32) {
                     uint32_t o[32];
                     pp_ld32(o_t + x, o);
                     pp_wait_ld32(o);
@@ -1568,18 +1533,20 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4 *>(a.part + at * D + x + e) =
-                                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            *reinterpret_cast<uint4 *>(part + x + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                 }
                 tc_fence_before();
             } else if (mine) {  // a part of the keys of which this tile sees none
-                for (int x = 0; x < D; x += 4) *reinterpret_cast<uint4 *>(a.part + at * D + x) = make_uint4(0, 0, 0, 0);
+                for (int x = 0; x < DH; x += 4) *reinterpret_cast<uint4 *>(part + x) = make_uint4(0, 0, 0, 0);
             }
-            if (mine && it.part >= 0) *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m * a.scale_log2, l);
-            unsigned todo = __ballot_sync(kFull, mine && (bad || l != l));
+            if (mine && it.part >= 0 && half == 0)
+                *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m * a.scale_log2, l);
+            bad = mine && (bad || l != l);
+            bad |= exchange(bad ? 1.f : 0.f) != 0.f;  // (behind it, both halves' writes are done)
+            unsigned todo = half ? 0u : __ballot_sync(kFull, bad);
             for (; todo; todo &= todo - 1) {  // rows with something that is not finite, over what they see
-                const int x = __ffs(todo) - 1, rr = quarter * 32 + x;
+                const int rr = quarter * 32 + __ffs(todo) - 1;
                 const int row2 = it.row + t * tile_rows + rr / a.pack, head2 = it.vh * a.pack + rr % a.pack;
                 const int seen = min(it.sees + t * tile_rows + rr / a.pack, it.keys);
                 float m2, l2, o2[8];
@@ -1603,7 +1570,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kPpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }

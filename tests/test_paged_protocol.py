@@ -14,7 +14,7 @@ def prompt_cta(items, stages, rnd, skip=None):
     """items: (key tiles of row tile 0, of row tile 1, whether tile 1 has rows).  skip: a wait that is left out (planted)."""
     q_full, q_empty, drain = Bar("q_full", 1), Bar("q_empty", 1), Bar("drain", 1)
     kf, ke, vf, ve = ([Bar(f"{x}{s}", 1) for s in range(stages)] for x in ("k_full", "k_empty", "v_full", "v_empty"))
-    sf, pf, pv = ([Bar(f"{x}{t}", c) for t in range(2)] for x, c in (("s_full", 1), ("p_full", 4), ("pv_done", 1)))
+    sf, pf, pv = ([Bar(f"{x}{t}", c) for t in range(2)] for x, c in (("s_full", 1), ("p_full", 8), ("pv_done", 1)))
     pending, tensor = [], []
     held_q = [None]
     held_k, held_v = [None] * stages, [None] * stages  # key tile that each stage holds
@@ -41,7 +41,7 @@ def prompt_cta(items, stages, rnd, skip=None):
             for b in tensor.pop(0)["bars"]:
                 b.arrive()
 
-    def issue(acc, effect, bars):
+    def issue_op(acc, effect, bars):
         tensor.append(dict(acc=acc, effect=effect, bars=bars, done=False))
         pending.append(complete_tensor)
 
@@ -71,67 +71,60 @@ def prompt_cta(items, stages, rnd, skip=None):
                     yield
                 g += 1
 
-    half = dict(k=set(), v=set(), q=set())  # stages that one of two row tiles is done with
-    at_g = [0, 0]         # the cursors' key tiles (None: done)
+    def mma():
+        g = 0
+        par_s, par_pv = [0, 0], [0, 0]  # products of either kind so far
+        todo = [None, None]
 
-    def release(which, x, both, bar):
-        """The barriers on which the product's commit arrives."""
-        if both and x not in half[which]:
-            half[which].add(x)
-            return []
-        half[which].discard(x)
-        return [bar]
+        def issue(t, k, j, act, q_last):
+            if todo[t]:
+                pk, pj, v = todo[t]
+                s = v % stages
+                yield from waits(pf[t], par_pv[t], "p_full")
+                yield from waits(vf[s], v // stages, "v_full")
 
-    def mma(t):
-        """One of the two cursors of the MMA thread (which asks them in turn)."""
-        g = n = 0
-        for k, item in enumerate(items):
-            nk, other = item[t], item[1 - t]
-            for j in range(nk):
-                s, both = g % stages, j < other
-                at_g[t] = g
-                while at_g[1 - t] is not None and g >= at_g[1 - t] + stages and skip != "lead":
-                    yield
-                if n > 0:
-                    yield from waits(pv[t], n - 1, "pv_done")
-                yield from waits(kf[s], g // stages, "k_full")
-                if j == 0:
-                    yield from waits(q_full, k, "q_full")
-
-                def effect(g=g, s=s, k=k, j=j):
-                    assert s_of[t] is None, ("S overwrites", s_of[t])
-                    assert held_q[0] == k and held_k[s] == g, "Q or K is not there"
-                    s_of[t] = ("s", k, j)
-
-                bars = [sf[t]] + release("k", s, both, ke[s])
-                if j + 1 == nk:
-                    bars += release("q", 0, other > 0, q_empty)
-                issue(("s", t), effect, bars)
-                yield
-                yield from waits(pf[t], n, "p_full")
-                yield from waits(vf[s], g // stages, "v_full")
-
-                def effect(g=g, s=s, k=k, j=j):
-                    assert s_of[t] == ("p", k, j), ("P V of another tile", s_of[t], k, j)
-                    assert held_v[s] == g, "V is not there"
-                    if j == 0:
+                def effect(s=s):
+                    assert s_of[t] == ("p", pk, pj), ("P V of another tile", s_of[t], pk, pj)
+                    assert held_v[s] == v, "V is not there"
+                    if pj == 0:
                         assert o_of[t] is None or o_of[t][0] in o_read[t], "O overwritten before it was read"
-                        o_of[t] = (k, 0)
-                    assert o_of[t] == (k, j)
-                    o_of[t] = (k, j + 1)
+                        o_of[t] = (pk, 0)
+                    assert o_of[t] == (pk, pj)
+                    o_of[t] = (pk, pj + 1)
                     s_of[t] = None
 
-                issue(("o", t), effect, [pv[t]] + release("v", s, both, ve[s]))
+                issue_op(("o", t), effect, [pv[t]] + ([ve[s]] if t == 1 or not todo[1] else []))
+                par_pv[t] += 1
                 yield
-                n += 1
+            if not act[t]:
+                return
+            s = g % stages
+            yield from waits(kf[s], g // stages, "k_full")
+            if par_s[t]:
+                yield from waits(pv[t], par_s[t] - 1, "pv_done")
+
+            def effect(g=g, s=s):
+                assert s_of[t] is None, ("S overwrites", s_of[t])
+                assert held_q[0] == k and held_k[s] == g, "Q or K is not there"
+                s_of[t] = ("s", k, j)
+
+            last = t == 1 or not act[1]
+            issue_op(("s", t), effect, [sf[t]] + ([ke[s]] if last else []) + ([q_empty] if last and q_last else []))
+            par_s[t] += 1
+            yield
+
+        for k, (n0, n1, _) in enumerate(items):
+            yield from waits(q_full, k, "q_full")
+            for j in range(max(n0, n1)):
+                act = (j < n0, j < n1)
+                for t in range(2):
+                    yield from issue(t, k, j, act, j + 1 == max(n0, n1))
+                todo = [(k, j, g) if act[t] else None for t in range(2)]
                 g += 1
-            g += max(0, other - nk)
-            # (the next item in which this tile sees keys is where the cursor stands)
-            at_g[t] = g
-        at_g[t] = None
-        if at_g == [None, None]:
-            issue("end", lambda: None, [drain])
-            yield from waits(drain, 0)
+        for t in range(2):
+            yield from issue(t, 0, 0, (False, False), False)
+        issue_op("end", lambda: None, [drain])
+        yield from waits(drain, 0)
 
     def softmax(t):
         g0 = n = 0
@@ -149,7 +142,7 @@ def prompt_cta(items, stages, rnd, skip=None):
                         yield from waits(vf[v % stages], v // stages)
                         assert held_v[v % stages] == v
                     s_of[t] = ("p", k, j)
-                    pf[t].arrive(4)
+                    pf[t].arrive(8)
                     yield
                     n += 1
                 if nk:
@@ -160,7 +153,7 @@ def prompt_cta(items, stages, rnd, skip=None):
                     o_read[t].add(k)
             g0 += max(n0, n1)
 
-    run_agents([producer(), mma(0), mma(1), softmax(0), softmax(1)], pending, rnd)
+    run_agents([producer(), mma(), softmax(0), softmax(1)], pending, rnd)
     assert out == [{k: i[t] for k, i in enumerate(items) if i[t]} for t in range(2)]
 
 
@@ -183,7 +176,7 @@ def test_prompt_protocol(seed, stages):
 
 
 @pytest.mark.parametrize("skip", ["q_empty", "k_empty", "v_empty", "p_full", "v_full", "pv_done", "k_full", "q_full",
-                                  "s_full", "pv_last", "lead"])
+                                  "s_full", "pv_last"])
 def test_a_wait_left_out_is_found(skip):
     found = 0
     for seed in range(200):
