@@ -35,7 +35,7 @@ enum {  // header words of a plan
     G_TOTAL,
     G_O_ROWS,   // per row: slot, position, request, 0
     G_O_REQS,   // per request with rows: its first tile
-    G_O_TILES,  // slot / 16 of every 16 positions
+    G_O_TILES,  // slot / 16 of every 16 positions (each request at a multiple of four)
     G_SMS,
     G_ITEMS,                       // work items by class (8, 16, 32 columns)
     G_PARTS = G_ITEMS + kClasses,  // partial columns of split items (per key/value head)
@@ -62,9 +62,10 @@ struct PagedSizes {
     int64_t off_rows, off_reqs, off_tiles, off_items, off_joins, off_pitems, off_pjoins, total;
 };
 
-// Prompts: rows x heads of one key/value head as the 128 rows of a tensor-core tile; two tiles share their keys.
+// Prompts: rows x heads of one key/value head as the 128 rows of a tensor-core tile; two tiles share their keys, 64 at
+// a time.
 constexpr int kPromptCols = 32;  // columns of a request from which on it is one
-constexpr int kPpRows = 128, kPpKeys = 128;
+constexpr int kPpRows = 128, kPpKeys = 64;
 bool is_prompt(const PagedBatch &b, int i) {
     return b.dtype && b.head_dim >= 64 && (int64_t)b.n_input[i] * (b.n_heads / b.n_kv_heads) > kPromptCols;
 }
@@ -114,14 +115,14 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
             row_pairs(b, i, [&](int64_t, int64_t, int64_t keys) { pwork += (keys + kPpKeys - 1) / kPpKeys * vheads; });
         else
             column_tiles(b, i, [&](int, int64_t, int64_t, int64_t keys) { work += keys * b.n_kv_heads; });
-        z->tiles += (c + n + 15) / 16;
+        z->tiles += up4((c + n + 15) / 16);
         z->maxpos = std::max(z->maxpos, c + n);
     }
     // a third of a block's share, so that uneven items even out over the blocks
     const int64_t share = work / ((int64_t)kCwCtasPerSm * num_sms * 3);
     z->chunk = std::max<int64_t>(kSplitAt, (share + 63) / 64 * 64);
     // half of a block's share of key tiles, eight at least
-    z->pchunk = std::max<int64_t>(8, pwork / num_sms / 2) * kPpKeys;
+    z->pchunk = std::max<int64_t>(16, pwork / num_sms / 2) * kPpKeys;
     for (int i = 0; i < b.n_req; ++i) {
         if (b.n_input[i] == 0) continue;
         if (is_prompt(b, i)) {
@@ -205,6 +206,7 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
         for (int64_t at = 0; at < c + n; at += 16)
             *tile++ = t[at / b.page_size] * per_page + (int32_t)(at % b.page_size) / 16;
         const int32_t *mine = buf + req[i];
+        tile = buf + up4(tile - buf);
         for (int64_t j = 0; j < n; ++j, row += 4) {
             const int64_t pos = c + j;
             row[0] = mine[pos / 16] * 16 + (int32_t)(pos % 16);
@@ -982,16 +984,19 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 // The rows of a tile are (row, head) pairs of one key/value head, heads
 // innermost, 128 / pack rows of a request: every key tile is loaded once for all
 // heads that share it, and short chunks of prompts still fill tiles.  An item is
-// two such tiles, t = 0 and 1, over one range of keys; each has a warpgroup of its own (a
-// thread per tile row), and while one's softmax runs the other's products do.
-//   S_t = Q_t K^T   128 x 128, both operands from shared memory
+// two such tiles, t = 0 and 1, over one range of keys, 64 at a time; each has a
+// warpgroup of its own, a thread per tile row.
+//   S_t = Q_t K^T   128 x 64, both operands from shared memory
 //   O_t += P_t V    P (bf16) from tensor memory, V as it lies in its pages
-// Tensor memory: S_0, S_1, O_0, O_1, 128 columns each; P_t takes the place of
-// S_t, so that S_t of the next key tile is issued once that P V has completed:
-// with X from S to P, a tile's step takes X and its two products, and the other
-// tile's products fit into X.  Shared memory:
-// Q of both tiles and a ring of key tiles; the loads are boxes of a page (or of
-// the part of it that divides 128 slots), a lane of the TMA warp each.
+// Tensor memory: two buffers of S per tile (64 columns each; P takes the first
+// half of its S), O_0, O_1 (128 each).  The chain from S over the softmax to P
+// V and back has some 2400 cycles of latency beside its work (products, commits,
+// waits, tensor-memory accesses; measured with that work left out), so the
+// next S is always under way: a softmax finds it when it is done with the last.
+// With one buffer of 128 keys the same work took 4400 cycles per 128 keys of both
+// tiles.  Shared memory: Q of two items and a ring of key tiles; the loads are
+// boxes of a page (or of the part of it that divides 64 slots), a lane of the
+// TMA warp each.
 // O is rescaled only where a row's maximum grew by more than 2^8, as every P is
 // formed against the maximum that O and l carry.
 // Keys past the item's last are masked by index and their V rows zeroed.  A
@@ -999,25 +1004,27 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 // is not finite are computed once more, key by key, over what they see.
 namespace {
 
-constexpr int kPpThreads = 640;  // four softmax warpgroups, one with the TMA and the MMA warp (and two that idle)
-constexpr int kPpTma = 16, kPpMma = 17;  // warps
-constexpr uint32_t kPpAtom = 16384;  // 128 rows of 128 bytes
+constexpr int kPpThreads = 384;  // two softmax warpgroups, one with the TMA and the MMA warps (and one that idles)
+constexpr int kPpTma = 8, kPpMma = 9;  // warps: the second MMA warp follows the first
+constexpr uint32_t kPpAtom = 16384;    // 128 rows of 128 bytes (Q)
+constexpr uint32_t kPpKv = 8192;       // 64 rows of 128 bytes (K, V)
 constexpr float kPpRescale = 8.f;
 
 template <int D>
 struct PpLayout {
     static constexpr int kAtoms = D / 64;
-    static constexpr int kStages = D == 64 ? 4 : 2;
-    static constexpr uint32_t kQ = 0;  // [tile][atom]
-    static constexpr uint32_t kK = 2 * kAtoms * kPpAtom;
-    static constexpr uint32_t kV = kK + kStages * kAtoms * kPpAtom;
-    static constexpr uint32_t kBars = kV + kStages * kAtoms * kPpAtom;
-    static constexpr uint32_t kRed = kBars + 512;         // [tile][turn][half][row] floats
-    static constexpr uint32_t kBytes = kRed + 2 * 2 * 2 * kPpRows * 4;
+    static constexpr int kStages = D == 64 ? 6 : 3;
+    static constexpr uint32_t kTile = kAtoms * kPpKv;  // a key tile's K or V
+    static constexpr uint32_t kQ = 0;                  // [item's parity][tile][atom]
+    static constexpr uint32_t kK = 4 * kAtoms * kPpAtom;
+    static constexpr uint32_t kV = kK + kStages * kTile;
+    static constexpr uint32_t kBars = kV + kStages * kTile;
+    static constexpr uint32_t kBytes = kBars + 512;
 };
 struct PpBars {
-    uint64_t q_full, q_empty, k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], pv_done[2];
-    uint64_t drain;
+    uint64_t q_full[2], q_empty[2], k_full[6], k_empty[6], v_full[6], v_empty[6];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [tile][buffer]
+    uint64_t drain[2];
     uint32_t tmem;
     int abort;
 };
@@ -1057,8 +1064,8 @@ __device__ __forceinline__ void pp_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc
         "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ uint64_t pp_desc_mn(uint32_t saddr) {  // MN-major, 64-element blocks kPpAtom apart
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((kPpAtom >> 4) & 0x3FFFu) << 16 | (uint64_t)(1024 >> 4) << 32 |
+__device__ __forceinline__ uint64_t pp_desc_mn(uint32_t saddr) {  // MN-major, 64-element blocks kPpKv apart
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((kPpKv >> 4) & 0x3FFFu) << 16 | (uint64_t)(1024 >> 4) << 32 |
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 __device__ __forceinline__ void pp_ld32(uint32_t taddr, uint32_t *r) {
@@ -1195,20 +1202,23 @@ __global__ void __launch_bounds__(kPpThreads, 1)
     volatile int *const abort = &bar.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        mbar_init(&bar.q_full, 1);
-        mbar_init(&bar.q_empty, 1);
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(&bar.k_full[s], 1);
-            mbar_init(&bar.k_empty[s], 1);
+            mbar_init(&bar.k_empty[s], 2);  // (both MMA threads, also for what their row tile does not see)
             mbar_init(&bar.v_full[s], 1);
-            mbar_init(&bar.v_empty[s], 1);
+            mbar_init(&bar.v_empty[s], 2);
         }
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(&bar.s_full[t], 1);
-            mbar_init(&bar.p_full[t], 8);  // an arrival per warp
-            mbar_init(&bar.pv_done[t], 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&bar.q_full[x], 1);
+            mbar_init(&bar.q_empty[x], 2);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&bar.s_full[x][b], 1);
+                mbar_init(&bar.p_full[x][b], 4);  // an arrival per warp
+                mbar_init(&bar.pv_done[x][b], 1);
+            }
         }
-        mbar_init(&bar.drain, 1);
+        mbar_init(&bar.drain[0], 1);
+        mbar_init(&bar.drain[1], 1);
         *abort = 0;
         fence_mbar_init();
         prefetch_tmap(&tmq);
@@ -1246,154 +1256,143 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         return true;
     };
     const auto wait = [&](uint64_t *b, uint32_t phase) { return pp_wait(b, phase & 1u, a.err, abort); };
-    const auto wait_all = [&](uint64_t *b, uint32_t phase) { return __all_sync(kFull, wait(b, phase)) != 0; };
     // Key tiles are numbered g = 0, 1, .. across this block's items (stage g % kStages, its use g / kStages).
 
-    // 640 threads of 96 registers: 4 x 32 of 64 leave 104 for the softmax warps, which hold half a row of S
-    if (warp >= kPpTma) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == kPpTma) {
-            // ------------------------------ TMA ------------------------------
+    if (warp == kPpTma) {
+        // ------------------------------ TMA ------------------------------
+        // One thread (a box per lane is issued lane after lane, at some 140 cycles each).
+        if (elect_one()) {
             const uint64_t pol = l2_policy_evict_normal();  // every row tile of the request reads them
+            const int per = a.box / 16;
             uint32_t g = 0, q_used = 0, k_used = 0, v_used = 0;
             bool ok = true;
             Item it;
             for (int k = 0; ok && item_at(k, it); ++k) {
-                if (k >= 1 && !(ok = wait_all(&bar.q_empty, (uint32_t)(k - 1)))) break;
-                if (lane == 0) {
-                    const int tiles = it.n_rows[1] > 0 ? 2 : 1;
-                    mbar_arrive_expect_tx(&bar.q_full, (uint32_t)(tiles * L::kAtoms * tile_rows * a.pack * 128));
-                    for (int t = 0; t < tiles; ++t)
-                        for (int c = 0; c < L::kAtoms; ++c)
-                            pp_tma_q(smem_u32(sm + L::kQ + (t * L::kAtoms + c) * kPpAtom), &tmq, &bar.q_full, 64 * c,
-                                     it.vh * a.pack, it.row + t * tile_rows);
-                }
-                __syncwarp();
+                if (k >= 2 && !(ok = wait(&bar.q_empty[k & 1], (uint32_t)(k - 2) >> 1))) break;
+                const int tiles = it.n_rows[1] > 0 ? 2 : 1;
+                mbar_arrive_expect_tx(&bar.q_full[k & 1], (uint32_t)(tiles * L::kAtoms * tile_rows * a.pack * 128));
+                for (int t = 0; t < tiles; ++t)
+#pragma unroll
+                    for (int c = 0; c < L::kAtoms; ++c)
+                        pp_tma_q(smem_u32(sm + L::kQ) + (uint32_t)((((k & 1) * 2 + t) * L::kAtoms + c)) * kPpAtom, &tmq,
+                                 &bar.q_full[k & 1], 64 * c, it.vh * a.pack, it.row + t * tile_rows);
                 ++q_used;
-                const int kvh = it.vh / a.per_kv, n_tiles = (it.keys + 15) / 16, per = a.box / 16;
-                const int b = lane / L::kAtoms, c = lane % L::kAtoms;  // this lane's box of a key tile, and its 64 components
-                const auto index = [&](int j) {  // slot / 16 of the box's first key in key tile j
-                    const int x = j * (kPpKeys / 16) + b * per;
-                    return b * a.box < kPpKeys && x < n_tiles ? a.plan[it.at + x] : -1;
-                };
-                int next = index(0);
+                const int kvh = it.vh / a.per_kv, n_tiles = (it.keys + 15) / 16;
+                // slots / 16 of a key tile's four 16 keys (the plan's tables of a request start 16-byte aligned, a part
+                // of its keys at a multiple of 64)
+                const int4 *index = reinterpret_cast<const int4 *>(a.plan + it.at);
+                int4 next = index[0];
                 for (int j = 0; j < it.n_kt; ++j, ++g) {
                     const uint32_t s = g % L::kStages, use = g / L::kStages;
-                    const int slot = next * 16;
-                    if (j + 1 < it.n_kt) next = index(j + 1);
-                    const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, slot >= 0)) * a.box * 128);
-                    if (g >= L::kStages && !(ok = wait_all(&bar.k_empty[s], use - 1))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&bar.k_full[s], bytes);
-                    __syncwarp();
-                    const uint32_t at = (s * L::kAtoms + c) * kPpAtom + (uint32_t)(b * a.box * 128);
-                    if (slot >= 0) pp_tma_kv(smem_u32(sm + L::kK + at), &tmkv, &bar.k_full[s], 64 * c, slot, kvh, 0, pol);
+                    const int slot[4] = {next.x, next.y, next.z, next.w}, here = min(n_tiles - 4 * j, 4);
+                    if (j + 1 < it.n_kt) next = index[j + 1];
+                    const uint32_t bytes = (uint32_t)((here + per - 1) / per * a.box * 128 * L::kAtoms);
+                    const auto load = [&](uint32_t base, uint64_t *full, int kv) {
+                        mbar_arrive_expect_tx(full, bytes);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (e < here && (e & (per - 1)) == 0)
+#pragma unroll
+                                for (int c = 0; c < L::kAtoms; ++c)
+                                    pp_tma_kv(base + s * L::kTile + c * kPpKv + e * 2048u, &tmkv, full, 64 * c,
+                                              slot[e] * 16, kvh, kv, pol);
+                    };
+                    if (g >= L::kStages && !(ok = wait(&bar.k_empty[s], use - 1))) break;
+                    load(smem_u32(sm + L::kK), &bar.k_full[s], 0);
                     ++k_used;
-                    if (g >= L::kStages && !(ok = wait_all(&bar.v_empty[s], use - 1))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&bar.v_full[s], bytes);
-                    __syncwarp();
-                    if (slot >= 0) pp_tma_kv(smem_u32(sm + L::kV + at), &tmkv, &bar.v_full[s], 64 * c, slot, kvh, 1, pol);
+                    if (g >= L::kStages && !(ok = wait(&bar.v_empty[s], use - 1))) break;
+                    load(smem_u32(sm + L::kV), &bar.v_full[s], 1);
                     ++v_used;
                 }
             }
             if (!ok) {  // the copies in flight land before the block ends
                 *abort = 1;
-                if (q_used > 0) mbar_wait_bounded(&bar.q_full, (q_used - 1) & 1u, a.err);
+                for (uint32_t x = q_used > 2 ? q_used - 2 : 0; x < q_used; ++x)
+                    mbar_wait_bounded(&bar.q_full[x & 1], (x >> 1) & 1u, a.err);
                 for (uint32_t x = k_used > L::kStages ? k_used - L::kStages : 0; x < k_used; ++x)
                     mbar_wait_bounded(&bar.k_full[x % L::kStages], (x / L::kStages) & 1u, a.err);
                 for (uint32_t x = v_used > L::kStages ? v_used - L::kStages : 0; x < v_used; ++x)
                     mbar_wait_bounded(&bar.v_full[x % L::kStages], (x / L::kStages) & 1u, a.err);
             }
-        } else if (warp == kPpMma) {
-            // ------------------------------ MMA ------------------------------
-            // One thread, in small loops: with the products unrolled and the row tiles polled, its own instructions
-            // (fetched anew every time between those of the other warps) took 2100 cycles of a tile's step.  The tiles
-            // in turn, S behind its own P V, so that one softmax runs beside the other's products.
-            if (elect_one()) {
-                const uint32_t idesc_s = idesc_bf16_f32(kPpRows, kPpKeys);
-                const uint32_t idesc_pv = idesc_bf16_f32(kPpRows, D) | (1u << 16);  // B (V) MN-major
-                uint32_t g = 0, par_s = 0, par_pv = 0, pending = 0;  // (bits by row tile: parities, P V to come)
-                bool ok = true, first = false;                       // first: the pending P V begin their item
-                // The last step's P V of tile t, then, if `s_too`, S of key tile g.
-                const auto issue = [&](uint32_t t, bool s_too, bool k_last, bool q_last) {
-                    if (pending >> t & 1u) {
-                        const uint32_t v = g - 1, st = v % L::kStages;
-                        if (!wait(&bar.p_full[t], par_pv >> t) || !wait(&bar.v_full[st], v / L::kStages)) return false;
-                        tc_fence_after();
-                        uint64_t vd = pp_desc_mn(smem_u32(sm + L::kV) + st * (L::kAtoms * kPpAtom));
-                        uint32_t pt = tmem + 128u * t;
-#pragma unroll 1
-                        for (uint32_t x = 0; x < kPpKeys / 16; ++x) {  // 16 keys: two groups of 8 rows of V, 8 columns of P
-                            pp_mma_ts(tmem + 256u + 128u * t, pt, vd, idesc_pv, (uint32_t)!first | x);
-                            vd += 2048 >> 4, pt += x == 3 ? 64u - 24u : 8u;
-                        }
-                        tc_commit(&bar.pv_done[t]);
-                        if (t == 1 || !(pending & 2u)) tc_commit(&bar.v_empty[st]);
-                        par_pv ^= 1u << t;
-                    }
-                    if (!s_too) return true;
-                    const uint32_t st = g % L::kStages;
-                    if (!wait(&bar.k_full[st], g / L::kStages)) return false;
-                    // S_t takes the place of P_t: behind the P V that read it (parity of the one before: none yet, passes)
-                    if (!wait(&bar.pv_done[t], (par_s >> t & 1u) ^ 1u)) return false;
-                    tc_fence_after();
-                    uint64_t qd = smem_desc_k128(smem_u32(sm + L::kQ) + t * (L::kAtoms * kPpAtom));
-                    uint64_t kd = smem_desc_k128(smem_u32(sm + L::kK) + st * (L::kAtoms * kPpAtom));
-#pragma unroll 1
-                    for (uint32_t x = 0; x < D / 16; ++x) {  // 16 components: 32 bytes of a 64-component block
-                        tc_mma_f16(tmem + 128u * t, qd, kd, idesc_s, x);
-                        const uint32_t o = (x & 3u) == 3u ? (kPpAtom - 96u) >> 4 : 32u >> 4;
-                        qd += o, kd += o;
-                    }
-                    tc_commit(&bar.s_full[t]);
-                    if (k_last) tc_commit(&bar.k_empty[st]);
-                    if (q_last) tc_commit(&bar.q_empty);
-                    par_s ^= 1u << t;
-                    return true;
-                };
-                Item it;
-                for (int k = 0; ok && item_at(k, it); ++k) {
-                    ok = wait(&bar.q_full, (uint32_t)k);
-                    for (int j = 0; ok && j < it.n_kt; ++j, ++g) {
-                        const uint32_t act = (j < it.nk[0] ? 1u : 0u) | (j < it.nk[1] ? 2u : 0u);
-#pragma unroll 1
-                        for (uint32_t t = 0; ok && t < 2; ++t) {
-                            const bool last = t == 1 || !(act & 2u);
-                            ok = issue(t, act >> t & 1u, last, last && j + 1 == it.n_kt);
-                        }
-                        pending = act, first = j == 0;
-                    }
-                }
-#pragma unroll 1
-                for (uint32_t t = 0; ok && t < 2; ++t) ok = issue(t, false, false, false);
-                if (!ok) *abort = 1;
-                // every product issued has completed before stages and tensor memory are given up
-                tc_commit(&bar.drain);
-                mbar_wait_bounded(&bar.drain, 0u, a.err);
-            }
-            __syncwarp();
         }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        __syncwarp();
+    } else if (warp == kPpMma || warp == kPpMma + 1) {
+        // ------------------------------ MMA ------------------------------
+        // A thread for each row tile: a product with its waits and commits takes it some 500 cycles, so that one thread
+        // for both tiles held up everything else.  It walks all key tiles of the block, the P V of key tile g in
+        // step; S runs ahead by up to two products, and less than the ring in key tiles (both may block for a load, which
+        // has to be one that no release of its own stands in front of).
+        if (elect_one()) {
+            const uint32_t t = (uint32_t)(warp - kPpMma);
+            const uint32_t idesc_s = idesc_bf16_f32(kPpRows, kPpKeys);
+            const uint32_t idesc_pv = idesc_bf16_f32(kPpRows, D) | (1u << 16);  // B (V) MN-major
+            Item is, iv;  // the items of S and of P V
+            int ks = 0, js = 0;
+            uint32_t gs = 0, ns = 0, np = 0;
+            bool more = item_at(0, is), ok = true;
+            const auto step_s = [&]() {  // key tile gs: S, if the row tile sees it
+                const uint32_t st = gs % L::kStages, b = ns & 1u;
+                const int nk = t ? is.nk[1] : is.nk[0];
+                if (!wait(&bar.k_full[st], gs / L::kStages) || (js == 0 && !wait(&bar.q_full[ks & 1], (uint32_t)ks >> 1)))
+                    return false;
+                const bool last = js + 1 == is.n_kt;
+                if (js < nk) {
+                    // S takes the place of P two products before it, whose P V this thread has issued: the tensor core
+                    // runs the products of one thread in their order.
+                    tc_fence_after();
+                    const uint64_t qd = smem_desc_k128(smem_u32(sm + L::kQ) + ((ks & 1) * 2 + t) * (L::kAtoms * kPpAtom));
+                    const uint64_t kd = smem_desc_k128(smem_u32(sm + L::kK) + st * L::kTile);
+#pragma unroll
+                    for (uint32_t x = 0; x < D / 16; ++x)  // 16 components: 32 bytes of a 64-component block
+                        tc_mma_f16(tmem + 128u * t + 64u * b, qd + (((x >> 2) * kPpAtom + (x & 3u) * 32u) >> 4),
+                                   kd + (((x >> 2) * kPpKv + (x & 3u) * 32u) >> 4), idesc_s, x);
+                    tc_commit(&bar.s_full[t][b]);
+                    ++ns;
+                    tc_commit(&bar.k_empty[st]);
+                } else {
+                    mbar_arrive(&bar.k_empty[st]);
+                }
+                // (a commit covers all of this thread's products so far)
+                if (last) tc_commit(&bar.q_empty[ks & 1]);
+                ++gs, ++js;
+                if (last) js = 0, more = item_at(++ks, is);
+                return true;
+            };
+            uint32_t g = 0;
+            for (int k = 0; ok && item_at(k, iv); ++k) {
+                const int nk = t ? iv.nk[1] : iv.nk[0];
+                for (int j = 0; ok && j < iv.n_kt; ++j, ++g) {
+                    while (ok && more && gs < g + L::kStages && (ns < np + 2 || js >= (t ? is.nk[1] : is.nk[0]))) ok = step_s();
+                    const uint32_t st = g % L::kStages, b = np & 1u;
+                    ok = ok && wait(&bar.v_full[st], g / L::kStages);
+                    if (j >= nk) {
+                        if (ok) mbar_arrive(&bar.v_empty[st]);
+                        continue;
+                    }
+                    // (an item's first P is written after the last item's O has been read out)
+                    if (!ok || !(ok = wait(&bar.p_full[t][b], np >> 1))) break;
+                    tc_fence_after();
+                    const uint64_t vd = pp_desc_mn(smem_u32(sm + L::kV) + st * L::kTile);
+                    const uint32_t pt = tmem + 128u * t + 64u * b;
+#pragma unroll
+                    for (uint32_t x = 0; x < kPpKeys / 16; ++x)  // 16 keys: 16 rows of V, 8 columns of P
+                        pp_mma_ts(tmem + 256u + 128u * t, pt + 8u * x, vd + x * (2048 >> 4), idesc_pv, (uint32_t)j | x);
+                    tc_commit(&bar.pv_done[t][b]);
+                    tc_commit(&bar.v_empty[st]);
+                    ++np;
+                }
+            }
+            if (!ok) *abort = 1;
+            // every product issued has completed before stages and tensor memory are given up
+            tc_commit(&bar.drain[t]);
+            mbar_wait_bounded(&bar.drain[t], 0u, a.err);
+        }
+        __syncwarp();
+    } else if (warp < kPpTma) {
         // ------------------------------ softmax ------------------------------
-        // Two threads per row, 64 keys of a tile (and half of O's components) each: with one thread per row
-        // the chain from S to P took 1980 cycles of a step's 4020, most of it latency of few warps.  P of either
-        // half lies over that half's own columns of S.
         // (A wait that gave up sets the abort flag, and the rest runs through on what is there.)
-        const int t = warp >> 3, half = warp >> 2 & 1, quarter = warp & 3, r = quarter * 32 + lane;
-        const uint32_t lane_t = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t s_t = lane_t + 128u * t + 64u * half, o_t = lane_t + 256u + 128u * t + (uint32_t)(D / 2 * half);
-        constexpr int DH = D / 2;
-        float *const red = reinterpret_cast<float *>(sm + L::kRed) + t * (4 * kPpRows) + r;
-        uint32_t turn = 0;
-        // The other half's value.  Slots of one parity are written again two turns later, when the other half has
-        // read them (it does so before it comes to the turn between).
-        const auto exchange = [&](float v) {
-            red[((turn & 1u) * 2 + half) * kPpRows] = v;
-            asm volatile("bar.sync %0, 64;" ::"r"(1 + t * 4 + quarter) : "memory");
-            v = red[((turn & 1u) * 2 + (half ^ 1)) * kPpRows];
-            ++turn;
-            return v;
-        };
+        const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lane_t = tmem + ((uint32_t)(quarter * 32) << 16), o_t = lane_t + 256u + 128u * t;
         uint32_t g0 = 0, n = 0;  // the item's first key tile, this row tile's key tiles so far
         Item it;
         for (int k = 0; item_at(k, it); g0 += it.n_kt, ++k) {
@@ -1401,10 +1400,11 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             if (n_rows == 0) continue;
             const int jr = r / a.pack, sees = it.sees + t * tile_rows + jr;  // keys 0 .. sees - 1 of the item are this row's
             const int first_sees = it.sees + t * tile_rows;
-            float m = -INFINITY, l = 0.f;  // (m in the units of S; l of this half)
+            float m = -INFINITY, l = 0.f;  // (m in the units of S)
             for (int j = 0; j < nk; ++j, ++n) {
                 const int kbase = j * kPpKeys;
-                wait(&bar.s_full[t], n);
+                const uint32_t b = n & 1u, s_t = lane_t + 128u * t + 64u * b;
+                wait(&bar.s_full[t][b], n >> 1);
                 tc_fence_after();
                 uint32_t s[64];
                 pp_ld32(s_t, s);
@@ -1412,22 +1412,19 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 pp_wait_ld32(s);
                 pp_wait_ld32(s + 32);
                 if (kbase + kPpKeys > first_sees || kbase + kPpKeys > it.keys) {
-                    const int valid = min(sees, it.keys) - kbase - 64 * half;
-                    if (!__all_sync(kFull, valid >= 64)) {
+                    const int valid = min(sees, it.keys) - kbase;
 #pragma unroll
-                        for (int x = 0; x < 64; ++x)
-                            if (x >= valid) s[x] = 0xff800000u;
-                    }
+                    for (int x = 0; x < 64; ++x)
+                        if (x >= valid) s[x] = 0xff800000u;
                 }
                 // Weights are formed against the last tile's m while the maximum is taken, and once more in the rare
                 // tile that lifts it by more than 2^8 (the first, and scores where s scale - m in one step would keep
-                // what m lost to rounding: maximum first).  Both halves come to the same decisions.
+                // what m lost to rounding: maximum first).
                 bool known = j == 0 || __any_sync(kFull, fabsf(m * a.scale_log2) > 16384.f);
                 float top = -INFINITY, ls;
                 if (known) {
 #pragma unroll
                     for (int x = 0; x < 64; x += 2) top = pp_max3(top, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
-                    top = fmaxf(top, exchange(top));
                 }
                 for (;;) {
                     float neg = -cw_base(m) * a.scale_log2;
@@ -1440,9 +1437,11 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                             m = top;
                             l *= alpha;
                         }
-                        if (__any_sync(kFull, alpha != 1.f)) {  // (the P V so far are done: S_t was issued behind them)
+                        if (__any_sync(kFull, alpha != 1.f)) {  // O: once the P V so far are done
+                            wait(&bar.pv_done[t][b ^ 1u], (n - 1) >> 1);
+                            tc_fence_after();
 #pragma unroll 1
-                            for (int x = 0; x < DH; x += 16) {
+                            for (int x = 0; x < D; x += 16) {
                                 float o[16];
                                 tmem_ld16(o_t + x, o);
                                 uint32_t w[16];
@@ -1481,7 +1480,6 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                     ls = l0 + l1;
                     if (known) break;
                     top = fmaxf(mx[0], mx[1]);
-                    top = fmaxf(top, exchange(top));
                     known = __any_sync(kFull, (top - m) * a.scale_log2 > kPpRescale);
                     if (!known) break;
                 }
@@ -1490,32 +1488,32 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 if (here < kPpKeys) {
                     const uint32_t v = g0 + j, st = v % L::kStages;
                     wait(&bar.v_full[st], v / L::kStages);
-                    if (r >= here && half < L::kAtoms)
+                    const int c = r / kPpKeys, vr = r % kPpKeys;  // (64 rows of up to two blocks)
+                    if (vr >= here && c < L::kAtoms)
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
-                            *reinterpret_cast<uint4 *>(sm + L::kV + (st * L::kAtoms + half) * kPpAtom + r * 128 + x * 16) =
+                            *reinterpret_cast<uint4 *>(sm + L::kV + st * L::kTile + c * kPpKv + vr * 128 + x * 16) =
                                 make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
                 pp_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.p_full[t]);
+                if (lane == 0) mbar_arrive(&bar.p_full[t][b]);
             }
             // ---- the item's output ----
             const bool mine = r < n_rows * a.pack;
             const int row = it.row + t * tile_rows + jr, head = it.vh * a.pack + r % a.pack;
-            bf16 *const dst = a.out + (int64_t)row * a.ld_out + (int64_t)head * D + DH * half;
+            bf16 *const dst = a.out + (int64_t)row * a.ld_out + (int64_t)head * D;
             const int64_t at = (int64_t)it.part * a.vheads + (int64_t)it.vh * (2 * kPpRows) + t * kPpRows + r;
-            float *const part = a.part + at * D + DH * half;
+            float *const part = a.part + at * D;
             bool bad = false;
-            l += exchange(l);
             if (nk > 0) {
-                wait(&bar.pv_done[t], n - 1);
+                wait(&bar.pv_done[t][(n - 1) & 1u], (n - 1) >> 1);
                 tc_fence_after();
                 const float inv = 1.f / l;
 #pragma unroll
-                for (int x = 0; x < DH; x += 32) {
+                for (int x = 0; x < D; x += 32) {
                     uint32_t o[32];
                     pp_ld32(o_t + x, o);
                     pp_wait_ld32(o);
@@ -1538,13 +1536,10 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 }
                 tc_fence_before();
             } else if (mine) {  // a part of the keys of which this tile sees none
-                for (int x = 0; x < DH; x += 4) *reinterpret_cast<uint4 *>(part + x) = make_uint4(0, 0, 0, 0);
+                for (int x = 0; x < D; x += 4) *reinterpret_cast<uint4 *>(part + x) = make_uint4(0, 0, 0, 0);
             }
-            if (mine && it.part >= 0 && half == 0)
-                *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m * a.scale_log2, l);
-            bad = mine && (bad || l != l);
-            bad |= exchange(bad ? 1.f : 0.f) != 0.f;  // (behind it, both halves' writes are done)
-            unsigned todo = half ? 0u : __ballot_sync(kFull, bad);
+            if (mine && it.part >= 0) *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m * a.scale_log2, l);
+            unsigned todo = __ballot_sync(kFull, mine && (bad || l != l));
             for (; todo; todo &= todo - 1) {  // rows with something that is not finite, over what they see
                 const int rr = quarter * 32 + __ffs(todo) - 1;
                 const int row2 = it.row + t * tile_rows + rr / a.pack, head2 = it.vh * a.pack + rr % a.pack;

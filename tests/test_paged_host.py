@@ -140,13 +140,13 @@ def cover(native, p, n, c, table, page, group, kv_heads):
                 written.setdefault(key, []).append(("c", part + x) if part >= 0 else None)
         at += 8 * p[ITEMS + cl]
     pack, box = int(p[PACK]), int(p[BOX])
-    assert group % pack == 0 and box % 16 == 0 and 128 % box == 0 and page % box == 0
+    assert group % pack == 0 and box % 16 == 0 and 64 % box == 0 and page % box == 0
     for r in p[p[O_PITEMS]:p[O_PITEMS] + 8 * p[PITEMS]].reshape(-1, 8):
         tile, keys, row0, nr, sees, part = (int(x) for x in r[:6])
         i, per = int(req_of[row0]), 128 // pack
         assert 1 <= nr <= 2 * per and row0 + nr <= first[i + 1]
         k0 = keys_ok(i, tile, keys)
-        assert k0 % 128 == 0 and sees == c[i] + row0 - first[i] + 1 - k0 and sees + nr - 1 >= 1
+        assert k0 % 64 == 0 and sees == c[i] + row0 - first[i] + 1 - k0 and sees + nr - 1 >= 1
         assert keys <= sees + nr - 1 and (part < 0 or part + 256 <= p[PPARTS])
         for j in range(nr):
             for g in range(group):  # (packed one by one: every head has the item's columns of its own)
