@@ -994,7 +994,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 // waits, tensor-memory accesses; measured with that work left out), so the
 // next S is always under way: a softmax finds it when it is done with the last.
 // With one buffer of 128 keys the same work took 4400 cycles per 128 keys of both
-// tiles.  Shared memory: Q of two items and a ring of key tiles; the loads are
+// tiles.  Shared memory: Q and a ring of key tiles; the loads are
 // boxes of a page (or of the part of it that divides 64 slots), a lane of the
 // TMA warp each.
 // O is rescaled only where a row's maximum grew by more than 2^8, as every P is
@@ -1013,17 +1013,18 @@ constexpr float kPpRescale = 8.f;
 template <int D>
 struct PpLayout {
     static constexpr int kAtoms = D / 64;
-    static constexpr int kStages = D == 64 ? 6 : 3;
+    static constexpr int kStages = D == 64 ? 8 : 5;
     static constexpr uint32_t kTile = kAtoms * kPpKv;  // a key tile's K or V
-    static constexpr uint32_t kQ = 0;                  // [item's parity][tile][atom]
-    static constexpr uint32_t kK = 4 * kAtoms * kPpAtom;
+    static constexpr uint32_t kQ = 0;                  // [tile][atom]
+    static constexpr uint32_t kK = 2 * kAtoms * kPpAtom;
     static constexpr uint32_t kV = kK + kStages * kTile;
     static constexpr uint32_t kBars = kV + kStages * kTile;
     static constexpr uint32_t kBytes = kBars + 512;
 };
 struct PpBars {
-    uint64_t q_full[2], q_empty[2], k_full[6], k_empty[6], v_full[6], v_empty[6];
-    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [tile][buffer]
+    uint64_t q_full, q_empty, kv_full[8], kv_empty[8];
+    uint64_t s_full[2][2], p_full[2][2];  // [tile][buffer]
+    uint64_t o_done[2][2];                // [tile]: the products of an item's last key tile but one, and of its last
     uint64_t drain[2];
     uint32_t tmem;
     int abort;
@@ -1055,19 +1056,34 @@ __device__ __forceinline__ void pp_tma_kv(uint32_t dst, const void *tmap, uint64
         "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(slot), "r"(h), "r"(kv), "l"(policy)
         : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem]: a row of A per lane, two elements per column.
-__device__ __forceinline__ void pp_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem] (a row of A per lane, two elements per column) and A[smem] * B[smem]; the
+// descriptors of shared memory by their lower halves, in which the address is.
+__device__ __forceinline__ void pp_mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                          uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ uint64_t pp_desc_mn(uint32_t saddr) {  // MN-major, 64-element blocks kPpKv apart
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((kPpKv >> 4) & 0x3FFFu) << 16 | (uint64_t)(1024 >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+__device__ __forceinline__ void pp_mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 a, {%1, %3};\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
+// Lower and upper halves of the descriptors (smem_desc_k128): an operand's leading stride goes into the lower one,
+// 1 where it is K-major (not used), the blocks' distance where V is read MN-major.
+constexpr uint32_t kPpDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t pp_desc_k(uint32_t saddr) { return (saddr >> 4 & 0x3FFFu) | 1u << 16; }
+__device__ __forceinline__ uint32_t pp_desc_mn(uint32_t saddr) { return (saddr >> 4 & 0x3FFFu) | (kPpKv >> 4) << 16; }
 __device__ __forceinline__ void pp_ld32(uint32_t taddr, uint32_t *r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -1120,11 +1136,22 @@ __device__ __forceinline__ uint64_t pp_add2(uint64_t a, uint64_t b) {
 }
 
 // A bounded wait; when it gives up, or another warp has, the abort flag is set and every later wait ends at once.
-__device__ __forceinline__ bool pp_wait(uint64_t *bar, uint32_t parity, unsigned *err, volatile int *abort) {
-    if (mbar_try_wait(bar, parity)) return true;
+__device__ __noinline__ bool pp_wait_on(uint32_t bar, uint32_t parity, unsigned *err, volatile int *abort);
+__device__ __forceinline__ bool pp_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ bool pp_wait_on(uint32_t bar, uint32_t parity, unsigned *err, volatile int *abort) {
     unsigned long long t0 = 0;
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (pp_try(bar, parity)) return true;
         if (*abort) return false;
         if ((it & 63u) == 0) {
             const unsigned long long now = global_timer_ns();
@@ -1136,6 +1163,12 @@ __device__ __forceinline__ bool pp_wait(uint64_t *bar, uint32_t parity, unsigned
             }
         }
     }
+}
+__device__ __forceinline__ bool pp_wait(uint32_t bar, uint32_t parity, unsigned *err, volatile int *abort) {
+    return pp_try(bar, parity) || pp_wait_on(bar, parity, err, abort);
+}
+__device__ __forceinline__ void pp_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ float pp_max3(float a, float b, float c) {
     float d;
@@ -1202,20 +1235,14 @@ __global__ void __launch_bounds__(kPpThreads, 1)
     volatile int *const abort = &bar.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < L::kStages; ++s) {
-            mbar_init(&bar.k_full[s], 1);
-            mbar_init(&bar.k_empty[s], 2);  // (both MMA threads, also for what their row tile does not see)
-            mbar_init(&bar.v_full[s], 1);
-            mbar_init(&bar.v_empty[s], 2);
-        }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(&bar.q_full[x], 1);
-            mbar_init(&bar.q_empty[x], 2);
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(&bar.s_full[x][b], 1);
-                mbar_init(&bar.p_full[x][b], 4);  // an arrival per warp
-                mbar_init(&bar.pv_done[x][b], 1);
-            }
+        // (the empty ones: both MMA threads, also for what their row tile does not see)
+        for (int s = 0; s < L::kStages; ++s) mbar_init(&bar.kv_full[s], 1), mbar_init(&bar.kv_empty[s], 2);
+        mbar_init(&bar.q_full, 1);
+        mbar_init(&bar.q_empty, 2);
+        for (int x = 0; x < 4; ++x) {
+            mbar_init(&bar.s_full[x >> 1][x & 1], 1);
+            mbar_init(&bar.p_full[x >> 1][x & 1], 4);  // an arrival per warp
+            mbar_init(&bar.o_done[x >> 1][x & 1], 1);
         }
         mbar_init(&bar.drain[0], 1);
         mbar_init(&bar.drain[1], 1);
@@ -1255,7 +1282,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         it.n_kt = max(it.nk[0], it.nk[1]);
         return true;
     };
-    const auto wait = [&](uint64_t *b, uint32_t phase) { return pp_wait(b, phase & 1u, a.err, abort); };
+    const auto wait = [&](uint64_t *b, uint32_t phase) { return pp_wait(smem_u32(b), phase & 1u, a.err, abort); };
     // Key tiles are numbered g = 0, 1, .. across this block's items (stage g % kStages, its use g / kStages).
 
     if (warp == kPpTma) {
@@ -1264,18 +1291,17 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         if (elect_one()) {
             const uint64_t pol = l2_policy_evict_normal();  // every row tile of the request reads them
             const int per = a.box / 16;
-            uint32_t g = 0, q_used = 0, k_used = 0, v_used = 0;
+            uint32_t g = 0, q_used = 0, kv_used = 0;
             bool ok = true;
             Item it;
             for (int k = 0; ok && item_at(k, it); ++k) {
-                if (k >= 2 && !(ok = wait(&bar.q_empty[k & 1], (uint32_t)(k - 2) >> 1))) break;
+                if (k >= 1 && !(ok = wait(&bar.q_empty, (uint32_t)(k - 1)))) break;
                 const int tiles = it.n_rows[1] > 0 ? 2 : 1;
-                mbar_arrive_expect_tx(&bar.q_full[k & 1], (uint32_t)(tiles * L::kAtoms * tile_rows * a.pack * 128));
+                mbar_arrive_expect_tx(&bar.q_full, (uint32_t)(tiles * L::kAtoms * tile_rows * a.pack * 128));
                 for (int t = 0; t < tiles; ++t)
 #pragma unroll
                     for (int c = 0; c < L::kAtoms; ++c)
-                        pp_tma_q(smem_u32(sm + L::kQ) + (uint32_t)((((k & 1) * 2 + t) * L::kAtoms + c)) * kPpAtom, &tmq,
-                                 &bar.q_full[k & 1], 64 * c, it.vh * a.pack, it.row + t * tile_rows);
+                        pp_tma_q(smem_u32(sm + L::kQ) + (uint32_t)(t * L::kAtoms + c) * kPpAtom, &tmq, &bar.q_full, 64 * c, it.vh * a.pack, it.row + t * tile_rows);
                 ++q_used;
                 const int kvh = it.vh / a.per_kv, n_tiles = (it.keys + 15) / 16;
                 // slots / 16 of a key tile's four 16 keys (the plan's tables of a request start 16-byte aligned, a part
@@ -1283,36 +1309,29 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 const int4 *index = reinterpret_cast<const int4 *>(a.plan + it.at);
                 int4 next = index[0];
                 for (int j = 0; j < it.n_kt; ++j, ++g) {
-                    const uint32_t s = g % L::kStages, use = g / L::kStages;
+                    const uint32_t s = g % L::kStages;
                     const int slot[4] = {next.x, next.y, next.z, next.w}, here = min(n_tiles - 4 * j, 4);
                     if (j + 1 < it.n_kt) next = index[j + 1];
-                    const uint32_t bytes = (uint32_t)((here + per - 1) / per * a.box * 128 * L::kAtoms);
-                    const auto load = [&](uint32_t base, uint64_t *full, int kv) {
-                        mbar_arrive_expect_tx(full, bytes);
+                    if (g >= L::kStages && !(ok = wait(&bar.kv_empty[s], g / L::kStages - 1))) break;
+                    mbar_arrive_expect_tx(&bar.kv_full[s],
+                                          (uint32_t)((here + per - 1) / per * a.box * (2 * 128 * L::kAtoms)));
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (e < here && (e & (per - 1)) == 0)
 #pragma unroll
                                 for (int c = 0; c < L::kAtoms; ++c)
-                                    pp_tma_kv(base + s * L::kTile + c * kPpKv + e * 2048u, &tmkv, full, 64 * c,
-                                              slot[e] * 16, kvh, kv, pol);
-                    };
-                    if (g >= L::kStages && !(ok = wait(&bar.k_empty[s], use - 1))) break;
-                    load(smem_u32(sm + L::kK), &bar.k_full[s], 0);
-                    ++k_used;
-                    if (g >= L::kStages && !(ok = wait(&bar.v_empty[s], use - 1))) break;
-                    load(smem_u32(sm + L::kV), &bar.v_full[s], 1);
-                    ++v_used;
+                                    pp_tma_kv(smem_u32(sm + (kv ? L::kV : L::kK)) + s * L::kTile + c * kPpKv + e * 2048u,
+                                              &tmkv, &bar.kv_full[s], 64 * c, slot[e] * 16, kvh, kv, pol);
+                    ++kv_used;
                 }
             }
             if (!ok) {  // the copies in flight land before the block ends
                 *abort = 1;
-                for (uint32_t x = q_used > 2 ? q_used - 2 : 0; x < q_used; ++x)
-                    mbar_wait_bounded(&bar.q_full[x & 1], (x >> 1) & 1u, a.err);
-                for (uint32_t x = k_used > L::kStages ? k_used - L::kStages : 0; x < k_used; ++x)
-                    mbar_wait_bounded(&bar.k_full[x % L::kStages], (x / L::kStages) & 1u, a.err);
-                for (uint32_t x = v_used > L::kStages ? v_used - L::kStages : 0; x < v_used; ++x)
-                    mbar_wait_bounded(&bar.v_full[x % L::kStages], (x / L::kStages) & 1u, a.err);
+                if (q_used > 0) mbar_wait_bounded(&bar.q_full, (q_used - 1) & 1u, a.err);
+                for (uint32_t x = kv_used > L::kStages ? kv_used - L::kStages : 0; x < kv_used; ++x)
+                    mbar_wait_bounded(&bar.kv_full[x % L::kStages], (x / L::kStages) & 1u, a.err);
             }
         }
         __syncwarp();
@@ -1329,56 +1348,97 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             Item is, iv;  // the items of S and of P V
             int ks = 0, js = 0;
             uint32_t gs = 0, ns = 0, np = 0;
-            bool more = item_at(0, is), ok = true;
-            const auto step_s = [&]() {  // key tile gs: S, if the row tile sees it
-                const uint32_t st = gs % L::kStages, b = ns & 1u;
-                const int nk = t ? is.nk[1] : is.nk[0];
-                if (!wait(&bar.k_full[st], gs / L::kStages) || (js == 0 && !wait(&bar.q_full[ks & 1], (uint32_t)ks >> 1)))
-                    return false;
-                const bool last = js + 1 == is.n_kt;
-                if (js < nk) {
-                    // S takes the place of P two products before it, whose P V this thread has issued: the tensor core
-                    // runs the products of one thread in their order.
-                    tc_fence_after();
-                    const uint64_t qd = smem_desc_k128(smem_u32(sm + L::kQ) + ((ks & 1) * 2 + t) * (L::kAtoms * kPpAtom));
-                    const uint64_t kd = smem_desc_k128(smem_u32(sm + L::kK) + st * L::kTile);
-#pragma unroll
-                    for (uint32_t x = 0; x < D / 16; ++x)  // 16 components: 32 bytes of a 64-component block
-                        tc_mma_f16(tmem + 128u * t + 64u * b, qd + (((x >> 2) * kPpAtom + (x & 3u) * 32u) >> 4),
-                                   kd + (((x >> 2) * kPpKv + (x & 3u) * 32u) >> 4), idesc_s, x);
-                    tc_commit(&bar.s_full[t][b]);
-                    ++ns;
-                    tc_commit(&bar.k_empty[st]);
-                } else {
-                    mbar_arrive(&bar.k_empty[st]);
+            bool more = item_at(0, is), ok = true, ready = false;
+            const auto next_s = [&]() {  // behind the last use of key tile gs
+                ++gs;
+                if (++js == is.n_kt) {
+                    tc_commit(&bar.q_empty);  // (a commit covers all of this thread's products so far)
+                    js = 0, more = item_at(++ks, is);
                 }
-                // (a commit covers all of this thread's products so far)
-                if (last) tc_commit(&bar.q_empty[ks & 1]);
-                ++gs, ++js;
-                if (last) js = 0, more = item_at(++ks, is);
-                return true;
+            };
+            // (Few commits: each holds up the products behind it.)
+            // Comes to the next key tile that the row tile sees, below key tile `end`, and waits for its keys.
+            const auto prepare_s = [&](uint32_t end) {
+                while (ok && !ready && more && gs < end) {
+                    const uint32_t st = gs % L::kStages;
+                    ok = wait(&bar.kv_full[st], gs / L::kStages) && (js > 0 || wait(&bar.q_full, (uint32_t)ks));
+                    if (!ok) break;
+                    ready = js < (t ? is.nk[1] : is.nk[0]);
+                    if (!ready) next_s();
+                }
+            };
+            // S of one key tile, P V of one key tile: the products, and the commit that says so.
+            const uint32_t s_t = tmem + 128u * t, qd = pp_desc_k(smem_u32(sm + L::kQ) + t * (L::kAtoms * kPpAtom));
+            const auto mma_s = [&](uint32_t b, uint32_t kd) {
+                // S takes the place of P two products before it, whose P V this thread has issued: the tensor core runs
+                // the products of one thread in their order.
+#pragma unroll
+                for (uint32_t x = 0; x < D / 16; ++x)  // 16 components: 32 bytes of a 64-component block
+                    pp_mma_ss(s_t + 64u * b, qd + (((x >> 2) * kPpAtom + (x & 3u) * 32u) >> 4),
+                              kd + (((x >> 2) * kPpKv + (x & 3u) * 32u) >> 4), kPpDescHi, idesc_s, x);
+                pp_commit(smem_u32(&bar.s_full[t][0]) + 8u * b);
+            };
+            const auto mma_pv = [&](uint32_t b, uint32_t vd, uint32_t accumulate) {
+#pragma unroll
+                for (uint32_t x = 0; x < kPpKeys / 16; ++x)  // 16 keys: 16 rows of V, 8 columns of P
+                    pp_mma_ts(s_t + 256u, s_t + 64u * b + 8u * x, vd + x * (2048 >> 4), kPpDescHi, idesc_pv, accumulate | x);
+            };
+            const uint32_t kd0 = pp_desc_k(smem_u32(sm + L::kK)), vd0 = pp_desc_mn(smem_u32(sm + L::kV));
+            const auto issue_s = [&]() {
+                tc_fence_after();
+                mma_s(ns & 1u, kd0 + gs % L::kStages * (L::kTile >> 4));
+                ++ns, ready = false;
+                next_s();
             };
             uint32_t g = 0;
             for (int k = 0; ok && item_at(k, iv); ++k) {
                 const int nk = t ? iv.nk[1] : iv.nk[0];
                 for (int j = 0; ok && j < iv.n_kt; ++j, ++g) {
-                    while (ok && more && gs < g + L::kStages && (ns < np + 2 || js >= (t ? is.nk[1] : is.nk[0]))) ok = step_s();
                     const uint32_t st = g % L::kStages, b = np & 1u;
-                    ok = ok && wait(&bar.v_full[st], g / L::kStages);
-                    if (j >= nk) {
-                        if (ok) mbar_arrive(&bar.v_empty[st]);
+                    for (;;) {  // (the next S is ready to go when P arrives)
+                        prepare_s(g + L::kStages);
+                        if (!ready || ns >= np + 2) break;
+                        issue_s();
+                    }
+                    if (!ok) break;
+                    if (j >= nk) {  // (S has come by here: the keys are there)
+                        mbar_arrive(&bar.kv_empty[st]);
                         continue;
                     }
                     // (an item's first P is written after the last item's O has been read out)
-                    if (!ok || !(ok = wait(&bar.p_full[t][b], np >> 1))) break;
+                    if (ready && ks == k && js == j + 2) {
+                        // The steps in the middle of an item, with as few instructions as they can do with: this thread
+                        // is alone, every one of them takes its whole latency (the general form some 1300 cycles a step).
+                        const uint32_t full0 = smem_u32(bar.kv_full), empty0 = smem_u32(bar.kv_empty);
+                        const uint32_t p0 = smem_u32(&bar.p_full[t][0]);
+                        uint32_t s_st = gs % L::kStages, s_ph = gs / L::kStages & 1u, v_st = st, n = np;
+                        const int steps = nk - js;  // S of the item's key tiles js .. nk - 1
+                        for (int i = 0; i < steps; ++i) {
+                            const uint32_t b = n & 1u;
+                            ok = pp_wait(full0 + 8u * s_st, s_ph, a.err, abort) &&
+                                 pp_wait(p0 + 8u * b, n >> 1 & 1u, a.err, abort);
+                            if (!ok) break;
+                            tc_fence_after();
+                            mma_pv(b, vd0 + v_st * (L::kTile >> 4), (uint32_t)(j + i));
+                            pp_commit(empty0 + 8u * v_st);
+                            mma_s(b, kd0 + s_st * (L::kTile >> 4));
+                            ++n;
+                            if (++v_st == L::kStages) v_st = 0;
+                            if (++s_st == L::kStages) s_st = 0, s_ph ^= 1u;
+                        }
+                        if (!ok) break;
+                        np += steps, ns += steps, ready = false;
+                        g += steps - 1, j += steps - 1;  // (this step among them)
+                        gs += steps - 1, js = nk - 1;
+                        next_s();
+                        continue;
+                    }
+                    if (!(ok = wait(&bar.p_full[t][b], np >> 1))) break;
                     tc_fence_after();
-                    const uint64_t vd = pp_desc_mn(smem_u32(sm + L::kV) + st * L::kTile);
-                    const uint32_t pt = tmem + 128u * t + 64u * b;
-#pragma unroll
-                    for (uint32_t x = 0; x < kPpKeys / 16; ++x)  // 16 keys: 16 rows of V, 8 columns of P
-                        pp_mma_ts(tmem + 256u + 128u * t, pt + 8u * x, vd + x * (2048 >> 4), idesc_pv, (uint32_t)j | x);
-                    tc_commit(&bar.pv_done[t][b]);
-                    tc_commit(&bar.v_empty[st]);
+                    mma_pv(b, vd0 + st * (L::kTile >> 4), (uint32_t)j);
+                    tc_commit(&bar.kv_empty[st]);
+                    if (j >= nk - 2) tc_commit(&bar.o_done[t][j == nk - 1]);
+                    if (ready) issue_s();
                     ++np;
                 }
             }
@@ -1393,7 +1453,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         // (A wait that gave up sets the abort flag, and the rest runs through on what is there.)
         const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_t = tmem + ((uint32_t)(quarter * 32) << 16), o_t = lane_t + 256u + 128u * t;
-        uint32_t g0 = 0, n = 0;  // the item's first key tile, this row tile's key tiles so far
+        uint32_t g0 = 0, n = 0, n_before = 0, n_last = 0;  // the item's first key tile, this row tile's so far, o_done's
         Item it;
         for (int k = 0; item_at(k, it); g0 += it.n_kt, ++k) {
             const int n_rows = t ? it.n_rows[1] : it.n_rows[0], nk = t ? it.nk[1] : it.nk[0];
@@ -1401,14 +1461,17 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             const int jr = r / a.pack, sees = it.sees + t * tile_rows + jr;  // keys 0 .. sees - 1 of the item are this row's
             const int first_sees = it.sees + t * tile_rows;
             float m = -INFINITY, l = 0.f;  // (m in the units of S)
+            uint32_t s[64];
+            const auto load = [&](uint32_t n) {  // starts the load of this row tile's n-th S
+                wait(&bar.s_full[t][n & 1u], n >> 1);
+                tc_fence_after();
+                pp_ld32(lane_t + 128u * t + 64u * (n & 1u), s);
+                pp_ld32(lane_t + 128u * t + 64u * (n & 1u) + 32, s + 32);
+            };
             for (int j = 0; j < nk; ++j, ++n) {
                 const int kbase = j * kPpKeys;
                 const uint32_t b = n & 1u, s_t = lane_t + 128u * t + 64u * b;
-                wait(&bar.s_full[t][b], n >> 1);
-                tc_fence_after();
-                uint32_t s[64];
-                pp_ld32(s_t, s);
-                pp_ld32(s_t + 32, s + 32);
+                load(n);
                 pp_wait_ld32(s);
                 pp_wait_ld32(s + 32);
                 if (kbase + kPpKeys > first_sees || kbase + kPpKeys > it.keys) {
@@ -1438,7 +1501,11 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                             l *= alpha;
                         }
                         if (__any_sync(kFull, alpha != 1.f)) {  // O: once the P V so far are done
-                            wait(&bar.pv_done[t][b ^ 1u], (n - 1) >> 1);
+                            // (the next S was issued behind them)
+                            if (j + 1 < nk)
+                                wait(&bar.s_full[t][b ^ 1u], (n + 1) >> 1);
+                            else
+                                wait(&bar.o_done[t][0], n_before);
                             tc_fence_after();
 #pragma unroll 1
                             for (int x = 0; x < D; x += 16) {
@@ -1487,7 +1554,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 const int here = it.keys - kbase;  // V rows past the item's last key: zero, once they have landed
                 if (here < kPpKeys) {
                     const uint32_t v = g0 + j, st = v % L::kStages;
-                    wait(&bar.v_full[st], v / L::kStages);
+                    wait(&bar.kv_full[st], v / L::kStages);
                     const int c = r / kPpKeys, vr = r % kPpKeys;  // (64 rows of up to two blocks)
                     if (vr >= here && c < L::kAtoms)
 #pragma unroll
@@ -1509,7 +1576,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             float *const part = a.part + at * D;
             bool bad = false;
             if (nk > 0) {
-                wait(&bar.pv_done[t][(n - 1) & 1u], (n - 1) >> 1);
+                if (nk >= 2) wait(&bar.o_done[t][0], n_before++);
+                wait(&bar.o_done[t][1], n_last++);
                 tc_fence_after();
                 const float inv = 1.f / l;
 #pragma unroll

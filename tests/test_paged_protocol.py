@@ -12,15 +12,14 @@ from test_protocol_models import Bar, run_agents, waitable
 
 def prompt_cta(items, stages, rnd, skip=None):
     """items: (key tiles of row tile 0, of row tile 1, whether tile 1 has rows).  skip: a wait that is left out (planted)."""
-    qf, qe = ([Bar(f"{x}{s}", c) for s in range(2)] for x, c in (("q_full", 1), ("q_empty", 2)))
-    kf, vf = ([Bar(f"{x}{s}", 1) for s in range(stages)] for x in ("k_full", "v_full"))
-    ke, ve = ([Bar(f"{x}{s}", 2) for s in range(stages)] for x in ("k_empty", "v_empty"))
-    sf, pf, pv = ([[Bar(f"{x}{t}{b}", c) for b in range(2)] for t in range(2)] for x, c in
-                  (("s_full", 1), ("p_full", 4), ("pv_done", 1)))
+    qf, qe = Bar("q_full", 1), Bar("q_empty", 2)
+    full, empty = ([Bar(f"{x}{s}", c) for s in range(stages)] for x, c in (("kv_full", 1), ("kv_empty", 2)))
+    sf, pf = ([[Bar(f"{x}{t}{b}", c) for b in range(2)] for t in range(2)] for x, c in (("s_full", 1), ("p_full", 4)))
+    od = [[Bar(f"o_done{t}{x}", 1) for x in range(2)] for t in range(2)]
     drain = [Bar(f"drain{t}", 1) for t in range(2)]
     pending, tensor = [], [[], []]  # tensor: the products of either MMA thread
-    held_q = [None, None]
-    held_k, held_v = [None] * stages, [None] * stages  # key tile that each stage holds
+    held_q = [None]
+    held = [None] * stages  # key tile that each stage holds
     s_of = [[None, None], [None, None]]  # ("s" or "p", item, step) in the buffers of S_t
     o_of = [None, None]   # item that O_t accumulates, and the steps it has
     o_read = [set(), set()]
@@ -46,79 +45,86 @@ def prompt_cta(items, stages, rnd, skip=None):
     def producer():
         g = 0
         for k, (n0, n1, _) in enumerate(items):
-            if k >= 2:
-                yield from waits(qe[k & 1], (k - 2) >> 1, "q_empty")
-            held_q[k & 1] = None
+            if k >= 1:
+                yield from waits(qe, k - 1, "q_empty")
+            held_q[0] = None
 
             def q_lands(k=k):
-                held_q[k & 1] = k
-                qf[k & 1].arrive()
+                held_q[0] = k
+                qf.arrive()
 
             pending.append(q_lands)
             for j in range(max(n0, n1)):
-                s, use = g % stages, g // stages
-                for full, empty, held, name in ((kf, ke, held_k, "k_empty"), (vf, ve, held_v, "v_empty")):
-                    if g >= stages:
-                        yield from waits(empty[s], use - 1, name)
-                    held[s] = None  # (the copy may write from now on)
+                s = g % stages
+                if g >= stages:
+                    yield from waits(empty[s], g // stages - 1, "kv_empty")
+                held[s] = None  # (the copy may write from now on)
 
-                    def lands(full=full, held=held, s=s, g=g):
-                        held[s] = g
-                        full[s].arrive()
+                def lands(s=s, g=g):
+                    held[s] = g
+                    full[s].arrive()
 
-                    pending.append(lands)
-                    yield
+                pending.append(lands)
+                yield
                 g += 1
 
     total = sum(max(n0, n1) for n0, n1, _ in items)
 
     def mma(t):
         """The thread of row tile t."""
-        at = dict(k=0, j=0, g=0, n=0)  # of S
+        at = dict(k=0, j=0, g=0, n=0, ready=False)  # of S
 
-        def step_s():
-            k, j, g = at["k"], at["j"], at["g"]
-            n0, n1, _ = items[k]
-            s, b = g % stages, at["n"] & 1
-            yield from waits(kf[s], g // stages, "k_full")
-            if j == 0:
-                yield from waits(qf[k & 1], k >> 1, "q_full")
-            last = j + 1 == max(n0, n1)
-            if j < (n0, n1)[t]:
-                def effect():
-                    assert s_of[t][b] is None, ("S overwrites", s_of[t][b])
-                    assert held_q[k & 1] == k and held_k[s] == g, "Q or K is not there"
-                    s_of[t][b] = ("s", k, j)
-
-                issue(t, effect, [sf[t][b], ke[s]] + ([qe[k & 1]] if last else []))
-                at["n"] += 1
-            else:
-                ke[s].arrive()
-                if last:
-                    issue(t, lambda: None, [qe[k & 1]])
+        def next_s():
+            last = at["j"] + 1 == max(items[at["k"]][:2])
+            if last:
+                issue(t, lambda: None, [qe])
+                at["j"], at["k"] = -1, at["k"] + 1
             at["g"] += 1
             at["j"] += 1
-            if last:
-                at["j"], at["k"] = 0, k + 1
-            yield
+
+        def prepare_s(end):
+            while not at["ready"] and at["g"] < min(end, total):
+                k, s = at["k"], at["g"] % stages
+                yield from waits(full[s], at["g"] // stages, "kv_full")
+                if at["j"] == 0:
+                    yield from waits(qf, k, "q_full")
+                at["ready"] = at["j"] < items[k][t]
+                if not at["ready"]:
+                    next_s()
+                yield
+
+        def issue_s():
+            k, j, g, s, b = at["k"], at["j"], at["g"], at["g"] % stages, at["n"] & 1
+
+            def effect():
+                assert s_of[t][b] is None, ("S overwrites", s_of[t][b])
+                assert held_q[0] == k and held[s] == g, "Q or K is not there"
+                s_of[t][b] = ("s", k, j)
+
+            issue(t, effect, [sf[t][b]])
+            at["n"] += 1
+            at["ready"] = False
+            next_s()
 
         np, g = 0, 0
         for k, item in enumerate(items):
             for j in range(max(item[0], item[1])):
-                while at["g"] < total and (skip == "lead" or at["g"] < g + stages) and \
-                        (at["n"] < np + 2 or at["j"] >= items[at["k"]][t]):
-                    yield from step_s()
+                while True:
+                    yield from prepare_s(total if skip == "lead" else g + stages)
+                    if not at["ready"] or at["n"] >= np + 2:
+                        break
+                    issue_s()
+                    yield
                 s, b = g % stages, np & 1
-                yield from waits(vf[s], g // stages, "v_full")
                 if j >= item[t]:
-                    ve[s].arrive()
+                    empty[s].arrive()
                     g += 1
                     continue
                 yield from waits(pf[t][b], np >> 1, "p_full")
 
                 def effect(g=g, s=s, k=k, j=j, b=b):
                     assert s_of[t][b] == ("p", k, j), ("P V of another tile", s_of[t][b], k, j)
-                    assert held_v[s] == g, "V is not there"
+                    assert held[s] == g, "V is not there"
                     if j == 0:
                         assert o_of[t] is None or o_of[t][0] in o_read[t], "O overwritten before it was read"
                         o_of[t] = (k, 0)
@@ -126,7 +132,9 @@ def prompt_cta(items, stages, rnd, skip=None):
                     o_of[t] = (k, j + 1)
                     s_of[t][b] = None
 
-                issue(t, effect, [pv[t][b], ve[s]])
+                issue(t, effect, [empty[s]] + ([od[t][j == item[t] - 1]] if j >= item[t] - 2 else []))
+                if at["ready"]:
+                    issue_s()
                 np += 1
                 g += 1
                 yield
@@ -135,6 +143,8 @@ def prompt_cta(items, stages, rnd, skip=None):
 
     def softmax(t):
         g0 = n = 0
+        n_o = [0, 0]
+
         for k, (n0, n1, two) in enumerate(items):
             nk = (n0, n1)[t]
             if t == 0 or two:
@@ -144,18 +154,23 @@ def prompt_cta(items, stages, rnd, skip=None):
                     assert s_of[t][b] == ("s", k, j), ("read another S", s_of[t][b], k, j)
                     yield
                     if j and rnd.random() < 0.3:  # a row's maximum grew: O is rescaled
-                        yield from waits(pv[t][b ^ 1], (n - 1) >> 1, "pv_rescale")
+                        if j + 1 < nk:
+                            yield from waits(sf[t][b ^ 1], (n + 1) >> 1, "s_rescale")
+                        else:
+                            yield from waits(od[t][0], n_o[0], "o_rescale")
                         assert o_of[t] == (k, j), "O rescaled before its products"
                     if j + 1 == max(n0, n1) and rnd.random() < 0.5:  # the last tile's V rows past the end
                         v = g0 + j
-                        yield from waits(vf[v % stages], v // stages)
-                        assert held_v[v % stages] == v
+                        yield from waits(full[v % stages], v // stages)
+                        assert held[v % stages] == v
                     s_of[t][b] = ("p", k, j)
                     pf[t][b].arrive(4)
                     yield
                     n += 1
                 if nk:
-                    yield from waits(pv[t][(n - 1) & 1], (n - 1) >> 1, "pv_last")
+                    for x in range(0 if nk >= 2 else 1, 2):
+                        yield from waits(od[t][x], n_o[x], "o_done")
+                        n_o[x] += 1
                     assert o_of[t] == (k, nk), "output read before its last product"
                     out[t][k] = nk
                     yield
@@ -177,20 +192,20 @@ def draw(rnd, most=6):
     return items
 
 
-@pytest.mark.parametrize("stages", [3, 6])
+@pytest.mark.parametrize("stages", [3, 5, 8])
 @pytest.mark.parametrize("seed", range(150))
 def test_prompt_protocol(seed, stages):
     rnd = random.Random(seed)
     prompt_cta(draw(rnd, rnd.choice([1, 2, 6])), stages, rnd)
 
 
-@pytest.mark.parametrize("skip", ["q_empty", "k_empty", "v_empty", "p_full", "v_full", "k_full", "q_full",
-                                  "s_full", "pv_last", "pv_rescale", "lead"])
+@pytest.mark.parametrize("skip", ["q_empty", "kv_empty", "p_full", "kv_full", "q_full", "s_full", "s_rescale", "o_rescale",
+                                  "o_done", "lead"])
 def test_a_wait_left_out_is_found(skip):
     for seed in range(200):
         rnd = random.Random(1000 + seed)
         try:
-            prompt_cta(draw(rnd, rnd.choice([1, 2, 6])), rnd.choice([3, 6]), rnd, skip)
+            prompt_cta(draw(rnd, rnd.choice([1, 2, 6])), rnd.choice([3, 5]), rnd, skip)
         except AssertionError:
             return
     assert False, "no schedule shows it"
