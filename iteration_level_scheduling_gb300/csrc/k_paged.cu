@@ -997,8 +997,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 // tiles.  Shared memory: Q and a ring of key tiles; the loads are
 // boxes of a page (or of the part of it that divides 64 slots), a lane of the
 // TMA warp each.
-// O is rescaled only where a row's maximum grew by more than 2^8, as every P is
-// formed against the maximum that O and l carry.
+// Every P is formed against the m that O and l carry, which is near a row's
+// maximum and need not be it: O is rescaled only where it lags by more than 2^8.
 // Keys past the item's last are masked by index and their V rows zeroed.  A
 // masked weight of 0 times a value that is not finite is NaN: rows whose output
 // is not finite are computed once more, key by key, over what they see.
@@ -1008,18 +1008,19 @@ constexpr int kPpThreads = 384;  // two softmax warpgroups, one with the TMA and
 constexpr int kPpTma = 8, kPpMma = 9;  // warps: the second MMA warp follows the first
 constexpr uint32_t kPpAtom = 16384;    // 128 rows of 128 bytes (Q)
 constexpr uint32_t kPpKv = 8192;       // 64 rows of 128 bytes (K, V)
-constexpr float kPpRescale = 8.f;
+constexpr float kPpGrown = 256.f;       // sum of a tile's weights from which on m follows
 
 template <int D>
 struct PpLayout {
     static constexpr int kAtoms = D / 64;
-    static constexpr int kStages = D == 64 ? 8 : 5;
+    static constexpr int kStages = D == 64 ? 8 : 4;
     static constexpr uint32_t kTile = kAtoms * kPpKv;  // a key tile's K or V
     static constexpr uint32_t kQ = 0;                  // [tile][atom]
     static constexpr uint32_t kK = 2 * kAtoms * kPpAtom;
     static constexpr uint32_t kV = kK + kStages * kTile;
     static constexpr uint32_t kBars = kV + kStages * kTile;
-    static constexpr uint32_t kBytes = kBars + 512;
+    static constexpr uint32_t kOut = kBars + 512;  // per softmax warp: 32 rows of 32 components, 80 bytes apart
+    static constexpr uint32_t kBytes = kOut + 8 * 32 * 80;
 };
 struct PpBars {
     uint64_t q_full, q_empty, kv_full[8], kv_empty[8];
@@ -1450,118 +1451,115 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         __syncwarp();
     } else if (warp < kPpTma) {
         // ------------------------------ softmax ------------------------------
+        // A thread per row.  What bounds it is the number of instructions between one S and the next: a tile's weights
+        // are formed against the m that is there, without a look at its maximum, and m follows with the next tile where
+        // their sum shows that it lags by more than 2^8 (O and l with it).  What overflows meanwhile is not finite in O
+        // and is computed once more below.
         // (A wait that gave up sets the abort flag, and the rest runs through on what is there.)
         const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_t = tmem + ((uint32_t)(quarter * 32) << 16), o_t = lane_t + 256u + 128u * t;
+        const uint32_t s_full = smem_u32(&bar.s_full[t][0]);
         uint32_t g0 = 0, n = 0, n_before = 0, n_last = 0;  // the item's first key tile, this row tile's so far, o_done's
+        uint32_t s[64];
+        const auto load = [&](uint32_t n) {  // starts the load of this row tile's n-th S
+            pp_wait(s_full + 8u * (n & 1u), n >> 1 & 1u, a.err, abort);
+            tc_fence_after();
+            const uint32_t s_t = lane_t + 128u * t + 64u * (n & 1u);
+            pp_ld32(s_t, s);
+            pp_ld32(s_t + 32, s + 32);
+        };
         Item it;
         for (int k = 0; item_at(k, it); g0 += it.n_kt, ++k) {
             const int n_rows = t ? it.n_rows[1] : it.n_rows[0], nk = t ? it.nk[1] : it.nk[0];
             if (n_rows == 0) continue;
             const int jr = r / a.pack, sees = it.sees + t * tile_rows + jr;  // keys 0 .. sees - 1 of the item are this row's
-            const int first_sees = it.sees + t * tile_rows;
-            float m = -INFINITY, l = 0.f;  // (m in the units of S)
-            uint32_t s[64];
-            const auto load = [&](uint32_t n) {  // starts the load of this row tile's n-th S
-                wait(&bar.s_full[t][n & 1u], n >> 1);
-                tc_fence_after();
-                pp_ld32(lane_t + 128u * t + 64u * (n & 1u), s);
-                pp_ld32(lane_t + 128u * t + 64u * (n & 1u) + 32, s + 32);
-            };
+            const int clean = min(it.sees + t * tile_rows, it.keys) / kPpKeys;  // key tiles that all rows see in full
+            float m = -INFINITY, l = 0.f, neg = 0.f, last = 0.f;  // m in the units of S, neg = -m scale, the last tile's sum
+            bool big = false;                                     // s scale - m in one step would keep what m lost
             for (int j = 0; j < nk; ++j, ++n) {
-                const int kbase = j * kPpKeys;
                 const uint32_t b = n & 1u, s_t = lane_t + 128u * t + 64u * b;
                 load(n);
+                const bool slow = __any_sync(kFull, last > kPpGrown || m == -INFINITY);
                 pp_wait_ld32(s);
                 pp_wait_ld32(s + 32);
-                if (kbase + kPpKeys > first_sees || kbase + kPpKeys > it.keys) {
-                    const int valid = min(sees, it.keys) - kbase;
+                if (j >= clean) {
+                    const int valid = min(sees, it.keys) - j * kPpKeys;
 #pragma unroll
                     for (int x = 0; x < 64; ++x)
                         if (x >= valid) s[x] = 0xff800000u;
                 }
-                // Weights are formed against the last tile's m while the maximum is taken, and once more in the rare
-                // tile that lifts it by more than 2^8 (the first, and scores where s scale - m in one step would keep
-                // what m lost to rounding: maximum first).
-                bool known = j == 0 || __any_sync(kFull, fabsf(m * a.scale_log2) > 16384.f);
-                float top = -INFINITY, ls;
-                if (known) {
+                if (slow) {
+                    float top = -INFINITY;
 #pragma unroll
                     for (int x = 0; x < 64; x += 2) top = pp_max3(top, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
-                }
-                for (;;) {
-                    float neg = -cw_base(m) * a.scale_log2;
-                    if (known) {
-                        float alpha = 1.f;
-                        if (j == 0) {
-                            m = top;
-                        } else if ((top - m) * a.scale_log2 > kPpRescale) {  // (from no key seen, -inf, as well)
-                            alpha = cw_exp2((m - top) * a.scale_log2);
-                            m = top;
-                            l *= alpha;
-                        }
-                        if (__any_sync(kFull, alpha != 1.f)) {  // O: once the P V so far are done
-                            // (the next S was issued behind them)
-                            if (j + 1 < nk)
-                                wait(&bar.s_full[t][b ^ 1u], (n + 1) >> 1);
-                            else
-                                wait(&bar.o_done[t][0], n_before);
-                            tc_fence_after();
+                    float alpha = 1.f;
+                    if (m == -INFINITY) {  // no key seen so far: O and l are 0
+                        m = top;
+                    } else if (last > kPpGrown) {
+                        const float to = fmaxf(top, m + __log2f(last) / a.scale_log2);
+                        alpha = cw_exp2((m - to) * a.scale_log2);
+                        m = to;
+                        l *= alpha;
+                    }
+                    if (__any_sync(kFull, alpha != 1.f)) {  // (not in an item's first tile)
+                        // O: once the P V so far are done (the next S was issued behind them)
+                        if (j + 1 < nk)
+                            pp_wait(s_full + 8u * (b ^ 1u), (n + 1) >> 1 & 1u, a.err, abort);
+                        else
+                            wait(&bar.o_done[t][0], n_before);
+                        tc_fence_after();
 #pragma unroll 1
-                            for (int x = 0; x < D; x += 16) {
-                                float o[16];
-                                tmem_ld16(o_t + x, o);
-                                uint32_t w[16];
+                        for (int x = 0; x < D; x += 16) {
+                            float o[16];
+                            tmem_ld16(o_t + x, o);
+                            uint32_t w[16];
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
-                                pp_st16(o_t + x, w);
-                            }
-                        }
-                        neg = -cw_base(m) * a.scale_log2;
-                        if (__any_sync(kFull, fabsf(neg) > 16384.f)) {
-#pragma unroll
-                            for (int x = 0; x < 64; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) - cw_base(m));
-                            neg = 0.f;
+                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+                            pp_st16(o_t + x, w);
                         }
                     }
-                    const uint64_t scale2 = pp_pair(a.scale_log2, a.scale_log2), neg2 = pp_pair(neg, neg);
-                    uint64_t sum[2] = {0, 0};
-                    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                    for (int x = 0; x < 64; x += 32) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float s0 = __uint_as_float(s[x + 2 * e]), s1 = __uint_as_float(s[x + 2 * e + 1]);
-                            float p0, p1;
-                            mx[e & 1] = pp_max3(mx[e & 1], s0, s1);
-                            pp_unpair(pp_fma2(pp_pair(s0, s1), scale2, neg2), p0, p1);
-                            p0 = cw_exp2(p0), p1 = cw_exp2(p1);
-                            sum[e & 1] = pp_add2(sum[e & 1], pp_pair(p0, p1));
-                            w[e] = cw_pack(p0, p1);
-                        }
-                        pp_st16(s_t + x / 2, w);
-                    }
-                    float l0, l1;
-                    pp_unpair(pp_add2(sum[0], sum[1]), l0, l1);
-                    ls = l0 + l1;
-                    if (known) break;
-                    top = fmaxf(mx[0], mx[1]);
-                    known = __any_sync(kFull, (top - m) * a.scale_log2 > kPpRescale);
-                    if (!known) break;
+                    neg = -cw_base(m) * a.scale_log2;
+                    big = __any_sync(kFull, fabsf(neg) > 16384.f);
+                    if (big) neg = 0.f;
                 }
-                l += ls;
-                const int here = it.keys - kbase;  // V rows past the item's last key: zero, once they have landed
-                if (here < kPpKeys) {
-                    const uint32_t v = g0 + j, st = v % L::kStages;
-                    wait(&bar.kv_full[st], v / L::kStages);
-                    const int c = r / kPpKeys, vr = r % kPpKeys;  // (64 rows of up to two blocks)
-                    if (vr >= here && c < L::kAtoms)
+                if (big) {
 #pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            *reinterpret_cast<uint4 *>(sm + L::kV + st * L::kTile + c * kPpKv + vr * 128 + x * 16) =
-                                make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
+                    for (int x = 0; x < 64; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) - cw_base(m));
+                }
+                const uint64_t scale2 = pp_pair(a.scale_log2, a.scale_log2), neg2 = pp_pair(neg, neg);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int x = 0; x < 64; x += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float p0, p1;
+                        pp_unpair(pp_fma2(pp_pair(__uint_as_float(s[x + 2 * e]), __uint_as_float(s[x + 2 * e + 1])), scale2,
+                                          neg2),
+                                  p0, p1);
+                        p0 = cw_exp2(p0), p1 = cw_exp2(p1);
+                        sum[e & 1] = pp_add2(sum[e & 1], pp_pair(p0, p1));
+                        w[e] = cw_pack(p0, p1);
+                    }
+                    pp_st16(s_t + x / 2, w);
+                }
+                float l0, l1;
+                pp_unpair(pp_add2(sum[0], sum[1]), l0, l1);
+                last = l0 + l1;
+                l += last;
+                if (j >= clean) {
+                    const int here = it.keys - j * kPpKeys;  // V rows past the item's last key: zero, once they have landed
+                    if (here < kPpKeys) {
+                        const uint32_t v = g0 + j, st = v % L::kStages;
+                        wait(&bar.kv_full[st], v / L::kStages);
+                        const int c = r / kPpKeys, vr = r % kPpKeys;  // (64 rows of up to two blocks)
+                        if (vr >= here && c < L::kAtoms)
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                *reinterpret_cast<uint4 *>(sm + L::kV + st * L::kTile + c * kPpKv + vr * 128 + x * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                    }
                 }
                 pp_wait_st();
                 tc_fence_before();
@@ -1571,7 +1569,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             // ---- the item's output ----
             const bool mine = r < n_rows * a.pack;
             const int row = it.row + t * tile_rows + jr, head = it.vh * a.pack + r % a.pack;
-            bf16 *const dst = a.out + (int64_t)row * a.ld_out + (int64_t)head * D;
+            const int64_t out_at = mine ? (int64_t)row * a.ld_out + (int64_t)head * D : -1;
+            uint8_t *const stage = sm + L::kOut + warp * (32 * 80);
             const int64_t at = (int64_t)it.part * a.vheads + (int64_t)it.vh * (2 * kPpRows) + t * kPpRows + r;
             float *const part = a.part + at * D;
             bool bad = false;
@@ -1587,16 +1586,22 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                     pp_wait_ld32(o);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) bad |= (o[e] & 0x7f800000u) == 0x7f800000u;
-                    if (!mine) continue;
-                    if (it.part < 0) {
+                    if (it.part < 0) {  // by way of shared memory: four lanes write 64 bytes of a row
+                        float f[32];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            float f[8];
+                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
 #pragma unroll
-                            for (int z = 0; z < 8; ++z) f[z] = __uint_as_float(o[e + z]) * inv;
-                            store16(dst + x + e, f);
+                        for (int e = 0; e < 4; ++e) store16(reinterpret_cast<bf16 *>(stage + lane * 80) + 8 * e, f + 8 * e);
+                        __syncwarp();
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const int rr = 8 * z + (lane >> 2);
+                            const int64_t to = __shfl_sync(kFull, out_at, rr);
+                            const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 80 + (lane & 3) * 16);
+                            if (to >= 0) *reinterpret_cast<uint4 *>(a.out + to + x + (lane & 3) * 8) = v;
                         }
-                    } else {
+                        __syncwarp();
+                    } else if (mine) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             *reinterpret_cast<uint4 *>(part + x + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
@@ -1607,7 +1612,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 for (int x = 0; x < D; x += 4) *reinterpret_cast<uint4 *>(part + x) = make_uint4(0, 0, 0, 0);
             }
             if (mine && it.part >= 0) *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m * a.scale_log2, l);
-            unsigned todo = __ballot_sync(kFull, mine && (bad || l != l));
+            unsigned todo = __ballot_sync(kFull, mine && (bad || (l - l) != 0.f));
             for (; todo; todo &= todo - 1) {  // rows with something that is not finite, over what they see
                 const int rr = quarter * 32 + __ffs(todo) - 1;
                 const int row2 = it.row + t * tile_rows + rr / a.pack, head2 = it.vh * a.pack + rr % a.pack;
