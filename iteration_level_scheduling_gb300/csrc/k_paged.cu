@@ -473,6 +473,7 @@ struct PagedArgs {
     const int4 *items;  // {tiles at, keys, first row, first column}, {columns, last key of row 0, part or -1, 0}
     int64_t ld_q, ld_out;
     int n_items, kv_heads, group;
+    int beside;  // another kernel of the same call was launched before this one
     float scale_log2;
     unsigned *err;
 };
@@ -485,14 +486,17 @@ struct CwShape {
     static constexpr uint32_t kBox = 2 * 16 * kRow;             // K and V of 16 keys
     static constexpr uint32_t kStage = kBlocks * kBox;
     static constexpr int kWant = (NT == 1 ? 24576 : 16384) / (int)kStage;
-    static constexpr int kStages = kWant < 2 ? 2 : kWant > 8 ? 8 : kWant;
-    static constexpr int kMerge = NT < 2 ? 8 : 16;  // columns that meet at a time
+    static constexpr int kStages = kWant < 1 ? 1 : kWant > 8 ? 8 : kWant;
+    static constexpr bool kQInSmem = kEs == 4 || NT == 4;  // (else the queries' fragments fit into registers)
+    static constexpr int kMerge = 8;                       // columns that meet at a time
+    static constexpr int kQRow = D * kEs + 16;             // bytes from column to column (no bank conflicts)
     static constexpr int kLd = D + 4;               // floats from column to column (no bank conflicts)
     static constexpr uint32_t kRing = kCwWarps * kStages * kStage;
     static constexpr uint32_t kO = kRing;
     static constexpr uint32_t kMl = kO + kCwWarps * kMerge * kLd * 4;
     static constexpr uint32_t kBars = kMl + kCwWarps * kMerge * 8;
-    static constexpr uint32_t kBytes = kBars + kCwWarps * kStages * 8;
+    static constexpr uint32_t kQ = (kBars + kCwWarps * kStages * 8 + 15) / 16 * 16;  // two items' queries
+    static constexpr uint32_t kBytes = kQ + (kQInSmem ? 2 * 8 * NT * kQRow : 0);
 };
 
 __device__ __forceinline__ void store4(float *p, float a, float b, float c, float d) {
@@ -545,14 +549,11 @@ __device__ __forceinline__ uint32_t cw_pack(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-// fp32 operands as two tf32 parts of 11 bits each, x = hi + lo up to 2^-22 |x|:
-// products hi hi + hi lo + lo hi.  An infinity has no lower part and takes no part
-// in the mixed products (0 * inf, inf - inf): they use `fin`.
-__device__ __forceinline__ void cw_split(uint32_t x, uint32_t &hi, uint32_t &lo, uint32_t &fin) {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "r"(x));
-    const float rest = hi == x ? 0.f : __uint_as_float(x) - __uint_as_float(hi);
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
-    fin = (hi & 0x7fffffffu) == 0x7f800000u ? 0u : hi;
+// fp32 operands as two tf32 parts, x = hi + lo: hi cut off, lo rounded to 11 bits, which leaves 2^-21 |x|; products
+// hi hi + hi lo + lo hi.  An infinity has no lower part (inf - inf): what it touches becomes NaN.
+__device__ __forceinline__ void cw_split(uint32_t x, uint32_t &hi, uint32_t &lo) {
+    hi = x & 0xffffe000u;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(__uint_as_float(x) - __uint_as_float(hi)));
 }
 __device__ __forceinline__ void cw_mma_tf32(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -575,10 +576,9 @@ __global__ void __launch_bounds__(kCwThreads, 2)
     using S = CwShape<T, D, NT>;
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int KS = D / (F32 ? 8 : 16), MT = D / 16;
-    constexpr bool kKeepQ = NT <= 2 && !F32;  // the queries' fragments stay in registers (else they come from L1 every tile)
+    constexpr bool kKeepQ = !S::kQInSmem;
     constexpr unsigned kFull = 0xffffffffu;
     extern __shared__ __align__(1024) uint8_t cw_smem[];
-    pdl_trigger();
     if (smem_u32(cw_smem) & 1023u) {  // uniform: every thread leaves
         if (threadIdx.x == 0) raise_err(a.err, 8u);
         return;
@@ -594,7 +594,10 @@ __global__ void __launch_bounds__(kCwThreads, 2)
         if (warp == 0) prefetch_tmap(&tm);
     }
     __syncwarp();
-    pdl_wait();
+    // The first kernel of a call triggers behind its wait, so that all in front of the call has ended when the next
+    // one starts: that one need not wait for the first, which it does not depend on, but before it ends.
+    if (!a.beside) pdl_wait();
+    pdl_trigger();
 
     const int total = a.n_items * a.kv_heads, G = gridDim.x;
     // The block's k-th (item, key/value head): items come longest first, dealt forwards and backwards in turn.
@@ -634,9 +637,35 @@ __global__ void __launch_bounds__(kCwThreads, 2)
     };
     for (int s = 0; s < S::kStages; ++s) issue();
 
+    // Queries of entry e to shared memory, buffer `buf` (columns behind the last repeat it and are not written).
+    const auto fetch_q = [&](int e, int buf) {
+        if (e < total) {
+            const int4 r = a.items[2 * (e / a.kv_heads)];
+            const int cols = a.items[2 * (e / a.kv_heads) + 1].x, h = e % a.kv_heads;
+            constexpr int CH = D * S::kEs / 16;
+            for (int x = threadIdx.x; x < 8 * NT * CH; x += kCwThreads) {
+                const int c = r.w + min(x / CH, cols - 1);
+                const T *src = reinterpret_cast<const T *>(a.q) + (int64_t)(r.z + c / a.group) * a.ld_q +
+                               (h * a.group + c % a.group) * D + x % CH * (16 / S::kEs);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 smem_u32(cw_smem) + S::kQ + (buf * 8 * NT + x / CH) * S::kQRow + x % CH * 16),
+                             "l"(src)
+                             : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if constexpr (!kKeepQ) fetch_q(nth(0), 0);
+
     for (int k = 0;; ++k) {
         const int e = nth(k);
         if (e >= total) break;
+        if constexpr (!kKeepQ) {
+            fetch_q(nth(k + 1), (k + 1) & 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncthreads();
+        }
+        const uint32_t qs = smem_u32(cw_smem) + S::kQ + (k & 1) * 8 * NT * S::kQRow;
         const int h = e % a.kv_heads;
         const int4 r0 = a.items[2 * (e / a.kv_heads)], r1 = a.items[2 * (e / a.kv_heads) + 1];
         const int keys = r0.y, n_tiles = (keys + 15) / 16, c0 = r0.w, n_cols = r1.x, last0 = r1.y;
@@ -649,17 +678,17 @@ __global__ void __launch_bounds__(kCwThreads, 2)
 #pragma unroll
             for (int i = 0; i < 2; ++i) sees[nt][i] = last0 + (c0 + 8 * nt + 2 * t4 + i) / a.group + 1;
         // q as the second operand: column g8, components 2 t4 + {0, 1} and + 8 of every 16
-        const uint32_t *qp[NT];
         uint32_t qb[NT][kKeepQ ? KS : 1][2];
+        if constexpr (kKeepQ) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int c = c0 + min(8 * nt + g8, n_cols - 1);  // (columns behind the last repeat it and are not written)
-            qp[nt] = reinterpret_cast<const uint32_t *>(reinterpret_cast<const T *>(a.q) +
-                                                        (int64_t)(r0.z + c / a.group) * a.ld_q +
-                                                        (h * a.group + c % a.group) * D) + t4;
-            if constexpr (kKeepQ)
+            for (int nt = 0; nt < NT; ++nt) {
+                const int c = c0 + min(8 * nt + g8, n_cols - 1);
+                const uint32_t *qp = reinterpret_cast<const uint32_t *>(reinterpret_cast<const T *>(a.q) +
+                                                                        (int64_t)(r0.z + c / a.group) * a.ld_q +
+                                                                        (h * a.group + c % a.group) * D) + t4;
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) qb[nt][ks][0] = qp[nt][8 * ks], qb[nt][ks][1] = qp[nt][8 * ks + 4];
+                for (int ks = 0; ks < KS; ++ks) qb[nt][ks][0] = qp[8 * ks], qb[nt][ks][1] = qp[8 * ks + 4];
+            }
         }
         float m[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
@@ -690,17 +719,18 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                 for (int x = 0; x < NC * NT * 4; ++x) (&hh[0][0][0])[x] = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t f[4], fh[4], fl[4], ff[4], qh[2], ql[2], qf[2];
+                    uint32_t f[4], fh[4], fl[4], qh[2], ql[2];
                     cw_ldsm(at(kb, lane & 15, 2 * ks + (lane >> 4)), f);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) cw_split(f[x], fh[x], fl[x], ff[x]);
+                    for (int x = 0; x < 4; ++x) cw_split(f[x], fh[x], fl[x]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        cw_split(qp[nt][8 * ks], qh[0], ql[0], qf[0]);
-                        cw_split(qp[nt][8 * ks + 4], qh[1], ql[1], qf[1]);
+                        const uint32_t q = qs + (8 * nt + g8) * S::kQRow + (8 * ks + t4) * 4;
+                        cw_split(cw_lds(q), qh[0], ql[0]);
+                        cw_split(cw_lds(q + 16), qh[1], ql[1]);
                         cw_mma_tf32(hh[ks % NC][nt], fh, qh[0], qh[1]);
-                        cw_mma_tf32(c[nt], ff, ql[0], ql[1]);
-                        cw_mma_tf32(c[nt], fl, qf[0], qf[1]);
+                        cw_mma_tf32(c[nt], fh, ql[0], ql[1]);
+                        cw_mma_tf32(c[nt], fl, qh[0], qh[1]);
                     }
                 }
 #pragma unroll
@@ -709,18 +739,50 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                     for (int x = 0; x < 4; ++x)
 #pragma unroll
                         for (int n = 0; n < NC; ++n) c[nt][x] += hh[n][nt][x];
+                // an infinity, or a NaN: these scores once more, component by component
+                bool odd = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) odd |= c[nt][x] != c[nt][x] && 16 * t + g8 + 8 * (x >> 1) < keys;
+                if (__any_sync(kFull, odd))
+#pragma unroll 1
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                        for (int d = 0; d < D; ++d)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                z[x] = fmaf(__uint_as_float(cw_lds(at(kb, g8 + 8 * (x >> 1), d / 4) + d % 4 * 4)),
+                                            __uint_as_float(cw_lds(qs + (8 * nt + 2 * t4 + (x & 1)) * S::kQRow + d * 4)),
+                                            z[x]);
+#pragma unroll
+                        for (int y = 0; y < NT; ++y)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                if (y == nt) c[y][x] = z[x];
+                    }
+            } else if constexpr (!kKeepQ) {
+#pragma unroll
+                for (int k2 = 0; k2 < KS; k2 += 2) {  // (head_dim 16: the second half of a load is not used)
+                    uint32_t f[2][4], q[4];
+#pragma unroll
+                    for (int z = 0; z < 2 && k2 + z < KS; ++z) cw_ldsm(at(kb, lane & 15, 2 * (k2 + z) + (lane >> 4)), f[z]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int ch = KS == 1 ? (lane >> 3 & 1) : 2 * k2 + (lane >> 3);
+                        cw_ldsm(qs + (8 * nt + (lane & 7)) * S::kQRow + ch * 16, q);
+#pragma unroll
+                        for (int z = 0; z < 2 && k2 + z < KS; ++z) cw_mma_bf16(c[nt], f[z], q[2 * z], q[2 * z + 1]);
+                    }
+                }
             } else {
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     uint32_t f[4];
                     cw_ldsm(at(kb, lane & 15, 2 * ks + (lane >> 4)), f);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if constexpr (kKeepQ)
-                            cw_mma_bf16(c[nt], f, qb[nt][ks][0], qb[nt][ks][1]);
-                        else
-                            cw_mma_bf16(c[nt], f, qp[nt][8 * ks], qp[nt][8 * ks + 4]);
-                    }
+                    for (int nt = 0; nt < NT; ++nt) cw_mma_bf16(c[nt], f, qb[nt][ks][0], qb[nt][ks][1]);
                 }
             }
             // scores of keys 16 t + g8 and + 8, columns 2 t4 and + 1 of every 8; those not seen are -inf
@@ -824,8 +886,7 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                             const int src = (2 * t4 + i) * 4 + (g8 >> 1);
                             const float p0 = __shfl_sync(kFull, c[nt][2 * x], src);
                             const float p1 = __shfl_sync(kFull, c[nt][2 * x + 1], src);
-                            uint32_t unused;  // (weights are finite, or their column is NaN)
-                            cw_split(__float_as_uint(g8 & 1 ? p1 : p0), ph[nt][x][i], pl[nt][x][i], unused);
+                            cw_split(__float_as_uint(g8 & 1 ? p1 : p0), ph[nt][x][i], pl[nt][x][i]);
                         }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
@@ -834,16 +895,16 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                     for (int nt = 0; nt < NT; ++nt) y[nt][0] = y[nt][1] = y[nt][2] = y[nt][3] = 0.f;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        uint32_t fh[4], fl[4], ff[4];
+                        uint32_t fh[4], fl[4];
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
                             const int d = 16 * mt + g8 + 8 * (z & 1);
-                            cw_split(cw_lds(at(vb, 8 * x + 2 * t4 + (z >> 1), d / 4) + d % 4 * 4), fh[z], fl[z], ff[z]);
+                            cw_split(cw_lds(at(vb, 8 * x + 2 * t4 + (z >> 1), d / 4) + d % 4 * 4), fh[z], fl[z]);
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             cw_mma_tf32(y[nt], fl, ph[nt][x][0], ph[nt][x][1]);
-                            cw_mma_tf32(y[nt], ff, pl[nt][x][0], pl[nt][x][1]);
+                            cw_mma_tf32(y[nt], fh, pl[nt][x][0], pl[nt][x][1]);
                             cw_mma_tf32(y[nt], fh, ph[nt][x][0], ph[nt][x][1]);
                         }
                     }
@@ -924,6 +985,7 @@ __global__ void __launch_bounds__(kCwThreads, 2)
     }
     // a wait that gave up: the copies in flight land before the block ends
     for (; used < issued; ++used) mbar_wait_bounded(&full[used % S::kStages], (used / S::kStages) & 1u, a.err);
+    if (a.beside) pdl_wait();
 }
 
 // Split keys: the parts of a column, in their order.  One block per (column tile,
@@ -1226,7 +1288,6 @@ __global__ void __launch_bounds__(kPpThreads, 1)
     using L = PpLayout<D>;
     constexpr unsigned kFull = 0xffffffffu;
     extern __shared__ __align__(1024) uint8_t pp_smem[];
-    pdl_trigger();
     if (smem_u32(pp_smem) & 1023u) {  // uniform: every thread leaves before any barrier
         if (threadIdx.x == 0) raise_err(a.err, 8u);
         return;
@@ -1261,6 +1322,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
     pdl_wait();
+    pdl_trigger();  // (behind the wait: paged_cols_kernel may run beside this one)
 
     const int total = a.n_items * a.vheads, G = gridDim.x, tile_rows = kPpRows / a.pack;
     struct Item {
@@ -1727,7 +1789,7 @@ cudaError_t launch_attention(const PagedAttn &p, const int32_t *hp, const int32_
         a.items = reinterpret_cast<const int4 *>(at), a.n_items = hp[G_ITEMS + c];
         at += 8 * (int64_t)a.n_items;
         if (!a.n_items) continue;
-        ++*launches;
+        a.beside = (*launches)++ > 0;
         if (c == 0)
             e = launch_cols<T, D, 1>(a, p.layer, hp[G_SLOTS], hp[G_SMS], st);
         else if (c == 1)
