@@ -1144,8 +1144,12 @@ bool overlap(const void *a, int64_t an, const void *b, int64_t bn) {
 int64_t orca_paged_plan_words(const orca_engine *E, const orca_paged_batch *batch) {
     PagedBatch b;
     if (!paged_batch(batch, &b)) return ORCA_ERR_INVALID;
-    const int64_t w = paged_plan_words(b, E ? E->num_sms : kPlanSms);
-    return w < 0 ? ORCA_ERR_INVALID : w;
+    try {
+        const int64_t w = paged_plan_words(b, E ? E->num_sms : kPlanSms);
+        return w < 0 ? ORCA_ERR_INVALID : w;
+    } catch (const std::bad_alloc &) {
+        return ORCA_ERR_OOM;
+    }
 }
 
 int orca_paged_plan_build(const orca_engine *E, const orca_paged_batch *batch, int32_t *host_buf, int64_t cap_words) {

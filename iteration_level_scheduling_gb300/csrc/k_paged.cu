@@ -40,35 +40,41 @@ enum {  // header words of a plan
     G_ITEMS,                       // work items by class (8, 16, 32 columns)
     G_PARTS = G_ITEMS + kClasses,  // partial columns of split items (per key/value head)
     G_JOINS,                       // column tiles whose keys are split
-    G_JOINCOLS,                    // most columns of one
+    G_JOINROWS,                    // blocks that one takes per key/value head, at most
     G_O_ITEMS,                     // 8 words each, class by class, most keys first
     G_O_JOINS,                     // 8 words each
     G_PITEMS,                      // the same for prompts: pairs of row tiles
     G_PPARTS,
     G_PJOINS,
+    G_PJOINROWS,
     G_O_PITEMS,
     G_O_PJOINS,
     G_PACK,  // heads of a prompt's row tile
     G_BOX,   // slots that one load of a prompt's keys may take
 };
 constexpr int kCwCtasPerSm = 2;
-constexpr int kSplitAt = 256;  // fewest keys of a part
+constexpr int kManyParts = 16;  // parts of a column from which on a block joins it alone
 
 int64_t up4(int64_t x) { return (x + 3) & ~int64_t(3); }
 
 struct PagedSizes {
-    int64_t rows, tiles, maxpos, chunk, items[kClasses], parts, joins, join_cols;
-    int64_t pchunk, pitems, pparts, pjoins;
+    int64_t rows, tiles, maxpos, chunk, items[kClasses], parts, joins, join_rows;
+    int64_t pchunk, pitems, pparts, pjoins, pjoin_rows;
     int64_t off_rows, off_reqs, off_tiles, off_items, off_joins, off_pitems, off_pjoins, total;
 };
 
 // Prompts: rows x heads of one key/value head as the 128 rows of a tensor-core tile; two tiles share their keys, 64 at
 // a time.
-constexpr int kPromptCols = 32;  // columns of a request from which on it is one
+constexpr int kPromptCols = 64;  // columns from which on the longest request makes a batch's requests prompts
 constexpr int kPpRows = 128, kPpKeys = 64;
-bool is_prompt(const PagedBatch &b, int i) {
-    return b.dtype && b.head_dim >= 64 && (int64_t)b.n_input[i] * (b.n_heads / b.n_kv_heads) > kPromptCols;
+int64_t columns(const PagedBatch &b, int i) { return (int64_t)b.n_input[i] * (b.n_heads / b.n_kv_heads); }
+// Whether the batch has prompts: all requests above 32 columns are then, since both kernels take their time.
+bool has_prompts(const PagedBatch &b) {
+    int64_t most = 0;
+    for (int i = 0; i < b.n_req; ++i) most = std::max(most, columns(b, i));
+    return b.dtype && b.head_dim >= 64 && most > kPromptCols;
 }
+bool is_prompt(const PagedBatch &b, int i) { return columns(b, i) > 32; }
 // Heads in a tile: all that share a key/value head, or one where they are too many to fill 128 rows well.
 int pack_of(int group) { return group <= 64 ? group : 1; }
 
@@ -97,10 +103,44 @@ void row_pairs(const PagedBatch &b, int i, F fn) {
 // Parts that a tile's keys are cut into.
 int64_t parts_of(int64_t keys, int64_t chunk) { return keys * 2 <= chunk * 3 ? 1 : (keys + chunk - 1) / chunk; }
 
+// Keys of a part, in units of 64, by a model of the time: an item takes its units and `extra` more, a block its items
+// one after another (the longest first, so that the last start evens out to half of the longest), and parts have to
+// be joined.  `units`: the items' keys, each for `heads` heads.
+int64_t choose_chunk(const std::vector<int32_t> &units, int64_t heads, int64_t blocks, double extra, double join,
+                     double per_part) {
+    int64_t total = 0, most = 1;
+    for (const int32_t u : units) total += u * heads, most = std::max<int64_t>(most, u);
+    int64_t best = most;
+    double least = 0;
+    const int64_t cand[] = {most, total / blocks + 1, total / (2 * blocks) + 1, total / (3 * blocks) + 1,
+                            total / (6 * blocks) + 1, 48, 32, 24, 16, 12, 8, 6, 4};
+    for (const int64_t c : cand) {
+        if (c > most || c < 4) continue;
+        int64_t items = 0, parts = 0;
+        double cost = 0, longest = 0;
+        for (const int32_t u : units) {
+            const int64_t p = parts_of(u, c);
+            items += p * heads, cost += (double)heads * ((double)u + extra * (double)p);
+            longest = std::max(longest, (p == 1 ? u : c) + extra);
+            if (p > 1) parts += p * heads;
+        }
+        double t = items <= blocks ? longest : std::max(longest, cost / (double)blocks + longest / 2);
+        if (parts) t += join + per_part * (double)parts;
+        if (c == most || t < least) best = c, least = t;
+    }
+    return best;
+}
+
 bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
     *z = {};
-    int64_t work = 0, pwork = 0;
-    const int64_t vheads = b.n_heads / pack_of(b.n_heads / b.n_kv_heads);
+    std::vector<int32_t> work, pwork;  // 64 keys each
+    const int64_t pack = pack_of(b.n_heads / b.n_kv_heads), vheads = b.n_heads / pack;
+    const bool prompts = has_prompts(b);
+    // blocks of paged_join_kernel for the columns of a tile
+    const auto join_rows = [&](int64_t cols, int64_t parts) {
+        const int64_t per = 512 / b.head_dim;
+        return parts >= kManyParts ? cols : (cols + per - 1) / per;
+    };
     const int64_t slots = b.n_pages * b.page_size;
     for (int i = 0; i < b.n_req; ++i) {
         const int64_t n = b.n_input[i], c = b.ctx_len[i];
@@ -111,32 +151,31 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
         for (int64_t p = 0; p * b.page_size < c + n; ++p)
             if (t[p] < 0 || t[p] >= b.n_pages) return false;
         z->rows += n;
-        if (is_prompt(b, i))
-            row_pairs(b, i, [&](int64_t, int64_t, int64_t keys) { pwork += (keys + kPpKeys - 1) / kPpKeys * vheads; });
+        if (prompts && is_prompt(b, i))
+            row_pairs(b, i, [&](int64_t, int64_t, int64_t keys) { pwork.push_back((int32_t)((keys + 63) / 64)); });
         else
-            column_tiles(b, i, [&](int, int64_t, int64_t, int64_t keys) { work += keys * b.n_kv_heads; });
+            column_tiles(b, i, [&](int, int64_t, int64_t, int64_t keys) { work.push_back((int32_t)((keys + 63) / 64)); });
         z->tiles += up4((c + n + 15) / 16);
         z->maxpos = std::max(z->maxpos, c + n);
     }
-    // a third of a block's share, so that uneven items even out over the blocks
-    const int64_t share = work / ((int64_t)kCwCtasPerSm * num_sms * 3);
-    z->chunk = std::max<int64_t>(kSplitAt, (share + 63) / 64 * 64);
-    // half of a block's share of key tiles, eight at least
-    z->pchunk = std::max<int64_t>(16, pwork / num_sms / 2) * kPpKeys;
+    z->chunk = 64 * choose_chunk(work, b.n_kv_heads, (int64_t)kCwCtasPerSm * num_sms, 4.0, 2.0, 0.0);
+    z->pchunk = 64 * choose_chunk(pwork, vheads, num_sms, 3.0, 3.0, 0.03);
     for (int i = 0; i < b.n_req; ++i) {
         if (b.n_input[i] == 0) continue;
-        if (is_prompt(b, i)) {
-            row_pairs(b, i, [&](int64_t, int64_t, int64_t keys) {
+        if (prompts && is_prompt(b, i)) {
+            row_pairs(b, i, [&](int64_t, int64_t rows, int64_t keys) {
                 const int64_t parts = parts_of(keys, z->pchunk);
                 z->pitems += parts;
-                if (parts > 1) z->pparts += parts * 2 * kPpRows, z->pjoins++;
+                if (parts == 1) return;
+                z->pparts += parts * 2 * kPpRows, z->pjoins++;
+                z->pjoin_rows = std::max(z->pjoin_rows, join_rows(rows * pack, parts));
             });
             continue;
         }
         column_tiles(b, i, [&](int cl, int64_t, int64_t n, int64_t keys) {
             const int64_t parts = parts_of(keys, z->chunk);
             z->items[cl] += parts;
-            if (parts > 1) z->parts += parts * (8 << cl), z->joins++, z->join_cols = std::max(z->join_cols, n);
+            if (parts > 1) z->parts += parts * (8 << cl), z->joins++, z->join_rows = std::max(z->join_rows, join_rows(n, parts));
         });
     }
     int64_t w = kPagedHdr;
@@ -188,7 +227,7 @@ int64_t paged_plan_words(const PagedBatch &b, int num_sms) {
 bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t cap) {
     PagedSizes z;
     if (!paged_sizes(b, num_sms, &z) || cap < z.total) return false;
-    const bool twice = writes_twice(b);
+    const bool twice = writes_twice(b), prompts = has_prompts(b);
     std::memset(buf, 0, sizeof(int32_t) * (size_t)z.total);
     int32_t *row = buf + z.off_rows, *req = buf + z.off_reqs, *tile = buf + z.off_tiles;
     const int32_t per_page = b.page_size / 16;
@@ -245,7 +284,7 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
             pjoin[4] = (int32_t)ppart, pjoin[5] = 2 * kPpRows, pjoin[6] = tile_rows * pack;
             pjoin += 8, ppart += parts * 2 * kPpRows;
         };
-        if (is_prompt(b, i))
+        if (prompts && is_prompt(b, i))
             row_pairs(b, i, pair);
         else
             column_tiles(b, i, tile_items);
@@ -278,7 +317,8 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
     buf[G_JOINS] = (int32_t)z.joins;
     buf[G_O_ITEMS] = (int32_t)z.off_items;
     buf[G_O_JOINS] = (int32_t)z.off_joins;
-    buf[G_JOINCOLS] = (int32_t)z.join_cols;
+    buf[G_JOINROWS] = (int32_t)z.join_rows;
+    buf[G_PJOINROWS] = (int32_t)z.pjoin_rows;
     buf[G_PITEMS] = (int32_t)z.pitems;
     buf[G_PPARTS] = (int32_t)z.pparts;
     buf[G_PJOINS] = (int32_t)z.pjoins;
@@ -989,7 +1029,7 @@ __global__ void __launch_bounds__(kCwThreads, 2)
 }
 
 // Split keys: the parts of a column, in their order.  One block per (column tile,
-// head) and column; 4 components per thread, the parts dealt to the thread groups.
+// head) and column, or column per thread group; 4 components per thread.
 // `heads` and `group`: key/value heads and the query heads of each; for prompts
 // the tiles' heads and the heads packed into each.
 struct JoinArgs {
@@ -1006,12 +1046,13 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
     __shared__ float2 sml[N];
     pdl_trigger();
     pdl_wait();
-    const int j = blockIdx.x / a.heads, h = blockIdx.x % a.heads, x = blockIdx.y;
+    const int j = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
     const int4 r0 = a.joins[2 * j], r1 = a.joins[2 * j + 1];
-    // (a tile of 128 may hold fewer columns than that)
-    const int col = x / kPpRows * r1.z + x % kPpRows;
-    if (x >= r1.y || x % kPpRows >= r1.z || col >= r0.z) return;
     const int grp = threadIdx.x / L4, d = threadIdx.x % L4;
+    const bool many = r0.w >= kManyParts;  // the groups share a column's parts, else each has a column
+    const int col = many ? blockIdx.y : blockIdx.y * N + grp;
+    if ((many ? col : (int)blockIdx.y * N) >= r0.z) return;
+    const int x = col / r1.z * kPpRows + col % r1.z;  // (a tile of 128 may hold fewer columns than that)
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     const auto add = [&](float m2, float l2, const float4 &o2) {
@@ -1019,18 +1060,23 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
         l = l * f + l2 * f2, m = mx;
         o.x = o.x * f + o2.x * f2, o.y = o.y * f + o2.y * f2, o.z = o.z * f + o2.z * f2, o.w = o.w * f + o2.w * f2;
     };
+    if (col < r0.z) {
 #pragma unroll 4
-    for (int p = grp; p < r0.w; p += N) {
-        const int64_t at = ((int64_t)r1.x + (int64_t)p * r1.y) * a.heads + (int64_t)h * r1.y + x;
-        const float2 v = *reinterpret_cast<const float2 *>(a.part_ml + 2 * at);
-        add(v.x, v.y, *reinterpret_cast<const float4 *>(a.part + at * D + 4 * d));
+        for (int p = many ? grp : 0; p < r0.w; p += many ? N : 1) {
+            const int64_t at = ((int64_t)r1.x + (int64_t)p * r1.y) * a.heads + (int64_t)h * r1.y + x;
+            const float2 v = *reinterpret_cast<const float2 *>(a.part_ml + 2 * at);
+            add(v.x, v.y, *reinterpret_cast<const float4 *>(a.part + at * D + 4 * d));
+        }
     }
-    so[grp][d] = o;
-    if (d == 0) sml[grp] = make_float2(m, l);
-    __syncthreads();
-    if (grp) return;
+    if (many) {
+        so[grp][d] = o;
+        if (d == 0) sml[grp] = make_float2(m, l);
+        __syncthreads();
+        if (grp) return;
 #pragma unroll
-    for (int z = 1; z < N; ++z) add(sml[z].x, sml[z].y, so[z][d]);
+        for (int z = 1; z < N; ++z) add(sml[z].x, sml[z].y, so[z][d]);
+    }
+    if (col >= r0.z) return;
     const int c = r0.y + col;
     T *dst = reinterpret_cast<T *>(a.out) + (int64_t)(r0.x + c / a.group) * a.ld_out +
              (h * a.group + c % a.group) * D + 4 * d;
@@ -1738,7 +1784,7 @@ cudaError_t launch_prompts(const PagedAttn &p, const int32_t *hp, const int32_t 
     ++*launches;
     const JoinArgs j = {a.part, a.part_ml, reinterpret_cast<const int4 *>(dp + hp[G_O_PJOINS]), p.out, p.ld_out, a.vheads,
                         a.pack};
-    return launch_pdl(paged_join_kernel<bf16, D>, dim3((unsigned)hp[G_PJOINS] * a.vheads, 2 * kPpRows), dim3(128), 0, st,
+    return launch_pdl(paged_join_kernel<bf16, D>, dim3((unsigned)hp[G_PJOINS] * a.vheads, (unsigned)hp[G_PJOINROWS]), dim3(128), 0, st,
                       j);
 }
 
@@ -1801,7 +1847,7 @@ cudaError_t launch_attention(const PagedAttn &p, const int32_t *hp, const int32_
     ++*launches;
     const JoinArgs j = {a.part, a.part_ml, reinterpret_cast<const int4 *>(dp + hp[G_O_JOINS]), p.out, p.ld_out,
                         a.kv_heads, a.group};
-    return launch_pdl(paged_join_kernel<T, D>, dim3((unsigned)hp[G_JOINS] * a.kv_heads, (unsigned)hp[G_JOINCOLS]),
+    return launch_pdl(paged_join_kernel<T, D>, dim3((unsigned)hp[G_JOINS] * a.kv_heads, (unsigned)hp[G_JOINROWS]),
                       dim3(128), 0, st, j);
 }
 

@@ -106,8 +106,8 @@ def test_oracle_by_hand():
 
 
 # words of a plan's header (k_paged.cu)
-O_ROWS, O_REQS, O_TILES, ITEMS, PARTS, JOINS, JOINCOLS, O_ITEMS, O_JOINS = 10, 11, 12, 14, 17, 18, 19, 20, 21
-PITEMS, PPARTS, PJOINS, O_PITEMS, O_PJOINS, PACK, BOX = 22, 23, 24, 25, 26, 27, 28
+O_ROWS, O_REQS, O_TILES, ITEMS, PARTS, JOINS, JOINROWS, O_ITEMS, O_JOINS = 10, 11, 12, 14, 17, 18, 19, 20, 21
+PITEMS, PPARTS, PJOINS, PJOINROWS, O_PITEMS, O_PJOINS, PACK, BOX = 22, 23, 24, 25, 26, 27, 28, 29
 
 
 def cover(native, p, n, c, table, page, group, kv_heads):
@@ -159,14 +159,14 @@ def cover(native, p, n, c, table, page, group, kv_heads):
         assert spans[0][0] == 0 and spans[-1][1] == c[req_of[r]] + r - first[req_of[r]] + 1
         assert all(a[1] == b[0] for a, b in zip(spans, spans[1:]))
     joined = {}
-    for kind, off, count, unit in (("c", O_JOINS, JOINS, group), ("p", O_PJOINS, PJOINS, pack)):
+    per = 512 // int(p[4])  # columns that a block joins, if they have few parts
+    for kind, off, count, most, unit in (("c", O_JOINS, JOINS, JOINROWS, group), ("p", O_PJOINS, PJOINS, PJOINROWS, pack)):
         for r in p[p[off]:p[off] + 8 * p[count]].reshape(-1, 8):
             row0, col0, cols, parts, part, step, tc = (int(v) for v in r[:7])
-            assert kind == "p" or cols <= p[JOINCOLS]
-            for x in range(256 if kind == "p" else int(p[JOINCOLS])):
-                col = x // 128 * tc + x % 128
-                if x >= step or x % 128 >= tc or col >= cols:
-                    continue
+            assert p[most] >= (cols if parts >= 16 else -(-cols // per))
+            for col in range(cols):
+                x = col // tc * 128 + col % tc
+                assert x < step
                 for g in range(group // unit):
                     key = (row0 + (col0 + col) // unit, g * unit + (col0 + col) % unit if unit == group else g)
                     assert key not in joined
