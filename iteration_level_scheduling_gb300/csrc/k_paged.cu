@@ -589,8 +589,8 @@ __device__ __forceinline__ uint32_t cw_pack(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-// fp32 operands as two tf32 parts, x = hi + lo: hi cut off, lo rounded to 11 bits, which leaves 2^-21 |x|; products
-// hi hi + hi lo + lo hi.  An infinity has no lower part (inf - inf): what it touches becomes NaN.
+// fp32 operands as two tf32 parts, x = hi + lo: hi cut off, lo rounded to 11 bits, which leaves 2^-21 |x| (both rounded:
+// 2^-22, and 10 % more time); products hi hi + hi lo + lo hi.  An infinity has no lower part (inf - inf): what it touches becomes NaN.
 __device__ __forceinline__ void cw_split(uint32_t x, uint32_t &hi, uint32_t &lo) {
     hi = x & 0xffffe000u;
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(__uint_as_float(x) - __uint_as_float(hi)));
@@ -617,6 +617,7 @@ __global__ void __launch_bounds__(kCwThreads, 2)
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int KS = D / (F32 ? 8 : 16), MT = D / 16;
     constexpr bool kKeepQ = !S::kQInSmem;
+    constexpr bool kTwo = NT < 4;  // weights in two bf16 parts: 1 % of the time of single rows, 8 % of that of 32 columns
     constexpr unsigned kFull = 0xffffffffu;
     extern __shared__ __align__(1024) uint8_t cw_smem[];
     if (smem_u32(cw_smem) & 1023u) {  // uniform: every thread leaves
@@ -859,8 +860,8 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                         for (int mt = 0; mt < MT; ++mt) o[nt][mt][i] *= corr, o[nt][mt][2 + i] *= corr;
                     }
             }
-            // weights; bf16: rounded for the second product, and l sums what is used
-            uint32_t pw[NT][2];
+            // weights; bf16: in two parts, 16 bits kept, in two products, or in one, and l sums what is used
+            uint32_t pw[NT][2], pl[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float b0 = cw_base(m[nt][0]), b1 = cw_base(m[nt][1]);
@@ -869,8 +870,11 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                     c[nt][2 * x] = cw_exp2(c[nt][2 * x] - b0), c[nt][2 * x + 1] = cw_exp2(c[nt][2 * x + 1] - b1);
                     if constexpr (!F32) {
                         pw[nt][x] = cw_pack(c[nt][2 * x], c[nt][2 * x + 1]);
-                        c[nt][2 * x] = __uint_as_float(pw[nt][x] << 16);
-                        c[nt][2 * x + 1] = __uint_as_float(pw[nt][x] & 0xffff0000u);
+                        const float w0 = __uint_as_float(pw[nt][x] << 16), w1 = __uint_as_float(pw[nt][x] & 0xffff0000u);
+                        if constexpr (kTwo)
+                            pl[nt][x] = cw_pack(c[nt][2 * x] - w0, c[nt][2 * x + 1] - w1);
+                        else
+                            c[nt][2 * x] = w0, c[nt][2 * x + 1] = w1;
                     }
                     l[nt][0] += c[nt][2 * x], l[nt][1] += c[nt][2 * x + 1];
                 }
@@ -916,7 +920,7 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                     }
             } else if constexpr (F32) {
                 // the keys of a product in the order 0 2 4 6 1 3 5 7, which spreads V's rows over the banks
-                uint32_t ph[NT][2][2], pl[NT][2][2];
+                uint32_t qh[NT][2][2], ql[NT][2][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -926,7 +930,7 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                             const int src = (2 * t4 + i) * 4 + (g8 >> 1);
                             const float p0 = __shfl_sync(kFull, c[nt][2 * x], src);
                             const float p1 = __shfl_sync(kFull, c[nt][2 * x + 1], src);
-                            cw_split(__float_as_uint(g8 & 1 ? p1 : p0), ph[nt][x][i], pl[nt][x][i]);
+                            cw_split(__float_as_uint(g8 & 1 ? p1 : p0), qh[nt][x][i], ql[nt][x][i]);
                         }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
@@ -943,9 +947,9 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            cw_mma_tf32(y[nt], fl, ph[nt][x][0], ph[nt][x][1]);
-                            cw_mma_tf32(y[nt], fh, pl[nt][x][0], pl[nt][x][1]);
-                            cw_mma_tf32(y[nt], fh, ph[nt][x][0], ph[nt][x][1]);
+                            cw_mma_tf32(y[nt], fl, qh[nt][x][0], qh[nt][x][1]);
+                            cw_mma_tf32(y[nt], fh, ql[nt][x][0], ql[nt][x][1]);
+                            cw_mma_tf32(y[nt], fh, qh[nt][x][0], qh[nt][x][1]);
                         }
                     }
 #pragma unroll
@@ -955,13 +959,21 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                 }
             } else {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) pw[nt][0] = cw_transpose(pw[nt][0]), pw[nt][1] = cw_transpose(pw[nt][1]);
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        pw[nt][x] = cw_transpose(pw[nt][x]);
+                        if constexpr (kTwo) pl[nt][x] = cw_transpose(pl[nt][x]);
+                    }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     uint32_t f[4];
                     cw_ldsm_t(at(vb, (lane >> 4) * 8 + (lane & 7), 2 * mt + ((lane >> 3) & 1)), f);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) cw_mma_bf16(o[nt][mt], f, pw[nt][0], pw[nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        cw_mma_bf16(o[nt][mt], f, pw[nt][0], pw[nt][1]);
+                        if constexpr (kTwo) cw_mma_bf16(o[nt][mt], f, pl[nt][0], pl[nt][1]);
+                    }
                 }
             }
             __syncwarp();  // every lane has read the stage
