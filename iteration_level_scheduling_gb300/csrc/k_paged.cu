@@ -1250,6 +1250,11 @@ __device__ __forceinline__ uint64_t pp_fma2(uint64_t a, uint64_t b, uint64_t c) 
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t pp_mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t pp_add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -1699,26 +1704,40 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 wait(&bar.o_done[t][1], n_last++);
                 tc_fence_after();
                 const float inv = 1.f / l;
+                const uint64_t inv2 = pp_pair(inv, inv);
+                uint64_t zero = 0;  // 0 times every component: NaN if one is not finite
+                bf16 *to[4];        // where this lane writes, of rows 8 z + lane / 4
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const int64_t at = __shfl_sync(kFull, out_at, 8 * z + (lane >> 2));
+                    to[z] = at >= 0 ? a.out + at + (lane & 3) * 8 : nullptr;
+                }
 #pragma unroll
                 for (int x = 0; x < D; x += 32) {
                     uint32_t o[32];
                     pp_ld32(o_t + x, o);
                     pp_wait_ld32(o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) bad |= (o[e] & 0x7f800000u) == 0x7f800000u;
+                    for (int e = 0; e < 32; e += 2)
+                        zero = pp_fma2(pp_pair(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), 0ull, zero);
                     if (it.part < 0) {  // by way of shared memory: four lanes write 64 bytes of a row
-                        float f[32];
+                        uint32_t w[16];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
+                        for (int e = 0; e < 16; ++e) {
+                            float f0, f1;
+                            pp_unpair(pp_mul2(pp_pair(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2), f0, f1);
+                            w[e] = cw_pack(f0, f1);
+                        }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) store16(reinterpret_cast<bf16 *>(stage + lane * 80) + 8 * e, f + 8 * e);
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<uint4 *>(stage + lane * 80)[e] =
+                                make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                         __syncwarp();
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
-                            const int rr = 8 * z + (lane >> 2);
-                            const int64_t to = __shfl_sync(kFull, out_at, rr);
-                            const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 80 + (lane & 3) * 16);
-                            if (to >= 0) *reinterpret_cast<uint4 *>(a.out + to + x + (lane & 3) * 8) = v;
+                            const uint4 v =
+                                *reinterpret_cast<const uint4 *>(stage + (8 * z + (lane >> 2)) * 80 + (lane & 3) * 16);
+                            if (to[z]) *reinterpret_cast<uint4 *>(to[z] + x) = v;
                         }
                         __syncwarp();
                     } else if (mine) {
@@ -1727,6 +1746,9 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                             *reinterpret_cast<uint4 *>(part + x + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                 }
+                float z0, z1;
+                pp_unpair(zero, z0, z1);
+                bad = z0 != 0.f || z1 != 0.f;
                 tc_fence_before();
             } else if (mine) {  // a part of the keys of which this tile sees none
                 for (int x = 0; x < D; x += 4) *reinterpret_cast<uint4 *>(part + x) = make_uint4(0, 0, 0, 0);
