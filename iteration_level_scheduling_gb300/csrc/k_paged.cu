@@ -392,11 +392,14 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
                     y[e] = p * c - q * s, y[e + 1] = q * c + p * s;
                 }
             }
-        } else if (u * VEC < half) {
+        } else if (u * VEC < half) {  // (half and c0 are multiples of VEC: aligned)
+            float c[VEC], s[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; e += 4) load16(cs + c0 + e, c + e), load16(cs + half + c0 + e, s + e);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float c = cs[c0 + e], s = cs[half + c0 + e], p = x[e], q = y[e];
-                x[e] = p * c - q * s, y[e] = q * c + p * s;
+                const float p = x[e], q = y[e];
+                x[e] = p * c[e] - q * s[e], y[e] = q * c[e] + p * s[e];
             }
         }
     }
@@ -409,43 +412,42 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
     store16(dst + c1, y);
 }
 
-// Halves whose middle is inside a 16-byte chunk: a warp per head's row, a
-// component's partner loaded on its own.
+// Halves whose middle is inside a 16-byte chunk: a thread per chunk, the
+// components' partners loaded one by one.  A head's row is within a warp, which
+// reads all of it before it writes.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) paged_append_odd_kernel(const AppendArgs a) {
-    constexpr int N = (D + 31) / 32;
+    constexpr int VEC = Elem<T>::kPer16, CH = D / VEC;
+    static_assert(32 % CH == 0, "a head's row in one warp");
     pdl_trigger();
     pdl_wait();
-    const int per_row = a.heads + 2 * a.kv_heads - a.first_head;
-    const int64_t at = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-    const int row = (int)(at / per_row), lane = threadIdx.x & 31;
-    if (row >= a.n_rows) return;
-    const int h = a.first_head + (int)(at - (int64_t)row * per_row);
+    const int per_row = (a.heads + 2 * a.kv_heads - a.first_head) * CH;
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int row = (int)min(at / per_row, (int64_t)a.n_rows - 1);  // (threads behind the last stay for the barrier)
+    const int rest = (int)(at % per_row), h = a.first_head + rest / CH, c0 = rest % CH * VEC;
     const int4 rec = a.rows[row];
     const T *src = reinterpret_cast<const T *>(a.qkv) + (int64_t)row * a.ld_qkv + h * D;
     const float *cs = a.rope + (int64_t)rec.y * a.rot;
     const int half = a.rot / 2;
+    float x[VEC];
+    load16(src + c0, x);
+    if (h < a.heads + a.kv_heads) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (c0 + e < a.rot) {
+                const bool low = c0 + e < half;
+                const int i = low ? c0 + e : c0 + e - half;
+                const float o = Elem<T>::to_f(src[low ? i + half : i]), c = cs[i], s = cs[half + i];
+                x[e] = low ? x[e] * c - o * s : x[e] * c + o * s;
+            }
+    }
     T *dst;
     if (h < a.heads)
         dst = reinterpret_cast<T *>(a.q_out) + (int64_t)row * a.ld_q + h * D;
     else
         dst = reinterpret_cast<T *>(a.layer) + ((int64_t)(h - a.heads) * a.slots + rec.x) * D;
-    float x[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int e = lane + 32 * i;
-        if (e >= D) continue;
-        x[i] = Elem<T>::to_f(src[e]);
-        if (h < a.heads + a.kv_heads && e < a.rot) {
-            const float c = cs[e % half], s = cs[half + e % half];
-            const float o = Elem<T>::to_f(src[e < half ? e + half : e - half]);
-            x[i] = e < half ? x[i] * c - o * s : x[i] * c + o * s;
-        }
-    }
     __syncwarp();  // the whole head is read before any of it is written
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (lane + 32 * i < D) dst[lane + 32 * i] = Elem<T>::from_f(x[i]);
+    if (at / per_row < a.n_rows) store16(dst + c0, x);
 }
 
 template <typename T, int D>
@@ -455,7 +457,7 @@ cudaError_t launch_append(const AppendArgs &a, bool neighbours, cudaStream_t st)
     const dim3 grid((unsigned)((heads * (D / VEC / 2) + 255) / 256));
     if (neighbours) return launch_pdl(paged_append_kernel<T, D, true>, grid, dim3(256), 0, st, a);
     if ((a.rot / 2) % VEC == 0) return launch_pdl(paged_append_kernel<T, D, false>, grid, dim3(256), 0, st, a);
-    return launch_pdl(paged_append_odd_kernel<T, D>, dim3((unsigned)((heads + 7) / 8)), dim3(256), 0, st, a);
+    return launch_pdl(paged_append_odd_kernel<T, D>, dim3((unsigned)((heads * (D / VEC) + 255) / 256)), dim3(256), 0, st, a);
 }
 
 }  // namespace

@@ -514,3 +514,126 @@ def test_a_prompt_and_its_tokens(native, eng):
                           qkv[:, heads + kv:].transpose(1, 0, 2), 0)
         got = out.float().cpu().numpy().reshape(N, heads, d)
         assert (np.abs(got - ref) <= lim).all()
+
+
+def test_slots_beyond_32_bits(native, eng):
+    """A layer of more than 2^32 elements, of which the last pages are used."""
+    kv, d, page, n_pages = 4, 128, 64, 70000  # 4.6e9 elements, 9 GB
+    g = np.random.default_rng(18)
+    layer = torch.empty((2, kv, n_pages * page, d), dtype=torch.bfloat16, device="cuda")
+    for dtype, heads, reqs in (("bf16", 8, [(1, 300), (5, 100), (150, 40)]),):
+        n, c = [a for a, _ in reqs], [b for _, b in reqs]
+        need = [-(-(a + b) // page) for a, b in reqs]
+        last, at = n_pages - 1 - g.permutation(sum(need)), 0
+        table = np.zeros((len(reqs), max(need)), np.int32)
+        for i, m in enumerate(need):
+            table[i, :m] = last[at:at + m]
+            at += m
+        plan = eng.paged_plan(1, heads, kv, d, page, n_pages, n, c, table)
+        dev = torch.from_numpy(plan).cuda()
+        work = torch.empty(max(16, eng.paged_workspace_bytes(plan)), dtype=torch.uint8, device="cuda")
+        keys = []
+        for i, (a, b) in enumerate(reqs):
+            s = torch.from_numpy(paged.slots(table[i], page, 0, a + b)).cuda()
+            x = rounded(g.standard_normal((2, kv, a + b, d)), dtype)
+            layer[:, :, s] = torch.from_numpy(x).cuda().bfloat16()
+            keys.append(x)
+        qkv = rounded(g.standard_normal((sum(n), heads + 2 * kv, d)), dtype)
+        r = 0
+        for i, (a, b) in enumerate(reqs):  # the rows' own keys and values, to be appended
+            keys[i][0, :, b:] = qkv[r:r + a, heads:heads + kv].transpose(1, 0, 2)
+            keys[i][1, :, b:] = qkv[r:r + a, heads + kv:].transpose(1, 0, 2)
+            r += a
+        dq = torch.from_numpy(qkv.reshape(len(qkv), -1)).cuda().bfloat16()
+        out = torch.empty((sum(n), heads * d), dtype=torch.bfloat16, device="cuda")
+        eng.op_paged_append(dq.data_ptr(), layer.data_ptr(), plan, dev.data_ptr())
+        eng.op_paged_attention(dq.data_ptr(), layer.data_ptr(), plan, dev.data_ptr(), work.data_ptr(), out.data_ptr(),
+                               ld_q=dq.shape[1])
+        got, r = out.float().cpu().numpy().reshape(-1, heads, d), 0
+        for i, (a, b) in enumerate(reqs):
+            ref, lim = limits(dtype, qkv[r:r + a, :heads], *keys[i], b)
+            assert (np.abs(got[r:r + a] - ref) <= lim).all()
+            r += a
+
+
+def test_steps_queued_behind_one_another(native, eng):
+    """Several layers' appends and attentions, over growing contexts, in one graph: the bits of the same calls one by
+    one.  (Kernels start early behind the ones in front of them; the next plan's rows are read behind the wait.)"""
+    heads, kv, d, page, steps, B = 8, 2, 128, 16, 6, 5
+    g = np.random.default_rng(19)
+    ctx0 = [3, 700, 40, 15, 1300]
+    need = [-(-(c + steps) // page) for c in ctx0]
+    table, at = np.zeros((B, max(need)), np.int32), 0
+    order = g.permutation(sum(need))
+    for i, m in enumerate(need):
+        table[i, :m] = order[at:at + m]
+        at += m
+    rope = torch.from_numpy(paged.rope_table(2000, d)).cuda()
+    first = torch.from_numpy(rounded(g.standard_normal((2, kv, sum(need) * page, d)), "bf16")).cuda().bfloat16()
+    plans = [eng.paged_plan(1, heads, kv, d, page, sum(need), [1] * B, [c + s for c in ctx0], table) for s in range(steps)]
+    devs = [torch.from_numpy(p).cuda() for p in plans]
+    work = torch.empty(max(max(16, eng.paged_workspace_bytes(p)) for p in plans), dtype=torch.uint8, device="cuda")
+    qkv = [torch.from_numpy(rounded(g.standard_normal((B, (heads + 2 * kv) * d)), "bf16")).cuda().bfloat16()
+           for _ in range(steps)]
+
+    def run(e, sync):
+        layer, q = first.clone(), torch.empty((B, heads * d), dtype=torch.bfloat16, device="cuda")
+        outs = [torch.empty_like(q) for _ in range(steps)]
+
+        def go():
+            for s in range(steps):
+                e.op_paged_append(qkv[s].data_ptr(), layer.data_ptr(), plans[s], devs[s].data_ptr(), q_out=q.data_ptr(),
+                                  rope=rope.data_ptr(), rope_len=2000, rot_dim=d, sync=sync)
+                e.op_paged_attention(q.data_ptr(), layer.data_ptr(), plans[s], devs[s].data_ptr(), work.data_ptr(),
+                                     outs[s].data_ptr(), sync=sync)
+        return go, layer, outs
+
+    go, layer, want = run(eng, True)
+    go()
+    side = torch.cuda.Stream()
+    e2 = native.Engine(1, 64, 1, 64, 64, 64, native.DTYPE_BF16, 64, 64, 64, None, side.cuda_stream)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        go2, layer2, got = run(e2, False)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            go2()
+        for _ in range(20):
+            layer2.copy_(first)
+            for o in got:
+                o.zero_()
+            graph.replay()
+            side.synchronize()
+            assert torch.equal(layer, layer2) and all(torch.equal(a, b) for a, b in zip(want, got))
+    del graph
+    e2.close()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_beside_the_engines_own_attention(native, eng, d):
+    """Pages in a row are a request's contiguous slots: the two attentions over one layer agree."""
+    heads, reqs, page = 4, [(1, 200), (40, 7), (1, 0), (130, 64)], 16
+    n, c = [a for a, _ in reqs], [b for _, b in reqs]
+    need = [-(-(a + b) // page) for a, b in reqs]
+    begin = np.concatenate([[0], np.cumsum(need)])[:-1]
+    table = np.zeros((len(reqs), max(need)), np.int32)
+    for i, m in enumerate(need):
+        table[i, :m] = begin[i] + np.arange(m)
+    s = Case(native, eng, 20, "bf16", heads, heads, d, page, reqs, table=table, n_pages=sum(need))
+    qkv = rounded(s.g.standard_normal((s.rows, 3, heads, d)), "bf16")
+    s.q, r = qkv[:, 0].copy(), 0
+    dq = torch.from_numpy(qkv.reshape(s.rows, -1)).cuda().bfloat16()
+    s.eng.op_paged_append(dq.data_ptr(), s.layer.data_ptr(), s.plan, s.dplan.data_ptr())
+    for (a, b), t in zip(reqs, table):
+        s.host[:, :, paged.slots(t, page, b, a)] = qkv[r:r + a, 1:].transpose(1, 2, 0, 3)
+        r += a
+    out, own = (torch.full((s.rows + 2, heads * d), 768.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    s.eng.op_paged_attention(dq.data_ptr(), s.layer.data_ptr(), s.plan, s.dplan.data_ptr(), s.work.data_ptr(),
+                             out.data_ptr(), ld_q=dq.shape[1])
+    e2 = native.Engine(1, heads * d, heads, 64, 64, 4096, native.DTYPE_BF16, 1024, 8, 64, None,
+                       torch.cuda.current_stream().cuda_stream)
+    e2.op_attention(1, dq.data_ptr(), s.layer.data_ptr(), s.slots, heads, d, n, c, begin * page, own.data_ptr())
+    e2.close()
+    s.check(out)
+    s.check(own)

@@ -196,3 +196,16 @@ def test_plans_cover_every_key_once(native, seed):
     p = plan(native, dtype=seed % 2, heads=group * kv, kv_heads=kv, d=int(g.choice([16, 64, 128])), page=page,
              n_pages=sum(need), n=n, c=c, table=table)
     cover(native, p, n, c, table, page, group, kv)
+
+
+def test_kernels_of_one_call_start_behind_what_is_in_front_of_it():
+    """The first kernel of an attention triggers behind its wait, so the second, which does not wait at its start, finds
+    all that was in front of the call; it waits before it ends, so that behind it both have ended."""
+    from test_launch_order import body, triggers_behind_wait
+    assert triggers_behind_wait("k_paged.cu", "paged_cols_kernel") and triggers_behind_wait("k_paged.cu", "paged_prompt_kernel")
+    b = body("k_paged.cu", "paged_cols_kernel")
+    assert b.find("if (!a.beside) pdl_wait();") < b.find("a.items[") and b.rfind("if (a.beside) pdl_wait();") > b.find("a.out")
+    assert b.find("if (!a.beside) pdl_wait();") < b.find("pdl_trigger();")
+    for kernel in ("paged_append_kernel", "paged_append_odd_kernel", "paged_join_kernel"):
+        b = body("k_paged.cu", kernel)
+        assert 0 <= b.find("pdl_wait();") < b.find("blockIdx")
