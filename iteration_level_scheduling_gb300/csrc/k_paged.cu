@@ -154,7 +154,8 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
         if (prompts && is_prompt(b, i))
             row_pairs(b, i, [&](int64_t, int64_t, int64_t keys) { pwork.push_back((int32_t)((keys + 63) / 64)); });
         else
-            column_tiles(b, i, [&](int, int64_t, int64_t, int64_t keys) { work.push_back((int32_t)((keys + 63) / 64)); });
+            column_tiles(b, i,
+                         [&](int, int64_t, int64_t, int64_t keys) { work.push_back((int32_t)((keys + 63) / 64)); });
         z->tiles += up4((c + n + 15) / 16);
         z->maxpos = std::max(z->maxpos, c + n);
     }
@@ -175,7 +176,9 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
         column_tiles(b, i, [&](int cl, int64_t, int64_t n, int64_t keys) {
             const int64_t parts = parts_of(keys, z->chunk);
             z->items[cl] += parts;
-            if (parts > 1) z->parts += parts * (8 << cl), z->joins++, z->join_rows = std::max(z->join_rows, join_rows(n, parts));
+            if (parts == 1) return;
+            z->parts += parts * (8 << cl), z->joins++;
+            z->join_rows = std::max(z->join_rows, join_rows(n, parts));
         });
     }
     int64_t w = kPagedHdr;
@@ -280,7 +283,8 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
                 pitem[5] = parts == 1 ? -1 : (int32_t)(ppart + p * 2 * kPpRows);
             }
             if (parts == 1) return;
-            pjoin[0] = (int32_t)(first_row + r0), pjoin[1] = 0, pjoin[2] = (int32_t)rows * pack, pjoin[3] = (int32_t)parts;
+            pjoin[0] = (int32_t)(first_row + r0), pjoin[1] = 0, pjoin[2] = (int32_t)rows * pack;
+            pjoin[3] = (int32_t)parts;
             pjoin[4] = (int32_t)ppart, pjoin[5] = 2 * kPpRows, pjoin[6] = tile_rows * pack;
             pjoin += 8, ppart += parts * 2 * kPpRows;
         };
@@ -331,7 +335,8 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
 
 bool paged_plan_ok(const int32_t *hp) { return hp && hp[0] == kPagedMagic; }
 PagedInfo paged_plan_info(const int32_t *hp) {
-    return {hp[G_DTYPE], hp[G_HEADS], hp[G_KV_HEADS], hp[G_DIM], hp[G_SLOTS], hp[G_ROWS], hp[G_MAXPOS], hp[G_TWICE] != 0};
+    return {hp[G_DTYPE], hp[G_HEADS],  hp[G_KV_HEADS],  hp[G_DIM],
+            hp[G_SLOTS], hp[G_ROWS], hp[G_MAXPOS], hp[G_TWICE] != 0};
 }
 
 int64_t paged_workspace_bytes(const int32_t *hp) {
@@ -353,7 +358,11 @@ struct AppendArgs {
     int n_rows, heads, kv_heads, rot, first_head;  // (first_head: heads are worked on from there)
 };
 
-// One thread per two 16-byte chunks of a head's row.
+// One thread per two 16-byte chunks of a head's row, which hold whole pairs: the
+// chunks i and rot / 2 + i, or two neighbouring ones.  In between it reads its
+// cosines and sines, which all heads of a row share in L1.  Bound by HBM: 8
+// prompts of <= 2047 rows, 40 + 16 heads of 128, 303 MB in 48.7 us, 92 % of the copy rate
+// (with the table read 16 bytes at a time 51.3).
 // NEIGH: components 2i and 2i + 1 are a pair; else i and i + rot / 2.
 // A thread reads all that it and its pairs need before it writes, so q_out may
 // be the queries' own place.
@@ -392,14 +401,11 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
                     y[e] = p * c - q * s, y[e + 1] = q * c + p * s;
                 }
             }
-        } else if (u * VEC < half) {  // (half and c0 are multiples of VEC: aligned)
-            float c[VEC], s[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; e += 4) load16(cs + c0 + e, c + e), load16(cs + half + c0 + e, s + e);
+        } else if (u * VEC < half) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float p = x[e], q = y[e];
-                x[e] = p * c[e] - q * s[e], y[e] = q * c[e] + p * s[e];
+                const float c = cs[c0 + e], s = cs[half + c0 + e], p = x[e], q = y[e];
+                x[e] = p * c - q * s, y[e] = q * c + p * s;
             }
         }
     }
@@ -457,7 +463,8 @@ cudaError_t launch_append(const AppendArgs &a, bool neighbours, cudaStream_t st)
     const dim3 grid((unsigned)((heads * (D / VEC / 2) + 255) / 256));
     if (neighbours) return launch_pdl(paged_append_kernel<T, D, true>, grid, dim3(256), 0, st, a);
     if ((a.rot / 2) % VEC == 0) return launch_pdl(paged_append_kernel<T, D, false>, grid, dim3(256), 0, st, a);
-    return launch_pdl(paged_append_odd_kernel<T, D>, dim3((unsigned)((heads * (D / VEC) + 255) / 256)), dim3(256), 0, st, a);
+    const dim3 chunks((unsigned)((heads * (D / VEC) + 255) / 256));
+    return launch_pdl(paged_append_odd_kernel<T, D>, chunks, dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -497,11 +504,26 @@ cudaError_t paged_append(const PagedAppend &p, const int32_t *hp, const int32_t 
 // is still several times what HBM delivers.
 //
 // Each warp is a pipeline of its own: it takes every fourth tile of 16 keys of
-// the item, loads it by TMA (K and V of a 64-dim block in one box) into its
-// own ring of stages several tiles ahead, across items, and keeps its own
-// running maximum m, sum l and outputs per column.  At the end of an item the
-// block's four warps meet and add up.  No warp waits for another while it
-// streams, and nothing is shared between blocks.
+// the item, loads it by TMA (K and V of a 64-dim block in one box; 16 slots
+// never cross a page) into its own ring of stages several tiles ahead, across items,
+// and keeps its own running maximum m, sum l and outputs per column.  At the end
+// of an item the block's four warps meet and add up.  No warp waits for another
+// while it streams, and nothing is shared between blocks: keys are split by the
+// plan where there are few items (choose_chunk), the parts joined by
+// paged_join_kernel, without atomics, in their order.
+//
+// Numerics: scores, m, l and outputs in fp32.  bf16: products of 16-bit operands
+// are exact; weights go into the second product in two bf16 parts (16 bits) up
+// to 16 columns, in one (2^-9) for 32.  fp32: cw_split.  No score at all is m =
+// -inf, from which cw_base subtracts 0.  Keys past a column's last are masked by
+// index.  0 times a value that is not finite is NaN, so a tile with such a value behind a
+// key that only some columns see is added up key by key.
+//
+// Bound by HBM for long contexts (64 requests of <= 4000 keys, 40 heads over 8 of
+// 128: 663 MB in 107 us, 91 % of the copy rate; 40 heads of their own, 64 x <= 1000 keys:
+// 97 %), by latency below some 20 MB: one request over 300 keys, 20 heads of 64, 4.8 us.
+// fp32 by issue: the parts cost some 800 instructions per 16 keys (64 x <= 1000 keys, 8
+// heads of 128: 60 us, 82 % of the copy rate).
 namespace {
 
 constexpr int kCwWarps = 4;
@@ -591,8 +613,10 @@ __device__ __forceinline__ uint32_t cw_pack(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-// fp32 operands as two tf32 parts, x = hi + lo: hi cut off, lo rounded to 11 bits, which leaves 2^-21 |x| (both rounded:
-// 2^-22, and 10 % more time); products hi hi + hi lo + lo hi.  An infinity has no lower part (inf - inf): what it touches becomes NaN.
+// fp32 operands as two tf32 parts, x = hi + lo: hi cut off, lo rounded to 11
+// bits, which leaves 2^-21 |x| (both rounded: 2^-22, and 10 % more time); products
+// hi hi + hi lo + lo hi.  An infinity has no lower part (inf - inf): what it touches
+// becomes NaN.
 __device__ __forceinline__ void cw_split(uint32_t x, uint32_t &hi, uint32_t &lo) {
     hi = x & 0xffffe000u;
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(__uint_as_float(x) - __uint_as_float(hi)));
@@ -619,7 +643,8 @@ __global__ void __launch_bounds__(kCwThreads, 2)
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int KS = D / (F32 ? 8 : 16), MT = D / 16;
     constexpr bool kKeepQ = !S::kQInSmem;
-    constexpr bool kTwo = NT < 4;  // weights in two bf16 parts: 1 % of the time of single rows, 8 % of that of 32 columns
+    // weights in two bf16 parts: 1 % of the time of single rows, 8 % of that of 32 columns
+    constexpr bool kTwo = NT < 4;
     constexpr unsigned kFull = 0xffffffffu;
     extern __shared__ __align__(1024) uint8_t cw_smem[];
     if (smem_u32(cw_smem) & 1023u) {  // uniform: every thread leaves
@@ -795,10 +820,11 @@ __global__ void __launch_bounds__(kCwThreads, 2)
 #pragma unroll 1
                         for (int d = 0; d < D; ++d)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                z[x] = fmaf(__uint_as_float(cw_lds(at(kb, g8 + 8 * (x >> 1), d / 4) + d % 4 * 4)),
-                                            __uint_as_float(cw_lds(qs + (8 * nt + 2 * t4 + (x & 1)) * S::kQRow + d * 4)),
-                                            z[x]);
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t kv = cw_lds(at(kb, g8 + 8 * (x >> 1), d / 4) + d % 4 * 4);
+                                const uint32_t qv = cw_lds(qs + (8 * nt + 2 * t4 + (x & 1)) * S::kQRow + 4 * d);
+                                z[x] = fmaf(__uint_as_float(kv), __uint_as_float(qv), z[x]);
+                            }
 #pragma unroll
                         for (int y = 0; y < NT; ++y)
 #pragma unroll
@@ -810,7 +836,8 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                 for (int k2 = 0; k2 < KS; k2 += 2) {  // (head_dim 16: the second half of a load is not used)
                     uint32_t f[2][4], q[4];
 #pragma unroll
-                    for (int z = 0; z < 2 && k2 + z < KS; ++z) cw_ldsm(at(kb, lane & 15, 2 * (k2 + z) + (lane >> 4)), f[z]);
+                    for (int z = 0; z < 2 && k2 + z < KS; ++z)
+                        cw_ldsm(at(kb, lane & 15, 2 * (k2 + z) + (lane >> 4)), f[z]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const int ch = KS == 1 ? (lane >> 3 & 1) : 2 * k2 + (lane >> 3);
@@ -872,7 +899,8 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                     c[nt][2 * x] = cw_exp2(c[nt][2 * x] - b0), c[nt][2 * x + 1] = cw_exp2(c[nt][2 * x + 1] - b1);
                     if constexpr (!F32) {
                         pw[nt][x] = cw_pack(c[nt][2 * x], c[nt][2 * x + 1]);
-                        const float w0 = __uint_as_float(pw[nt][x] << 16), w1 = __uint_as_float(pw[nt][x] & 0xffff0000u);
+                        const float w0 = __uint_as_float(pw[nt][x] << 16);
+                        const float w1 = __uint_as_float(pw[nt][x] & 0xffff0000u);
                         if constexpr (kTwo)
                             pl[nt][x] = cw_pack(c[nt][2 * x] - w0, c[nt][2 * x + 1] - w1);
                         else
@@ -917,7 +945,8 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                                 const float vf = __uint_as_float(F32 ? v : d % 4 ? v & 0xffff0000u : v << 16);
 #pragma unroll
                                 for (int i = 0; i < 2; ++i)
-                                    if (16 * t + r < sees[nt][i]) o[nt][mt][2 * x + i] = fmaf(p[i], vf, o[nt][mt][2 * x + i]);
+                                    if (16 * t + r < sees[nt][i])
+                                        o[nt][mt][2 * x + i] = fmaf(p[i], vf, o[nt][mt][2 * x + i]);
                             }
                     }
             } else if constexpr (F32) {
@@ -1003,7 +1032,8 @@ __global__ void __launch_bounds__(kCwThreads, 2)
                     if (g8 == 0) ml[x] = make_float2(m[nt][i], l[nt][i]);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
-                        mo[x * S::kLd + 16 * mt + g8] = o[nt][mt][i], mo[x * S::kLd + 16 * mt + g8 + 8] = o[nt][mt][2 + i];
+                        mo[x * S::kLd + 16 * mt + g8] = o[nt][mt][i],
+                        mo[x * S::kLd + 16 * mt + g8 + 8] = o[nt][mt][2 + i];
                 }
             __syncthreads();
             for (int x = threadIdx.x; x < S::kMerge * (D / 4); x += kCwThreads) {
@@ -1115,10 +1145,14 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 // V and back has some 2400 cycles of latency beside its work (products, commits,
 // waits, tensor-memory accesses; measured with that work left out), so the
 // next S is always under way: a softmax finds it when it is done with the last.
-// With one buffer of 128 keys the same work took 4400 cycles per 128 keys of both
-// tiles.  Shared memory: Q and a ring of key tiles; the loads are
-// boxes of a page (or of the part of it that divides 64 slots), a lane of the
-// TMA warp each.
+// (With one buffer of 128 keys the same work took 4400 cycles per 128 keys of both
+// tiles, now some 3000.)  Shared memory: Q and a ring of key tiles; the loads are
+// boxes of a page (or of the part of it that divides 64 slots).
+// Bound: head_dim 128 by shared memory, which feeds Q again for every 64 keys (160
+// KB per step, 1250 of the 1500 cycles that one takes); head_dim 64 by the softmax (64
+// exponentials and 130 other instructions per row and step, 850 of 1240 cycles).
+// 4 prompts of <= 1024 rows over <= 1000 keys, 40 heads over 8 of 128: 75 us, 0.52 of
+// the tensor peak; 8 of <= 2047 rows, 16 over 2 of 64: 52 us, 0.32.
 // Every P is formed against the m that O and l carry, which is near a row's
 // maximum and need not be it: O is rescaled only where it lags by more than 2^8.
 // Keys past the item's last are masked by index and their V rows zeroed.  A
@@ -1307,7 +1341,8 @@ __device__ __forceinline__ float pp_max3(float a, float b, float c) {
 // One row over keys 0 .. n - 1 of its item by the whole warp: afterwards every
 // lane holds m, l and 8 components of o, lane % (D / 8) * 8 on.
 template <int D>
-__device__ __noinline__ void pp_row(const PpArgs &a, const bf16 *q, const int32_t *tiles, int n, int kvh, float &m, float &l, float *o) {
+__device__ __noinline__ void pp_row(const PpArgs &a, const bf16 *q, const int32_t *tiles, int n, int kvh, float &m,
+                                    float &l, float *o) {
     constexpr int LPT = D / 8, TPW = 32 / LPT;
     const int lane = threadIdx.x & 31, g = lane / LPT, sub = lane % LPT;
     const bf16 *kb = a.layer + (int64_t)kvh * a.slots * D + sub * 8, *vb = kb + (int64_t)a.kv_heads * a.slots * D;
@@ -1429,7 +1464,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 for (int t = 0; t < tiles; ++t)
 #pragma unroll
                     for (int c = 0; c < L::kAtoms; ++c)
-                        pp_tma_q(smem_u32(sm + L::kQ) + (uint32_t)(t * L::kAtoms + c) * kPpAtom, &tmq, &bar.q_full, 64 * c, it.vh * a.pack, it.row + t * tile_rows);
+                        pp_tma_q(smem_u32(sm + L::kQ) + (uint32_t)(t * L::kAtoms + c) * kPpAtom, &tmq, &bar.q_full, 64 * c,
+                                 it.vh * a.pack, it.row + t * tile_rows);
                 ++q_used;
                 const int kvh = it.vh / a.per_kv, n_tiles = (it.keys + 15) / 16;
                 // slots / 16 of a key tile's four 16 keys (the plan's tables of a request start 16-byte aligned, a part
@@ -1450,7 +1486,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                             if (e < here && (e & (per - 1)) == 0)
 #pragma unroll
                                 for (int c = 0; c < L::kAtoms; ++c)
-                                    pp_tma_kv(smem_u32(sm + (kv ? L::kV : L::kK)) + s * L::kTile + c * kPpKv + e * 2048u,
+                                    pp_tma_kv(smem_u32(sm + (kv ? L::kV : L::kK)) + s * L::kTile + c * kPpKv +
+                                                  e * 2048u,
                                               &tmkv, &bar.kv_full[s], 64 * c, slot[e] * 16, kvh, kv, pol);
                     ++kv_used;
                 }
@@ -1467,8 +1504,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         // ------------------------------ MMA ------------------------------
         // A thread for each row tile: a product with its waits and commits takes it some 500 cycles, so that one thread
         // for both tiles held up everything else.  It walks all key tiles of the block, the P V of key tile g in
-        // step; S runs ahead by up to two products, and less than the ring in key tiles (both may block for a load, which
-        // has to be one that no release of its own stands in front of).
+        // step; S runs ahead by up to two products, and less than the ring in key tiles (both may block for a load,
+        // which has to be one that no release of its own stands in front of).
         if (elect_one()) {
             const uint32_t t = (uint32_t)(warp - kPpMma);
             const uint32_t idesc_s = idesc_bf16_f32(kPpRows, kPpKeys);
@@ -1484,7 +1521,6 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                     js = 0, more = item_at(++ks, is);
                 }
             };
-            // (Few commits: each holds up the products behind it.)
             // Comes to the next key tile that the row tile sees, below key tile `end`, and waits for its keys.
             const auto prepare_s = [&](uint32_t end) {
                 while (ok && !ready && more && gs < end) {
@@ -1509,7 +1545,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             const auto mma_pv = [&](uint32_t b, uint32_t vd, uint32_t accumulate) {
 #pragma unroll
                 for (uint32_t x = 0; x < kPpKeys / 16; ++x)  // 16 keys: 16 rows of V, 8 columns of P
-                    pp_mma_ts(s_t + 256u, s_t + 64u * b + 8u * x, vd + x * (2048 >> 4), kPpDescHi, idesc_pv, accumulate | x);
+                    pp_mma_ts(s_t + 256u, s_t + 64u * b + 8u * x, vd + x * (2048 >> 4), kPpDescHi, idesc_pv,
+                              accumulate | x);
             };
             const uint32_t kd0 = pp_desc_k(smem_u32(sm + L::kK)), vd0 = pp_desc_mn(smem_u32(sm + L::kV));
             const auto issue_s = [&]() {
@@ -1535,8 +1572,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                     }
                     // (an item's first P is written after the last item's O has been read out)
                     if (ready && ks == k && js == j + 2) {
-                        // The steps in the middle of an item, with as few instructions as they can do with: this thread
-                        // is alone, every one of them takes its whole latency (the general form some 1300 cycles a step).
+                        // The steps in the middle of an item, with as few instructions as they can do with: this
+                        // thread is alone, each of them takes its whole latency.
                         const uint32_t full0 = smem_u32(bar.kv_full), empty0 = smem_u32(bar.kv_empty);
                         const uint32_t p0 = smem_u32(&bar.p_full[t][0]);
                         uint32_t s_st = gs % L::kStages, s_ph = gs / L::kStages & 1u, v_st = st, n = np;
@@ -1586,7 +1623,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_t = tmem + ((uint32_t)(quarter * 32) << 16), o_t = lane_t + 256u + 128u * t;
         const uint32_t s_full = smem_u32(&bar.s_full[t][0]);
-        uint32_t g0 = 0, n = 0, n_before = 0, n_last = 0;  // the item's first key tile, this row tile's so far, o_done's
+        // the item's first key tile, this row tile's key tiles so far, the uses of o_done
+        uint32_t g0 = 0, n = 0, n_before = 0, n_last = 0;
         uint32_t s[64];
         const auto load = [&](uint32_t n) {  // starts the load of this row tile's n-th S
             pp_wait(s_full + 8u * (n & 1u), n >> 1 & 1u, a.err, abort);
@@ -1599,9 +1637,11 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         for (int k = 0; item_at(k, it); g0 += it.n_kt, ++k) {
             const int n_rows = t ? it.n_rows[1] : it.n_rows[0], nk = t ? it.nk[1] : it.nk[0];
             if (n_rows == 0) continue;
-            const int jr = r / a.pack, sees = it.sees + t * tile_rows + jr;  // keys 0 .. sees - 1 of the item are this row's
+            // keys 0 .. sees - 1 of the item are this row's
+            const int jr = r / a.pack, sees = it.sees + t * tile_rows + jr;
             const int clean = min(it.sees + t * tile_rows, it.keys) / kPpKeys;  // key tiles that all rows see in full
-            float m = -INFINITY, l = 0.f, neg = 0.f, last = 0.f;  // m in the units of S, neg = -m scale, the last tile's sum
+            // m in the units of S, neg = -m scale, the last tile's sum
+            float m = -INFINITY, l = 0.f, neg = 0.f, last = 0.f;
             bool big = false;                                     // s scale - m in one step would keep what m lost
             for (int j = 0; j < nk; ++j, ++n) {
                 const uint32_t b = n & 1u, s_t = lane_t + 128u * t + 64u * b;
@@ -1618,7 +1658,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 if (slow) {
                     float top = -INFINITY;
 #pragma unroll
-                    for (int x = 0; x < 64; x += 2) top = pp_max3(top, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+                    for (int x = 0; x < 64; x += 2)
+                        top = pp_max3(top, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
                     float alpha = 1.f;
                     if (m == -INFINITY) {  // no key seen so far: O and l are 0
                         m = top;
@@ -1661,9 +1702,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float p0, p1;
-                        pp_unpair(pp_fma2(pp_pair(__uint_as_float(s[x + 2 * e]), __uint_as_float(s[x + 2 * e + 1])), scale2,
-                                          neg2),
-                                  p0, p1);
+                        const uint64_t sp = pp_pair(__uint_as_float(s[x + 2 * e]), __uint_as_float(s[x + 2 * e + 1]));
+                        pp_unpair(pp_fma2(sp, scale2, neg2), p0, p1);
                         p0 = cw_exp2(p0), p1 = cw_exp2(p1);
                         sum[e & 1] = pp_add2(sum[e & 1], pp_pair(p0, p1));
                         w[e] = cw_pack(p0, p1);
@@ -1675,7 +1715,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 last = l0 + l1;
                 l += last;
                 if (j >= clean) {
-                    const int here = it.keys - j * kPpKeys;  // V rows past the item's last key: zero, once they have landed
+                    // V rows past the item's last key: zero, once they have landed
+                    const int here = it.keys - j * kPpKeys;
                     if (here < kPpKeys) {
                         const uint32_t v = g0 + j, st = v % L::kStages;
                         wait(&bar.kv_full[st], v / L::kStages);
@@ -1727,7 +1768,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float f0, f1;
-                            pp_unpair(pp_mul2(pp_pair(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2), f0, f1);
+                            pp_unpair(pp_mul2(pp_pair(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2),
+                                      f0, f1);
                             w[e] = cw_pack(f0, f1);
                         }
 #pragma unroll
@@ -1755,15 +1797,16 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             } else if (mine) {  // a part of the keys of which this tile sees none
                 for (int x = 0; x < D; x += 4) *reinterpret_cast<uint4 *>(part + x) = make_uint4(0, 0, 0, 0);
             }
-            if (mine && it.part >= 0) *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m * a.scale_log2, l);
+            if (mine && it.part >= 0)
+                *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m * a.scale_log2, l);
             unsigned todo = __ballot_sync(kFull, mine && (bad || (l - l) != 0.f));
             for (; todo; todo &= todo - 1) {  // rows with something that is not finite, over what they see
                 const int rr = quarter * 32 + __ffs(todo) - 1;
                 const int row2 = it.row + t * tile_rows + rr / a.pack, head2 = it.vh * a.pack + rr % a.pack;
                 const int seen = min(it.sees + t * tile_rows + rr / a.pack, it.keys);
                 float m2, l2, o2[8];
-                pp_row<D>(a, a.q + (int64_t)row2 * a.ld_q + (int64_t)head2 * D, a.plan + it.at, seen, it.vh / a.per_kv, m2, l2,
-                          o2);
+                pp_row<D>(a, a.q + (int64_t)row2 * a.ld_q + (int64_t)head2 * D, a.plan + it.at, seen, it.vh / a.per_kv,
+                          m2, l2, o2);
                 const int64_t at2 = at - r + rr;
                 if (lane < D / 8) {
                     if (it.part < 0) {
@@ -1818,10 +1861,10 @@ cudaError_t launch_prompts(const PagedAttn &p, const int32_t *hp, const int32_t 
     e = launch_pdl(paged_prompt_kernel<D>, dim3((unsigned)grid), dim3(kPpThreads), L::kBytes, st, tmq, tmkv, a);
     if (e != cudaSuccess || !hp[G_PJOINS]) return e;
     ++*launches;
-    const JoinArgs j = {a.part, a.part_ml, reinterpret_cast<const int4 *>(dp + hp[G_O_PJOINS]), p.out, p.ld_out, a.vheads,
-                        a.pack};
-    return launch_pdl(paged_join_kernel<bf16, D>, dim3((unsigned)hp[G_PJOINS] * a.vheads, (unsigned)hp[G_PJOINROWS]), dim3(128), 0, st,
-                      j);
+    const int4 *joins = reinterpret_cast<const int4 *>(dp + hp[G_O_PJOINS]);
+    const JoinArgs j = {a.part, a.part_ml, joins, p.out, p.ld_out, a.vheads, a.pack};
+    return launch_pdl(paged_join_kernel<bf16, D>, dim3((unsigned)hp[G_PJOINS] * a.vheads, (unsigned)hp[G_PJOINROWS]),
+                      dim3(128), 0, st, j);
 }
 
 }  // namespace

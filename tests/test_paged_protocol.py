@@ -1,7 +1,7 @@
 """Model of the barrier protocol of paged_prompt_kernel (k_paged.cu), checked under random schedules (no GPU): which
 mbarrier each role waits on, for which use of it, and what it arrives on, with copies completing in random order and
-products in the order in which their thread issued them.  Checked: every wait ends after the phase that it means and no other, no schedule
-stalls, and no buffer is written while it is still read."""
+products in the order in which their thread issued them.  Checked: every wait ends after the phase that it means and no
+other, no schedule stalls, and no buffer is written while it is still read."""
 
 import random
 
