@@ -9,7 +9,9 @@
 // tile of 16 keys never crosses a page.
 #include <algorithm>
 #include <cstring>
+#include <functional>
 #include <numeric>
+#include <utility>
 #include <vector>
 
 #include "common.cuh"
@@ -51,6 +53,7 @@ enum {  // header words of a plan
     G_O_PJOINS,
     G_PACK,  // heads of a prompt's row tile
     G_BOX,   // slots that one load of a prompt's keys may take
+    G_O_DEAL,  // per block its first entry, then the entries: item * tile heads + tile head
 };
 constexpr int kCwCtasPerSm = 2;
 constexpr int kManyParts = 16;  // parts of a column from which on a block joins it alone
@@ -60,13 +63,15 @@ int64_t up4(int64_t x) { return (x + 3) & ~int64_t(3); }
 struct PagedSizes {
     int64_t rows, tiles, maxpos, chunk, items[kClasses], parts, joins, join_rows;
     int64_t pchunk, pitems, pparts, pjoins, pjoin_rows;
-    int64_t off_rows, off_reqs, off_tiles, off_items, off_joins, off_pitems, off_pjoins, total;
+    int64_t off_rows, off_reqs, off_tiles, off_items, off_joins, off_pitems, off_pjoins, off_deal, total;
+    int64_t blocks;  // of paged_prompt_kernel
 };
 
 // Prompts: rows x heads of one key/value head as the 128 rows of a tensor-core tile; two tiles share their keys, 64 at
 // a time.
 constexpr int kPromptCols = 64;  // columns from which on the longest request makes a batch's requests prompts
 constexpr int kPpRows = 128, kPpKeys = 64;
+constexpr int kPromptExtra = 3;  // what an item takes beside its keys, in key tiles
 int64_t columns(const PagedBatch &b, int i) { return (int64_t)b.n_input[i] * (b.n_heads / b.n_kv_heads); }
 // Whether the batch has prompts: all requests above 32 columns are then, since both kernels take their time.
 bool has_prompts(const PagedBatch &b) {
@@ -160,7 +165,7 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
         z->maxpos = std::max(z->maxpos, c + n);
     }
     z->chunk = 64 * choose_chunk(work, b.n_kv_heads, (int64_t)kCwCtasPerSm * num_sms, 4.0, 2.0, 0.0);
-    z->pchunk = 64 * choose_chunk(pwork, vheads, num_sms, 3.0, 3.0, 0.03);
+    z->pchunk = 64 * choose_chunk(pwork, vheads, num_sms, kPromptExtra, 3.0, 0.03);
     for (int i = 0; i < b.n_req; ++i) {
         if (b.n_input[i] == 0) continue;
         if (prompts && is_prompt(b, i)) {
@@ -190,6 +195,8 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
     z->off_joins = w, w = up4(w + 8 * z->joins);
     z->off_pitems = w, w = up4(w + 8 * z->pitems);
     z->off_pjoins = w, w = up4(w + 8 * z->pjoins);
+    z->blocks = std::min<int64_t>(z->pitems * vheads, num_sms);
+    z->off_deal = w, w = up4(w + z->blocks + 1 + z->pitems * vheads);
     z->total = w;
     // 32-bit table entries and grid sizes
     return w <= INT32_MAX && z->rows * b.n_heads <= INT32_MAX && items * b.n_kv_heads <= INT32_MAX / 2 &&
@@ -245,16 +252,12 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
         if (n == 0) continue;
         const int32_t *t = b.page_table + (int64_t)i * b.table_ld;
         req[i] = (int32_t)(tile - buf);
-        for (int64_t at = 0; at < c + n; at += 16)
-            *tile++ = t[at / b.page_size] * per_page + (int32_t)(at % b.page_size) / 16;
+        for (int64_t left = (c + n + 15) / 16; left > 0; ++t)
+            for (int32_t k = 0; k < per_page && left > 0; ++k, --left) *tile++ = *t * per_page + k;
         const int32_t *mine = buf + req[i];
         tile = buf + up4(tile - buf);
-        for (int64_t j = 0; j < n; ++j, row += 4) {
-            const int64_t pos = c + j;
-            row[0] = mine[pos / 16] * 16 + (int32_t)(pos % 16);
-            row[1] = (int32_t)pos;
-            row[2] = i;
-        }
+        for (int32_t pos = (int32_t)c; pos < c + n; ++pos, row += 4)
+            row[0] = mine[pos / 16] * 16 + pos % 16, row[1] = pos, row[2] = i;
         const auto tile_items = [&](int cl, int64_t col, int64_t cols, int64_t keys) {
             const int64_t parts = parts_of(keys, z.chunk), per = parts == 1 ? keys : z.chunk;
             for (int64_t p = 0; p < parts; ++p, item[cl] += 8) {
@@ -302,6 +305,24 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
         std::stable_sort(rec, rec + z.items[c], [](const Rec &x, const Rec &y) { return x.w[1] > y.w[1]; });
     rec = reinterpret_cast<Rec *>(buf + z.off_pitems);
     std::stable_sort(rec, rec + z.pitems, [](const Rec &x, const Rec &y) { return x.w[1] > y.w[1]; });
+    // Longest first to the block with the least work so far (forwards and backwards in turn: four prompts of 1024 rows
+    // over 1000 keys, 40 heads over 8, left the busiest block 13 % above the mean, this way 2 %).
+    if (z.pitems) {
+        const int64_t vheads = b.n_heads / pack;
+        std::vector<std::pair<int64_t, int32_t>> load((size_t)z.blocks);  // a heap, the least first
+        std::vector<int32_t> to((size_t)(z.pitems * vheads));
+        int32_t *first = buf + z.off_deal, *entry = first + z.blocks + 1;
+        for (int32_t c = 0; c < (int32_t)z.blocks; ++c) load[c] = {0, c};
+        for (size_t e = 0; e < to.size(); ++e) {
+            std::pop_heap(load.begin(), load.end(), std::greater<>());
+            to[e] = load.back().second, ++first[to[e] + 1];
+            load.back().first += (rec[e / vheads].w[1] + kPpKeys - 1) / kPpKeys + kPromptExtra;
+            std::push_heap(load.begin(), load.end(), std::greater<>());
+        }
+        for (int64_t c = 0; c < z.blocks; ++c) first[c + 1] += first[c];
+        std::vector<int32_t> at(first, first + z.blocks);
+        for (size_t e = 0; e < to.size(); ++e) entry[at[to[e]]++] = (int32_t)e;
+    }
     buf[G_MAGIC] = kPagedMagic;
     buf[G_DTYPE] = b.dtype;
     buf[G_HEADS] = b.n_heads;
@@ -328,6 +349,7 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
     buf[G_PJOINS] = (int32_t)z.pjoins;
     buf[G_O_PITEMS] = (int32_t)z.off_pitems;
     buf[G_O_PJOINS] = (int32_t)z.off_pjoins;
+    buf[G_O_DEAL] = (int32_t)z.off_deal;
     buf[G_PACK] = pack;
     buf[G_BOX] = std::gcd(b.page_size, kPpKeys);
     return true;
@@ -1160,8 +1182,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 // is not finite are computed once more, key by key, over what they see.
 namespace {
 
-constexpr int kPpThreads = 384;  // two softmax warpgroups, one with the TMA and the MMA warps (and one that idles)
-constexpr int kPpTma = 8, kPpMma = 9;  // warps: the second MMA warp follows the first
+constexpr int kPpThreads = 384;  // two softmax warpgroups, one with the TMA and the MMA warps
+constexpr int kPpTma = 8, kPpMma = 9, kPpTmaV = 11;  // warps: Q and K, products of either row tile, V
 constexpr uint32_t kPpAtom = 16384;    // 128 rows of 128 bytes (Q)
 constexpr uint32_t kPpKv = 8192;       // 64 rows of 128 bytes (K, V)
 constexpr float kPpGrown = 256.f;       // sum of a tile's weights from which on m follows
@@ -1179,7 +1201,7 @@ struct PpLayout {
     static constexpr uint32_t kBytes = kOut + 8 * 32 * 80;
 };
 struct PpBars {
-    uint64_t q_full, q_empty, kv_full[8], kv_empty[8];
+    uint64_t q_full, q_empty, full[2][8], empty[2][8];  // (K, V)
     uint64_t s_full[2][2], p_full[2][2];  // [tile][buffer]
     uint64_t o_done[2][2];                // [tile]: the products of an item's last key tile but one, and of its last
     uint64_t drain[2];
@@ -1192,8 +1214,9 @@ struct PpArgs {
     float *part, *part_ml;
     const int32_t *plan;
     const int4 *items;  // {tiles at, keys, first row, rows}, {keys that the first row sees, part or -1, 0, 0}
+    const int32_t *deal;
     int64_t ld_q, ld_out, slots;
-    int n_items, vheads, pack, per_kv, kv_heads, box;  // (per_kv: tile heads of a key/value head)
+    int vheads, pack, per_kv, kv_heads, box;  // (per_kv: tile heads of a key/value head)
     float scale_log2;
     unsigned *err;
 };
@@ -1398,7 +1421,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         // (the empty ones: both MMA threads, also for what their row tile does not see)
-        for (int s = 0; s < L::kStages; ++s) mbar_init(&bar.kv_full[s], 1), mbar_init(&bar.kv_empty[s], 2);
+        for (int kv = 0; kv < 2; ++kv)
+            for (int s = 0; s < L::kStages; ++s) mbar_init(&bar.full[kv][s], 1), mbar_init(&bar.empty[kv][s], 2);
         mbar_init(&bar.q_full, 1);
         mbar_init(&bar.q_empty, 2);
         for (int x = 0; x < 4; ++x) {
@@ -1424,15 +1448,19 @@ __global__ void __launch_bounds__(kPpThreads, 1)
     pdl_wait();
     pdl_trigger();  // (behind the wait: paged_cols_kernel may run beside this one)
 
-    const int total = a.n_items * a.vheads, G = gridDim.x, tile_rows = kPpRows / a.pack;
+    const int tile_rows = kPpRows / a.pack;
+    const int32_t *const entry = a.deal + gridDim.x + 1 + a.deal[blockIdx.x];
+    const int entries = a.deal[blockIdx.x + 1] - a.deal[blockIdx.x];
     struct Item {
+        int next;  // the entry after this one
         int vh, at, keys, row, rows, sees, part;
         int n_rows[2], nk[2], n_kt;  // rows and key tiles of either row tile, key tiles of the item
     };
-    // The block's k-th item (longest first, dealt forwards and backwards in turn); false behind the last.
+    // The block's k-th item, asked for in order; false behind the last.
     const auto item_at = [&](int k, Item &it) {
-        const int e = k * G + ((k & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
-        if (e >= total) return false;
+        if (k && k >= entries) return false;
+        const int e = k ? it.next : (int)blockIdx.x;  // (which is entry[0], without waiting for it)
+        if (k + 1 < entries) it.next = entry[k + 1];
         const int4 r0 = a.items[2 * (e / a.vheads)], r1 = a.items[2 * (e / a.vheads) + 1];
         it.vh = e % a.vheads;
         it.at = r0.x, it.keys = r0.y, it.row = r0.z, it.rows = r0.w, it.sees = r1.x, it.part = r1.y;
@@ -1448,25 +1476,31 @@ __global__ void __launch_bounds__(kPpThreads, 1)
     const auto wait = [&](uint64_t *b, uint32_t phase) { return pp_wait(smem_u32(b), phase & 1u, a.err, abort); };
     // Key tiles are numbered g = 0, 1, .. across this block's items (stage g % kStages, its use g / kStages).
 
-    if (warp == kPpTma) {
+    if (warp == kPpTma || warp == kPpTmaV) {
         // ------------------------------ TMA ------------------------------
-        // One thread (a box per lane is issued lane after lane, at some 140 cycles each).
+        // One thread for Q and K, one for V (a box per lane is issued lane after lane, at some 140 cycles each).  K and V
+        // have a ring each: a stage of K is free once its S is done, two steps ahead of its P V.
         if (elect_one()) {
+            const int kv = warp == kPpTmaV;
+            uint64_t *const full = bar.full[kv], *const empty = bar.empty[kv];
+            const uint32_t ring = smem_u32(sm + (kv ? L::kV : L::kK));
             const uint64_t pol = l2_policy_evict_normal();  // every row tile of the request reads them
             const int per = a.box / 16;
-            uint32_t g = 0, q_used = 0, kv_used = 0;
+            uint32_t g = 0, q_used = 0, used = 0;
             bool ok = true;
             Item it;
             for (int k = 0; ok && item_at(k, it); ++k) {
-                if (k >= 1 && !(ok = wait(&bar.q_empty, (uint32_t)(k - 1)))) break;
-                const int tiles = it.n_rows[1] > 0 ? 2 : 1;
-                mbar_arrive_expect_tx(&bar.q_full, (uint32_t)(tiles * L::kAtoms * tile_rows * a.pack * 128));
-                for (int t = 0; t < tiles; ++t)
+                if (!kv) {
+                    if (k >= 1 && !(ok = wait(&bar.q_empty, (uint32_t)(k - 1)))) break;
+                    const int tiles = it.n_rows[1] > 0 ? 2 : 1;
+                    mbar_arrive_expect_tx(&bar.q_full, (uint32_t)(tiles * L::kAtoms * tile_rows * a.pack * 128));
+                    for (int t = 0; t < tiles; ++t)
 #pragma unroll
-                    for (int c = 0; c < L::kAtoms; ++c)
-                        pp_tma_q(smem_u32(sm + L::kQ) + (uint32_t)(t * L::kAtoms + c) * kPpAtom, &tmq, &bar.q_full, 64 * c,
-                                 it.vh * a.pack, it.row + t * tile_rows);
-                ++q_used;
+                        for (int c = 0; c < L::kAtoms; ++c)
+                            pp_tma_q(smem_u32(sm + L::kQ) + (uint32_t)(t * L::kAtoms + c) * kPpAtom, &tmq, &bar.q_full,
+                                     64 * c, it.vh * a.pack, it.row + t * tile_rows);
+                    ++q_used;
+                }
                 const int kvh = it.vh / a.per_kv, n_tiles = (it.keys + 15) / 16;
                 // slots / 16 of a key tile's four 16 keys (the plan's tables of a request start 16-byte aligned, a part
                 // of its keys at a multiple of 64)
@@ -1476,27 +1510,23 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                     const uint32_t s = g % L::kStages;
                     const int slot[4] = {next.x, next.y, next.z, next.w}, here = min(n_tiles - 4 * j, 4);
                     if (j + 1 < it.n_kt) next = index[j + 1];
-                    if (g >= L::kStages && !(ok = wait(&bar.kv_empty[s], g / L::kStages - 1))) break;
-                    mbar_arrive_expect_tx(&bar.kv_full[s],
-                                          (uint32_t)((here + per - 1) / per * a.box * (2 * 128 * L::kAtoms)));
+                    if (g >= L::kStages && !(ok = wait(&empty[s], g / L::kStages - 1))) break;
+                    mbar_arrive_expect_tx(&full[s], (uint32_t)((here + per - 1) / per * a.box * (128 * L::kAtoms)));
 #pragma unroll
-                    for (int kv = 0; kv < 2; ++kv)
+                    for (int e = 0; e < 4; ++e)
+                        if (e < here && (e & (per - 1)) == 0)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (e < here && (e & (per - 1)) == 0)
-#pragma unroll
-                                for (int c = 0; c < L::kAtoms; ++c)
-                                    pp_tma_kv(smem_u32(sm + (kv ? L::kV : L::kK)) + s * L::kTile + c * kPpKv +
-                                                  e * 2048u,
-                                              &tmkv, &bar.kv_full[s], 64 * c, slot[e] * 16, kvh, kv, pol);
-                    ++kv_used;
+                            for (int c = 0; c < L::kAtoms; ++c)
+                                pp_tma_kv(ring + s * L::kTile + c * kPpKv + e * 2048u, &tmkv, &full[s], 64 * c,
+                                          slot[e] * 16, kvh, kv, pol);
+                    ++used;
                 }
             }
             if (!ok) {  // the copies in flight land before the block ends
                 *abort = 1;
                 if (q_used > 0) mbar_wait_bounded(&bar.q_full, (q_used - 1) & 1u, a.err);
-                for (uint32_t x = kv_used > L::kStages ? kv_used - L::kStages : 0; x < kv_used; ++x)
-                    mbar_wait_bounded(&bar.kv_full[x % L::kStages], (x / L::kStages) & 1u, a.err);
+                for (uint32_t x = used > L::kStages ? used - L::kStages : 0; x < used; ++x)
+                    mbar_wait_bounded(&full[x % L::kStages], (x / L::kStages) & 1u, a.err);
             }
         }
         __syncwarp();
@@ -1525,10 +1555,10 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             const auto prepare_s = [&](uint32_t end) {
                 while (ok && !ready && more && gs < end) {
                     const uint32_t st = gs % L::kStages;
-                    ok = wait(&bar.kv_full[st], gs / L::kStages) && (js > 0 || wait(&bar.q_full, (uint32_t)ks));
+                    ok = wait(&bar.full[0][st], gs / L::kStages) && (js > 0 || wait(&bar.q_full, (uint32_t)ks));
                     if (!ok) break;
                     ready = js < (t ? is.nk[1] : is.nk[0]);
-                    if (!ready) next_s();
+                    if (!ready) mbar_arrive(&bar.empty[0][st]), next_s();
                 }
             };
             // S of one key tile, P V of one key tile: the products, and the commit that says so.
@@ -1552,43 +1582,51 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             const auto issue_s = [&]() {
                 tc_fence_after();
                 mma_s(ns & 1u, kd0 + gs % L::kStages * (L::kTile >> 4));
+                tc_commit(&bar.empty[0][gs % L::kStages]);
                 ++ns, ready = false;
                 next_s();
             };
             uint32_t g = 0;
             for (int k = 0; ok && item_at(k, iv); ++k) {
                 const int nk = t ? iv.nk[1] : iv.nk[0];
+                // (not into the next item: its queries come once the last S of this one is done, and its P V wait behind)
+                const uint32_t item_end = g + iv.n_kt;
                 for (int j = 0; ok && j < iv.n_kt; ++j, ++g) {
                     const uint32_t st = g % L::kStages, b = np & 1u;
                     for (;;) {  // (the next S is ready to go when P arrives)
-                        prepare_s(g + L::kStages);
+                        prepare_s(min(g + L::kStages, item_end));
                         if (!ready || ns >= np + 2) break;
                         issue_s();
                     }
                     if (!ok) break;
-                    if (j >= nk) {  // (S has come by here: the keys are there)
-                        mbar_arrive(&bar.kv_empty[st]);
+                    if (j >= nk) {  // (its own arrivals are in the order of the loads)
+                        if (!(ok = wait(&bar.full[1][st], g / L::kStages))) break;
+                        mbar_arrive(&bar.empty[1][st]);
                         continue;
                     }
                     // (an item's first P is written after the last item's O has been read out)
                     if (ready && ks == k && js == j + 2) {
                         // The steps in the middle of an item, with as few instructions as they can do with: this
                         // thread is alone, each of them takes its whole latency.
-                        const uint32_t full0 = smem_u32(bar.kv_full), empty0 = smem_u32(bar.kv_empty);
+                        const uint32_t k_full = smem_u32(bar.full[0]), k_empty = smem_u32(bar.empty[0]);
+                        const uint32_t v_full = smem_u32(bar.full[1]), v_empty = smem_u32(bar.empty[1]);
                         const uint32_t p0 = smem_u32(&bar.p_full[t][0]);
-                        uint32_t s_st = gs % L::kStages, s_ph = gs / L::kStages & 1u, v_st = st, n = np;
+                        uint32_t s_st = gs % L::kStages, s_ph = gs / L::kStages & 1u, n = np;
+                        uint32_t v_st = st, v_ph = g / L::kStages & 1u;
                         const int steps = nk - js;  // S of the item's key tiles js .. nk - 1
                         for (int i = 0; i < steps; ++i) {
                             const uint32_t b = n & 1u;
-                            ok = pp_wait(full0 + 8u * s_st, s_ph, a.err, abort) &&
+                            ok = pp_wait(k_full + 8u * s_st, s_ph, a.err, abort) &&
+                                 pp_wait(v_full + 8u * v_st, v_ph, a.err, abort) &&
                                  pp_wait(p0 + 8u * b, n >> 1 & 1u, a.err, abort);
                             if (!ok) break;
                             tc_fence_after();
                             mma_pv(b, vd0 + v_st * (L::kTile >> 4), (uint32_t)(j + i));
-                            pp_commit(empty0 + 8u * v_st);
+                            pp_commit(v_empty + 8u * v_st);
                             mma_s(b, kd0 + s_st * (L::kTile >> 4));
+                            pp_commit(k_empty + 8u * s_st);
                             ++n;
-                            if (++v_st == L::kStages) v_st = 0;
+                            if (++v_st == L::kStages) v_st = 0, v_ph ^= 1u;
                             if (++s_st == L::kStages) s_st = 0, s_ph ^= 1u;
                         }
                         if (!ok) break;
@@ -1598,10 +1636,10 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                         next_s();
                         continue;
                     }
-                    if (!(ok = wait(&bar.p_full[t][b], np >> 1))) break;
+                    if (!(ok = wait(&bar.full[1][st], g / L::kStages) && wait(&bar.p_full[t][b], np >> 1))) break;
                     tc_fence_after();
                     mma_pv(b, vd0 + st * (L::kTile >> 4), (uint32_t)j);
-                    tc_commit(&bar.kv_empty[st]);
+                    tc_commit(&bar.empty[1][st]);
                     if (j >= nk - 2) tc_commit(&bar.o_done[t][j == nk - 1]);
                     if (ready) issue_s();
                     ++np;
@@ -1719,7 +1757,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                     const int here = it.keys - j * kPpKeys;
                     if (here < kPpKeys) {
                         const uint32_t v = g0 + j, st = v % L::kStages;
-                        wait(&bar.kv_full[st], v / L::kStages);
+                        wait(&bar.full[1][st], v / L::kStages);
                         const int c = r / kPpKeys, vr = r % kPpKeys;  // (64 rows of up to two blocks)
                         if (vr >= here && c < L::kAtoms)
 #pragma unroll
@@ -1840,7 +1878,7 @@ cudaError_t launch_prompts(const PagedAttn &p, const int32_t *hp, const int32_t 
     PpArgs a;
     a.q = reinterpret_cast<const bf16 *>(p.q), a.layer = reinterpret_cast<const bf16 *>(p.layer);
     a.out = reinterpret_cast<bf16 *>(p.out), a.ld_q = p.ld_q, a.ld_out = p.ld_out, a.slots = hp[G_SLOTS];
-    a.plan = dp, a.items = reinterpret_cast<const int4 *>(dp + hp[G_O_PITEMS]), a.n_items = hp[G_PITEMS];
+    a.plan = dp, a.items = reinterpret_cast<const int4 *>(dp + hp[G_O_PITEMS]), a.deal = dp + hp[G_O_DEAL];
     a.pack = hp[G_PACK], a.vheads = hp[G_HEADS] / a.pack, a.kv_heads = hp[G_KV_HEADS];
     a.per_kv = a.vheads / a.kv_heads, a.box = hp[G_BOX], a.scale_log2 = scale_log2, a.err = err;
     a.part = part, a.part_ml = part + (int64_t)hp[G_PPARTS] * a.vheads * D;
@@ -1856,7 +1894,7 @@ cudaError_t launch_prompts(const PagedAttn &p, const int32_t *hp, const int32_t 
         !encode_tensor_map(&tmkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p.layer, dims, strides, box,
                            CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    const int grid = (int)std::min<int64_t>((int64_t)a.n_items * a.vheads, hp[G_SMS]);
+    const int grid = (int)std::min<int64_t>((int64_t)hp[G_PITEMS] * a.vheads, hp[G_SMS]);
     ++*launches;
     e = launch_pdl(paged_prompt_kernel<D>, dim3((unsigned)grid), dim3(kPpThreads), L::kBytes, st, tmq, tmkv, a);
     if (e != cudaSuccess || !hp[G_PJOINS]) return e;

@@ -108,6 +108,7 @@ def test_oracle_by_hand():
 # words of a plan's header (k_paged.cu)
 O_ROWS, O_REQS, O_TILES, ITEMS, PARTS, JOINS, JOINROWS, O_ITEMS, O_JOINS = 10, 11, 12, 14, 17, 18, 19, 20, 21
 PITEMS, PPARTS, PJOINS, PJOINROWS, O_PITEMS, O_PJOINS, PACK, BOX = 22, 23, 24, 25, 26, 27, 28, 29
+O_DEAL = 30
 
 
 def cover(native, p, n, c, table, page, group, kv_heads):
@@ -209,3 +210,26 @@ def test_kernels_of_one_call_start_behind_what_is_in_front_of_it():
     for kernel in ("paged_append_kernel", "paged_append_odd_kernel", "paged_join_kernel"):
         b = body("k_paged.cu", kernel)
         assert 0 <= b.find("pdl_wait();") < b.find("blockIdx")
+
+
+@pytest.mark.parametrize("heads,kv_heads,n,c", [(40, 8, (1024,) * 4, (1000,) * 4), (16, 2, (2047, 1500, 300), (0, 7, 0)),
+                                                (2, 2, (200,), (0,)), (70, 1, (100,), (900,))])
+def test_prompt_items_are_dealt_evenly(native, heads, kv_heads, n, c):
+    need = max(-(-(a + b) // 16) for a, b in zip(n, c))
+    p = plan(native, heads=heads, kv_heads=kv_heads, d=128, n=n, c=c, n_pages=need * len(n),
+             table=np.arange(need * len(n)).reshape(len(n), need))
+    tile_heads = heads // int(p[PACK])
+    total = int(p[PITEMS]) * tile_heads
+    blocks = min(152, total)
+    first = p[p[O_DEAL]:p[O_DEAL] + blocks + 1]
+    entry = p[p[O_DEAL] + blocks + 1:p[O_DEAL] + blocks + 1 + total]
+    assert first[0] == 0 and first[-1] == total and (np.diff(first) >= 1).all()
+    assert (np.sort(entry) == np.arange(total)).all() and p[O_DEAL] + blocks + 1 + total <= len(p)
+    assert (entry[first[:-1]] == np.arange(blocks)).all()  # a block knows its first without reading it
+    keys = p[p[O_PITEMS]:p[O_PITEMS] + 8 * p[PITEMS]].reshape(-1, 8)[:, 1]
+    cost = -(-keys[entry // tile_heads] // 64) + 3
+    load = np.add.reduceat(cost, first[:-1])
+    # the longest first to the least busy block: no block is above the mean by more than one item
+    assert load.max() <= cost.sum() / blocks + cost.max()
+    for a, b in zip(first, first[1:]):
+        assert (np.diff(cost[a:b]) <= 0).all()

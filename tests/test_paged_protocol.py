@@ -11,15 +11,16 @@ from test_protocol_models import Bar, run_agents, waitable
 
 
 def prompt_cta(items, stages, rnd, skip=None):
-    """items: (key tiles of row tile 0, of row tile 1, whether tile 1 has rows).  skip: a wait that is left out (planted)."""
+    """items: (key tiles of row tile 0, of row tile 1, whether tile 1 has rows).  skip: a wait left out (planted)."""
     qf, qe = Bar("q_full", 1), Bar("q_empty", 2)
-    full, empty = ([Bar(f"{x}{s}", c) for s in range(stages)] for x, c in (("kv_full", 1), ("kv_empty", 2)))
+    full, empty = ([[Bar(f"{kv}_{x}{s}", c) for s in range(stages)] for kv in "kv"]
+                   for x, c in (("full", 1), ("empty", 2)))
     sf, pf = ([[Bar(f"{x}{t}{b}", c) for b in range(2)] for t in range(2)] for x, c in (("s_full", 1), ("p_full", 4)))
     od = [[Bar(f"o_done{t}{x}", 1) for x in range(2)] for t in range(2)]
     drain = [Bar(f"drain{t}", 1) for t in range(2)]
     pending, tensor = [], [[], []]  # tensor: the products of either MMA thread
     held_q = [None]
-    held = [None] * stages  # key tile that each stage holds
+    held = [[None] * stages, [None] * stages]  # key tile that each stage of K and of V holds
     s_of = [[None, None], [None, None]]  # ("s" or "p", item, step) in the buffers of S_t
     o_of = [None, None]   # item that O_t accumulates, and the steps it has
     o_read = [set(), set()]
@@ -42,27 +43,29 @@ def prompt_cta(items, stages, rnd, skip=None):
         tensor[t].append((effect, bars))
         pending.append(complete)
 
-    def producer():
+    def producer(kv):
+        """The thread that loads Q and K, or V."""
         g = 0
         for k, (n0, n1, _) in enumerate(items):
-            if k >= 1:
-                yield from waits(qe, k - 1, "q_empty")
-            held_q[0] = None
+            if not kv:
+                if k >= 1:
+                    yield from waits(qe, k - 1, "q_empty")
+                held_q[0] = None
 
-            def q_lands(k=k):
-                held_q[0] = k
-                qf.arrive()
+                def q_lands(k=k):
+                    held_q[0] = k
+                    qf.arrive()
 
-            pending.append(q_lands)
+                pending.append(q_lands)
             for j in range(max(n0, n1)):
                 s = g % stages
                 if g >= stages:
-                    yield from waits(empty[s], g // stages - 1, "kv_empty")
-                held[s] = None  # (the copy may write from now on)
+                    yield from waits(empty[kv][s], g // stages - 1, "kv"[kv] + "_empty")
+                held[kv][s] = None  # (the copy may write from now on)
 
                 def lands(s=s, g=g):
-                    held[s] = g
-                    full[s].arrive()
+                    held[kv][s] = g
+                    full[kv][s].arrive()
 
                 pending.append(lands)
                 yield
@@ -85,11 +88,12 @@ def prompt_cta(items, stages, rnd, skip=None):
         def prepare_s(end):
             while not at["ready"] and at["g"] < min(end, total):
                 k, s = at["k"], at["g"] % stages
-                yield from waits(full[s], at["g"] // stages, "kv_full")
+                yield from waits(full[0][s], at["g"] // stages, "k_full")
                 if at["j"] == 0:
                     yield from waits(qf, k, "q_full")
                 at["ready"] = at["j"] < items[k][t]
                 if not at["ready"]:
+                    empty[0][s].arrive()
                     next_s()
                 yield
 
@@ -98,33 +102,35 @@ def prompt_cta(items, stages, rnd, skip=None):
 
             def effect():
                 assert s_of[t][b] is None, ("S overwrites", s_of[t][b])
-                assert held_q[0] == k and held[s] == g, "Q or K is not there"
+                assert held_q[0] == k and held[0][s] == g, "Q or K is not there"
                 s_of[t][b] = ("s", k, j)
 
-            issue(t, effect, [sf[t][b]])
+            issue(t, effect, [sf[t][b], empty[0][s]])
             at["n"] += 1
             at["ready"] = False
             next_s()
 
         np, g = 0, 0
         for k, item in enumerate(items):
+            item_end = g + max(item[0], item[1])
             for j in range(max(item[0], item[1])):
                 while True:
-                    yield from prepare_s(total if skip == "lead" else g + stages)
+                    yield from prepare_s(total if skip == "lead" else min(g + stages, item_end))
                     if not at["ready"] or at["n"] >= np + 2:
                         break
                     issue_s()
                     yield
                 s, b = g % stages, np & 1
+                yield from waits(full[1][s], g // stages, "v_full")
                 if j >= item[t]:
-                    empty[s].arrive()
+                    empty[1][s].arrive()
                     g += 1
                     continue
                 yield from waits(pf[t][b], np >> 1, "p_full")
 
                 def effect(g=g, s=s, k=k, j=j, b=b):
                     assert s_of[t][b] == ("p", k, j), ("P V of another tile", s_of[t][b], k, j)
-                    assert held[s] == g, "V is not there"
+                    assert held[1][s] == g, "V is not there"
                     if j == 0:
                         assert o_of[t] is None or o_of[t][0] in o_read[t], "O overwritten before it was read"
                         o_of[t] = (k, 0)
@@ -132,7 +138,7 @@ def prompt_cta(items, stages, rnd, skip=None):
                     o_of[t] = (k, j + 1)
                     s_of[t][b] = None
 
-                issue(t, effect, [empty[s]] + ([od[t][j == item[t] - 1]] if j >= item[t] - 2 else []))
+                issue(t, effect, [empty[1][s]] + ([od[t][j == item[t] - 1]] if j >= item[t] - 2 else []))
                 if at["ready"]:
                     issue_s()
                 np += 1
@@ -161,8 +167,8 @@ def prompt_cta(items, stages, rnd, skip=None):
                         assert o_of[t] == (k, j), "O rescaled before its products"
                     if j + 1 == max(n0, n1) and rnd.random() < 0.5:  # the last tile's V rows past the end
                         v = g0 + j
-                        yield from waits(full[v % stages], v // stages)
-                        assert held[v % stages] == v
+                        yield from waits(full[1][v % stages], v // stages)
+                        assert held[1][v % stages] == v
                     s_of[t][b] = ("p", k, j)
                     pf[t][b].arrive(4)
                     yield
@@ -177,7 +183,7 @@ def prompt_cta(items, stages, rnd, skip=None):
                     o_read[t].add(k)
             g0 += max(n0, n1)
 
-    run_agents([producer(), mma(0), mma(1), softmax(0), softmax(1)], pending, rnd)
+    run_agents([producer(0), producer(1), mma(0), mma(1), softmax(0), softmax(1)], pending, rnd)
     assert out == [{k: i[t] for k, i in enumerate(items) if i[t]} for t in range(2)]
 
 
@@ -199,8 +205,8 @@ def test_prompt_protocol(seed, stages):
     prompt_cta(draw(rnd, rnd.choice([1, 2, 6])), stages, rnd)
 
 
-@pytest.mark.parametrize("skip", ["q_empty", "kv_empty", "p_full", "kv_full", "q_full", "s_full", "s_rescale", "o_rescale",
-                                  "o_done", "lead"])
+@pytest.mark.parametrize("skip", ["q_empty", "k_empty", "v_empty", "p_full", "k_full", "v_full", "q_full", "s_full",
+                                  "s_rescale", "o_rescale", "o_done", "lead"])
 def test_a_wait_left_out_is_found(skip):
     for seed in range(200):
         rnd = random.Random(1000 + seed)
