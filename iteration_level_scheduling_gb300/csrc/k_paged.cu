@@ -86,11 +86,38 @@ int pack_of(int group) { return group <= 64 ? group : 1; }
 // Columns of a request: the smallest class that holds them all, else tiles of the widest (fp32: 16, by registers).
 int class_of(int64_t cols, int dtype) { return cols <= 8 ? 0 : cols <= 16 || !dtype ? 1 : 2; }
 
+// The class whose launch takes a class's requests along: bf16, the next wider one of the batch if that has at least as
+// many keys (9 requests of <= 5 / <= 7 rows over <= 1500 keys, 32 heads over 8: 22.4 / 18.0 us in launches of their
+// own, 14.6 / 16.2 this way; 16 single rows and 4 of 7 over 3000 keys 52.9, all in the widest 57.3).  fp32 pays for
+// empty columns in products: 27.6 us would become 32.6.
+struct Classes {
+    int to[kClasses] = {0, 1, 2};
+};
+Classes merged(const PagedBatch &b) {
+    Classes c;
+    if (!b.dtype) return c;
+    const bool prompts = has_prompts(b);
+    int64_t keys[kClasses] = {};
+    for (int i = 0; i < b.n_req; ++i)
+        if (b.n_input[i] > 0 && !(prompts && is_prompt(b, i))) {
+            const int64_t cols = columns(b, i);
+            keys[class_of(cols, 1)] += (cols + 31) / 32 * ((int64_t)b.ctx_len[i] + b.n_input[i]);
+        }
+    for (int x = 0, next; x + 1 < kClasses; ++x) {
+        for (next = x + 1; next < kClasses && !keys[next];) ++next;
+        if (next == kClasses || !keys[x] || keys[x] > keys[next]) continue;
+        for (int &y : c.to)
+            if (y == x) y = next;
+        keys[next] += keys[x];
+    }
+    return c;
+}
+
 // The column tiles of request i: fn(class, first column, columns, keys that the last of them sees).
 template <typename F>
-void column_tiles(const PagedBatch &b, int i, F fn) {
+void column_tiles(const PagedBatch &b, int i, const Classes &classes, F fn) {
     const int64_t group = b.n_heads / b.n_kv_heads, cols = b.n_input[i] * group;
-    const int cl = class_of(cols, b.dtype);
+    const int cl = classes.to[class_of(cols, b.dtype)];
     for (int64_t c = 0; c < cols; c += 8 << cl) {
         const int64_t n = std::min<int64_t>(8 << cl, cols - c);
         fn(cl, c, n, b.ctx_len[i] + (c + n - 1) / group + 1);
@@ -141,6 +168,7 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
     std::vector<int32_t> work, pwork;  // 64 keys each
     const int64_t pack = pack_of(b.n_heads / b.n_kv_heads), vheads = b.n_heads / pack;
     const bool prompts = has_prompts(b);
+    const Classes classes = merged(b);
     // blocks of paged_join_kernel for the columns of a tile
     const auto join_rows = [&](int64_t cols, int64_t parts) {
         const int64_t per = 512 / b.head_dim;
@@ -159,7 +187,7 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
         if (prompts && is_prompt(b, i))
             row_pairs(b, i, [&](int64_t, int64_t, int64_t keys) { pwork.push_back((int32_t)((keys + 63) / 64)); });
         else
-            column_tiles(b, i,
+            column_tiles(b, i, classes,
                          [&](int, int64_t, int64_t, int64_t keys) { work.push_back((int32_t)((keys + 63) / 64)); });
         z->tiles += up4((c + n + 15) / 16);
         z->maxpos = std::max(z->maxpos, c + n);
@@ -178,7 +206,7 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
             });
             continue;
         }
-        column_tiles(b, i, [&](int cl, int64_t, int64_t n, int64_t keys) {
+        column_tiles(b, i, classes, [&](int cl, int64_t, int64_t n, int64_t keys) {
             const int64_t parts = parts_of(keys, z->chunk);
             z->items[cl] += parts;
             if (parts == 1) return;
@@ -238,6 +266,7 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
     PagedSizes z;
     if (!paged_sizes(b, num_sms, &z) || cap < z.total) return false;
     const bool twice = writes_twice(b), prompts = has_prompts(b);
+    const Classes classes = merged(b);
     std::memset(buf, 0, sizeof(int32_t) * (size_t)z.total);
     int32_t *row = buf + z.off_rows, *req = buf + z.off_reqs, *tile = buf + z.off_tiles;
     const int32_t per_page = b.page_size / 16;
@@ -294,7 +323,7 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
         if (prompts && is_prompt(b, i))
             row_pairs(b, i, pair);
         else
-            column_tiles(b, i, tile_items);
+            column_tiles(b, i, classes, tile_items);
         first_row += n;
     }
     struct Rec {
@@ -1170,11 +1199,15 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 // (With one buffer of 128 keys the same work took 4400 cycles per 128 keys of both
 // tiles, now some 3000.)  Shared memory: Q and a ring of key tiles; the loads are
 // boxes of a page (or of the part of it that divides 64 slots).
-// Bound: head_dim 128 by shared memory, which feeds Q again for every 64 keys (160
-// KB per step, 1250 of the 1500 cycles that one takes); head_dim 64 by the softmax (64
-// exponentials and 130 other instructions per row and step, 850 of 1240 cycles).
-// 4 prompts of <= 1024 rows over <= 1000 keys, 40 heads over 8 of 128: 75 us, 0.52 of
-// the tensor peak; 8 of <= 2047 rows, 16 over 2 of 64: 52 us, 0.32.
+// Bound: a step of both tiles takes some 1200 cycles.  head_dim 128: the tensor
+// core has 1024 of them, and shared memory, which feeds Q again for every 64 keys, as
+// many.  head_dim 64: the softmax, two warps of a scheduler at once (64 exponentials and
+// 130 other instructions per row: 830 cycles, then 350 of waits and tensor-memory
+// accesses).  Beside that 1.5 to 2.4 us at an item's end, where the tensor core idles.
+// 4 prompts of <= 1024 rows over <= 1000 keys, 40 heads over 8 of 128: 68 us, 0.57 of
+// the tensor peak; 8 of <= 2047 rows, 16 over 2 of 64: 48 us, 0.35.  (K and V released
+// together: 72.5 us, and 200 rows over 30000 keys, 32 heads over 8, 138 us for 105;
+// the two tiles half a step apart: 75 and 46.6 us, dropped.)
 // Every P is formed against the m that O and l carry, which is near a row's
 // maximum and need not be it: O is rescaled only where it lags by more than 2^8.
 // Keys past the item's last are masked by index and their V rows zeroed.  A

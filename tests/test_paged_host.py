@@ -233,3 +233,18 @@ def test_prompt_items_are_dealt_evenly(native, heads, kv_heads, n, c):
     assert load.max() <= cost.sum() / blocks + cost.max()
     for a, b in zip(first, first[1:]):
         assert (np.diff(cost[a:b]) <= 0).all()
+
+
+@pytest.mark.parametrize("dtype,n,c,want", [
+    (1, (1, 1), (100, 50), (2, 0, 0)),
+    (1, (1, 3), (99, 98), (0, 2, 0)),         # 100 keys beside 101: along with the wider class
+    (1, (1, 3), (101, 98), (1, 1, 0)),        # 102 beside 101: a launch of their own
+    (1, (1, 7), (106, 100), (0, 0, 2)),
+    (1, (1, 3, 7), (50, 60, 120), (0, 0, 3)),  # 51 into 63, and these 114 into 127
+    (1, (1, 3, 7), (50, 80, 120), (0, 2, 1)),
+    (1, (1, 3, 7), (90, 70, 80), (1, 0, 2)),
+    (0, (1, 3), (50, 150), (1, 1, 0)),        # fp32: each its own
+])
+def test_narrow_requests_go_along_with_wider_ones(native, dtype, n, c, want):
+    p = plan(native, dtype=dtype, heads=8, kv_heads=2, n=n, c=c, n_pages=40, table=np.arange(30).reshape(3, 10)[:len(n)])
+    assert tuple(p[ITEMS:ITEMS + 3]) == want
