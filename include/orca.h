@@ -473,8 +473,8 @@ int64_t orca_paged_workspace_bytes(const int32_t *host_plan);
  *   if two rows share a slot, or qkv, q_out and the layer overlap in another way.
  * attention: row j of request i (a row of q: n_heads * head_dim elements) sees
  *   the positions 0 .. ctx_len + j of its request: softmax(scale q k) v per
- *   head, to the same row of out.  scale 0 means 1 / sqrt(head_dim); it must be
- *   finite and not negative.  The rows' own K/V must have been appended.  Scores
+ *   head, to the same row of out.  scale 0 means 1 / sqrt(head_dim); it must not be
+ *   negative or above 2^127.  The rows' own K/V must have been appended.  Scores
  *   and sums are held in fp32; bf16 weights enter the second product with 16 bits
  *   (up to 16 rows x heads per key/value head) or 8; fp32 operands are used as two
  *   parts, 21 bits.  The plan chooses by the whole batch how a request's rows are
@@ -483,7 +483,7 @@ int64_t orca_paged_workspace_bytes(const int32_t *host_plan);
  *   makes the rows that see it not finite (a key in the whole head, unless its
  *   score is -inf, which takes it out; a value in its component at least), and no
  *   others.  A row whose scores are all -inf is NaN.  Sizes beyond 2^100 may
- *   overflow.  INVALID if out overlaps q or the layer. */
+ *   overflow.  INVALID if out or the workspace overlaps another of the four. */
 int orca_op_paged_append(orca_engine *eng, const void *qkv, int64_t ld_qkv, void *kv_layer, const int32_t *host_plan,
                          const int32_t *dev_plan, const float *rope, int32_t rope_len, int32_t rot_dim,
                          int32_t neighbours, void *q_out, int64_t ld_q);

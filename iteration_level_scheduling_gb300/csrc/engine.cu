@@ -1203,12 +1203,16 @@ int orca_op_paged_attention(orca_engine *E, const void *q, int64_t ld_q, const v
     if (!ld_out) ld_out = w;
     if (!aligned16(kv_layer) || !aligned16(dev_plan) || !rows_ok(q, ld_q, w, (int)es) ||
         !rows_ok(out, ld_out, w, (int)es) || !aligned16(workspace) ||
-        (!workspace && paged_workspace_bytes(host_plan) > 0) || !(scale >= 0.f) || scale > 3e38f || !on_device(E))
+        (!workspace && paged_workspace_bytes(host_plan) > 0) || !(scale >= 0.f) || scale > 0x1p127f || !on_device(E))
         return ORCA_ERR_INVALID;
     if (p.rows == 0) return ORCA_OK;
     const int64_t q_bytes = ((p.rows - 1) * ld_q + w) * es, out_bytes = ((p.rows - 1) * ld_out + w) * es;
     const int64_t layer_bytes = 2 * (int64_t)p.kv_heads * p.slots * p.head_dim * es;
-    if (overlap(out, out_bytes, q, q_bytes) || overlap(out, out_bytes, kv_layer, layer_bytes)) return ORCA_ERR_INVALID;
+    const int64_t ws_bytes = paged_workspace_bytes(host_plan);
+    if (overlap(out, out_bytes, q, q_bytes) || overlap(out, out_bytes, kv_layer, layer_bytes) ||
+        (ws_bytes && (overlap(workspace, ws_bytes, q, q_bytes) || overlap(workspace, ws_bytes, out, out_bytes) ||
+                      overlap(workspace, ws_bytes, kv_layer, layer_bytes))))
+        return ORCA_ERR_INVALID;
     int n = 0;
     const float s = scale > 0.f ? scale : 1.f / std::sqrt((float)p.head_dim);
     const cudaError_t e =

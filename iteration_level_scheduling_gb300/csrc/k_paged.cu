@@ -97,15 +97,15 @@ Classes merged(const PagedBatch &b) {
     Classes c;
     if (!b.dtype) return c;
     const bool prompts = has_prompts(b);
-    int64_t keys[kClasses] = {};
+    double keys[kClasses] = {};  // (of a batch whose sizes are not checked yet)
     for (int i = 0; i < b.n_req; ++i)
         if (b.n_input[i] > 0 && !(prompts && is_prompt(b, i))) {
             const int64_t cols = columns(b, i);
-            keys[class_of(cols, 1)] += (cols + 31) / 32 * ((int64_t)b.ctx_len[i] + b.n_input[i]);
+            keys[class_of(cols, 1)] += (double)((cols + 31) / 32) * ((double)b.ctx_len[i] + b.n_input[i]);
         }
     for (int x = 0, next; x + 1 < kClasses; ++x) {
-        for (next = x + 1; next < kClasses && !keys[next];) ++next;
-        if (next == kClasses || !keys[x] || keys[x] > keys[next]) continue;
+        for (next = x + 1; next < kClasses && keys[next] == 0;) ++next;
+        if (next == kClasses || keys[x] == 0 || keys[x] > keys[next]) continue;
         for (int &y : c.to)
             if (y == x) y = next;
         keys[next] += keys[x];

@@ -637,3 +637,31 @@ def test_beside_the_engines_own_attention(native, eng, d):
     e2.close()
     s.check(out)
     s.check(own)
+
+
+@pytest.mark.parametrize("reqs", [[(1, 300), (3, 700), (6, 900), (1, 0)],
+                                  [(1, 40), (4, 90), (1, 15)],
+                                  [(2, 500), (7, 100), (3, 450), (1, 20)]])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 16), ("fp32", 64)])
+def test_requests_of_few_rows_in_a_wider_launch(native, eng, dtype, d, reqs):
+    s = Case(native, eng, 31, dtype, 8, 2, d, 16, reqs)
+    s.check(s.attention())
+
+
+def test_a_workspace_that_overlaps_is_refused(native, eng):
+    s = Case(native, eng, 32, "bf16", 4, 1, 128, 16, [(1, 30000)])
+    size = eng.paged_workspace_bytes(s.plan)
+    assert size > 0
+    out = torch.zeros((1, 512), dtype=torch.bfloat16, device="cuda")
+    both = torch.zeros(size + 4096, dtype=torch.uint8, device="cuda")
+    ok = dict(q=s.dq.data_ptr(), layer=s.layer.data_ptr(), plan=s.plan, dev_plan=s.dplan.data_ptr(),
+              workspace=both.data_ptr(), out=out.data_ptr())
+    for bad in (dict(workspace=ok["layer"]), dict(workspace=ok["layer"] + 1024), dict(out=both.data_ptr()),
+                dict(out=both.data_ptr() + size - 16), dict(q=both.data_ptr()), dict(q=both.data_ptr() + size - 16),
+                dict(scale=2.0 ** 127.5)):
+        with pytest.raises(native.OrcaError) as e:
+            eng.op_paged_attention(**{**ok, **bad})
+        assert e.value.code == native.ERR_INVALID, bad
+    up = (size + 15) // 16 * 16
+    eng.op_paged_attention(**{**ok, "out": both.data_ptr() + up})  # right behind it
+    eng.sync()
