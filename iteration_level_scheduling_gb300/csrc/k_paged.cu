@@ -8,6 +8,7 @@
 // the first divided by 16), so that no kernel divides by the page size and a
 // tile of 16 keys never crosses a page.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <functional>
 #include <numeric>
@@ -69,55 +70,65 @@ struct PagedSizes {
 
 // Prompts: rows x heads of one key/value head as the 128 rows of a tensor-core tile; two tiles share their keys, 64 at
 // a time.
-constexpr int kPromptCols = 64;  // columns from which on the longest request makes a batch's requests prompts
 constexpr int kPpRows = 128, kPpKeys = 64;
 constexpr int kPromptExtra = 3;  // what an item takes beside its keys, in key tiles
-int64_t columns(const PagedBatch &b, int i) { return (int64_t)b.n_input[i] * (b.n_heads / b.n_kv_heads); }
-// Whether the batch has prompts: all requests above 32 columns are then, since both kernels take their time.
-bool has_prompts(const PagedBatch &b) {
-    int64_t most = 0;
-    for (int i = 0; i < b.n_req; ++i) most = std::max(most, columns(b, i));
-    return b.dtype && b.head_dim >= 64 && most > kPromptCols;
-}
-bool is_prompt(const PagedBatch &b, int i) { return columns(b, i) > 32; }
 // Heads in a tile: all that share a key/value head, or one where they are too many to fill 128 rows well.
 int pack_of(int group) { return group <= 64 ? group : 1; }
 
-// Columns of a request: the smallest class that holds them all, else tiles of the widest (fp32: 16, by registers).
-int class_of(int64_t cols, int dtype) { return cols <= 8 ? 0 : cols <= 16 || !dtype ? 1 : 2; }
-
-// The class whose launch takes a class's requests along: bf16, the next wider one of the batch if that has at least as
-// many keys (9 requests of <= 5 / <= 7 rows over <= 1500 keys, 32 heads over 8: 22.4 / 18.0 us in launches of their
-// own, 14.6 / 16.2 this way; 16 single rows and 4 of 7 over 3000 keys 52.9, all in the widest 57.3).  fp32 pays for
-// empty columns in products: 27.6 us would become 32.6.
+// How requests are attended: classes 0 to 2 as column tiles of 8, 16 and 32, kClasses as prompts.  A request is in the
+// narrowest class that holds all its columns (rows x heads of a key/value head; fp32: 16 at most, by registers).
+// Prompts (bf16, head_dim 64 and 128): above 32 columns, unless the batch has none above 64 and more keys below (one of
+// 12 rows over 8000 keys, 32 heads over 8: 14.1 us, as tiles of 32 19.0; 32 of <= 12 over <= 1500 50.3 and 38.5);
+// where heads are tiles of their own, above 32 rows (8 of 1 / 8 / <= 110 rows over <= 1000 keys, 71 heads over one: as
+// prompts 38 / 39 / 41, as tiles 13 / 17 / 78).
+// A class goes along with the next wider one of the batch that has at least as many keys, which saves a launch
+// beside another (9 of <= 5 / <= 7 rows over <= 1500 keys: 22.4 / 18.0 us in launches of their own, 14.6 / 16.2 this way,
+// 32 of <= 16 46.5 and 30.4; 64 single rows beside 2000 over 1000 keys 88 and 96; over 36 batches of single rows
+// beside a prompt 2 % less).  fp32 pays for empty columns in products: 9 of <= 3 rows 27.6 and 32.6, so there none does.
 struct Classes {
-    int to[kClasses] = {0, 1, 2};
-};
-Classes merged(const PagedBatch &b) {
-    Classes c;
-    if (!b.dtype) return c;
-    const bool prompts = has_prompts(b);
-    double keys[kClasses] = {};  // (of a batch whose sizes are not checked yet)
-    for (int i = 0; i < b.n_req; ++i)
-        if (b.n_input[i] > 0 && !(prompts && is_prompt(b, i))) {
-            const int64_t cols = columns(b, i);
-            keys[class_of(cols, 1)] += (double)((cols + 31) / 32) * ((double)b.ctx_len[i] + b.n_input[i]);
-        }
-    for (int x = 0, next; x + 1 < kClasses; ++x) {
-        for (next = x + 1; next < kClasses && keys[next] == 0;) ++next;
-        if (next == kClasses || keys[x] == 0 || keys[x] > keys[next]) continue;
-        for (int &y : c.to)
-            if (y == x) y = next;
-        keys[next] += keys[x];
+    int to[kClasses + 1] = {0, 1, 2, kClasses};
+    bool fp32, prompts = false;
+    int64_t group;
+
+    int base(int64_t n) const {
+        const int64_t cols = n * group;
+        if (cols <= 8) return 0;
+        if (fp32 || cols <= 16) return 1;
+        return prompts && (group <= 64 ? cols > 32 : n > 32) ? kClasses : 2;
     }
-    return c;
-}
+    int of(int64_t n) const { return to[base(n)]; }
+
+    explicit Classes(const PagedBatch &b) : fp32(!b.dtype), group(b.n_heads / b.n_kv_heads) {
+        if (fp32) return;
+        double keys[kClasses + 1];
+        bool sure = false;
+        const auto count = [&]() {  // (of a batch whose sizes are not checked yet)
+            std::fill(keys, keys + kClasses + 1, 0.);
+            for (int i = 0; i < b.n_req; ++i) {
+                const double n = b.n_input[i], cols = n * (double)group;
+                if (n <= 0) continue;
+                keys[base(b.n_input[i])] += std::ceil(cols / (prompts ? 256 : 32)) * (b.ctx_len[i] + n);
+                sure |= cols > 64;
+            }
+        };
+        prompts = b.head_dim >= 64;
+        count();
+        if (prompts && !sure && keys[kClasses] < keys[0] + keys[1] + keys[2]) prompts = false, count();
+        for (int x = 0, next; x < kClasses; ++x) {
+            for (next = x + 1; next <= kClasses && keys[next] == 0;) ++next;
+            if (next > kClasses || keys[x] == 0 || keys[x] > keys[next]) continue;
+            for (int &y : to)
+                if (y == x) y = next;
+            keys[next] += keys[x];
+        }
+    }
+};
 
 // The column tiles of request i: fn(class, first column, columns, keys that the last of them sees).
 template <typename F>
 void column_tiles(const PagedBatch &b, int i, const Classes &classes, F fn) {
-    const int64_t group = b.n_heads / b.n_kv_heads, cols = b.n_input[i] * group;
-    const int cl = classes.to[class_of(cols, b.dtype)];
+    const int64_t group = classes.group, cols = b.n_input[i] * group;
+    const int cl = classes.of(b.n_input[i]);
     for (int64_t c = 0; c < cols; c += 8 << cl) {
         const int64_t n = std::min<int64_t>(8 << cl, cols - c);
         fn(cl, c, n, b.ctx_len[i] + (c + n - 1) / group + 1);
@@ -167,8 +178,7 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
     *z = {};
     std::vector<int32_t> work, pwork;  // 64 keys each
     const int64_t pack = pack_of(b.n_heads / b.n_kv_heads), vheads = b.n_heads / pack;
-    const bool prompts = has_prompts(b);
-    const Classes classes = merged(b);
+    const Classes classes(b);
     // blocks of paged_join_kernel for the columns of a tile
     const auto join_rows = [&](int64_t cols, int64_t parts) {
         const int64_t per = 512 / b.head_dim;
@@ -184,7 +194,7 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
         for (int64_t p = 0; p * b.page_size < c + n; ++p)
             if (t[p] < 0 || t[p] >= b.n_pages) return false;
         z->rows += n;
-        if (prompts && is_prompt(b, i))
+        if (classes.of(b.n_input[i]) == kClasses)
             row_pairs(b, i, [&](int64_t, int64_t, int64_t keys) { pwork.push_back((int32_t)((keys + 63) / 64)); });
         else
             column_tiles(b, i, classes,
@@ -196,7 +206,7 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
     z->pchunk = 64 * choose_chunk(pwork, vheads, num_sms, kPromptExtra, 3.0, 0.03);
     for (int i = 0; i < b.n_req; ++i) {
         if (b.n_input[i] == 0) continue;
-        if (prompts && is_prompt(b, i)) {
+        if (classes.of(b.n_input[i]) == kClasses) {
             row_pairs(b, i, [&](int64_t, int64_t rows, int64_t keys) {
                 const int64_t parts = parts_of(keys, z->pchunk);
                 z->pitems += parts;
@@ -265,8 +275,8 @@ int64_t paged_plan_words(const PagedBatch &b, int num_sms) {
 bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t cap) {
     PagedSizes z;
     if (!paged_sizes(b, num_sms, &z) || cap < z.total) return false;
-    const bool twice = writes_twice(b), prompts = has_prompts(b);
-    const Classes classes = merged(b);
+    const bool twice = writes_twice(b);
+    const Classes classes(b);
     std::memset(buf, 0, sizeof(int32_t) * (size_t)z.total);
     int32_t *row = buf + z.off_rows, *req = buf + z.off_reqs, *tile = buf + z.off_tiles;
     const int32_t per_page = b.page_size / 16;
@@ -320,7 +330,7 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
             pjoin[4] = (int32_t)ppart, pjoin[5] = 2 * kPpRows, pjoin[6] = tile_rows * pack;
             pjoin += 8, ppart += parts * 2 * kPpRows;
         };
-        if (prompts && is_prompt(b, i))
+        if (classes.of(b.n_input[i]) == kClasses)
             row_pairs(b, i, pair);
         else
             column_tiles(b, i, classes, tile_items);

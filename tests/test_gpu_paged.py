@@ -665,3 +665,13 @@ def test_a_workspace_that_overlaps_is_refused(native, eng):
     up = (size + 15) // 16 * 16
     eng.op_paged_attention(**{**ok, "out": both.data_ptr() + up})  # right behind it
     eng.sync()
+
+
+@pytest.mark.parametrize("heads,kv,reqs", [(8, 2, [(40, 300), (8, 200), (1, 100), (1, 0)]),
+                                           (8, 2, [(9, 70), (8, 30), (1, 15)]),
+                                           (8, 2, [(9, 70), (8, 300), (8, 200)]), (71, 1, [(33, 40), (1, 30), (7, 0)]),
+                                           (71, 1, [(32, 40), (1, 300)]), (16, 16, [(130, 5), (20, 100), (1, 60)])])
+@pytest.mark.parametrize("d", [64, 128])
+def test_requests_of_few_rows_as_prompts(native, eng, d, heads, kv, reqs):
+    s = Case(native, eng, 33, "bf16", heads, kv, d, 16, reqs)
+    s.check(s.attention())

@@ -248,3 +248,20 @@ def test_prompt_items_are_dealt_evenly(native, heads, kv_heads, n, c):
 def test_narrow_requests_go_along_with_wider_ones(native, dtype, n, c, want):
     p = plan(native, dtype=dtype, heads=8, kv_heads=2, n=n, c=c, n_pages=40, table=np.arange(30).reshape(3, 10)[:len(n)])
     assert tuple(p[ITEMS:ITEMS + 3]) == want
+
+
+@pytest.mark.parametrize("heads,d,n,c,want", [
+    (8, 64, (9,), (50,), (0, 0, 0, 1)),                 # 36 columns
+    (8, 64, (8,), (50,), (0, 0, 1, 0)),
+    (8, 32, (9,), (50,), (0, 0, 2, 0)),
+    (8, 64, (9, 8), (50, 40), (0, 0, 0, 2)),            # 48 keys go along with 59
+    (8, 64, (9, 8), (50, 60), (0, 0, 3, 0)),            # 68 do not, and what has 64 columns at most is tiles then
+    (8, 64, (17, 8), (50, 60), (0, 0, 1, 1)),
+    (8, 64, (17, 1, 8), (50, 20, 60), (0, 0, 2, 1)),
+    (8, 64, (17, 1, 8), (50, 60, 2), (1, 0, 0, 2)),
+    (142, 64, (32,), (50,), (0, 0, 71, 0)),             # 71 heads over one: tiles of a head's rows
+    (142, 64, (33,), (50,), (0, 0, 0, 1)),
+])
+def test_which_requests_are_prompts(native, heads, d, n, c, want):
+    p = plan(native, heads=heads, kv_heads=2, d=d, n=n, c=c, n_pages=40, table=np.arange(30).reshape(3, 10)[:len(n)])
+    assert tuple(p[ITEMS:ITEMS + 3]) + (p[PITEMS],) == want
