@@ -77,14 +77,15 @@ int pack_of(int group) { return group <= 64 ? group : 1; }
 
 // How requests are attended: classes 0 to 2 as column tiles of 8, 16 and 32, kClasses as prompts.  A request is in the
 // narrowest class that holds all its columns (rows x heads of a key/value head; fp32: 16 at most, by registers).
-// Prompts (bf16, head_dim 64 and 128): above 32 columns, unless the batch has none above 64 and more keys below (one of
-// 12 rows over 8000 keys, 32 heads over 8: 14.1 us, as tiles of 32 19.0; 32 of <= 12 over <= 1500 50.3 and 38.5);
-// where heads are tiles of their own, above 32 rows (8 of 1 / 8 / <= 110 rows over <= 1000 keys, 71 heads over one: as
-// prompts 38 / 39 / 41, as tiles 13 / 17 / 78).
-// A class goes along with the next wider one of the batch that has at least as many keys, which saves a launch
-// beside another (9 of <= 5 / <= 7 rows over <= 1500 keys: 22.4 / 18.0 us in launches of their own, 14.6 / 16.2 this way,
-// 32 of <= 16 46.5 and 30.4; 64 single rows beside 2000 over 1000 keys 88 and 96; over 36 batches of single rows
-// beside a prompt 2 % less).  fp32 pays for empty columns in products: 9 of <= 3 rows 27.6 and 32.6, so there none does.
+// Prompts (bf16, head_dim 64 and 128): above 16 columns (4 requests of <= 7 rows over <= 500 keys, 32 heads over 8: 8.7
+// us, as tiles of 32 13.7; 64 single rows over <= 8000, 40 heads over one: 41 and 67), unless the batch has none above
+// 64 columns and more than twice their keys below (9 of <= 5 over <= 1500: 14.9 us, with a launch of prompts 20.9).
+// Where heads are tiles of their own, above 32 rows (8 of 1 / 8 / <= 110 rows over <= 1000 keys, 71 heads over one: as
+// prompts 38 / 39 / 41 us, as tiles 13 / 17 / 78).
+// A class goes along with the next wider one of the batch if that has at least as many keys, which saves a launch
+// beside another (64 of <= 7 over <= 3000: 103 us in three launches, 86 in one; 64 single rows beside 2000 over 1000
+// keys 88 and 96; over 36 batches of single rows beside a prompt 2 % less).  fp32 pays for empty columns in products:
+// 9 of <= 3 rows 27.6 and 32.6, so there none does.
 struct Classes {
     int to[kClasses + 1] = {0, 1, 2, kClasses};
     bool fp32, prompts = false;
@@ -94,7 +95,7 @@ struct Classes {
         const int64_t cols = n * group;
         if (cols <= 8) return 0;
         if (fp32 || cols <= 16) return 1;
-        return prompts && (group <= 64 ? cols > 32 : n > 32) ? kClasses : 2;
+        return prompts && (group <= 64 || n > 32) ? kClasses : 2;
     }
     int of(int64_t n) const { return to[base(n)]; }
 
@@ -113,13 +114,12 @@ struct Classes {
         };
         prompts = b.head_dim >= 64;
         count();
-        if (prompts && !sure && keys[kClasses] < keys[0] + keys[1] + keys[2]) prompts = false, count();
-        for (int x = 0, next; x < kClasses; ++x) {
-            for (next = x + 1; next <= kClasses && keys[next] == 0;) ++next;
-            if (next > kClasses || keys[x] == 0 || keys[x] > keys[next]) continue;
-            for (int &y : to)
-                if (y == x) y = next;
-            keys[next] += keys[x];
+        if (prompts && !sure && 2 * keys[kClasses] < keys[0] + keys[1] + keys[2]) prompts = false, count();
+        for (int x = kClasses - 1; x >= 0; --x) {
+            int next = x + 1;
+            while (next <= kClasses && keys[next] == 0) ++next;
+            if (next > kClasses || keys[x] > keys[to[next]]) continue;
+            to[x] = to[next], keys[to[x]] += keys[x];
         }
     }
 };

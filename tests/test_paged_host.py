@@ -240,25 +240,27 @@ def test_prompt_items_are_dealt_evenly(native, heads, kv_heads, n, c):
     (1, (1, 3), (99, 98), (0, 2, 0)),         # 100 keys beside 101: along with the wider class
     (1, (1, 3), (101, 98), (1, 1, 0)),        # 102 beside 101: a launch of their own
     (1, (1, 7), (106, 100), (0, 0, 2)),
-    (1, (1, 3, 7), (50, 60, 120), (0, 0, 3)),  # 51 into 63, and these 114 into 127
-    (1, (1, 3, 7), (50, 80, 120), (0, 2, 1)),
-    (1, (1, 3, 7), (90, 70, 80), (1, 0, 2)),
+    (1, (1, 3, 7), (150, 60, 120), (0, 0, 3)),  # 63 into 127, then 151 into these 190
+    (1, (1, 3, 7), (50, 130, 120), (0, 2, 1)),
+    (1, (1, 3, 7), (150, 50, 70), (1, 0, 2)),
     (0, (1, 3), (50, 150), (1, 1, 0)),        # fp32: each its own
 ])
 def test_narrow_requests_go_along_with_wider_ones(native, dtype, n, c, want):
-    p = plan(native, dtype=dtype, heads=8, kv_heads=2, n=n, c=c, n_pages=40, table=np.arange(30).reshape(3, 10)[:len(n)])
+    p = plan(native, dtype=dtype, heads=8, kv_heads=2, d=32, n=n, c=c, n_pages=40,
+             table=np.arange(30).reshape(3, 10)[:len(n)])
     assert tuple(p[ITEMS:ITEMS + 3]) == want
 
 
 @pytest.mark.parametrize("heads,d,n,c,want", [
-    (8, 64, (9,), (50,), (0, 0, 0, 1)),                 # 36 columns
-    (8, 64, (8,), (50,), (0, 0, 1, 0)),
-    (8, 32, (9,), (50,), (0, 0, 2, 0)),
-    (8, 64, (9, 8), (50, 40), (0, 0, 0, 2)),            # 48 keys go along with 59
-    (8, 64, (9, 8), (50, 60), (0, 0, 3, 0)),            # 68 do not, and what has 64 columns at most is tiles then
-    (8, 64, (17, 8), (50, 60), (0, 0, 1, 1)),
-    (8, 64, (17, 1, 8), (50, 20, 60), (0, 0, 2, 1)),
-    (8, 64, (17, 1, 8), (50, 60, 2), (1, 0, 0, 2)),
+    (8, 64, (5,), (50,), (0, 0, 0, 1)),                 # 20 columns
+    (8, 64, (4,), (50,), (0, 1, 0, 0)),
+    (8, 32, (5,), (50,), (0, 0, 1, 0)),
+    (8, 64, (5, 4), (50, 51), (0, 0, 0, 2)),            # 55 keys go along with 55
+    (8, 64, (5, 4), (50, 52), (0, 1, 0, 1)),            # 56 do not
+    (8, 64, (5, 4), (50, 106), (0, 1, 0, 1)),
+    (8, 64, (5, 4), (50, 107), (0, 1, 1, 0)),           # twice the prompts' keys: these are tiles, of 64 columns at most
+    (8, 64, (17, 4), (50, 140), (0, 1, 0, 1)),          # 68 columns: a prompt whatever is beside it
+    (8, 64, (9, 1, 3), (50, 60, 50), (0, 0, 0, 3)),      # 53 into 59, then 61 into 112
     (142, 64, (32,), (50,), (0, 0, 71, 0)),             # 71 heads over one: tiles of a head's rows
     (142, 64, (33,), (50,), (0, 0, 0, 1)),
 ])
