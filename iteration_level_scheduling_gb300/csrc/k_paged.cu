@@ -148,17 +148,17 @@ int64_t parts_of(int64_t keys, int64_t chunk) { return keys * 2 <= chunk * 3 ? 1
 
 // Keys of a part, in units of 64, by a model of the time: an item takes its units and `extra` more, a block its items
 // one after another (the longest first, so that the last start evens out to half of the longest), and parts have to
-// be joined.  `units`: the items' keys, each for `heads` heads.
-int64_t choose_chunk(const std::vector<int32_t> &units, int64_t heads, int64_t blocks, double extra, double join,
-                     double per_part) {
+// be joined.  `units`: the items' keys, each for `heads` heads; a part has `least_units` or more.
+int64_t choose_chunk(const std::vector<int32_t> &units, int64_t heads, int64_t blocks, int64_t least_units, double extra,
+                     double join, double per_part) {
     int64_t total = 0, most = 1;
     for (const int32_t u : units) total += u * heads, most = std::max<int64_t>(most, u);
     int64_t best = most;
     double least = 0;
     const int64_t cand[] = {most, total / blocks + 1, total / (2 * blocks) + 1, total / (3 * blocks) + 1,
-                            total / (6 * blocks) + 1, 48, 32, 24, 16, 12, 8, 6, 4};
+                            total / (6 * blocks) + 1, 48, 32, 24, 16, 12, 8, 6, 4, 3, 2};
     for (const int64_t c : cand) {
-        if (c > most || c < 4) continue;
+        if (c > most || c < least_units) continue;
         int64_t items = 0, parts = 0;
         double cost = 0, longest = 0;
         for (const int32_t u : units) {
@@ -202,8 +202,11 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
         z->tiles += up4((c + n + 15) / 16);
         z->maxpos = std::max(z->maxpos, c + n);
     }
-    z->chunk = 64 * choose_chunk(work, b.n_kv_heads, (int64_t)kCwCtasPerSm * num_sms, 4.0, 2.0, 0.0);
-    z->pchunk = 64 * choose_chunk(pwork, vheads, num_sms, kPromptExtra, 3.0, 0.03);
+    // a unit's time goes with its bytes (one request over 500 / 2000 keys, 32 heads over 8 of 128: 6.8 / 8.0 us with
+    // parts of 256 keys or more, 5.7 / 6.0 of 128; 300 keys, 20 heads of 64: 5.0 whole, 5.8 in parts of 128)
+    const double small = std::min(2.0, 256.0 / (b.head_dim * (b.dtype ? 2 : 4)));
+    z->chunk = 64 * choose_chunk(work, b.n_kv_heads, (int64_t)kCwCtasPerSm * num_sms, 2, 4 * small, 2 * small, 0.0);
+    z->pchunk = 64 * choose_chunk(pwork, vheads, num_sms, 4, kPromptExtra, 3.0, 0.03);
     for (int i = 0; i < b.n_req; ++i) {
         if (b.n_input[i] == 0) continue;
         if (classes.of(b.n_input[i]) == kClasses) {
