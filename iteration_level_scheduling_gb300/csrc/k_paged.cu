@@ -144,7 +144,7 @@ void row_pairs(const PagedBatch &b, int i, F fn) {
     }
 }
 // Parts that a tile's keys are cut into.
-int64_t parts_of(int64_t keys, int64_t chunk) { return keys * 2 <= chunk * 3 ? 1 : (keys + chunk - 1) / chunk; }
+int64_t parts_of(int64_t keys, int64_t chunk) { return keys * 4 <= chunk * 5 ? 1 : (keys + chunk - 1) / chunk; }
 
 // Keys of a part, in units of 64, by a model of the time: an item takes its units and `extra` more, a block its items
 // one after another (the longest first, so that the last start evens out to half of the longest), and parts have to
@@ -156,7 +156,7 @@ int64_t choose_chunk(const std::vector<int32_t> &units, int64_t heads, int64_t b
     int64_t best = most;
     double least = 0;
     const int64_t cand[] = {most, total / blocks + 1, total / (2 * blocks) + 1, total / (3 * blocks) + 1,
-                            total / (6 * blocks) + 1, 48, 32, 24, 16, 12, 8, 6, 4, 3, 2};
+                            total / (6 * blocks) + 1, 48, 40, 32, 28, 24, 20, 16, 14, 12, 10, 8, 6, 4, 3, 2};
     for (const int64_t c : cand) {
         if (c > most || c < least_units) continue;
         int64_t items = 0, parts = 0;
