@@ -584,7 +584,7 @@ cudaError_t paged_append(const PagedAppend &p, const int32_t *hp, const int32_t 
 // key that only some columns see is added up key by key.
 //
 // Bound by HBM for long contexts (64 requests of <= 4000 keys, 40 heads over 8 of
-// 128: 663 MB in 107 us, 91 % of the copy rate; 40 heads of their own, 64 x <= 1000 keys:
+// 128: 663 MB in 105 us, 93 % of the copy rate; 40 heads of their own, 64 x <= 1000 keys:
 // 97 %), by latency below some 20 MB: one request over 300 keys, 20 heads of 64, 4.8 us.
 // fp32 by issue: the parts cost some 800 instructions per 16 keys (64 x <= 1000 keys, 8
 // heads of 128: 60 us, 82 % of the copy rate).
