@@ -1252,7 +1252,7 @@ struct PpBars {
     uint64_t o_done[2][2];                // [tile]: the products of an item's last key tile but one, and of its last
     uint64_t drain[2];
     uint32_t tmem;
-    int abort;
+    int abort, alive;  // alive: changes while a softmax warp works on rows key by key
 };
 struct PpArgs {
     const bf16 *q, *layer;
@@ -1366,7 +1366,8 @@ __device__ __forceinline__ uint64_t pp_add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// A bounded wait; when it gives up, or another warp has, the abort flag is set and every later wait ends at once.
+// A bounded wait; when it gives up, or another warp has, the abort flag is set and every later wait ends at once.  A
+// warp that computes rows once more, key by key, takes seconds over long contexts: its time does not count.
 __device__ __noinline__ bool pp_wait_on(uint32_t bar, uint32_t parity, unsigned *err, volatile int *abort);
 __device__ __forceinline__ bool pp_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -1381,12 +1382,13 @@ __device__ __forceinline__ bool pp_try(uint32_t bar, uint32_t parity) {
 }
 __device__ bool pp_wait_on(uint32_t bar, uint32_t parity, unsigned *err, volatile int *abort) {
     unsigned long long t0 = 0;
+    int alive = abort[1];
     for (uint32_t it = 1;; ++it) {
         if (pp_try(bar, parity)) return true;
         if (*abort) return false;
         if ((it & 63u) == 0) {
             const unsigned long long now = global_timer_ns();
-            if (t0 == 0) t0 = now;
+            if (t0 == 0 || alive != abort[1]) t0 = now, alive = abort[1];
             if (now - t0 > kWaitLimitNs) {
                 raise_err(err, ERR_WAIT_TIMEOUT);
                 *abort = 1;
@@ -1411,7 +1413,7 @@ __device__ __forceinline__ float pp_max3(float a, float b, float c) {
 // lane holds m, l and 8 components of o, lane % (D / 8) * 8 on.
 template <int D>
 __device__ __noinline__ void pp_row(const PpArgs &a, const bf16 *q, const int32_t *tiles, int n, int kvh, float &m,
-                                    float &l, float *o) {
+                                    float &l, float *o, volatile int *alive) {
     constexpr int LPT = D / 8, TPW = 32 / LPT;
     const int lane = threadIdx.x & 31, g = lane / LPT, sub = lane % LPT;
     const bf16 *kb = a.layer + (int64_t)kvh * a.slots * D + sub * 8, *vb = kb + (int64_t)a.kv_heads * a.slots * D;
@@ -1422,6 +1424,7 @@ __device__ __noinline__ void pp_row(const PpArgs &a, const bf16 *q, const int32_
     for (int e = 0; e < 8; ++e) o[e] = 0.f;
     for (int t0 = 0; t0 < n; t0 += TPW) {
         const int t = t0 + g;
+        if (t0 % 4096 == 0) *alive = *alive + 1;  // (which of the warps' counts stays does not matter)
         float k[8], v[8], s = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) k[e] = v[e] = 0.f;
@@ -1478,7 +1481,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         }
         mbar_init(&bar.drain[0], 1);
         mbar_init(&bar.drain[1], 1);
-        *abort = 0;
+        *abort = 0, abort[1] = 0;
         fence_mbar_init();
         prefetch_tmap(&tmq);
         prefetch_tmap(&tmkv);
@@ -1890,7 +1893,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 const int seen = min(it.sees + t * tile_rows + rr / a.pack, it.keys);
                 float m2, l2, o2[8];
                 pp_row<D>(a, a.q + (int64_t)row2 * a.ld_q + (int64_t)head2 * D, a.plan + it.at, seen, it.vh / a.per_kv,
-                          m2, l2, o2);
+                          m2, l2, o2, abort + 1);
                 const int64_t at2 = at - r + rr;
                 if (lane < D / 8) {
                     if (it.part < 0) {

@@ -675,3 +675,24 @@ def test_a_workspace_that_overlaps_is_refused(native, eng):
 def test_requests_of_few_rows_as_prompts(native, eng, d, heads, kv, reqs):
     s = Case(native, eng, 33, "bf16", heads, kv, d, 16, reqs)
     s.check(s.attention())
+
+
+def test_rows_that_take_seconds_hold_nobody_up(native, eng):
+    """Rows over a value that is not finite are computed once more, key by key: over 600,000 keys that is longer than a
+    wait may last, and the requests behind them on the same block still come out."""
+    d, page, ctx, rows, sms = 128, 64, 600000, 250, torch.cuda.get_device_properties(0).multi_processor_count
+    pages = -(-(ctx + rows) // page)
+    table = np.tile(np.arange(1, pages + 1, dtype=np.int32), (2 * sms, 1))
+    table[:sms, 0] = 0  # the first half of the requests begins with a page of its own
+    layer = torch.zeros((2, 1, (pages + 1) * page, d), dtype=torch.bfloat16, device="cuda")
+    layer[1] = 1
+    layer[1, 0, 3, 5] = float("nan")
+    plan = eng.paged_plan(1, 1, 1, d, page, pages + 1, [rows] * (2 * sms), [ctx] * (2 * sms), table)
+    dplan = torch.from_numpy(plan).cuda()
+    q = torch.ones((2 * sms * rows, d), dtype=torch.bfloat16, device="cuda")
+    out, work = torch.zeros_like(q), torch.zeros(eng.paged_workspace_bytes(plan) + 16, dtype=torch.uint8, device="cuda")
+    eng.op_paged_attention(q.data_ptr(), layer.data_ptr(), plan, dplan.data_ptr(), work.data_ptr(), out.data_ptr())
+    eng.sync()
+    want = torch.ones_like(out)
+    want[:sms * rows, 5] = float("nan")
+    assert torch.equal(torch.nan_to_num(out, 7.0), torch.nan_to_num(want, 7.0))
