@@ -1210,7 +1210,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 // waits, tensor-memory accesses; measured with that work left out), so the
 // next S is always under way: a softmax finds it when it is done with the last.
 // (With one buffer of 128 keys the same work took 4400 cycles per 128 keys of both
-// tiles, now some 3000.)  Shared memory: Q and a ring of key tiles; the loads are
+// tiles, now 2400.)  Shared memory: Q, a ring of K and one of V; the loads are
 // boxes of a page (or of the part of it that divides 64 slots).
 // Bound: a step of both tiles takes some 1200 cycles.  head_dim 128: the tensor
 // core has 1024 of them, and shared memory, which feeds Q again for every 64 keys, as
