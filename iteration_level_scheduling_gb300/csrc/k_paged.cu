@@ -1486,6 +1486,9 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         prefetch_tmap(&tmq);
         prefetch_tmap(&tmkv);
     }
+    // Tensor memory only once the kernel in front has ended: one that triggers ahead of its own allocation could wait
+    // for these columns, and this one for its end.
+    pdl_wait();
     if (warp == kPpMma) {
         tmem_alloc(&bar.tmem, 512);
         tmem_relinquish();
@@ -1494,7 +1497,6 @@ __global__ void __launch_bounds__(kPpThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
-    pdl_wait();
     pdl_trigger();  // (behind the wait: paged_cols_kernel may run beside this one)
 
     const int tile_rows = kPpRows / a.pack;

@@ -267,3 +267,11 @@ def test_narrow_requests_go_along_with_wider_ones(native, dtype, n, c, want):
 def test_which_requests_are_prompts(native, heads, d, n, c, want):
     p = plan(native, heads=heads, kv_heads=2, d=d, n=n, c=c, n_pages=40, table=np.arange(30).reshape(3, 10)[:len(n)])
     assert tuple(p[ITEMS:ITEMS + 3]) + (p[PITEMS],) == want
+
+
+def test_tensor_memory_is_taken_once_the_kernel_in_front_has_ended():
+    """A kernel in front that triggers ahead of its own allocation would wait for the columns, and they for its end; what
+    follows this one starts when all its blocks have theirs."""
+    from test_launch_order import body
+    b = body("k_paged.cu", "paged_prompt_kernel")
+    assert 0 <= b.find("pdl_wait();") < b.find("tmem_alloc(") < b.find("__syncthreads();") < b.find("pdl_trigger();")
