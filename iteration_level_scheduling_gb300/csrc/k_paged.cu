@@ -1729,8 +1729,11 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             // keys 0 .. sees - 1 of the item are this row's
             const int jr = r / a.pack, sees = it.sees + t * tile_rows + jr;
             const int clean = min(it.sees + t * tile_rows, it.keys) / kPpKeys;  // key tiles that all rows see in full
+            // Lanes without a row of the item (the next request's rows, or what lay in shared memory where the heads of a
+            // tile do not divide 128) take no part in the warp's votes: m stays 0, their sums are not looked at.
+            const bool mine = r < n_rows * a.pack;
             // m in the units of S, neg = -m scale, the last tile's sum
-            float m = -INFINITY, l = 0.f, neg = 0.f, last = 0.f;
+            float m = mine ? -INFINITY : 0.f, l = 0.f, neg = 0.f, last = 0.f;
             bool big = false;                                     // s scale - m in one step would keep what m lost
             for (int j = 0; j < nk; ++j, ++n) {
                 const uint32_t b = n & 1u, s_t = lane_t + 128u * t + 64u * b;
@@ -1801,7 +1804,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 }
                 float l0, l1;
                 pp_unpair(pp_add2(sum[0], sum[1]), l0, l1);
-                last = l0 + l1;
+                last = mine ? l0 + l1 : 0.f;
                 l += last;
                 if (j >= clean) {
                     // V rows past the item's last key: zero, once they have landed
@@ -1824,7 +1827,6 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 if (lane == 0) mbar_arrive(&bar.p_full[t][b]);
             }
             // ---- the item's output ----
-            const bool mine = r < n_rows * a.pack;
             const int row = it.row + t * tile_rows + jr, head = it.vh * a.pack + r % a.pack;
             const int64_t out_at = mine ? (int64_t)row * a.ld_out + (int64_t)head * D : -1;
             uint8_t *const stage = sm + L::kOut + warp * (32 * 80);

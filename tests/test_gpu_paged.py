@@ -696,3 +696,47 @@ def test_rows_that_take_seconds_hold_nobody_up(native, eng):
     want = torch.ones_like(out)
     want[:sms * rows, 5] = float("nan")
     assert torch.equal(torch.nan_to_num(out, 7.0), torch.nan_to_num(want, 7.0))
+
+
+# --------------------------------------------------------------------------- #
+# what a row's bits may depend on
+# --------------------------------------------------------------------------- #
+def fill_shared_memory(native, eng, word):
+    """An attention of fp32 rows on every SM whose queries, keys and values are `word` throughout: what the kernels after it
+    find in shared memory that they do not write themselves."""
+    sms, ctx = torch.cuda.get_device_properties(0).multi_processor_count, 255
+    n_pages = 4 * sms * (ctx + 1) // 16
+    plan = eng.paged_plan(native.DTYPE_FP32, 1, 1, 128, 16, n_pages, [1] * 4 * sms, [ctx] * 4 * sms,
+                          np.arange(n_pages).reshape(4 * sms, -1))
+    layer, q = (torch.full(s, word, dtype=torch.int32, device="cuda") for s in ((2, n_pages * 16, 128), (4 * sms, 128)))
+    dev, out = torch.from_numpy(plan).cuda(), torch.empty((4 * sms, 128), device="cuda")
+    work = torch.empty(max(16, eng.paged_workspace_bytes(plan)), dtype=torch.uint8, device="cuda")
+    eng.op_paged_attention(q.data_ptr(), layer.data_ptr(), plan, dev.data_ptr(), work.data_ptr(), out.data_ptr())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,kv_heads", [(40, 8), (6, 2), (7, 1), (12, 2), (44, 1)])
+def test_bits_do_not_depend_on_what_ran_before(native, eng, heads, kv_heads, d):
+    """Groups that do not divide 128 leave rows of a prompt's tile without a query.  Words that are large, or NaN, as
+    two bf16 numbers lie there; zero is the calm case."""
+    s = Case(native, eng, 41, "bf16", heads, kv_heads, d, 16, [(150, 90), (64, 300), (257, 0)])
+    outs = []
+    for word in (0, 0x70007000, 0x7FC07FC0, 0x71007F80 - (1 << 31)):
+        fill_shared_memory(native, eng, word)
+        outs.append(s.attention())
+    s.check(outs[0])
+    for o in outs[1:]:
+        assert torch.equal(outs[0], o)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,kv_heads", [(8, 2), (40, 8), (16, 16)])
+def test_bits_do_not_depend_on_the_next_requests_rows(native, eng, heads, kv_heads, d):
+    """A request's last tile is filled up with rows of the next request, which are not its own."""
+    s = Case(native, eng, 42, "bf16", heads, kv_heads, d, 16, [(30, 100), (45, 200), (70, 130)])
+    want, calm = s.attention(), s.q[30:].copy()
+    s.check(want)
+    for factor in (1e30, -1e36, np.nan):
+        s.q[30:] = rounded(calm * factor, "bf16")
+        s.upload()
+        assert torch.equal(want[:30], s.attention()[:30])
