@@ -476,10 +476,11 @@ int64_t orca_paged_workspace_bytes(const int32_t *host_plan);
  *   head, to the same row of out.  scale 0 means 1 / sqrt(head_dim); it must not be
  *   negative or above 2^127.  The rows' own K/V must have been appended.  Scores
  *   and sums are held in fp32; bf16 weights enter the second product with 16 bits
- *   (requests of up to 16 rows x heads per key/value head, unless wider ones of the
- *   batch take them along) or 8; fp32 operands are used as two parts, 21 bits.  The plan chooses by the whole batch how a request's rows are
- *   attended and where its keys are split, so the last bits of a row may depend on
- *   the batch (never from call to call of a plan).  A key or value that is not finite
+ *   for requests of up to 16 rows x heads per key/value head, whatever is beside them
+ *   in the batch, and with 8 for others; fp32 operands are used as two parts, 21 bits.
+ *   The plan chooses by the whole batch how a request's rows are attended and where its
+ *   keys are split, so the last bits of a row may depend on the batch (never from call
+ *   to call of a plan).  A key or value that is not finite
  *   makes the rows that see it not finite (a key in the whole head, unless its
  *   score is -inf, which takes it out; a value in its component at least), and no
  *   others.  A row whose scores are all -inf is NaN.  Sizes beyond 2^100 may

@@ -740,3 +740,55 @@ def test_bits_do_not_depend_on_the_next_requests_rows(native, eng, heads, kv_hea
         s.q[30:] = rounded(calm * factor, "bf16")
         s.upload()
         assert torch.equal(want[:30], s.attention()[:30])
+
+
+def narrow_limits(q, k, v, c):
+    """limits() where weights enter the second product with 16 bits: rounded to bf16 and what is left of them rounded again,
+    so that each is off by 2^-8 2^-8 of itself at most and the output by 2^-16 sum w |v| <= 2^-16 max |v|."""
+    heads, d = q.shape[1:]
+    ref, _ = paged.attention(q, k, v, c, 1 / np.sqrt(d))
+    size = max((np.abs(q[:, h]) @ np.abs(k[h // (heads // len(k))]).T).max() for h in range(heads)) / np.sqrt(d)
+    tol = 2 * (d + 16) * 2.0 ** -23 * size + 3 * 2.0 ** -20 + k.shape[1] * 2.0 ** -23 + 2.0 ** -16
+    return ref, U["bf16"] * np.abs(ref) + tol * np.abs(v).max()
+
+
+def one_part(q, k, v, c):
+    """The output where weights are rounded to bf16 once: what narrow_limits() has to tell from it."""
+    n, heads, d = q.shape
+    out = np.zeros(q.shape)
+    for h in range(heads):
+        kk, vv = (x[h // (heads // len(k))].astype(np.float64) for x in (k, v))
+        s = q[:, h].astype(np.float64) @ kk.T / np.sqrt(d)
+        s = np.where(np.arange(kk.shape[0])[None] <= c + np.arange(n)[:, None], s, -np.inf)
+        w = np.exp(s - s.max(1, keepdims=True))
+        out[:, h] = rounded(w, "bf16") @ vv / w.sum(1, keepdims=True)
+    return rounded(out, "bf16")
+
+
+# Requests of at most 16 rows x heads of a key/value head, alone, beside one another and beside wider ones: prompts, and
+# (at head_dim 16 and 32, or where there are few of them) tiles of 32 columns.
+COMPANY = [(8, 2, [(1, 40)], 1), (8, 2, [(1, 40), (4, 30), (2, 60)], 3), (8, 2, [(1, 40), (4, 30), (2, 60), (200, 100)], 3),
+           (8, 2, [(1, 40), (3, 20), (9, 50)], 2), (8, 2, [(1, 40), (4, 20), (5, 30), (7, 20)], 2),
+           (8, 2, [(4, 20), (1, 100), (1, 90), (6, 30)], 3), (12, 4, [(5, 33), (1, 64), (1, 20), (300, 0)], 3),
+           (4, 4, [(16, 30), (1, 70), (128, 0), (500, 20)], 2),
+           (40, 8, [(1, 50), (3, 40), (1, 300), (260, 300)], 3), (16, 1, [(1, 60), (20, 50)], 1)]
+
+
+@pytest.mark.parametrize("heads,kv_heads,reqs,narrow", COMPANY)
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+def test_narrow_requests_keep_16_bits_of_their_weights(native, eng, d, heads, kv_heads, reqs, narrow):
+    s = Case(native, eng, 43, "bf16", heads, kv_heads, d, 16, reqs)
+    s.q = rounded(s.q / 4, "bf16")
+    s.host[1] = np.where(np.isnan(s.host[1]), np.nan, rounded(s.g.uniform(-1, 1, s.host[1].shape), "bf16"))
+    s.upload()
+    out = s.attention()
+    s.check(out)
+    got, r, told = out.float().cpu().numpy()[:s.rows, :s.H].reshape(s.rows, heads, d), 0, 0
+    for i, ((n, c), t) in enumerate(zip(reqs, s.table)):
+        if i < narrow:
+            k, v = s.host[:, :, paged.slots(t, 16, 0, n + c)]
+            ref, lim = narrow_limits(s.q[r:r + n], k, v, c)
+            assert (np.abs(got[r:r + n] - ref) <= lim).all(), float((np.abs(got[r:r + n] - ref) / lim).max())
+            told += (np.abs(one_part(s.q[r:r + n], k, v, c) - ref) > lim).sum()
+        r += n
+    assert told  # (one part would be seen)
