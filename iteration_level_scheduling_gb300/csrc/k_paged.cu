@@ -1731,7 +1731,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         // are formed against the m that is there, without a look at its maximum, and m follows with the next tile where
         // their sum shows that it lags by more than 2^8 (O and l with it).  What overflows meanwhile is not finite in O
         // and is computed once more below.
-        // (A wait that gave up sets the abort flag, and the rest runs through on what is there.)
+        // (A wait that gave up sets the abort flag: the item's key tiles run through on what is there, then the role ends
+        // without an output.)
         const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_t = tmem + ((uint32_t)(quarter * 32) << 16), o_t = lane_t + 256u + 128u * t;
         const uint32_t s_full = smem_u32(&bar.s_full[t][0]);
@@ -1840,9 +1841,9 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                         const int here = it.keys - j * kPpKeys;
                         if (here < kPpKeys) {
                             const uint32_t v = g0 + j, st = v % L::kStages;
-                            wait(&bar.full[1][st], v / L::kStages);
+                            const bool landed = wait(&bar.full[1][st], v / L::kStages);
                             const int c = r / kPpKeys, vr = r % kPpKeys;  // (64 rows of up to two blocks)
-                            if (vr >= here && c < L::kAtoms)
+                            if (landed && vr >= here && c < L::kAtoms)
 #pragma unroll
                                 for (int x = 0; x < 8; ++x)
                                     *reinterpret_cast<uint4 *>(sm + L::kV + st * L::kTile + c * kPpKv + vr * 128 +
@@ -1861,6 +1862,11 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             else
                 key_tiles(std::false_type());
             // ---- the item's output ----
+            if (nk > 0) {
+                if (nk >= 2) wait(&bar.o_done[t][0], n_before++);
+                wait(&bar.o_done[t][1], n_last++);
+            }
+            if (__any_sync(kFull, *abort != 0)) break;
             const int row = it.row + t * tile_rows + jr, head = it.vh * a.pack + r % a.pack;
             const int64_t out_at = mine ? (int64_t)row * a.ld_out + (int64_t)head * D : -1;
             uint8_t *const stage = sm + L::kOut + warp * (32 * 80);
@@ -1868,8 +1874,6 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             float *const part = a.part + at * D;
             bool bad = false;
             if (nk > 0) {
-                if (nk >= 2) wait(&bar.o_done[t][0], n_before++);
-                wait(&bar.o_done[t][1], n_last++);
                 tc_fence_after();
                 const float inv = 1.f / l;
                 const uint64_t inv2 = pp_pair(inv, inv);
@@ -1925,7 +1929,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             if (mine && it.part >= 0)
                 *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m * a.scale_log2, l);
             unsigned todo = __ballot_sync(kFull, mine && (bad || (l - l) != 0.f));
-            for (; todo; todo &= todo - 1) {  // rows with something that is not finite, over what they see
+            for (; todo && !__any_sync(kFull, *abort != 0); todo &= todo - 1) {  // rows with something that is not finite, over what they see
                 const int rr = quarter * 32 + __ffs(todo) - 1;
                 const int row2 = it.row + t * tile_rows + rr / a.pack, head2 = it.vh * a.pack + rr % a.pack;
                 const int seen = min(it.sees + t * tile_rows + rr / a.pack, it.keys);

@@ -275,3 +275,20 @@ def test_tensor_memory_is_taken_once_the_kernel_in_front_has_ended():
     from test_launch_order import body
     b = body("k_paged.cu", "paged_prompt_kernel")
     assert 0 <= b.find("pdl_wait();") < b.find("tmem_alloc(") < b.find("__syncthreads();") < b.find("pdl_trigger();")
+
+
+def test_a_wait_that_gave_up_ends_the_softmax_role():
+    """Of the prompt kernel, once a wait has run out: no item's output is written, no row is computed key by key (which
+    takes seconds over long contexts and holds up the other waits' limits), and values that may still be landing are left
+    alone."""
+    from test_launch_order import body
+    b = body("k_paged.cu", "paged_prompt_kernel")
+    b = b[b.index("warp < kPpTma)"):]
+    votes = "__any_sync(kFull, *abort != 0)"
+    end = b.index("if (" + votes + ") break;")
+    assert b.rindex("wait(", 0, end) < end < min(b.index("a.out"), b.index("part + x"), b.index("a.part_ml"))
+    assert "wait(" not in b[end:]  # the last of the item's waits stand in front of it
+    loop = b.index("pp_row<D>")
+    assert b[b.rindex("for (", 0, loop):loop].count(votes) == 1
+    zero = b.index("make_uint4(0, 0, 0, 0)")
+    assert "landed = wait(&bar.full[1]" in b[:zero] and "if (landed &&" in b[b.index("landed = "):zero]
