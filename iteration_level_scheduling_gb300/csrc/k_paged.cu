@@ -1178,10 +1178,14 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
     const int x = col / r1.z * kPpRows + col % r1.z;  // (a tile of 128 may hold fewer columns than that)
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // (A prompt's sums may be 2^127 over an m that lags as far behind: factors in two halves, exp2 ends at 2^-126.)
+    constexpr bool kHalves = sizeof(T) == 2;
     const auto add = [&](float m2, float l2, const float4 &o2) {
-        const float mx = fmaxf(m, m2), base = cw_base(mx), f = cw_exp2(m - base), f2 = cw_exp2(m2 - base);
-        l = l * f + l2 * f2, m = mx;
-        o.x = o.x * f + o2.x * f2, o.y = o.y * f + o2.y * f2, o.z = o.z * f + o2.z * f2, o.w = o.w * f + o2.w * f2;
+        const float mx = fmaxf(m, m2), base = cw_base(mx), power = kHalves ? 0.5f : 1.f;
+        const float f = cw_exp2(power * (m - base)), f2 = cw_exp2(power * (m2 - base));
+        const auto sum = [&](float x, float y) { return kHalves ? x * f * f + y * f2 * f2 : x * f + y * f2; };
+        l = sum(l, l2), m = mx;
+        o = make_float4(sum(o.x, o2.x), sum(o.y, o2.y), sum(o.z, o2.z), sum(o.w, o2.w));
     };
     if (col < r0.z) {
 #pragma unroll 4
@@ -1779,14 +1783,15 @@ __global__ void __launch_bounds__(kPpThreads, 1)
 #pragma unroll
                         for (int x = 0; x < 64; x += 2)
                             top = pp_max3(top, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+                        // The factor in two halves: sums of up to 2^128 have to come down to 1, and exp2 ends at 2^-126.
                         float alpha = 1.f;
                         if (m == -INFINITY) {  // no key seen so far: O and l are 0
                             m = top;
                         } else if (last > kPpGrown) {
                             const float to = fmaxf(top, m + __log2f(last) / a.scale_log2);
-                            alpha = cw_exp2((m - to) * a.scale_log2);
+                            alpha = cw_exp2(0.5f * ((m - to) * a.scale_log2));
                             m = to;
-                            l *= alpha;
+                            l = l * alpha * alpha;
                         }
                         if (__any_sync(kFull, alpha != 1.f)) {  // (not in an item's first tile)
                             // O: once the P V so far are done (the next S was issued behind them)
@@ -1801,7 +1806,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                                 tmem_ld16(o_t + x, o);
                                 uint32_t w[16];
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha * alpha);
                                 pp_st16(o_t + x, w);
                             }
                         }

@@ -792,3 +792,21 @@ def test_narrow_requests_keep_16_bits_of_their_weights(native, eng, d, heads, kv
             told += (np.abs(one_part(s.q[r:r + n], k, v, c) - ref) > lim).sum()
         r += n
     assert told  # (one part would be seen)
+
+
+@pytest.mark.parametrize("jump", [60.0, 100.0, 125.0, 126.0, 126.5, 127.0, 127.5])
+@pytest.mark.parametrize("reqs,first,second", [([(150, 100)], 70, 130), ([(150, 100)], 70, 98), ([(33, 217)], 130, 195),
+                                               ([(40, 3000)], 250, 256), ([(40, 3000)], 200, 700),
+                                               ([(40, 3000)], 10, 2600), ([(40, 3000)], 250, 2999)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_sums_near_the_end_of_fp32(native, eng, d, reqs, first, second, jump):
+    """Two keys that are 2^jump above all others: in tiles or in parts of the keys that follow one another, whose weights are
+    as large as fp32 holds over the maximum in front of them, and one when it has followed."""
+    s = Case(native, eng, 44, "bf16", 8, 2, d, 16, reqs)
+    (n, c), at = reqs[0], paged.slots(s.table[0], 16, 0, sum(reqs[0]))
+    s.q[:], s.q[..., 0] = 0, 1
+    s.host[0][:, at] = 0
+    s.host[0][:, at[[first, second]], 0] = jump
+    s.host[1][:, at] = rounded(s.g.uniform(-1, 1, s.host[1][:, at].shape), "bf16")
+    s.upload()
+    s.check(s.attention(scale=float(np.log(2.0))), scale=float(np.log(2.0)))
