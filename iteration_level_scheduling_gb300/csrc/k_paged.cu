@@ -1867,17 +1867,17 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             else
                 key_tiles(std::false_type());
             // ---- the item's output ----
-            if (nk > 0) {
-                if (nk >= 2) wait(&bar.o_done[t][0], n_before++);
-                wait(&bar.o_done[t][1], n_last++);
-            }
-            if (__any_sync(kFull, *abort != 0)) break;
             const int row = it.row + t * tile_rows + jr, head = it.vh * a.pack + r % a.pack;
             const int64_t out_at = mine ? (int64_t)row * a.ld_out + (int64_t)head * D : -1;
             uint8_t *const stage = sm + L::kOut + warp * (32 * 80);
             const int64_t at = (int64_t)it.part * a.vheads + (int64_t)it.vh * (2 * kPpRows) + t * kPpRows + r;
             float *const part = a.part + at * D;
             bool bad = false;
+            if (nk > 0) {
+                if (nk >= 2) wait(&bar.o_done[t][0], n_before++);
+                wait(&bar.o_done[t][1], n_last++);
+            }
+            if (__any_sync(kFull, *abort != 0)) break;
             if (nk > 0) {
                 tc_fence_after();
                 const float inv = 1.f / l;
