@@ -484,7 +484,10 @@ int64_t orca_paged_workspace_bytes(const int32_t *host_plan);
  *   makes the rows that see it not finite (a key in the whole head, unless its
  *   score is -inf, which takes it out; a value in its component at least), and no
  *   others.  A row whose scores are all -inf is NaN.  Sizes beyond 2^100 may
- *   overflow.  INVALID if out or the workspace overlaps another of the four. */
+ *   overflow.  Rows attended as prompts take hundreds of times as long, and the others
+ *   of the call wait for them, where a score is +inf or 88 (2^127 as a weight) above all
+ *   scores of the keys in front of its 64 keys, or where they lie in one tile (128 rows x
+ *   heads) with a row that sees a value which is not finite and theirs to miss.  INVALID if out or the workspace overlaps another of the four. */
 int orca_op_paged_append(orca_engine *eng, const void *qkv, int64_t ld_qkv, void *kv_layer, const int32_t *host_plan,
                          const int32_t *dev_plan, const float *rope, int32_t rope_len, int32_t rot_dim,
                          int32_t neighbours, void *q_out, int64_t ld_q);

@@ -1244,8 +1244,13 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 // Every P is formed against the m that O and l carry, which is near a row's
 // maximum and need not be it: O is rescaled only where it lags by more than 2^8.
 // Keys past the item's last are masked by index and their V rows zeroed.  A
-// masked weight of 0 times a value that is not finite is NaN: rows whose output
-// is not finite are computed once more, key by key, over what they see.
+// masked weight of 0 times a value that is not finite is NaN, and a tile's weights
+// overflow where its scores are 2^127 above all in front of them: a row whose output is
+// not finite, and of which one of these may be so, is computed once more, key by key,
+// over what it sees, 1.2 us for two keys (head_dim 64: four): four prompts of <= 1024
+// rows over <= 1000 keys, the largest with scores that grow by more than 2^127 from
+// tile to tile, 42 ms for 61 us.  (Weights formed anew against the maximum within
+// the tile took 120 us there, but 5 to 12 % of everyone else's time.)
 namespace {
 
 constexpr int kPpThreads = 384;  // two softmax warpgroups, one with the TMA and the MMA warps
@@ -1253,6 +1258,7 @@ constexpr int kPpTma = 8, kPpMma = 9, kPpTmaV = 11;  // warps: Q and K, products
 constexpr uint32_t kPpAtom = 16384;    // 128 rows of 128 bytes (Q)
 constexpr uint32_t kPpKv = 8192;       // 64 rows of 128 bytes (K, V)
 constexpr float kPpGrown = 256.f;       // sum of a tile's weights from which on m follows
+constexpr float kPpOver = 0x1p20f;      // and from which on O may overflow (values of 2^100)
 
 template <int D>
 struct PpLayout {
@@ -1445,6 +1451,7 @@ __device__ __noinline__ void pp_row(const PpArgs &a, const bf16 *q, const int32_
     for (int t0 = 0; t0 < n; t0 += TPW) {
         const int t = t0 + g;
         if (t0 % 4096 == 0) *alive = *alive + 1;  // (which of the warps' counts stays does not matter)
+        if (t0 % 64 == 0 && __any_sync(0xffffffffu, l != l)) break;  // a score of +inf or NaN: so is every component
         float k[8], v[8], s = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) k[e] = v[e] = 0.f;
@@ -1471,6 +1478,23 @@ __device__ __noinline__ void pp_row(const PpArgs &a, const bf16 *q, const int32_
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = o[e] * f + __shfl_xor_sync(0xffffffffu, o[e], x) * f2;
     }
+}
+
+// The last of keys first .. end - 1 of an item whose value is not finite in some component, or -1; by the whole warp.
+template <int D>
+__device__ __noinline__ int pp_last_odd(const PpArgs &a, const int32_t *tiles, int first, int end, int kvh) {
+    constexpr int LPT = D / 8, TPW = 32 / LPT;
+    const int lane = threadIdx.x & 31;
+    const bf16 *vb = a.layer + ((int64_t)a.kv_heads + kvh) * a.slots * D + lane % LPT * 8;
+    int last = -1;
+    for (int t = first + lane / LPT; t < end; t += TPW) {
+        float v[8], z = 0.f;
+        load16(vb + ((int64_t)tiles[t / 16] * 16 + t % 16) * D, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z = fmaf(v[e], 0.f, z);
+        if (z != 0.f) last = t;
+    }
+    return __reduce_max_sync(0xffffffffu, last);
 }
 
 template <int D>
@@ -1760,8 +1784,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             // Lanes without a row of the item (the next request's rows, or what lay in shared memory where the heads of a
             // tile do not divide 128) take no part in the warp's votes: m stays 0, their sums are not looked at.
             const bool mine = r < n_rows * a.pack;
-            // m in the units of S, neg = -m scale, the last tile's sum
-            float m = mine ? -INFINITY : 0.f, l = 0.f, neg = 0.f, last = 0.f;
+            // m in the units of S, neg = -m scale, the last tile's sum and the largest from which m followed
+            float m = mine ? -INFINITY : 0.f, l = 0.f, neg = 0.f, last = 0.f, most = 0.f;
             bool big = false;                                     // s scale - m in one step would keep what m lost
             // (The key tiles' loop twice: with narrow requests' part as a branch of one loop, the others took 4 to 7 % more.)
             const auto key_tiles = [&](auto narrow) __attribute__((always_inline)) {
@@ -1792,6 +1816,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                             alpha = cw_exp2(0.5f * ((m - to) * a.scale_log2));
                             m = to;
                             l = l * alpha * alpha;
+                            most = fmaxf(most, last);
                         }
                         if (__any_sync(kFull, alpha != 1.f)) {  // (not in an item's first tile)
                             // O: once the P V so far are done (the next S was issued behind them)
@@ -1934,7 +1959,16 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             if (mine && it.part >= 0)
                 *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m * a.scale_log2, l);
             unsigned todo = __ballot_sync(kFull, mine && (bad || (l - l) != 0.f));
-            for (; todo && !__any_sync(kFull, *abort != 0); todo &= todo - 1) {  // rows with something that is not finite, over what they see
+            if (todo) {
+                // Rows that are not finite and might not have to be: where a tile's weights outgrew m, and where (no score but)
+                // a value is not finite that the tiles held and that is not the row's to see.
+                const bool jumped = fmaxf(most, last) > kPpOver;
+                const int odd = pp_last_odd<D>(a, a.plan + it.at, max(it.sees + t * tile_rows, 0),
+                                               min(nk * kPpKeys, it.keys), it.vh / a.per_kv);
+                todo &= __ballot_sync(kFull, jumped || ((l - l) == 0.f && sees <= odd));
+            }
+            // (key by key over what they see)
+            for (; todo && !__any_sync(kFull, *abort != 0); todo &= todo - 1) {
                 const int rr = quarter * 32 + __ffs(todo) - 1;
                 const int row2 = it.row + t * tile_rows + rr / a.pack, head2 = it.vh * a.pack + rr % a.pack;
                 const int seen = min(it.sees + t * tile_rows + rr / a.pack, it.keys);

@@ -810,3 +810,80 @@ def test_sums_near_the_end_of_fp32(native, eng, d, reqs, first, second, jump):
     s.host[1][:, at] = rounded(s.g.uniform(-1, 1, s.host[1][:, at].shape), "bf16")
     s.upload()
     s.check(s.attention(scale=float(np.log(2.0))), scale=float(np.log(2.0)))
+
+
+# --------------------------------------------------------------------------- #
+# what one request may cost the others
+# --------------------------------------------------------------------------- #
+def microseconds(call):
+    best = []
+    for _ in range(5):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        call()
+        b.record()
+        b.synchronize()
+        best.append(a.elapsed_time(b) * 1e3)
+    return min(best)
+
+
+def growing(s, i, per_tile):
+    """Request i's queries and keys positive, its keys growing by `per_tile` with every 64 of them."""
+    r, (n, c) = sum(s.n[:i]), s.reqs[i]
+    at = paged.slots(s.table[i], s.page, 0, n + c)
+    s.q[r:r + n] = np.abs(s.q[r:r + n])
+    s.host[0][:, at] = rounded(np.abs(s.host[0][:, at]) * (np.arange(n + c) // 64 * per_tile)[None, :, None], s.dtype)
+    s.upload()
+
+
+@pytest.mark.parametrize("per_tile", [0.5, 3.0, 20.0, 1e6, 1e25])
+@pytest.mark.parametrize("reqs", [[(150, 700)], [(40, 3000), (2, 900)], [(3, 500), (130, 100)]])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_that_outgrow_the_maximum(native, eng, d, reqs, per_tile):
+    """Every tile of 64 keys is by far above the ones before it (also by more than fp32 holds as a weight)."""
+    s = Case(native, eng, 51, "bf16", 8, 2, d, 16, reqs)
+    growing(s, 0, per_tile)
+    s.check(s.attention())
+
+
+@pytest.mark.parametrize("heads,kv_heads,d", [(40, 8, 128), (16, 2, 64)])
+def test_one_request_does_not_hold_up_the_others(native, eng, heads, kv_heads, d):
+    """A key or a value that is not finite but seen by all rows takes about the time of others (a row at a time, key by key,
+    took some 500 times as long)."""
+    s = Case(native, eng, 52, "bf16", heads, kv_heads, d, 16, [(700, 900), (600, 800), (500, 300)])
+    calm_keys = s.host.copy()
+    s.q[..., 5] = np.abs(s.q[..., 5]) + 1  # (a key of +inf gives scores of +inf)
+    s.upload()
+    s.attention()
+    calm = microseconds(lambda: s.attention(sync=False))
+    for which, bad in ((1, np.nan), (1, np.inf), (0, np.nan), (0, np.inf)):
+        s.host[:] = calm_keys
+        s.host[which, :, paged.slots(s.table[0], 16, 100, 1)[0], 5] = bad
+        s.upload()
+        if which or np.isnan(bad):  # (a score of +inf cannot be told from one that outgrew fp32)
+            assert microseconds(lambda: s.attention(sync=False)) < 20 * calm
+        out = s.attention()
+        assert not torch.isfinite(out[:700, 5]).all() and torch.isfinite(out[700:]).all()
+        assert torch.isfinite(out[:700, 6]).all() == (which == 1)
+
+
+def test_rows_beside_a_value_that_is_not_theirs_hold_nobody_up(native, eng):
+    """Rows in front of a value that is not finite, in one tile with it, are computed once more, key by key: over 600,000
+    keys that is longer than a wait may last, and the requests behind them on the same block still come out."""
+    d, page, ctx, rows, sms = 128, 64, 600000, 250, torch.cuda.get_device_properties(0).multi_processor_count
+    pages = -(-(ctx + rows) // page)
+    table = np.tile(np.arange(1, pages + 2, dtype=np.int32), (2 * sms, 1))[:, :pages]
+    table[:sms, -1] = 0  # the first half of the requests ends with a page of its own
+    layer = torch.zeros((2, 1, (pages + 2) * page, d), dtype=torch.bfloat16, device="cuda")
+    layer[1] = 1
+    last = (ctx + rows - 1) % page
+    layer[1, 0, last, 5] = float("nan")
+    plan = eng.paged_plan(1, 1, 1, d, page, pages + 2, [rows] * (2 * sms), [ctx] * (2 * sms), table)
+    dplan = torch.from_numpy(plan).cuda()
+    q = torch.ones((2 * sms * rows, d), dtype=torch.bfloat16, device="cuda")
+    out, work = torch.zeros_like(q), torch.zeros(eng.paged_workspace_bytes(plan) + 16, dtype=torch.uint8, device="cuda")
+    eng.op_paged_attention(q.data_ptr(), layer.data_ptr(), plan, dplan.data_ptr(), work.data_ptr(), out.data_ptr())
+    eng.sync()
+    want = torch.ones_like(out)
+    want[rows - 1:sms * rows:rows, 5] = float("nan")
+    assert torch.equal(torch.nan_to_num(out, 7.0), torch.nan_to_num(want, 7.0))
