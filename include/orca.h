@@ -470,7 +470,8 @@ int64_t orca_paged_workspace_bytes(const int32_t *host_plan);
  *   [rope_len][rot_dim], rope_len at least every ctx_len + n_input of the batch.
  *   Keys and values go to their positions' slots, queries to rows of q_out (ld_q
  *   apart; NULL: left alone; qkv itself with ld_q = ld_qkv: in place).  INVALID
- *   if two rows share a slot, or qkv, q_out and the layer overlap in another way.
+ *   if two rows share a slot, if qkv, q_out and the layer overlap in another way, or if
+ *   q_out or the layer overlaps the plan or the table.
  * attention: row j of request i (a row of q: n_heads * head_dim elements) sees
  *   the positions 0 .. ctx_len + j of its request: softmax(scale q k) v per
  *   head, to the same row of out.  scale 0 means 1 / sqrt(head_dim); it must not be
@@ -487,7 +488,8 @@ int64_t orca_paged_workspace_bytes(const int32_t *host_plan);
  *   overflow.  Rows attended as prompts take hundreds of times as long, and the others
  *   of the call wait for them, where a score is +inf or 88 (2^127 as a weight) above all
  *   scores of the keys in front of its 64 keys, or where they lie in one tile (128 rows x
- *   heads) with a row that sees a value which is not finite and theirs to miss.  INVALID if out or the workspace overlaps another of the four. */
+ *   heads) with a row that sees a value which is not finite and theirs to miss.
+ *   INVALID if out or the workspace overlaps another of the four or the plan. */
 int orca_op_paged_append(orca_engine *eng, const void *qkv, int64_t ld_qkv, void *kv_layer, const int32_t *host_plan,
                          const int32_t *dev_plan, const float *rope, int32_t rope_len, int32_t rot_dim,
                          int32_t neighbours, void *q_out, int64_t ld_q);

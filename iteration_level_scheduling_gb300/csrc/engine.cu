@@ -1181,10 +1181,15 @@ int orca_op_paged_append(orca_engine *E, const void *qkv, int64_t ld_qkv, void *
     if (rot_dim > 0 && (!rope || !aligned16(rope) || rope_len < p.max_pos)) return ORCA_ERR_INVALID;
     const int64_t qkv_bytes = p.rows ? ((p.rows - 1) * ld_qkv + w) * es : 0;
     const int64_t layer_bytes = 2 * (int64_t)p.kv_heads * p.slots * p.head_dim * es;
-    if (overlap(qkv, qkv_bytes, kv_layer, layer_bytes)) return ORCA_ERR_INVALID;
+    const int64_t plan_bytes = 4 * (int64_t)p.words, rope_bytes = 4 * (int64_t)rope_len * rot_dim;
+    const auto tables = [&](const void *x, int64_t n) {  // what is written shares a byte with what is read beside the rows
+        return overlap(x, n, dev_plan, plan_bytes) || (rot_dim > 0 && overlap(x, n, rope, rope_bytes));
+    };
+    if (overlap(qkv, qkv_bytes, kv_layer, layer_bytes) || tables(kv_layer, layer_bytes)) return ORCA_ERR_INVALID;
     if (q_out) {
         const int64_t q_bytes = p.rows ? ((p.rows - 1) * ld_q + qw) * es : 0;
         if (!rows_ok(q_out, ld_q, qw, (int)es) || overlap(q_out, q_bytes, kv_layer, layer_bytes) ||
+            tables(q_out, q_bytes) ||
             (q_out == qkv ? ld_q != ld_qkv : overlap(q_out, q_bytes, qkv, qkv_bytes)))
             return ORCA_ERR_INVALID;
     }
@@ -1208,7 +1213,10 @@ int orca_op_paged_attention(orca_engine *E, const void *q, int64_t ld_q, const v
     if (p.rows == 0) return ORCA_OK;
     const int64_t q_bytes = ((p.rows - 1) * ld_q + w) * es, out_bytes = ((p.rows - 1) * ld_out + w) * es;
     const int64_t layer_bytes = 2 * (int64_t)p.kv_heads * p.slots * p.head_dim * es;
-    const int64_t ws_bytes = paged_workspace_bytes(host_plan);
+    const int64_t ws_bytes = paged_workspace_bytes(host_plan), plan_bytes = 4 * (int64_t)p.words;
+    if (overlap(out, out_bytes, dev_plan, plan_bytes) ||
+        (ws_bytes && overlap(workspace, ws_bytes, dev_plan, plan_bytes)))
+        return ORCA_ERR_INVALID;
     if (overlap(out, out_bytes, q, q_bytes) || overlap(out, out_bytes, kv_layer, layer_bytes) ||
         (ws_bytes && (overlap(workspace, ws_bytes, q, q_bytes) || overlap(workspace, ws_bytes, out, out_bytes) ||
                       overlap(workspace, ws_bytes, kv_layer, layer_bytes))))

@@ -404,8 +404,8 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
 
 bool paged_plan_ok(const int32_t *hp) { return hp && hp[0] == kPagedMagic; }
 PagedInfo paged_plan_info(const int32_t *hp) {
-    return {hp[G_DTYPE], hp[G_HEADS],  hp[G_KV_HEADS],  hp[G_DIM],
-            hp[G_SLOTS], hp[G_ROWS], hp[G_MAXPOS], hp[G_TWICE] != 0};
+    return {hp[G_DTYPE], hp[G_HEADS],  hp[G_KV_HEADS], hp[G_DIM],          hp[G_SLOTS],
+            hp[G_ROWS],  hp[G_MAXPOS], hp[G_TOTAL],    hp[G_TWICE] != 0};
 }
 
 int64_t paged_workspace_bytes(const int32_t *hp) {

@@ -196,7 +196,7 @@ struct PagedBatch {
     const int32_t *n_input, *ctx_len, *page_table;
 };
 struct PagedInfo {
-    int dtype, heads, kv_heads, head_dim, slots, rows, max_pos;
+    int dtype, heads, kv_heads, head_dim, slots, rows, max_pos, words;
     bool twice;  // two rows of the batch share a slot
 };
 struct PagedAppend {

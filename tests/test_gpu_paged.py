@@ -887,3 +887,46 @@ def test_rows_beside_a_value_that_is_not_theirs_hold_nobody_up(native, eng):
     want = torch.ones_like(out)
     want[rows - 1:sms * rows:rows, 5] = float("nan")
     assert torch.equal(torch.nan_to_num(out, 7.0), torch.nan_to_num(want, 7.0))
+
+
+def test_tables_that_are_written_are_refused(native, eng):
+    """The plan and the cosines are read while the rows are written."""
+    s = append_case(native, eng, 61, "bf16", 4, 1, 128, 16, [(1, 30000), (2, 5)], 128, False)
+    size, words = eng.paged_workspace_bytes(s.plan), len(s.plan)
+    assert size > 0
+    room = torch.zeros(4 * words + size + 2 * s.layer.numel() + 65536, dtype=torch.uint8, device="cuda")
+    at = room.data_ptr()
+    room[:4 * words] = s.dplan.view(torch.uint8)
+    ok = dict(qkv=s.dqkv.data_ptr(), layer=s.layer.data_ptr(), plan=s.plan, dev_plan=at, q_out=s.q_out.data_ptr(),
+              rope=s.drope.data_ptr(), rope_len=len(s.rope), rot_dim=128, ld_q=s.q_out.shape[1])
+    rope_end = ok["rope"] + s.drope.numel() * 4
+    for bad in (dict(q_out=at), dict(q_out=at + 4 * words - 16), dict(layer=at), dict(layer=at + 4 * words - 16),
+                dict(q_out=ok["rope"]), dict(q_out=rope_end - 16), dict(layer=ok["rope"]), dict(layer=rope_end - 16)):
+        with pytest.raises(native.OrcaError) as e:
+            eng.op_paged_append(**{**ok, **bad})
+        assert e.value.code == native.ERR_INVALID, bad
+    up = at + (4 * words + 15) // 16 * 16
+    q = dict(q=s.q_out.data_ptr(), layer=s.layer.data_ptr(), plan=s.plan, dev_plan=at, workspace=up,
+             out=up + (size + 15) // 16 * 16)
+    for bad in (dict(out=at), dict(out=at + 4 * words - 16), dict(workspace=at), dict(workspace=at + 4 * words - 16)):
+        with pytest.raises(native.OrcaError) as e:
+            eng.op_paged_attention(**{**q, **bad})
+        assert e.value.code == native.ERR_INVALID, bad
+    eng.op_paged_append(**ok)
+    eng.op_paged_attention(**q)  # right behind one another
+    eng.sync()
+
+
+def test_split_keys_need_a_workspace(native, eng):
+    s = Case(native, eng, 62, "bf16", 4, 1, 128, 16, [(1, 30000)])
+    assert eng.paged_workspace_bytes(s.plan) > 0
+    out = torch.full((1, s.H), 768.0, dtype=torch.bfloat16, device="cuda")
+    call = lambda work: eng.op_paged_attention(s.dq.data_ptr(), s.layer.data_ptr(), s.plan, s.dplan.data_ptr(), work,
+                                               out.data_ptr())
+    with pytest.raises(native.OrcaError) as e:
+        call(0)
+    assert e.value.code == native.ERR_INVALID
+    eng.sync()
+    assert (out == 768).all()
+    call(s.work.data_ptr())
+    assert (out != 768).all()
