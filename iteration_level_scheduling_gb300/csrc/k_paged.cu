@@ -37,8 +37,8 @@ enum {  // header words of a plan
     G_MAXPOS,  // positions of the batch: the largest ctx + n
     G_TWICE,
     G_TOTAL,
-    G_O_ROWS,   // per row: slot, position, request, 0
-    G_O_REQS,   // per request with rows: its first tile
+    G_O_ROWS,   // per row: slot, position, 0, 0
+    G_O_REQS,   // per request with rows: its first tile (for who reads a plan; the items have their own)
     G_O_TILES,  // slot / 16 of every 16 positions (each request at a multiple of four)
     G_SMS,
     G_ITEMS,                       // work items by class (8, 16, 32 columns)
@@ -78,15 +78,16 @@ int pack_of(int group) { return group <= 64 ? group : 1; }
 
 // How requests are attended: classes 0 to 2 as column tiles of 8, 16 and 32, kClasses as prompts.  A request is in the
 // narrowest class that holds all its columns (rows x heads of a key/value head; fp32: 16 at most, by registers).
-// Prompts (bf16, head_dim 64 and 128): above 16 columns (4 requests of <= 7 rows over <= 500 keys, 32 heads over 8: 8.7
-// us, as tiles of 32 13.7; 64 single rows over <= 8000, 40 heads over one: 41 and 67), unless the batch has none above
-// 64 columns and more than twice their keys below (9 of <= 5 over <= 1500: 14.9 us, with a launch of prompts 20.9).
-// Where heads are tiles of their own, above 32 rows (8 of 1 / 8 / <= 110 rows over <= 1000 keys, 71 heads over one: as
-// prompts 38 / 39 / 41 us, as tiles 13 / 17 / 78).
+// Prompts (bf16, head_dim 64 and 128): above 16 columns (4 requests of <= 7 rows over <= 500 keys, 32 heads over 8: 9.7
+// us, from 65 columns on 11.3; 64 single rows over <= 8000, 40 heads over one: 43 and 70), unless the batch has none
+// above 64 columns and more than twice their keys below (9 of <= 5 over <= 1500: 17.5 us, with a launch of prompts 22.7).
+// Where heads are tiles of their own, above 32 rows (8 of 1 / 8 rows over <= 1000 keys, 71 heads over one: 11.8 / 18.4
+// us, as prompts 40 / 40; <= 110 rows 43, as tiles 78).
 // A class goes along with the next wider one of the batch if that has at least as many keys, which saves a launch
-// beside another (64 of <= 7 over <= 3000: 103 us in three launches, 86 in one; 64 single rows beside 2000 over 1000
-// keys 88 and 96; over 36 batches of single rows beside a prompt 2 % less).  fp32 pays for empty columns in products:
-// 9 of <= 3 rows 27.6 and 32.6, so there none does.
+// beside another: 9 of <= 7 over <= 1500 17.4 us, each class in its own 22.9; 4 over <= 500 9.7 and 12.6.  Where the
+// narrow ones have many keys it is a loss: 64 of <= 7 over <= 3000 94 and 92; 64 single rows over <= 1000 keys beside
+// 2000 over 1000, 40 heads over 8, 95 and 89, 32 over 8 86 and 74.  fp32 pays for empty columns in products, so there
+// none does: 9 of <= 3 rows 27.9 us, along with one another 32.1.  (Calls among others.)
 struct Classes {
     int to[kClasses + 1] = {0, 1, 2, kClasses};
     bool fp32, prompts = false;
@@ -206,7 +207,7 @@ bool paged_sizes(const PagedBatch &b, int num_sms, PagedSizes *z) {
         z->maxpos = std::max(z->maxpos, c + n);
     }
     // a unit's time goes with its bytes (one request over 500 / 2000 keys, 32 heads over 8 of 128: 6.8 / 8.0 us with
-    // parts of 256 keys or more, 5.7 / 6.0 of 128; 300 keys, 20 heads of 64: 5.0 whole, 5.8 in parts of 128)
+    // parts of 256 keys or more, 5.7 / 6.0 of 128; 300 keys, 20 heads of 64: 5.0 whole, 5.8 in parts of 128; replayed)
     const double small = std::min(2.0, 256.0 / (b.head_dim * (b.dtype ? 2 : 4)));
     z->chunk = 64 * choose_chunk(work, b.n_kv_heads, (int64_t)kCwCtasPerSm * num_sms, 2, 4 * small, 2 * small, 0.0);
     z->pchunk = 64 * choose_chunk(pwork, vheads, num_sms, 4, kPromptExtra, 3.0, 0.03);
@@ -302,7 +303,7 @@ bool paged_plan_build(const PagedBatch &b, int num_sms, int32_t *buf, int64_t ca
         const int32_t *mine = buf + req[i];
         tile = buf + up4(tile - buf);
         for (int32_t pos = (int32_t)c; pos < c + n; ++pos, row += 4)
-            row[0] = mine[pos / 16] * 16 + pos % 16, row[1] = pos, row[2] = i;
+            row[0] = mine[pos / 16] * 16 + pos % 16, row[1] = pos;
         const auto tile_items = [&](int cl, int64_t col, int64_t cols, int64_t keys) {
             const int64_t parts = parts_of(keys, z.chunk), per = parts == 1 ? keys : z.chunk;
             for (int64_t p = 0; p < parts; ++p, item[cl] += 8) {
@@ -430,8 +431,8 @@ struct AppendArgs {
 // One thread per two 16-byte chunks of a head's row, which hold whole pairs: the
 // chunks i and rot / 2 + i, or two neighbouring ones.  In between it reads its
 // cosines and sines, which all heads of a row share in L1.  Bound by HBM: 8
-// prompts of <= 2047 rows, 40 + 16 heads of 128, 303 MB in 48.7 us, 92 % of the copy rate
-// (with the table read 16 bytes at a time 51.3).
+// prompts of <= 2047 rows, 40 + 16 heads of 128, 303 MB in 48.9 us, 91 % of the copy rate
+// (neighbours 51.4; with the table read 16 bytes at a time 51.3).
 // NEIGH: components 2i and 2i + 1 are a pair; else i and i + rot / 2.
 // A thread reads all that it and its pairs need before it writes, so q_out may
 // be the queries' own place.
@@ -489,7 +490,9 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
 
 // Halves whose middle is inside a 16-byte chunk: a thread per chunk, the
 // components' partners loaded one by one.  A head's row is within a warp, which
-// reads all of it before it writes.
+// reads all of it before it writes.  Bound by issue (three quarters of the slots, 2.7
+// times the instructions of the kernel above): the same prompts with 20 or 126
+// rotated components 84 us, floor 44.6; in fp32 121 us, floor 89.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) paged_append_odd_kernel(const AppendArgs a) {
     constexpr int VEC = Elem<T>::kPer16, CH = D / VEC;
@@ -574,8 +577,10 @@ cudaError_t paged_append(const PagedAppend &p, const int32_t *hp, const int32_t 
 //
 // Each warp is a pipeline of its own: it takes every fourth tile of 16 keys of
 // the item, loads it by TMA (K and V of a 64-dim block in one box; 16 slots
-// never cross a page) into its own ring of stages several tiles ahead, across items,
-// and keeps its own running maximum m, sum l and outputs per column.  At the end
+// never cross a page) into its own ring of stages, across items, and keeps its own
+// running maximum m, sum l and outputs per column.  (Stages, tiles of 8 columns / of
+// more: bf16 of head_dim 128 3 / 2, 64 6 / 4, below 8; fp32 of 64 3 / 2, and of 128 one, so
+// that nothing is loaded ahead there but what the block's other warps have under way.)  At the end
 // of an item the block's four warps meet and add up.  No warp waits for another
 // while it streams, and nothing is shared between blocks: keys are split by the
 // plan where there are few items (choose_chunk), the parts joined by
@@ -591,9 +596,15 @@ cudaError_t paged_append(const PagedAppend &p, const int32_t *hp, const int32_t 
 //
 // Bound by HBM for long contexts (64 requests of <= 4000 keys, 40 heads over 8 of
 // 128: 663 MB in 105 us, 93 % of the copy rate; 40 heads of their own, 64 x <= 1000 keys:
-// 97 %), by latency below some 20 MB: one request over 300 keys, 20 heads of 64, 4.8 us.
-// fp32 by issue: the parts cost some 800 instructions per 16 keys (64 x <= 1000 keys, 8
-// heads of 128: 60 us, 82 % of the copy rate).
+// 97 %), by latency below some 20 MB: one request over 300 keys, 20 heads of 64, 5.1 us.
+// fp32 single rows by latency too, over a tile's chain of loads, splits and products
+// (some 800 instructions per 16 keys, issued in 24 to 31 % of the slots by 6 warps per SM,
+// DRAM 22 to 47 %): 17 x <= 900 keys, 12 heads over 4 of 64, 10.4 us, floor 3.1; 64 x <=
+// 1000 keys, 8 heads of 128, 66, floor 49.  Several rows there by issue and tensor pipe
+// (48 and 31 %; a prompt's keys are read once for every 16 columns): 4 x <= 200 rows over
+// <= 1000 keys, 12 over 4 of 64, 51 us, floor 1.7.  Rows of head_dim 32 / 16 as tiles of 32,
+// by issue (40 %) and the chain: 4 x <= 1024 over <= 1000 keys, 12 heads over 4, 74 / 78
+// us, floor 3.2 / 1.6.
 namespace {
 
 constexpr int kCwWarps = 4;
@@ -1225,22 +1236,24 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 //   O_t += P_t V    P (bf16) from tensor memory, V as it lies in its pages
 // Tensor memory: two buffers of S per tile (64 columns each; P takes the first
 // half of its S, the second part of a narrow request's weights the other), O_0, O_1
-// (128 each).  The chain from S over the softmax to P
-// V and back has some 2400 cycles of latency beside its work (products, commits,
+// (128 each).  The chain from S over the softmax to P V and back has some 2400 cycles of latency beside its work (products, commits,
 // waits, tensor-memory accesses; measured with that work left out), so the
 // next S is always under way: a softmax finds it when it is done with the last.
 // (With one buffer of 128 keys the same work took 4400 cycles per 128 keys of both
 // tiles, now 2400.)  Shared memory: Q, a ring of K and one of V; the loads are
 // boxes of a page (or of the part of it that divides 64 slots).
-// Bound: a step of both tiles takes some 1200 cycles.  head_dim 128: the tensor
-// core has 1024 of them, and shared memory, which feeds Q again for every 64 keys, as
-// many.  head_dim 64: the softmax, two warps of a scheduler at once (64 exponentials and
-// 130 other instructions per row: 830 cycles, then 350 of waits and tensor-memory
-// accesses).  Beside that 1.5 to 2.4 us at an item's end, where the tensor core idles.
-// 4 prompts of <= 1024 rows over <= 1000 keys, 40 heads over 8 of 128: 68 us, 0.57 of
-// the tensor peak; 8 of <= 2047 rows, 16 over 2 of 64: 48 us, 0.35.  (K and V released
+// Bound: a step of both tiles takes some 1200 cycles.  head_dim 128: tensor core and
+// shared memory, which feeds Q again for every 64 keys, have 1024 of them each, but not
+// the same ones: a product of S is 32 cycles of the one and 48 of the other, one of P V
+// 64 and 32, which is 1280 if no product overlaps the next.  head_dim 64: nothing is
+// full (tensor core 512, exponentials 512, issue 40 %); the softmax of two warps per
+// scheduler takes 830, then 350 of waits and tensor-memory accesses: the chain.  Beside
+// that 1.5 to 2.4 us at an item's end, where the tensor core idles.
+// 4 prompts of <= 1024 rows over <= 1000 keys, 40 heads over 8 of 128: 69.8 us, 0.56 of
+// the tensor peak; 8 of <= 2047 rows, 16 over 2 of 64: 49 us, 0.35.  (K and V released
 // together: 72.5 us, and 200 rows over 30000 keys, 32 heads over 8, 138 us for 105;
 // the two tiles half a step apart: 75 and 46.6 us, dropped.)
+// Weights of two bf16 parts for all requests, not only for narrow ones, would be 87 and 56 us.
 // Every P is formed against the m that O and l carry, which is near a row's
 // maximum and need not be it: O is rescaled only where it lags by more than 2^8.
 // Keys past the item's last are masked by index and their V rows zeroed.  A
@@ -1759,8 +1772,8 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         // are formed against the m that is there, without a look at its maximum, and m follows with the next tile where
         // their sum shows that it lags by more than 2^8 (O and l with it).  What overflows meanwhile is not finite in O
         // and is computed once more below.
-        // (A wait that gave up sets the abort flag: the item's key tiles run through on what is there, then the role ends
-        // without an output.)
+        // (A wait that gave up sets the abort flag, with which all others give up too: the item's key tiles run through on
+        // what is there, then the role ends at the wait for their products.)
         const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_t = tmem + ((uint32_t)(quarter * 32) << 16), o_t = lane_t + 256u + 128u * t;
         const uint32_t s_full = smem_u32(&bar.s_full[t][0]);
@@ -1900,10 +1913,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             bool bad = false;
             if (nk > 0) {
                 if (nk >= 2) wait(&bar.o_done[t][0], n_before++);
-                wait(&bar.o_done[t][1], n_last++);
-            }
-            if (__any_sync(kFull, *abort != 0)) break;
-            if (nk > 0) {
+                if (!__all_sync(kFull, wait(&bar.o_done[t][1], n_last++))) break;  // (gave up)
                 tc_fence_after();
                 const float inv = 1.f / l;
                 const uint64_t inv2 = pp_pair(inv, inv);

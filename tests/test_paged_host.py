@@ -278,17 +278,16 @@ def test_tensor_memory_is_taken_once_the_kernel_in_front_has_ended():
 
 
 def test_a_wait_that_gave_up_ends_the_softmax_role():
-    """Of the prompt kernel, once a wait has run out: no item's output is written, no row is computed key by key (which
-    takes seconds over long contexts and holds up the other waits' limits), and values that may still be landing are left
-    alone."""
+    """Of the prompt kernel, once a wait has run out: the role ends at the item's last wait, in front of its output, no row
+    is computed key by key (which takes seconds over long contexts and holds up the other waits' limits), and values that
+    may still be landing are left alone."""
     from test_launch_order import body
     b = body("k_paged.cu", "paged_prompt_kernel")
     b = b[b.index("warp < kPpTma)"):]
-    votes = "__any_sync(kFull, *abort != 0)"
-    end = b.index("if (" + votes + ") break;")
-    assert b.rindex("wait(", 0, end) < end < min(b.index("a.out"), b.index("part + x"), b.index("a.part_ml"))
-    assert "wait(" not in b[end:]  # the last of the item's waits stand in front of it
+    end = b.index("if (!__all_sync(kFull, wait(&bar.o_done[t][1], n_last++))) break;")
+    assert end < min(b.index("a.out"), b.index("part + x"), b.index("a.part_ml"))
+    assert b[end:].count("wait(") == 1  # the last of the item's waits
     loop = b.index("pp_row<D>")
-    assert b[b.rindex("for (", 0, loop):loop].count(votes) == 1
+    assert b[b.rindex("for (", 0, loop):loop].count("__any_sync(kFull, *abort != 0)") == 1
     zero = b.index("make_uint4(0, 0, 0, 0)")
     assert "landed = wait(&bar.full[1]" in b[:zero] and "if (landed &&" in b[b.index("landed = "):zero]
