@@ -1249,8 +1249,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 // full (tensor core 512, exponentials 512, issue 40 %); the softmax of two warps per
 // scheduler takes 830, then 350 of waits and tensor-memory accesses: the chain.  Beside
 // that 1.5 to 2.4 us at an item's end, where the tensor core idles.
-// 4 prompts of <= 1024 rows over <= 1000 keys, 40 heads over 8 of 128: 69.8 us, 0.56 of
-// the tensor peak; 8 of <= 2047 rows, 16 over 2 of 64: 49 us, 0.35.  (K and V released
+// 4 prompts of <= 1024 rows over <= 1000 keys, 40 heads over 8 of 128: 70 us, 0.55 of
+// the tensor peak; 8 of <= 2047 rows, 16 over 2 of 64: 49 us, 0.34.  (K and V released
 // together: 72.5 us, and 200 rows over 30000 keys, 32 heads over 8, 138 us for 105;
 // the two tiles half a step apart: 75 and 46.6 us, dropped.)
 // Weights of two bf16 parts for all requests, not only for narrow ones, would be 87 and 56 us.

@@ -291,3 +291,23 @@ def test_a_wait_that_gave_up_ends_the_softmax_role():
     assert b[b.rindex("for (", 0, loop):loop].count("__any_sync(kFull, *abort != 0)") == 1
     zero = b.index("make_uint4(0, 0, 0, 0)")
     assert "landed = wait(&bar.full[1]" in b[:zero] and "if (landed &&" in b[b.index("landed = "):zero]
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_narrow_requests_are_marked_in_every_launch(native, seed):
+    """Up to 16 rows x heads of a key/value head, whichever class they go along with: weights of 16 bits."""
+    g = np.random.default_rng(100 + seed)
+    n = [int(x) for x in g.choice([1, 1, 2, 3, 4, 5, 9, 16, 17, 40, 150], int(g.integers(2, 9)))]
+    c = [int(x) for x in g.choice([0, 20, 300, 2000], len(n))]
+    group, need = int(g.choice([1, 3, 4, 5, 8, 16, 71])), [-(-(a + b) // 16) for a, b in zip(n, c)]
+    first, table = np.concatenate([[0], np.cumsum(need)]), np.zeros((len(n), max(need)), np.int32)
+    for i, m in enumerate(need):
+        table[i, :m] = first[i] + np.arange(m)
+    p = plan(native, heads=2 * group, kv_heads=2, d=int(g.choice([16, 64, 128])), n=n, c=c, n_pages=sum(need), table=table)
+    req_of, seen = np.repeat(np.arange(len(n)), n), set()
+    for off, count, mark in ((O_ITEMS, p[ITEMS:ITEMS + 3].sum(), 7), (O_PITEMS, p[PITEMS], 6)):
+        for r in p[p[off]:p[off] + 8 * count].reshape(-1, 8):
+            i = int(req_of[r[2]])
+            assert r[mark] == (n[i] * group <= 16)
+            seen.add(i)
+    assert seen == set(range(len(n)))
