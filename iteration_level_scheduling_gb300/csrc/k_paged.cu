@@ -1250,10 +1250,12 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 // scheduler takes 830, then 350 of waits and tensor-memory accesses: the chain.  Beside
 // that 1.5 to 2.4 us at an item's end, where the tensor core idles.
 // 4 prompts of <= 1024 rows over <= 1000 keys, 40 heads over 8 of 128: 70 us, 0.55 of
-// the tensor peak; 8 of <= 2047 rows, 16 over 2 of 64: 49 us, 0.34.  (K and V released
+// the tensor peak; 8 of <= 2047 rows, 16 over 2 of 64: 51 us, 0.33.  (K and V released
 // together: 72.5 us, and 200 rows over 30000 keys, 32 heads over 8, 138 us for 105;
 // the two tiles half a step apart: 75 and 46.6 us, dropped.)
-// Weights of two bf16 parts for all requests, not only for narrow ones, would be 87 and 56 us.
+// Weights of two bf16 parts for all requests, not only for narrow ones, would be 87 and 56 us.  Those of one part
+// are summed up as they are used (4 % of the time at head_dim 64, 0.3 % at 128), so that a row of which one weight is
+// above all others does not have that one's rounding in its output.
 // Every P is formed against the m that O and l carry, which is near a row's
 // maximum and need not be it: O is rescaled only where it lags by more than 2^8.
 // Keys past the item's last are masked by index and their V rows zeroed.  A
@@ -1399,10 +1401,14 @@ __device__ __forceinline__ uint64_t pp_mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint64_t pp_add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
+// Adds the two numbers of a bf16 pair to two fp32 sums.
+__device__ __forceinline__ void pp_add_bf16(float &lo, float &hi, uint32_t w) {
+    asm("{\n\t.reg .b16 x, y;\n\t"
+        "mov.b32 {x, y}, %2;\n\t"
+        "add.rn.f32.bf16 %0, x, %0;\n\t"
+        "add.rn.f32.bf16 %1, y, %1;\n\t}"
+        : "+f"(lo), "+f"(hi)
+        : "r"(w));
 }
 
 // A bounded wait; when it gives up, or another warp has, the abort flag is set and every later wait ends at once.  A
@@ -1857,7 +1863,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                         for (int x = 0; x < 64; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) - cw_base(m));
                     }
                     const uint64_t scale2 = pp_pair(a.scale_log2, a.scale_log2), neg2 = pp_pair(neg, neg);
-                    uint64_t sum[2] = {0, 0};
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int x = 0; x < 64; x += 32) {
                         uint32_t w[16], low[16];  // (low: of a narrow request's weights, what bf16 leaves of them)
@@ -1868,16 +1874,19 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                                 pp_pair(__uint_as_float(s[x + 2 * e]), __uint_as_float(s[x + 2 * e + 1]));
                             pp_unpair(pp_fma2(sp, scale2, neg2), p0, p1);
                             p0 = cw_exp2(p0), p1 = cw_exp2(p1);
-                            sum[e & 1] = pp_add2(sum[e & 1], pp_pair(p0, p1));
                             w[e] = cw_pack(p0, p1);
-                            if constexpr (kNarrow) low[e] = cw_pack(p0 - cw_lower(w[e]), p1 - cw_upper(w[e]));
+                            float *const of = sum + 2 * (e & 1);
+                            if constexpr (kNarrow) {
+                                low[e] = cw_pack(p0 - cw_lower(w[e]), p1 - cw_upper(w[e]));
+                                of[0] += p0, of[1] += p1;
+                            } else {  // l sums what is used: one weight above all others leaves its value as it is
+                                pp_add_bf16(of[0], of[1], w[e]);
+                            }
                         }
                         pp_st16(s_t + x / 2, w);
                         if constexpr (kNarrow) pp_st16(s_t + 32 + x / 2, low);
                     }
-                    float l0, l1;
-                    pp_unpair(pp_add2(sum[0], sum[1]), l0, l1);
-                    last = mine ? l0 + l1 : 0.f;
+                    last = mine ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
                     l += last;
                     if (j >= clean) {
                         // V rows past the item's last key: zero, once they have landed

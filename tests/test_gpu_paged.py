@@ -930,3 +930,19 @@ def test_split_keys_need_a_workspace(native, eng):
     assert (out == 768).all()
     call(s.work.data_ptr())
     assert (out != 768).all()
+
+
+@pytest.mark.parametrize("reqs,key", [([(150, 100)], 70), ([(40, 3000)], 300), ([(40, 3000)], 3000), ([(33, 217)], 130),
+                                      ([(5, 100), (200, 0)], 70), ([(7, 90), (1, 50), (2, 300)], 85)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 32), ("fp32", 64)])
+def test_one_weight_above_all_others(native, eng, dtype, d, reqs, key):
+    """A key of 2^20 times the others' weight, its own a number that bf16 rounds by half a step (2^20 (1 + 2^-8)): what is
+    rounded of it goes out of the sum as well, so that the output is the key's value."""
+    s = Case(native, eng, 45, dtype, 8, 2, d, 16, reqs)
+    s.q[:], s.q[..., :2] = 0, 1
+    for (n, c), t in zip(reqs, s.table):
+        at = paged.slots(t, 16, 0, n + c)
+        s.host[0][:, at] = 0
+        s.host[0][:, at[min(key, c)], :2] = rounded(np.array([20, np.log2(1 + 2.0 ** -8)]), dtype)
+    s.upload()
+    s.check(s.attention(scale=float(np.log(2.0))), scale=float(np.log(2.0)))
