@@ -580,8 +580,8 @@ cudaError_t paged_append(const PagedAppend &p, const int32_t *hp, const int32_t 
 // never cross a page) into its own ring of stages, across items, and keeps its own
 // running maximum m, sum l and outputs per column.  (Stages, tiles of 8 columns / of
 // more: bf16 of head_dim 128 3 / 2, 64 6 / 4, below 8; fp32 of 64 3 / 2, and of 128 one, so
-// that nothing is loaded ahead there but what the block's other warps have under way.)  At the end
-// of an item the block's four warps meet and add up.  No warp waits for another
+// that nothing is loaded ahead there but what the block's other warps have under
+// way.)  At the end of an item the block's four warps meet and add up.  No warp waits for another
 // while it streams, and nothing is shared between blocks: keys are split by the
 // plan where there are few items (choose_chunk), the parts joined by
 // paged_join_kernel, without atomics, in their order.
@@ -1236,9 +1236,10 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 //   O_t += P_t V    P (bf16) from tensor memory, V as it lies in its pages
 // Tensor memory: two buffers of S per tile (64 columns each; P takes the first
 // half of its S, the second part of a narrow request's weights the other), O_0, O_1
-// (128 each).  The chain from S over the softmax to P V and back has some 2400 cycles of latency beside its work (products, commits,
-// waits, tensor-memory accesses; measured with that work left out), so the
-// next S is always under way: a softmax finds it when it is done with the last.
+// (128 each).  The chain from S over the softmax to P V and back has some 2400 cycles
+// of latency beside its work (products, commits, waits, tensor-memory accesses;
+// measured with that work left out), so the next S is always under way: a softmax
+// finds it when it is done with the last.
 // (With one buffer of 128 keys the same work took 4400 cycles per 128 keys of both
 // tiles, now 2400.)  Shared memory: Q, a ring of K and one of V; the loads are
 // boxes of a page (or of the part of it that divides 64 slots).
@@ -1246,16 +1247,17 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
 // shared memory, which feeds Q again for every 64 keys, have 1024 of them each, but not
 // the same ones: a product of S is 32 cycles of the one and 48 of the other, one of P V
 // 64 and 32, which is 1280 if no product overlaps the next.  head_dim 64: nothing is
-// full (tensor core 512, exponentials 512, issue 40 %); the softmax of two warps per
+// full (tensor core 512, exponentials 512, issue 42 %); the softmax of two warps per
 // scheduler takes 830, then 350 of waits and tensor-memory accesses: the chain.  Beside
 // that 1.5 to 2.4 us at an item's end, where the tensor core idles.
 // 4 prompts of <= 1024 rows over <= 1000 keys, 40 heads over 8 of 128: 70 us, 0.55 of
 // the tensor peak; 8 of <= 2047 rows, 16 over 2 of 64: 51 us, 0.33.  (K and V released
 // together: 72.5 us, and 200 rows over 30000 keys, 32 heads over 8, 138 us for 105;
 // the two tiles half a step apart: 75 and 46.6 us, dropped.)
-// Weights of two bf16 parts for all requests, not only for narrow ones, would be 87 and 56 us.  Those of one part
-// are summed up as they are used (4 % of the time at head_dim 64, 0.3 % at 128), so that a row of which one weight is
-// above all others does not have that one's rounding in its output.
+// Weights of two bf16 parts for all requests, not only for narrow ones, would be 87
+// and 56 us.  Those of one part are summed up as they are used (4 % of the time at
+// head_dim 64, 0.3 % at 128), so that a row of which one weight is above all others does
+// not have that one's rounding in its output.
 // Every P is formed against the m that O and l carry, which is near a row's
 // maximum and need not be it: O is rescaled only where it lags by more than 2^8.
 // Keys past the item's last are masked by index and their V rows zeroed.  A
